@@ -1,7 +1,10 @@
 /*
  * ssm.h -- C ABI of libssm.so, the gfx950 (MI355X) selective-scan library.
  *
- * Four operations, all from the Mamba pages (cited by page title and section):
+ * Four operations from the Mamba pages (cited by page title and section), and
+ * two families next to them: a gated linear recurrence (ssm_gated_*) and a
+ * quantised cache of recurrent states (ssm_state_cache_*,
+ * ssm_selective_state_update_cached), each described at its arguments.
  *
  *   ssm_selective_scan_fwd  -- prefill.  For every batch row b, channel d and
  *     state index n, with Delta_t = softplus(delta_t + bias[d]) (Mamba paper
@@ -92,7 +95,9 @@ typedef enum ssm_status {
                               ssm_scan_args)                                   */
   SSM_ERR_HIP = 8,         /* the HIP runtime rejected the launch              */
   SSM_ERR_SCRATCH = 9      /* ssm_selective_scan_fwd_noalloc: the segment
-                              scratch exceeds SSM_NOALLOC_SCRATCH_BYTES        */
+                              scratch exceeds SSM_NOALLOC_SCRATCH_BYTES; the
+                              gated scan and its backward: the workspace is
+                              missing or smaller than their size function says */
 } ssm_status;
 
 typedef enum ssm_dtype { SSM_F32 = 0, SSM_BF16 = 1 } ssm_dtype;
@@ -356,6 +361,196 @@ typedef struct ssm_ssd_args {
   void* workspace;    size_t workspace_bytes;
 } ssm_ssd_args;
 
+/* Arguments of the gated linear recurrence: one state per channel, decay and
+ * input scale from the token.  For every sequence and channel d, with
+ * s_d = c softplus(lam[d]) and sigma the logistic function:
+ *     a_t = exp(-s_d sigma(gate_a_t))
+ *     h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigma(gate_x_t) x_t
+ *     out_t = h_t
+ * from h_{-1} = h0 (or zero), optionally returning the last h.
+ *   x, gate_a, gate_x, out : (batch, seqlen, dim), dim stride 1; element
+ *                (b, t, d) at ptr[b * *_batch_stride + t * *_seq_stride + d].
+ *   lam        : (dim) fp32, contiguous.  c: positive and finite.
+ *   cu_seqlens : NULL: every batch row is one sequence.  Otherwise batch must
+ *                be 1 and the row holds nseq packed sequences: int32, device
+ *                memory, nseq + 1 entries, not decreasing, sequence k being
+ *                tokens cu_seqlens[k] .. cu_seqlens[k + 1] - 1 (none if equal).
+ *                Tokens before cu_seqlens[0] or from cu_seqlens[nseq] on belong
+ *                to no sequence: their rows of out are left as they are, or set
+ *                to zero with zero_outside.  The values are read on the device
+ *                and not checked on the host; values that break these rules give
+ *                unspecified results but no access outside the tensors.
+ *   h0, last_state : (nseq, dim), or (batch, dim) without cu_seqlens; fp32,
+ *                contiguous.  h0 NULL is a zero state, last_state NULL: not
+ *                wanted.  An empty sequence's last state is its h0 (or zero).
+ *   checkpoints : fp32 (batch, ceil(seqlen / SSM_CHECKPOINT_TOKENS), dim),
+ *                contiguous; element (b, k, d) is h entering token
+ *                k * SSM_CHECKPOINT_TOKENS, for ssm_gated_scan_bwd (what it
+ *                holds where that token begins a sequence or is in none is
+ *                unspecified).  NULL: none written.
+ * Sizes: zero sizes are no-ops, but that empty sequences still set last_state;
+ * seqlen below 2^31 - 64.  The number of workgroups,
+ * batch * ceil(seqlen / 16) * ceil(dim / 64), must be below 2^31
+ * (SSM_ERR_UNSUPPORTED).
+ * Precision: fp32 arithmetic and state; bf16 inputs are widened exactly and
+ * out is rounded once.
+ * Aliasing: out, last_state, checkpoints and the workspace must not overlap
+ * any input or each other, except that last_state may be exactly h0.
+ * Workspace: device scratch owned by the caller, 8-byte aligned, of at least
+ * ssm_gated_scan_workspace_size() bytes where that is not 0 (required:
+ * SSM_ERR_SCRATCH otherwise), not overlapping any tensor and not in use by
+ * another call that may run at the same time.  Its contents before the call
+ * do not matter, and nothing is kept in it between calls. */
+typedef struct ssm_gated_args {
+  int64_t batch, seqlen, dim, nseq;
+  int32_t io_dtype;      /* ssm_dtype */
+  int32_t zero_outside;  /* bool */
+  float c;
+  const void* x;       int64_t x_batch_stride, x_seq_stride;
+  const void* gate_a;  int64_t gate_a_batch_stride, gate_a_seq_stride;
+  const void* gate_x;  int64_t gate_x_batch_stride, gate_x_seq_stride;
+  const float* lam;
+  const int32_t* cu_seqlens;
+  const float* h0;
+  float* last_state;
+  void* out;           int64_t out_batch_stride, out_seq_stride;
+  float* checkpoints;
+  void* workspace;     size_t workspace_bytes;
+} ssm_gated_args;
+
+/* Arguments of its backward.  The forward inputs keep their meaning and must
+ * be the ones the forward ran with; `checkpoints` (required) is what it wrote.
+ *   dout    : like out.  dlast: like last_state, NULL means 0.
+ * Outputs, fully overwritten (tokens outside every sequence get zeros):
+ *   dx, dgate_a, dgate_x : like x, io_dtype, dim stride 1.
+ *   dlam    : (dim) fp32, summed over all tokens.
+ *   dh0     : like h0, fp32; NULL: not wanted.
+ * Where a_t rounds to 1 and its input scale to 0, the derivative of the square
+ * root is taken as 0.  All sums run in a fixed order: every output is the same
+ * bits from run to run.
+ * Sizes, aliasing and workspace (ssm_gated_scan_bwd_workspace_size(), always
+ * required) as for the forward. */
+typedef struct ssm_gated_bwd_args {
+  int64_t batch, seqlen, dim, nseq;
+  int32_t io_dtype;      /* ssm_dtype */
+  float c;
+  const void* x;       int64_t x_batch_stride, x_seq_stride;
+  const void* gate_a;  int64_t gate_a_batch_stride, gate_a_seq_stride;
+  const void* gate_x;  int64_t gate_x_batch_stride, gate_x_seq_stride;
+  const float* lam;
+  const int32_t* cu_seqlens;
+  const float* h0;
+  const float* checkpoints;
+  const void* dout;    int64_t dout_batch_stride, dout_seq_stride;
+  const float* dlast;
+  void* dx;            int64_t dx_batch_stride, dx_seq_stride;
+  void* dgate_a;       int64_t dgate_a_batch_stride, dgate_a_seq_stride;
+  void* dgate_x;       int64_t dgate_x_batch_stride, dgate_x_seq_stride;
+  float* dlam;
+  float* dh0;
+  void* workspace;     size_t workspace_bytes;
+} ssm_gated_bwd_args;
+
+/* Arguments of its single-token step on a pool of states.
+ *   state  : (nslots, dim) fp32, dim stride 1, updated IN PLACE.
+ *   x, gate_a, gate_x, out : (batch, dim), dim stride 1.
+ *   slots  : int32 (batch) in device memory: row b's state is state[slots[b]].
+ *            NULL: row b's state is state[b] (batch must not exceed nslots).
+ * A row whose slot is outside [0, nslots) (a padded batch) touches no state
+ * and gets a zero row of out.  Rows that name the same slot are taken in the
+ * order of the rows, each on the state that the one before left.
+ * Sizes: batch at most 65535. */
+typedef struct ssm_gated_update_args {
+  int64_t batch, nslots, dim;
+  int32_t io_dtype;    /* ssm_dtype */
+  float c;
+  float* state;        int64_t state_slot_stride;
+  const void* x;       int64_t x_batch_stride;
+  const void* gate_a;  int64_t gate_a_batch_stride;
+  const void* gate_x;  int64_t gate_x_batch_stride;
+  const float* lam;
+  const int32_t* slots;
+  void* out;           int64_t out_batch_stride;
+} ssm_gated_update_args;
+
+/* Formats of the quantised state cache.  A state is `outer` rows of `inner`
+ * values (for the scan's (dim, dstate) state outer = dim, inner = dstate).
+ * Each row is cut into blocks of SSM_CACHE_BLOCK values (the last one may be
+ * shorter).  A block has one scale byte E, standing for 2^(E - 127): the least
+ * power of two, not below 2^-127, that brings the block's largest magnitude
+ * within the codes' range M.  A code is value / 2^(E - 127) rounded to nearest
+ * even on the codes' grid:
+ *   SSM_CACHE_INT8 : two's complement, M = 127.
+ *   SSM_CACHE_FP8  : 1 sign, 4 exponent (bias 7), 3 mantissa bits, M = 448.
+ *   SSM_CACHE_FP4  : 1 sign, 2 exponent (bias 1), 1 mantissa bit, M = 6 (the
+ *                    values 0, 0.5, 1, 1.5, 2, 3, 4, 6); two codes a byte, the
+ *                    even element in the low half; inner must be even.
+ * A block that holds a NaN or an infinity has E = 255 and reads back as NaN. */
+#define SSM_CACHE_BLOCK 32
+typedef enum ssm_cache_format { SSM_CACHE_INT8 = 0, SSM_CACHE_FP8 = 1, SSM_CACHE_FP4 = 2 } ssm_cache_format;
+
+/* Arguments of writing states to the cache and of reading them back.
+ *   codes  : bytes, (nslots, outer, inner) (FP4: inner / 2), contiguous within
+ *            a slot; slot k at codes + k * codes_slot_stride.
+ *   scales : bytes, (nslots, outer, ceil(inner / SSM_CACHE_BLOCK)), likewise.
+ *   states : (batch, outer, inner), io_dtype, contiguous within a row of the
+ *            batch, row b at states + b * states_batch_stride elements.
+ *   slots  : int32 (batch), device memory; NULL: row b goes with slot b (batch
+ *            must not exceed nslots).
+ * Write: a row whose slot is outside [0, nslots) is not written; of rows that
+ * name the same slot the last one is.  Read: a row whose slot is outside is
+ * zeros; bf16 states are rounded to nearest even (int8 and e4m3 codes and e2m1
+ * ones are exact in bf16 within its exponent range).
+ * Sizes: zero sizes are no-ops; batch at most 65535;
+ * outer * ceil(inner / 32) below 2^31 - 256.
+ * Aliasing: what is written must not overlap what is read. */
+typedef struct ssm_state_cache_args {
+  int64_t batch, nslots, outer, inner;
+  int32_t format;      /* ssm_cache_format */
+  int32_t io_dtype;    /* ssm_dtype of states */
+  uint8_t* codes;      int64_t codes_slot_stride;
+  uint8_t* scales;     int64_t scales_slot_stride;
+  void* states;        int64_t states_batch_stride;
+  const int32_t* slots;
+} ssm_state_cache_args;
+
+/* Arguments of the decode update (ssm_update_args, without the conv branch) on
+ * states held in an SSM_CACHE_INT8 cache: outer = dim, inner = dstate.
+ *   codes, scales, nslots, slots : as above; updated IN PLACE.
+ *   x, dt, z, out, B, C, A, D, dt_bias, ngroups : as in ssm_update_args.
+ *   seed   : one int64 in device memory, read when the kernel runs.  The new
+ *            state is rounded stochastically: with X = 256 s / 2^(E - 127)
+ *            rounded to nearest even, code = floor((X + u) / 256), u the byte
+ *            of Philox-4x32 with 7 rounds at counter (channel, row, n / 16, 0),
+ *            key seed: word (n % 16) / 4, byte n % 4 from the low end.  The
+ *            expected code is X / 256, so changes smaller than a code are kept
+ *            on average; give every step another seed.
+ *            NULL: rounded to nearest even (small changes then get lost).
+ * out is computed from the new state before it is rounded.  Rows that name the
+ * same slot are taken in their order; a row whose slot is outside [0, nslots)
+ * touches no state and gets a zero row of out.
+ * Sizes as in ssm_update_args; aliasing: out, codes and scales must not
+ * overlap any input or each other. */
+typedef struct ssm_cached_update_args {
+  int64_t batch, nslots, dim, dstate;
+  int32_t io_dtype;    /* ssm_dtype */
+  int32_t dt_softplus; /* bool */
+  uint8_t* codes;     int64_t codes_slot_stride;
+  uint8_t* scales;    int64_t scales_slot_stride;
+  const void* x;      int64_t x_batch_stride;
+  const void* dt;     int64_t dt_batch_stride;
+  const void* z;      int64_t z_batch_stride;
+  const void* B;      int64_t B_batch_stride, B_group_stride;
+  const void* C;      int64_t C_batch_stride, C_group_stride;
+  const float* A;     int64_t A_dim_stride;
+  const float* D;
+  const float* dt_bias;
+  void* out;          int64_t out_batch_stride;
+  const int32_t* slots;
+  const int64_t* seed;
+  int64_t ngroups;    /* B/C groups; 0 or 1: one group */
+} ssm_cached_update_args;
+
 /* ABI version of the loaded library (SSM_ABI_VERSION at build time). */
 int ssm_abi_version(void);
 
@@ -364,6 +559,11 @@ size_t ssm_scan_args_size(void);
 size_t ssm_scan_bwd_args_size(void);
 size_t ssm_update_args_size(void);
 size_t ssm_ssd_args_size(void);
+size_t ssm_gated_args_size(void);
+size_t ssm_gated_bwd_args_size(void);
+size_t ssm_gated_update_args_size(void);
+size_t ssm_state_cache_args_size(void);
+size_t ssm_cached_update_args_size(void);
 
 /* Workspace bytes the scan can use for this argument block (0 when it would
  * run single-segment anyway): for G segments, with BD = batch * dim and
@@ -388,6 +588,12 @@ size_t ssm_ssd_workspace_size(const ssm_ssd_args* args);
  * atomics anyway).  Reads only sizes; pure host code. */
 size_t ssm_scan_bwd_workspace_size(const ssm_scan_bwd_args* args);
 
+/* Workspace bytes the gated scan and its backward need for this argument
+ * block (0: none).  Read only sizes and whether cu_seqlens is given; pure host
+ * code. */
+size_t ssm_gated_scan_workspace_size(const ssm_gated_args* args);
+size_t ssm_gated_scan_bwd_workspace_size(const ssm_gated_bwd_args* args);
+
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char* ssm_status_string(int status);
 
@@ -397,6 +603,12 @@ int ssm_validate_scan(const ssm_scan_args* args);
 int ssm_validate_scan_bwd(const ssm_scan_bwd_args* args);
 int ssm_validate_update(const ssm_update_args* args);
 int ssm_validate_ssd(const ssm_ssd_args* args);
+int ssm_validate_gated(const ssm_gated_args* args);
+int ssm_validate_gated_bwd(const ssm_gated_bwd_args* args);
+int ssm_validate_gated_update(const ssm_gated_update_args* args);
+int ssm_validate_state_cache_write(const ssm_state_cache_args* args);
+int ssm_validate_state_cache_read(const ssm_state_cache_args* args);
+int ssm_validate_cached_update(const ssm_cached_update_args* args);
 
 /* Prefill scan (see ssm_scan_args).  Validates, then launches on `stream`. */
 int ssm_selective_scan_fwd(const ssm_scan_args* args, void* stream);
@@ -429,6 +641,18 @@ int ssm_selective_state_update(const ssm_update_args* args, void* stream);
 /* Mamba-2 SSM prefill (see ssm_ssd_args).  Validates, then launches on
  * `stream`. */
 int ssm_ssd_scan_fwd(const ssm_ssd_args* args, void* stream);
+
+/* Gated linear recurrence, its backward and its single-token step (see
+ * ssm_gated_args, ssm_gated_bwd_args, ssm_gated_update_args). */
+int ssm_gated_scan_fwd(const ssm_gated_args* args, void* stream);
+int ssm_gated_scan_bwd(const ssm_gated_bwd_args* args, void* stream);
+int ssm_gated_state_update(const ssm_gated_update_args* args, void* stream);
+
+/* Quantised state cache (see ssm_state_cache_args), and the decode update on
+ * states held in one (see ssm_cached_update_args). */
+int ssm_state_cache_write(const ssm_state_cache_args* args, void* stream);
+int ssm_state_cache_read(const ssm_state_cache_args* args, void* stream);
+int ssm_selective_state_update_cached(const ssm_cached_update_args* args, void* stream);
 
 #ifdef __cplusplus
 }

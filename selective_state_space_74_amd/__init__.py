@@ -16,6 +16,18 @@ CPU fallback, and importing a missing library raises.
            ddelta_bias, dh0 for the inputs that were given)
     selective_state_update(state, x, dt, A, B, C, D=None, z=None,
                            dt_bias=None, dt_softplus=True) -> out  (state updated in place)
+    selective_state_update_cached(codes, scales, x, dt, A, B, C, ..., slots=None, seed=None)
+        -> out  (the same step on states held in an int8 cache, updated in place)
+    state_cache_write(codes, scales, states, slots=None, format="int8")
+    state_cache_read(codes, scales, slots=None, format="int8", dtype=float32) -> states
+        (a cache of states in int8, e4m3 or e2m1 with a scale per 32 values)
+    gated_scan_fwd(x, gate_a, gate_x, lam, c=8.0, h0=None, cu_seqlens=None,
+                   return_last_state=False, checkpoints=None) -> out, or (out, last_state)
+    gated_scan_bwd(dout, x, gate_a, gate_x, lam, checkpoints, ...) -> dict of gradients
+    gated_scan(x, gate_a, gate_x, lam, ...)  (the two as a differentiable torch op)
+    gated_state_update(state, x, gate_a, gate_x, lam, c=8.0, slots=None) -> out
+        (a gated linear recurrence with one state per channel, token-major,
+        batched or packed: prefill, gradients, and its single-token step)
 
 Shapes (N = dstate, 1..64): u, delta, z (batch, dim, L) with time stride 1;
 B, C (batch, N, L), or (batch, G, N, L) for G groups of dim // G channels,
@@ -26,7 +38,9 @@ IO tensors are float32 or bfloat16 (all of one dtype).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -40,6 +54,9 @@ STATUS = {0: "SSM_OK", 1: "SSM_ERR_NULL", 2: "SSM_ERR_SHAPE", 3: "SSM_ERR_STRIDE
           4: "SSM_ERR_DTYPE", 5: "SSM_ERR_ALIGN", 6: "SSM_ERR_ALIAS", 7: "SSM_ERR_UNSUPPORTED",
           8: "SSM_ERR_HIP", 9: "SSM_ERR_SCRATCH"}
 NOALLOC_SCRATCH_BYTES = 32 << 20
+
+CACHE_BLOCK = 32
+CACHE_FORMATS = {"int8": 0, "fp8": 1, "fp4": 2}
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -122,6 +139,70 @@ class SsdArgs(ctypes.Structure):
                 ("out_head_stride", _I64), ("workspace", _P), ("workspace_bytes", ctypes.c_size_t)]
 
 
+class GatedArgs(ctypes.Structure):
+    """Mirror of ssm_gated_args."""
+    _fields_ = [("batch", _I64), ("seqlen", _I64), ("dim", _I64), ("nseq", _I64),
+                ("io_dtype", _I32), ("zero_outside", _I32), ("c", ctypes.c_float),
+                ("x", _P), ("x_batch_stride", _I64), ("x_seq_stride", _I64),
+                ("gate_a", _P), ("gate_a_batch_stride", _I64), ("gate_a_seq_stride", _I64),
+                ("gate_x", _P), ("gate_x_batch_stride", _I64), ("gate_x_seq_stride", _I64),
+                ("lam", _P), ("cu_seqlens", _P), ("h0", _P), ("last_state", _P),
+                ("out", _P), ("out_batch_stride", _I64), ("out_seq_stride", _I64),
+                ("checkpoints", _P), ("workspace", _P), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class GatedBwdArgs(ctypes.Structure):
+    """Mirror of ssm_gated_bwd_args."""
+    _fields_ = [("batch", _I64), ("seqlen", _I64), ("dim", _I64), ("nseq", _I64),
+                ("io_dtype", _I32), ("c", ctypes.c_float),
+                ("x", _P), ("x_batch_stride", _I64), ("x_seq_stride", _I64),
+                ("gate_a", _P), ("gate_a_batch_stride", _I64), ("gate_a_seq_stride", _I64),
+                ("gate_x", _P), ("gate_x_batch_stride", _I64), ("gate_x_seq_stride", _I64),
+                ("lam", _P), ("cu_seqlens", _P), ("h0", _P), ("checkpoints", _P),
+                ("dout", _P), ("dout_batch_stride", _I64), ("dout_seq_stride", _I64),
+                ("dlast", _P),
+                ("dx", _P), ("dx_batch_stride", _I64), ("dx_seq_stride", _I64),
+                ("dgate_a", _P), ("dgate_a_batch_stride", _I64), ("dgate_a_seq_stride", _I64),
+                ("dgate_x", _P), ("dgate_x_batch_stride", _I64), ("dgate_x_seq_stride", _I64),
+                ("dlam", _P), ("dh0", _P), ("workspace", _P), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class GatedUpdateArgs(ctypes.Structure):
+    """Mirror of ssm_gated_update_args."""
+    _fields_ = [("batch", _I64), ("nslots", _I64), ("dim", _I64),
+                ("io_dtype", _I32), ("c", ctypes.c_float),
+                ("state", _P), ("state_slot_stride", _I64),
+                ("x", _P), ("x_batch_stride", _I64),
+                ("gate_a", _P), ("gate_a_batch_stride", _I64),
+                ("gate_x", _P), ("gate_x_batch_stride", _I64),
+                ("lam", _P), ("slots", _P), ("out", _P), ("out_batch_stride", _I64)]
+
+
+class StateCacheArgs(ctypes.Structure):
+    """Mirror of ssm_state_cache_args."""
+    _fields_ = [("batch", _I64), ("nslots", _I64), ("outer", _I64), ("inner", _I64),
+                ("format", _I32), ("io_dtype", _I32),
+                ("codes", _P), ("codes_slot_stride", _I64),
+                ("scales", _P), ("scales_slot_stride", _I64),
+                ("states", _P), ("states_batch_stride", _I64), ("slots", _P)]
+
+
+class CachedUpdateArgs(ctypes.Structure):
+    """Mirror of ssm_cached_update_args."""
+    _fields_ = [("batch", _I64), ("nslots", _I64), ("dim", _I64), ("dstate", _I64),
+                ("io_dtype", _I32), ("dt_softplus", _I32),
+                ("codes", _P), ("codes_slot_stride", _I64),
+                ("scales", _P), ("scales_slot_stride", _I64),
+                ("x", _P), ("x_batch_stride", _I64),
+                ("dt", _P), ("dt_batch_stride", _I64),
+                ("z", _P), ("z_batch_stride", _I64),
+                ("B", _P), ("B_batch_stride", _I64), ("B_group_stride", _I64),
+                ("C", _P), ("C_batch_stride", _I64), ("C_group_stride", _I64),
+                ("A", _P), ("A_dim_stride", _I64), ("D", _P), ("dt_bias", _P),
+                ("out", _P), ("out_batch_stride", _I64),
+                ("slots", _P), ("seed", _P), ("ngroups", _I64)]
+
+
 class SSMError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -167,6 +248,20 @@ def lib():
         L.ssm_selective_state_update.argtypes = [ctypes.POINTER(UpdateArgs), _P]
         L.ssm_ssd_scan_fwd.restype = ctypes.c_int
         L.ssm_ssd_scan_fwd.argtypes = [ctypes.POINTER(SsdArgs), _P]
+        for name, T in (("gated_scan_fwd", GatedArgs), ("gated_scan_bwd", GatedBwdArgs),
+                        ("gated_state_update", GatedUpdateArgs), ("state_cache_write", StateCacheArgs),
+                        ("state_cache_read", StateCacheArgs),
+                        ("selective_state_update_cached", CachedUpdateArgs)):
+            f = getattr(L, "ssm_" + name)
+            f.restype, f.argtypes = ctypes.c_int, [ctypes.POINTER(T), _P]
+        for name, T in (("gated", GatedArgs), ("gated_bwd", GatedBwdArgs),
+                        ("gated_update", GatedUpdateArgs), ("state_cache_write", StateCacheArgs),
+                        ("state_cache_read", StateCacheArgs), ("cached_update", CachedUpdateArgs)):
+            f = getattr(L, "ssm_validate_" + name)
+            f.restype, f.argtypes = ctypes.c_int, [ctypes.POINTER(T)]
+        for name, T in (("gated_scan", GatedArgs), ("gated_scan_bwd", GatedBwdArgs)):
+            f = getattr(L, "ssm_%s_workspace_size" % name)
+            f.restype, f.argtypes = ctypes.c_size_t, [ctypes.POINTER(T)]
         if L.ssm_abi_version() != SSM_ABI_VERSION:
             raise ImportError(f"libssm.so ABI {L.ssm_abi_version()} != {SSM_ABI_VERSION}")
         if (L.ssm_scan_args_size() != ctypes.sizeof(ScanArgs)
@@ -174,6 +269,12 @@ def lib():
                 or L.ssm_update_args_size() != ctypes.sizeof(UpdateArgs)
                 or L.ssm_ssd_args_size() != ctypes.sizeof(SsdArgs)):
             raise ImportError("libssm.so argument struct layout differs from the binding")
+        for name, T in (("gated", GatedArgs), ("gated_bwd", GatedBwdArgs), ("gated_update", GatedUpdateArgs),
+                        ("state_cache", StateCacheArgs), ("cached_update", CachedUpdateArgs)):
+            f = getattr(L, "ssm_%s_args_size" % name)
+            f.restype = ctypes.c_size_t
+            if f() != ctypes.sizeof(T):
+                raise ImportError("libssm.so argument struct layout differs from the binding")
         _lib = L
     return _lib
 
@@ -667,3 +768,421 @@ def selective_scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, delta_sof
                     g.get("dD"), g.get("dz"), g.get("ddelta_bias"))
 
     return _Scan.apply(u, delta, A, B, C, D, z, delta_bias)
+
+
+# ---------------------------------------------------------------------------
+# the gated linear recurrence and the quantised state cache
+
+def validate_gated(args: GatedArgs) -> int:
+    return lib().ssm_validate_gated(ctypes.byref(args))
+
+
+def validate_gated_bwd(args: GatedBwdArgs) -> int:
+    return lib().ssm_validate_gated_bwd(ctypes.byref(args))
+
+
+def validate_gated_update(args: GatedUpdateArgs) -> int:
+    return lib().ssm_validate_gated_update(ctypes.byref(args))
+
+
+def validate_state_cache_write(args: StateCacheArgs) -> int:
+    return lib().ssm_validate_state_cache_write(ctypes.byref(args))
+
+
+def validate_state_cache_read(args: StateCacheArgs) -> int:
+    return lib().ssm_validate_state_cache_read(ctypes.byref(args))
+
+
+def validate_cached_update(args: CachedUpdateArgs) -> int:
+    return lib().ssm_validate_cached_update(ctypes.byref(args))
+
+
+def gated_scan_workspace_size(args: GatedArgs) -> int:
+    return lib().ssm_gated_scan_workspace_size(ctypes.byref(args))
+
+
+def gated_scan_bwd_workspace_size(args: GatedBwdArgs) -> int:
+    return lib().ssm_gated_scan_bwd_workspace_size(ctypes.byref(args))
+
+
+@contextlib.contextmanager
+def _on(device, stream):
+    """The tensors' device and the call's stream as the current ones: what is
+    allocated meanwhile belongs to that stream."""
+    torch = _torch()
+    with torch.cuda.device(device):
+        if stream is None:
+            yield torch.cuda.current_stream().cuda_stream
+            return
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        with torch.cuda.stream(stream):
+            yield stream.cuda_stream
+
+
+def _launch(name, args, stream):
+    st = getattr(lib(), "ssm_" + name)(ctypes.byref(args), _P(stream or None))
+    if st != 0:
+        raise SSMError(st, "ssm_" + name)
+
+
+def _like_tokens(name, t, x):
+    if t is None:
+        return
+    if tuple(t.shape) != tuple(x.shape):
+        raise ValueError(f"{name} must be shaped like x")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have dim stride 1")
+
+
+def _set_tokens(a, name, t):
+    """Pointer and (batch, token) strides; a packed (tokens, dim) tensor is one batch row."""
+    setattr(a, name, _ptr(t))
+    setattr(a, name + "_batch_stride", t.stride(0) if t.dim() == 3 else 0)
+    setattr(a, name + "_seq_stride", t.stride(-2))
+
+
+def _gated_setup(a, x, gate_a, gate_x, lam, c, h0, cu_seqlens):
+    """Checks and fields that the gated scan and its backward share; returns the
+    number of sequences."""
+    torch = _torch()
+    if cu_seqlens is None and x.dim() != 3:
+        raise ValueError("x must be (batch, L, dim), or (tokens, dim) with cu_seqlens")
+    if cu_seqlens is not None and x.dim() != 2:
+        raise ValueError("x must be (tokens, dim) with cu_seqlens")
+    dev, dim = x.device, x.shape[-1]
+    code = _io_code(x)
+    _check_dev("x", x, dev, x.dtype)
+    for name, t in (("gate_a", gate_a), ("gate_x", gate_x)):
+        _check_dev(name, t, dev, x.dtype)
+    for name, t in (("x", x), ("gate_a", gate_a), ("gate_x", gate_x)):
+        _like_tokens(name, t, x)
+    _check_dev("lam", lam, dev, torch.float32)
+    _contig_f32("lam", lam, (dim,))
+    if cu_seqlens is not None:
+        _check_dev("cu_seqlens", cu_seqlens, dev, torch.int32)
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1 or not cu_seqlens.is_contiguous():
+            raise ValueError("cu_seqlens must be a contiguous int32 vector of nseq + 1 entries")
+    n = x.shape[0] if cu_seqlens is None else cu_seqlens.numel() - 1
+    _check_dev("h0", h0, dev, torch.float32)
+    _contig_f32("h0", h0, (n, dim))
+    c = float(c)
+    if not 0.0 < c < float("inf"):
+        raise ValueError("c must be positive and finite")
+    a.batch, a.seqlen, a.dim = (x.shape[0] if cu_seqlens is None else 1), x.shape[-2], dim
+    a.nseq, a.io_dtype, a.c = (0 if cu_seqlens is None else n), code, c
+    for name, t in (("x", x), ("gate_a", gate_a), ("gate_x", gate_x)):
+        _set_tokens(a, name, t)
+    a.lam, a.h0, a.cu_seqlens = _ptr(lam), _ptr(h0), _ptr(cu_seqlens)
+    return n
+
+
+def _set_workspace(a, need, workspace, device):
+    torch = _torch()
+    if not need:
+        return None
+    if workspace is None or workspace.numel() * workspace.element_size() < need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    _check_dev("workspace", workspace, device)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
+    return workspace
+
+
+def gated_checkpoint_shape(shape):
+    """Shape of the fp32 checkpoints that gated_scan_fwd writes for the
+    backward, for x of the given shape."""
+    shape = tuple(shape)
+    return shape[:-2] + ((shape[-2] + CHECKPOINT_TOKENS - 1) // CHECKPOINT_TOKENS, shape[-1])
+
+
+def gated_scan_fwd(x, gate_a, gate_x, lam, c=8.0, h0=None, cu_seqlens=None, return_last_state=False,
+                   out=None, last_state=None, checkpoints=None, stream=None, workspace=None):
+    """Gated linear recurrence over whole sequences on the GPU:
+        a_t = exp(-c softplus(lam) sigmoid(gate_a_t))
+        h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(gate_x_t) x_t,   out_t = h_t
+
+    x, gate_a, gate_x: (batch, L, dim), or (tokens, dim) with cu_seqlens, the
+    int32 device tensor of nseq + 1 sequence bounds; dim stride 1, any token
+    stride, float32 or bfloat16.  lam (dim,) fp32; h0 (batch or nseq, dim)
+    fp32.  Returns out, or (out, last_state); an empty sequence's last state
+    is its h0.  Tokens outside every sequence: zero rows in an `out` made
+    here, left as they were in one that is given.
+    `checkpoints` (optional): an fp32 tensor of gated_checkpoint_shape(x.shape)
+    for gated_scan_bwd.  `last_state` may be h0 itself.  `workspace`: a device
+    tensor reused across calls (by one call at a time); None allocates one."""
+    torch = _torch()
+    a = GatedArgs()
+    n = _gated_setup(a, x, gate_a, gate_x, lam, c, h0, cu_seqlens)
+    dev, dim = x.device, x.shape[-1]
+    _check_dev("out", out, dev, x.dtype)
+    _like_tokens("out", out, x)
+    for name, t, shape in (("last_state", last_state, (n, dim)),
+                           ("checkpoints", checkpoints, gated_checkpoint_shape(x.shape))):
+        _check_dev(name, t, dev, torch.float32)
+        _contig_f32(name, t, shape)
+    with _on(dev, stream) as s:
+        if out is None:
+            a.zero_outside = 1
+            out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        if return_last_state and last_state is None:
+            last_state = torch.empty((n, dim), dtype=torch.float32, device=dev)
+        _set_tokens(a, "out", out)
+        a.last_state, a.checkpoints = _ptr(last_state), _ptr(checkpoints)
+        workspace = _set_workspace(a, gated_scan_workspace_size(a), workspace, dev)
+        _launch("gated_scan_fwd", a, s)
+    return (out, last_state) if return_last_state else out
+
+
+def gated_scan_bwd(dout, x, gate_a, gate_x, lam, checkpoints, c=8.0, h0=None, cu_seqlens=None,
+                   dlast=None, stream=None, workspace=None):
+    """Gradients of gated_scan_fwd for the upstream gradient dout on out (and
+    dlast on last_state), from the checkpoints that forward wrote.  Returns a
+    dict: dx, dgate_a, dgate_x (like x), dlam (fp32) and, with h0, dh0 (fp32).
+    Rows of tokens outside every sequence are zero.  Every output is the same
+    bits from run to run.  `workspace`: as for gated_scan_fwd."""
+    torch = _torch()
+    a = GatedBwdArgs()
+    n = _gated_setup(a, x, gate_a, gate_x, lam, c, h0, cu_seqlens)
+    dev, dim = x.device, x.shape[-1]
+    _check_dev("dout", dout, dev, x.dtype)
+    _like_tokens("dout", dout, x)
+    for name, t, shape in (("dlast", dlast, (n, dim)),
+                           ("checkpoints", checkpoints, gated_checkpoint_shape(x.shape))):
+        _check_dev(name, t, dev, torch.float32)
+        _contig_f32(name, t, shape)
+    with _on(dev, stream) as s:
+        g = {k: torch.empty(x.shape, dtype=x.dtype, device=dev) for k in ("dx", "dgate_a", "dgate_x")}
+        for k, t in g.items():
+            _set_tokens(a, k, t)
+        g["dlam"] = torch.empty(dim, dtype=torch.float32, device=dev)
+        if h0 is not None:
+            g["dh0"] = torch.empty((n, dim), dtype=torch.float32, device=dev)
+        _set_tokens(a, "dout", dout)
+        a.checkpoints, a.dlast = _ptr(checkpoints), _ptr(dlast)
+        a.dlam, a.dh0 = _ptr(g["dlam"]), _ptr(g.get("dh0"))
+        workspace = _set_workspace(a, gated_scan_bwd_workspace_size(a), workspace, dev)
+        _launch("gated_scan_bwd", a, s)
+    return g
+
+
+def gated_scan(x, gate_a, gate_x, lam, c=8.0, h0=None, cu_seqlens=None, return_last_state=False):
+    """gated_scan_fwd as a differentiable torch op: gradients flow to x,
+    gate_a, gate_x, lam and h0, from out and from the last state."""
+    torch = _torch()
+
+    class _GatedScan(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, gate_a, gate_x, lam, h0):
+            ctx.set_materialize_grads(False)
+            ck = torch.empty(gated_checkpoint_shape(x.shape), dtype=torch.float32, device=x.device)
+            out, last = gated_scan_fwd(x, gate_a, gate_x, lam, c=c, h0=h0, cu_seqlens=cu_seqlens,
+                                       return_last_state=True, checkpoints=ck)
+            ctx.save_for_backward(x, gate_a, gate_x, lam, h0, cu_seqlens, ck)
+            return out, last
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, dout, dlast):
+            x, gate_a, gate_x, lam, h0, cu, ck = ctx.saved_tensors
+            dout = torch.zeros_like(x, memory_format=torch.contiguous_format) if dout is None else dout.contiguous()
+            g = gated_scan_bwd(dout, x, gate_a, gate_x, lam, ck, c=c, h0=h0, cu_seqlens=cu,
+                               dlast=None if dlast is None else dlast.contiguous())
+            return g["dx"], g["dgate_a"], g["dgate_x"], g["dlam"], g.get("dh0")
+
+    out, last = _GatedScan.apply(x, gate_a, gate_x, lam, h0)
+    return (out, last) if return_last_state else out
+
+
+def _check_slots(slots, batch, nslots, device):
+    torch = _torch()
+    if slots is None:
+        if batch > nslots:
+            raise ValueError("without slots, the batch must not be larger than the pool")
+        return
+    _check_dev("slots", slots, device, torch.int32)
+    if tuple(slots.shape) != (batch,) or not slots.is_contiguous():
+        raise ValueError("slots must be a contiguous int32 vector with one entry per batch row")
+
+
+def _check_row_tokens(name, t, batch, dim):
+    if t is not None and (tuple(t.shape) != (batch, dim) or (dim > 1 and t.stride(1) != 1)):
+        raise ValueError(f"{name} must be (batch, dim) with dim stride 1")
+
+
+def gated_state_update(state, x, gate_a, gate_x, lam, c=8.0, slots=None, out=None, stream=None):
+    """Single-token step of the gated recurrence; `state` (nslots, dim) fp32 is
+    updated in place.  x, gate_a, gate_x: (batch, dim).  slots: int32 (batch,),
+    the pool row of each batch row (None: row b on state b); a slot outside
+    the pool marks a padding row (no state touched, zero out), and rows naming
+    the same slot are taken in order."""
+    torch = _torch()
+    if state.dim() != 2 or x.dim() != 2:
+        raise ValueError("state must be (nslots, dim) and x (batch, dim)")
+    (nslots, dim), batch, dev = state.shape, x.shape[0], state.device
+    a = GatedUpdateArgs()
+    a.io_dtype = _io_code(x)
+    _check_dev("state", state, dev, torch.float32)
+    if dim > 1 and state.stride(1) != 1:
+        raise ValueError("state must have dim stride 1")
+    for name, t in (("x", x), ("gate_a", gate_a), ("gate_x", gate_x), ("out", out)):
+        _check_dev(name, t, dev, x.dtype)
+        _check_row_tokens(name, t, batch, dim)
+    _check_dev("lam", lam, dev, torch.float32)
+    _contig_f32("lam", lam, (dim,))
+    _check_slots(slots, batch, nslots, dev)
+    c = float(c)
+    if not 0.0 < c < float("inf"):
+        raise ValueError("c must be positive and finite")
+    with _on(dev, stream) as s:
+        if out is None:
+            out = torch.empty((batch, dim), dtype=x.dtype, device=dev)
+        a.batch, a.nslots, a.dim, a.c = batch, nslots, dim, c
+        a.state, a.state_slot_stride = _ptr(state), state.stride(0)
+        for name, t in (("x", x), ("gate_a", gate_a), ("gate_x", gate_x), ("out", out)):
+            setattr(a, name, _ptr(t))
+            setattr(a, name + "_batch_stride", t.stride(0))
+        a.lam, a.slots = _ptr(lam), _ptr(slots)
+        _launch("gated_state_update", a, s)
+    return out
+
+
+def state_cache_shape(nslots, shape, format="int8"):
+    """Shapes of the two uint8 tensors (codes, scales) of a cache of nslots
+    states of the given shape; its last axis is cut into blocks of
+    CACHE_BLOCK values with one scale each."""
+    shape = tuple(shape)
+    if format not in CACHE_FORMATS:
+        raise ValueError(f"format must be one of {sorted(CACHE_FORMATS)}")
+    if not shape:
+        raise ValueError("a state has at least one axis")
+    if format == "fp4" and shape[-1] % 2:
+        raise ValueError("fp4 needs an even last axis")
+    held = shape[-1] // 2 if format == "fp4" else shape[-1]
+    return (nslots,) + shape[:-1] + (held,), (nslots,) + shape[:-1] + (-(-shape[-1] // CACHE_BLOCK),)
+
+
+def _inner_contiguous(t):
+    """Whether each t[i] is contiguous."""
+    return t.shape[0] == 0 or t[0].is_contiguous()
+
+
+def _cache_setup(a, codes, scales, shape, format):
+    """Checks and fields of a cache's two tensors for states of a shape."""
+    torch = _torch()
+    dev, n = codes.device, codes.shape[0] if codes.dim() else 0
+    want = state_cache_shape(n, shape, format)
+    for name, t, w in (("codes", codes, want[0]), ("scales", scales, want[1])):
+        _check_dev(name, t, dev, torch.uint8)
+        if tuple(t.shape) != w:
+            raise ValueError(f"{name} must have shape {w} for this state and format, got {tuple(t.shape)}")
+        if not _inner_contiguous(t):
+            raise ValueError(f"{name} must be contiguous within a slot")
+    a.nslots = n
+    a.codes, a.codes_slot_stride = _ptr(codes), codes.stride(0)
+    a.scales, a.scales_slot_stride = _ptr(scales), scales.stride(0)
+    return n
+
+
+def _cache_args(codes, scales, states, slots, format):
+    if states.dim() < 2:
+        raise ValueError("states must be (batch, ...)")
+    dev, batch = codes.device, states.shape[0]
+    a = StateCacheArgs()
+    n = _cache_setup(a, codes, scales, states.shape[1:], format)
+    _check_dev("states", states, dev, states.dtype)
+    a.io_dtype, a.format = _io_code(states), CACHE_FORMATS[format]
+    if not _inner_contiguous(states):
+        raise ValueError("states must be contiguous within a batch row")
+    _check_slots(slots, batch, n, dev)
+    a.batch, a.inner = batch, states.shape[-1]
+    a.outer = math.prod(states.shape[1:-1])
+    a.states, a.states_batch_stride, a.slots = _ptr(states), states.stride(0), _ptr(slots)
+    return a
+
+
+def state_cache_write(codes, scales, states, slots=None, format="int8", stream=None):
+    """Quantise states (batch, *shape), float32 or bfloat16, into slots of a
+    cache (codes, scales: uint8, of state_cache_shape(nslots, shape, format)).
+    Each block of 32 values along the last axis shares a power-of-two scale;
+    int8, e4m3 ("fp8") or e2m1 ("fp4") codes, rounded to nearest even.
+    slots: int32 (batch,); None: row b to slot b.  A slot outside the cache is
+    not written; of rows naming the same slot the last is.  A block with a NaN
+    or an infinity reads back as NaN."""
+    a = _cache_args(codes, scales, states, slots, format)
+    with _on(codes.device, stream) as s:
+        _launch("state_cache_write", a, s)
+
+
+def state_cache_read(codes, scales, slots=None, format="int8", dtype=None, out=None, stream=None):
+    """The states held in slots of a cache (all of it without slots), as
+    float32 or `dtype` bfloat16, or into `out`.  A slot outside the cache reads
+    as a zero state."""
+    torch = _torch()
+    if codes.dim() < 2:
+        raise ValueError("codes must be (nslots, ...)")
+    if format not in CACHE_FORMATS:
+        raise ValueError(f"format must be one of {sorted(CACHE_FORMATS)}")
+    batch = codes.shape[0] if slots is None else slots.shape[0]
+    shape = (batch,) + tuple(codes.shape[1:-1]) + (codes.shape[-1] * (2 if format == "fp4" else 1),)
+    if out is not None and (tuple(out.shape) != shape or (dtype is not None and out.dtype != dtype)):
+        raise ValueError(f"out must have shape {shape} and the dtype asked for")
+    with _on(codes.device, stream) as s:
+        if out is None:
+            out = torch.empty(shape, dtype=dtype or torch.float32, device=codes.device)
+        _launch("state_cache_read", _cache_args(codes, scales, out, slots, format), s)
+    return out
+
+
+def selective_state_update_cached(codes, scales, x, dt, A, B, C, D=None, z=None, dt_bias=None,
+                                  dt_softplus=True, slots=None, seed=None, out=None, stream=None):
+    """selective_state_update on states held in an int8 cache, updated in place:
+    codes (nslots, dim, dstate) and scales (nslots, dim, ceil(dstate / 32)),
+    uint8, as state_cache_write fills them.  slots: int32 (batch,), the slot of
+    each batch row (None: row b on slot b); a slot outside the cache marks a
+    padding row (no state touched, zero out), and rows naming the same slot are
+    taken in order.  seed: an int64 device tensor of one element; the new
+    states are then rounded stochastically (unbiased), with random bytes that
+    its value determines: give every step another value.  None rounds to
+    nearest, in which changes below half a code are lost.  out is computed
+    before the rounding."""
+    torch = _torch()
+    if codes.dim() != 3 or x.dim() != 2:
+        raise ValueError("codes must be (nslots, dim, dstate) and x (batch, dim)")
+    (nslots, dim, N), batch, dev, io = codes.shape, x.shape[0], codes.device, x.dtype
+    a = CachedUpdateArgs()
+    a.io_dtype, a.dt_softplus = _io_code(x), int(bool(dt_softplus))
+    _cache_setup(a, codes, scales, (dim, N), "int8")
+    for name, t in (("x", x), ("dt", dt), ("z", z), ("out", out)):
+        _check_dev(name, t, dev, io)
+        _check_row_tokens(name, t, batch, dim)
+    for name, t in (("B", B), ("C", C)):
+        _check_dev(name, t, dev, io)
+        if N > 1 and t.stride(-1) != 1:
+            raise ValueError(f"{name} must have state stride 1")
+    G = _bc_groups(B, C, batch, dim, N, ())
+    for name, t in (("A", A), ("D", D), ("dt_bias", dt_bias)):
+        _check_dev(name, t, dev, torch.float32)
+    if tuple(A.shape) != (dim, N) or (N > 1 and A.stride(1) != 1):
+        raise ValueError("A must be (dim, dstate) with state stride 1")
+    _contig_f32("D", D, (dim,))
+    _contig_f32("dt_bias", dt_bias, (dim,))
+    _check_slots(slots, batch, nslots, dev)
+    if seed is not None:
+        _check_dev("seed", seed, dev, torch.int64)
+        if seed.numel() != 1:
+            raise ValueError("seed must hold one int64")
+    with _on(dev, stream) as s:
+        if out is None:
+            out = torch.empty((batch, dim), dtype=io, device=dev)
+        a.batch, a.dim, a.dstate = batch, dim, N
+        for name, t in (("x", x), ("dt", dt), ("z", z), ("out", out)):
+            if t is not None:
+                setattr(a, name, _ptr(t))
+                setattr(a, name + "_batch_stride", t.stride(0))
+        _set_bc(a, B, C, G, time=False)
+        a.A, a.A_dim_stride, a.D, a.dt_bias = _ptr(A), A.stride(0), _ptr(D), _ptr(dt_bias)
+        a.slots, a.seed = _ptr(slots), _ptr(seed)
+        _launch("selective_state_update_cached", a, s)
+    return out

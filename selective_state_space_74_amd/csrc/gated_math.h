@@ -1,0 +1,30 @@
+// The gated recurrence's per-token arithmetic, shared by its forward, backward
+// and single-token kernels.
+#pragma once
+
+#include "ssm_internal.h"
+
+namespace ssm {
+
+constexpr int kCkpt = SSM_CHECKPOINT_TOKENS;
+
+// 1 / (1 + e^-z) on the hardware exp2 and reciprocal: 0 and 1 at -inf and inf.
+__device__ __forceinline__ float sigmoid_f32(float z) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-z * kLog2e));
+}
+
+// 1 - a^2 for a = e^-v, v >= 0.  Below 2v = 1/4 the difference would cancel
+// (a layer that remembers thousands of tokens sits at v ~ 1e-3), so the series
+// of 1 - e^-u, u = 2v, is summed instead: its first omitted term, u^7 / 5040,
+// is under 2^-24 of the sum there.  Above, 1 - a^2 >= 0.22 keeps full accuracy.
+__device__ __forceinline__ float one_minus_square(float a, float v) {
+  const float u = 2.0f * v;
+  float s = fmaf(u, -1.0f / 6.0f, 1.0f);
+  s = fmaf(u * s, -1.0f / 5.0f, 1.0f);
+  s = fmaf(u * s, -1.0f / 4.0f, 1.0f);
+  s = fmaf(u * s, -1.0f / 3.0f, 1.0f);
+  s = fmaf(u * s, -1.0f / 2.0f, 1.0f);
+  return u < 0.25f ? u * s : fmaf(-a, a, 1.0f);
+}
+
+}  // namespace ssm

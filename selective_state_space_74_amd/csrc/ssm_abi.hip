@@ -4,58 +4,10 @@
 #include <stdint.h>
 #include <string.h>
 
+#include "abi_checks.h"
 #include "ssm_internal.h"
 
-namespace {
-
-struct Span {  // byte range [lo, hi)
-  uintptr_t lo = 0, hi = 0;
-  bool empty() const { return hi <= lo; }
-};
-
-bool overlap(const Span& a, const Span& b) {
-  return !a.empty() && !b.empty() && a.lo < b.hi && b.lo < a.hi;
-}
-
-// Bytes touched by a (n0, n1, n2) tensor with strides (s0, s1, 1).
-Span span3(const void* p, int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t n2,
-           int64_t esz) {
-  Span s;
-  if (!p || n0 <= 0 || n1 <= 0 || n2 <= 0) return s;
-  s.lo = reinterpret_cast<uintptr_t>(p);
-  s.hi = s.lo + static_cast<uintptr_t>(((n0 - 1) * s0 + (n1 - 1) * s1 + n2) * esz);
-  return s;
-}
-
-Span span1(const void* p, int64_t n, int64_t esz) { return span3(p, 1, 0, 1, 0, n, esz); }
-
-// Bytes touched by a (n0, n1, n2, n3) tensor with strides (s0, s1, s2, 1).
-Span span4(const void* p, int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t n2,
-           int64_t s2, int64_t n3, int64_t esz) {
-  Span s;
-  if (!p || n0 <= 0 || n1 <= 0 || n2 <= 0 || n3 <= 0) return s;
-  s.lo = reinterpret_cast<uintptr_t>(p);
-  s.hi = s.lo + static_cast<uintptr_t>(((n0 - 1) * s0 + (n1 - 1) * s1 + (n2 - 1) * s2 + n3) * esz);
-  return s;
-}
-
-// B/C groups: 0 or 1 is one group; otherwise it must divide dim.
-int64_t groups_of(int64_t ngroups) { return ngroups > 1 ? ngroups : 1; }
-bool bad_groups(int64_t ngroups, int64_t dim) {
-  return ngroups < 0 || (dim > 0 && dim % groups_of(ngroups) != 0);
-}
-
-bool misaligned(const void* p, int64_t align) {
-  return p && (reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(align)) != 0;
-}
-
-int64_t io_size(int32_t dt) { return dt == SSM_BF16 ? 2 : 4; }
-
-// Token indices are 32-bit inside the scan kernel.
-constexpr int64_t kMaxSeqlen = (int64_t{1} << 31) - 64;
-constexpr int64_t kCkptTokens = SSM_CHECKPOINT_TOKENS;
-
-}  // namespace
+using namespace ssm;  // the checks of abi_checks.h
 
 extern "C" {
 
@@ -93,7 +45,7 @@ const char* ssm_status_string(int status) {
     case SSM_ERR_ALIAS: return "an output overlaps an input";
     case SSM_ERR_UNSUPPORTED: return "unsupported configuration (dstate or B/C groups outside what is built, or a size past the limits in ssm.h)";
     case SSM_ERR_HIP: return "HIP runtime error at launch";
-    case SSM_ERR_SCRATCH: return "the scan needs more segment scratch than the no-allocation entry point's static buffer (SSM_NOALLOC_SCRATCH_BYTES) holds";
+    case SSM_ERR_SCRATCH: return "the scan needs more segment scratch than the no-allocation entry point's static buffer (SSM_NOALLOC_SCRATCH_BYTES) holds, or a required workspace is missing or too small";
     default: return "unknown status";
   }
 }

@@ -22,6 +22,14 @@ bool scan_bwd_windows_fit(const ssm_scan_bwd_args& a);
 size_t scan_bwd_workspace_bytes(const ssm_scan_bwd_args& a);
 hipError_t launch_ssd_fwd(const ssm_ssd_args& a, hipStream_t stream);
 size_t ssd_workspace_bytes(const ssm_ssd_args& a);
+hipError_t launch_gated_fwd(const ssm_gated_args& a, hipStream_t stream);
+size_t gated_workspace_bytes(const ssm_gated_args& a);
+hipError_t launch_gated_bwd(const ssm_gated_bwd_args& a, hipStream_t stream);
+size_t gated_bwd_workspace_bytes(const ssm_gated_bwd_args& a);
+hipError_t launch_gated_step(const ssm_gated_update_args& a, hipStream_t stream);
+hipError_t launch_cache_write(const ssm_state_cache_args& a, hipStream_t stream);
+hipError_t launch_cache_read(const ssm_state_cache_args& a, hipStream_t stream);
+hipError_t launch_cached_update(const ssm_cached_update_args& a, hipStream_t stream);
 
 // ---------------------------------------------------------------------------
 // Device helpers.

@@ -1,0 +1,248 @@
+"""Host-side checks of the gated recurrence and the state cache: every argument
+block is validated without touching a GPU (the addresses are made up)."""
+import ctypes
+import os
+import re
+
+import pytest
+
+import selective_state_space_74_amd as ssm
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+OK, NULL, SHAPE, STRIDE, DTYPE, ALIGN, ALIAS, UNSUP, SCRATCH = 0, 1, 2, 3, 4, 5, 6, 7, 9
+BASE = 0x7F0000000000
+
+
+def addr(i):
+    return BASE + (i << 32)
+
+
+def good_gated(batch=2, L=64, D=32, io=0, packed=False):
+    a = ssm.GatedArgs()
+    a.batch, a.seqlen, a.dim, a.io_dtype, a.c = batch, L, D, io, 8.0
+    for i, k in enumerate(("x", "gate_a", "gate_x", "out")):
+        setattr(a, k, addr(i))
+        setattr(a, k + "_batch_stride", L * D)
+        setattr(a, k + "_seq_stride", D)
+    a.lam, a.h0, a.last_state, a.checkpoints = addr(5), addr(6), addr(7), addr(8)
+    if packed:
+        a.batch, a.nseq, a.cu_seqlens = 1, 5, addr(9)
+    need = ssm.gated_scan_workspace_size(a)
+    if need:
+        a.workspace, a.workspace_bytes = addr(10), need
+    return a
+
+
+def good_bwd(**kw):
+    f = good_gated(**kw)
+    a = ssm.GatedBwdArgs()
+    for k in ("batch", "seqlen", "dim", "nseq", "io_dtype", "c", "lam", "h0", "cu_seqlens", "checkpoints"):
+        setattr(a, k, getattr(f, k))
+    for i, k in enumerate(("x", "gate_a", "gate_x", "dout", "dx", "dgate_a", "dgate_x")):
+        setattr(a, k, addr(20 + i))
+        setattr(a, k + "_batch_stride", f.seqlen * f.dim)
+        setattr(a, k + "_seq_stride", f.dim)
+    a.dlast, a.dlam, a.dh0 = addr(30), addr(31), addr(32)
+    a.workspace, a.workspace_bytes = addr(33), ssm.gated_scan_bwd_workspace_size(a)
+    return a
+
+
+def good_step(batch=4, nslots=9, D=64, io=1):
+    a = ssm.GatedUpdateArgs()
+    a.batch, a.nslots, a.dim, a.io_dtype, a.c = batch, nslots, D, io, 8.0
+    a.state, a.state_slot_stride = addr(0), D
+    for i, k in enumerate(("x", "gate_a", "gate_x", "out")):
+        setattr(a, k, addr(1 + i))
+        setattr(a, k + "_batch_stride", D)
+    a.lam, a.slots = addr(6), addr(7)
+    return a
+
+
+def good_cache(batch=3, nslots=8, outer=20, inner=16, format=0, io=0):
+    a = ssm.StateCacheArgs()
+    a.batch, a.nslots, a.outer, a.inner, a.format, a.io_dtype = batch, nslots, outer, inner, format, io
+    a.codes, a.codes_slot_stride = addr(0), outer * inner // (2 if format == 2 else 1)
+    a.scales, a.scales_slot_stride = addr(1), outer * -(-inner // 32)
+    a.states, a.states_batch_stride, a.slots = addr(2), outer * inner, addr(3)
+    return a
+
+
+def good_cached(batch=4, nslots=9, D=64, N=16, io=1, G=0):
+    a = ssm.CachedUpdateArgs()
+    a.batch, a.nslots, a.dim, a.dstate, a.io_dtype, a.dt_softplus, a.ngroups = batch, nslots, D, N, io, 1, G
+    a.codes, a.codes_slot_stride = addr(0), D * N
+    a.scales, a.scales_slot_stride = addr(1), D * -(-N // 32)
+    for i, k in enumerate(("x", "dt", "z", "out")):
+        setattr(a, k, addr(2 + i))
+        setattr(a, k + "_batch_stride", D)
+    for i, k in enumerate(("B", "C")):
+        setattr(a, k, addr(6 + i))
+        setattr(a, k + "_batch_stride", max(G, 1) * N)
+        setattr(a, k + "_group_stride", N)
+    a.A, a.A_dim_stride, a.D, a.dt_bias = addr(8), N, addr(9), addr(10)
+    a.slots, a.seed = addr(11), addr(12)
+    return a
+
+
+def expect(make, check, status, **fields):
+    a = make()
+    for k, v in fields.items():
+        setattr(a, k, v)
+    assert check(a) == status, (fields, check(a))
+
+
+def test_struct_sizes_and_constants():
+    L = ssm.lib()
+    for name, T in (("gated", ssm.GatedArgs), ("gated_bwd", ssm.GatedBwdArgs), ("gated_update", ssm.GatedUpdateArgs),
+                    ("state_cache", ssm.StateCacheArgs), ("cached_update", ssm.CachedUpdateArgs)):
+        assert getattr(L, f"ssm_{name}_args_size")() == ctypes.sizeof(T)
+    header = open(os.path.join(ROOT, "include", "ssm.h")).read()
+    assert f"#define SSM_CACHE_BLOCK {ssm.CACHE_BLOCK}" in header
+    for k, v in ssm.CACHE_FORMATS.items():
+        assert re.search(rf"SSM_CACHE_{k.upper()} = {v}\b", header)
+
+
+def test_good_blocks_pass():
+    for io in (0, 1):
+        for packed in (False, True):
+            assert ssm.validate_gated(good_gated(io=io, packed=packed)) == OK
+            assert ssm.validate_gated_bwd(good_bwd(io=io, packed=packed)) == OK
+        assert ssm.validate_gated_update(good_step(io=io)) == OK
+        for f in range(3):
+            a = good_cache(format=f, io=io)
+            assert ssm.validate_state_cache_write(a) == OK and ssm.validate_state_cache_read(a) == OK
+        for N in (1, 16, 20, 64):
+            assert ssm.validate_cached_update(good_cached(io=io, N=N, G=4)) == OK
+
+
+def test_null_blocks():
+    for f in ("gated", "gated_bwd", "gated_update", "state_cache_write", "state_cache_read", "cached_update"):
+        assert getattr(ssm.lib(), "ssm_validate_" + f)(None) == NULL
+    for f in ("gated_scan_fwd", "gated_scan_bwd", "gated_state_update", "state_cache_write", "state_cache_read",
+              "selective_state_update_cached"):
+        assert getattr(ssm.lib(), "ssm_" + f)(None, None) == NULL
+    assert ssm.lib().ssm_gated_scan_workspace_size(None) == 0
+
+
+@pytest.mark.parametrize("make,check", [(good_gated, ssm.validate_gated), (good_bwd, ssm.validate_gated_bwd)])
+def test_gated_refusals(make, check):
+    e = lambda status, **f: expect(make, check, status, **f)  # noqa: E731
+    e(SHAPE, batch=-1), e(SHAPE, seqlen=-1), e(SHAPE, dim=-1), e(SHAPE, nseq=-1)
+    e(SHAPE, cu_seqlens=addr(9), batch=2)
+    for c in (0.0, -1.0, float("nan"), float("inf")):
+        e(SHAPE, c=c)
+    e(DTYPE, io_dtype=2)
+    e(UNSUP, seqlen=(1 << 31) - 63)
+    e(UNSUP, batch=1 << 20, seqlen=1 << 20)
+    for k in ("x", "gate_a", "gate_x", "lam"):
+        e(NULL, **{k: None})
+    for k in ("x", "gate_a", "gate_x"):
+        e(STRIDE, **{k + "_seq_stride": -1})
+        e(ALIGN, **{k: addr(40) + 2})
+    e(ALIGN, h0=addr(40) + 2), e(ALIGN, checkpoints=addr(40) + 1)
+
+
+def test_gated_forward_refusals():
+    e = lambda status, **f: expect(good_gated, ssm.validate_gated, status, **f)  # noqa: E731
+    e(NULL, out=None)
+    e(ALIAS, out=addr(0)), e(ALIAS, out=addr(5)), e(ALIAS, last_state=addr(0)), e(ALIAS, checkpoints=addr(2))
+    e(OK, last_state=addr(6)), e(ALIAS, last_state=addr(6) + 4)
+    e(ALIAS, out_seq_stride=16), e(ALIAS, out_seq_stride=0), e(ALIAS, out_batch_stride=0)
+    # sequence-major rows: batch rows interleave without colliding
+    e(OK, out_seq_stride=64, out_batch_stride=32)
+    # out and x as the halves of one tensor
+    half = dict(x_seq_stride=64, x_batch_stride=64 * 64, out_seq_stride=64, out_batch_stride=64 * 64)
+    e(OK, out=addr(0) + 32 * 4, **half), e(ALIAS, out=addr(0) + 31 * 4, **half), e(ALIAS, out=addr(0) + 33 * 4, **half)
+
+
+def test_gated_workspace_is_required():
+    a = good_bwd()
+    a.workspace_bytes -= 1
+    assert ssm.validate_gated_bwd(a) == SCRATCH
+    a = good_bwd()
+    a.workspace = None
+    assert ssm.validate_gated_bwd(a) == SCRATCH
+    assert "workspace" in ssm.status_string(SCRATCH)
+    a = good_bwd()
+    a.workspace = addr(20)
+    assert ssm.validate_gated_bwd(a) == ALIAS
+    a = good_gated(packed=True)
+    if a.workspace_bytes:
+        a.workspace_bytes -= 1
+        assert ssm.validate_gated(a) == SCRATCH
+
+
+def test_gated_backward_refusals():
+    e = lambda status, **f: expect(good_bwd, ssm.validate_gated_bwd, status, **f)  # noqa: E731
+    for k in ("checkpoints", "dout", "dx", "dgate_a", "dgate_x", "dlam"):
+        e(NULL, **{k: None})
+    e(ALIAS, dx=addr(20)), e(ALIAS, dgate_a=addr(24)), e(ALIAS, dlam=addr(30)), e(ALIAS, dh0=addr(6))
+    e(ALIAS, dx_seq_stride=1)
+    half = dict(dgate_a_seq_stride=64, dgate_a_batch_stride=4096, dgate_x_seq_stride=64, dgate_x_batch_stride=4096)
+    e(OK, dgate_x=addr(25) + 128, **half), e(ALIAS, dgate_x=addr(25) + 124, **half)
+
+
+def test_step_refusals():
+    e = lambda status, **f: expect(good_step, ssm.validate_gated_update, status, **f)  # noqa: E731
+    e(SHAPE, batch=-1), e(SHAPE, c=0.0), e(DTYPE, io_dtype=7), e(UNSUP, batch=65536)
+    e(SHAPE, slots=None, batch=10), e(OK, slots=None), e(OK, nslots=0), e(OK, batch=0)
+    for k in ("state", "x", "gate_a", "gate_x", "lam", "out"):
+        e(NULL, **{k: None})
+    e(STRIDE, x_batch_stride=-1), e(STRIDE, state_slot_stride=-1)
+    e(ALIGN, state=addr(0) + 2), e(ALIGN, x=addr(1) + 1), e(ALIGN, slots=addr(7) + 2)
+    e(ALIAS, out=addr(0)), e(ALIAS, out=addr(1)), e(ALIAS, state=addr(6)), e(ALIAS, state_slot_stride=63)
+    e(ALIAS, out_batch_stride=8)
+
+
+def test_cache_refusals():
+    for check in (ssm.validate_state_cache_write, ssm.validate_state_cache_read):
+        e = lambda status, **f: expect(good_cache, check, status, **f)  # noqa: E731
+        e(SHAPE, batch=-1), e(SHAPE, outer=-1), e(SHAPE, inner=-1), e(SHAPE, slots=None, batch=9), e(OK, slots=None)
+        e(SHAPE, format=2, inner=15), e(DTYPE, format=3), e(DTYPE, io_dtype=2)
+        e(UNSUP, batch=65536), e(UNSUP, outer=1 << 31), e(UNSUP, inner=1 << 31)
+        for k in ("codes", "scales", "states"):
+            e(NULL, **{k: None})
+        e(STRIDE, codes_slot_stride=-1), e(ALIGN, states=addr(2) + 2), e(ALIAS, codes=addr(2))
+    w = lambda status, **f: expect(good_cache, ssm.validate_state_cache_write, status, **f)  # noqa: E731
+    w(ALIAS, codes_slot_stride=319), w(ALIAS, scales=addr(0)), w(ALIAS, codes=addr(3))
+    # a read may take one slot's codes for every row, or one row of states for a write
+    expect(good_cache, ssm.validate_state_cache_read, OK, codes_slot_stride=0, scales_slot_stride=0)
+    expect(good_cache, ssm.validate_state_cache_read, ALIAS, states_batch_stride=319)
+    w(OK, states_batch_stride=0)
+
+
+def test_cached_update_refusals():
+    e = lambda status, **f: expect(good_cached, ssm.validate_cached_update, status, **f)  # noqa: E731
+    e(SHAPE, batch=-1), e(SHAPE, dstate=0), e(SHAPE, ngroups=5), e(SHAPE, slots=None, batch=10), e(OK, slots=None)
+    e(UNSUP, dstate=65), e(UNSUP, batch=65536), e(DTYPE, io_dtype=2)
+    for k in ("codes", "scales", "x", "dt", "B", "C", "A", "out"):
+        e(NULL, **{k: None})
+    for k in ("z", "D", "dt_bias", "seed"):
+        e(OK, **{k: None})
+    e(STRIDE, B_batch_stride=-1), e(ALIGN, x=addr(2) + 1), e(ALIGN, seed=addr(12) + 4)
+    e(ALIAS, out=addr(0)), e(ALIAS, codes=addr(1)), e(ALIAS, scales=addr(8)), e(ALIAS, codes_slot_stride=1023)
+    e(ALIAS, out_batch_stride=63), e(ALIAS, codes=addr(12))
+
+
+def test_binding_refuses_host_tensors_and_wrong_shapes():
+    torch = pytest.importorskip("torch")
+    x = torch.zeros(2, 4, 8)
+    lam = torch.zeros(8)
+    with pytest.raises(ValueError):
+        ssm.gated_scan_fwd(x, x, x, lam)                              # not on a GPU
+    with pytest.raises(ValueError):
+        ssm.gated_scan_fwd(x[0], x[0], x[0], lam)                     # two axes need cu_seqlens
+    with pytest.raises(TypeError):
+        ssm.gated_scan_fwd(x.half(), x.half(), x.half(), lam)
+    with pytest.raises(ValueError):
+        ssm.gated_state_update(torch.zeros(3, 8), x[0], x[0], x[0], lam)
+    with pytest.raises(ValueError):
+        ssm.state_cache_shape(3, (4, 5), "fp4")
+    with pytest.raises(ValueError):
+        ssm.state_cache_shape(3, (4, 5), "int4")
+    assert ssm.state_cache_shape(3, (4, 70), "int8") == ((3, 4, 70), (3, 4, 3))
+    assert ssm.state_cache_shape(3, (4, 70), "fp4") == ((3, 4, 35), (3, 4, 3))
+    codes, scales = (torch.zeros(s, dtype=torch.uint8) for s in ssm.state_cache_shape(3, (4, 16)))
+    with pytest.raises(ValueError):
+        ssm.state_cache_write(codes, scales, torch.zeros(2, 4, 16))   # not on a GPU
+    assert ssm.gated_checkpoint_shape((2, 33, 7)) == (2, 3, 7) and ssm.gated_checkpoint_shape((0, 7)) == (0, 7)
