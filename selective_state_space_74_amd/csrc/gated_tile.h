@@ -1,0 +1,182 @@
+// Tiles, packed-sequence marks and the carry between tiles, shared by the
+// gated recurrence's forward and backward kernels.
+//
+// A workgroup takes kWaveTokens tokens per wavefront of a group of channels,
+// with its inputs kept in registers, so that the data is read once: the
+// recurrence over a tile is h_out = P h_in + H, and only (P, H) of each tile
+// has to travel to the tiles after it.
+//
+// The carry.  Tiles are numbered along the scan (backwards in time for the
+// adjoint) and every kChainGroup of them form a group.  A tile publishes its
+// (P, H) as soon as it has them, without waiting for anything.  It then takes
+// the state that left the group before, and folds the (P, H) of its
+// predecessors within the group into it, in order; the last tile of a group
+// publishes the state that leaves the group.  The order of the sums is fixed,
+// so results do not depend on which tile came first.
+//
+// Every wait ends.  A workgroup takes its tile from a counter (a ticket), so
+// the tiles before it are held by workgroups that already run (or have run),
+// whatever order the hardware dispatches in and whatever else shares the GPU.
+// The running workgroup with the lowest ticket only waits for words that
+// finished workgroups have written; hence it finishes, and so on upwards.
+// (Without tickets two such kernels on two streams could hold each other's
+// places: each resident on the compute units that the other's next tile
+// needs.)
+//
+// Words.  A pair travels as one 64-bit word, written and read by relaxed
+// atomics of device scope, so that no other memory needs ordering; the words
+// are filled with kNoWord before the kernel, which no published pair equals:
+// its low half would be one particular NaN, and NaNs are published as another.
+#pragma once
+
+#include "gated_math.h"
+
+namespace ssm {
+
+constexpr int kChainGroup = 16;
+constexpr uint64_t kNoWord = ~uint64_t{0};
+
+__device__ __forceinline__ uint64_t chain_word(float p, float h) {
+  const uint32_t lo = p != p ? 0x7fc00000u : __float_as_uint(p);
+  return lo | static_cast<uint64_t>(__float_as_uint(h)) << 32;
+}
+__device__ __forceinline__ float word_p(uint64_t w) { return __uint_as_float(static_cast<uint32_t>(w)); }
+__device__ __forceinline__ float word_h(uint64_t w) { return __uint_as_float(static_cast<uint32_t>(w >> 32)); }
+
+__device__ __forceinline__ void chain_store(uint64_t* p, uint64_t w) {
+  __hip_atomic_store(p, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint64_t chain_load(uint64_t* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint64_t chain_wait(uint64_t* p, uint64_t w) {
+  while (w == kNoWord) {
+    __builtin_amdgcn_s_sleep(1);
+    w = chain_load(p);
+  }
+  return w;
+}
+
+// A stretch of packed tokens in which a sequence begins passes nothing on.
+// That is not P = 0, which would turn an infinity or a NaN of the sequence
+// before into a NaN: it is marked by a negative P, which no product of decays
+// is.
+constexpr float kCut = -1.0f;
+template <bool PACKED>
+__device__ __forceinline__ float chain_apply(float p, float h, float in) {
+  const float r = fmaf(p, in, h);
+  return PACKED && p < 0.0f ? h : r;
+}
+// P of a stretch (p) followed by another (q).
+template <bool PACKED>
+__device__ __forceinline__ float chain_product(float p, float q) {
+  return PACKED && (p < 0.0f || q < 0.0f) ? kCut : p * q;
+}
+
+// Where one group of `width` channels of one batch row keeps its words: tile
+// k's pair at tiles[k * width], the state leaving group j at groups[j * width].
+struct Chain {
+  uint64_t* tiles;
+  uint64_t* groups;
+  int64_t width;
+};
+
+// The state entering tile k for one channel, whose own pair is (p, h); `first`
+// is the state entering tile 0.  Publishes the pair, and the state leaving
+// the group at its last tile.
+template <bool PACKED>
+__device__ __forceinline__ float chain_carry(const Chain& c, int64_t k, int64_t ntiles, int channel,
+                                             float p, float h, float first) {
+  uint64_t* const mine = c.tiles + k * c.width + channel;
+  const int in_group = static_cast<int>(k % kChainGroup);
+  const int64_t group = k / kChainGroup;
+  if (in_group != kChainGroup - 1) chain_store(mine, chain_word(p, h));
+  uint64_t w[kChainGroup];
+#pragma unroll
+  for (int i = 0; i < kChainGroup - 1; ++i)
+    if (i < in_group) w[i] = chain_load(mine - (in_group - i) * c.width);
+  float carry = first;
+  if (group > 0) {
+    uint64_t* const before = c.groups + (group - 1) * c.width + channel;
+    carry = word_h(chain_wait(before, chain_load(before)));
+  }
+#pragma unroll
+  for (int i = 0; i < kChainGroup - 1; ++i)
+    if (i < in_group) {
+      w[i] = chain_wait(mine - (in_group - i) * c.width, w[i]);
+      carry = chain_apply<PACKED>(word_p(w[i]), word_h(w[i]), carry);
+    }
+  if (in_group == kChainGroup - 1 && k + 1 < ntiles)
+    chain_store(c.groups + group * c.width + channel, chain_word(0.0f, chain_apply<PACKED>(p, h, carry)));
+  return carry;
+}
+
+// Marks of a packed token: the sequence it belongs to and whether it is its
+// first or last token; kOutside: in no sequence.
+constexpr int32_t kOutside = -1;   // its lowest bit, too, says that no state comes in
+__device__ __forceinline__ int32_t mark_of(int32_t seq, bool first, bool last) {
+  return seq << 2 | (first ? 1 : 0) | (last ? 2 : 0);
+}
+// Sequences are numbered below 2^29 (checked on the host).
+constexpr int64_t kMaxPacked = int64_t{1} << 29;
+
+// Before the scan: chain words to kNoWord, the ticket counter to 0, and with
+// cu_seqlens the token marks and the last states of empty sequences.
+// `empty_out` receives, for each empty sequence, the row of `empty_in` (or
+// zeros).
+struct PrepParams {
+  uint32_t* ticket;
+  uint64_t* words;
+  int64_t nwords;
+  const int32_t* cu;
+  int32_t* marks;
+  const float* empty_in;
+  float* empty_out;
+  int64_t L, nseq, D;
+};
+hipError_t launch_gated_prep(const PrepParams& p, hipStream_t stream);
+
+// V consecutive channels of one token as they are stored.
+template <typename T, int V> struct alignas(sizeof(T) * V) Raw { T v[V]; };
+
+template <typename T> __device__ __forceinline__ float widen(T v);
+template <> __device__ __forceinline__ float widen<float>(float v) { return v; }
+template <> __device__ __forceinline__ float widen<uint16_t>(uint16_t v) { return bf16_to_f32(v); }
+template <typename T> __device__ __forceinline__ T narrow(float v);
+template <> __device__ __forceinline__ float narrow<float>(float v) { return v; }
+template <> __device__ __forceinline__ uint16_t narrow<uint16_t>(float v) { return f32_to_bf16(v); }
+
+template <typename T, int V>
+__device__ __forceinline__ Raw<T, V> load_raw(const void* base, int64_t elements, uint32_t lane_bytes) {
+  return *reinterpret_cast<const Raw<T, V>*>(static_cast<const char*>(base) + elements * static_cast<int64_t>(sizeof(T)) +
+                                             lane_bytes);
+}
+
+constexpr int kWaveTokens = kCkpt;   // tokens of a wavefront: one checkpoint each
+constexpr int kMaxWaves = 8;
+
+// How a call is cut into workgroups, and the parts of its workspace (bytes
+// from its start, each 256-byte aligned).
+struct GatedPlan {
+  int waves;            // wavefronts a workgroup
+  int64_t tiles, cols;  // along the sequence, along the channels
+  int64_t words;        // 0: one tile a sequence, no chain
+  int64_t marks_at, words_at, parts_at, bytes;
+};
+
+inline GatedPlan gated_plan(int64_t batch, int64_t L, int64_t D, bool packed, int V, int64_t part_rows_per_tile) {
+  auto round256 = [](int64_t v) { return (v + 255) / 256 * 256; };
+  GatedPlan q{};
+  const int64_t blocks = (L + kWaveTokens - 1) / kWaveTokens;
+  q.waves = static_cast<int>(blocks < 1 ? 1 : blocks < kMaxWaves ? blocks : kMaxWaves);
+  q.tiles = (blocks + q.waves - 1) / q.waves;
+  q.cols = (D + 64 * V - 1) / (64 * V);
+  q.words = q.tiles > 1 ? batch * q.cols * (q.tiles + (q.tiles + kChainGroup - 1) / kChainGroup) * 64 * V : 0;
+  q.marks_at = q.words ? 256 : 0;   // the ticket counter
+  q.words_at = q.marks_at + (packed ? round256(blocks * kWaveTokens * 4) : 0);
+  q.parts_at = q.words_at + round256(q.words * 8);
+  q.bytes = q.parts_at + part_rows_per_tile * q.tiles * batch * D * 4;
+  return q;
+}
+
+}  // namespace ssm
