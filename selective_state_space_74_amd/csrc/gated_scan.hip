@@ -28,7 +28,7 @@ template <typename T, int V, bool PACKED, bool CHAIN>
 __global__ __launch_bounds__(64 * kMaxWaves) void gated_fwd_kernel(FwdParams p) {
   constexpr int W = 64 * V;
   __shared__ float2 pairs[kMaxWaves][W];
-  __shared__ float entering[W];
+  __shared__ ChainShared<CHAIN ? W : 1> before;
   __shared__ uint32_t taken;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -44,70 +44,72 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_fwd_kernel(FwdParams p) 
   const uint32_t col = id % p.cols, row = id / p.cols % p.batch, tile = id / p.cols / p.batch;
   const int64_t b = row, t0 = (static_cast<int64_t>(tile) * waves + wave) * kWaveTokens;
   const int n = static_cast<int>(min(static_cast<int64_t>(kWaveTokens), max(int64_t{0}, p.L - t0)));
+  constexpr int kBytes = V * sizeof(T);
   const int64_t ch = static_cast<int64_t>(col) * W + lane * V;
   const bool live = ch < p.D;
-  const int64_t d = live ? ch : p.D - V;   // lanes past the channels repeat the last ones, and store nothing
-  const uint32_t lane_bytes = static_cast<uint32_t>(d - static_cast<int64_t>(col) * W) * sizeof(T);
-  const int64_t col_at = static_cast<int64_t>(col) * W;
+  const int64_t d = live ? ch : p.D - V;   // per-channel values: lanes past the channels repeat the last ones
+  const uint32_t at = static_cast<uint32_t>(ch) * sizeof(T);
 
-  float s[V], a[kWaveTokens][V], u[kWaveTokens][V], P[V], H[V];
+  Rate s[V];
+  float a[kWaveTokens][V], u[kWaveTokens][V], P[V], H[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    s[v] = p.c * softplus_f32(p.lam[d + v]);
+    s[v] = Rate(p.c, p.lam[d + v]);
     P[v] = 1.0f;
     H[v] = 0.0f;
   }
-  int32_t mark[kWaveTokens];
-  if constexpr (PACKED) {
-#pragma unroll
-    for (int j = 0; j < kWaveTokens; ++j) mark[j] = n > 0 ? p.marks[t0 + j] : kOutside;
-  }
+  // Wavefronts of 16 tokens of one sequence, none of them its first or last,
+  // take a path without branches.  The marks of the others: one load, a scalar
+  // for each token where it is asked for.
+  int32_t marks = 0;
+  if constexpr (PACKED) marks = n > 0 ? p.marks[t0 + lane % kWaveTokens] : kOutside;
+  const bool plain = n == kWaveTokens && (!PACKED || __ballot(marks < 0 || (marks & 3)) == 0);
+  auto mark = [&](int j) { return __builtin_amdgcn_readlane(marks, j); };
 
   // tokens to (a, b) of h = a h + b; past the end of the row (1, 0)
-  auto tokens = [&](auto full) {
-    constexpr bool FULL = decltype(full)::value;
-    Raw<T, V> rx[kWaveTokens], ra[kWaveTokens], rg[kWaveTokens];
-    const int64_t xo = b * p.xb + t0 * p.xs + col_at, ao = b * p.gab + t0 * p.gas + col_at,
-                  go = b * p.gxb + t0 * p.gxs + col_at;
+  auto tokens = [&](auto every) {
+    constexpr bool PLAIN = decltype(every)::value;
+    constexpr bool MARKED = PACKED && !PLAIN;
+    uint32_t rx[kWaveTokens], ra[kWaveTokens], rg[kWaveTokens];
+    const TokenRows x = token_rows<T>(p.x, b * p.xb + t0 * p.xs, p.xs, p.D),
+                    ga = token_rows<T>(p.ga, b * p.gab + t0 * p.gas, p.gas, p.D),
+                    gx = token_rows<T>(p.gx, b * p.gxb + t0 * p.gxs, p.gxs, p.D);
 #pragma unroll
     for (int j = 0; j < kWaveTokens; ++j) {
-      const int jj = FULL ? j : min(j, n - 1);
-      ra[j] = load_raw<T, V>(p.ga, ao + jj * p.gas, lane_bytes);
-      rg[j] = load_raw<T, V>(p.gx, go + jj * p.gxs, lane_bytes);
-      rx[j] = load_raw<T, V>(p.x, xo + jj * p.xs, lane_bytes);
+      const int jj = PLAIN ? j : min(j, n - 1);
+      ra[j] = ga.load<kBytes>(jj, at);
+      rg[j] = gx.load<kBytes>(jj, at);
+      rx[j] = x.load<kBytes>(jj, at);
     }
 #pragma unroll
     for (int j = 0; j < kWaveTokens; ++j) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float r = s[v] * sigmoid_f32(widen<T>(ra[j].v[v]));
-        float aj = __builtin_amdgcn_exp2f(-r * kLog2e);
-        float bj = __builtin_amdgcn_sqrtf(one_minus_square(aj, r)) *
-                   (sigmoid_f32(widen<T>(rg[j].v[v])) * widen<T>(rx[j].v[v]));
-        if constexpr (PACKED) {
-          if (mark[j] & 1) {   // first token of its sequence, or in none
-            const float h0 = mark[j] >= 0 && p.h0 ? p.h0[static_cast<int64_t>(mark[j] >> 2) * p.D + d + v] : 0.0f;
-            bj = mark[j] >= 0 ? fmaf(aj, h0, bj) : 0.0f;
+        const float sa = sigmoid_f32(widen<T, V>(ra[j], v));
+        float aj = __builtin_amdgcn_exp2f(s[v].log2a * sa);
+        float bj = __builtin_amdgcn_sqrtf(one_minus_square(aj, s[v].u * sa)) *
+                   (sigmoid_f32(widen<T, V>(rg[j], v)) * widen<T, V>(rx[j], v));
+        if constexpr (MARKED) {
+          if (mark(j) & 1) {   // first token of its sequence, or in none
+            const float h0 = mark(j) >= 0 && p.h0 ? p.h0[static_cast<int64_t>(mark(j) >> 2) * p.D + d + v] : 0.0f;
+            bj = mark(j) >= 0 ? fmaf(aj, h0, bj) : 0.0f;
           }
         }
-        if constexpr (!FULL) {
+        if constexpr (!PLAIN) {
           aj = j < n ? aj : 1.0f;
           bj = j < n ? bj : 0.0f;
         }
         a[j][v] = aj;
         u[j][v] = bj;
         P[v] *= aj;
-        H[v] = PACKED && (mark[j] & 1) ? bj : fmaf(aj, H[v], bj);
+        H[v] = MARKED && (mark(j) & 1) ? bj : fmaf(aj, H[v], bj);
       }
     }
   };
-  if (n == kWaveTokens) tokens(std::true_type{});
+  if (plain) tokens(std::true_type{});
   else if (n > 0) tokens(std::false_type{});
   if constexpr (PACKED) {
-    int32_t any = 0;
-#pragma unroll
-    for (int j = 0; j < kWaveTokens; ++j) any |= mark[j];
-    if (n > 0 && (any & 1)) {
+    if (n > 0 && __ballot(marks & 1)) {
 #pragma unroll
       for (int v = 0; v < V; ++v) P[v] = kCut;
     }
@@ -116,31 +118,28 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_fwd_kernel(FwdParams p) 
 #pragma unroll
   for (int v = 0; v < V; ++v) pairs[wave][lane * V + v] = make_float2(P[v], H[v]);
   __syncthreads();
-  for (int c = threadIdx.x; c < W; c += blockDim.x) {   // once with eight wavefronts
-    const int64_t dc = min(col_at + c, p.D - 1);
-    float h = 0.0f;
-    if (!PACKED && p.h0) h = p.h0[b * p.D + dc];
-    if constexpr (CHAIN) {
-      float tp = 1.0f, th = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kMaxWaves; ++w) {
-        const float2 q = pairs[w][c];
-        tp = chain_product<PACKED>(tp, q.x);
-        th = chain_apply<PACKED>(q.x, q.y, th);
-      }
-      // the words of (row, col): tiles, then groups
-      const int64_t ngroups = (p.tiles + kChainGroup - 1) / kChainGroup;
-      uint64_t* const base = p.words + (static_cast<int64_t>(row) * p.cols + col) * (p.tiles + ngroups) * W;
-      h = chain_carry<PACKED>(Chain{base, base + static_cast<int64_t>(p.tiles) * W, W}, tile, p.tiles, c, tp, th, h);
-    }
-    entering[c] = h;
-  }
-  __syncthreads();
-  if (n <= 0) return;
-
   float h[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) h[v] = entering[lane * V + v];
+  for (int v = 0; v < V; ++v) h[v] = !PACKED && p.h0 ? p.h0[b * p.D + d + v] : 0.0f;
+  if constexpr (CHAIN) {
+    // the words of (row, col): tiles, then groups
+    const int64_t ngroups = (p.tiles + kChainGroup - 1) / kChainGroup;
+    uint64_t* const base = p.words + (static_cast<int64_t>(row) * p.cols + col) * (p.tiles + ngroups) * W;
+    const Chain chain{base, base + static_cast<int64_t>(p.tiles) * W, W};
+    chain_gather<PACKED, W>(chain, tile, pairs, before, [](int w) { return w; });
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      h[v] = chain_entering<PACKED, W>(tile, lane * V + v, before, h[v]);
+      if (wave == 0 && chain_hands_on(tile, p.tiles)) {
+        float out = h[v];
+#pragma unroll
+        for (int w = 0; w < kMaxWaves; ++w) out = chain_apply<PACKED>(pairs[w][lane * V + v].x, pairs[w][lane * V + v].y, out);
+        chain_leave(chain, tile, lane * V + v, out);
+      }
+    }
+  }
+  if (n <= 0) return;
   for (int w = 0; w < wave; ++w)
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -152,26 +151,26 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_fwd_kernel(FwdParams p) 
 #pragma unroll
     for (int v = 0; v < V; ++v) ck[v] = h[v];
   }
-  char* const out = static_cast<char*>(p.out) + (b * p.ob + t0 * p.os + col_at) * static_cast<int64_t>(sizeof(T));
+  const TokenRows out = token_rows<T>(p.out, b * p.ob + t0 * p.os, p.os, p.D);
+  auto outputs = [&](auto every) {
+    constexpr bool PLAIN = decltype(every)::value;
+    constexpr bool MARKED = PACKED && !PLAIN;
 #pragma unroll
-  for (int j = 0; j < kWaveTokens; ++j) {
-    if (j >= n) continue;
-    Raw<T, V> r;
+    for (int j = 0; j < kWaveTokens; ++j) {
+      if (!PLAIN && j >= n) continue;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      h[v] = PACKED && (mark[j] & 1) ? u[j][v] : fmaf(a[j][v], h[v], u[j][v]);
-      r.v[v] = narrow<T>(h[v]);
-    }
-    bool store = true;
-    if constexpr (PACKED) {
-      store = mark[j] >= 0 || p.zero_outside;
-      if (mark[j] >= 0 && (mark[j] & 2) && p.last && live) {
+      for (int v = 0; v < V; ++v) h[v] = MARKED && (mark(j) & 1) ? u[j][v] : fmaf(a[j][v], h[v], u[j][v]);
+      if constexpr (MARKED) {
+        if (mark(j) >= 0 && (mark(j) & 2) && p.last && live) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) p.last[static_cast<int64_t>(mark[j] >> 2) * p.D + d + v] = h[v];
+          for (int v = 0; v < V; ++v) p.last[static_cast<int64_t>(mark(j) >> 2) * p.D + d + v] = h[v];
+        }
       }
+      if (!MARKED || mark(j) >= 0 || p.zero_outside) out.store<kBytes>(j, at, narrow<T, V>(h));
     }
-    if (store && live) *reinterpret_cast<Raw<T, V>*>(out + j * p.os * static_cast<int64_t>(sizeof(T)) + lane_bytes) = r;
-  }
+  };
+  if (plain) outputs(std::true_type{});
+  else outputs(std::false_type{});
   if constexpr (!PACKED) {
     if (p.last && live && t0 + n == p.L) {
 #pragma unroll
@@ -201,7 +200,7 @@ __global__ __launch_bounds__(kThreads) void gated_step_kernel(StepParams p) {
   if (p.slots)
     for (int64_t i = 0; i < b0; ++i)
       if (p.slots[i] == slot) return;
-  const float s = p.c * softplus_f32(p.lam[d]);
+  const Rate s(p.c, p.lam[d]);
   float h = p.state[slot * p.ss + d];
   for (int64_t b = b0; b < p.batch; ++b) {
     if (b > b0 && (!p.slots || p.slots[b] != slot)) {
@@ -209,10 +208,10 @@ __global__ __launch_bounds__(kThreads) void gated_step_kernel(StepParams p) {
       continue;
     }
     const float x = io<T>::load(static_cast<const T*>(p.x) + b * p.xb + d);
-    const float v = s * sigmoid_f32(io<T>::load(static_cast<const T*>(p.ga) + b * p.gab + d));
+    const float sa = sigmoid_f32(io<T>::load(static_cast<const T*>(p.ga) + b * p.gab + d));
     const float g = sigmoid_f32(io<T>::load(static_cast<const T*>(p.gx) + b * p.gxb + d));
-    const float a = __builtin_amdgcn_exp2f(-v * kLog2e);
-    h = fmaf(a, h, sqrtf(one_minus_square(a, v)) * (g * x));
+    const float a = __builtin_amdgcn_exp2f(s.log2a * sa);
+    h = fmaf(a, h, __builtin_amdgcn_sqrtf(one_minus_square(a, s.u * sa)) * (g * x));
     io<T>::store(static_cast<T*>(p.out) + b * p.ob + d, h);
   }
   p.state[slot * p.ss + d] = h;

@@ -32,10 +32,10 @@ struct BwdParams {
 // so the three gradients' factors of e are ready before e is known; only
 // e_t = dout_t + a_{t+1} e_{t+1} waits for the tiles behind.
 template <typename T, int V, bool PACKED, bool CHAIN>
-__global__ __launch_bounds__(64 * kMaxWaves) void gated_bwd_kernel(BwdParams p) {
+__global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams p) {
   constexpr int W = 64 * V;
   __shared__ float2 pairs[kMaxWaves][W];
-  __shared__ float entering[W];
+  __shared__ ChainShared<CHAIN ? W : 1> before;
   __shared__ uint32_t taken;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -53,69 +53,77 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_bwd_kernel(BwdParams p) 
   const int n = static_cast<int>(min(static_cast<int64_t>(kWaveTokens), max(int64_t{0}, p.L - t0)));
   const int64_t col_at = static_cast<int64_t>(col) * W, ch = col_at + lane * V;
   const bool live = ch < p.D;
-  const int64_t d = live ? ch : p.D - V;   // lanes past the channels repeat the last ones, and store nothing
-  const uint32_t lane_bytes = static_cast<uint32_t>(d - col_at) * sizeof(T);
+  const int64_t d = live ? ch : p.D - V;   // per-channel values: lanes past the channels repeat the last ones
+  constexpr int kBytes = V * sizeof(T);
+  const uint32_t at = static_cast<uint32_t>(ch) * sizeof(T);
 
   // e's factors: dx = e fx, dgate_x = e fg, dgate_a = e fa, dlam's sum e fl
-  float s[V], a[kWaveTokens][V], fx[kWaveTokens][V], fg[kWaveTokens][V], fa[kWaveTokens][V], fl[kWaveTokens][V],
+  Rate s[V];
+  float a[kWaveTokens][V], fx[kWaveTokens][V], fg[kWaveTokens][V], fa[kWaveTokens][V], fl[kWaveTokens][V],
       dout[kWaveTokens][V], P[V], Q[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    s[v] = p.c * softplus_f32(p.lam[d + v]);
+    s[v] = Rate(p.c, p.lam[d + v]);
     P[v] = 1.0f;
     Q[v] = 0.0f;
   }
-  int32_t mark[kWaveTokens];
-  if constexpr (PACKED) {
-#pragma unroll
-    for (int j = 0; j < kWaveTokens; ++j) mark[j] = n > 0 ? p.marks[t0 + j] : kOutside;
-  }
+  // Wavefronts of 16 tokens of one sequence, none of them its first or last,
+  // take a path without branches.  The marks of the others: one load, a scalar
+  // for each token where it is asked for.
+  int32_t marks = 0;
+  if constexpr (PACKED) marks = n > 0 ? p.marks[t0 + lane % kWaveTokens] : kOutside;
+  const bool plain = n == kWaveTokens && (!PACKED || __ballot(marks < 0 || (marks & 3)) == 0);
+  auto mark = [&](int j) { return __builtin_amdgcn_readlane(marks, j); };
 
-  auto tokens = [&](auto full) {
-    constexpr bool FULL = decltype(full)::value;
-    Raw<T, V> rx[kWaveTokens], ra[kWaveTokens], rg[kWaveTokens], rd[kWaveTokens];
-    const int64_t xo = b * p.xb + t0 * p.xs + col_at, ao = b * p.gab + t0 * p.gas + col_at,
-                  go = b * p.gxb + t0 * p.gxs + col_at, eo = b * p.dob + t0 * p.dos + col_at;
+  auto tokens = [&](auto every) {
+    constexpr bool PLAIN = decltype(every)::value;
+    constexpr bool MARKED = PACKED && !PLAIN;
+    uint32_t rx[kWaveTokens], ra[kWaveTokens], rg[kWaveTokens], rd[kWaveTokens];
+    const TokenRows tx = token_rows<T>(p.x, b * p.xb + t0 * p.xs, p.xs, p.D),
+                    ta = token_rows<T>(p.ga, b * p.gab + t0 * p.gas, p.gas, p.D),
+                    tg = token_rows<T>(p.gx, b * p.gxb + t0 * p.gxs, p.gxs, p.D),
+                    td = token_rows<T>(p.dout, b * p.dob + t0 * p.dos, p.dos, p.D);
     float h[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) h[v] = p.ck[(b * p.nck + t0 / kCkpt) * p.D + d + v];
 #pragma unroll
     for (int j = 0; j < kWaveTokens; ++j) {
-      const int jj = FULL ? j : min(j, n - 1);
-      ra[j] = load_raw<T, V>(p.ga, ao + jj * p.gas, lane_bytes);
-      rg[j] = load_raw<T, V>(p.gx, go + jj * p.gxs, lane_bytes);
-      rx[j] = load_raw<T, V>(p.x, xo + jj * p.xs, lane_bytes);
-      rd[j] = load_raw<T, V>(p.dout, eo + jj * p.dos, lane_bytes);
+      const int jj = PLAIN ? j : min(j, n - 1);
+      ra[j] = ta.load<kBytes>(jj, at);
+      rg[j] = tg.load<kBytes>(jj, at);
+      rx[j] = tx.load<kBytes>(jj, at);
+      rd[j] = td.load<kBytes>(jj, at);
     }
 #pragma unroll
     for (int j = 0; j < kWaveTokens; ++j) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        if constexpr (PACKED) {
-          if (mark[j] & 1)   // first token of its sequence, or in none
-            h[v] = mark[j] >= 0 && p.h0 ? p.h0[static_cast<int64_t>(mark[j] >> 2) * p.D + d + v] : 0.0f;
+        if constexpr (MARKED) {
+          if (mark(j) & 1)   // first token of its sequence, or in none
+            h[v] = mark(j) >= 0 && p.h0 ? p.h0[static_cast<int64_t>(mark(j) >> 2) * p.D + d + v] : 0.0f;
         }
-        const float x = widen<T>(rx[j].v[v]), sa = sigmoid_f32(widen<T>(ra[j].v[v])), g = sigmoid_f32(widen<T>(rg[j].v[v]));
-        const float r = s[v] * sa;
-        const float aj = __builtin_amdgcn_exp2f(-r * kLog2e);
-        const float q = one_minus_square(aj, r);
-        // below fp32's normal numbers the hardware's root takes q for 0
-        const float inv = q >= 0x1p-126f ? __builtin_amdgcn_rsqf(q) : 0.0f;
-        const float m = q * inv * g;               // beta g
+        const float x = widen<T, V>(rx[j], v), sa = sigmoid_f32(widen<T, V>(ra[j], v)),
+                    g = sigmoid_f32(widen<T, V>(rg[j], v));
+        const float aj = __builtin_amdgcn_exp2f(s[v].log2a * sa);
+        const float q = one_minus_square(aj, s[v].u * sa);
+        // 1 / beta, finite where beta is 0: the factors below have sigma(gate_a) or s,
+        // one of which is then 0
+        const float inv = __builtin_amdgcn_rsqf(fmaxf(q, 0x1p-126f));
+        const float m = q * inv * g, mx = m * x;   // beta g, b
         const float dv = fmaf(g * x, aj * aj * inv, -aj * h[v]) * sa;
-        h[v] = fmaf(aj, h[v], m * x);
+        h[v] = fmaf(aj, h[v], mx);
         a[j][v] = aj;
         fx[j][v] = m;
-        fg[j][v] = m * x * (1.0f - g);
+        fg[j][v] = fmaf(-mx, g, mx);
         fl[j][v] = dv;
-        fa[j][v] = dv * s[v] * (1.0f - sa);
-        dout[j][v] = widen<T>(rd[j].v[v]);
-        if constexpr (PACKED) {
+        fa[j][v] = dv * fmaf(-s[v].s, sa, s[v].s);
+        dout[j][v] = widen<T, V>(rd[j], v);
+        if constexpr (MARKED) {
           // dlast enters at a sequence's last token
-          if (mark[j] >= 0 && (mark[j] & 2) && p.dlast)
-            dout[j][v] += p.dlast[static_cast<int64_t>(mark[j] >> 2) * p.D + d + v];
+          if (mark(j) >= 0 && (mark(j) & 2) && p.dlast)
+            dout[j][v] += p.dlast[static_cast<int64_t>(mark(j) >> 2) * p.D + d + v];
         }
-        if constexpr (!FULL) {
+        if constexpr (!PLAIN) {
           a[j][v] = j < n ? a[j][v] : 1.0f;
           dout[j][v] = j < n ? dout[j][v] : 0.0f;
         }
@@ -126,16 +134,13 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_bwd_kernel(BwdParams p) 
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         P[v] *= a[j][v];
-        Q[v] = PACKED && (mark[j] & 1) && (FULL || j < n) ? 0.0f : a[j][v] * (dout[j][v] + Q[v]);
+        Q[v] = MARKED && (mark(j) & 1) && (PLAIN || j < n) ? 0.0f : a[j][v] * (dout[j][v] + Q[v]);
       }
   };
-  if (n == kWaveTokens) tokens(std::true_type{});
+  if (plain) tokens(std::true_type{});
   else if (n > 0) tokens(std::false_type{});
   if constexpr (PACKED) {
-    int32_t any = 0;
-#pragma unroll
-    for (int j = 0; j < kWaveTokens; ++j) any |= mark[j];
-    if (n > 0 && (any & 1)) {
+    if (n > 0 && __ballot(marks & 1)) {
 #pragma unroll
       for (int v = 0; v < V; ++v) P[v] = kCut;
     }
@@ -144,69 +149,70 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_bwd_kernel(BwdParams p) 
 #pragma unroll
   for (int v = 0; v < V; ++v) pairs[wave][lane * V + v] = make_float2(P[v], Q[v]);
   __syncthreads();
-  for (int c = threadIdx.x; c < W; c += blockDim.x) {   // once with eight wavefronts
-    const int64_t dc = min(col_at + c, p.D - 1);
-    float e = 0.0f;
-    if (!PACKED && p.dlast) e = p.dlast[b * p.D + dc];
-    if constexpr (CHAIN) {
-      float tp = 1.0f, tq = 0.0f;
+  float e[V];
 #pragma unroll
-      for (int w = kMaxWaves - 1; w >= 0; --w) {
-        const float2 q = pairs[w][c];
-        tp = chain_product<PACKED>(tp, q.x);
-        tq = chain_apply<PACKED>(q.x, q.y, tq);
+  for (int v = 0; v < V; ++v) e[v] = !PACKED && p.dlast ? p.dlast[b * p.D + d + v] : 0.0f;
+  if constexpr (CHAIN) {
+    // the words of (row, col): tiles, then groups
+    const int64_t ngroups = (p.tiles + kChainGroup - 1) / kChainGroup;
+    uint64_t* const base = p.words + (static_cast<int64_t>(row) * p.cols + col) * (p.tiles + ngroups) * W;
+    const Chain chain{base, base + static_cast<int64_t>(p.tiles) * W, W};
+    chain_gather<PACKED, W>(chain, k, pairs, before, [](int w) { return kMaxWaves - 1 - w; });
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      e[v] = chain_entering<PACKED, W>(k, lane * V + v, before, e[v]);
+      if (wave == 0 && chain_hands_on(k, p.tiles)) {
+        float out = e[v];
+#pragma unroll
+        for (int w = kMaxWaves - 1; w >= 0; --w) out = chain_apply<PACKED>(pairs[w][lane * V + v].x, pairs[w][lane * V + v].y, out);
+        chain_leave(chain, k, lane * V + v, out);
       }
-      const int64_t ngroups = (p.tiles + kChainGroup - 1) / kChainGroup;
-      uint64_t* const base = p.words + (static_cast<int64_t>(row) * p.cols + col) * (p.tiles + ngroups) * W;
-      e = chain_carry<PACKED>(Chain{base, base + static_cast<int64_t>(p.tiles) * W, W}, k, p.tiles, c, tp, tq, e);
     }
-    entering[c] = e;
   }
-  __syncthreads();
-
   float acc[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) acc[v] = 0.0f;
   if (n > 0) {
-    float e[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) e[v] = entering[lane * V + v];
     for (int w = waves - 1; w > wave; --w)
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const float2 q = pairs[w][lane * V + v];
         e[v] = chain_apply<PACKED>(q.x, q.y, e[v]);
       }
-    constexpr int64_t esz = sizeof(T);
-    char* const dx = static_cast<char*>(p.dx) + (b * p.dxb + t0 * p.dxs + col_at) * esz + lane_bytes;
-    char* const dga = static_cast<char*>(p.dga) + (b * p.dgab + t0 * p.dgas + col_at) * esz + lane_bytes;
-    char* const dgx = static_cast<char*>(p.dgx) + (b * p.dgxb + t0 * p.dgxs + col_at) * esz + lane_bytes;
+    const TokenRows dx = token_rows<T>(p.dx, b * p.dxb + t0 * p.dxs, p.dxs, p.D),
+                    dga = token_rows<T>(p.dga, b * p.dgab + t0 * p.dgas, p.dgas, p.D),
+                    dgx = token_rows<T>(p.dgx, b * p.dgxb + t0 * p.dgxs, p.dgxs, p.D);
+    auto outputs = [&](auto every) {
+      constexpr bool PLAIN = decltype(every)::value;
+      constexpr bool MARKED = PACKED && !PLAIN;
 #pragma unroll
-    for (int j = kWaveTokens - 1; j >= 0; --j) {
-      if (j >= n) continue;
-      Raw<T, V> ox, oa, og;
+      for (int j = kWaveTokens - 1; j >= 0; --j) {
+        if (!PLAIN && j >= n) continue;
+        float ox[V], oa[V], og[V];
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const bool in = !PACKED || mark[j] >= 0;
-        const float et = dout[j][v] + e[v];
-        ox.v[v] = narrow<T>(in ? et * fx[j][v] : 0.0f);
-        og.v[v] = narrow<T>(in ? et * fg[j][v] : 0.0f);
-        oa.v[v] = narrow<T>(in ? et * fa[j][v] : 0.0f);
-        if (in) acc[v] = fmaf(et, fl[j][v], acc[v]);
-        e[v] = a[j][v] * et;
-        if constexpr (PACKED) {
-          if (mark[j] & 1) {
-            if (in && p.dh0 && live) p.dh0[static_cast<int64_t>(mark[j] >> 2) * p.D + d + v] = e[v];
-            e[v] = 0.0f;
+        for (int v = 0; v < V; ++v) {
+          const bool in = !MARKED || mark(j) >= 0;
+          const float et = dout[j][v] + e[v];
+          ox[v] = in ? et * fx[j][v] : 0.0f;
+          og[v] = in ? et * fg[j][v] : 0.0f;
+          oa[v] = in ? et * fa[j][v] : 0.0f;
+          if (in) acc[v] = fmaf(et, fl[j][v], acc[v]);
+          e[v] = a[j][v] * et;
+          if constexpr (MARKED) {
+            if (mark(j) & 1) {
+              if (in && p.dh0 && live) p.dh0[static_cast<int64_t>(mark(j) >> 2) * p.D + d + v] = e[v];
+              e[v] = 0.0f;
+            }
           }
         }
+        dx.store<kBytes>(j, at, narrow<T, V>(ox));
+        dga.store<kBytes>(j, at, narrow<T, V>(oa));
+        dgx.store<kBytes>(j, at, narrow<T, V>(og));
       }
-      if (live) {
-        *reinterpret_cast<Raw<T, V>*>(dx + j * p.dxs * esz) = ox;
-        *reinterpret_cast<Raw<T, V>*>(dga + j * p.dgas * esz) = oa;
-        *reinterpret_cast<Raw<T, V>*>(dgx + j * p.dgxs * esz) = og;
-      }
-    }
+    };
+    if (plain) outputs(std::true_type{});
+    else outputs(std::false_type{});
     if constexpr (!PACKED) {
       if (p.dh0 && live && t0 == 0) {
 #pragma unroll

@@ -33,6 +33,8 @@
 
 namespace ssm {
 
+constexpr int kWaveTokens = kCkpt;   // tokens of a wavefront: one checkpoint each
+constexpr int kMaxWaves = 8;
 constexpr int kChainGroup = 16;
 constexpr uint64_t kNoWord = ~uint64_t{0};
 
@@ -81,34 +83,69 @@ struct Chain {
   int64_t width;
 };
 
-// The state entering tile k for one channel, whose own pair is (p, h); `first`
-// is the state entering tile 0.  Publishes the pair, and the state leaving
-// the group at its last tile.
-template <bool PACKED>
-__device__ __forceinline__ float chain_carry(const Chain& c, int64_t k, int64_t ntiles, int channel,
-                                             float p, float h, float first) {
-  uint64_t* const mine = c.tiles + k * c.width + channel;
+// What a workgroup keeps of the tiles before it.
+template <int W>
+struct ChainShared {
+  float2 tiles[kChainGroup - 1][W];
+  float before[W];
+};
+
+// Called by all threads of a tile once its wavefronts' pairs are in LDS, in
+// `order` (the wavefront that the scan passes w-th).  Publishes the tile's
+// pair, then brings the predecessors' words into LDS, a few each thread, so
+// that their latencies run side by side and no wavefront holds them all in
+// registers.
+template <bool PACKED, int W, typename Order>
+__device__ __forceinline__ void chain_gather(const Chain& c, int64_t k, float2 (&pairs)[kMaxWaves][W],
+                                             ChainShared<W>& sh, Order order) {
+  constexpr int kParts = 64 * kMaxWaves / W, kMine = (kChainGroup - 2) / kParts + 1;
+  const int ch = threadIdx.x % W, part = threadIdx.x / W;
   const int in_group = static_cast<int>(k % kChainGroup);
   const int64_t group = k / kChainGroup;
-  if (in_group != kChainGroup - 1) chain_store(mine, chain_word(p, h));
-  uint64_t w[kChainGroup];
+  uint64_t* const mine = c.tiles + k * c.width + ch;
+  if (part == 0 && in_group != kChainGroup - 1) {
+    float p = 1.0f, h = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kChainGroup - 1; ++i)
-    if (i < in_group) w[i] = chain_load(mine - (in_group - i) * c.width);
-  float carry = first;
-  if (group > 0) {
-    uint64_t* const before = c.groups + (group - 1) * c.width + channel;
-    carry = word_h(chain_wait(before, chain_load(before)));
-  }
-#pragma unroll
-  for (int i = 0; i < kChainGroup - 1; ++i)
-    if (i < in_group) {
-      w[i] = chain_wait(mine - (in_group - i) * c.width, w[i]);
-      carry = chain_apply<PACKED>(word_p(w[i]), word_h(w[i]), carry);
+    for (int w = 0; w < kMaxWaves; ++w) {
+      const float2 q = pairs[order(w)][ch];
+      p = chain_product<PACKED>(p, q.x);
+      h = chain_apply<PACKED>(q.x, q.y, h);
     }
-  if (in_group == kChainGroup - 1 && k + 1 < ntiles)
-    chain_store(c.groups + group * c.width + channel, chain_word(0.0f, chain_apply<PACKED>(p, h, carry)));
-  return carry;
+    chain_store(mine, chain_word(p, h));
+  }
+  uint64_t w[kMine], before = 0;
+#pragma unroll
+  for (int i = 0; i < kMine; ++i)
+    if (part + i * kParts < in_group) w[i] = chain_load(mine - (in_group - part - i * kParts) * c.width);
+  uint64_t* const left = c.groups + (group - 1) * c.width + ch;
+  if (part == kParts - 1 && group > 0) before = chain_load(left);
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    const int j = part + i * kParts;
+    if (j < in_group) {
+      w[i] = chain_wait(mine - (in_group - j) * c.width, w[i]);
+      sh.tiles[j][ch] = make_float2(word_p(w[i]), word_h(w[i]));
+    }
+  }
+  if (part == kParts - 1 && group > 0) sh.before[ch] = word_h(chain_wait(left, before));
+}
+
+// After a barrier: the state entering tile k for a channel, `first` being the
+// one entering tile 0.
+template <bool PACKED, int W>
+__device__ __forceinline__ float chain_entering(int64_t k, int ch, const ChainShared<W>& sh, float first) {
+  float h = k >= kChainGroup ? sh.before[ch] : first;
+  const int in_group = static_cast<int>(k % kChainGroup);
+  for (int j = 0; j < in_group; ++j) h = chain_apply<PACKED>(sh.tiles[j][ch].x, sh.tiles[j][ch].y, h);
+  return h;
+}
+
+// Whether tile k hands the state that leaves it to the next group.
+__device__ __forceinline__ bool chain_hands_on(int64_t k, int64_t ntiles) {
+  return k % kChainGroup == kChainGroup - 1 && k + 1 < ntiles;
+}
+__device__ __forceinline__ void chain_leave(const Chain& c, int64_t k, int ch, float h) {
+  chain_store(c.groups + k / kChainGroup * c.width + ch, chain_word(0.0f, h));
 }
 
 // Marks of a packed token: the sequence it belongs to and whether it is its
@@ -117,8 +154,6 @@ constexpr int32_t kOutside = -1;   // its lowest bit, too, says that no state co
 __device__ __forceinline__ int32_t mark_of(int32_t seq, bool first, bool last) {
   return seq << 2 | (first ? 1 : 0) | (last ? 2 : 0);
 }
-// Sequences are numbered below 2^29 (checked on the host).
-constexpr int64_t kMaxPacked = int64_t{1} << 29;
 
 // Before the scan: chain words to kNoWord, the ticket counter to 0, and with
 // cu_seqlens the token marks and the last states of empty sequences.
@@ -136,24 +171,58 @@ struct PrepParams {
 };
 hipError_t launch_gated_prep(const PrepParams& p, hipStream_t stream);
 
-// V consecutive channels of one token as they are stored.
-template <typename T, int V> struct alignas(sizeof(T) * V) Raw { T v[V]; };
-
-template <typename T> __device__ __forceinline__ float widen(T v);
-template <> __device__ __forceinline__ float widen<float>(float v) { return v; }
-template <> __device__ __forceinline__ float widen<uint16_t>(uint16_t v) { return bf16_to_f32(v); }
-template <typename T> __device__ __forceinline__ T narrow(float v);
-template <> __device__ __forceinline__ float narrow<float>(float v) { return v; }
-template <> __device__ __forceinline__ uint16_t narrow<uint16_t>(float v) { return f32_to_bf16(v); }
-
+// V consecutive channels of a token as they are stored, at most 4 bytes: one
+// fp32, one or two bf16.
 template <typename T, int V>
-__device__ __forceinline__ Raw<T, V> load_raw(const void* base, int64_t elements, uint32_t lane_bytes) {
-  return *reinterpret_cast<const Raw<T, V>*>(static_cast<const char*>(base) + elements * static_cast<int64_t>(sizeof(T)) +
-                                             lane_bytes);
+__device__ __forceinline__ float widen(uint32_t raw, int v) {
+  if constexpr (sizeof(T) == 4) return __uint_as_float(raw);
+  else return __uint_as_float(v == 0 ? raw << 16 : raw & 0xffff0000u);
+}
+template <typename T, int V>
+__device__ __forceinline__ uint32_t narrow(const float (&h)[V]) {
+  if constexpr (sizeof(T) == 4) {
+    return __float_as_uint(h[0]);
+  } else if constexpr (V == 1) {
+    return f32_to_bf16(h[0]);
+  } else {
+    return f32_to_bf16(h[0]) | static_cast<uint32_t>(f32_to_bf16(h[1])) << 16;
+  }
 }
 
-constexpr int kWaveTokens = kCkpt;   // tokens of a wavefront: one checkpoint each
-constexpr int kMaxWaves = 8;
+// One tensor's rows from a wavefront's first token on.  A row is reached
+// through a buffer descriptor of its own: the descriptor is scalar work, the
+// lane's offset is the same for every row and tensor, and lanes past the
+// channels read zeros and write nothing.
+struct TokenRows {
+  char* first;
+  int64_t stride;     // bytes
+  uint32_t row_bytes;
+  template <typename T>
+  __device__ __forceinline__ void set(const void* p, int64_t elements, int64_t row_stride, int64_t D, T) {
+    first = static_cast<char*>(const_cast<void*>(p)) + elements * static_cast<int64_t>(sizeof(T));
+    stride = row_stride * static_cast<int64_t>(sizeof(T));
+    row_bytes = static_cast<uint32_t>(D * static_cast<int64_t>(sizeof(T)));
+  }
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t row(int j) const {
+    return __builtin_amdgcn_make_buffer_rsrc(first + j * stride, 0, static_cast<int>(row_bytes), kRsrcWord3);
+  }
+  template <int BYTES>
+  __device__ __forceinline__ uint32_t load(int j, uint32_t at) const {
+    if constexpr (BYTES == 4) return __builtin_amdgcn_raw_buffer_load_b32(row(j), at, 0, 0);
+    else return __builtin_amdgcn_raw_buffer_load_b16(row(j), at, 0, 0);
+  }
+  template <int BYTES>
+  __device__ __forceinline__ void store(int j, uint32_t at, uint32_t v) const {
+    if constexpr (BYTES == 4) __builtin_amdgcn_raw_buffer_store_b32(v, row(j), at, 0, 0);
+    else __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(v), row(j), at, 0, 0);
+  }
+};
+template <typename T>
+__device__ __forceinline__ TokenRows token_rows(const void* p, int64_t elements, int64_t row_stride, int64_t D) {
+  TokenRows r;
+  r.set(p, elements, row_stride, D, T{});
+  return r;
+}
 
 // How a call is cut into workgroups, and the parts of its workspace (bytes
 // from its start, each 256-byte aligned).

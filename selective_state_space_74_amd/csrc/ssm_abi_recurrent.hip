@@ -28,6 +28,8 @@ bool collide(const Tokens& t, int64_t batch, int64_t L, int64_t D) {
 }
 
 constexpr int64_t kMaxGroups = int64_t{1} << 31;
+constexpr int64_t kMaxDim = int64_t{1} << 28;
+constexpr int64_t kMaxPacked = int64_t{1} << 29;   // sequence numbers and two marks share 32 bits
 bool too_many_groups(int64_t batch, int64_t L, int64_t D) {
   const int64_t tiles = (L + 15) / 16, cols = (D + 63) / 64;
   if (tiles == 0 || cols == 0 || batch == 0) return batch >= kMaxGroups || cols >= kMaxGroups;
@@ -41,8 +43,10 @@ int check_gated(const Args* a) {
   if (a->cu_seqlens && a->batch != 1) return SSM_ERR_SHAPE;
   if (!(a->c > 0.0f) || !isfinite(a->c)) return SSM_ERR_SHAPE;
   if (bad_dtype(a->io_dtype)) return SSM_ERR_DTYPE;
-  if (a->seqlen > kMaxSeqlen || a->nseq > kMaxSeqlen) return SSM_ERR_UNSUPPORTED;
-  if (too_many_groups(a->batch, a->seqlen, a->dim)) return SSM_ERR_UNSUPPORTED;
+  if (a->seqlen > kMaxSeqlen) return SSM_ERR_UNSUPPORTED;
+  // rows are addressed by 32-bit byte offsets
+  if (a->dim > kMaxDim || too_many_groups(a->batch, a->seqlen, a->dim)) return SSM_ERR_UNSUPPORTED;
+  if (a->cu_seqlens && a->nseq >= kMaxPacked) return SSM_ERR_UNSUPPORTED;
   return SSM_OK;
 }
 
