@@ -502,7 +502,7 @@ typedef enum ssm_cache_format { SSM_CACHE_INT8 = 0, SSM_CACHE_FP8 = 1, SSM_CACHE
  * zeros; bf16 states are rounded to nearest even (int8 and e4m3 codes and e2m1
  * ones are exact in bf16 within its exponent range).
  * Sizes: zero sizes are no-ops; batch at most 65535;
- * outer * ceil(inner / 32) below 2^31 - 256.
+ * inner below 2^31; outer * ceil(inner / 32) at most 2^28.
  * Aliasing: what is written must not overlap what is read. */
 typedef struct ssm_state_cache_args {
   int64_t batch, nslots, outer, inner;

@@ -1,85 +1,331 @@
 // cached_update.hip -- the decode update of state_update.hip on states held in
-// an int8 cache (state_cache.h): dequantise, step, read out, quantise again.
+// an int8 cache (state_cache.h): dequantise, step, read out, quantise again,
+// with the state in registers in between.
+//
+// A lane has one channel and all its states: 16 codes are one 16-byte access,
+// and a wavefront's are one run of 1 KB.  (The fp32 update spreads a channel
+// over four lanes for the same reason.)  The readout and the block's maximum
+// then need no exchange between lanes.  A channel's row of A is loaded once for
+// kRows batch rows; B and C, the same for every lane where the wavefront is
+// inside one B/C group, come through scalar loads and are unpacked by scalar
+// instructions.
+//
+// 256 x 5120 x 16 states move 53 MB a step where the fp32 update moves 178 MB,
+// and cost about 17 vector instructions a state, four of them the generator's:
+// memory and issue bind about equally.
 #include "state_cache.h"
 
 namespace ssm {
 namespace {
 
-constexpr int kThreads = 64;
+constexpr int kThreads = 256;
+constexpr int kRows = 4;              // batch rows a thread, up to 16 states
+constexpr int kNames = 4;             // slots a lane compares at a time
+constexpr int64_t kMinBlocks = 512;   // ... where that leaves the GPU enough workgroups
 
 struct CachedParams {
   uint8_t* codes; uint8_t* scales;
   const void* x; const void* dt; const void* z; const void* B; const void* C;
   const float* A; const float* D; const float* bias; void* out;
   const int32_t* slots; const int64_t* seed;
-  int64_t cs, ss, xb, dtb, zb, Bb, Bg, Cb, Cg, Ad, ob, batch, nslots, dim, cpg;
-  int N, softplus;
+  int64_t cs, ss, xb, dtb, zb, Bb, Bg, Cb, Cg, Ad, ob, dim, cpg;
+  int batch, nslots, N, softplus;
 };
 
-// One thread a channel of a row.
+// Uniform values read through the scalar cache (the memory is not written by
+// the kernel).
+template <typename U>
+using Uniform = const __attribute__((address_space(4))) U;
+
 template <typename T>
-__global__ __launch_bounds__(kThreads) void cached_update_kernel(CachedParams p) {
-  const int64_t d = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const int64_t b0 = blockIdx.y;
-  if (d >= p.dim) return;
-  const int64_t slot = p.slots ? p.slots[b0] : b0;
-  if (slot < 0 || slot >= p.nslots) {
-    io<T>::store(static_cast<T*>(p.out) + b0 * p.ob + d, 0.0f);
-    return;
+__device__ __forceinline__ float uniform_value(const T* p, int i) {
+  if constexpr (sizeof(T) == 4) {
+    return reinterpret_cast<Uniform<float>*>(reinterpret_cast<uintptr_t>(p))[i];
+  } else {
+    const uint32_t w = reinterpret_cast<Uniform<uint32_t>*>(reinterpret_cast<uintptr_t>(p))[i / 2];
+    return __uint_as_float(i % 2 ? w & 0xffff0000u : w << 16);
   }
-  if (p.slots)   // the first row of a slot takes every row of it, in order
-    for (int64_t i = 0; i < b0; ++i)
-      if (p.slots[i] == slot) return;
-  const int nblk = (p.N + kCacheBlock - 1) / kCacheBlock;
-  uint8_t* codes = p.codes + slot * p.cs + d * p.N;
-  uint8_t* scales = p.scales + slot * p.ss + d * nblk;
-  const int64_t g = d / p.cpg;
-  for (int64_t b = b0; b < p.batch; ++b) {
-    if (b > b0) {
-      if (!p.slots) break;
-      if (p.slots[b] != slot) continue;
-    }
-    const float x = io<T>::load(static_cast<const T*>(p.x) + b * p.xb + d);
-    float dl = io<T>::load(static_cast<const T*>(p.dt) + b * p.dtb + d) + (p.bias ? p.bias[d] : 0.0f);
-    if (p.softplus) dl = softplus_f32(dl);
-    float y = 0.0f;
-    for (int k = 0; k < nblk; ++k) {
-      const int n = min(kCacheBlock, p.N - k * kCacheBlock);
-      const float unit = scale_value(scales[k]);
-      float h[kCacheBlock];
-      uint32_t amax = 0;
-      for (int j = 0; j < n; ++j) {
-        const int i = k * kCacheBlock + j;
-        h[j] = static_cast<float>(static_cast<int8_t>(codes[i])) * unit;
-        h[j] = fmaf(__builtin_amdgcn_exp2f(dl * (p.A[d * p.Ad + i] * kLog2e)), h[j],
-                    dl * x * io<T>::load(static_cast<const T*>(p.B) + b * p.Bb + g * p.Bg + i));
-        y = fmaf(io<T>::load(static_cast<const T*>(p.C) + b * p.Cb + g * p.Cg + i), h[j], y);
-        amax = max(amax, magnitude(h[j]));
+}
+
+// The next row of the batch after row `from` that names this slot, or batch.
+__device__ __forceinline__ int named_next(const int32_t* slots, int from, int batch, int slot, int lane) {
+  for (int base = from + 1; base < batch; base += 64) {
+    const int i = base + lane;
+    const uint64_t hits = __ballot(i < batch && slots[i] == slot);
+    if (hits) return base + __builtin_ctzll(hits);
+  }
+  return batch;
+}
+
+// CH: 16-state chunks of a channel.  WIDE: N = 16 CH, and every access may take
+// 16 codes (4 values of A); UNIFORM: one B/C group a wavefront, rows of B and C
+// readable by 32-bit words.  SEEDED: stochastic rounding.
+template <typename T, int CH, bool WIDE, bool UNIFORM, bool SEEDED>
+struct Channel {
+  static constexpr int NS = 16 * CH, NB = (CH + 1) / 2;
+  uint32_t q[4 * CH];   // codes
+  uint32_t e[NB];       // scale bytes
+
+  // the channel's row of A, times log2(e)
+  __device__ static __forceinline__ void load_a(const CachedParams& p, int64_t d, float (&a)[NS]) {
+#pragma unroll
+    for (int n = 0; n < NS; n += 4) {
+      if constexpr (WIDE) {
+        const float4 f = *reinterpret_cast<const float4*>(p.A + d * p.Ad + n);
+        a[n] = f.x; a[n + 1] = f.y; a[n + 2] = f.z; a[n + 3] = f.w;
+      } else {
+#pragma unroll
+        for (int i = n; i < n + 4; ++i) a[i] = i < p.N ? p.A[d * p.Ad + i] : 0.0f;
       }
-      const uint32_t e = scale_byte<SSM_CACHE_INT8>(amax);
-      const float inv = scale_inverse(e);
-      scales[k] = static_cast<uint8_t>(e);
-      uint32_t r[4];
-      for (int j = 0; j < n; ++j) {
-        const float v = e == 255u ? 0.0f : h[j];
-        uint32_t q;
-        if (p.seed) {
-          if (j % 16 == 0) {
-            r[0] = static_cast<uint32_t>(d); r[1] = static_cast<uint32_t>(b);
-            r[2] = static_cast<uint32_t>(k * 2 + j / 16); r[3] = 0;
-            philox7(r, static_cast<uint64_t>(*p.seed));
-          }
-          const uint32_t w = j % 16 < 4 ? r[0] : j % 16 < 8 ? r[1] : j % 16 < 12 ? r[2] : r[3];
-          q = (nearest_bits(v * inv, 256.0f) + ((w >> (8 * (j & 3))) & 0xffu)) >> 8;
-        } else {
-          q = nearest_bits(v, inv);
+    }
+#pragma unroll
+    for (int n = 0; n < NS; ++n) a[n] *= kLog2e;
+  }
+
+  __device__ __forceinline__ void load(const CachedParams& p, int64_t slot, int64_t d) {
+    const uint8_t* const c = p.codes + slot * p.cs + d * p.N;
+    const int nb = (p.N + kCacheBlock - 1) / kCacheBlock;
+#pragma unroll
+    for (int k = 0; k < NB; ++k) e[k] = p.scales[slot * p.ss + d * nb + k];
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      if constexpr (WIDE) {
+        const uint4 w = reinterpret_cast<const uint4*>(c)[k];
+        q[4 * k] = w.x; q[4 * k + 1] = w.y; q[4 * k + 2] = w.z; q[4 * k + 3] = w.w;
+      } else {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          q[4 * k + w] = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (16 * k + 4 * w + i < p.N) q[4 * k + w] |= static_cast<uint32_t>(c[16 * k + 4 * w + i]) << (8 * i);
         }
-        codes[k * kCacheBlock + j] = static_cast<uint8_t>(q);
       }
     }
-    y = fmaf(p.D ? p.D[d] : 0.0f, x, y);
-    if (p.z) y *= silu_f32(io<T>::load(static_cast<const T*>(p.z) + b * p.zb + d));
-    io<T>::store(static_cast<T*>(p.out) + b * p.ob + d, y);
+  }
+
+  __device__ __forceinline__ void store(const CachedParams& p, int64_t slot, int64_t d) const {
+    uint8_t* const c = p.codes + slot * p.cs + d * p.N;
+    const int nb = (p.N + kCacheBlock - 1) / kCacheBlock;
+#pragma unroll
+    for (int k = 0; k < NB; ++k) p.scales[slot * p.ss + d * nb + k] = static_cast<uint8_t>(e[k]);
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      if constexpr (WIDE) {
+        reinterpret_cast<uint4*>(c)[k] = make_uint4(q[4 * k], q[4 * k + 1], q[4 * k + 2], q[4 * k + 3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (16 * k + i < p.N) c[16 * k + i] = static_cast<uint8_t>(q[4 * k + i / 4] >> (8 * (i % 4)));
+      }
+    }
+  }
+
+  // One step of row b on the state in q, e; returns sum_n C s'.
+  __device__ __forceinline__ float step(const CachedParams& p, int b, int64_t d, const float (&a)[NS], float dl, float x,
+                                        uint64_t seed) {
+    const int64_t g = UNIFORM && p.cpg == p.dim ? 0 : d / p.cpg;
+    const T* Bp = static_cast<const T*>(p.B) + b * p.Bb + g * p.Bg;
+    const T* Cp = static_cast<const T*>(p.C) + b * p.Cb + g * p.Cg;
+    if constexpr (UNIFORM) {
+      // the same address in every lane: make that known
+      auto first = [](const T* v) {
+        const uint64_t u = reinterpret_cast<uint64_t>(v);
+        return reinterpret_cast<const T*>(
+            static_cast<uint64_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(u >> 32))) << 32 |
+            static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(u))));
+      };
+      Bp = first(Bp);
+      Cp = first(Cp);
+    }
+    auto bc = [&](const T* v, int n) -> float {
+      if constexpr (UNIFORM) return uniform_value(v, n);
+      else return n < p.N ? io<T>::load(v + n) : 0.0f;
+    };
+    float h[NS];
+    const float dlx = dl * x;
+    float y = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 4 * CH; ++k) {
+      float s[4];
+      decode4_int8(q[k], scale_value(e[k / 8]), s);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int n = 4 * k + i;
+        h[n] = fmaf(__builtin_amdgcn_exp2f(dl * a[n]), s[i], dlx * bc(Bp, n));
+        y = fmaf(bc(Cp, n), h[n], y);
+      }
+    }
+    // Largest magnitudes.  fmax drops a NaN; but a state that is not finite
+    // makes y so too, and then the maximum is taken over the magnitudes' bits.
+    const bool finite = magnitude(y) < 0x7f800000u;
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      constexpr int kIn = NS < kCacheBlock ? NS : kCacheBlock;
+      float m = 0.0f;
+#pragma unroll
+      for (int n = k * kCacheBlock; n < k * kCacheBlock + kIn && n < NS; ++n) m = fmaxf(m, fabsf(h[n]));
+      uint32_t bits = __float_as_uint(m);
+      if (!finite) {
+        bits = 0;
+#pragma unroll
+        for (int n = k * kCacheBlock; n < k * kCacheBlock + kIn && n < NS; ++n) bits = max(bits, magnitude(h[n]));
+      }
+      e[k] = scale_byte<SSM_CACHE_INT8>(bits);
+    }
+    // 256 2^(127 - E) is no fp32 number for E < 8 (states below 2^-112): scale in
+    // two steps there
+    bool tiny = false;
+#pragma unroll
+    for (int k = 0; k < NB; ++k) tiny |= e[k] < 8u;
+    const bool two = SEEDED && __any(tiny);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const uint32_t eb = e[c / 2];
+      const float inv = scale_inverse(eb);
+      uint32_t t[16];
+      if constexpr (SEEDED) {
+        uint32_t r[4] = {static_cast<uint32_t>(d), static_cast<uint32_t>(b), static_cast<uint32_t>(c), 0u};
+        philox7(r, seed);
+        const float fine = 256.0f * inv;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) t[i] = nearest_bits(h[16 * c + i], fine);
+        if (two) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) t[i] = nearest_bits(h[16 * c + i] * inv, 256.0f);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) t[i] += (r[i / 4] >> (8 * (i % 4))) & 0xffu;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) q[4 * c + w] = gather_bytes<1>(t[4 * w], t[4 * w + 1], t[4 * w + 2], t[4 * w + 3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) t[i] = nearest_bits(h[16 * c + i], inv);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) q[4 * c + w] = gather_bytes<0>(t[4 * w], t[4 * w + 1], t[4 * w + 2], t[4 * w + 3]);
+      }
+    }
+    return y;
+  }
+};
+
+template <typename T, int CH, bool WIDE, bool UNIFORM, bool SEEDED, int ROWS>
+__global__ __launch_bounds__(kThreads) void cached_update_kernel(CachedParams p) {
+  const int lane = threadIdx.x & 63;
+  const int64_t d0 = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  const int64_t wave0 = static_cast<int64_t>(blockIdx.x) * kThreads + (threadIdx.x & ~63);
+  if (wave0 >= p.dim) return;
+  const bool live = d0 < p.dim;
+  const int64_t d = live ? d0 : p.dim - 1;   // lanes past the channels repeat the last one, and store nothing
+  const int first = blockIdx.y * ROWS;
+
+  using Ch = Channel<T, CH, WIDE, UNIFORM, SEEDED>;
+  Ch ch[ROWS];
+  float a[Ch::NS], xv[ROWS], dtv[ROWS], zv[ROWS];
+  int slot[ROWS];
+  const uint64_t seed = SEEDED ? static_cast<uint64_t>(*p.seed) : 0;
+  auto inputs = [&](int b, float& x, float& dt, float& z) {
+    x = io<T>::load(static_cast<const T*>(p.x) + b * p.xb + d);
+    dt = io<T>::load(static_cast<const T*>(p.dt) + b * p.dtb + d);
+    z = p.z ? io<T>::load(static_cast<const T*>(p.z) + b * p.zb + d) : 0.0f;
+  };
+  // every row's codes and inputs are on their way before the first is used
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    const int b = min(first + r, p.batch - 1);
+    slot[r] = p.slots ? p.slots[b] : b;
+    if (slot[r] < 0 || slot[r] >= p.nslots) slot[r] = -1;
+  }
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    if (slot[r] >= 0) ch[r].load(p, slot[r], d);
+    inputs(min(first + r, p.batch - 1), xv[r], dtv[r], zv[r]);
+  }
+  Ch::load_a(p, d, a);
+  const float bias = p.bias ? p.bias[d] : 0.0f, Dd = p.D ? p.D[d] : 0.0f;
+  // The first row of a slot takes every row of it, in order: whether a row
+  // before names the same slot, and the next that does.
+  uint32_t before = 0;
+  int next[ROWS];
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) next[r] = p.batch;
+  if (p.slots) {
+    for (int base = 0; base < p.batch; base += 64 * kNames) {
+      int named[kNames];
+#pragma unroll
+      for (int k = 0; k < kNames; ++k) {
+        const int i = base + 64 * k + lane;
+        named[k] = i < p.batch ? p.slots[i] : -2;
+      }
+#pragma unroll
+      for (int k = 0; k < kNames; ++k)
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+          const int own = first + r - base - 64 * k;   // this row's bit
+          const uint64_t hits = __ballot(named[k] == slot[r]);
+          const uint64_t below = own <= 0 ? 0 : own > 63 ? ~uint64_t{0} : (uint64_t{1} << own) - 1;
+          const uint64_t above = own < 0 ? ~uint64_t{0} : own > 62 ? 0 : ~uint64_t{0} << (own + 1);
+          if (hits & below) before |= 1u << r;
+          if ((hits & above) && next[r] == p.batch) next[r] = base + 64 * k + __builtin_ctzll(hits & above);
+        }
+    }
+  }
+
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    int b = first + r;
+    if (b >= p.batch) break;
+    T* const out = static_cast<T*>(p.out) + d;
+    if (slot[r] < 0) {
+      if (live) io<T>::store(out + b * p.ob, 0.0f);
+      continue;
+    }
+    if (before >> r & 1) continue;
+    for (;;) {
+      float dl = dtv[r] + bias;
+      if (p.softplus) dl = softplus_f32(dl);
+      float y = fmaf(Dd, xv[r], ch[r].step(p, b, d, a, dl, xv[r], seed));
+      if (p.z) y *= silu_f32(zv[r]);
+      if (live) io<T>::store(out + b * p.ob, y);
+      b = b == first + r ? next[r] : named_next(p.slots, b, p.batch, slot[r], lane);
+      if (b >= p.batch) break;
+      inputs(b, xv[r], dtv[r], zv[r]);
+    }
+    if (live) ch[r].store(p, slot[r], d);
+  }
+}
+
+template <typename T, int CH, bool WIDE, bool UNIFORM>
+void launch_u(const CachedParams& p, hipStream_t stream) {
+  const unsigned xb = static_cast<unsigned>((p.dim + kThreads - 1) / kThreads);
+  if constexpr (CH == 1) {
+    const int64_t rows = (p.batch + kRows - 1) / kRows;
+    if (xb * rows >= kMinBlocks) {
+      const dim3 grid(xb, static_cast<unsigned>(rows));
+      if (p.seed) cached_update_kernel<T, CH, WIDE, UNIFORM, true, kRows><<<grid, kThreads, 0, stream>>>(p);
+      else cached_update_kernel<T, CH, WIDE, UNIFORM, false, kRows><<<grid, kThreads, 0, stream>>>(p);
+      return;
+    }
+  }
+  const dim3 grid(xb, static_cast<unsigned>(p.batch));
+  if (p.seed) cached_update_kernel<T, CH, WIDE, UNIFORM, true, 1><<<grid, kThreads, 0, stream>>>(p);
+  else cached_update_kernel<T, CH, WIDE, UNIFORM, false, 1><<<grid, kThreads, 0, stream>>>(p);
+}
+
+template <typename T, int CH>
+void launch_c(bool wide, bool uniform, const CachedParams& p, hipStream_t stream) {
+  // the short forms: whole chunks with uniform B and C, or everything element by element
+  if (wide && uniform) launch_u<T, CH, true, true>(p, stream);
+  else launch_u<T, CH, false, false>(p, stream);
+}
+
+template <typename T>
+void launch_t(bool wide, bool uniform, const CachedParams& p, hipStream_t stream) {
+  switch ((p.N + 15) / 16) {
+    case 1: launch_c<T, 1>(wide, uniform, p, stream); break;
+    case 2: launch_c<T, 2>(wide, uniform, p, stream); break;
+    case 3: launch_c<T, 3>(wide, uniform, p, stream); break;
+    default: launch_c<T, 4>(wide, uniform, p, stream); break;
   }
 }
 
@@ -87,14 +333,19 @@ __global__ __launch_bounds__(kThreads) void cached_update_kernel(CachedParams p)
 
 hipError_t launch_cached_update(const ssm_cached_update_args& a, hipStream_t stream) {
   const int64_t G = a.ngroups > 1 ? a.ngroups : 1;
-  CachedParams p{a.codes, a.scales, a.x, a.dt, a.z, a.B, a.C, a.A, a.D, a.dt_bias, a.out, a.slots, a.seed,
-                 a.codes_slot_stride, a.scales_slot_stride, a.x_batch_stride, a.dt_batch_stride,
-                 a.z_batch_stride, a.B_batch_stride, G > 1 ? a.B_group_stride : 0, a.C_batch_stride,
-                 G > 1 ? a.C_group_stride : 0, a.A_dim_stride, a.out_batch_stride, a.batch, a.nslots,
-                 a.dim, a.dim / G, static_cast<int>(a.dstate), a.dt_softplus ? 1 : 0};
-  const dim3 grid(static_cast<unsigned>((a.dim + kThreads - 1) / kThreads), static_cast<unsigned>(a.batch));
-  if (a.io_dtype == SSM_BF16) cached_update_kernel<uint16_t><<<grid, kThreads, 0, stream>>>(p);
-  else cached_update_kernel<float><<<grid, kThreads, 0, stream>>>(p);
+  const CachedParams p{a.codes, a.scales, a.x, a.dt, a.z, a.B, a.C, a.A, a.D, a.dt_bias, a.out, a.slots, a.seed,
+                       a.codes_slot_stride, a.scales_slot_stride, a.x_batch_stride, a.dt_batch_stride,
+                       a.z_batch_stride, a.B_batch_stride, G > 1 ? a.B_group_stride : 0, a.C_batch_stride,
+                       G > 1 ? a.C_group_stride : 0, a.A_dim_stride, a.out_batch_stride, a.dim, a.dim / G,
+                       static_cast<int>(a.batch), static_cast<int>(a.nslots < 0x7fffffff ? a.nslots : 0x7fffffff),
+                       static_cast<int>(a.dstate), a.dt_softplus ? 1 : 0};
+  auto al = [](const void* q, int64_t bytes) { return reinterpret_cast<uintptr_t>(q) % static_cast<uintptr_t>(bytes) == 0; };
+  const int64_t w = a.io_dtype == SSM_BF16 ? 2 : 1;   // elements of a 32-bit word
+  const bool wide = p.N % 16 == 0 && al(a.codes, 16) && a.codes_slot_stride % 16 == 0 && al(a.A, 16) && a.A_dim_stride % 4 == 0;
+  const bool uniform = (G == 1 || p.cpg % 64 == 0) && al(a.B, 4) && al(a.C, 4) && p.Bb % w == 0 && p.Cb % w == 0 &&
+                       p.Bg % w == 0 && p.Cg % w == 0;
+  if (a.io_dtype == SSM_BF16) launch_t<uint16_t>(wide, uniform, p, stream);
+  else launch_t<float>(wide, uniform, p, stream);
   return hipGetLastError();
 }
 

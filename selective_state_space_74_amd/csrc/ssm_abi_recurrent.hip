@@ -198,10 +198,10 @@ int check_cache(const ssm_state_cache_args* a, bool write) {
   if (bad_dtype(a->io_dtype)) return SSM_ERR_DTYPE;
   if (a->format != SSM_CACHE_INT8 && a->format != SSM_CACHE_FP8 && a->format != SSM_CACHE_FP4) return SSM_ERR_DTYPE;
   if (a->format == SSM_CACHE_FP4 && a->inner % 2) return SSM_ERR_SHAPE;
-  const int64_t limit = (int64_t{1} << 31) - 256;
-  if (a->batch > 65535 || a->inner >= limit) return SSM_ERR_UNSUPPORTED;
+  const int64_t limit = int64_t{1} << 28;   // 8 lanes a block, numbered in 32 bits
+  if (a->batch > 65535 || a->inner >= (int64_t{1} << 31)) return SSM_ERR_UNSUPPORTED;
   const int64_t nblk = (a->inner + SSM_CACHE_BLOCK - 1) / SSM_CACHE_BLOCK;
-  if (nblk && a->outer >= limit / nblk) return SSM_ERR_UNSUPPORTED;
+  if (nblk && a->outer > limit / nblk) return SSM_ERR_UNSUPPORTED;
   if (a->batch == 0 || a->outer == 0 || a->inner == 0) return SSM_OK;
   if (((!a->codes || !a->scales) && a->nslots > 0) || !a->states) return SSM_ERR_NULL;
   if (a->codes_slot_stride < 0 || a->scales_slot_stride < 0 || a->states_batch_stride < 0) return SSM_ERR_STRIDE;

@@ -55,33 +55,47 @@ __device__ __forceinline__ uint32_t nearest_bits(float v, float unit) {
   return __float_as_uint(fmaf(v, unit, kIntMagic));
 }
 
-// Two values to two codes: int8 and fp8 in the low two bytes, fp4 in the low
-// byte.
+// Byte n of each of four words, in order.
+template <int BYTE>
+__device__ __forceinline__ uint32_t gather_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  // byte n of the second operand, then of the first; 0x0c gives zero
+  constexpr uint32_t kPick = (4u + BYTE) << 8 | BYTE;
+  return __builtin_amdgcn_perm(b, a, 0x0c0c0000u | kPick) | __builtin_amdgcn_perm(d, c, kPick << 16 | 0x0c0cu);
+}
+
+// Four values to four codes: int8 and fp8 in 32 bits, fp4 in the low 16.
 template <int F>
-__device__ __forceinline__ uint32_t encode2(float v0, float v1, float inv) {
+__device__ __forceinline__ uint32_t encode4(const float (&v)[4], float inv) {
   if constexpr (F == SSM_CACHE_INT8) {
-    return (nearest_bits(v0, inv) & 0xffu) | ((nearest_bits(v1, inv) & 0xffu) << 8);
+    return gather_bytes<0>(nearest_bits(v[0], inv), nearest_bits(v[1], inv), nearest_bits(v[2], inv),
+                           nearest_bits(v[3], inv));
   } else if constexpr (F == SSM_CACHE_FP8) {
-    return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(v0 * inv, v1 * inv, 0, false)) & 0xffffu;
+    const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * inv, v[1] * inv, 0, false);
+    return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(v[2] * inv, v[3] * inv, lo, true));
   } else {
-    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, v0 * inv, v1 * inv, 1.0f, 0) & 0xffu;
+    const uint32_t lo = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, v[0] * inv, v[1] * inv, 1.0f, 0);
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(lo, v[2] * inv, v[3] * inv, 1.0f, 1) & 0xffffu;
   }
 }
 
-// The inverse: the values the codes stand for, unscaled.
+// Four int8 codes to their values times unit.
+__device__ __forceinline__ void decode4_int8(uint32_t codes, float unit, float (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = static_cast<float>(static_cast<int8_t>(codes >> (8 * i))) * unit;
+}
+
 template <int F>
-__device__ __forceinline__ void decode2(uint32_t bits, float& v0, float& v1) {
+__device__ __forceinline__ void decode4(uint32_t codes, float unit, float (&v)[4]) {
   if constexpr (F == SSM_CACHE_INT8) {
-    v0 = static_cast<float>(static_cast<int8_t>(bits & 0xffu));
-    v1 = static_cast<float>(static_cast<int8_t>((bits >> 8) & 0xffu));
+    decode4_int8(codes, unit, v);
   } else if constexpr (F == SSM_CACHE_FP8) {
-    const auto r = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(bits), false);
-    v0 = r[0];
-    v1 = r[1];
+    const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(codes), false);
+    const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(codes), true);
+    v[0] = lo[0] * unit; v[1] = lo[1] * unit; v[2] = hi[0] * unit; v[3] = hi[1] * unit;
   } else {
-    const auto r = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(bits, 1.0f, 0);
-    v0 = r[0];
-    v1 = r[1];
+    const auto lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 0);
+    const auto hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 1);
+    v[0] = lo[0] * unit; v[1] = lo[1] * unit; v[2] = hi[0] * unit; v[3] = hi[1] * unit;
   }
 }
 

@@ -1,5 +1,12 @@
 // state_cache.hip -- writing recurrent states to a quantised cache and reading
 // them back, for gfx950.  Formats: state_cache.h.
+//
+// Both are bound by memory traffic: 4 bytes (fp32) against 1 or 1/2 a value,
+// and a scale byte a block.  A lane takes 4 consecutive values of a block, so
+// that the lanes of a block (8 for 32 values, fewer for shorter rows) read or
+// write 16 bytes each in one run, and the block's maximum is two or three DPP
+// steps.  Which row of the batch a workgroup has comes from the grid; only the
+// row's place in the cache waits for its slot.
 #include "state_cache.h"
 
 namespace ssm {
@@ -9,88 +16,177 @@ constexpr int kThreads = 256;
 
 struct CacheParams {
   uint8_t* codes; uint8_t* scales; void* states; const int32_t* slots;
-  int64_t cs, ss, vs, batch, nslots, outer, inner, nblk;
+  int64_t cs, ss, vs;
+  int batch, nslots;
+  uint32_t inner, nblk, blocks;   // blocks: of one state
+  int lane_bits;                  // log2 of the lanes of a block
 };
 
-// One thread a block of 32 values.
-template <int F, typename T>
-__global__ __launch_bounds__(kThreads) void cache_write_kernel(CacheParams p) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  if (i >= p.outer * p.nblk) return;
-  const int64_t b = blockIdx.y, o = i / p.nblk, k = i % p.nblk;
-  const int64_t slot = p.slots ? p.slots[b] : b;
-  if (slot < 0 || slot >= p.nslots) return;
-  if (p.slots)   // the last row of a slot is the one written
-    for (int64_t j = b + 1; j < p.batch; ++j)
-      if (p.slots[j] == slot) return;
-  const int n = static_cast<int>(min(static_cast<int64_t>(kCacheBlock), p.inner - k * kCacheBlock));
-  const T* v = static_cast<const T*>(p.states) + b * p.vs + o * p.inner + k * kCacheBlock;
-  uint32_t amax = 0;
-  for (int j = 0; j < n; ++j) amax = max(amax, magnitude(io<T>::load(v + j)));
-  const uint32_t e = scale_byte<F>(amax);
-  const float inv = scale_inverse(e);
-  p.scales[slot * p.ss + i] = static_cast<uint8_t>(e);
-  const bool nan = e == 255u;
-  for (int j = 0; j < n; j += 2) {
-    const float v0 = nan ? 0.0f : io<T>::load(v + j), v1 = nan || j + 1 >= n ? 0.0f : io<T>::load(v + j + 1);
-    const uint32_t q = encode2<F>(v0, v1, inv);
-    if constexpr (F == SSM_CACHE_FP4) {
-      p.codes[slot * p.cs + (o * p.inner + k * kCacheBlock + j) / 2] = static_cast<uint8_t>(q);
-    } else {
-      uint8_t* c = p.codes + slot * p.cs + o * p.inner + k * kCacheBlock + j;
-      c[0] = static_cast<uint8_t>(q);
-      if (j + 1 < n) c[1] = static_cast<uint8_t>(q >> 8);
-    }
-  }
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), CTRL, 0xf, 0xf, true));
+}
+// The maximum over groups of 2^bits lanes.
+__device__ __forceinline__ uint32_t group_max(uint32_t v, int bits) {
+  // quads: lanes (1,0,3,2), then (2,3,0,1); then each half row of 8, mirrored
+  if (bits > 0) v = max(v, dpp<0xB1>(v));
+  if (bits > 1) v = max(v, dpp<0x4E>(v));
+  if (bits > 2) v = max(v, dpp<0x141>(v));
+  return v;
 }
 
-template <int F, typename T>
-__global__ __launch_bounds__(kThreads) void cache_read_kernel(CacheParams p) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  if (i >= p.outer * p.nblk) return;
-  const int64_t b = blockIdx.y, o = i / p.nblk, k = i % p.nblk;
-  const int64_t slot = p.slots ? p.slots[b] : b;
-  const bool held = slot >= 0 && slot < p.nslots;
-  const int n = static_cast<int>(min(static_cast<int64_t>(kCacheBlock), p.inner - k * kCacheBlock));
-  T* v = static_cast<T*>(p.states) + b * p.vs + o * p.inner + k * kCacheBlock;
-  const float unit = held ? scale_value(p.scales[slot * p.ss + i]) : 0.0f;
-  for (int j = 0; j < n; j += 2) {
-    float v0 = 0.0f, v1 = 0.0f;
-    if (held) {
-      if constexpr (F == SSM_CACHE_FP4) {
-        decode2<F>(p.codes[slot * p.cs + (o * p.inner + k * kCacheBlock + j) / 2], v0, v1);
+// Where a lane's 4 values are: the block's number in the state, the values'
+// offset in the state, and how many of the 4 there are.
+struct Place {
+  uint32_t block;
+  int64_t at;
+  int count;
+};
+__device__ __forceinline__ Place place(const CacheParams& p, uint32_t thread) {
+  Place r;
+  r.block = thread >> p.lane_bits;
+  const uint32_t first = (thread & ((1u << p.lane_bits) - 1)) * 4;
+  const uint32_t o = p.nblk == 1 ? r.block : r.block / p.nblk, k = r.block - o * p.nblk;
+  const uint32_t in_row = k * kCacheBlock + first;
+  r.at = static_cast<int64_t>(o) * p.inner + in_row;
+  const uint32_t end = min(p.inner, (k + 1) * kCacheBlock);
+  r.count = r.block < p.blocks && in_row < end ? static_cast<int>(min(4u, end - in_row)) : 0;
+  return r;
+}
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void load4(const T* q, int count, float (&v)[4]) {
+  if constexpr (VEC) {
+    v[0] = v[1] = v[2] = v[3] = 0.0f;
+    if (count) {
+      if constexpr (sizeof(T) == 4) {
+        const float4 f = *reinterpret_cast<const float4*>(q);
+        v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
       } else {
-        const uint8_t* c = p.codes + slot * p.cs + o * p.inner + k * kCacheBlock + j;
-        decode2<F>(c[0] | (j + 1 < n ? c[1] << 8 : 0), v0, v1);
+        const uint2 f = *reinterpret_cast<const uint2*>(q);
+        v[0] = __uint_as_float(f.x << 16); v[1] = __uint_as_float(f.x & 0xffff0000u);
+        v[2] = __uint_as_float(f.y << 16); v[3] = __uint_as_float(f.y & 0xffff0000u);
       }
     }
-    io<T>::store(v + j, v0 * unit);
-    if (j + 1 < n) io<T>::store(v + j + 1, v1 * unit);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = i < count ? io<T>::load(q + i) : 0.0f;
   }
 }
 
-CacheParams params(const ssm_state_cache_args& a) {
-  return CacheParams{a.codes, a.scales, a.states, a.slots, a.codes_slot_stride, a.scales_slot_stride,
-                     a.states_batch_stride, a.batch, a.nslots, a.outer, a.inner,
-                     (a.inner + kCacheBlock - 1) / kCacheBlock};
+// VEC: rows of a multiple of 4 values, all of them aligned for accesses of 4.
+template <int F, typename T, bool VEC>
+__global__ __launch_bounds__(kThreads) void cache_write_kernel(CacheParams p) {
+  const int b = blockIdx.y;
+  const Place w = place(p, blockIdx.x * kThreads + threadIdx.x);
+  float v[4];
+  load4<T, VEC>(static_cast<const T*>(p.states) + b * p.vs + w.at, w.count, v);
+  const int slot = p.slots ? p.slots[b] : b;
+  if (p.slots) {
+    // the last row of a slot is the one written
+    bool later = false;
+    for (int j = b + 1 + (threadIdx.x & 63); j < p.batch; j += 64) later |= p.slots[j] == slot;
+    if (__any(later) || slot < 0 || slot >= p.nslots) return;
+  }
+  const uint32_t amax = group_max(max(max(magnitude(v[0]), magnitude(v[1])), max(magnitude(v[2]), magnitude(v[3]))), p.lane_bits);
+  const uint32_t e = scale_byte<F>(amax);
+  const uint32_t q = encode4<F>(v, scale_inverse(e));
+  if (w.count == 0) return;
+  if ((threadIdx.x & ((1u << p.lane_bits) - 1)) == 0) p.scales[slot * p.ss + w.block] = static_cast<uint8_t>(e);
+  if constexpr (F == SSM_CACHE_FP4) {
+    uint8_t* const c = p.codes + slot * p.cs + w.at / 2;
+    if constexpr (VEC) {
+      *reinterpret_cast<uint16_t*>(c) = static_cast<uint16_t>(q);
+    } else {
+      c[0] = static_cast<uint8_t>(q);
+      if (w.count > 2) c[1] = static_cast<uint8_t>(q >> 8);
+    }
+  } else {
+    uint8_t* const c = p.codes + slot * p.cs + w.at;
+    if constexpr (VEC) {
+      *reinterpret_cast<uint32_t*>(c) = q;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < w.count) c[i] = static_cast<uint8_t>(q >> (8 * i));
+    }
+  }
+}
+
+template <int F, typename T, bool VEC>
+__global__ __launch_bounds__(kThreads) void cache_read_kernel(CacheParams p) {
+  const int b = blockIdx.y;
+  const Place w = place(p, blockIdx.x * kThreads + threadIdx.x);
+  if (w.count == 0) return;
+  const int slot = p.slots ? p.slots[b] : b;
+  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (slot >= 0 && slot < p.nslots) {
+    const float unit = scale_value(p.scales[slot * p.ss + w.block]);
+    uint32_t q = 0;
+    if constexpr (F == SSM_CACHE_FP4) {
+      const uint8_t* const c = p.codes + slot * p.cs + w.at / 2;
+      if constexpr (VEC) q = *reinterpret_cast<const uint16_t*>(c);
+      else q = c[0] | (w.count > 2 ? c[1] << 8 : 0);
+    } else {
+      const uint8_t* const c = p.codes + slot * p.cs + w.at;
+      if constexpr (VEC) {
+        q = *reinterpret_cast<const uint32_t*>(c);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i < w.count) q |= static_cast<uint32_t>(c[i]) << (8 * i);
+      }
+    }
+    decode4<F>(q, unit, v);
+  }
+  T* const out = static_cast<T*>(p.states) + b * p.vs + w.at;
+  if constexpr (VEC) {
+    if constexpr (sizeof(T) == 4) {
+      *reinterpret_cast<float4*>(out) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+      *reinterpret_cast<uint2*>(out) = make_uint2(f32_to_bf16(v[0]) | static_cast<uint32_t>(f32_to_bf16(v[1])) << 16,
+                                                  f32_to_bf16(v[2]) | static_cast<uint32_t>(f32_to_bf16(v[3])) << 16);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < w.count) io<T>::store(out + i, v[i]);
+  }
+}
+
+template <int F, typename T, bool VEC>
+void launch_v(bool write, dim3 grid, const CacheParams& p, hipStream_t stream) {
+  if (write) cache_write_kernel<F, T, VEC><<<grid, kThreads, 0, stream>>>(p);
+  else cache_read_kernel<F, T, VEC><<<grid, kThreads, 0, stream>>>(p);
 }
 
 template <int F, typename T>
-void launch(bool write, const CacheParams& p, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>((p.outer * p.nblk + kThreads - 1) / kThreads),
-                  static_cast<unsigned>(p.batch));
-  if (write) cache_write_kernel<F, T><<<grid, kThreads, 0, stream>>>(p);
-  else cache_read_kernel<F, T><<<grid, kThreads, 0, stream>>>(p);
+hipError_t launch(bool write, const ssm_state_cache_args& a, hipStream_t stream) {
+  CacheParams p{a.codes, a.scales, a.states, a.slots, a.codes_slot_stride, a.scales_slot_stride, a.states_batch_stride,
+                static_cast<int>(a.batch), static_cast<int>(a.nslots < 0x7fffffff ? a.nslots : 0x7fffffff),
+                static_cast<uint32_t>(a.inner), static_cast<uint32_t>((a.inner + kCacheBlock - 1) / kCacheBlock), 0, 0};
+  p.blocks = static_cast<uint32_t>(a.outer * p.nblk);
+  while (p.lane_bits < 3 && (4u << p.lane_bits) < p.inner) ++p.lane_bits;
+  auto fits = [](const void* q, int64_t stride, int64_t bytes) {
+    return reinterpret_cast<uintptr_t>(q) % static_cast<uintptr_t>(bytes) == 0 && stride % bytes == 0;
+  };
+  const int64_t esz = sizeof(T), held = F == SSM_CACHE_FP4 ? 2 : 4;
+  const bool vec = a.inner % 4 == 0 && fits(a.states, a.states_batch_stride * esz, 4 * esz) &&
+                   fits(a.codes, a.codes_slot_stride, held);
+  const dim3 grid(static_cast<unsigned>(((static_cast<int64_t>(p.blocks) << p.lane_bits) + kThreads - 1) / kThreads),
+                  static_cast<unsigned>(a.batch));
+  if (vec) launch_v<F, T, true>(write, grid, p, stream);
+  else launch_v<F, T, false>(write, grid, p, stream);
+  return hipGetLastError();
 }
 
 template <typename T>
 hipError_t launch_format(bool write, const ssm_state_cache_args& a, hipStream_t stream) {
   switch (a.format) {
-    case SSM_CACHE_INT8: launch<SSM_CACHE_INT8, T>(write, params(a), stream); break;
-    case SSM_CACHE_FP8: launch<SSM_CACHE_FP8, T>(write, params(a), stream); break;
-    default: launch<SSM_CACHE_FP4, T>(write, params(a), stream); break;
+    case SSM_CACHE_INT8: return launch<SSM_CACHE_INT8, T>(write, a, stream);
+    case SSM_CACHE_FP8: return launch<SSM_CACHE_FP8, T>(write, a, stream);
+    default: return launch<SSM_CACHE_FP4, T>(write, a, stream);
   }
-  return hipGetLastError();
 }
 
 }  // namespace
