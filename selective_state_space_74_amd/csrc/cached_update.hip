@@ -13,6 +13,7 @@
 // 256 x 5120 x 16 states move 53 MB a step where the fp32 update moves 178 MB,
 // and cost about 17 vector instructions a state, four of them the generator's:
 // memory and issue bind about equally.
+#include "slots.h"
 #include "state_cache.h"
 
 namespace ssm {
@@ -20,7 +21,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kRows = 4;              // batch rows a thread, up to 16 states
-constexpr int kNames = 4;             // slots a lane compares at a time
 constexpr int64_t kMinBlocks = 512;   // ... where that leaves the GPU enough workgroups
 
 struct CachedParams {
@@ -45,16 +45,6 @@ __device__ __forceinline__ float uniform_value(const T* p, int i) {
     const uint32_t w = reinterpret_cast<Uniform<uint32_t>*>(reinterpret_cast<uintptr_t>(p))[i / 2];
     return __uint_as_float(i % 2 ? w & 0xffff0000u : w << 16);
   }
-}
-
-// The next row of the batch after row `from` that names this slot, or batch.
-__device__ __forceinline__ int named_next(const int32_t* slots, int from, int batch, int slot, int lane) {
-  for (int base = from + 1; base < batch; base += 64) {
-    const int i = base + lane;
-    const uint64_t hits = __ballot(i < batch && slots[i] == slot);
-    if (hits) return base + __builtin_ctzll(hits);
-  }
-  return batch;
 }
 
 // CH: 16-state chunks of a channel.  WIDE: N = 16 CH, and every access may take
@@ -243,33 +233,10 @@ __global__ __launch_bounds__(kThreads) void cached_update_kernel(CachedParams p)
   }
   Ch::load_a(p, d, a);
   const float bias = p.bias ? p.bias[d] : 0.0f, Dd = p.D ? p.D[d] : 0.0f;
-  // The first row of a slot takes every row of it, in order: whether a row
-  // before names the same slot, and the next that does.
+  // the first row of a slot takes every row of it, in order
   uint32_t before = 0;
   int next[ROWS];
-#pragma unroll
-  for (int r = 0; r < ROWS; ++r) next[r] = p.batch;
-  if (p.slots) {
-    for (int base = 0; base < p.batch; base += 64 * kNames) {
-      int named[kNames];
-#pragma unroll
-      for (int k = 0; k < kNames; ++k) {
-        const int i = base + 64 * k + lane;
-        named[k] = i < p.batch ? p.slots[i] : -2;
-      }
-#pragma unroll
-      for (int k = 0; k < kNames; ++k)
-#pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-          const int own = first + r - base - 64 * k;   // this row's bit
-          const uint64_t hits = __ballot(named[k] == slot[r]);
-          const uint64_t below = own <= 0 ? 0 : own > 63 ? ~uint64_t{0} : (uint64_t{1} << own) - 1;
-          const uint64_t above = own < 0 ? ~uint64_t{0} : own > 62 ? 0 : ~uint64_t{0} << (own + 1);
-          if (hits & below) before |= 1u << r;
-          if ((hits & above) && next[r] == p.batch) next[r] = base + 64 * k + __builtin_ctzll(hits & above);
-        }
-    }
-  }
+  slot_order<ROWS>(p.slots, first, p.batch, slot, lane, before, next);
 
 #pragma unroll
   for (int r = 0; r < ROWS; ++r) {

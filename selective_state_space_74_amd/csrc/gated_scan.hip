@@ -5,11 +5,12 @@
 #include <type_traits>
 
 #include "gated_tile.h"
+#include "slots.h"
 
 namespace ssm {
 namespace {
 
-constexpr int kThreads = 64;
+constexpr int kThreads = 256;   // of the single-token step
 
 struct FwdParams {
   const void* x; const void* ga; const void* gx;
@@ -184,39 +185,72 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_fwd_kernel(FwdParams p) 
 struct StepParams {
   float* state; const void* x; const void* ga; const void* gx;
   const float* lam; const int32_t* slots; void* out;
-  int64_t ss, xb, gab, gxb, ob, batch, nslots, D;
+  int64_t ss, xb, gab, gxb, ob, D;
+  int batch, nslots;
   float c;
 };
 
-template <typename T>
+// A lane has V channels of a row: 16 bytes of its fp32 state.
+template <typename T, int V>
 __global__ __launch_bounds__(kThreads) void gated_step_kernel(StepParams p) {
-  const int64_t d = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const int64_t b0 = blockIdx.y;
-  if (d >= p.D) return;
-  const int64_t slot = p.slots ? p.slots[b0] : b0;
-  if (slot < 0 || slot >= p.nslots) {
-    io<T>::store(static_cast<T*>(p.out) + b0 * p.ob + d, 0.0f);
-    return;
-  }
-  // the first row of a slot takes every row of it, in order
-  if (p.slots)
-    for (int64_t i = 0; i < b0; ++i)
-      if (p.slots[i] == slot) return;
-  const Rate s(p.c, p.lam[d]);
-  float h = p.state[slot * p.ss + d];
-  for (int64_t b = b0; b < p.batch; ++b) {
-    if (b > b0 && (!p.slots || p.slots[b] != slot)) {
-      if (!p.slots) break;
-      continue;
+  struct alignas(sizeof(T) * V) Vec { T v[V]; };
+  struct alignas(4 * V) State { float v[V]; };
+  const int lane = threadIdx.x & 63;
+  const int64_t d0 = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) * V;
+  const bool live = d0 < p.D;
+  const int64_t d = live ? d0 : p.D - V;   // lanes past the channels repeat the last ones, and store nothing
+  const int row = blockIdx.y;
+  int slot[1] = {p.slots ? p.slots[row] : row};
+  if (slot[0] < 0 || slot[0] >= p.nslots) slot[0] = -1;
+  auto at = [&](const void* q, int64_t stride, int64_t b) {
+    return *reinterpret_cast<const Vec*>(static_cast<const T*>(q) + b * stride + d);
+  };
+  Vec x = at(p.x, p.xb, row), ga = at(p.ga, p.gab, row), gx = at(p.gx, p.gxb, row);
+  State h{};
+  if (slot[0] >= 0) h = *reinterpret_cast<const State*>(p.state + slot[0] * p.ss + d);
+  Rate s[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) s[v] = Rate(p.c, p.lam[d + v]);
+  uint32_t before;
+  int next[1];
+  slot_order<1>(p.slots, row, p.batch, slot, lane, before, next);
+  if (before && slot[0] >= 0) return;
+
+  for (int b = row;;) {
+    Vec o{};
+    if (slot[0] >= 0) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float sa = sigmoid_f32(io<T>::load(&ga.v[v])), g = sigmoid_f32(io<T>::load(&gx.v[v]));
+        const float a = __builtin_amdgcn_exp2f(s[v].log2a * sa);
+        h.v[v] = fmaf(a, h.v[v], __builtin_amdgcn_sqrtf(one_minus_square(a, s[v].u * sa)) * (g * io<T>::load(&x.v[v])));
+        io<T>::store(&o.v[v], h.v[v]);
+      }
     }
-    const float x = io<T>::load(static_cast<const T*>(p.x) + b * p.xb + d);
-    const float sa = sigmoid_f32(io<T>::load(static_cast<const T*>(p.ga) + b * p.gab + d));
-    const float g = sigmoid_f32(io<T>::load(static_cast<const T*>(p.gx) + b * p.gxb + d));
-    const float a = __builtin_amdgcn_exp2f(s.log2a * sa);
-    h = fmaf(a, h, __builtin_amdgcn_sqrtf(one_minus_square(a, s.u * sa)) * (g * x));
-    io<T>::store(static_cast<T*>(p.out) + b * p.ob + d, h);
+    if (live) *reinterpret_cast<Vec*>(static_cast<T*>(p.out) + b * p.ob + d) = o;
+    if (slot[0] < 0) return;
+    b = b == row ? next[0] : named_next(p.slots, b, p.batch, slot[0], lane);
+    if (b >= p.batch) break;
+    x = at(p.x, p.xb, b);
+    ga = at(p.ga, p.gab, b);
+    gx = at(p.gx, p.gxb, b);
   }
-  p.state[slot * p.ss + d] = h;
+  if (live) *reinterpret_cast<State*>(p.state + slot[0] * p.ss + d) = h;
+}
+
+template <typename T>
+void launch_step(const StepParams& p, hipStream_t stream) {
+  // 4 channels a lane where every row allows accesses of 4
+  constexpr int64_t esz = sizeof(T);
+  auto fits = [](const void* q, int64_t stride, int64_t bytes) {
+    return reinterpret_cast<uintptr_t>(q) % static_cast<uintptr_t>(4 * bytes) == 0 && stride % 4 == 0;
+  };
+  const bool four = p.D % 4 == 0 && fits(p.state, p.ss, 4) && fits(p.x, p.xb, esz) && fits(p.ga, p.gab, esz) &&
+                    fits(p.gx, p.gxb, esz) && fits(p.out, p.ob, esz);
+  const int64_t lanes = four ? p.D / 4 : p.D;
+  const dim3 grid(static_cast<unsigned>((lanes + kThreads - 1) / kThreads), static_cast<unsigned>(p.batch));
+  if (four) gated_step_kernel<T, 4><<<grid, kThreads, 0, stream>>>(p);
+  else gated_step_kernel<T, 1><<<grid, kThreads, 0, stream>>>(p);
 }
 
 }  // namespace
@@ -293,12 +327,11 @@ hipError_t launch_gated_fwd(const ssm_gated_args& a, hipStream_t stream) {
 }
 
 hipError_t launch_gated_step(const ssm_gated_update_args& a, hipStream_t stream) {
-  StepParams p{a.state, a.x, a.gate_a, a.gate_x, a.lam, a.slots, a.out, a.state_slot_stride,
-               a.x_batch_stride, a.gate_a_batch_stride, a.gate_x_batch_stride, a.out_batch_stride,
-               a.batch, a.nslots, a.dim, a.c};
-  const dim3 grid(static_cast<unsigned>((a.dim + kThreads - 1) / kThreads), static_cast<unsigned>(a.batch));
-  if (a.io_dtype == SSM_BF16) gated_step_kernel<uint16_t><<<grid, kThreads, 0, stream>>>(p);
-  else gated_step_kernel<float><<<grid, kThreads, 0, stream>>>(p);
+  const StepParams p{a.state, a.x, a.gate_a, a.gate_x, a.lam, a.slots, a.out, a.state_slot_stride,
+                     a.x_batch_stride, a.gate_a_batch_stride, a.gate_x_batch_stride, a.out_batch_stride, a.dim,
+                     static_cast<int>(a.batch), static_cast<int>(a.nslots < 0x7fffffff ? a.nslots : 0x7fffffff), a.c};
+  if (a.io_dtype == SSM_BF16) launch_step<uint16_t>(p, stream);
+  else launch_step<float>(p, stream);
   return hipGetLastError();
 }
 

@@ -1,0 +1,54 @@
+// Rows of a batch that name the same slot of a pool.  They are taken in the
+// order of the rows: the workgroup of the first such row takes them all, and
+// the others leave theirs to it, so no two workgroups touch one slot.
+#pragma once
+
+#include "ssm_internal.h"
+
+namespace ssm {
+
+constexpr int kNames = 4;   // slots a lane compares at a time
+
+// For rows first .. first + ROWS - 1 with slots slot[]: bit r of `before` says
+// whether an earlier row names slot[r]; next[r] is the next row that does, or
+// batch.  Rows with slot -1 are of no account.  Without slots every row has its
+// own.
+template <int ROWS>
+__device__ __forceinline__ void slot_order(const int32_t* slots, int first, int batch, const int (&slot)[ROWS], int lane,
+                                           uint32_t& before, int (&next)[ROWS]) {
+  before = 0;
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) next[r] = batch;
+  if (!slots) return;
+  for (int base = 0; base < batch; base += 64 * kNames) {
+    int named[kNames];
+#pragma unroll
+    for (int k = 0; k < kNames; ++k) {
+      const int i = base + 64 * k + lane;
+      named[k] = i < batch ? slots[i] : -2;
+    }
+#pragma unroll
+    for (int k = 0; k < kNames; ++k)
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) {
+        const int own = first + r - base - 64 * k;   // this row's bit
+        const uint64_t hits = __ballot(named[k] == slot[r]);
+        const uint64_t below = own <= 0 ? 0 : own > 63 ? ~uint64_t{0} : (uint64_t{1} << own) - 1;
+        const uint64_t above = own < 0 ? ~uint64_t{0} : own > 62 ? 0 : ~uint64_t{0} << (own + 1);
+        if (hits & below) before |= 1u << r;
+        if ((hits & above) && next[r] == batch) next[r] = base + 64 * k + __builtin_ctzll(hits & above);
+      }
+  }
+}
+
+// The next row of the batch after row `from` that names this slot, or batch.
+__device__ __forceinline__ int named_next(const int32_t* slots, int from, int batch, int slot, int lane) {
+  for (int base = from + 1; base < batch; base += 64) {
+    const int i = base + lane;
+    const uint64_t hits = __ballot(i < batch && slots[i] == slot);
+    if (hits) return base + __builtin_ctzll(hits);
+  }
+  return batch;
+}
+
+}  // namespace ssm
