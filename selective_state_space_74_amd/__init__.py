@@ -805,10 +805,22 @@ def gated_scan_bwd_workspace_size(args: GatedBwdArgs) -> int:
     return lib().ssm_gated_scan_bwd_workspace_size(ctypes.byref(args))
 
 
+class _Current:
+    """The current stream as a context: nothing to switch."""
+    __slots__ = ("raw",)
+
+    def __init__(self, raw):
+        self.raw = raw
+
+    def __enter__(self):
+        return self.raw
+
+    def __exit__(self, *exc):
+        return False
+
+
 @contextlib.contextmanager
-def _on(device, stream):
-    """The tensors' device and the call's stream as the current ones: what is
-    allocated meanwhile belongs to that stream."""
+def _switched(device, stream):
     torch = _torch()
     with torch.cuda.device(device):
         if stream is None:
@@ -820,73 +832,78 @@ def _on(device, stream):
             yield stream.cuda_stream
 
 
-def _launch(name, args, stream):
-    st = getattr(lib(), "ssm_" + name)(ctypes.byref(args), _P(stream or None))
-    if st != 0:
-        raise SSMError(st, "ssm_" + name)
-
-
-def _like_tokens(name, t, x):
-    if t is None:
-        return
-    if tuple(t.shape) != tuple(x.shape):
-        raise ValueError(f"{name} must be shaped like x")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name} must have dim stride 1")
-
-
-def _set_tokens(a, name, t):
-    """Pointer and (batch, token) strides; a packed (tokens, dim) tensor is one batch row."""
-    setattr(a, name, _ptr(t))
-    setattr(a, name + "_batch_stride", t.stride(0) if t.dim() == 3 else 0)
-    setattr(a, name + "_seq_stride", t.stride(-2))
-
-
-def _gated_setup(a, x, gate_a, gate_x, lam, c, h0, cu_seqlens):
-    """Checks and fields that the gated scan and its backward share; returns the
-    number of sequences."""
+def _on(device, stream):
+    """The tensors' device and the call's stream as the current ones, and the
+    stream's handle: what is allocated meanwhile belongs to that stream."""
     torch = _torch()
-    if cu_seqlens is None and x.dim() != 3:
-        raise ValueError("x must be (batch, L, dim), or (tokens, dim) with cu_seqlens")
-    if cu_seqlens is not None and x.dim() != 2:
-        raise ValueError("x must be (tokens, dim) with cu_seqlens")
-    dev, dim = x.device, x.shape[-1]
-    code = _io_code(x)
-    _check_dev("x", x, dev, x.dtype)
-    for name, t in (("gate_a", gate_a), ("gate_x", gate_x)):
-        _check_dev(name, t, dev, x.dtype)
-    for name, t in (("x", x), ("gate_a", gate_a), ("gate_x", gate_x)):
-        _like_tokens(name, t, x)
-    _check_dev("lam", lam, dev, torch.float32)
-    _contig_f32("lam", lam, (dim,))
-    if cu_seqlens is not None:
-        _check_dev("cu_seqlens", cu_seqlens, dev, torch.int32)
-        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1 or not cu_seqlens.is_contiguous():
-            raise ValueError("cu_seqlens must be a contiguous int32 vector of nseq + 1 entries")
-    n = x.shape[0] if cu_seqlens is None else cu_seqlens.numel() - 1
-    _check_dev("h0", h0, dev, torch.float32)
-    _contig_f32("h0", h0, (n, dim))
+    if stream is None and device.index == torch.cuda.current_device():
+        return _Current(torch._C._cuda_getCurrentRawStream(device.index))
+    return _switched(device, stream)
+
+
+def _launch(name, args, stream):
+    st = getattr(lib(), name)(ctypes.byref(args), stream or None)
+    if st != 0:
+        raise SSMError(st, name)
+
+
+def _tokens(name, t, shape, dtype, device):
+    """Pointer and (batch, token) strides of a tensor shaped and typed like x; a
+    packed (tokens, dim) tensor is one batch row."""
+    if t.device != device or not t.is_cuda or t.dtype != dtype:
+        _check_dev(name, t, device, dtype)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be shaped like x")
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"{name} must have dim stride 1")
+    return (t.data_ptr(), st[0], st[1]) if len(st) == 3 else (t.data_ptr(), 0, st[0])
+
+
+def _fp32(name, t, shape, device):
+    """Pointer of a contiguous fp32 tensor of this shape, None for None."""
+    if t is None:
+        return None
+    if t.device != device or t.dtype != _torch().float32:
+        _check_dev(name, t, device, _torch().float32)
+    if t.shape != shape or not t.is_contiguous():
+        _contig_f32(name, t, shape)
+    return t.data_ptr()
+
+
+def _decay_constant(c):
     c = float(c)
     if not 0.0 < c < float("inf"):
         raise ValueError("c must be positive and finite")
-    a.batch, a.seqlen, a.dim = (x.shape[0] if cu_seqlens is None else 1), x.shape[-2], dim
-    a.nseq, a.io_dtype, a.c = (0 if cu_seqlens is None else n), code, c
-    for name, t in (("x", x), ("gate_a", gate_a), ("gate_x", gate_x)):
-        _set_tokens(a, name, t)
-    a.lam, a.h0, a.cu_seqlens = _ptr(lam), _ptr(h0), _ptr(cu_seqlens)
-    return n
+    return c
+
+
+def _gated_sizes(x, cu_seqlens):
+    """(batch, tokens of a row, number of sequences, nseq field, bounds' pointer)."""
+    torch = _torch()
+    if cu_seqlens is None:
+        if x.dim() != 3:
+            raise ValueError("x must be (batch, L, dim), or (tokens, dim) with cu_seqlens")
+        return x.shape[0], x.shape[1], x.shape[0], 0, None
+    if x.dim() != 2:
+        raise ValueError("x must be (tokens, dim) with cu_seqlens")
+    _check_dev("cu_seqlens", cu_seqlens, x.device, torch.int32)
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1 or not cu_seqlens.is_contiguous():
+        raise ValueError("cu_seqlens must be a contiguous int32 vector of nseq + 1 entries")
+    n = cu_seqlens.numel() - 1
+    return 1, x.shape[0], n, n, cu_seqlens.data_ptr()
 
 
 def _set_workspace(a, need, workspace, device):
-    torch = _torch()
     if not need:
         return None
     if workspace is None or workspace.numel() * workspace.element_size() < need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    _check_dev("workspace", workspace, device)
-    if not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
+        workspace = _torch().empty(need, dtype=_torch().uint8, device=device)
+    else:
+        _check_dev("workspace", workspace, device)
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+    a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     return workspace
 
 
@@ -913,25 +930,26 @@ def gated_scan_fwd(x, gate_a, gate_x, lam, c=8.0, h0=None, cu_seqlens=None, retu
     for gated_scan_bwd.  `last_state` may be h0 itself.  `workspace`: a device
     tensor reused across calls (by one call at a time); None allocates one."""
     torch = _torch()
-    a = GatedArgs()
-    n = _gated_setup(a, x, gate_a, gate_x, lam, c, h0, cu_seqlens)
-    dev, dim = x.device, x.shape[-1]
-    _check_dev("out", out, dev, x.dtype)
-    _like_tokens("out", out, x)
-    for name, t, shape in (("last_state", last_state, (n, dim)),
-                           ("checkpoints", checkpoints, gated_checkpoint_shape(x.shape))):
-        _check_dev(name, t, dev, torch.float32)
-        _contig_f32(name, t, shape)
+    shape, dev, io = x.shape, x.device, x.dtype
+    code = _io_code(x)
+    batch, L, n, nseq, cu = _gated_sizes(x, cu_seqlens)
+    dim = shape[-1]
+    inputs = _tokens("x", x, shape, io, dev) + _tokens("gate_a", gate_a, shape, io, dev) + \
+        _tokens("gate_x", gate_x, shape, io, dev)
+    lam_p, h0_p = _fp32("lam", lam, (dim,), dev), _fp32("h0", h0, (n, dim), dev)
+    c = _decay_constant(c)
     with _on(dev, stream) as s:
-        if out is None:
-            a.zero_outside = 1
-            out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        made = out is None
+        if made:
+            out = torch.empty(shape, dtype=io, device=dev)
         if return_last_state and last_state is None:
             last_state = torch.empty((n, dim), dtype=torch.float32, device=dev)
-        _set_tokens(a, "out", out)
-        a.last_state, a.checkpoints = _ptr(last_state), _ptr(checkpoints)
+        a = GatedArgs(batch, L, dim, nseq, code, made, c, *inputs, lam_p, cu, h0_p,
+                      _fp32("last_state", last_state, (n, dim), dev), *_tokens("out", out, shape, io, dev),
+                      checkpoints if checkpoints is None else
+                      _fp32("checkpoints", checkpoints, gated_checkpoint_shape(shape), dev))
         workspace = _set_workspace(a, gated_scan_workspace_size(a), workspace, dev)
-        _launch("gated_scan_fwd", a, s)
+        _launch("ssm_gated_scan_fwd", a, s)
     return (out, last_state) if return_last_state else out
 
 
@@ -943,27 +961,29 @@ def gated_scan_bwd(dout, x, gate_a, gate_x, lam, checkpoints, c=8.0, h0=None, cu
     Rows of tokens outside every sequence are zero.  Every output is the same
     bits from run to run.  `workspace`: as for gated_scan_fwd."""
     torch = _torch()
-    a = GatedBwdArgs()
-    n = _gated_setup(a, x, gate_a, gate_x, lam, c, h0, cu_seqlens)
-    dev, dim = x.device, x.shape[-1]
-    _check_dev("dout", dout, dev, x.dtype)
-    _like_tokens("dout", dout, x)
-    for name, t, shape in (("dlast", dlast, (n, dim)),
-                           ("checkpoints", checkpoints, gated_checkpoint_shape(x.shape))):
-        _check_dev(name, t, dev, torch.float32)
-        _contig_f32(name, t, shape)
+    shape, dev, io = x.shape, x.device, x.dtype
+    code = _io_code(x)
+    batch, L, n, nseq, cu = _gated_sizes(x, cu_seqlens)
+    dim = shape[-1]
+    inputs = _tokens("x", x, shape, io, dev) + _tokens("gate_a", gate_a, shape, io, dev) + \
+        _tokens("gate_x", gate_x, shape, io, dev)
+    lam_p, h0_p = _fp32("lam", lam, (dim,), dev), _fp32("h0", h0, (n, dim), dev)
+    ck_p = _fp32("checkpoints", checkpoints, gated_checkpoint_shape(shape), dev)
+    upstream = _tokens("dout", dout, shape, io, dev)
+    dlast_p = _fp32("dlast", dlast, (n, dim), dev)
+    c = _decay_constant(c)
     with _on(dev, stream) as s:
-        g = {k: torch.empty(x.shape, dtype=x.dtype, device=dev) for k in ("dx", "dgate_a", "dgate_x")}
-        for k, t in g.items():
-            _set_tokens(a, k, t)
-        g["dlam"] = torch.empty(dim, dtype=torch.float32, device=dev)
+        dx, dga, dgx = (torch.empty(shape, dtype=io, device=dev) for _ in range(3))
+        g = dict(dx=dx, dgate_a=dga, dgate_x=dgx, dlam=torch.empty(dim, dtype=torch.float32, device=dev))
         if h0 is not None:
             g["dh0"] = torch.empty((n, dim), dtype=torch.float32, device=dev)
-        _set_tokens(a, "dout", dout)
-        a.checkpoints, a.dlast = _ptr(checkpoints), _ptr(dlast)
-        a.dlam, a.dh0 = _ptr(g["dlam"]), _ptr(g.get("dh0"))
+        # the three gradients have the same strides: a row of tokens after another
+        rows = (L * dim, dim)
+        a = GatedBwdArgs(batch, L, dim, nseq, code, c, *inputs, lam_p, cu, h0_p, ck_p, *upstream, dlast_p,
+                         dx.data_ptr(), *rows, dga.data_ptr(), *rows, dgx.data_ptr(), *rows, g["dlam"].data_ptr(),
+                         _ptr(g.get("dh0")))
         workspace = _set_workspace(a, gated_scan_bwd_workspace_size(a), workspace, dev)
-        _launch("gated_scan_bwd", a, s)
+        _launch("ssm_gated_scan_bwd", a, s)
     return g
 
 
@@ -1006,9 +1026,15 @@ def _check_slots(slots, batch, nslots, device):
         raise ValueError("slots must be a contiguous int32 vector with one entry per batch row")
 
 
-def _check_row_tokens(name, t, batch, dim):
-    if t is not None and (tuple(t.shape) != (batch, dim) or (dim > 1 and t.stride(1) != 1)):
+def _row_tokens(name, t, batch, dim, dtype, device):
+    """Pointer and row stride of a (batch, dim) tensor, (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if t.device != device or not t.is_cuda or t.dtype != dtype:
+        _check_dev(name, t, device, dtype)
+    if t.shape != (batch, dim) or (dim > 1 and t.stride(1) != 1):
         raise ValueError(f"{name} must be (batch, dim) with dim stride 1")
+    return t.data_ptr(), t.stride(0)
 
 
 def gated_state_update(state, x, gate_a, gate_x, lam, c=8.0, slots=None, out=None, stream=None):
@@ -1020,31 +1046,22 @@ def gated_state_update(state, x, gate_a, gate_x, lam, c=8.0, slots=None, out=Non
     torch = _torch()
     if state.dim() != 2 or x.dim() != 2:
         raise ValueError("state must be (nslots, dim) and x (batch, dim)")
-    (nslots, dim), batch, dev = state.shape, x.shape[0], state.device
-    a = GatedUpdateArgs()
-    a.io_dtype = _io_code(x)
+    (nslots, dim), batch, dev, io = state.shape, x.shape[0], state.device, x.dtype
+    code = _io_code(x)
     _check_dev("state", state, dev, torch.float32)
     if dim > 1 and state.stride(1) != 1:
         raise ValueError("state must have dim stride 1")
-    for name, t in (("x", x), ("gate_a", gate_a), ("gate_x", gate_x), ("out", out)):
-        _check_dev(name, t, dev, x.dtype)
-        _check_row_tokens(name, t, batch, dim)
-    _check_dev("lam", lam, dev, torch.float32)
-    _contig_f32("lam", lam, (dim,))
+    inputs = _row_tokens("x", x, batch, dim, io, dev) + _row_tokens("gate_a", gate_a, batch, dim, io, dev) + \
+        _row_tokens("gate_x", gate_x, batch, dim, io, dev)
+    lam_p = _fp32("lam", lam, (dim,), dev)
     _check_slots(slots, batch, nslots, dev)
-    c = float(c)
-    if not 0.0 < c < float("inf"):
-        raise ValueError("c must be positive and finite")
+    c = _decay_constant(c)
     with _on(dev, stream) as s:
         if out is None:
-            out = torch.empty((batch, dim), dtype=x.dtype, device=dev)
-        a.batch, a.nslots, a.dim, a.c = batch, nslots, dim, c
-        a.state, a.state_slot_stride = _ptr(state), state.stride(0)
-        for name, t in (("x", x), ("gate_a", gate_a), ("gate_x", gate_x), ("out", out)):
-            setattr(a, name, _ptr(t))
-            setattr(a, name + "_batch_stride", t.stride(0))
-        a.lam, a.slots = _ptr(lam), _ptr(slots)
-        _launch("gated_state_update", a, s)
+            out = torch.empty((batch, dim), dtype=io, device=dev)
+        a = GatedUpdateArgs(batch, nslots, dim, code, c, state.data_ptr(), state.stride(0), *inputs, lam_p, _ptr(slots),
+                            *_row_tokens("out", out, batch, dim, io, dev))
+        _launch("ssm_gated_state_update", a, s)
     return out
 
 
@@ -1068,38 +1085,32 @@ def _inner_contiguous(t):
     return t.shape[0] == 0 or t[0].is_contiguous()
 
 
-def _cache_setup(a, codes, scales, shape, format):
-    """Checks and fields of a cache's two tensors for states of a shape."""
-    torch = _torch()
-    dev, n = codes.device, codes.shape[0] if codes.dim() else 0
-    want = state_cache_shape(n, shape, format)
-    for name, t, w in (("codes", codes, want[0]), ("scales", scales, want[1])):
-        _check_dev(name, t, dev, torch.uint8)
-        if tuple(t.shape) != w:
-            raise ValueError(f"{name} must have shape {w} for this state and format, got {tuple(t.shape)}")
-        if not _inner_contiguous(t):
+def _cache_fields(codes, scales, shape, format):
+    """Pointers and slot strides of a cache's two tensors, for states of a shape."""
+    uint8, dev = _torch().uint8, codes.device
+    fields = ()
+    for name, t, want in zip(("codes", "scales"), (codes, scales),
+                             state_cache_shape(codes.shape[0] if codes.dim() else 0, shape, format)):
+        _check_dev(name, t, dev, uint8)
+        if t.shape != want:
+            raise ValueError(f"{name} must have shape {want} for this state and format, got {tuple(t.shape)}")
+        if not t.is_contiguous() and not _inner_contiguous(t):
             raise ValueError(f"{name} must be contiguous within a slot")
-    a.nslots = n
-    a.codes, a.codes_slot_stride = _ptr(codes), codes.stride(0)
-    a.scales, a.scales_slot_stride = _ptr(scales), scales.stride(0)
-    return n
+        fields += (t.data_ptr(), t.stride(0))
+    return fields
 
 
 def _cache_args(codes, scales, states, slots, format):
     if states.dim() < 2:
         raise ValueError("states must be (batch, ...)")
-    dev, batch = codes.device, states.shape[0]
-    a = StateCacheArgs()
-    n = _cache_setup(a, codes, scales, states.shape[1:], format)
+    dev, shape, nslots = codes.device, states.shape, codes.shape[0] if codes.dim() else 0
+    fields = _cache_fields(codes, scales, shape[1:], format)
     _check_dev("states", states, dev, states.dtype)
-    a.io_dtype, a.format = _io_code(states), CACHE_FORMATS[format]
-    if not _inner_contiguous(states):
+    if not states.is_contiguous() and not _inner_contiguous(states):
         raise ValueError("states must be contiguous within a batch row")
-    _check_slots(slots, batch, n, dev)
-    a.batch, a.inner = batch, states.shape[-1]
-    a.outer = math.prod(states.shape[1:-1])
-    a.states, a.states_batch_stride, a.slots = _ptr(states), states.stride(0), _ptr(slots)
-    return a
+    _check_slots(slots, shape[0], nslots, dev)
+    return StateCacheArgs(shape[0], nslots, math.prod(shape[1:-1]), shape[-1], CACHE_FORMATS[format], _io_code(states),
+                          *fields, states.data_ptr(), states.stride(0), _ptr(slots))
 
 
 def state_cache_write(codes, scales, states, slots=None, format="int8", stream=None):
@@ -1112,7 +1123,7 @@ def state_cache_write(codes, scales, states, slots=None, format="int8", stream=N
     or an infinity reads back as NaN."""
     a = _cache_args(codes, scales, states, slots, format)
     with _on(codes.device, stream) as s:
-        _launch("state_cache_write", a, s)
+        _launch("ssm_state_cache_write", a, s)
 
 
 def state_cache_read(codes, scales, slots=None, format="int8", dtype=None, out=None, stream=None):
@@ -1131,7 +1142,7 @@ def state_cache_read(codes, scales, slots=None, format="int8", dtype=None, out=N
     with _on(codes.device, stream) as s:
         if out is None:
             out = torch.empty(shape, dtype=dtype or torch.float32, device=codes.device)
-        _launch("state_cache_read", _cache_args(codes, scales, out, slots, format), s)
+        _launch("ssm_state_cache_read", _cache_args(codes, scales, out, slots, format), s)
     return out
 
 
@@ -1151,23 +1162,19 @@ def selective_state_update_cached(codes, scales, x, dt, A, B, C, D=None, z=None,
     if codes.dim() != 3 or x.dim() != 2:
         raise ValueError("codes must be (nslots, dim, dstate) and x (batch, dim)")
     (nslots, dim, N), batch, dev, io = codes.shape, x.shape[0], codes.device, x.dtype
-    a = CachedUpdateArgs()
-    a.io_dtype, a.dt_softplus = _io_code(x), int(bool(dt_softplus))
-    _cache_setup(a, codes, scales, (dim, N), "int8")
-    for name, t in (("x", x), ("dt", dt), ("z", z), ("out", out)):
-        _check_dev(name, t, dev, io)
-        _check_row_tokens(name, t, batch, dim)
+    code = _io_code(x)
+    held = _cache_fields(codes, scales, (dim, N), "int8")
+    inputs = _row_tokens("x", x, batch, dim, io, dev) + _row_tokens("dt", dt, batch, dim, io, dev) + \
+        _row_tokens("z", z, batch, dim, io, dev)
     for name, t in (("B", B), ("C", C)):
         _check_dev(name, t, dev, io)
         if N > 1 and t.stride(-1) != 1:
             raise ValueError(f"{name} must have state stride 1")
     G = _bc_groups(B, C, batch, dim, N, ())
-    for name, t in (("A", A), ("D", D), ("dt_bias", dt_bias)):
-        _check_dev(name, t, dev, torch.float32)
-    if tuple(A.shape) != (dim, N) or (N > 1 and A.stride(1) != 1):
+    _check_dev("A", A, dev, torch.float32)
+    if A.shape != (dim, N) or (N > 1 and A.stride(1) != 1):
         raise ValueError("A must be (dim, dstate) with state stride 1")
-    _contig_f32("D", D, (dim,))
-    _contig_f32("dt_bias", dt_bias, (dim,))
+    D_p, bias_p = _fp32("D", D, (dim,), dev), _fp32("dt_bias", dt_bias, (dim,), dev)
     _check_slots(slots, batch, nslots, dev)
     if seed is not None:
         _check_dev("seed", seed, dev, torch.int64)
@@ -1176,13 +1183,9 @@ def selective_state_update_cached(codes, scales, x, dt, A, B, C, D=None, z=None,
     with _on(dev, stream) as s:
         if out is None:
             out = torch.empty((batch, dim), dtype=io, device=dev)
-        a.batch, a.dim, a.dstate = batch, dim, N
-        for name, t in (("x", x), ("dt", dt), ("z", z), ("out", out)):
-            if t is not None:
-                setattr(a, name, _ptr(t))
-                setattr(a, name + "_batch_stride", t.stride(0))
-        _set_bc(a, B, C, G, time=False)
-        a.A, a.A_dim_stride, a.D, a.dt_bias = _ptr(A), A.stride(0), _ptr(D), _ptr(dt_bias)
-        a.slots, a.seed = _ptr(slots), _ptr(seed)
-        _launch("selective_state_update_cached", a, s)
+        a = CachedUpdateArgs(batch, nslots, dim, N, code, bool(dt_softplus), *held, *inputs,
+                             B.data_ptr(), B.stride(0), B.stride(1) if G else 0,
+                             C.data_ptr(), C.stride(0), C.stride(1) if G else 0, A.data_ptr(), A.stride(0), D_p, bias_p,
+                             *_row_tokens("out", out, batch, dim, io, dev), _ptr(slots), _ptr(seed), G)
+        _launch("ssm_selective_state_update_cached", a, s)
     return out
