@@ -47,21 +47,25 @@ __device__ __forceinline__ float uniform_value(const T* p, int i) {
   }
 }
 
-// CH: 16-state chunks of a channel.  WIDE: N = 16 CH, and every access may take
-// 16 codes (4 values of A); UNIFORM: one B/C group a wavefront, rows of B and C
-// readable by 32-bit words.  SEEDED: stochastic rounding.
-template <typename T, int CH, bool WIDE, bool UNIFORM, bool SEEDED>
+// CH: 16-state chunks of a channel.  WIDTH: states of an access to the codes:
+// 16 (N = 16 CH), 4 (N and every row a multiple of 4) or 1.  With 16 and 4 a
+// wavefront is in one B/C group, whose rows come in 32-bit words.  SEEDED:
+// stochastic rounding.
+template <typename T, int CH, int WIDTH, bool SEEDED>
 struct Channel {
   static constexpr int NS = 16 * CH, NB = (CH + 1) / 2;
   uint32_t q[4 * CH];   // codes
   uint32_t e[NB];       // scale bytes
+  static constexpr bool kUniform = WIDTH > 1;
+  // whether the channel has states from n on (uniform; always with whole chunks)
+  __device__ static __forceinline__ bool has(const CachedParams& p, int n) { return WIDTH == 16 || n < p.N; }
 
   // the channel's row of A, times log2(e)
   __device__ static __forceinline__ void load_a(const CachedParams& p, int64_t d, float (&a)[NS]) {
 #pragma unroll
     for (int n = 0; n < NS; n += 4) {
-      if constexpr (WIDE) {
-        const float4 f = *reinterpret_cast<const float4*>(p.A + d * p.Ad + n);
+      if constexpr (WIDTH > 1) {
+        const float4 f = has(p, n) ? *reinterpret_cast<const float4*>(p.A + d * p.Ad + n) : make_float4(0, 0, 0, 0);
         a[n] = f.x; a[n + 1] = f.y; a[n + 2] = f.z; a[n + 3] = f.w;
       } else {
 #pragma unroll
@@ -79,9 +83,12 @@ struct Channel {
     for (int k = 0; k < NB; ++k) e[k] = p.scales[slot * p.ss + d * nb + k];
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      if constexpr (WIDE) {
+      if constexpr (WIDTH == 16) {
         const uint4 w = reinterpret_cast<const uint4*>(c)[k];
         q[4 * k] = w.x; q[4 * k + 1] = w.y; q[4 * k + 2] = w.z; q[4 * k + 3] = w.w;
+      } else if constexpr (WIDTH == 4) {
+#pragma unroll
+        for (int w = 4 * k; w < 4 * k + 4; ++w) q[w] = has(p, 4 * w) ? reinterpret_cast<const uint32_t*>(c)[w] : 0u;
       } else {
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
@@ -101,7 +108,11 @@ struct Channel {
     for (int k = 0; k < NB; ++k) p.scales[slot * p.ss + d * nb + k] = static_cast<uint8_t>(e[k]);
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      if constexpr (WIDE) {
+      if constexpr (WIDTH == 4) {
+#pragma unroll
+        for (int w = 4 * k; w < 4 * k + 4; ++w)
+          if (has(p, 4 * w)) reinterpret_cast<uint32_t*>(c)[w] = q[w];
+      } else if constexpr (WIDTH == 16) {
         reinterpret_cast<uint4*>(c)[k] = make_uint4(q[4 * k], q[4 * k + 1], q[4 * k + 2], q[4 * k + 3]);
       } else {
 #pragma unroll
@@ -111,25 +122,13 @@ struct Channel {
     }
   }
 
-  // One step of row b on the state in q, e; returns sum_n C s'.
-  __device__ __forceinline__ float step(const CachedParams& p, int b, int64_t d, const float (&a)[NS], float dl, float x,
-                                        uint64_t seed) {
-    const int64_t g = UNIFORM && p.cpg == p.dim ? 0 : d / p.cpg;
-    const T* Bp = static_cast<const T*>(p.B) + b * p.Bb + g * p.Bg;
-    const T* Cp = static_cast<const T*>(p.C) + b * p.Cb + g * p.Cg;
-    if constexpr (UNIFORM) {
-      // the same address in every lane: make that known
-      auto first = [](const T* v) {
-        const uint64_t u = reinterpret_cast<uint64_t>(v);
-        return reinterpret_cast<const T*>(
-            static_cast<uint64_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(u >> 32))) << 32 |
-            static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(u))));
-      };
-      Bp = first(Bp);
-      Cp = first(Cp);
-    }
+  // One step of row b (B/C group g) on the state in q, e; returns sum_n C s'.
+  __device__ __forceinline__ float step(const CachedParams& p, int b, int64_t g, int64_t d, const float (&a)[NS], float dl,
+                                        float x, uint64_t seed) {
+    const T* const Bp = static_cast<const T*>(p.B) + b * p.Bb + g * p.Bg;
+    const T* const Cp = static_cast<const T*>(p.C) + b * p.Cb + g * p.Cg;
     auto bc = [&](const T* v, int n) -> float {
-      if constexpr (UNIFORM) return uniform_value(v, n);
+      if constexpr (kUniform) return uniform_value(v, n);
       else return n < p.N ? io<T>::load(v + n) : 0.0f;
     };
     float h[NS];
@@ -137,6 +136,10 @@ struct Channel {
     float y = 0.0f;
 #pragma unroll
     for (int k = 0; k < 4 * CH; ++k) {
+      if (!has(p, 4 * k)) {
+        h[4 * k] = h[4 * k + 1] = h[4 * k + 2] = h[4 * k + 3] = 0.0f;
+        continue;
+      }
       float s[4];
       decode4_int8(q[k], scale_value(e[k / 8]), s);
 #pragma unroll
@@ -147,8 +150,8 @@ struct Channel {
       }
     }
     // Largest magnitudes.  fmax drops a NaN; but a state that is not finite
-    // makes y so too, and then the maximum is taken over the magnitudes' bits.
-    const bool finite = magnitude(y) < 0x7f800000u;
+    // makes y so too, and then the magnitudes' bits are compared.
+    const bool odd = __any(magnitude(y) >= 0x7f800000u);
 #pragma unroll
     for (int k = 0; k < NB; ++k) {
       constexpr int kIn = NS < kCacheBlock ? NS : kCacheBlock;
@@ -156,8 +159,7 @@ struct Channel {
 #pragma unroll
       for (int n = k * kCacheBlock; n < k * kCacheBlock + kIn && n < NS; ++n) m = fmaxf(m, fabsf(h[n]));
       uint32_t bits = __float_as_uint(m);
-      if (!finite) {
-        bits = 0;
+      if (odd) {
 #pragma unroll
         for (int n = k * kCacheBlock; n < k * kCacheBlock + kIn && n < NS; ++n) bits = max(bits, magnitude(h[n]));
       }
@@ -171,6 +173,7 @@ struct Channel {
     const bool two = SEEDED && __any(tiny);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
+      if (!has(p, 16 * c)) continue;
       const uint32_t eb = e[c / 2];
       const float inv = scale_inverse(eb);
       uint32_t t[16];
@@ -199,7 +202,7 @@ struct Channel {
   }
 };
 
-template <typename T, int CH, bool WIDE, bool UNIFORM, bool SEEDED, int ROWS>
+template <typename T, int CH, int WIDTH, bool SEEDED, int ROWS>
 __global__ __launch_bounds__(kThreads) void cached_update_kernel(CachedParams p) {
   const int lane = threadIdx.x & 63;
   const int64_t d0 = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
@@ -208,8 +211,15 @@ __global__ __launch_bounds__(kThreads) void cached_update_kernel(CachedParams p)
   const bool live = d0 < p.dim;
   const int64_t d = live ? d0 : p.dim - 1;   // lanes past the channels repeat the last one, and store nothing
   const int first = blockIdx.y * ROWS;
+  // the channel's B/C group, a scalar where the wavefront is in one
+  int64_t g = 0;
+  if (p.cpg != p.dim) {
+    if constexpr (Channel<T, CH, WIDTH, SEEDED>::kUniform)
+      g = __builtin_amdgcn_readfirstlane(static_cast<int>(static_cast<uint32_t>(wave0) / static_cast<uint32_t>(p.cpg)));
+    else g = static_cast<uint32_t>(d) / static_cast<uint32_t>(p.cpg);
+  }
 
-  using Ch = Channel<T, CH, WIDE, UNIFORM, SEEDED>;
+  using Ch = Channel<T, CH, WIDTH, SEEDED>;
   Ch ch[ROWS];
   float a[Ch::NS], xv[ROWS], dtv[ROWS], zv[ROWS];
   int slot[ROWS];
@@ -251,7 +261,7 @@ __global__ __launch_bounds__(kThreads) void cached_update_kernel(CachedParams p)
     for (;;) {
       float dl = dtv[r] + bias;
       if (p.softplus) dl = softplus_f32(dl);
-      float y = fmaf(Dd, xv[r], ch[r].step(p, b, d, a, dl, xv[r], seed));
+      float y = fmaf(Dd, xv[r], ch[r].step(p, b, g, d, a, dl, xv[r], seed));
       if (p.z) y *= silu_f32(zv[r]);
       if (live) io<T>::store(out + b * p.ob, y);
       b = b == first + r ? next[r] : named_next(p.slots, b, p.batch, slot[r], lane);
@@ -262,37 +272,37 @@ __global__ __launch_bounds__(kThreads) void cached_update_kernel(CachedParams p)
   }
 }
 
-template <typename T, int CH, bool WIDE, bool UNIFORM>
-void launch_u(const CachedParams& p, hipStream_t stream) {
+template <typename T, int CH, int WIDTH>
+void launch_w(const CachedParams& p, hipStream_t stream) {
   const unsigned xb = static_cast<unsigned>((p.dim + kThreads - 1) / kThreads);
   if constexpr (CH == 1) {
     const int64_t rows = (p.batch + kRows - 1) / kRows;
     if (xb * rows >= kMinBlocks) {
       const dim3 grid(xb, static_cast<unsigned>(rows));
-      if (p.seed) cached_update_kernel<T, CH, WIDE, UNIFORM, true, kRows><<<grid, kThreads, 0, stream>>>(p);
-      else cached_update_kernel<T, CH, WIDE, UNIFORM, false, kRows><<<grid, kThreads, 0, stream>>>(p);
+      if (p.seed) cached_update_kernel<T, CH, WIDTH, true, kRows><<<grid, kThreads, 0, stream>>>(p);
+      else cached_update_kernel<T, CH, WIDTH, false, kRows><<<grid, kThreads, 0, stream>>>(p);
       return;
     }
   }
   const dim3 grid(xb, static_cast<unsigned>(p.batch));
-  if (p.seed) cached_update_kernel<T, CH, WIDE, UNIFORM, true, 1><<<grid, kThreads, 0, stream>>>(p);
-  else cached_update_kernel<T, CH, WIDE, UNIFORM, false, 1><<<grid, kThreads, 0, stream>>>(p);
+  if (p.seed) cached_update_kernel<T, CH, WIDTH, true, 1><<<grid, kThreads, 0, stream>>>(p);
+  else cached_update_kernel<T, CH, WIDTH, false, 1><<<grid, kThreads, 0, stream>>>(p);
 }
 
 template <typename T, int CH>
-void launch_c(bool wide, bool uniform, const CachedParams& p, hipStream_t stream) {
-  // the short forms: whole chunks with uniform B and C, or everything element by element
-  if (wide && uniform) launch_u<T, CH, true, true>(p, stream);
-  else launch_u<T, CH, false, false>(p, stream);
+void launch_c(int width, const CachedParams& p, hipStream_t stream) {
+  if (width == 16) launch_w<T, CH, 16>(p, stream);
+  else if (width == 4) launch_w<T, CH, 4>(p, stream);
+  else launch_w<T, CH, 1>(p, stream);
 }
 
 template <typename T>
-void launch_t(bool wide, bool uniform, const CachedParams& p, hipStream_t stream) {
+void launch_t(int width, const CachedParams& p, hipStream_t stream) {
   switch ((p.N + 15) / 16) {
-    case 1: launch_c<T, 1>(wide, uniform, p, stream); break;
-    case 2: launch_c<T, 2>(wide, uniform, p, stream); break;
-    case 3: launch_c<T, 3>(wide, uniform, p, stream); break;
-    default: launch_c<T, 4>(wide, uniform, p, stream); break;
+    case 1: launch_c<T, 1>(width, p, stream); break;
+    case 2: launch_c<T, 2>(width, p, stream); break;
+    case 3: launch_c<T, 3>(width, p, stream); break;
+    default: launch_c<T, 4>(width, p, stream); break;
   }
 }
 
@@ -308,11 +318,12 @@ hipError_t launch_cached_update(const ssm_cached_update_args& a, hipStream_t str
                        static_cast<int>(a.dstate), a.dt_softplus ? 1 : 0};
   auto al = [](const void* q, int64_t bytes) { return reinterpret_cast<uintptr_t>(q) % static_cast<uintptr_t>(bytes) == 0; };
   const int64_t w = a.io_dtype == SSM_BF16 ? 2 : 1;   // elements of a 32-bit word
-  const bool wide = p.N % 16 == 0 && al(a.codes, 16) && a.codes_slot_stride % 16 == 0 && al(a.A, 16) && a.A_dim_stride % 4 == 0;
   const bool uniform = (G == 1 || p.cpg % 64 == 0) && al(a.B, 4) && al(a.C, 4) && p.Bb % w == 0 && p.Cb % w == 0 &&
                        p.Bg % w == 0 && p.Cg % w == 0;
-  if (a.io_dtype == SSM_BF16) launch_t<uint16_t>(wide, uniform, p, stream);
-  else launch_t<float>(wide, uniform, p, stream);
+  auto fits = [&](int64_t n) { return p.N % n == 0 && al(a.codes, n) && a.codes_slot_stride % n == 0; };
+  const int width = !uniform || !al(a.A, 16) || a.A_dim_stride % 4 != 0 ? 1 : fits(16) ? 16 : fits(4) ? 4 : 1;
+  if (a.io_dtype == SSM_BF16) launch_t<uint16_t>(width, p, stream);
+  else launch_t<float>(width, p, stream);
   return hipGetLastError();
 }
 

@@ -20,6 +20,8 @@ __device__ __forceinline__ void slot_order(const int32_t* slots, int first, int 
 #pragma unroll
   for (int r = 0; r < ROWS; ++r) next[r] = batch;
   if (!slots) return;
+  // hardly ever does any: look for that first
+  bool shared = false;
   for (int base = 0; base < batch; base += 64 * kNames) {
     int named[kNames];
 #pragma unroll
@@ -30,14 +32,19 @@ __device__ __forceinline__ void slot_order(const int32_t* slots, int first, int 
 #pragma unroll
     for (int k = 0; k < kNames; ++k)
 #pragma unroll
-      for (int r = 0; r < ROWS; ++r) {
-        const int own = first + r - base - 64 * k;   // this row's bit
-        const uint64_t hits = __ballot(named[k] == slot[r]);
-        const uint64_t below = own <= 0 ? 0 : own > 63 ? ~uint64_t{0} : (uint64_t{1} << own) - 1;
-        const uint64_t above = own < 0 ? ~uint64_t{0} : own > 62 ? 0 : ~uint64_t{0} << (own + 1);
-        if (hits & below) before |= 1u << r;
-        if ((hits & above) && next[r] == batch) next[r] = base + 64 * k + __builtin_ctzll(hits & above);
-      }
+      for (int r = 0; r < ROWS; ++r) shared |= named[k] == slot[r] && base + 64 * k + lane != first + r;
+  }
+  if (!__any(shared)) return;
+  for (int base = 0; base < batch; base += 64) {
+    const int i = base + lane;
+    const int named = i < batch ? slots[i] : -2;
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      const bool hit = named == slot[r];
+      if (__any(hit && i < first + r)) before |= 1u << r;
+      const uint64_t later = __ballot(hit && i > first + r);
+      if (later && next[r] == batch) next[r] = base + __builtin_ctzll(later);
+    }
   }
 }
 

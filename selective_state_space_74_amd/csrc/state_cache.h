@@ -102,15 +102,18 @@ __device__ __forceinline__ void decode4(uint32_t codes, float unit, float (&v)[4
 // Philox-4x32 (Salmon, Moraes, Dror and Shaw, "Parallel random numbers: as easy
 // as 1, 2, 3", 2011) with 7 rounds, the fewest that paper found to pass its
 // tests: 16 random bytes for a counter and a 64-bit key.
+__device__ __forceinline__ uint32_t xor3(uint32_t a, uint32_t b, uint32_t c) {
+  return __builtin_amdgcn_bitop3_b32(a, b, c, 0x96);   // the truth table of a ^ b ^ c
+}
 __device__ __forceinline__ void philox7(uint32_t (&c)[4], uint64_t seed) {
   uint32_t k0 = static_cast<uint32_t>(seed), k1 = static_cast<uint32_t>(seed >> 32);
 #pragma unroll
   for (int r = 0; r < 7; ++r) {
     const uint64_t p0 = static_cast<uint64_t>(0xD2511F53u) * c[0];
     const uint64_t p1 = static_cast<uint64_t>(0xCD9E8D57u) * c[2];
-    c[0] = static_cast<uint32_t>(p1 >> 32) ^ c[1] ^ k0;
+    c[0] = xor3(static_cast<uint32_t>(p1 >> 32), c[1], k0);
     c[1] = static_cast<uint32_t>(p1);
-    c[2] = static_cast<uint32_t>(p0 >> 32) ^ c[3] ^ k1;
+    c[2] = xor3(static_cast<uint32_t>(p0 >> 32), c[3], k1);
     c[3] = static_cast<uint32_t>(p0);
     k0 += 0x9E3779B9u;
     k1 += 0xBB67AE85u;
