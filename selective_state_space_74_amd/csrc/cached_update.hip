@@ -20,8 +20,6 @@ namespace ssm {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRows = 4;              // batch rows a thread, up to 16 states
-constexpr int64_t kMinBlocks = 512;   // ... where that leaves the GPU enough workgroups
 
 struct CachedParams {
   uint8_t* codes; uint8_t* scales;
@@ -47,6 +45,13 @@ __device__ __forceinline__ float uniform_value(const T* p, int i) {
   }
 }
 
+// A value in a branch that is hardly ever taken: keeps the branch from being
+// computed on every path (56 vector instructions of 327 a wavefront).
+__device__ __forceinline__ float rarely(float v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
 // CH: 16-state chunks of a channel.  WIDTH: states of an access to the codes:
 // 16 (N = 16 CH), 4 (N and every row a multiple of 4) or 1.  With 16 and 4 a
 // wavefront is in one B/C group, whose rows come in 32-bit words.  SEEDED:
@@ -60,7 +65,7 @@ struct Channel {
   // whether the channel has states from n on (uniform; always with whole chunks)
   __device__ static __forceinline__ bool has(const CachedParams& p, int n) { return WIDTH == 16 || n < p.N; }
 
-  // the channel's row of A, times log2(e)
+  // the channel's row of A
   __device__ static __forceinline__ void load_a(const CachedParams& p, int64_t d, float (&a)[NS]) {
 #pragma unroll
     for (int n = 0; n < NS; n += 4) {
@@ -72,8 +77,6 @@ struct Channel {
         for (int i = n; i < n + 4; ++i) a[i] = i < p.N ? p.A[d * p.Ad + i] : 0.0f;
       }
     }
-#pragma unroll
-    for (int n = 0; n < NS; ++n) a[n] *= kLog2e;
   }
 
   __device__ __forceinline__ void load(const CachedParams& p, int64_t slot, int64_t d) {
@@ -123,6 +126,8 @@ struct Channel {
   }
 
   // One step of row b (B/C group g) on the state in q, e; returns sum_n C s'.
+  // (B and C are read here and not ahead of the slot: the scalar registers for
+  // that cost more than the wait, 20.9 us against 19.3.)
   __device__ __forceinline__ float step(const CachedParams& p, int b, int64_t g, int64_t d, const float (&a)[NS], float dl,
                                         float x, uint64_t seed) {
     const T* const Bp = static_cast<const T*>(p.B) + b * p.Bb + g * p.Bg;
@@ -132,7 +137,7 @@ struct Channel {
       else return n < p.N ? io<T>::load(v + n) : 0.0f;
     };
     float h[NS];
-    const float dlx = dl * x;
+    const float dlx = dl * x, dl2 = dl * kLog2e;
     float y = 0.0f;
 #pragma unroll
     for (int k = 0; k < 4 * CH; ++k) {
@@ -145,7 +150,7 @@ struct Channel {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int n = 4 * k + i;
-        h[n] = fmaf(__builtin_amdgcn_exp2f(dl * a[n]), s[i], dlx * bc(Bp, n));
+        h[n] = fmaf(__builtin_amdgcn_exp2f(dl2 * a[n]), s[i], dlx * bc(Bp, n));
         y = fmaf(bc(Cp, n), h[n], y);
       }
     }
@@ -161,7 +166,7 @@ struct Channel {
       uint32_t bits = __float_as_uint(m);
       if (odd) {
 #pragma unroll
-        for (int n = k * kCacheBlock; n < k * kCacheBlock + kIn && n < NS; ++n) bits = max(bits, magnitude(h[n]));
+        for (int n = k * kCacheBlock; n < k * kCacheBlock + kIn && n < NS; ++n) bits = max(bits, magnitude(rarely(h[n])));
       }
       e[k] = scale_byte<SSM_CACHE_INT8>(bits);
     }
@@ -185,7 +190,7 @@ struct Channel {
         for (int i = 0; i < 16; ++i) t[i] = nearest_bits(h[16 * c + i], fine);
         if (two) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) t[i] = nearest_bits(h[16 * c + i] * inv, 256.0f);
+          for (int i = 0; i < 16; ++i) t[i] = nearest_bits(rarely(h[16 * c + i]) * inv, 256.0f);
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) t[i] += (r[i / 4] >> (8 * (i % 4))) & 0xffu;
@@ -202,7 +207,7 @@ struct Channel {
   }
 };
 
-template <typename T, int CH, int WIDTH, bool SEEDED, int ROWS>
+template <typename T, int CH, int WIDTH, bool SEEDED>
 __global__ __launch_bounds__(kThreads) void cached_update_kernel(CachedParams p) {
   const int lane = threadIdx.x & 63;
   const int64_t d0 = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
@@ -210,83 +215,60 @@ __global__ __launch_bounds__(kThreads) void cached_update_kernel(CachedParams p)
   if (wave0 >= p.dim) return;
   const bool live = d0 < p.dim;
   const int64_t d = live ? d0 : p.dim - 1;   // lanes past the channels repeat the last one, and store nothing
-  const int first = blockIdx.y * ROWS;
+  const int row = blockIdx.y;
+  using Ch = Channel<T, CH, WIDTH, SEEDED>;
   // the channel's B/C group, a scalar where the wavefront is in one
   int64_t g = 0;
   if (p.cpg != p.dim) {
-    if constexpr (Channel<T, CH, WIDTH, SEEDED>::kUniform)
+    if constexpr (Ch::kUniform)
       g = __builtin_amdgcn_readfirstlane(static_cast<int>(static_cast<uint32_t>(wave0) / static_cast<uint32_t>(p.cpg)));
     else g = static_cast<uint32_t>(d) / static_cast<uint32_t>(p.cpg);
   }
 
-  using Ch = Channel<T, CH, WIDTH, SEEDED>;
-  Ch ch[ROWS];
-  float a[Ch::NS], xv[ROWS], dtv[ROWS], zv[ROWS];
-  int slot[ROWS];
+  Ch ch;
+  float a[Ch::NS], xv, dtv, zv;
+  int slot = p.slots ? p.slots[row] : row;
+  if (slot < 0 || slot >= p.nslots) slot = -1;
   const uint64_t seed = SEEDED ? static_cast<uint64_t>(*p.seed) : 0;
-  auto inputs = [&](int b, float& x, float& dt, float& z) {
-    x = io<T>::load(static_cast<const T*>(p.x) + b * p.xb + d);
-    dt = io<T>::load(static_cast<const T*>(p.dt) + b * p.dtb + d);
-    z = p.z ? io<T>::load(static_cast<const T*>(p.z) + b * p.zb + d) : 0.0f;
+  auto inputs = [&](int b) {
+    xv = io<T>::load(static_cast<const T*>(p.x) + b * p.xb + d);
+    dtv = io<T>::load(static_cast<const T*>(p.dt) + b * p.dtb + d);
+    zv = p.z ? io<T>::load(static_cast<const T*>(p.z) + b * p.zb + d) : 0.0f;
   };
-  // every row's codes and inputs are on their way before the first is used
-#pragma unroll
-  for (int r = 0; r < ROWS; ++r) {
-    const int b = min(first + r, p.batch - 1);
-    slot[r] = p.slots ? p.slots[b] : b;
-    if (slot[r] < 0 || slot[r] >= p.nslots) slot[r] = -1;
-  }
-#pragma unroll
-  for (int r = 0; r < ROWS; ++r) {
-    if (slot[r] >= 0) ch[r].load(p, slot[r], d);
-    inputs(min(first + r, p.batch - 1), xv[r], dtv[r], zv[r]);
-  }
+  // what does not wait for the slot goes first
+  inputs(row);
   Ch::load_a(p, d, a);
   const float bias = p.bias ? p.bias[d] : 0.0f, Dd = p.D ? p.D[d] : 0.0f;
+  T* const out = static_cast<T*>(p.out) + d;
+  if (slot >= 0) ch.load(p, slot, d);
   // the first row of a slot takes every row of it, in order
-  uint32_t before = 0;
-  int next[ROWS];
-  slot_order<ROWS>(p.slots, first, p.batch, slot, lane, before, next);
-
-#pragma unroll
-  for (int r = 0; r < ROWS; ++r) {
-    int b = first + r;
-    if (b >= p.batch) break;
-    T* const out = static_cast<T*>(p.out) + d;
-    if (slot[r] < 0) {
-      if (live) io<T>::store(out + b * p.ob, 0.0f);
-      continue;
-    }
-    if (before >> r & 1) continue;
-    for (;;) {
-      float dl = dtv[r] + bias;
-      if (p.softplus) dl = softplus_f32(dl);
-      float y = fmaf(Dd, xv[r], ch[r].step(p, b, g, d, a, dl, xv[r], seed));
-      if (p.z) y *= silu_f32(zv[r]);
-      if (live) io<T>::store(out + b * p.ob, y);
-      b = b == first + r ? next[r] : named_next(p.slots, b, p.batch, slot[r], lane);
-      if (b >= p.batch) break;
-      inputs(b, xv[r], dtv[r], zv[r]);
-    }
-    if (live) ch[r].store(p, slot[r], d);
+  bool before;
+  int next;
+  slot_order(p.slots, row, p.batch, slot, lane, before, next);
+  if (slot < 0) {   // a padding row
+    if (live) io<T>::store(out + row * p.ob, 0.0f);
+    return;
   }
+  if (before) return;
+
+  for (int b = row;;) {
+    float dl = dtv + bias;
+    if (p.softplus) dl = softplus_f32(dl);
+    float y = fmaf(Dd, xv, ch.step(p, b, g, d, a, dl, xv, seed));
+    if (p.z) y *= silu_f32(zv);
+    if (live) io<T>::store(out + b * p.ob, y);
+    b = b == row ? next : named_next(p.slots, b, p.batch, slot, lane);
+    if (b >= p.batch) break;
+    inputs(b);
+  }
+  if (live) ch.store(p, slot, d);
 }
 
 template <typename T, int CH, int WIDTH>
 void launch_w(const CachedParams& p, hipStream_t stream) {
-  const unsigned xb = static_cast<unsigned>((p.dim + kThreads - 1) / kThreads);
-  if constexpr (CH == 1) {
-    const int64_t rows = (p.batch + kRows - 1) / kRows;
-    if (xb * rows >= kMinBlocks) {
-      const dim3 grid(xb, static_cast<unsigned>(rows));
-      if (p.seed) cached_update_kernel<T, CH, WIDTH, true, kRows><<<grid, kThreads, 0, stream>>>(p);
-      else cached_update_kernel<T, CH, WIDTH, false, kRows><<<grid, kThreads, 0, stream>>>(p);
-      return;
-    }
-  }
-  const dim3 grid(xb, static_cast<unsigned>(p.batch));
-  if (p.seed) cached_update_kernel<T, CH, WIDTH, true, 1><<<grid, kThreads, 0, stream>>>(p);
-  else cached_update_kernel<T, CH, WIDTH, false, 1><<<grid, kThreads, 0, stream>>>(p);
+  const dim3 grid(static_cast<unsigned>((p.dim + kThreads - 1) / kThreads), static_cast<unsigned>(p.batch));
+  if (p.seed) cached_update_kernel<T, CH, WIDTH, true><<<grid, kThreads, 0, stream>>>(p);
+  else cached_update_kernel<T, CH, WIDTH, false><<<grid, kThreads, 0, stream>>>(p);
 }
 
 template <typename T, int CH>

@@ -200,25 +200,25 @@ __global__ __launch_bounds__(kThreads) void gated_step_kernel(StepParams p) {
   const bool live = d0 < p.D;
   const int64_t d = live ? d0 : p.D - V;   // lanes past the channels repeat the last ones, and store nothing
   const int row = blockIdx.y;
-  int slot[1] = {p.slots ? p.slots[row] : row};
-  if (slot[0] < 0 || slot[0] >= p.nslots) slot[0] = -1;
+  int slot = p.slots ? p.slots[row] : row;
+  if (slot < 0 || slot >= p.nslots) slot = -1;
   auto at = [&](const void* q, int64_t stride, int64_t b) {
     return *reinterpret_cast<const Vec*>(static_cast<const T*>(q) + b * stride + d);
   };
   Vec x = at(p.x, p.xb, row), ga = at(p.ga, p.gab, row), gx = at(p.gx, p.gxb, row);
   State h{};
-  if (slot[0] >= 0) h = *reinterpret_cast<const State*>(p.state + slot[0] * p.ss + d);
+  if (slot >= 0) h = *reinterpret_cast<const State*>(p.state + slot * p.ss + d);
   Rate s[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) s[v] = Rate(p.c, p.lam[d + v]);
-  uint32_t before;
-  int next[1];
-  slot_order<1>(p.slots, row, p.batch, slot, lane, before, next);
-  if (before && slot[0] >= 0) return;
+  bool before;
+  int next;
+  slot_order(p.slots, row, p.batch, slot, lane, before, next);
+  if (before && slot >= 0) return;
 
   for (int b = row;;) {
     Vec o{};
-    if (slot[0] >= 0) {
+    if (slot >= 0) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const float sa = sigmoid_f32(io<T>::load(&ga.v[v])), g = sigmoid_f32(io<T>::load(&gx.v[v]));
@@ -228,14 +228,14 @@ __global__ __launch_bounds__(kThreads) void gated_step_kernel(StepParams p) {
       }
     }
     if (live) *reinterpret_cast<Vec*>(static_cast<T*>(p.out) + b * p.ob + d) = o;
-    if (slot[0] < 0) return;
-    b = b == row ? next[0] : named_next(p.slots, b, p.batch, slot[0], lane);
+    if (slot < 0) return;
+    b = b == row ? next : named_next(p.slots, b, p.batch, slot, lane);
     if (b >= p.batch) break;
     x = at(p.x, p.xb, b);
     ga = at(p.ga, p.gab, b);
     gx = at(p.gx, p.gxb, b);
   }
-  if (live) *reinterpret_cast<State*>(p.state + slot[0] * p.ss + d) = h;
+  if (live) *reinterpret_cast<State*>(p.state + slot * p.ss + d) = h;
 }
 
 template <typename T>

@@ -9,16 +9,12 @@ namespace ssm {
 
 constexpr int kNames = 4;   // slots a lane compares at a time
 
-// For rows first .. first + ROWS - 1 with slots slot[]: bit r of `before` says
-// whether an earlier row names slot[r]; next[r] is the next row that does, or
-// batch.  Rows with slot -1 are of no account.  Without slots every row has its
-// own.
-template <int ROWS>
-__device__ __forceinline__ void slot_order(const int32_t* slots, int first, int batch, const int (&slot)[ROWS], int lane,
-                                           uint32_t& before, int (&next)[ROWS]) {
-  before = 0;
-#pragma unroll
-  for (int r = 0; r < ROWS; ++r) next[r] = batch;
+// Whether an earlier row than `row` names its slot, and the next row that does,
+// or batch.  Without slots every row has its own.
+__device__ __forceinline__ void slot_order(const int32_t* slots, int row, int batch, int slot, int lane, bool& before,
+                                           int& next) {
+  before = false;
+  next = batch;
   if (!slots) return;
   // hardly ever does any: look for that first
   bool shared = false;
@@ -27,24 +23,18 @@ __device__ __forceinline__ void slot_order(const int32_t* slots, int first, int 
 #pragma unroll
     for (int k = 0; k < kNames; ++k) {
       const int i = base + 64 * k + lane;
-      named[k] = i < batch ? slots[i] : -2;
+      named[k] = i < batch && i != row ? slots[i] : -1;
     }
 #pragma unroll
-    for (int k = 0; k < kNames; ++k)
-#pragma unroll
-      for (int r = 0; r < ROWS; ++r) shared |= named[k] == slot[r] && base + 64 * k + lane != first + r;
+    for (int k = 0; k < kNames; ++k) shared |= named[k] == slot;
   }
   if (!__any(shared)) return;
   for (int base = 0; base < batch; base += 64) {
     const int i = base + lane;
-    const int named = i < batch ? slots[i] : -2;
-#pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      const bool hit = named == slot[r];
-      if (__any(hit && i < first + r)) before |= 1u << r;
-      const uint64_t later = __ballot(hit && i > first + r);
-      if (later && next[r] == batch) next[r] = base + __builtin_ctzll(later);
-    }
+    const bool hit = i < batch && slots[i] == slot;
+    if (__any(hit && i < row)) before = true;
+    const uint64_t later = __ballot(hit && i > row);
+    if (later && next == batch) next = base + __builtin_ctzll(later);
   }
 }
 
