@@ -21,11 +21,12 @@ struct FwdParams {
   int64_t xb, xs, gab, gas, gxb, gxs, ob, os;
   int64_t L, D, nck;
   uint32_t batch, tiles, cols;
+  int shift;   // narrow calls: log2 of the channels
   float c;
   int zero_outside;
 };
 
-template <typename T, int V, bool PACKED, bool CHAIN>
+template <typename T, int V, bool PACKED, bool CHAIN, bool NARROW>
 __global__ __launch_bounds__(64 * kMaxWaves) void gated_fwd_kernel(FwdParams p) {
   constexpr int W = 64 * V;
   __shared__ float2 pairs[kMaxWaves][W];
@@ -43,13 +44,24 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_fwd_kernel(FwdParams p) 
   }
   // along the channels first, then the batch: neighbours read neighbouring bytes
   const uint32_t col = id % p.cols, row = id / p.cols % p.batch, tile = id / p.cols / p.batch;
-  const int64_t b = row, t0 = (static_cast<int64_t>(tile) * waves + wave) * kWaveTokens;
-  const int n = static_cast<int>(min(static_cast<int64_t>(kWaveTokens), max(int64_t{0}, p.L - t0)));
+  // A wavefront has 16 tokens of 64 V channels; in a narrow call each stretch of
+  // 2^shift lanes has 16 tokens of its own.
   constexpr int kBytes = V * sizeof(T);
-  const int64_t ch = static_cast<int64_t>(col) * W + lane * V;
+  const int shift = NARROW ? p.shift : V == 2 ? 7 : 6;
+  const int width = 1 << shift, subs = NARROW ? 64 >> shift : 1;
+  const int sub = NARROW ? lane >> shift : 0, c = NARROW ? lane & (width - 1) : lane;
+  const int64_t b = row, wave_t0 = (static_cast<int64_t>(tile) * waves + wave) * (kWaveTokens * subs);
+  const int64_t t0 = wave_t0 + sub * kWaveTokens;
+  const int n = static_cast<int>(min(static_cast<int64_t>(kWaveTokens), max(int64_t{0}, p.L - t0)));
+  const bool some = NARROW ? wave_t0 < p.L : n > 0;   // of the wavefront
+  const int64_t ch = static_cast<int64_t>(col) * W + c * V;
   const bool live = ch < p.D;
   const int64_t d = live ? ch : p.D - V;   // per-channel values: lanes past the channels repeat the last ones
-  const uint32_t at = static_cast<uint32_t>(ch) * sizeof(T);
+  // a lane's offset from the wavefront's row j of a tensor
+  auto at = [&](int64_t stride) {
+    if constexpr (NARROW) return live ? static_cast<uint32_t>((c + sub * kWaveTokens * stride) * sizeof(T)) : kNowhere;
+    else return static_cast<uint32_t>(ch) * static_cast<uint32_t>(sizeof(T));
+  };
 
   Rate s[V];
   float a[kWaveTokens][V], u[kWaveTokens][V], P[V], H[V];
@@ -64,24 +76,27 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_fwd_kernel(FwdParams p) 
   // one load brings, as scalars.  (Fetching the rows before the marks that
   // decide the path are known measured slower, 314 us against 295 us for forward
   // and backward of 30,011 x 1536 bf16: the rows' uses then wait together.)
-  int32_t marks = 0;
-  if constexpr (PACKED) marks = n > 0 ? p.marks[t0 + lane % kWaveTokens] : kOutside;
-  auto mark = [&](int j) { return __builtin_amdgcn_readlane(marks, j); };
+  int32_t marks = 0, each[NARROW ? kWaveTokens : 1];
+  if constexpr (PACKED && !NARROW) marks = some ? p.marks[t0 + lane % kWaveTokens] : kOutside;
+  if constexpr (PACKED && NARROW)
+    for (int i = c; i < n; i += width) marks |= p.marks[t0 + i];   // kOutside sets every bit
+  auto mark = [&](int j) { return NARROW ? each[NARROW ? j : 0] : __builtin_amdgcn_readlane(marks, j); };
 
   // tokens to (a, b) of h = a h + b; past the end of the row (1, 0)
   auto tokens = [&](auto every) {
     constexpr bool PLAIN = decltype(every)::value;
     constexpr bool MARKED = PACKED && !PLAIN;
     uint32_t rx[kWaveTokens], ra[kWaveTokens], rg[kWaveTokens];
-    const TokenRows x = token_rows<T>(p.x, b * p.xb + t0 * p.xs, p.xs, p.D),
-                    ga = token_rows<T>(p.ga, b * p.gab + t0 * p.gas, p.gas, p.D),
-                    gx = token_rows<T>(p.gx, b * p.gxb + t0 * p.gxs, p.gxs, p.D);
+    const TokenRows x = token_rows<T>(p.x, b * p.xb + wave_t0 * p.xs, p.xs, p.D, subs),
+                    ga = token_rows<T>(p.ga, b * p.gab + wave_t0 * p.gas, p.gas, p.D, subs),
+                    gx = token_rows<T>(p.gx, b * p.gxb + wave_t0 * p.gxs, p.gxs, p.D, subs);
 #pragma unroll
     for (int j = 0; j < kWaveTokens; ++j) {
-      const int jj = PLAIN ? j : min(j, n - 1);
-      ra[j] = ga.load<kBytes>(jj, at);
-      rg[j] = gx.load<kBytes>(jj, at);
-      rx[j] = x.load<kBytes>(jj, at);
+      const int jj = PLAIN || NARROW ? j : min(j, n - 1);
+      const bool in = PLAIN || !NARROW || j < n;
+      ra[j] = ga.load<kBytes>(jj, in ? at(p.gas) : kNowhere);
+      rg[j] = gx.load<kBytes>(jj, in ? at(p.gxs) : kNowhere);
+      rx[j] = x.load<kBytes>(jj, in ? at(p.xs) : kNowhere);
     }
 #pragma unroll
     for (int j = 0; j < kWaveTokens; ++j) {
@@ -108,18 +123,34 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_fwd_kernel(FwdParams p) 
       }
     }
   };
-  const bool plain = n == kWaveTokens && (!PACKED || __ballot(marks < 0 || (marks & 3)) == 0);
+  bool plain;
+  if constexpr (NARROW) plain = __all(n == kWaveTokens) && !__any(marks < 0 || (marks & 3));
+  else plain = n == kWaveTokens && (!PACKED || __ballot(marks < 0 || (marks & 3)) == 0);
   if (plain) tokens(std::true_type{});
-  if (!plain && n > 0) tokens(std::false_type{});
+  if (!plain && some) {
+    if constexpr (PACKED && NARROW) {
+#pragma unroll
+      for (int j = 0; j < kWaveTokens; ++j) each[j] = j < n ? p.marks[t0 + j] : kOutside;
+      marks = 0;   // of the lane's own stretch now
+#pragma unroll
+      for (int j = 0; j < kWaveTokens; ++j) marks |= j < n ? each[j] : 0;
+    }
+    tokens(std::false_type{});
+  }
   if constexpr (PACKED) {
-    if (n > 0 && __ballot(marks & 1)) {
+    if (NARROW ? !plain && (marks & 1) : some && __ballot(marks & 1)) {
 #pragma unroll
       for (int v = 0; v < V; ++v) P[v] = kCut;
     }
   }
 
+  if constexpr (NARROW) {
+    const float2 all = wave_stretches<PACKED, false>(shift, P[0], H[0]);
+    if (sub == subs - 1) pairs[wave][c] = all;
+  } else {
 #pragma unroll
-  for (int v = 0; v < V; ++v) pairs[wave][lane * V + v] = make_float2(P[v], H[v]);
+    for (int v = 0; v < V; ++v) pairs[wave][lane * V + v] = make_float2(P[v], H[v]);
+  }
   __syncthreads();
   float h[V];
 #pragma unroll
@@ -127,40 +158,41 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_fwd_kernel(FwdParams p) 
   if constexpr (CHAIN) {
     // the words of (row, col): tiles, then groups
     const int64_t ngroups = (p.tiles + kChainGroup - 1) / kChainGroup;
-    uint64_t* const base = p.words + (static_cast<int64_t>(row) * p.cols + col) * (p.tiles + ngroups) * W;
-    const Chain chain{base, base + static_cast<int64_t>(p.tiles) * W, W};
-    chain_gather<PACKED, W>(chain, tile, pairs, before, [](int w) { return w; });
+    uint64_t* const base = p.words + (static_cast<int64_t>(row) * p.cols + col) * (p.tiles + ngroups) * width;
+    const Chain chain{base, base + static_cast<int64_t>(p.tiles) * width, width};
+    chain_gather<PACKED, W, NARROW ? 1 : 2 * V>(chain, tile, pairs, before, shift, [](int w) { return w; });
     __syncthreads();
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      h[v] = chain_entering<PACKED, W>(tile, lane * V + v, before, h[v]);
-      if (wave == 0 && chain_hands_on(tile, p.tiles)) {
+      h[v] = chain_entering<PACKED, W>(tile, c * V + v, before, h[v]);
+      if (wave == 0 && sub == 0 && chain_hands_on(tile, p.tiles)) {
         float out = h[v];
 #pragma unroll
-        for (int w = 0; w < kMaxWaves; ++w) out = chain_apply<PACKED>(pairs[w][lane * V + v].x, pairs[w][lane * V + v].y, out);
-        chain_leave(chain, tile, lane * V + v, out);
+        for (int w = 0; w < kMaxWaves; ++w) out = chain_apply<PACKED>(pairs[w][c * V + v].x, pairs[w][c * V + v].y, out);
+        chain_leave(chain, tile, c * V + v, out);
       }
     }
   }
-  if (n <= 0) return;
+  if (!some) return;
   for (int w = 0; w < wave; ++w)
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const float2 q = pairs[w][lane * V + v];
+      const float2 q = pairs[w][c * V + v];
       h[v] = chain_apply<PACKED>(q.x, q.y, h[v]);
     }
-  if (p.ck && live) {
+  if constexpr (NARROW) h[0] = chain_apply<PACKED>(P[0], H[0], h[0]);   // the stretches before this one
+  if (p.ck && live && (!NARROW || n > 0)) {
     float* const ck = p.ck + (b * p.nck + t0 / kCkpt) * p.D + d;
 #pragma unroll
     for (int v = 0; v < V; ++v) ck[v] = h[v];
   }
-  const TokenRows out = token_rows<T>(p.out, b * p.ob + t0 * p.os, p.os, p.D);
+  const TokenRows out = token_rows<T>(p.out, b * p.ob + wave_t0 * p.os, p.os, p.D, subs);
   auto outputs = [&](auto every) {
     constexpr bool PLAIN = decltype(every)::value;
     constexpr bool MARKED = PACKED && !PLAIN;
 #pragma unroll
     for (int j = 0; j < kWaveTokens; ++j) {
-      if (!PLAIN && j >= n) continue;
+      if (!PLAIN && !NARROW && j >= n) continue;
 #pragma unroll
       for (int v = 0; v < V; ++v) h[v] = MARKED && (mark(j) & 1) ? u[j][v] : fmaf(a[j][v], h[v], u[j][v]);
       if constexpr (MARKED) {
@@ -169,13 +201,14 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_fwd_kernel(FwdParams p) 
           for (int v = 0; v < V; ++v) p.last[static_cast<int64_t>(mark(j) >> 2) * p.D + d + v] = h[v];
         }
       }
-      if (!MARKED || mark(j) >= 0 || p.zero_outside) out.store<kBytes>(j, at, narrow<T, V>(h));
+      const bool write = (!MARKED || mark(j) >= 0 || p.zero_outside) && (PLAIN || !NARROW || j < n);
+      if (NARROW || write) out.store<kBytes>(j, write ? at(p.os) : kNowhere, narrow<T, V>(h));
     }
   };
   if (plain) outputs(std::true_type{});
   else outputs(std::false_type{});
   if constexpr (!PACKED) {
-    if (p.last && live && t0 + n == p.L) {
+    if (p.last && live && n > 0 && t0 + n == p.L) {
 #pragma unroll
       for (int v = 0; v < V; ++v) p.last[b * p.D + d + v] = h[v];
     }
@@ -272,33 +305,42 @@ int channels_per_lane(const ssm_gated_args& a) {
              ? 2 : 1;
 }
 
-GatedPlan plan(const ssm_gated_args& a, int V) {
-  return gated_plan(a.batch, a.seqlen, a.dim, a.cu_seqlens != nullptr, V, 0);
+GatedPlan plan(const ssm_gated_args& a, int V, int shift) {
+  return gated_plan(a.batch, a.seqlen, a.dim, a.cu_seqlens != nullptr, V, shift, 0);
 }
 
-template <typename T, int V>
+int shift_of(const ssm_gated_args& a) {
+  const int64_t esz = a.io_dtype == SSM_BF16 ? 2 : 4;
+  for (int64_t stride : {a.x_seq_stride, a.gate_a_seq_stride, a.gate_x_seq_stride, a.out_seq_stride})
+    if (!narrow_fits(a.dim, stride, esz)) return 0;
+  return narrow_shift(a.dim);
+}
+
+template <typename T, int V, bool NARROW>
 void launch_fwd(const FwdParams& p, const GatedPlan& q, bool packed, hipStream_t stream) {
   const dim3 grid(static_cast<unsigned>(q.tiles * q.cols * p.batch)), block(64 * q.waves);
   if (packed) {
-    if (q.words) gated_fwd_kernel<T, V, true, true><<<grid, block, 0, stream>>>(p);
-    else gated_fwd_kernel<T, V, true, false><<<grid, block, 0, stream>>>(p);
+    if (q.words) gated_fwd_kernel<T, V, true, true, NARROW><<<grid, block, 0, stream>>>(p);
+    else gated_fwd_kernel<T, V, true, false, NARROW><<<grid, block, 0, stream>>>(p);
   } else {
-    if (q.words) gated_fwd_kernel<T, V, false, true><<<grid, block, 0, stream>>>(p);
-    else gated_fwd_kernel<T, V, false, false><<<grid, block, 0, stream>>>(p);
+    if (q.words) gated_fwd_kernel<T, V, false, true, NARROW><<<grid, block, 0, stream>>>(p);
+    else gated_fwd_kernel<T, V, false, false, NARROW><<<grid, block, 0, stream>>>(p);
   }
 }
 
 }  // namespace
 
-// The size for either number of channels a lane: it depends on no address.
+// The size for whichever form runs: it depends on no address.
 size_t gated_workspace_bytes(const ssm_gated_args& a) {
-  const int64_t one = plan(a, 1).bytes, two = plan(a, 2).bytes;
+  const int shift = shift_of(a);
+  const int64_t one = plan(a, 1, shift).bytes, two = shift ? 0 : plan(a, 2, 0).bytes;
   return static_cast<size_t>(one > two ? one : two);
 }
 
 hipError_t launch_gated_fwd(const ssm_gated_args& a, hipStream_t stream) {
-  const int V = channels_per_lane(a);
-  const GatedPlan q = plan(a, V);
+  const int shift = shift_of(a);
+  const int V = shift ? 1 : channels_per_lane(a);
+  const GatedPlan q = plan(a, V, shift);
   char* const ws = static_cast<char*>(a.workspace);
   const bool packed = a.cu_seqlens != nullptr;
   const int64_t nseq = packed ? a.nseq : a.batch;
@@ -316,12 +358,14 @@ hipError_t launch_gated_fwd(const ssm_gated_args& a, hipStream_t stream) {
                     a.x_batch_stride, a.x_seq_stride, a.gate_a_batch_stride, a.gate_a_seq_stride,
                     a.gate_x_batch_stride, a.gate_x_seq_stride, a.out_batch_stride, a.out_seq_stride,
                     a.seqlen, a.dim, (a.seqlen + kCkpt - 1) / kCkpt, static_cast<uint32_t>(a.batch),
-                    static_cast<uint32_t>(q.tiles), static_cast<uint32_t>(q.cols), a.c, a.zero_outside};
+                    static_cast<uint32_t>(q.tiles), static_cast<uint32_t>(q.cols), q.shift, a.c, a.zero_outside};
   if (a.io_dtype == SSM_BF16) {
-    if (V == 2) launch_fwd<uint16_t, 2>(p, q, packed, stream);
-    else launch_fwd<uint16_t, 1>(p, q, packed, stream);
+    if (shift) launch_fwd<uint16_t, 1, true>(p, q, packed, stream);
+    else if (V == 2) launch_fwd<uint16_t, 2, false>(p, q, packed, stream);
+    else launch_fwd<uint16_t, 1, false>(p, q, packed, stream);
   } else {
-    launch_fwd<float, 1>(p, q, packed, stream);
+    if (shift) launch_fwd<float, 1, true>(p, q, packed, stream);
+    else launch_fwd<float, 1, false>(p, q, packed, stream);
   }
   return hipGetLastError();
 }

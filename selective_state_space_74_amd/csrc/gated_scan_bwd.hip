@@ -24,6 +24,7 @@ struct BwdParams {
   int64_t xb, xs, gab, gas, gxb, gxs, dob, dos, dxb, dxs, dgab, dgas, dgxb, dgxs;
   int64_t L, D, nck;
   uint32_t batch, tiles, cols;
+  int shift;   // narrow calls: log2 of the channels
   float c;
 };
 
@@ -31,7 +32,7 @@ struct BwdParams {
 // The states before each token come forward from the wavefront's checkpoint,
 // so the three gradients' factors of e are ready before e is known; only
 // e_t = dout_t + a_{t+1} e_{t+1} waits for the tiles behind.
-template <typename T, int V, bool PACKED, bool CHAIN>
+template <typename T, int V, bool PACKED, bool CHAIN, bool NARROW>
 __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams p) {
   constexpr int W = 64 * V;
   __shared__ float2 pairs[kMaxWaves][W];
@@ -49,15 +50,25 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams 
   }
   const uint32_t col = id % p.cols, row = id / p.cols % p.batch, k = id / p.cols / p.batch;
   const uint32_t tile = p.tiles - 1 - k;
-  const int64_t b = row, t0 = (static_cast<int64_t>(tile) * waves + wave) * kWaveTokens;
+  // A wavefront has 16 tokens of 64 V channels; in a narrow call each stretch of
+  // 2^shift lanes has 16 tokens of its own.
+  constexpr int kBytes = V * sizeof(T);
+  const int shift = NARROW ? p.shift : V == 2 ? 7 : 6;
+  const int width = 1 << shift, subs = NARROW ? 64 >> shift : 1;
+  const int sub = NARROW ? lane >> shift : 0, c = NARROW ? lane & (width - 1) : lane;
+  const int64_t b = row, wave_t0 = (static_cast<int64_t>(tile) * waves + wave) * (kWaveTokens * subs);
+  const int64_t t0 = wave_t0 + sub * kWaveTokens;
   const int n = static_cast<int>(min(static_cast<int64_t>(kWaveTokens), max(int64_t{0}, p.L - t0)));
-  const int64_t col_at = static_cast<int64_t>(col) * W, ch = col_at + lane * V;
+  const bool some = NARROW ? wave_t0 < p.L : n > 0;   // of the wavefront
+  const int64_t ch = static_cast<int64_t>(col) * W + c * V;
   const bool live = ch < p.D;
   const int64_t d = live ? ch : p.D - V;   // per-channel values: lanes past the channels repeat the last ones
-  constexpr int kBytes = V * sizeof(T);
-  const uint32_t at = static_cast<uint32_t>(ch) * sizeof(T);
+  // a lane's offset from the wavefront's row j of a tensor
+  auto at = [&](int64_t stride) {
+    if constexpr (NARROW) return live ? static_cast<uint32_t>((c + sub * kWaveTokens * stride) * sizeof(T)) : kNowhere;
+    else return static_cast<uint32_t>(ch) * static_cast<uint32_t>(sizeof(T));
+  };
 
-  // e's factors: dx = e fx, dgate_x = e fg, dgate_a = e fa, dlam's sum e fl
   Rate s[V];
   float a[kWaveTokens][V], fx[kWaveTokens][V], fg[kWaveTokens][V], fa[kWaveTokens][V], fl[kWaveTokens][V],
       dout[kWaveTokens][V], P[V], Q[V];
@@ -72,28 +83,31 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams 
   // one load brings, as scalars.  (Fetching the rows before the marks that
   // decide the path are known measured slower, 314 us against 295 us for forward
   // and backward of 30,011 x 1536 bf16: the rows' uses then wait together.)
-  int32_t marks = 0;
-  if constexpr (PACKED) marks = n > 0 ? p.marks[t0 + lane % kWaveTokens] : kOutside;
-  auto mark = [&](int j) { return __builtin_amdgcn_readlane(marks, j); };
+  int32_t marks = 0, each[NARROW ? kWaveTokens : 1];
+  if constexpr (PACKED && !NARROW) marks = some ? p.marks[t0 + lane % kWaveTokens] : kOutside;
+  if constexpr (PACKED && NARROW)
+    for (int i = c; i < n; i += width) marks |= p.marks[t0 + i];   // kOutside sets every bit
+  auto mark = [&](int j) { return NARROW ? each[NARROW ? j : 0] : __builtin_amdgcn_readlane(marks, j); };
 
   auto tokens = [&](auto every) {
     constexpr bool PLAIN = decltype(every)::value;
     constexpr bool MARKED = PACKED && !PLAIN;
     uint32_t rx[kWaveTokens], ra[kWaveTokens], rg[kWaveTokens], rd[kWaveTokens];
-    const TokenRows tx = token_rows<T>(p.x, b * p.xb + t0 * p.xs, p.xs, p.D),
-                    ta = token_rows<T>(p.ga, b * p.gab + t0 * p.gas, p.gas, p.D),
-                    tg = token_rows<T>(p.gx, b * p.gxb + t0 * p.gxs, p.gxs, p.D),
-                    td = token_rows<T>(p.dout, b * p.dob + t0 * p.dos, p.dos, p.D);
+    const TokenRows tx = token_rows<T>(p.x, b * p.xb + wave_t0 * p.xs, p.xs, p.D, subs),
+                    ta = token_rows<T>(p.ga, b * p.gab + wave_t0 * p.gas, p.gas, p.D, subs),
+                    tg = token_rows<T>(p.gx, b * p.gxb + wave_t0 * p.gxs, p.gxs, p.D, subs),
+                    td = token_rows<T>(p.dout, b * p.dob + wave_t0 * p.dos, p.dos, p.D, subs);
     float h[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = p.ck[(b * p.nck + t0 / kCkpt) * p.D + d + v];
+    for (int v = 0; v < V; ++v) h[v] = p.ck[(b * p.nck + (NARROW ? min(t0 / kCkpt, p.nck - 1) : t0 / kCkpt)) * p.D + d + v];
 #pragma unroll
     for (int j = 0; j < kWaveTokens; ++j) {
-      const int jj = PLAIN ? j : min(j, n - 1);
-      ra[j] = ta.load<kBytes>(jj, at);
-      rg[j] = tg.load<kBytes>(jj, at);
-      rx[j] = tx.load<kBytes>(jj, at);
-      rd[j] = td.load<kBytes>(jj, at);
+      const int jj = PLAIN || NARROW ? j : min(j, n - 1);
+      const bool in = PLAIN || !NARROW || j < n;
+      ra[j] = ta.load<kBytes>(jj, in ? at(p.gas) : kNowhere);
+      rg[j] = tg.load<kBytes>(jj, in ? at(p.gxs) : kNowhere);
+      rx[j] = tx.load<kBytes>(jj, in ? at(p.xs) : kNowhere);
+      rd[j] = td.load<kBytes>(jj, in ? at(p.dos) : kNowhere);
     }
 #pragma unroll
     for (int j = 0; j < kWaveTokens; ++j) {
@@ -138,18 +152,34 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams 
         Q[v] = MARKED && (mark(j) & 1) && (PLAIN || j < n) ? 0.0f : a[j][v] * (dout[j][v] + Q[v]);
       }
   };
-  const bool plain = n == kWaveTokens && (!PACKED || __ballot(marks < 0 || (marks & 3)) == 0);
+  bool plain;
+  if constexpr (NARROW) plain = __all(n == kWaveTokens) && !__any(marks < 0 || (marks & 3));
+  else plain = n == kWaveTokens && (!PACKED || __ballot(marks < 0 || (marks & 3)) == 0);
   if (plain) tokens(std::true_type{});
-  if (!plain && n > 0) tokens(std::false_type{});
+  if (!plain && some) {
+    if constexpr (PACKED && NARROW) {
+#pragma unroll
+      for (int j = 0; j < kWaveTokens; ++j) each[j] = j < n ? p.marks[t0 + j] : kOutside;
+      marks = 0;   // of the lane's own stretch now
+#pragma unroll
+      for (int j = 0; j < kWaveTokens; ++j) marks |= j < n ? each[j] : 0;
+    }
+    tokens(std::false_type{});
+  }
   if constexpr (PACKED) {
-    if (n > 0 && __ballot(marks & 1)) {
+    if (NARROW ? !plain && (marks & 1) : some && __ballot(marks & 1)) {
 #pragma unroll
       for (int v = 0; v < V; ++v) P[v] = kCut;
     }
   }
 
+  if constexpr (NARROW) {
+    const float2 all = wave_stretches<PACKED, true>(shift, P[0], Q[0]);
+    if (sub == 0) pairs[wave][c] = all;
+  } else {
 #pragma unroll
-  for (int v = 0; v < V; ++v) pairs[wave][lane * V + v] = make_float2(P[v], Q[v]);
+    for (int v = 0; v < V; ++v) pairs[wave][lane * V + v] = make_float2(P[v], Q[v]);
+  }
   __syncthreads();
   float e[V];
 #pragma unroll
@@ -157,44 +187,45 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams 
   if constexpr (CHAIN) {
     // the words of (row, col): tiles, then groups
     const int64_t ngroups = (p.tiles + kChainGroup - 1) / kChainGroup;
-    uint64_t* const base = p.words + (static_cast<int64_t>(row) * p.cols + col) * (p.tiles + ngroups) * W;
-    const Chain chain{base, base + static_cast<int64_t>(p.tiles) * W, W};
-    chain_gather<PACKED, W>(chain, k, pairs, before, [](int w) { return kMaxWaves - 1 - w; });
+    uint64_t* const base = p.words + (static_cast<int64_t>(row) * p.cols + col) * (p.tiles + ngroups) * width;
+    const Chain chain{base, base + static_cast<int64_t>(p.tiles) * width, width};
+    chain_gather<PACKED, W, NARROW ? 1 : 2 * V>(chain, k, pairs, before, shift, [](int w) { return kMaxWaves - 1 - w; });
     __syncthreads();
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      e[v] = chain_entering<PACKED, W>(k, lane * V + v, before, e[v]);
-      if (wave == 0 && chain_hands_on(k, p.tiles)) {
+      e[v] = chain_entering<PACKED, W>(k, c * V + v, before, e[v]);
+      if (wave == 0 && sub == 0 && chain_hands_on(k, p.tiles)) {
         float out = e[v];
 #pragma unroll
-        for (int w = kMaxWaves - 1; w >= 0; --w) out = chain_apply<PACKED>(pairs[w][lane * V + v].x, pairs[w][lane * V + v].y, out);
-        chain_leave(chain, k, lane * V + v, out);
+        for (int w = kMaxWaves - 1; w >= 0; --w) out = chain_apply<PACKED>(pairs[w][c * V + v].x, pairs[w][c * V + v].y, out);
+        chain_leave(chain, k, c * V + v, out);
       }
     }
   }
   float acc[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) acc[v] = 0.0f;
-  if (n > 0) {
+  if (some) {
     for (int w = waves - 1; w > wave; --w)
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float2 q = pairs[w][lane * V + v];
+        const float2 q = pairs[w][c * V + v];
         e[v] = chain_apply<PACKED>(q.x, q.y, e[v]);
       }
-    const TokenRows dx = token_rows<T>(p.dx, b * p.dxb + t0 * p.dxs, p.dxs, p.D),
-                    dga = token_rows<T>(p.dga, b * p.dgab + t0 * p.dgas, p.dgas, p.D),
-                    dgx = token_rows<T>(p.dgx, b * p.dgxb + t0 * p.dgxs, p.dgxs, p.D);
+    if constexpr (NARROW) e[0] = chain_apply<PACKED>(P[0], Q[0], e[0]);   // the stretches behind this one
+    const TokenRows dx = token_rows<T>(p.dx, b * p.dxb + wave_t0 * p.dxs, p.dxs, p.D, subs),
+                    dga = token_rows<T>(p.dga, b * p.dgab + wave_t0 * p.dgas, p.dgas, p.D, subs),
+                    dgx = token_rows<T>(p.dgx, b * p.dgxb + wave_t0 * p.dgxs, p.dgxs, p.D, subs);
     auto outputs = [&](auto every) {
       constexpr bool PLAIN = decltype(every)::value;
       constexpr bool MARKED = PACKED && !PLAIN;
 #pragma unroll
       for (int j = kWaveTokens - 1; j >= 0; --j) {
-        if (!PLAIN && j >= n) continue;
+        if (!PLAIN && !NARROW && j >= n) continue;
         float ox[V], oa[V], og[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          const bool in = !MARKED || mark(j) >= 0;
+          const bool in = (!MARKED || mark(j) >= 0) && (PLAIN || !NARROW || j < n);
           const float et = dout[j][v] + e[v];
           ox[v] = in ? et * fx[j][v] : 0.0f;
           og[v] = in ? et * fg[j][v] : 0.0f;
@@ -208,15 +239,16 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams 
             }
           }
         }
-        dx.store<kBytes>(j, at, narrow<T, V>(ox));
-        dga.store<kBytes>(j, at, narrow<T, V>(oa));
-        dgx.store<kBytes>(j, at, narrow<T, V>(og));
+        const bool write = PLAIN || !NARROW || j < n;
+        dx.store<kBytes>(j, write ? at(p.dxs) : kNowhere, narrow<T, V>(ox));
+        dga.store<kBytes>(j, write ? at(p.dgas) : kNowhere, narrow<T, V>(oa));
+        dgx.store<kBytes>(j, write ? at(p.dgxs) : kNowhere, narrow<T, V>(og));
       }
     };
     if (plain) outputs(std::true_type{});
     else outputs(std::false_type{});
     if constexpr (!PACKED) {
-      if (p.dh0 && live && t0 == 0) {
+      if (p.dh0 && live && t0 == 0 && n > 0) {
 #pragma unroll
         for (int v = 0; v < V; ++v) p.dh0[b * p.D + d + v] = e[v];
       }
@@ -224,13 +256,19 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams 
   }
   // the tile's part of dlam, wavefront by wavefront
   __syncthreads();
+  if constexpr (NARROW) {
+    for (int k = 32; k >= width; k >>= 1) acc[0] += __shfl_down(acc[0], k);
+    if (sub == 0) pairs[wave][c].x = acc[0];
+  } else {
 #pragma unroll
-  for (int v = 0; v < V; ++v) pairs[wave][lane * V + v].x = acc[v];
+    for (int v = 0; v < V; ++v) pairs[wave][lane * V + v].x = acc[v];
+  }
   __syncthreads();
-  for (int c = threadIdx.x; c < W; c += blockDim.x) {
+  for (int i = threadIdx.x; i < width; i += blockDim.x) {
     float sum = 0.0f;
-    for (int w = 0; w < waves; ++w) sum += pairs[w][c].x;
-    if (col_at + c < p.D) p.part[(static_cast<int64_t>(row) * p.tiles + tile) * p.D + col_at + c] = sum;
+    for (int w = 0; w < waves; ++w) sum += pairs[w][i].x;
+    const int64_t di = static_cast<int64_t>(col) * W + i;
+    if (di < p.D) p.part[(static_cast<int64_t>(row) * p.tiles + tile) * p.D + di] = sum;
   }
 }
 
@@ -256,29 +294,38 @@ __global__ __launch_bounds__(kSumCols * kSumRows) void gated_dlam_kernel(const f
   }
 }
 
-GatedPlan plan(const ssm_gated_bwd_args& a, int V) {
-  return gated_plan(a.batch, a.seqlen, a.dim, a.cu_seqlens != nullptr, V, 1);
+constexpr int kV = 1;   // channels a lane
+
+int shift_of(const ssm_gated_bwd_args& a) {
+  const int64_t esz = a.io_dtype == SSM_BF16 ? 2 : 4;
+  for (int64_t stride : {a.x_seq_stride, a.gate_a_seq_stride, a.gate_x_seq_stride, a.dout_seq_stride, a.dx_seq_stride,
+                         a.dgate_a_seq_stride, a.dgate_x_seq_stride})
+    if (!narrow_fits(a.dim, stride, esz)) return 0;
+  return narrow_shift(a.dim);
 }
 
-template <typename T, int V>
+GatedPlan plan(const ssm_gated_bwd_args& a) {
+  return gated_plan(a.batch, a.seqlen, a.dim, a.cu_seqlens != nullptr, kV, shift_of(a), 1);
+}
+
+template <typename T, bool NARROW>
 void launch_bwd(const BwdParams& p, const GatedPlan& q, bool packed, hipStream_t stream) {
   const dim3 grid(static_cast<unsigned>(q.tiles * q.cols * p.batch)), block(64 * q.waves);
   if (packed) {
-    if (q.words) gated_bwd_kernel<T, V, true, true><<<grid, block, 0, stream>>>(p);
-    else gated_bwd_kernel<T, V, true, false><<<grid, block, 0, stream>>>(p);
+    if (q.words) gated_bwd_kernel<T, kV, true, true, NARROW><<<grid, block, 0, stream>>>(p);
+    else gated_bwd_kernel<T, kV, true, false, NARROW><<<grid, block, 0, stream>>>(p);
   } else {
-    if (q.words) gated_bwd_kernel<T, V, false, true><<<grid, block, 0, stream>>>(p);
-    else gated_bwd_kernel<T, V, false, false><<<grid, block, 0, stream>>>(p);
+    if (q.words) gated_bwd_kernel<T, kV, false, true, NARROW><<<grid, block, 0, stream>>>(p);
+    else gated_bwd_kernel<T, kV, false, false, NARROW><<<grid, block, 0, stream>>>(p);
   }
 }
 
 }  // namespace
 
-size_t gated_bwd_workspace_bytes(const ssm_gated_bwd_args& a) { return static_cast<size_t>(plan(a, 1).bytes); }
+size_t gated_bwd_workspace_bytes(const ssm_gated_bwd_args& a) { return static_cast<size_t>(plan(a).bytes); }
 
 hipError_t launch_gated_bwd(const ssm_gated_bwd_args& a, hipStream_t stream) {
-  constexpr int V = 1;
-  const GatedPlan q = plan(a, V);
+  const GatedPlan q = plan(a);
   char* const ws = static_cast<char*>(a.workspace);
   const bool packed = a.cu_seqlens != nullptr;
   const int64_t nseq = packed ? a.nseq : a.batch;
@@ -298,11 +345,12 @@ hipError_t launch_gated_bwd(const ssm_gated_bwd_args& a, hipStream_t stream) {
                     a.dx_batch_stride, a.dx_seq_stride, a.dgate_a_batch_stride, a.dgate_a_seq_stride,
                     a.dgate_x_batch_stride, a.dgate_x_seq_stride,
                     a.seqlen, a.dim, (a.seqlen + kCkpt - 1) / kCkpt, static_cast<uint32_t>(a.batch),
-                    static_cast<uint32_t>(q.tiles), static_cast<uint32_t>(q.cols), a.c};
+                    static_cast<uint32_t>(q.tiles), static_cast<uint32_t>(q.cols), q.shift, a.c};
   const int64_t rows = q.tiles * a.batch;
   if (rows > 0) {
-    if (a.io_dtype == SSM_BF16) launch_bwd<uint16_t, V>(p, q, packed, stream);
-    else launch_bwd<float, V>(p, q, packed, stream);
+    const bool bf16 = a.io_dtype == SSM_BF16;
+    if (q.shift) bf16 ? launch_bwd<uint16_t, true>(p, q, packed, stream) : launch_bwd<float, true>(p, q, packed, stream);
+    else bf16 ? launch_bwd<uint16_t, false>(p, q, packed, stream) : launch_bwd<float, false>(p, q, packed, stream);
   }
   gated_dlam_kernel<<<static_cast<unsigned>((a.dim + kSumCols - 1) / kSumCols), kSumCols * kSumRows, 0, stream>>>(
       p.part, rows, a.dim, a.lam, a.c, a.dlam);

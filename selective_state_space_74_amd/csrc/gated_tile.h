@@ -95,11 +95,12 @@ struct ChainShared {
 // pair, then brings the predecessors' words into LDS, a few each thread, so
 // that their latencies run side by side and no wavefront holds them all in
 // registers.
-template <bool PACKED, int W, typename Order>
+template <bool PACKED, int W, int MINE, typename Order>
 __device__ __forceinline__ void chain_gather(const Chain& c, int64_t k, float2 (&pairs)[kMaxWaves][W],
-                                             ChainShared<W>& sh, Order order) {
-  constexpr int kParts = 64 * kMaxWaves / W, kMine = (kChainGroup - 2) / kParts + 1;
-  const int ch = threadIdx.x % W, part = threadIdx.x / W;
+                                             ChainShared<W>& sh, int shift, Order order) {
+  // 2^shift channels; MINE predecessors a thread are enough
+  const int parts = (64 * kMaxWaves) >> shift;
+  const int ch = threadIdx.x & ((1 << shift) - 1), part = threadIdx.x >> shift;
   const int in_group = static_cast<int>(k % kChainGroup);
   const int64_t group = k / kChainGroup;
   uint64_t* const mine = c.tiles + k * c.width + ch;
@@ -113,21 +114,21 @@ __device__ __forceinline__ void chain_gather(const Chain& c, int64_t k, float2 (
     }
     chain_store(mine, chain_word(p, h));
   }
-  uint64_t w[kMine], before = 0;
+  uint64_t w[MINE], before = 0;
 #pragma unroll
-  for (int i = 0; i < kMine; ++i)
-    if (part + i * kParts < in_group) w[i] = chain_load(mine - (in_group - part - i * kParts) * c.width);
+  for (int i = 0; i < MINE; ++i)
+    if (part + i * parts < in_group) w[i] = chain_load(mine - (in_group - part - i * parts) * c.width);
   uint64_t* const left = c.groups + (group - 1) * c.width + ch;
-  if (part == kParts - 1 && group > 0) before = chain_load(left);
+  if (part == parts - 1 && group > 0) before = chain_load(left);
 #pragma unroll
-  for (int i = 0; i < kMine; ++i) {
-    const int j = part + i * kParts;
+  for (int i = 0; i < MINE; ++i) {
+    const int j = part + i * parts;
     if (j < in_group) {
       w[i] = chain_wait(mine - (in_group - j) * c.width, w[i]);
       sh.tiles[j][ch] = make_float2(word_p(w[i]), word_h(w[i]));
     }
   }
-  if (part == kParts - 1 && group > 0) sh.before[ch] = word_h(chain_wait(left, before));
+  if (part == parts - 1 && group > 0) sh.before[ch] = word_h(chain_wait(left, before));
 }
 
 // After a barrier: the state entering tile k for a channel, `first` being the
@@ -146,6 +147,28 @@ __device__ __forceinline__ bool chain_hands_on(int64_t k, int64_t ntiles) {
 }
 __device__ __forceinline__ void chain_leave(const Chain& c, int64_t k, int ch, float h) {
   chain_store(c.groups + k / kChainGroup * c.width + ch, chain_word(0.0f, h));
+}
+
+// Narrow calls: a wavefront's lanes hold 64 >> shift stretches of 2^shift
+// channels, in the scan's order (from the last stretch to the first for REV).
+// Turns each lane's pair into that of the stretches before its own, and returns
+// the whole wavefront's in the lanes of the stretch that the scan reaches last.
+template <bool PACKED, bool REV>
+__device__ __forceinline__ float2 wave_stretches(int shift, float& p, float& h) {
+  const int lane = threadIdx.x & 63, rank = REV ? 63 - lane : lane;
+  float ip = p, ih = h;
+  for (int k = 1 << shift; k < 64; k <<= 1) {
+    const float pp = REV ? __shfl_down(ip, k) : __shfl_up(ip, k), hh = REV ? __shfl_down(ih, k) : __shfl_up(ih, k);
+    if (rank >= k) {
+      ih = chain_apply<PACKED>(ip, ih, hh);
+      ip = chain_product<PACKED>(pp, ip);
+    }
+  }
+  const int one = 1 << shift;
+  const float pp = REV ? __shfl_down(ip, one) : __shfl_up(ip, one), hh = REV ? __shfl_down(ih, one) : __shfl_up(ih, one);
+  p = rank >= one ? pp : 1.0f;
+  h = rank >= one ? hh : 0.0f;
+  return make_float2(ip, ih);
 }
 
 // Marks of a packed token: the sequence it belongs to and whether it is its
@@ -185,7 +208,9 @@ __device__ __forceinline__ uint32_t narrow(const float (&h)[V]) {
   } else if constexpr (V == 1) {
     return f32_to_bf16(h[0]);
   } else {
-    return f32_to_bf16(h[0]) | static_cast<uint32_t>(f32_to_bf16(h[1])) << 16;
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{h[0], h[1]}, b2));   // one v_cvt_pk_bf16_f32
   }
 }
 
@@ -196,20 +221,22 @@ constexpr int kStream = 2;
 
 // One tensor's rows from a wavefront's first token on.  A row is reached
 // through a buffer descriptor of its own: the descriptor is scalar work, the
-// lane's offset is the same for every row and tensor, and lanes past the
-// channels read zeros and write nothing.
+// lane's offset the same for every row, and lanes past the channels read zeros
+// and write nothing.  `subs` rows of 16 tokens apart are reached through one
+// descriptor (narrow calls); a lane without a token there has offset kNowhere.
+constexpr uint32_t kNowhere = ~0u;
 struct TokenRows {
   char* first;
   int64_t stride;     // bytes
-  uint32_t row_bytes;
+  uint32_t bytes;
   template <typename T>
-  __device__ __forceinline__ void set(const void* p, int64_t elements, int64_t row_stride, int64_t D, T) {
+  __device__ __forceinline__ void set(const void* p, int64_t elements, int64_t row_stride, int64_t D, int subs, T) {
     first = static_cast<char*>(const_cast<void*>(p)) + elements * static_cast<int64_t>(sizeof(T));
     stride = row_stride * static_cast<int64_t>(sizeof(T));
-    row_bytes = static_cast<uint32_t>(D * static_cast<int64_t>(sizeof(T)));
+    bytes = static_cast<uint32_t>((subs - 1) * kWaveTokens * stride + D * static_cast<int64_t>(sizeof(T)));
   }
   __device__ __forceinline__ __amdgpu_buffer_rsrc_t row(int j) const {
-    return __builtin_amdgcn_make_buffer_rsrc(first + j * stride, 0, static_cast<int>(row_bytes), kRsrcWord3);
+    return __builtin_amdgcn_make_buffer_rsrc(first + j * stride, 0, static_cast<int>(bytes), kRsrcWord3);
   }
   template <int BYTES>
   __device__ __forceinline__ uint32_t load(int j, uint32_t at) const {
@@ -223,9 +250,10 @@ struct TokenRows {
   }
 };
 template <typename T>
-__device__ __forceinline__ TokenRows token_rows(const void* p, int64_t elements, int64_t row_stride, int64_t D) {
+__device__ __forceinline__ TokenRows token_rows(const void* p, int64_t elements, int64_t row_stride, int64_t D,
+                                                int subs = 1) {
   TokenRows r;
-  r.set(p, elements, row_stride, D, T{});
+  r.set(p, elements, row_stride, D, subs, T{});
   return r;
 }
 
@@ -233,24 +261,40 @@ __device__ __forceinline__ TokenRows token_rows(const void* p, int64_t elements,
 // from its start, each 256-byte aligned).
 struct GatedPlan {
   int waves;            // wavefronts a workgroup
+  int shift;            // see gated_plan
   int64_t tiles, cols;  // along the sequence, along the channels
   int64_t words;        // 0: one tile a sequence, no chain
   int64_t marks_at, words_at, parts_at, bytes;
 };
 
-inline GatedPlan gated_plan(int64_t batch, int64_t L, int64_t D, bool packed, int V, int64_t part_rows_per_tile) {
+// shift: 0, or log2 of the channels that a wavefront of a narrow call takes for
+// each of its 64 >> shift blocks of tokens.
+inline GatedPlan gated_plan(int64_t batch, int64_t L, int64_t D, bool packed, int V, int shift, int64_t part_rows_per_tile) {
   auto round256 = [](int64_t v) { return (v + 255) / 256 * 256; };
   GatedPlan q{};
-  const int64_t blocks = (L + kWaveTokens - 1) / kWaveTokens;
-  q.waves = static_cast<int>(blocks < 1 ? 1 : blocks < kMaxWaves ? blocks : kMaxWaves);
-  q.tiles = (blocks + q.waves - 1) / q.waves;
-  q.cols = (D + 64 * V - 1) / (64 * V);
-  q.words = q.tiles > 1 ? batch * q.cols * (q.tiles + (q.tiles + kChainGroup - 1) / kChainGroup) * 64 * V : 0;
+  const int64_t width = shift ? int64_t{1} << shift : 64 * V, subs = shift ? 64 >> shift : 1;
+  const int64_t blocks = (L + kWaveTokens - 1) / kWaveTokens, wave_blocks = (blocks + subs - 1) / subs;
+  q.shift = shift;
+  q.waves = static_cast<int>(wave_blocks < 1 ? 1 : wave_blocks < kMaxWaves ? wave_blocks : kMaxWaves);
+  q.tiles = (wave_blocks + q.waves - 1) / q.waves;
+  q.cols = (D + width - 1) / width;
+  q.words = q.tiles > 1 ? batch * q.cols * (q.tiles + (q.tiles + kChainGroup - 1) / kChainGroup) * width : 0;
   q.marks_at = q.words ? 256 : 0;   // the ticket counter
   q.words_at = q.marks_at + (packed ? round256(blocks * kWaveTokens * 4) : 0);
   q.parts_at = q.words_at + round256(q.words * 8);
   q.bytes = q.parts_at + part_rows_per_tile * q.tiles * batch * D * 4;
   return q;
+}
+
+// Channels of up to 32 leave half of a wavefront's lanes or more without work,
+// and the carry through its tiles, one after another, then bounds long
+// sequences (337,272 packed x 13 fp32: 214 us for 70 MB): there a wavefront
+// takes several blocks of 16 tokens side by side.
+inline int narrow_shift(int64_t D) { return D > 32 ? 0 : D > 16 ? 5 : D > 8 ? 4 : 3; }
+// Its rows are 16 tokens apart behind one descriptor, of less than 4 GB.
+inline bool narrow_fits(int64_t D, int64_t row_stride, int64_t esz) {
+  const int64_t subs = 64 >> narrow_shift(D);
+  return row_stride < (int64_t{1} << 31) / (subs * kWaveTokens * esz);
 }
 
 }  // namespace ssm
