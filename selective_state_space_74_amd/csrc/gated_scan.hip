@@ -153,25 +153,21 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_fwd_kernel(FwdParams p) 
   }
   __syncthreads();
   float h[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) h[v] = !PACKED && p.h0 ? p.h0[b * p.D + d + v] : 0.0f;
   if constexpr (CHAIN) {
     // the words of (row, col): tiles, then groups
     const int64_t ngroups = (p.tiles + kChainGroup - 1) / kChainGroup;
     uint64_t* const base = p.words + (static_cast<int64_t>(row) * p.cols + col) * (p.tiles + ngroups) * width;
     const Chain chain{base, base + static_cast<int64_t>(p.tiles) * width, width};
-    chain_gather<PACKED, W, NARROW ? 1 : 2 * V>(chain, tile, pairs, before, shift, [](int w) { return w; });
-    __syncthreads();
+    // thread i of the first 2^shift has channel i of the group
+    const int64_t di = min(static_cast<int64_t>(col) * W + (threadIdx.x & (width - 1)), p.D - 1);
+    const float first = !PACKED && p.h0 ? p.h0[b * p.D + di] : 0.0f;
+    chain_carry<PACKED, W, NARROW ? kMineNarrow : kMine * V>(chain, tile, p.tiles, pairs, before, shift, first,
+                                                             [](int w) { return w; });
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      h[v] = chain_entering<PACKED, W>(tile, c * V + v, before, h[v]);
-      if (wave == 0 && sub == 0 && chain_hands_on(tile, p.tiles)) {
-        float out = h[v];
+    for (int v = 0; v < V; ++v) h[v] = before.entering[c * V + v];
+  } else {
 #pragma unroll
-        for (int w = 0; w < kMaxWaves; ++w) out = chain_apply<PACKED>(pairs[w][c * V + v].x, pairs[w][c * V + v].y, out);
-        chain_leave(chain, tile, c * V + v, out);
-      }
-    }
+    for (int v = 0; v < V; ++v) h[v] = !PACKED && p.h0 ? p.h0[b * p.D + d + v] : 0.0f;
   }
   if (!some) return;
   for (int w = 0; w < wave; ++w)

@@ -182,25 +182,21 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams 
   }
   __syncthreads();
   float e[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) e[v] = !PACKED && p.dlast ? p.dlast[b * p.D + d + v] : 0.0f;
   if constexpr (CHAIN) {
     // the words of (row, col): tiles, then groups
     const int64_t ngroups = (p.tiles + kChainGroup - 1) / kChainGroup;
     uint64_t* const base = p.words + (static_cast<int64_t>(row) * p.cols + col) * (p.tiles + ngroups) * width;
     const Chain chain{base, base + static_cast<int64_t>(p.tiles) * width, width};
-    chain_gather<PACKED, W, NARROW ? 1 : 2 * V>(chain, k, pairs, before, shift, [](int w) { return kMaxWaves - 1 - w; });
-    __syncthreads();
+    // thread i of the first 2^shift has channel i of the group
+    const int64_t di = min(static_cast<int64_t>(col) * W + (threadIdx.x & (width - 1)), p.D - 1);
+    const float first = !PACKED && p.dlast ? p.dlast[b * p.D + di] : 0.0f;
+    chain_carry<PACKED, W, NARROW ? kMineNarrow : kMine * V>(chain, k, p.tiles, pairs, before, shift, first,
+                                                             [](int w) { return kMaxWaves - 1 - w; });
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      e[v] = chain_entering<PACKED, W>(k, c * V + v, before, e[v]);
-      if (wave == 0 && sub == 0 && chain_hands_on(k, p.tiles)) {
-        float out = e[v];
+    for (int v = 0; v < V; ++v) e[v] = before.entering[c * V + v];
+  } else {
 #pragma unroll
-        for (int w = kMaxWaves - 1; w >= 0; --w) out = chain_apply<PACKED>(pairs[w][c * V + v].x, pairs[w][c * V + v].y, out);
-        chain_leave(chain, k, c * V + v, out);
-      }
-    }
+    for (int v = 0; v < V; ++v) e[v] = !PACKED && p.dlast ? p.dlast[b * p.D + d + v] : 0.0f;
   }
   float acc[V];
 #pragma unroll

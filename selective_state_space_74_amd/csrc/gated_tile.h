@@ -10,9 +10,9 @@
 // adjoint) and every kChainGroup of them form a group.  A tile publishes its
 // (P, H) as soon as it has them, without waiting for anything.  It then takes
 // the state that left the group before, and folds the (P, H) of its
-// predecessors within the group into it, in order; the last tile of a group
-// publishes the state that leaves the group.  The order of the sums is fixed,
-// so results do not depend on which tile came first.
+// predecessors within the group into it; the last tile of a group
+// publishes the state that leaves the group.  The order of the products and
+// sums is fixed, so results do not depend on which tile came first.
 //
 // Every wait ends.  A workgroup takes its tile from a counter (a ticket), so
 // the tiles before it are held by workgroups that already run (or have run),
@@ -36,6 +36,10 @@ namespace ssm {
 constexpr int kWaveTokens = kCkpt;   // tokens of a wavefront: one checkpoint each
 constexpr int kMaxWaves = 8;
 constexpr int kChainGroup = 16;
+// Words of predecessors that a thread fetches at most: with 64 channels the
+// workgroup has 8 threads a channel; narrow calls have 16 or more.
+constexpr int kMine = (kChainGroup - 1 + kMaxWaves - 1) / kMaxWaves;
+constexpr int kMineNarrow = (kChainGroup - 1 + 2 * kMaxWaves - 1) / (2 * kMaxWaves);
 constexpr uint64_t kNoWord = ~uint64_t{0};
 
 __device__ __forceinline__ uint64_t chain_word(float p, float h) {
@@ -83,43 +87,45 @@ struct Chain {
   int64_t width;
 };
 
-// What a workgroup keeps of the tiles before it.
+// What a workgroup keeps of the tiles before it, and the state entering it.
 template <int W>
 struct ChainShared {
   float2 tiles[kChainGroup - 1][W];
-  float before[W];
+  float entering[W];
 };
 
-// Called by all threads of a tile once its wavefronts' pairs are in LDS, in
-// `order` (the wavefront that the scan passes w-th).  Publishes the tile's
-// pair, then brings the predecessors' words into LDS, a few each thread, so
-// that their latencies run side by side and no wavefront holds them all in
-// registers.
+// Called by all threads of a tile once its wavefronts' pairs are in LDS, `order`
+// giving the wavefront that the scan passes w-th; `first` is the state entering
+// tile 0, for channel threadIdx.x of the first 2^shift threads.  On return
+// sh.entering holds the state entering tile k.
+//
+// The tile's pair goes out before anything is waited for.  The predecessors'
+// words are brought into LDS by all wavefronts, at most MINE a thread, so that
+// their latencies run side by side and none holds them all in registers.  They
+// are folded into one pair, and the tile's own wavefronts into another, before
+// the state that left the group before is asked for: from group to group the
+// carry costs one product, one read and one write.
 template <bool PACKED, int W, int MINE, typename Order>
-__device__ __forceinline__ void chain_gather(const Chain& c, int64_t k, float2 (&pairs)[kMaxWaves][W],
-                                             ChainShared<W>& sh, int shift, Order order) {
-  // 2^shift channels; MINE predecessors a thread are enough
+__device__ __forceinline__ void chain_carry(const Chain& c, int64_t k, int64_t ntiles, float2 (&pairs)[kMaxWaves][W],
+                                            ChainShared<W>& sh, int shift, float first, Order order) {
   const int parts = (64 * kMaxWaves) >> shift;
   const int ch = threadIdx.x & ((1 << shift) - 1), part = threadIdx.x >> shift;
   const int in_group = static_cast<int>(k % kChainGroup);
   const int64_t group = k / kChainGroup;
   uint64_t* const mine = c.tiles + k * c.width + ch;
-  if (part == 0 && in_group != kChainGroup - 1) {
-    float p = 1.0f, h = 0.0f;
+  float2 own = make_float2(1.0f, 0.0f);
+  if (part == 0) {
 #pragma unroll
     for (int w = 0; w < kMaxWaves; ++w) {
       const float2 q = pairs[order(w)][ch];
-      p = chain_product<PACKED>(p, q.x);
-      h = chain_apply<PACKED>(q.x, q.y, h);
+      own = make_float2(chain_product<PACKED>(own.x, q.x), chain_apply<PACKED>(q.x, q.y, own.y));
     }
-    chain_store(mine, chain_word(p, h));
+    if (in_group != kChainGroup - 1) chain_store(mine, chain_word(own.x, own.y));
   }
-  uint64_t w[MINE], before = 0;
+  uint64_t w[MINE];
 #pragma unroll
   for (int i = 0; i < MINE; ++i)
     if (part + i * parts < in_group) w[i] = chain_load(mine - (in_group - part - i * parts) * c.width);
-  uint64_t* const left = c.groups + (group - 1) * c.width + ch;
-  if (part == parts - 1 && group > 0) before = chain_load(left);
 #pragma unroll
   for (int i = 0; i < MINE; ++i) {
     const int j = part + i * parts;
@@ -128,25 +134,23 @@ __device__ __forceinline__ void chain_gather(const Chain& c, int64_t k, float2 (
       sh.tiles[j][ch] = make_float2(word_p(w[i]), word_h(w[i]));
     }
   }
-  if (part == parts - 1 && group > 0) sh.before[ch] = word_h(chain_wait(left, before));
-}
-
-// After a barrier: the state entering tile k for a channel, `first` being the
-// one entering tile 0.
-template <bool PACKED, int W>
-__device__ __forceinline__ float chain_entering(int64_t k, int ch, const ChainShared<W>& sh, float first) {
-  float h = k >= kChainGroup ? sh.before[ch] : first;
-  const int in_group = static_cast<int>(k % kChainGroup);
-  for (int j = 0; j < in_group; ++j) h = chain_apply<PACKED>(sh.tiles[j][ch].x, sh.tiles[j][ch].y, h);
-  return h;
-}
-
-// Whether tile k hands the state that leaves it to the next group.
-__device__ __forceinline__ bool chain_hands_on(int64_t k, int64_t ntiles) {
-  return k % kChainGroup == kChainGroup - 1 && k + 1 < ntiles;
-}
-__device__ __forceinline__ void chain_leave(const Chain& c, int64_t k, int ch, float h) {
-  chain_store(c.groups + k / kChainGroup * c.width + ch, chain_word(0.0f, h));
+  __syncthreads();
+  if (part == 0) {
+    float2 q = make_float2(1.0f, 0.0f);   // of the group's tiles before this one
+#pragma unroll
+    for (int j = 0; j < kChainGroup - 1; ++j) {
+      if (j < in_group) {
+        const float2 t = sh.tiles[j][ch];
+        q = make_float2(chain_product<PACKED>(q.x, t.x), chain_apply<PACKED>(t.x, t.y, q.y));
+      }
+    }
+    uint64_t* const left = c.groups + (group - 1) * c.width + ch;
+    const float h = chain_apply<PACKED>(q.x, q.y, group > 0 ? word_h(chain_wait(left, chain_load(left))) : first);
+    if (in_group == kChainGroup - 1 && k + 1 < ntiles)
+      chain_store(c.groups + group * c.width + ch, chain_word(0.0f, chain_apply<PACKED>(own.x, own.y, h)));
+    sh.entering[ch] = h;
+  }
+  __syncthreads();
 }
 
 // Narrow calls: a wavefront's lanes hold 64 >> shift stretches of 2^shift
