@@ -26,7 +26,7 @@ struct FwdParams {
   int zero_outside;
 };
 
-template <typename T, int V, bool PACKED, bool CHAIN, bool NARROW>
+template <typename T, int V, bool PACKED, bool CHAIN, bool NARROW, int CACHE>
 __global__ __launch_bounds__(64 * kMaxWaves) void gated_fwd_kernel(FwdParams p) {
   constexpr int W = 64 * V;
   __shared__ float2 pairs[kMaxWaves][W];
@@ -94,9 +94,9 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_fwd_kernel(FwdParams p) 
     for (int j = 0; j < kWaveTokens; ++j) {
       const int jj = PLAIN || NARROW ? j : min(j, n - 1);
       const bool in = PLAIN || !NARROW || j < n;
-      ra[j] = ga.load<kBytes>(jj, in ? at(p.gas) : kNowhere);
-      rg[j] = gx.load<kBytes>(jj, in ? at(p.gxs) : kNowhere);
-      rx[j] = x.load<kBytes>(jj, in ? at(p.xs) : kNowhere);
+      ra[j] = ga.load<kBytes, CACHE>(jj, in ? at(p.gas) : kNowhere);
+      rg[j] = gx.load<kBytes, CACHE>(jj, in ? at(p.gxs) : kNowhere);
+      rx[j] = x.load<kBytes, CACHE>(jj, in ? at(p.xs) : kNowhere);
     }
 #pragma unroll
     for (int j = 0; j < kWaveTokens; ++j) {
@@ -198,7 +198,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_fwd_kernel(FwdParams p) 
         }
       }
       const bool write = (!MARKED || mark(j) >= 0 || p.zero_outside) && (PLAIN || !NARROW || j < n);
-      if (NARROW || write) out.store<kBytes>(j, write ? at(p.os) : kNowhere, narrow<T, V>(h));
+      if (NARROW || write) out.store<kBytes, CACHE>(j, write ? at(p.os) : kNowhere, narrow<T, V>(h));
     }
   };
   if (plain) outputs(std::true_type{});
@@ -312,15 +312,15 @@ int shift_of(const ssm_gated_args& a) {
   return narrow_shift(a.dim);
 }
 
-template <typename T, int V, bool NARROW>
+template <typename T, int V, bool NARROW, int CACHE>
 void launch_fwd(const FwdParams& p, const GatedPlan& q, bool packed, hipStream_t stream) {
   const dim3 grid(static_cast<unsigned>(q.tiles * q.cols * p.batch)), block(64 * q.waves);
   if (packed) {
-    if (q.words) gated_fwd_kernel<T, V, true, true, NARROW><<<grid, block, 0, stream>>>(p);
-    else gated_fwd_kernel<T, V, true, false, NARROW><<<grid, block, 0, stream>>>(p);
+    if (q.words) gated_fwd_kernel<T, V, true, true, NARROW, CACHE><<<grid, block, 0, stream>>>(p);
+    else gated_fwd_kernel<T, V, true, false, NARROW, CACHE><<<grid, block, 0, stream>>>(p);
   } else {
-    if (q.words) gated_fwd_kernel<T, V, false, true, NARROW><<<grid, block, 0, stream>>>(p);
-    else gated_fwd_kernel<T, V, false, false, NARROW><<<grid, block, 0, stream>>>(p);
+    if (q.words) gated_fwd_kernel<T, V, false, true, NARROW, CACHE><<<grid, block, 0, stream>>>(p);
+    else gated_fwd_kernel<T, V, false, false, NARROW, CACHE><<<grid, block, 0, stream>>>(p);
   }
 }
 
@@ -355,13 +355,20 @@ hipError_t launch_gated_fwd(const ssm_gated_args& a, hipStream_t stream) {
                     a.gate_x_batch_stride, a.gate_x_seq_stride, a.out_batch_stride, a.out_seq_stride,
                     a.seqlen, a.dim, (a.seqlen + kCkpt - 1) / kCkpt, static_cast<uint32_t>(a.batch),
                     static_cast<uint32_t>(q.tiles), static_cast<uint32_t>(q.cols), q.shift, a.c, a.zero_outside};
+  const int64_t esz = a.io_dtype == SSM_BF16 ? 2 : 4;
+  const bool lines = on_lines(a.x, a.x_batch_stride, a.x_seq_stride, esz) &&
+                     on_lines(a.gate_a, a.gate_a_batch_stride, a.gate_a_seq_stride, esz) &&
+                     on_lines(a.gate_x, a.gate_x_batch_stride, a.gate_x_seq_stride, esz) &&
+                     on_lines(a.out, a.out_batch_stride, a.out_seq_stride, esz);
   if (a.io_dtype == SSM_BF16) {
-    if (shift) launch_fwd<uint16_t, 1, true>(p, q, packed, stream);
-    else if (V == 2) launch_fwd<uint16_t, 2, false>(p, q, packed, stream);
-    else launch_fwd<uint16_t, 1, false>(p, q, packed, stream);
+    if (shift) launch_fwd<uint16_t, 1, true, kPlain>(p, q, packed, stream);
+    else if (V == 1) launch_fwd<uint16_t, 1, false, kPlain>(p, q, packed, stream);
+    else if (lines) launch_fwd<uint16_t, 2, false, kStream>(p, q, packed, stream);
+    else launch_fwd<uint16_t, 2, false, kPlain>(p, q, packed, stream);
   } else {
-    if (shift) launch_fwd<float, 1, true>(p, q, packed, stream);
-    else launch_fwd<float, 1, false>(p, q, packed, stream);
+    if (shift) launch_fwd<float, 1, true, kPlain>(p, q, packed, stream);
+    else if (lines) launch_fwd<float, 1, false, kStream>(p, q, packed, stream);
+    else launch_fwd<float, 1, false, kPlain>(p, q, packed, stream);
   }
   return hipGetLastError();
 }

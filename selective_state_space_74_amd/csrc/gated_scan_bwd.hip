@@ -32,7 +32,7 @@ struct BwdParams {
 // The states before each token come forward from the wavefront's checkpoint,
 // so the three gradients' factors of e are ready before e is known; only
 // e_t = dout_t + a_{t+1} e_{t+1} waits for the tiles behind.
-template <typename T, int V, bool PACKED, bool CHAIN, bool NARROW>
+template <typename T, int V, bool PACKED, bool CHAIN, bool NARROW, int CACHE>
 __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams p) {
   constexpr int W = 64 * V;
   __shared__ float2 pairs[kMaxWaves][W];
@@ -104,10 +104,10 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams 
     for (int j = 0; j < kWaveTokens; ++j) {
       const int jj = PLAIN || NARROW ? j : min(j, n - 1);
       const bool in = PLAIN || !NARROW || j < n;
-      ra[j] = ta.load<kBytes>(jj, in ? at(p.gas) : kNowhere);
-      rg[j] = tg.load<kBytes>(jj, in ? at(p.gxs) : kNowhere);
-      rx[j] = tx.load<kBytes>(jj, in ? at(p.xs) : kNowhere);
-      rd[j] = td.load<kBytes>(jj, in ? at(p.dos) : kNowhere);
+      ra[j] = ta.load<kBytes, CACHE>(jj, in ? at(p.gas) : kNowhere);
+      rg[j] = tg.load<kBytes, CACHE>(jj, in ? at(p.gxs) : kNowhere);
+      rx[j] = tx.load<kBytes, CACHE>(jj, in ? at(p.xs) : kNowhere);
+      rd[j] = td.load<kBytes, CACHE>(jj, in ? at(p.dos) : kNowhere);
     }
 #pragma unroll
     for (int j = 0; j < kWaveTokens; ++j) {
@@ -236,9 +236,9 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams 
           }
         }
         const bool write = PLAIN || !NARROW || j < n;
-        dx.store<kBytes>(j, write ? at(p.dxs) : kNowhere, narrow<T, V>(ox));
-        dga.store<kBytes>(j, write ? at(p.dgas) : kNowhere, narrow<T, V>(oa));
-        dgx.store<kBytes>(j, write ? at(p.dgxs) : kNowhere, narrow<T, V>(og));
+        dx.store<kBytes, CACHE>(j, write ? at(p.dxs) : kNowhere, narrow<T, V>(ox));
+        dga.store<kBytes, CACHE>(j, write ? at(p.dgas) : kNowhere, narrow<T, V>(oa));
+        dgx.store<kBytes, CACHE>(j, write ? at(p.dgxs) : kNowhere, narrow<T, V>(og));
       }
     };
     if (plain) outputs(std::true_type{});
@@ -304,16 +304,31 @@ GatedPlan plan(const ssm_gated_bwd_args& a) {
   return gated_plan(a.batch, a.seqlen, a.dim, a.cu_seqlens != nullptr, kV, shift_of(a), 1);
 }
 
-template <typename T, bool NARROW>
+template <typename T, bool NARROW, int CACHE>
 void launch_bwd(const BwdParams& p, const GatedPlan& q, bool packed, hipStream_t stream) {
   const dim3 grid(static_cast<unsigned>(q.tiles * q.cols * p.batch)), block(64 * q.waves);
   if (packed) {
-    if (q.words) gated_bwd_kernel<T, kV, true, true, NARROW><<<grid, block, 0, stream>>>(p);
-    else gated_bwd_kernel<T, kV, true, false, NARROW><<<grid, block, 0, stream>>>(p);
+    if (q.words) gated_bwd_kernel<T, kV, true, true, NARROW, CACHE><<<grid, block, 0, stream>>>(p);
+    else gated_bwd_kernel<T, kV, true, false, NARROW, CACHE><<<grid, block, 0, stream>>>(p);
   } else {
-    if (q.words) gated_bwd_kernel<T, kV, false, true, NARROW><<<grid, block, 0, stream>>>(p);
-    else gated_bwd_kernel<T, kV, false, false, NARROW><<<grid, block, 0, stream>>>(p);
+    if (q.words) gated_bwd_kernel<T, kV, false, true, NARROW, CACHE><<<grid, block, 0, stream>>>(p);
+    else gated_bwd_kernel<T, kV, false, false, NARROW, CACHE><<<grid, block, 0, stream>>>(p);
   }
+}
+
+template <typename T>
+void launch_rows(const ssm_gated_bwd_args& a, const BwdParams& p, const GatedPlan& q, bool packed, hipStream_t stream) {
+  constexpr int64_t esz = sizeof(T);
+  const bool lines = on_lines(a.x, a.x_batch_stride, a.x_seq_stride, esz) &&
+                     on_lines(a.gate_a, a.gate_a_batch_stride, a.gate_a_seq_stride, esz) &&
+                     on_lines(a.gate_x, a.gate_x_batch_stride, a.gate_x_seq_stride, esz) &&
+                     on_lines(a.dout, a.dout_batch_stride, a.dout_seq_stride, esz) &&
+                     on_lines(a.dx, a.dx_batch_stride, a.dx_seq_stride, esz) &&
+                     on_lines(a.dgate_a, a.dgate_a_batch_stride, a.dgate_a_seq_stride, esz) &&
+                     on_lines(a.dgate_x, a.dgate_x_batch_stride, a.dgate_x_seq_stride, esz);
+  if (q.shift) launch_bwd<T, true, kPlain>(p, q, packed, stream);
+  else if (lines) launch_bwd<T, false, kStream>(p, q, packed, stream);
+  else launch_bwd<T, false, kPlain>(p, q, packed, stream);
 }
 
 }  // namespace
@@ -344,9 +359,8 @@ hipError_t launch_gated_bwd(const ssm_gated_bwd_args& a, hipStream_t stream) {
                     static_cast<uint32_t>(q.tiles), static_cast<uint32_t>(q.cols), q.shift, a.c};
   const int64_t rows = q.tiles * a.batch;
   if (rows > 0) {
-    const bool bf16 = a.io_dtype == SSM_BF16;
-    if (q.shift) bf16 ? launch_bwd<uint16_t, true>(p, q, packed, stream) : launch_bwd<float, true>(p, q, packed, stream);
-    else bf16 ? launch_bwd<uint16_t, false>(p, q, packed, stream) : launch_bwd<float, false>(p, q, packed, stream);
+    if (a.io_dtype == SSM_BF16) launch_rows<uint16_t>(a, p, q, packed, stream);
+    else launch_rows<float>(a, p, q, packed, stream);
   }
   gated_dlam_kernel<<<static_cast<unsigned>((a.dim + kSumCols - 1) / kSumCols), kSumCols * kSumRows, 0, stream>>>(
       p.part, rows, a.dim, a.lam, a.c, a.dlam);
