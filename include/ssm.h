@@ -399,8 +399,10 @@ typedef struct ssm_ssd_args {
  * Workspace: device scratch owned by the caller, 8-byte aligned, of at least
  * ssm_gated_scan_workspace_size() bytes where that is not 0 (required:
  * SSM_ERR_SCRATCH otherwise), not overlapping any tensor and not in use by
- * another call that may run at the same time.  Its contents before the call
- * do not matter, and nothing is kept in it between calls. */
+ * another call that may run at the same time (calls on two streams, or two
+ * captured graphs, take a workspace each; sharing one gives unspecified or NaN
+ * outputs).  Its contents before the call do not matter, and nothing is kept in
+ * it between calls. */
 typedef struct ssm_gated_args {
   int64_t batch, seqlen, dim, nseq;
   int32_t io_dtype;      /* ssm_dtype */

@@ -928,7 +928,8 @@ def gated_scan_fwd(x, gate_a, gate_x, lam, c=8.0, h0=None, cu_seqlens=None, retu
     here, left as they were in one that is given.
     `checkpoints` (optional): an fp32 tensor of gated_checkpoint_shape(x.shape)
     for gated_scan_bwd.  `last_state` may be h0 itself.  `workspace`: a device
-    tensor reused across calls (by one call at a time); None allocates one."""
+    tensor reused across calls, by one call at a time (calls on two streams or
+    two captured graphs take one each); None allocates one."""
     torch = _torch()
     shape, dev, io = x.shape, x.device, x.dtype
     code = _io_code(x)
@@ -996,7 +997,9 @@ def gated_scan(x, gate_a, gate_x, lam, c=8.0, h0=None, cu_seqlens=None, return_l
         @staticmethod
         def forward(ctx, x, gate_a, gate_x, lam, h0):
             ctx.set_materialize_grads(False)
-            ck = torch.empty(gated_checkpoint_shape(x.shape), dtype=torch.float32, device=x.device)
+            ck = None
+            if any(ctx.needs_input_grad):
+                ck = torch.empty(gated_checkpoint_shape(x.shape), dtype=torch.float32, device=x.device)
             out, last = gated_scan_fwd(x, gate_a, gate_x, lam, c=c, h0=h0, cu_seqlens=cu_seqlens,
                                        return_last_state=True, checkpoints=ck)
             ctx.save_for_backward(x, gate_a, gate_x, lam, h0, cu_seqlens, ck)

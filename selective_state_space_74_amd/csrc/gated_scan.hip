@@ -19,7 +19,7 @@ struct FwdParams {
   const int32_t* marks;
   uint32_t* ticket; uint64_t* words;
   int64_t xb, xs, gab, gas, gxb, gxs, ob, os;
-  int64_t L, D, nck;
+  int64_t L, D, nck, nseq;
   uint32_t batch, tiles, cols;
   int shift;   // narrow calls: log2 of the channels
   float c;
@@ -41,6 +41,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_fwd_kernel(FwdParams p) 
     if (threadIdx.x == 0) taken = atomicAdd(p.ticket, 1u);
     __syncthreads();
     id = __builtin_amdgcn_readfirstlane(taken);
+    if (id >= p.tiles * p.cols * p.batch) return;   // only if another call reset the counter
   }
   // along the channels first, then the batch: neighbours read neighbouring bytes
   const uint32_t col = id % p.cols, row = id / p.cols % p.batch, tile = id / p.cols / p.batch;
@@ -77,9 +78,13 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_fwd_kernel(FwdParams p) 
   // decide the path are known measured slower, 314 us against 295 us for forward
   // and backward of 30,011 x 1536 bf16: the rows' uses then wait together.)
   int32_t marks = 0, each[NARROW ? kWaveTokens : 1];
-  if constexpr (PACKED && !NARROW) marks = some ? p.marks[t0 + lane % kWaveTokens] : kOutside;
+  auto mark_at = [&](int64_t t) {
+    const int32_t m = p.marks[t];
+    return m >> 2 < p.nseq ? m : kOutside;
+  };
+  if constexpr (PACKED && !NARROW) marks = some ? mark_at(t0 + lane % kWaveTokens) : kOutside;
   if constexpr (PACKED && NARROW)
-    for (int i = c; i < n; i += width) marks |= p.marks[t0 + i];   // kOutside sets every bit
+    for (int i = c; i < n; i += width) marks |= mark_at(t0 + i);   // kOutside sets every bit
   auto mark = [&](int j) { return NARROW ? each[NARROW ? j : 0] : __builtin_amdgcn_readlane(marks, j); };
 
   // tokens to (a, b) of h = a h + b; past the end of the row (1, 0)
@@ -130,7 +135,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_fwd_kernel(FwdParams p) 
   if (!plain && some) {
     if constexpr (PACKED && NARROW) {
 #pragma unroll
-      for (int j = 0; j < kWaveTokens; ++j) each[j] = j < n ? p.marks[t0 + j] : kOutside;
+      for (int j = 0; j < kWaveTokens; ++j) each[j] = j < n ? mark_at(t0 + j) : kOutside;
       marks = 0;   // of the lane's own stretch now
 #pragma unroll
       for (int j = 0; j < kWaveTokens; ++j) marks |= j < n ? each[j] : 0;
@@ -353,7 +358,7 @@ hipError_t launch_gated_fwd(const ssm_gated_args& a, hipStream_t stream) {
                     reinterpret_cast<uint64_t*>(ws + q.words_at),
                     a.x_batch_stride, a.x_seq_stride, a.gate_a_batch_stride, a.gate_a_seq_stride,
                     a.gate_x_batch_stride, a.gate_x_seq_stride, a.out_batch_stride, a.out_seq_stride,
-                    a.seqlen, a.dim, (a.seqlen + kCkpt - 1) / kCkpt, static_cast<uint32_t>(a.batch),
+                    a.seqlen, a.dim, (a.seqlen + kCkpt - 1) / kCkpt, nseq, static_cast<uint32_t>(a.batch),
                     static_cast<uint32_t>(q.tiles), static_cast<uint32_t>(q.cols), q.shift, a.c, a.zero_outside};
   const int64_t esz = a.io_dtype == SSM_BF16 ? 2 : 4;
   const bool lines = on_lines(a.x, a.x_batch_stride, a.x_seq_stride, esz) &&

@@ -22,7 +22,7 @@ struct BwdParams {
   const int32_t* marks;
   uint32_t* ticket; uint64_t* words;
   int64_t xb, xs, gab, gas, gxb, gxs, dob, dos, dxb, dxs, dgab, dgas, dgxb, dgxs;
-  int64_t L, D, nck;
+  int64_t L, D, nck, nseq;
   uint32_t batch, tiles, cols;
   int shift;   // narrow calls: log2 of the channels
   float c;
@@ -47,6 +47,7 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams 
     if (threadIdx.x == 0) taken = atomicAdd(p.ticket, 1u);
     __syncthreads();
     id = __builtin_amdgcn_readfirstlane(taken);
+    if (id >= p.tiles * p.cols * p.batch) return;   // only if another call reset the counter
   }
   const uint32_t col = id % p.cols, row = id / p.cols % p.batch, k = id / p.cols / p.batch;
   const uint32_t tile = p.tiles - 1 - k;
@@ -84,9 +85,13 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams 
   // decide the path are known measured slower, 314 us against 295 us for forward
   // and backward of 30,011 x 1536 bf16: the rows' uses then wait together.)
   int32_t marks = 0, each[NARROW ? kWaveTokens : 1];
-  if constexpr (PACKED && !NARROW) marks = some ? p.marks[t0 + lane % kWaveTokens] : kOutside;
+  auto mark_at = [&](int64_t t) {
+    const int32_t m = p.marks[t];
+    return m >> 2 < p.nseq ? m : kOutside;
+  };
+  if constexpr (PACKED && !NARROW) marks = some ? mark_at(t0 + lane % kWaveTokens) : kOutside;
   if constexpr (PACKED && NARROW)
-    for (int i = c; i < n; i += width) marks |= p.marks[t0 + i];   // kOutside sets every bit
+    for (int i = c; i < n; i += width) marks |= mark_at(t0 + i);   // kOutside sets every bit
   auto mark = [&](int j) { return NARROW ? each[NARROW ? j : 0] : __builtin_amdgcn_readlane(marks, j); };
 
   auto tokens = [&](auto every) {
@@ -159,7 +164,7 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams 
   if (!plain && some) {
     if constexpr (PACKED && NARROW) {
 #pragma unroll
-      for (int j = 0; j < kWaveTokens; ++j) each[j] = j < n ? p.marks[t0 + j] : kOutside;
+      for (int j = 0; j < kWaveTokens; ++j) each[j] = j < n ? mark_at(t0 + j) : kOutside;
       marks = 0;   // of the lane's own stretch now
 #pragma unroll
       for (int j = 0; j < kWaveTokens; ++j) marks |= j < n ? each[j] : 0;
@@ -355,7 +360,7 @@ hipError_t launch_gated_bwd(const ssm_gated_bwd_args& a, hipStream_t stream) {
                     a.gate_x_batch_stride, a.gate_x_seq_stride, a.dout_batch_stride, a.dout_seq_stride,
                     a.dx_batch_stride, a.dx_seq_stride, a.dgate_a_batch_stride, a.dgate_a_seq_stride,
                     a.dgate_x_batch_stride, a.dgate_x_seq_stride,
-                    a.seqlen, a.dim, (a.seqlen + kCkpt - 1) / kCkpt, static_cast<uint32_t>(a.batch),
+                    a.seqlen, a.dim, (a.seqlen + kCkpt - 1) / kCkpt, nseq, static_cast<uint32_t>(a.batch),
                     static_cast<uint32_t>(q.tiles), static_cast<uint32_t>(q.cols), q.shift, a.c};
   const int64_t rows = q.tiles * a.batch;
   if (rows > 0) {

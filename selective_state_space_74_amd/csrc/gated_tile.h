@@ -55,8 +55,14 @@ __device__ __forceinline__ void chain_store(uint64_t* p, uint64_t w) {
 __device__ __forceinline__ uint64_t chain_load(uint64_t* p) {
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
+// A word that is awaited.  By the argument above it comes within microseconds; a
+// workspace that another call overwrites meanwhile, which the interface forbids,
+// could take it away, and then the wait is given up after some seconds with
+// kNoWord itself, whose halves are NaNs: wrong use shows as NaN outputs and not
+// as a GPU that hangs.
+constexpr int kPolls = 1 << 22;
 __device__ __forceinline__ uint64_t chain_wait(uint64_t* p, uint64_t w) {
-  while (w == kNoWord) {
+  for (int i = 0; w == kNoWord && i < kPolls; ++i) {
     __builtin_amdgcn_s_sleep(1);
     w = chain_load(p);
   }

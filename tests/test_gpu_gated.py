@@ -192,6 +192,25 @@ def test_nan_stays_in_its_channel_and_sequence():
     assert torch.isnan(p[100:150, 10]).all() and torch.isfinite(p[150:]).all() and torch.isfinite(last[1]).all()
 
 
+@pytest.mark.parametrize("D", [12, 66])
+def test_nan_of_one_sequence_spares_the_others_gradients(D):
+    """In x (the states after it are NaN) and in dout (the adjoints before it),
+    next to a border inside a block of tokens and far from one."""
+    t = make((700,), D, "f32", n=3, seed=24)
+    cu = torch.tensor([0, 300, 317, 700], dtype=torch.int32, device=DEV)
+    t["x"][305, 5] = float("nan")
+    t["dout"][310, 7] = float("inf")
+    out, last, ck = forward(t, cu)
+    g = backward(t, ck, cu)
+    for k in ("dx", "dgate_a", "dgate_x"):
+        assert torch.isfinite(g[k][:300]).all() and torch.isfinite(g[k][317:]).all(), k
+        keep = torch.ones(D, dtype=torch.bool, device=DEV)
+        keep[5] = keep[7] = False
+        assert torch.isfinite(g[k][:, keep]).all(), k
+    assert torch.isfinite(g["dh0"][[0, 2]]).all()
+    assert torch.isfinite(out[:300]).all() and torch.isfinite(out[317:]).all() and torch.isfinite(last[[0, 2]]).all()
+
+
 def test_zero_sizes():
     for lead in ((0, 5), (3, 0)):
         t = make(lead, 8, "f32", n=lead[0], seed=15)
