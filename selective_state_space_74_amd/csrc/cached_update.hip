@@ -5,14 +5,16 @@
 // A lane has one channel and all its states: 16 codes are one 16-byte access,
 // and a wavefront's are one run of 1 KB.  (The fp32 update spreads a channel
 // over four lanes for the same reason.)  The readout and the block's maximum
-// then need no exchange between lanes.  A channel's row of A is loaded once for
-// kRows batch rows; B and C, the same for every lane where the wavefront is
-// inside one B/C group, come through scalar loads and are unpacked by scalar
-// instructions.
+// then need no exchange between lanes.  B and C, the same for every lane where
+// the wavefront is inside one B/C group, come through scalar loads and are
+// unpacked by scalar instructions.  (Several batch rows a thread, to load A once
+// for them, measured 19.7 us with two and 21.5 with four against 20.0 at
+// 256 x 5120 x 16; A's rows come from L2 anyway.)
 //
-// 256 x 5120 x 16 states move 53 MB a step where the fp32 update moves 178 MB,
-// and cost about 17 vector instructions a state, four of them the generator's:
-// memory and issue bind about equally.
+// 256 x 5120 x 16 states move 53 MB a step, 10 us of memory time, where the
+// fp32 update moves 178 MB; 327 vector instructions a wavefront, a fifth of them
+// the generator's, are 11 us of issue.  A wavefront loads, computes and stores
+// once, six of them a SIMD: 19.3 us.
 #include "slots.h"
 #include "state_cache.h"
 

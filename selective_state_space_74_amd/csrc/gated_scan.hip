@@ -12,6 +12,10 @@ namespace {
 
 constexpr int kThreads = 256;   // of the single-token step
 
+// The tile kernel (gated_tile.h says how tiles are joined): (a, b) of every token
+// in registers, then one product and one sum a token with the state that
+// entered.  16 tokens a wavefront: with 8, halves as many bytes would be on
+// their way a workgroup, and twice the pairs to hand on.
 struct FwdParams {
   const void* x; const void* ga; const void* gx;
   const float* lam; const float* h0;
@@ -224,7 +228,8 @@ struct StepParams {
   float c;
 };
 
-// A lane has V channels of a row: 16 bytes of its fp32 state.
+// A lane has V channels of a row: 16 bytes of its fp32 state.  256 x 5120 bf16
+// take 6 us (21 MB); what is left is the way from the slot to the state.
 template <typename T, int V>
 __global__ __launch_bounds__(kThreads) void gated_step_kernel(StepParams p) {
   struct alignas(sizeof(T) * V) Vec { T v[V]; };
@@ -292,9 +297,10 @@ void launch_step(const StepParams& p, hipStream_t stream) {
 namespace {
 
 // A lane takes 4 bytes of a row: one fp32 channel, or two bf16 ones where every
-// row allows 4-byte accesses.  Measured at 16,411 x 1536 packed fp32 tokens:
-// 99 us, and 128 us with two channels (8 bytes) a lane; at 262,144 x 1536
-// bf16: 789 us, and 971 us with one channel (2 bytes).
+// row allows 4-byte accesses.  Measured at 262,144 x 1536 bf16: 596 us, and 684
+// us with one channel (2 bytes) a lane.  Two fp32 channels (8 bytes) cost
+// registers and with them a workgroup a compute unit: 128 us against 99 at
+// 16,411 x 1536, in the kernel's first form (84 us now).
 int channels_per_lane(const ssm_gated_args& a) {
   auto ok = [&](const void* p, int64_t sb, int64_t ss) {
     return reinterpret_cast<uintptr_t>(p) % 4 == 0 && sb % 2 == 0 && ss % 2 == 0;
