@@ -361,6 +361,9 @@ typedef struct ssm_ssd_args {
   void* workspace;    size_t workspace_bytes;
 } ssm_ssd_args;
 
+/* Tokens between two state checkpoints of the gated scan. */
+#define SSM_GATED_CHECKPOINT_TOKENS 8
+
 /* Arguments of the gated linear recurrence: one state per channel, decay and
  * input scale from the token.  For every sequence and channel d, with
  * s_d = c softplus(lam[d]) and sigma the logistic function:
@@ -383,9 +386,9 @@ typedef struct ssm_ssd_args {
  *   h0, last_state : (nseq, dim), or (batch, dim) without cu_seqlens; fp32,
  *                contiguous.  h0 NULL is a zero state, last_state NULL: not
  *                wanted.  An empty sequence's last state is its h0 (or zero).
- *   checkpoints : fp32 (batch, ceil(seqlen / SSM_CHECKPOINT_TOKENS), dim),
+ *   checkpoints : fp32 (batch, ceil(seqlen / SSM_GATED_CHECKPOINT_TOKENS), dim),
  *                contiguous; element (b, k, d) is h entering token
- *                k * SSM_CHECKPOINT_TOKENS, for ssm_gated_scan_bwd (what it
+ *                k * SSM_GATED_CHECKPOINT_TOKENS, for ssm_gated_scan_bwd (what it
  *                holds where that token begins a sequence or is in none is
  *                unspecified).  NULL: none written.
  * Sizes: zero sizes are no-ops, but that empty sequences still set last_state;

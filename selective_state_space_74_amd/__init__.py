@@ -48,6 +48,7 @@ LIB_PATH = os.path.join(_PKG, "libssm.so")
 
 SSM_ABI_VERSION = 8
 CHECKPOINT_TOKENS = 16
+GATED_CHECKPOINT_TOKENS = 8
 MAX_CONV = 8
 SSM_F32, SSM_BF16 = 0, 1
 STATUS = {0: "SSM_OK", 1: "SSM_ERR_NULL", 2: "SSM_ERR_SHAPE", 3: "SSM_ERR_STRIDE",
@@ -911,7 +912,7 @@ def gated_checkpoint_shape(shape):
     """Shape of the fp32 checkpoints that gated_scan_fwd writes for the
     backward, for x of the given shape."""
     shape = tuple(shape)
-    return shape[:-2] + ((shape[-2] + CHECKPOINT_TOKENS - 1) // CHECKPOINT_TOKENS, shape[-1])
+    return shape[:-2] + ((shape[-2] + GATED_CHECKPOINT_TOKENS - 1) // GATED_CHECKPOINT_TOKENS, shape[-1])
 
 
 def gated_scan_fwd(x, gate_a, gate_x, lam, c=8.0, h0=None, cu_seqlens=None, return_last_state=False,

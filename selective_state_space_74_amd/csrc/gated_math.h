@@ -6,7 +6,7 @@
 
 namespace ssm {
 
-constexpr int kCkpt = SSM_CHECKPOINT_TOKENS;
+constexpr int kGatedCkpt = SSM_GATED_CHECKPOINT_TOKENS;
 
 // 1 / (1 + e^-z) on the hardware exp2 and reciprocal: 0 and 1 at -inf and inf.
 __device__ __forceinline__ float sigmoid_f32(float z) {

@@ -17,7 +17,7 @@ __global__ __launch_bounds__(kThreads) void gated_prep_kernel(PrepParams p) {
   for (int64_t i = i0; i < p.nwords / 2; i += step) w[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
   if (p.marks) {
     // padded to whole wavefronts of tokens with tokens outside
-    const int64_t n = (p.L + kCkpt - 1) / kCkpt * kCkpt;
+    const int64_t n = (p.L + kWaveTokens - 1) / kWaveTokens * kWaveTokens;
     for (int64_t t = i0; t < n; t += step) {
       // entries not above t, by halving: the last of equal ones begins a
       // sequence that has tokens

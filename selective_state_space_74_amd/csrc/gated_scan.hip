@@ -186,11 +186,12 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_fwd_kernel(FwdParams p) 
       h[v] = chain_apply<PACKED>(q.x, q.y, h[v]);
     }
   if constexpr (NARROW) h[0] = chain_apply<PACKED>(P[0], H[0], h[0]);   // the stretches before this one
-  if (p.ck && live && (!NARROW || n > 0)) {
-    float* const ck = p.ck + (b * p.nck + t0 / kCkpt) * p.D + d;
+  // the state entering token j, for the backward
+  auto checkpoint = [&](int j) {
+    float* const ck = p.ck + (b * p.nck + (t0 + j) / kGatedCkpt) * p.D + d;
 #pragma unroll
     for (int v = 0; v < V; ++v) ck[v] = h[v];
-  }
+  };
   const TokenRows out = token_rows<T>(p.out, b * p.ob + wave_t0 * p.os, p.os, p.D, subs);
   auto outputs = [&](auto every) {
     constexpr bool PLAIN = decltype(every)::value;
@@ -198,6 +199,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_fwd_kernel(FwdParams p) 
 #pragma unroll
     for (int j = 0; j < kWaveTokens; ++j) {
       if (!PLAIN && !NARROW && j >= n) continue;
+      if (j % kGatedCkpt == 0 && p.ck && live && (PLAIN || !NARROW || j < n)) checkpoint(j);
 #pragma unroll
       for (int v = 0; v < V; ++v) h[v] = MARKED && (mark(j) & 1) ? u[j][v] : fmaf(a[j][v], h[v], u[j][v]);
       if constexpr (MARKED) {
@@ -313,7 +315,7 @@ int channels_per_lane(const ssm_gated_args& a) {
 }
 
 GatedPlan plan(const ssm_gated_args& a, int V, int shift) {
-  return gated_plan(a.batch, a.seqlen, a.dim, a.cu_seqlens != nullptr, V, shift, 0);
+  return gated_plan(a.batch, a.seqlen, a.dim, a.cu_seqlens != nullptr, V, kWaveTokens, shift, 0);
 }
 
 int shift_of(const ssm_gated_args& a) {
@@ -364,7 +366,7 @@ hipError_t launch_gated_fwd(const ssm_gated_args& a, hipStream_t stream) {
                     reinterpret_cast<uint64_t*>(ws + q.words_at),
                     a.x_batch_stride, a.x_seq_stride, a.gate_a_batch_stride, a.gate_a_seq_stride,
                     a.gate_x_batch_stride, a.gate_x_seq_stride, a.out_batch_stride, a.out_seq_stride,
-                    a.seqlen, a.dim, (a.seqlen + kCkpt - 1) / kCkpt, nseq, static_cast<uint32_t>(a.batch),
+                    a.seqlen, a.dim, (a.seqlen + kGatedCkpt - 1) / kGatedCkpt, nseq, static_cast<uint32_t>(a.batch),
                     static_cast<uint32_t>(q.tiles), static_cast<uint32_t>(q.cols), q.shift, a.c, a.zero_outside};
   const int64_t esz = a.io_dtype == SSM_BF16 ? 2 : 4;
   const bool lines = on_lines(a.x, a.x_batch_stride, a.x_seq_stride, esz) &&

@@ -38,6 +38,7 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams 
   __shared__ float2 pairs[kMaxWaves][W];
   __shared__ ChainShared<CHAIN ? W : 1> before;
   __shared__ uint32_t taken;
+  constexpr int kTok = V == 2 ? kGatedCkpt : kWaveTokens;   // tokens of a wavefront
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int waves = blockDim.x >> 6;
@@ -51,28 +52,29 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams 
   }
   const uint32_t col = id % p.cols, row = id / p.cols % p.batch, k = id / p.cols / p.batch;
   const uint32_t tile = p.tiles - 1 - k;
-  // A wavefront has 16 tokens of 64 V channels; in a narrow call each stretch of
-  // 2^shift lanes has 16 tokens of its own.
+  // A wavefront has 16 tokens of 64 channels or 8 of 128 (its registers hold six
+  // values for each); in a narrow call each stretch of 2^shift lanes has 16
+  // tokens of its own.
   constexpr int kBytes = V * sizeof(T);
   const int shift = NARROW ? p.shift : V == 2 ? 7 : 6;
   const int width = 1 << shift, subs = NARROW ? 64 >> shift : 1;
   const int sub = NARROW ? lane >> shift : 0, c = NARROW ? lane & (width - 1) : lane;
-  const int64_t b = row, wave_t0 = (static_cast<int64_t>(tile) * waves + wave) * (kWaveTokens * subs);
-  const int64_t t0 = wave_t0 + sub * kWaveTokens;
-  const int n = static_cast<int>(min(static_cast<int64_t>(kWaveTokens), max(int64_t{0}, p.L - t0)));
+  const int64_t b = row, wave_t0 = (static_cast<int64_t>(tile) * waves + wave) * (kTok * subs);
+  const int64_t t0 = wave_t0 + sub * kTok;
+  const int n = static_cast<int>(min(static_cast<int64_t>(kTok), max(int64_t{0}, p.L - t0)));
   const bool some = NARROW ? wave_t0 < p.L : n > 0;   // of the wavefront
   const int64_t ch = static_cast<int64_t>(col) * W + c * V;
   const bool live = ch < p.D;
   const int64_t d = live ? ch : p.D - V;   // per-channel values: lanes past the channels repeat the last ones
   // a lane's offset from the wavefront's row j of a tensor
   auto at = [&](int64_t stride) {
-    if constexpr (NARROW) return live ? static_cast<uint32_t>((c + sub * kWaveTokens * stride) * sizeof(T)) : kNowhere;
+    if constexpr (NARROW) return live ? static_cast<uint32_t>((c + sub * kTok * stride) * sizeof(T)) : kNowhere;
     else return static_cast<uint32_t>(ch) * static_cast<uint32_t>(sizeof(T));
   };
 
   Rate s[V];
-  float a[kWaveTokens][V], fx[kWaveTokens][V], fg[kWaveTokens][V], fa[kWaveTokens][V], fl[kWaveTokens][V],
-      dout[kWaveTokens][V], P[V], Q[V];
+  float a[kTok][V], fx[kTok][V], fg[kTok][V], fa[kTok][V], fl[kTok][V],
+      dout[kTok][V], P[V], Q[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     s[v] = Rate(p.c, p.lam[d + v]);
@@ -84,12 +86,12 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams 
   // one load brings, as scalars.  (Fetching the rows before the marks that
   // decide the path are known measured slower, 314 us against 295 us for forward
   // and backward of 30,011 x 1536 bf16: the rows' uses then wait together.)
-  int32_t marks = 0, each[NARROW ? kWaveTokens : 1];
+  int32_t marks = 0, each[NARROW ? kTok : 1];
   auto mark_at = [&](int64_t t) {
     const int32_t m = p.marks[t];
     return m >> 2 < p.nseq ? m : kOutside;
   };
-  if constexpr (PACKED && !NARROW) marks = some ? mark_at(t0 + lane % kWaveTokens) : kOutside;
+  if constexpr (PACKED && !NARROW) marks = some ? mark_at(t0 + lane % kTok) : kOutside;
   if constexpr (PACKED && NARROW)
     for (int i = c; i < n; i += width) marks |= mark_at(t0 + i);   // kOutside sets every bit
   auto mark = [&](int j) { return NARROW ? each[NARROW ? j : 0] : __builtin_amdgcn_readlane(marks, j); };
@@ -97,16 +99,16 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams 
   auto tokens = [&](auto every) {
     constexpr bool PLAIN = decltype(every)::value;
     constexpr bool MARKED = PACKED && !PLAIN;
-    uint32_t rx[kWaveTokens], ra[kWaveTokens], rg[kWaveTokens], rd[kWaveTokens];
+    uint32_t rx[kTok], ra[kTok], rg[kTok], rd[kTok];
     const TokenRows tx = token_rows<T>(p.x, b * p.xb + wave_t0 * p.xs, p.xs, p.D, subs),
                     ta = token_rows<T>(p.ga, b * p.gab + wave_t0 * p.gas, p.gas, p.D, subs),
                     tg = token_rows<T>(p.gx, b * p.gxb + wave_t0 * p.gxs, p.gxs, p.D, subs),
                     td = token_rows<T>(p.dout, b * p.dob + wave_t0 * p.dos, p.dos, p.D, subs);
     float h[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = p.ck[(b * p.nck + (NARROW ? min(t0 / kCkpt, p.nck - 1) : t0 / kCkpt)) * p.D + d + v];
+    for (int v = 0; v < V; ++v) h[v] = p.ck[(b * p.nck + (NARROW ? min(t0 / kGatedCkpt, p.nck - 1) : t0 / kGatedCkpt)) * p.D + d + v];
 #pragma unroll
-    for (int j = 0; j < kWaveTokens; ++j) {
+    for (int j = 0; j < kTok; ++j) {
       const int jj = PLAIN || NARROW ? j : min(j, n - 1);
       const bool in = PLAIN || !NARROW || j < n;
       ra[j] = ta.load<kBytes, CACHE>(jj, in ? at(p.gas) : kNowhere);
@@ -115,7 +117,7 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams 
       rd[j] = td.load<kBytes, CACHE>(jj, in ? at(p.dos) : kNowhere);
     }
 #pragma unroll
-    for (int j = 0; j < kWaveTokens; ++j) {
+    for (int j = 0; j < kTok; ++j) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         if constexpr (MARKED) {
@@ -150,7 +152,7 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams 
       }
     }
 #pragma unroll
-    for (int j = kWaveTokens - 1; j >= 0; --j)
+    for (int j = kTok - 1; j >= 0; --j)
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         P[v] *= a[j][v];
@@ -158,16 +160,16 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams 
       }
   };
   bool plain;
-  if constexpr (NARROW) plain = __all(n == kWaveTokens) && !__any(marks < 0 || (marks & 3));
-  else plain = n == kWaveTokens && (!PACKED || __ballot(marks < 0 || (marks & 3)) == 0);
+  if constexpr (NARROW) plain = __all(n == kTok) && !__any(marks < 0 || (marks & 3));
+  else plain = n == kTok && (!PACKED || __ballot(marks < 0 || (marks & 3)) == 0);
   if (plain) tokens(std::true_type{});
   if (!plain && some) {
     if constexpr (PACKED && NARROW) {
 #pragma unroll
-      for (int j = 0; j < kWaveTokens; ++j) each[j] = j < n ? mark_at(t0 + j) : kOutside;
+      for (int j = 0; j < kTok; ++j) each[j] = j < n ? mark_at(t0 + j) : kOutside;
       marks = 0;   // of the lane's own stretch now
 #pragma unroll
-      for (int j = 0; j < kWaveTokens; ++j) marks |= j < n ? each[j] : 0;
+      for (int j = 0; j < kTok; ++j) marks |= j < n ? each[j] : 0;
     }
     tokens(std::false_type{});
   }
@@ -221,7 +223,7 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams 
       constexpr bool PLAIN = decltype(every)::value;
       constexpr bool MARKED = PACKED && !PLAIN;
 #pragma unroll
-      for (int j = kWaveTokens - 1; j >= 0; --j) {
+      for (int j = kTok - 1; j >= 0; --j) {
         if (!PLAIN && !NARROW && j >= n) continue;
         float ox[V], oa[V], og[V];
 #pragma unroll
@@ -295,8 +297,6 @@ __global__ __launch_bounds__(kSumCols * kSumRows) void gated_dlam_kernel(const f
   }
 }
 
-constexpr int kV = 1;   // channels a lane
-
 int shift_of(const ssm_gated_bwd_args& a) {
   const int64_t esz = a.io_dtype == SSM_BF16 ? 2 : 4;
   for (int64_t stride : {a.x_seq_stride, a.gate_a_seq_stride, a.gate_x_seq_stride, a.dout_seq_stride, a.dx_seq_stride,
@@ -305,24 +305,46 @@ int shift_of(const ssm_gated_bwd_args& a) {
   return narrow_shift(a.dim);
 }
 
-GatedPlan plan(const ssm_gated_bwd_args& a) {
-  return gated_plan(a.batch, a.seqlen, a.dim, a.cu_seqlens != nullptr, kV, shift_of(a), 1);
+// Two channels a lane as in the forward, where a call has at least four groups
+// of 128 channels and more than one tile.  A tile is then 64 tokens and not 128:
+// with fewer groups the carry through the tiles, about 0.9 tokens a nanosecond
+// and group, would bound the call, and a second tile costs a launch.  Forward and
+// backward with two against one: 390 against 400 us at 4 x 4096 x 5120 bf16, 261
+// against 273 at 2 x 8587 x 2306; with one group, 282 against 203 at 250,095 x 40.
+constexpr int64_t kMinGroups = 4;
+int channels_per_lane(const ssm_gated_bwd_args& a) {
+  auto ok = [&](const void* p, int64_t sb, int64_t ss) {
+    return reinterpret_cast<uintptr_t>(p) % 4 == 0 && sb % 2 == 0 && ss % 2 == 0;
+  };
+  return a.io_dtype == SSM_BF16 && a.dim % 2 == 0 && a.seqlen > kMaxWaves * kWaveTokens &&
+                 a.batch * ((a.dim + 127) / 128) >= kMinGroups &&
+                 ok(a.x, a.x_batch_stride, a.x_seq_stride) && ok(a.gate_a, a.gate_a_batch_stride, a.gate_a_seq_stride) &&
+                 ok(a.gate_x, a.gate_x_batch_stride, a.gate_x_seq_stride) &&
+                 ok(a.dout, a.dout_batch_stride, a.dout_seq_stride) && ok(a.dx, a.dx_batch_stride, a.dx_seq_stride) &&
+                 ok(a.dgate_a, a.dgate_a_batch_stride, a.dgate_a_seq_stride) &&
+                 ok(a.dgate_x, a.dgate_x_batch_stride, a.dgate_x_seq_stride)
+             ? 2 : 1;
 }
 
-template <typename T, bool NARROW, int CACHE>
+GatedPlan plan(const ssm_gated_bwd_args& a, int V, int shift) {
+  return gated_plan(a.batch, a.seqlen, a.dim, a.cu_seqlens != nullptr, V, V == 2 ? kGatedCkpt : kWaveTokens, shift, 1);
+}
+
+template <typename T, int V, bool NARROW, int CACHE>
 void launch_bwd(const BwdParams& p, const GatedPlan& q, bool packed, hipStream_t stream) {
   const dim3 grid(static_cast<unsigned>(q.tiles * q.cols * p.batch)), block(64 * q.waves);
-  if (packed) {
-    if (q.words) gated_bwd_kernel<T, kV, true, true, NARROW, CACHE><<<grid, block, 0, stream>>>(p);
-    else gated_bwd_kernel<T, kV, true, false, NARROW, CACHE><<<grid, block, 0, stream>>>(p);
-  } else {
-    if (q.words) gated_bwd_kernel<T, kV, false, true, NARROW, CACHE><<<grid, block, 0, stream>>>(p);
-    else gated_bwd_kernel<T, kV, false, false, NARROW, CACHE><<<grid, block, 0, stream>>>(p);
+  if (V == 2 || q.words) {
+    if (packed) gated_bwd_kernel<T, V, true, true, NARROW, CACHE><<<grid, block, 0, stream>>>(p);
+    else gated_bwd_kernel<T, V, false, true, NARROW, CACHE><<<grid, block, 0, stream>>>(p);
+  } else if constexpr (V == 1) {   // two channels a lane: more than one tile
+    if (packed) gated_bwd_kernel<T, V, true, false, NARROW, CACHE><<<grid, block, 0, stream>>>(p);
+    else gated_bwd_kernel<T, V, false, false, NARROW, CACHE><<<grid, block, 0, stream>>>(p);
   }
 }
 
 template <typename T>
-void launch_rows(const ssm_gated_bwd_args& a, const BwdParams& p, const GatedPlan& q, bool packed, hipStream_t stream) {
+void launch_rows(const ssm_gated_bwd_args& a, const BwdParams& p, const GatedPlan& q, int V, bool packed,
+                 hipStream_t stream) {
   constexpr int64_t esz = sizeof(T);
   const bool lines = on_lines(a.x, a.x_batch_stride, a.x_seq_stride, esz) &&
                      on_lines(a.gate_a, a.gate_a_batch_stride, a.gate_a_seq_stride, esz) &&
@@ -331,17 +353,29 @@ void launch_rows(const ssm_gated_bwd_args& a, const BwdParams& p, const GatedPla
                      on_lines(a.dx, a.dx_batch_stride, a.dx_seq_stride, esz) &&
                      on_lines(a.dgate_a, a.dgate_a_batch_stride, a.dgate_a_seq_stride, esz) &&
                      on_lines(a.dgate_x, a.dgate_x_batch_stride, a.dgate_x_seq_stride, esz);
-  if (q.shift) launch_bwd<T, true, kPlain>(p, q, packed, stream);
-  else if (lines) launch_bwd<T, false, kStream>(p, q, packed, stream);
-  else launch_bwd<T, false, kPlain>(p, q, packed, stream);
+  if (q.shift) return launch_bwd<T, 1, true, kPlain>(p, q, packed, stream);
+  if constexpr (sizeof(T) == 2) {
+    if (V == 2) {
+      if (lines) return launch_bwd<T, 2, false, kStream>(p, q, packed, stream);
+      return launch_bwd<T, 2, false, kPlain>(p, q, packed, stream);
+    }
+  }
+  if (lines) launch_bwd<T, 1, false, kStream>(p, q, packed, stream);
+  else launch_bwd<T, 1, false, kPlain>(p, q, packed, stream);
 }
 
 }  // namespace
 
-size_t gated_bwd_workspace_bytes(const ssm_gated_bwd_args& a) { return static_cast<size_t>(plan(a).bytes); }
+// The size for whichever form runs: it depends on no address.
+size_t gated_bwd_workspace_bytes(const ssm_gated_bwd_args& a) {
+  const int shift = shift_of(a);
+  const int64_t one = plan(a, 1, shift).bytes, two = shift ? 0 : plan(a, 2, 0).bytes;
+  return static_cast<size_t>(one > two ? one : two);
+}
 
 hipError_t launch_gated_bwd(const ssm_gated_bwd_args& a, hipStream_t stream) {
-  const GatedPlan q = plan(a);
+  const int shift = shift_of(a), V = shift ? 1 : channels_per_lane(a);
+  const GatedPlan q = plan(a, V, shift);
   char* const ws = static_cast<char*>(a.workspace);
   const bool packed = a.cu_seqlens != nullptr;
   const int64_t nseq = packed ? a.nseq : a.batch;
@@ -360,12 +394,12 @@ hipError_t launch_gated_bwd(const ssm_gated_bwd_args& a, hipStream_t stream) {
                     a.gate_x_batch_stride, a.gate_x_seq_stride, a.dout_batch_stride, a.dout_seq_stride,
                     a.dx_batch_stride, a.dx_seq_stride, a.dgate_a_batch_stride, a.dgate_a_seq_stride,
                     a.dgate_x_batch_stride, a.dgate_x_seq_stride,
-                    a.seqlen, a.dim, (a.seqlen + kCkpt - 1) / kCkpt, nseq, static_cast<uint32_t>(a.batch),
+                    a.seqlen, a.dim, (a.seqlen + kGatedCkpt - 1) / kGatedCkpt, nseq, static_cast<uint32_t>(a.batch),
                     static_cast<uint32_t>(q.tiles), static_cast<uint32_t>(q.cols), q.shift, a.c};
   const int64_t rows = q.tiles * a.batch;
   if (rows > 0) {
-    if (a.io_dtype == SSM_BF16) launch_rows<uint16_t>(a, p, q, packed, stream);
-    else launch_rows<float>(a, p, q, packed, stream);
+    if (a.io_dtype == SSM_BF16) launch_rows<uint16_t>(a, p, q, V, packed, stream);
+    else launch_rows<float>(a, p, q, V, packed, stream);
   }
   gated_dlam_kernel<<<static_cast<unsigned>((a.dim + kSumCols - 1) / kSumCols), kSumCols * kSumRows, 0, stream>>>(
       p.part, rows, a.dim, a.lam, a.c, a.dlam);

@@ -37,7 +37,7 @@
 
 namespace ssm {
 
-constexpr int kWaveTokens = kCkpt;   // tokens of a wavefront: one checkpoint each
+constexpr int kWaveTokens = 16;   // tokens of a wavefront (the backward with two channels a lane: 8)
 constexpr int kMaxWaves = 8;
 constexpr int kChainGroup = 16;
 // Words of predecessors that a thread fetches at most: with 64 channels the
@@ -290,18 +290,19 @@ struct GatedPlan {
 
 // shift: 0, or log2 of the channels that a wavefront of a narrow call takes for
 // each of its 64 >> shift blocks of tokens.
-inline GatedPlan gated_plan(int64_t batch, int64_t L, int64_t D, bool packed, int V, int shift, int64_t part_rows_per_tile) {
+inline GatedPlan gated_plan(int64_t batch, int64_t L, int64_t D, bool packed, int V, int tokens, int shift,
+                            int64_t part_rows_per_tile) {
   auto round256 = [](int64_t v) { return (v + 255) / 256 * 256; };
   GatedPlan q{};
   const int64_t width = shift ? int64_t{1} << shift : 64 * V, subs = shift ? 64 >> shift : 1;
-  const int64_t blocks = (L + kWaveTokens - 1) / kWaveTokens, wave_blocks = (blocks + subs - 1) / subs;
+  const int64_t blocks = (L + tokens - 1) / tokens, wave_blocks = (blocks + subs - 1) / subs;
   q.shift = shift;
   q.waves = static_cast<int>(wave_blocks < 1 ? 1 : wave_blocks < kMaxWaves ? wave_blocks : kMaxWaves);
   q.tiles = (wave_blocks + q.waves - 1) / q.waves;
   q.cols = (D + width - 1) / width;
   q.words = q.tiles > 1 ? batch * q.cols * (q.tiles + (q.tiles + kChainGroup - 1) / kChainGroup) * width : 0;
   q.marks_at = q.words ? 256 : 0;   // the ticket counter
-  q.words_at = q.marks_at + (packed ? round256(blocks * kWaveTokens * 4) : 0);
+  q.words_at = q.marks_at + (packed ? round256((L + kWaveTokens - 1) / kWaveTokens * kWaveTokens * 4) : 0);
   q.parts_at = q.words_at + round256(q.words * 8);
   q.bytes = q.parts_at + part_rows_per_tile * q.tiles * batch * D * 4;
   return q;

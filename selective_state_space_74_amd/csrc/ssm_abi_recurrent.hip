@@ -28,6 +28,7 @@ bool collide(const Tokens& t, int64_t batch, int64_t L, int64_t D) {
 }
 
 constexpr int64_t kMaxGroups = int64_t{1} << 31;
+constexpr int64_t kGatedTokens = SSM_GATED_CHECKPOINT_TOKENS;
 constexpr int64_t kMaxDim = int64_t{1} << 28;
 constexpr int64_t kMaxPacked = int64_t{1} << 29;   // sequence numbers and two marks share 32 bits
 bool too_many_groups(int64_t batch, int64_t L, int64_t D) {
@@ -105,7 +106,7 @@ int ssm_validate_gated(const ssm_gated_args* a) {
   const Rows inputs[] = {rows(in[0]), rows(in[1]), rows(in[2]), flat(a->lam, D, 4),
                          flat(a->cu_seqlens, S + 1, 4), flat(a->h0, S * D, 4)};
   const Rows outputs[] = {rows(out), flat(a->last_state, S * D, 4),
-                          flat(a->checkpoints, B * ((L + kCkptTokens - 1) / kCkptTokens) * D, 4),
+                          flat(a->checkpoints, B * ((L + kGatedTokens - 1) / kGatedTokens) * D, 4),
                           flat(a->workspace, static_cast<int64_t>(a->workspace_bytes), 1)};
   for (const Rows& o : outputs) {
     for (const Rows& i : inputs) {
@@ -150,7 +151,7 @@ int ssm_validate_gated_bwd(const ssm_gated_bwd_args* a) {
   auto flat = [&](const void* p, int64_t n, int64_t e) { return Rows{span1(p, n, e)}; };
   const Rows inputs[] = {rows(in[0]), rows(in[1]), rows(in[2]), rows(in[3]), flat(a->lam, D, 4),
                          flat(a->cu_seqlens, S + 1, 4), flat(a->h0, S * D, 4), flat(a->dlast, S * D, 4),
-                         flat(a->checkpoints, B * ((L + kCkptTokens - 1) / kCkptTokens) * D, 4)};
+                         flat(a->checkpoints, B * ((L + kGatedTokens - 1) / kGatedTokens) * D, 4)};
   const Rows outputs[] = {rows(out[0]), rows(out[1]), rows(out[2]), flat(a->dlam, D, 4), flat(a->dh0, S * D, 4),
                           flat(a->workspace, static_cast<int64_t>(a->workspace_bytes), 1)};
   for (const Rows& o : outputs) {

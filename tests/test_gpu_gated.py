@@ -86,7 +86,9 @@ def run_and_check(t, io, what, cu=None, dlast=True):
 SHAPES = [(1, 1, 1), (2, 3, 5), (1, 15, 64), (1, 16, 66), (3, 17, 65), (2, 64, 128), (1, 127, 130), (2, 128, 256),
           (1, 129, 8), (2, 300, 33), (5, 500, 100), (1, 2049, 130), (1, 5000, 34), (40, 2, 258), (300, 1, 7),
           # up to 32 channels: several blocks of tokens a wavefront
-          (1, 5000, 13), (2, 3000, 8), (1, 2100, 32), (3, 700, 20), (1, 20000, 3), (2, 1024, 16), (1, 1025, 1)]
+          (1, 5000, 13), (2, 3000, 8), (1, 2100, 32), (3, 700, 20), (1, 20000, 3), (2, 1024, 16), (1, 1025, 1),
+          # four groups of 128 channels and more: two bf16 channels a lane backward
+          (4, 200, 100), (1, 1030, 514), (5, 129, 2)]
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
@@ -111,7 +113,7 @@ PACKED = {
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 @pytest.mark.parametrize("name", PACKED)
-@pytest.mark.parametrize("D,h0", [(64, True), (131, False), (256, True), (7, True), (13, False), (32, True)])
+@pytest.mark.parametrize("D,h0", [(64, True), (131, False), (256, True), (7, True), (13, False), (32, True), (400, True)])
 def test_packed(name, D, h0, io):
     cu = torch.tensor(PACKED[name], dtype=torch.int32, device=DEV)
     T = PACKED[name][-1] + (13 if name in ("outside", "all_empty", "none") else 0)

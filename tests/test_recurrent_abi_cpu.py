@@ -98,6 +98,7 @@ def test_struct_sizes_and_constants():
         assert getattr(L, f"ssm_{name}_args_size")() == ctypes.sizeof(T)
     header = open(os.path.join(ROOT, "include", "ssm.h")).read()
     assert f"#define SSM_CACHE_BLOCK {ssm.CACHE_BLOCK}" in header
+    assert f"#define SSM_GATED_CHECKPOINT_TOKENS {ssm.GATED_CHECKPOINT_TOKENS}" in header
     for k, v in ssm.CACHE_FORMATS.items():
         assert re.search(rf"SSM_CACHE_{k.upper()} = {v}\b", header)
 
@@ -245,4 +246,4 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
     codes, scales = (torch.zeros(s, dtype=torch.uint8) for s in ssm.state_cache_shape(3, (4, 16)))
     with pytest.raises(ValueError):
         ssm.state_cache_write(codes, scales, torch.zeros(2, 4, 16))   # not on a GPU
-    assert ssm.gated_checkpoint_shape((2, 33, 7)) == (2, 3, 7) and ssm.gated_checkpoint_shape((0, 7)) == (0, 7)
+    assert ssm.gated_checkpoint_shape((2, 33, 7)) == (2, 5, 7) and ssm.gated_checkpoint_shape((0, 7)) == (0, 7)
