@@ -834,12 +834,34 @@ def _switched(device, stream):
 
 
 def _on(device, stream):
-    """The tensors' device and the call's stream as the current ones, and the
-    stream's handle: what is allocated meanwhile belongs to that stream."""
-    torch = _torch()
-    if stream is None and device.index == torch.cuda.current_device():
-        return _Current(torch._C._cuda_getCurrentRawStream(device.index))
+    """The tensors' device (its index) and the call's stream as the current
+    ones, and the stream's handle: what is allocated meanwhile belongs to that
+    stream."""
+    C = _torch()._C
+    if stream is None and device == C._cuda_getDevice():
+        return _Current(C._cuda_getCurrentRawStream(device))
     return _switched(device, stream)
+
+
+def _gpu(name, t):
+    """The index of the GPU a tensor is on."""
+    device = t.get_device()
+    if device < 0:
+        raise ValueError(f"{name} must be on a GPU, got {t.device}")
+    return device
+
+
+def _placed(name, t, dtype, device):
+    if t.get_device() != device or t.dtype != dtype:
+        _check_dev(name, t, _torch().device("cuda", device), dtype)
+
+
+def _empty(like, shape, dtype, device):
+    """A new tensor of this shape, by the shorter way where `like` has it."""
+    torch = _torch()
+    if like.shape == shape and like.dtype == dtype and like.is_contiguous():
+        return torch.empty_like(like)
+    return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _launch(name, args, stream):
@@ -851,8 +873,7 @@ def _launch(name, args, stream):
 def _tokens(name, t, shape, dtype, device):
     """Pointer and (batch, token) strides of a tensor shaped and typed like x; a
     packed (tokens, dim) tensor is one batch row."""
-    if t.device != device or not t.is_cuda or t.dtype != dtype:
-        _check_dev(name, t, device, dtype)
+    _placed(name, t, dtype, device)
     if t.shape != shape:
         raise ValueError(f"{name} must be shaped like x")
     st = t.stride()
@@ -865,8 +886,7 @@ def _fp32(name, t, shape, device):
     """Pointer of a contiguous fp32 tensor of this shape, None for None."""
     if t is None:
         return None
-    if t.device != device or t.dtype != _torch().float32:
-        _check_dev(name, t, device, _torch().float32)
+    _placed(name, t, _torch().float32, device)
     if t.shape != shape or not t.is_contiguous():
         _contig_f32(name, t, shape)
     return t.data_ptr()
@@ -888,7 +908,7 @@ def _gated_sizes(x, cu_seqlens):
         return x.shape[0], x.shape[1], x.shape[0], 0, None
     if x.dim() != 2:
         raise ValueError("x must be (tokens, dim) with cu_seqlens")
-    _check_dev("cu_seqlens", cu_seqlens, x.device, torch.int32)
+    _placed("cu_seqlens", cu_seqlens, torch.int32, x.get_device())
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1 or not cu_seqlens.is_contiguous():
         raise ValueError("cu_seqlens must be a contiguous int32 vector of nseq + 1 entries")
     n = cu_seqlens.numel() - 1
@@ -901,7 +921,7 @@ def _set_workspace(a, need, workspace, device):
     if workspace is None or workspace.numel() * workspace.element_size() < need:
         workspace = _torch().empty(need, dtype=_torch().uint8, device=device)
     else:
-        _check_dev("workspace", workspace, device)
+        _placed("workspace", workspace, workspace.dtype, device)
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
     a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -932,8 +952,8 @@ def gated_scan_fwd(x, gate_a, gate_x, lam, c=8.0, h0=None, cu_seqlens=None, retu
     tensor reused across calls, by one call at a time (calls on two streams or
     two captured graphs take one each); None allocates one."""
     torch = _torch()
-    shape, dev, io = x.shape, x.device, x.dtype
     code = _io_code(x)
+    shape, dev, io = x.shape, _gpu("x", x), x.dtype
     batch, L, n, nseq, cu = _gated_sizes(x, cu_seqlens)
     dim = shape[-1]
     inputs = _tokens("x", x, shape, io, dev) + _tokens("gate_a", gate_a, shape, io, dev) + \
@@ -943,7 +963,7 @@ def gated_scan_fwd(x, gate_a, gate_x, lam, c=8.0, h0=None, cu_seqlens=None, retu
     with _on(dev, stream) as s:
         made = out is None
         if made:
-            out = torch.empty(shape, dtype=io, device=dev)
+            out = _empty(x, shape, io, dev)
         if return_last_state and last_state is None:
             last_state = torch.empty((n, dim), dtype=torch.float32, device=dev)
         a = GatedArgs(batch, L, dim, nseq, code, made, c, *inputs, lam_p, cu, h0_p,
@@ -963,8 +983,8 @@ def gated_scan_bwd(dout, x, gate_a, gate_x, lam, checkpoints, c=8.0, h0=None, cu
     Rows of tokens outside every sequence are zero.  Every output is the same
     bits from run to run.  `workspace`: as for gated_scan_fwd."""
     torch = _torch()
-    shape, dev, io = x.shape, x.device, x.dtype
     code = _io_code(x)
+    shape, dev, io = x.shape, _gpu("x", x), x.dtype
     batch, L, n, nseq, cu = _gated_sizes(x, cu_seqlens)
     dim = shape[-1]
     inputs = _tokens("x", x, shape, io, dev) + _tokens("gate_a", gate_a, shape, io, dev) + \
@@ -975,7 +995,7 @@ def gated_scan_bwd(dout, x, gate_a, gate_x, lam, checkpoints, c=8.0, h0=None, cu
     dlast_p = _fp32("dlast", dlast, (n, dim), dev)
     c = _decay_constant(c)
     with _on(dev, stream) as s:
-        dx, dga, dgx = (torch.empty(shape, dtype=io, device=dev) for _ in range(3))
+        dx, dga, dgx = (_empty(dout, shape, io, dev) for _ in range(3))
         g = dict(dx=dx, dgate_a=dga, dgate_x=dgx, dlam=torch.empty(dim, dtype=torch.float32, device=dev))
         if h0 is not None:
             g["dh0"] = torch.empty((n, dim), dtype=torch.float32, device=dev)
@@ -1020,25 +1040,24 @@ def gated_scan(x, gate_a, gate_x, lam, c=8.0, h0=None, cu_seqlens=None, return_l
 
 
 def _check_slots(slots, batch, nslots, device):
-    torch = _torch()
     if slots is None:
         if batch > nslots:
             raise ValueError("without slots, the batch must not be larger than the pool")
         return
-    _check_dev("slots", slots, device, torch.int32)
-    if tuple(slots.shape) != (batch,) or not slots.is_contiguous():
+    _placed("slots", slots, _torch().int32, device)
+    if slots.shape != (batch,) or not slots.is_contiguous():
         raise ValueError("slots must be a contiguous int32 vector with one entry per batch row")
 
 
-def _row_tokens(name, t, batch, dim, dtype, device):
+def _row_tokens(name, t, shape, dtype, device):
     """Pointer and row stride of a (batch, dim) tensor, (None, 0) for None."""
     if t is None:
         return None, 0
-    if t.device != device or not t.is_cuda or t.dtype != dtype:
-        _check_dev(name, t, device, dtype)
-    if t.shape != (batch, dim) or (dim > 1 and t.stride(1) != 1):
+    _placed(name, t, dtype, device)
+    st = t.stride()
+    if t.shape != shape or (st[1] != 1 and shape[1] > 1):
         raise ValueError(f"{name} must be (batch, dim) with dim stride 1")
-    return t.data_ptr(), t.stride(0)
+    return t.data_ptr(), st[0]
 
 
 def gated_state_update(state, x, gate_a, gate_x, lam, c=8.0, slots=None, out=None, stream=None):
@@ -1050,21 +1069,23 @@ def gated_state_update(state, x, gate_a, gate_x, lam, c=8.0, slots=None, out=Non
     torch = _torch()
     if state.dim() != 2 or x.dim() != 2:
         raise ValueError("state must be (nslots, dim) and x (batch, dim)")
-    (nslots, dim), batch, dev, io = state.shape, x.shape[0], state.device, x.dtype
     code = _io_code(x)
-    _check_dev("state", state, dev, torch.float32)
-    if dim > 1 and state.stride(1) != 1:
+    (nslots, dim), dev, io = state.shape, _gpu("state", state), x.dtype
+    shape = (x.shape[0], dim)
+    _placed("state", state, torch.float32, dev)
+    pool = state.stride()
+    if dim > 1 and pool[1] != 1:
         raise ValueError("state must have dim stride 1")
-    inputs = _row_tokens("x", x, batch, dim, io, dev) + _row_tokens("gate_a", gate_a, batch, dim, io, dev) + \
-        _row_tokens("gate_x", gate_x, batch, dim, io, dev)
+    inputs = _row_tokens("x", x, shape, io, dev) + _row_tokens("gate_a", gate_a, shape, io, dev) + \
+        _row_tokens("gate_x", gate_x, shape, io, dev)
     lam_p = _fp32("lam", lam, (dim,), dev)
-    _check_slots(slots, batch, nslots, dev)
+    _check_slots(slots, shape[0], nslots, dev)
     c = _decay_constant(c)
     with _on(dev, stream) as s:
         if out is None:
-            out = torch.empty((batch, dim), dtype=io, device=dev)
-        a = GatedUpdateArgs(batch, nslots, dim, code, c, state.data_ptr(), state.stride(0), *inputs, lam_p, _ptr(slots),
-                            *_row_tokens("out", out, batch, dim, io, dev))
+            out = _empty(x, shape, io, dev)
+        a = GatedUpdateArgs(shape[0], nslots, dim, code, c, state.data_ptr(), pool[0], *inputs, lam_p, _ptr(slots),
+                            *_row_tokens("out", out, shape, io, dev))
         _launch("ssm_gated_state_update", a, s)
     return out
 
@@ -1089,31 +1110,31 @@ def _inner_contiguous(t):
     return t.shape[0] == 0 or t[0].is_contiguous()
 
 
-def _cache_fields(codes, scales, shape, format):
+def _cache_fields(codes, scales, shape, format, device):
     """Pointers and slot strides of a cache's two tensors, for states of a shape."""
-    uint8, dev = _torch().uint8, codes.device
-    fields = ()
-    for name, t, want in zip(("codes", "scales"), (codes, scales),
-                             state_cache_shape(codes.shape[0] if codes.dim() else 0, shape, format)):
-        _check_dev(name, t, dev, uint8)
-        if t.shape != want:
-            raise ValueError(f"{name} must have shape {want} for this state and format, got {tuple(t.shape)}")
+    uint8 = _torch().uint8
+    want = state_cache_shape(codes.shape[0] if codes.dim() else 0, shape, format)
+    for name, t, w in (("codes", codes, want[0]), ("scales", scales, want[1])):
+        _placed(name, t, uint8, device)
+        if t.shape != w:
+            raise ValueError(f"{name} must have shape {w} for this state and format, got {tuple(t.shape)}")
         if not t.is_contiguous() and not _inner_contiguous(t):
             raise ValueError(f"{name} must be contiguous within a slot")
-        fields += (t.data_ptr(), t.stride(0))
-    return fields
+    return codes.data_ptr(), codes.stride(0), scales.data_ptr(), scales.stride(0)
 
 
 def _cache_args(codes, scales, states, slots, format):
-    if states.dim() < 2:
+    dev, shape = _gpu("codes", codes), states.shape
+    if len(shape) < 2:
         raise ValueError("states must be (batch, ...)")
-    dev, shape, nslots = codes.device, states.shape, codes.shape[0] if codes.dim() else 0
-    fields = _cache_fields(codes, scales, shape[1:], format)
-    _check_dev("states", states, dev, states.dtype)
+    fields = _cache_fields(codes, scales, shape[1:], format, dev)
+    code = _io_code(states)
+    _placed("states", states, states.dtype, dev)
     if not states.is_contiguous() and not _inner_contiguous(states):
         raise ValueError("states must be contiguous within a batch row")
+    nslots = codes.shape[0]
     _check_slots(slots, shape[0], nslots, dev)
-    return StateCacheArgs(shape[0], nslots, math.prod(shape[1:-1]), shape[-1], CACHE_FORMATS[format], _io_code(states),
+    return StateCacheArgs(shape[0], nslots, math.prod(shape[1:-1]), shape[-1], CACHE_FORMATS[format], code,
                           *fields, states.data_ptr(), states.stride(0), _ptr(slots))
 
 
@@ -1126,7 +1147,7 @@ def state_cache_write(codes, scales, states, slots=None, format="int8", stream=N
     not written; of rows naming the same slot the last is.  A block with a NaN
     or an infinity reads back as NaN."""
     a = _cache_args(codes, scales, states, slots, format)
-    with _on(codes.device, stream) as s:
+    with _on(codes.get_device(), stream) as s:
         _launch("ssm_state_cache_write", a, s)
 
 
@@ -1139,13 +1160,14 @@ def state_cache_read(codes, scales, slots=None, format="int8", dtype=None, out=N
         raise ValueError("codes must be (nslots, ...)")
     if format not in CACHE_FORMATS:
         raise ValueError(f"format must be one of {sorted(CACHE_FORMATS)}")
+    dev = _gpu("codes", codes)
     batch = codes.shape[0] if slots is None else slots.shape[0]
     shape = (batch,) + tuple(codes.shape[1:-1]) + (codes.shape[-1] * (2 if format == "fp4" else 1),)
     if out is not None and (tuple(out.shape) != shape or (dtype is not None and out.dtype != dtype)):
         raise ValueError(f"out must have shape {shape} and the dtype asked for")
-    with _on(codes.device, stream) as s:
+    with _on(dev, stream) as s:
         if out is None:
-            out = torch.empty(shape, dtype=dtype or torch.float32, device=codes.device)
+            out = torch.empty(shape, dtype=dtype or torch.float32, device=dev)
         _launch("ssm_state_cache_read", _cache_args(codes, scales, out, slots, format), s)
     return out
 
@@ -1165,31 +1187,32 @@ def selective_state_update_cached(codes, scales, x, dt, A, B, C, D=None, z=None,
     torch = _torch()
     if codes.dim() != 3 or x.dim() != 2:
         raise ValueError("codes must be (nslots, dim, dstate) and x (batch, dim)")
-    (nslots, dim, N), batch, dev, io = codes.shape, x.shape[0], codes.device, x.dtype
     code = _io_code(x)
-    held = _cache_fields(codes, scales, (dim, N), "int8")
-    inputs = _row_tokens("x", x, batch, dim, io, dev) + _row_tokens("dt", dt, batch, dim, io, dev) + \
-        _row_tokens("z", z, batch, dim, io, dev)
+    (nslots, dim, N), dev, io = codes.shape, _gpu("codes", codes), x.dtype
+    shape = (x.shape[0], dim)
+    held = _cache_fields(codes, scales, (dim, N), "int8", dev)
+    inputs = _row_tokens("x", x, shape, io, dev) + _row_tokens("dt", dt, shape, io, dev) + \
+        _row_tokens("z", z, shape, io, dev)
     for name, t in (("B", B), ("C", C)):
-        _check_dev(name, t, dev, io)
+        _placed(name, t, io, dev)
         if N > 1 and t.stride(-1) != 1:
             raise ValueError(f"{name} must have state stride 1")
-    G = _bc_groups(B, C, batch, dim, N, ())
-    _check_dev("A", A, dev, torch.float32)
+    G = _bc_groups(B, C, shape[0], dim, N, ())
+    _placed("A", A, torch.float32, dev)
     if A.shape != (dim, N) or (N > 1 and A.stride(1) != 1):
         raise ValueError("A must be (dim, dstate) with state stride 1")
     D_p, bias_p = _fp32("D", D, (dim,), dev), _fp32("dt_bias", dt_bias, (dim,), dev)
-    _check_slots(slots, batch, nslots, dev)
+    _check_slots(slots, shape[0], nslots, dev)
     if seed is not None:
-        _check_dev("seed", seed, dev, torch.int64)
+        _placed("seed", seed, torch.int64, dev)
         if seed.numel() != 1:
             raise ValueError("seed must hold one int64")
     with _on(dev, stream) as s:
         if out is None:
-            out = torch.empty((batch, dim), dtype=io, device=dev)
-        a = CachedUpdateArgs(batch, nslots, dim, N, code, bool(dt_softplus), *held, *inputs,
+            out = _empty(x, shape, io, dev)
+        a = CachedUpdateArgs(shape[0], nslots, dim, N, code, bool(dt_softplus), *held, *inputs,
                              B.data_ptr(), B.stride(0), B.stride(1) if G else 0,
                              C.data_ptr(), C.stride(0), C.stride(1) if G else 0, A.data_ptr(), A.stride(0), D_p, bias_p,
-                             *_row_tokens("out", out, batch, dim, io, dev), _ptr(slots), _ptr(seed), G)
+                             *_row_tokens("out", out, shape, io, dev), _ptr(slots), _ptr(seed), G)
         _launch("ssm_selective_state_update_cached", a, s)
     return out
