@@ -255,7 +255,7 @@ __global__ __launch_bounds__(kThreads) void cached_update_kernel(CachedParams p)
 
   for (int b = row;;) {
     float dl = dtv + bias;
-    if (p.softplus) dl = softplus_f32(dl);
+    if (p.softplus) dl = softplus_close_f32(dl);
     float y = fmaf(Dd, xv, ch.step(p, b, g, d, a, dl, xv, seed));
     if (p.z) y *= silu_f32(zv);
     if (live) io<T>::store(out + b * p.ob, y);

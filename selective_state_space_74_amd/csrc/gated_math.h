@@ -31,7 +31,7 @@ __device__ __forceinline__ float one_minus_square(float a, float u) {
 struct Rate {
   float s, log2a, u;
   __device__ __forceinline__ Rate() {}
-  __device__ __forceinline__ Rate(float c, float lam) : s(c * softplus_f32(lam)), log2a(-s * kLog2e), u(2.0f * s) {}
+  __device__ __forceinline__ Rate(float c, float lam) : s(c * softplus_close_f32(lam)), log2a(-s * kLog2e), u(2.0f * s) {}
 };
 
 }  // namespace ssm

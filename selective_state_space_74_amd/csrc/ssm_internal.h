@@ -75,6 +75,20 @@ __device__ __forceinline__ float softplus_f32(float x) {
   return fmaxf(x, 0.0f) + lp;
 }
 
+// softplus_f32 with two of its roundings mended: what the product |x| log2 e
+// loses (up to |x| 2^-24 of the exponential) and the second order of e.  Over
+// step sizes of 0.001 to 0.1 its error is 0.97 2^-24 (rms), softplus_f32's 2.7.
+// For kernels that take one a channel, whose states or tokens all get its error.
+constexpr float kLog2eRest = 1.92596298909109e-08f;   // log2 e - kLog2e
+__device__ __forceinline__ float softplus_close_f32(float x) {
+  const float v = -fabsf(x), t = v * kLog2e;
+  const float rest = fmaf(v, kLog2eRest, fmaf(v, kLog2e, -t));
+  const float y0 = __builtin_amdgcn_exp2f(t), y = v >= -128.0f ? fmaf(y0, rest * kLn2, y0) : y0;
+  const float u = 1.0f + y;
+  const float e = y - (u - 1.0f);
+  return fmaxf(x, 0.0f) + fmaf(__builtin_amdgcn_logf(u), kLn2, fmaf(-e, y, e));
+}
+
 // silu(z) = z * sigmoid(z) = z / (1 + 2^(-z log2 e))
 __device__ __forceinline__ float silu_f32(float z) {
   return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-z * kLog2e));
