@@ -81,24 +81,31 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams 
     P[v] = 1.0f;
     Q[v] = 0.0f;
   }
-  // Wavefronts of 16 tokens of one sequence, none of them its first or last,
-  // take a path without branches; the others ask for their tokens' marks, which
-  // one load brings, as scalars.  (Fetching the rows before the marks that
-  // decide the path are known measured slower, 314 us against 295 us for forward
-  // and backward of 30,011 x 1536 bf16: the rows' uses then wait together.)
+  // Packed rows: the tokens' marks.  A wavefront of more than 32 channels has
+  // them in scalars, a bit a token, and branches over what a sequence's first or
+  // last token and a token in none ask for; a narrow one, whose stretches differ,
+  // takes a path without branches where none of its tokens is marked.
+  constexpr bool BITS = PACKED && !NARROW;
+  uint32_t firsts = 0, lasts = 0, outs = 0;
   int32_t marks = 0, each[NARROW ? kTok : 1];
   auto mark_at = [&](int64_t t) {
     const int32_t m = p.marks[t];
     return m >> 2 < p.nseq ? m : kOutside;
   };
-  if constexpr (PACKED && !NARROW) marks = some ? mark_at(t0 + lane % kTok) : kOutside;
+  if constexpr (BITS) {
+    marks = some ? mark_at(t0 + lane % kTok) : kOutside;
+    firsts = static_cast<uint32_t>(__ballot(marks & 1));
+    outs = static_cast<uint32_t>(__ballot(marks < 0));
+    lasts = static_cast<uint32_t>(__ballot(marks & 2)) & ~outs;
+  }
+  auto bit = [](uint32_t of, int j) { return (of >> j & 1) != 0; };
   if constexpr (PACKED && NARROW)
     for (int i = c; i < n; i += width) marks |= mark_at(t0 + i);   // kOutside sets every bit
   auto mark = [&](int j) { return NARROW ? each[NARROW ? j : 0] : __builtin_amdgcn_readlane(marks, j); };
 
   auto tokens = [&](auto every) {
     constexpr bool PLAIN = decltype(every)::value;
-    constexpr bool MARKED = PACKED && !PLAIN;
+    constexpr bool MARKED = NARROW && PACKED && !PLAIN;
     uint32_t rx[kTok], ra[kTok], rg[kTok], rd[kTok];
     const TokenRows tx = token_rows<T>(p.x, b * p.xb + wave_t0 * p.xs, p.xs, p.D, subs),
                     ta = token_rows<T>(p.ga, b * p.gab + wave_t0 * p.gas, p.gas, p.D, subs),
@@ -111,13 +118,21 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams 
     for (int j = 0; j < kTok; ++j) {
       const int jj = PLAIN || NARROW ? j : min(j, n - 1);
       const bool in = PLAIN || !NARROW || j < n;
-      ra[j] = ta.load<kBytes, CACHE>(jj, in ? at(p.gas) : kNowhere);
-      rg[j] = tg.load<kBytes, CACHE>(jj, in ? at(p.gxs) : kNowhere);
-      rx[j] = tx.load<kBytes, CACHE>(jj, in ? at(p.xs) : kNowhere);
-      rd[j] = td.load<kBytes, CACHE>(jj, in ? at(p.dos) : kNowhere);
+      const bool none = BITS && bit(outs, j);
+      ra[j] = ta.load<kBytes, CACHE>(jj, in ? at(p.gas) : kNowhere, none);
+      rg[j] = tg.load<kBytes, CACHE>(jj, in ? at(p.gxs) : kNowhere, none);
+      rx[j] = tx.load<kBytes, CACHE>(jj, in ? at(p.xs) : kNowhere, none);
+      rd[j] = td.load<kBytes, CACHE>(jj, in ? at(p.dos) : kNowhere, none);
     }
 #pragma unroll
     for (int j = 0; j < kTok; ++j) {
+      if constexpr (BITS) {
+        if (bit(firsts, j)) [[unlikely]] {
+#pragma unroll
+          for (int v = 0; v < V; ++v)
+            h[v] = !bit(outs, j) && p.h0 ? p.h0[static_cast<int64_t>(mark(j) >> 2) * p.D + d + v] : 0.0f;
+        }
+      }
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         if constexpr (MARKED) {
@@ -145,25 +160,41 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams 
           if (mark(j) >= 0 && (mark(j) & 2) && p.dlast)
             dout[j][v] += p.dlast[static_cast<int64_t>(mark(j) >> 2) * p.D + d + v];
         }
-        if constexpr (!PLAIN) {
+        if constexpr (!PLAIN && !BITS) {
           a[j][v] = j < n ? a[j][v] : 1.0f;
           dout[j][v] = j < n ? dout[j][v] : 0.0f;
         }
       }
+      if constexpr (BITS) {
+        if (bit(outs | lasts, j)) [[unlikely]] {
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            if (bit(outs, j)) a[j][v] = fx[j][v] = fg[j][v] = fl[j][v] = fa[j][v] = 0.0f;
+            else if (p.dlast) dout[j][v] += p.dlast[static_cast<int64_t>(mark(j) >> 2) * p.D + d + v];
+          }
+        }
+      }
     }
 #pragma unroll
-    for (int j = kTok - 1; j >= 0; --j)
+    for (int j = kTok - 1; j >= 0; --j) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         P[v] *= a[j][v];
         Q[v] = MARKED && (mark(j) & 1) && (PLAIN || j < n) ? 0.0f : a[j][v] * (dout[j][v] + Q[v]);
       }
+      if constexpr (BITS) {
+        if (bit(firsts, j)) [[unlikely]] {
+#pragma unroll
+          for (int v = 0; v < V; ++v) Q[v] = 0.0f;
+        }
+      }
+    }
   };
   bool plain;
   if constexpr (NARROW) plain = __all(n == kTok) && !__any(marks < 0 || (marks & 3));
-  else plain = n == kTok && (!PACKED || __ballot(marks < 0 || (marks & 3)) == 0);
+  else plain = BITS ? some : n == kTok;
   if (plain) tokens(std::true_type{});
-  if (!plain && some) {
+  if (!BITS && !plain && some) {
     if constexpr (PACKED && NARROW) {
 #pragma unroll
       for (int j = 0; j < kTok; ++j) each[j] = j < n ? mark_at(t0 + j) : kOutside;
@@ -174,7 +205,7 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams 
     tokens(std::false_type{});
   }
   if constexpr (PACKED) {
-    if (NARROW ? !plain && (marks & 1) : some && __ballot(marks & 1)) {
+    if (NARROW ? !plain && (marks & 1) : some && firsts) {
 #pragma unroll
       for (int v = 0; v < V; ++v) P[v] = kCut;
     }
@@ -221,7 +252,7 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams 
                     dgx = token_rows<T>(p.dgx, b * p.dgxb + wave_t0 * p.dgxs, p.dgxs, p.D, subs);
     auto outputs = [&](auto every) {
       constexpr bool PLAIN = decltype(every)::value;
-      constexpr bool MARKED = PACKED && !PLAIN;
+      constexpr bool MARKED = NARROW && PACKED && !PLAIN;
 #pragma unroll
       for (int j = kTok - 1; j >= 0; --j) {
         if (!PLAIN && !NARROW && j >= n) continue;
@@ -242,14 +273,24 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams 
             }
           }
         }
+        if constexpr (BITS) {
+          if (bit(firsts, j)) [[unlikely]] {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+              if (!bit(outs, j) && p.dh0 && live) p.dh0[static_cast<int64_t>(mark(j) >> 2) * p.D + d + v] = e[v];
+              e[v] = 0.0f;
+            }
+          }
+        }
         const bool write = PLAIN || !NARROW || j < n;
-        dx.store<kBytes, CACHE>(j, write ? at(p.dxs) : kNowhere, narrow<T, V>(ox));
-        dga.store<kBytes, CACHE>(j, write ? at(p.dgas) : kNowhere, narrow<T, V>(oa));
-        dgx.store<kBytes, CACHE>(j, write ? at(p.dgxs) : kNowhere, narrow<T, V>(og));
+        const bool past = BITS && j >= n;
+        dx.store<kBytes, CACHE>(j, write ? at(p.dxs) : kNowhere, narrow<T, V>(ox), past);
+        dga.store<kBytes, CACHE>(j, write ? at(p.dgas) : kNowhere, narrow<T, V>(oa), past);
+        dgx.store<kBytes, CACHE>(j, write ? at(p.dgxs) : kNowhere, narrow<T, V>(og), past);
       }
     };
     if (plain) outputs(std::true_type{});
-    else outputs(std::false_type{});
+    else if constexpr (!BITS) outputs(std::false_type{});
     if constexpr (!PACKED) {
       if (p.dh0 && live && t0 == 0 && n > 0) {
 #pragma unroll

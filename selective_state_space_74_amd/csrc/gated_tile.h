@@ -256,18 +256,19 @@ struct TokenRows {
     stride = row_stride * static_cast<int64_t>(sizeof(T));
     bytes = static_cast<uint32_t>((subs - 1) * kWaveTokens * stride + D * static_cast<int64_t>(sizeof(T)));
   }
-  __device__ __forceinline__ __amdgpu_buffer_rsrc_t row(int j) const {
-    return __builtin_amdgcn_make_buffer_rsrc(first + j * stride, 0, static_cast<int>(bytes), kRsrcWord3);
+  // none: a row of no bytes
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t row(int j, bool none) const {
+    return __builtin_amdgcn_make_buffer_rsrc(first + j * stride, 0, none ? 0 : static_cast<int>(bytes), kRsrcWord3);
   }
   template <int BYTES, int CACHE>
-  __device__ __forceinline__ uint32_t load(int j, uint32_t at) const {
-    if constexpr (BYTES == 4) return __builtin_amdgcn_raw_buffer_load_b32(row(j), at, 0, CACHE);
-    else return __builtin_amdgcn_raw_buffer_load_b16(row(j), at, 0, CACHE);
+  __device__ __forceinline__ uint32_t load(int j, uint32_t at, bool none = false) const {
+    if constexpr (BYTES == 4) return __builtin_amdgcn_raw_buffer_load_b32(row(j, none), at, 0, CACHE);
+    else return __builtin_amdgcn_raw_buffer_load_b16(row(j, none), at, 0, CACHE);
   }
   template <int BYTES, int CACHE>
-  __device__ __forceinline__ void store(int j, uint32_t at, uint32_t v) const {
-    if constexpr (BYTES == 4) __builtin_amdgcn_raw_buffer_store_b32(v, row(j), at, 0, CACHE);
-    else __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(v), row(j), at, 0, CACHE);
+  __device__ __forceinline__ void store(int j, uint32_t at, uint32_t v, bool none = false) const {
+    if constexpr (BYTES == 4) __builtin_amdgcn_raw_buffer_store_b32(v, row(j, none), at, 0, CACHE);
+    else __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(v), row(j, none), at, 0, CACHE);
   }
 };
 template <typename T>
