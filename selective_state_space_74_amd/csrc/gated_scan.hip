@@ -78,9 +78,10 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_fwd_kernel(FwdParams p) 
   }
   // Wavefronts of 16 tokens of one sequence, none of them its first or last,
   // take a path without branches; the others ask for their tokens' marks, which
-  // one load brings, as scalars.  (Fetching the rows before the marks that
-  // decide the path are known measured slower, 314 us against 295 us for forward
-  // and backward of 30,011 x 1536 bf16: the rows' uses then wait together.)
+  // one load brings, as scalars.  (One path with a branch a token, as in the
+  // backward, measured slower here: 598 us against 574 at 262144 x 1536 bf16.
+  // So did fetching the rows before the marks that decide the path are known:
+  // the rows' uses then wait together.)
   int32_t marks = 0, each[NARROW ? kWaveTokens : 1];
   auto mark_at = [&](int64_t t) {
     const int32_t m = p.marks[t];

@@ -81,18 +81,21 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams 
     P[v] = 1.0f;
     Q[v] = 0.0f;
   }
-  // Packed rows: the tokens' marks.  A wavefront of more than 32 channels has
-  // them in scalars, a bit a token, and branches over what a sequence's first or
-  // last token and a token in none ask for; a narrow one, whose stretches differ,
-  // takes a path without branches where none of its tokens is marked.
-  constexpr bool BITS = PACKED && !NARROW;
+  // Which tokens are a sequence's first or last, or in none (past the end of the
+  // row, or of every packed sequence): a bit each, in scalars, and a branch over
+  // what such a token asks for.  (With a path of its own for wavefronts that hold
+  // any, 30,011 x 1536 bf16 packed from 64 sequences took 190 us, and from one 161;
+  // now 151 and 151: its code came from memory, and registers were spilled.)  In
+  // a narrow call, whose stretches differ, wavefronts without such tokens do take
+  // a path of their own.
   uint32_t firsts = 0, lasts = 0, outs = 0;
   int32_t marks = 0, each[NARROW ? kTok : 1];
   auto mark_at = [&](int64_t t) {
     const int32_t m = p.marks[t];
     return m >> 2 < p.nseq ? m : kOutside;
   };
-  if constexpr (BITS) {
+  if constexpr (!NARROW && !PACKED) outs = ~0u << n;
+  if constexpr (!NARROW && PACKED) {
     marks = some ? mark_at(t0 + lane % kTok) : kOutside;
     firsts = static_cast<uint32_t>(__ballot(marks & 1));
     outs = static_cast<uint32_t>(__ballot(marks < 0));
@@ -116,17 +119,15 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams 
     for (int v = 0; v < V; ++v) h[v] = p.ck[(b * p.nck + (NARROW ? min(t0 / kGatedCkpt, p.nck - 1) : t0 / kGatedCkpt)) * p.D + d + v];
 #pragma unroll
     for (int j = 0; j < kTok; ++j) {
-      const int jj = PLAIN || NARROW ? j : min(j, n - 1);
-      const bool in = PLAIN || !NARROW || j < n;
-      const bool none = BITS && bit(outs, j);
-      ra[j] = ta.load<kBytes, CACHE>(jj, in ? at(p.gas) : kNowhere, none);
-      rg[j] = tg.load<kBytes, CACHE>(jj, in ? at(p.gxs) : kNowhere, none);
-      rx[j] = tx.load<kBytes, CACHE>(jj, in ? at(p.xs) : kNowhere, none);
-      rd[j] = td.load<kBytes, CACHE>(jj, in ? at(p.dos) : kNowhere, none);
+      const bool in = !NARROW || PLAIN || j < n, none = !NARROW && bit(outs, j);
+      ra[j] = ta.load<kBytes, CACHE>(j, in ? at(p.gas) : kNowhere, none);
+      rg[j] = tg.load<kBytes, CACHE>(j, in ? at(p.gxs) : kNowhere, none);
+      rx[j] = tx.load<kBytes, CACHE>(j, in ? at(p.xs) : kNowhere, none);
+      rd[j] = td.load<kBytes, CACHE>(j, in ? at(p.dos) : kNowhere, none);
     }
 #pragma unroll
     for (int j = 0; j < kTok; ++j) {
-      if constexpr (BITS) {
+      if constexpr (!NARROW && PACKED) {
         if (bit(firsts, j)) [[unlikely]] {
 #pragma unroll
           for (int v = 0; v < V; ++v)
@@ -160,17 +161,19 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams 
           if (mark(j) >= 0 && (mark(j) & 2) && p.dlast)
             dout[j][v] += p.dlast[static_cast<int64_t>(mark(j) >> 2) * p.D + d + v];
         }
-        if constexpr (!PLAIN && !BITS) {
+        if constexpr (!PLAIN) {
           a[j][v] = j < n ? a[j][v] : 1.0f;
           dout[j][v] = j < n ? dout[j][v] : 0.0f;
         }
       }
-      if constexpr (BITS) {
+      if constexpr (!NARROW) {
         if (bit(outs | lasts, j)) [[unlikely]] {
 #pragma unroll
           for (int v = 0; v < V; ++v) {
-            if (bit(outs, j)) a[j][v] = fx[j][v] = fg[j][v] = fl[j][v] = fa[j][v] = 0.0f;
-            else if (p.dlast) dout[j][v] += p.dlast[static_cast<int64_t>(mark(j) >> 2) * p.D + d + v];
+            if (bit(outs, j)) {   // dout was read as 0
+              a[j][v] = PACKED ? 0.0f : 1.0f;
+              fx[j][v] = fg[j][v] = fl[j][v] = fa[j][v] = 0.0f;
+            } else if (p.dlast) dout[j][v] += p.dlast[static_cast<int64_t>(mark(j) >> 2) * p.D + d + v];
           }
         }
       }
@@ -182,7 +185,7 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams 
         P[v] *= a[j][v];
         Q[v] = MARKED && (mark(j) & 1) && (PLAIN || j < n) ? 0.0f : a[j][v] * (dout[j][v] + Q[v]);
       }
-      if constexpr (BITS) {
+      if constexpr (!NARROW && PACKED) {
         if (bit(firsts, j)) [[unlikely]] {
 #pragma unroll
           for (int v = 0; v < V; ++v) Q[v] = 0.0f;
@@ -190,19 +193,19 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams 
       }
     }
   };
-  bool plain;
-  if constexpr (NARROW) plain = __all(n == kTok) && !__any(marks < 0 || (marks & 3));
-  else plain = BITS ? some : n == kTok;
+  const bool plain = NARROW ? __all(n == kTok) && !__any(marks < 0 || (marks & 3)) : some;
   if (plain) tokens(std::true_type{});
-  if (!BITS && !plain && some) {
-    if constexpr (PACKED && NARROW) {
+  if constexpr (NARROW) {
+    if (!plain && some) {
+      if constexpr (PACKED) {
 #pragma unroll
-      for (int j = 0; j < kTok; ++j) each[j] = j < n ? mark_at(t0 + j) : kOutside;
-      marks = 0;   // of the lane's own stretch now
+        for (int j = 0; j < kTok; ++j) each[j] = j < n ? mark_at(t0 + j) : kOutside;
+        marks = 0;   // of the lane's own stretch now
 #pragma unroll
-      for (int j = 0; j < kTok; ++j) marks |= j < n ? each[j] : 0;
+        for (int j = 0; j < kTok; ++j) marks |= j < n ? each[j] : 0;
+      }
+      tokens(std::false_type{});
     }
-    tokens(std::false_type{});
   }
   if constexpr (PACKED) {
     if (NARROW ? !plain && (marks & 1) : some && firsts) {
@@ -255,11 +258,11 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams 
       constexpr bool MARKED = NARROW && PACKED && !PLAIN;
 #pragma unroll
       for (int j = kTok - 1; j >= 0; --j) {
-        if (!PLAIN && !NARROW && j >= n) continue;
+        if (!NARROW && !PACKED && bit(outs, j)) continue;
         float ox[V], oa[V], og[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          const bool in = (!MARKED || mark(j) >= 0) && (PLAIN || !NARROW || j < n);
+          const bool in = (!MARKED || mark(j) >= 0) && (PLAIN || j < n);
           const float et = dout[j][v] + e[v];
           ox[v] = in ? et * fx[j][v] : 0.0f;
           og[v] = in ? et * fg[j][v] : 0.0f;
@@ -273,7 +276,7 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams 
             }
           }
         }
-        if constexpr (BITS) {
+        if constexpr (!NARROW && PACKED) {
           if (bit(firsts, j)) [[unlikely]] {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
@@ -282,15 +285,14 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams 
             }
           }
         }
-        const bool write = PLAIN || !NARROW || j < n;
-        const bool past = BITS && j >= n;
+        const bool write = !NARROW || PLAIN || j < n, past = !NARROW && PACKED && j >= n;
         dx.store<kBytes, CACHE>(j, write ? at(p.dxs) : kNowhere, narrow<T, V>(ox), past);
         dga.store<kBytes, CACHE>(j, write ? at(p.dgas) : kNowhere, narrow<T, V>(oa), past);
         dgx.store<kBytes, CACHE>(j, write ? at(p.dgxs) : kNowhere, narrow<T, V>(og), past);
       }
     };
     if (plain) outputs(std::true_type{});
-    else if constexpr (!BITS) outputs(std::false_type{});
+    else if constexpr (NARROW) outputs(std::false_type{});
     if constexpr (!PACKED) {
       if (p.dh0 && live && t0 == 0 && n > 0) {
 #pragma unroll
