@@ -34,7 +34,8 @@ template <typename T, int V, bool PACKED, bool CHAIN, bool NARROW, int CACHE>
 __global__ __launch_bounds__(64 * kMaxWaves) void gated_fwd_kernel(FwdParams p) {
   constexpr int W = 64 * V;
   __shared__ float2 pairs[kMaxWaves][W];
-  __shared__ ChainShared<CHAIN ? W : 1> before;
+  constexpr int kGroup = chain_group(NARROW);
+  __shared__ ChainShared<CHAIN ? W : 1, kGroup> before;
   __shared__ uint32_t taken;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -165,13 +166,13 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_fwd_kernel(FwdParams p) 
   float h[V];
   if constexpr (CHAIN) {
     // the words of (row, col): tiles, then groups
-    const int64_t ngroups = (p.tiles + kChainGroup - 1) / kChainGroup;
+    const int64_t ngroups = (p.tiles + kGroup - 1) / kGroup;
     uint64_t* const base = p.words + (static_cast<int64_t>(row) * p.cols + col) * (p.tiles + ngroups) * width;
     const Chain chain{base, base + static_cast<int64_t>(p.tiles) * width, width};
     // thread i of the first 2^shift has channel i of the group
     const int64_t di = min(static_cast<int64_t>(col) * W + (threadIdx.x & (width - 1)), p.D - 1);
     const float first = !PACKED && p.h0 ? p.h0[b * p.D + di] : 0.0f;
-    chain_carry<PACKED, W, NARROW ? kMineNarrow : kMine * V>(chain, tile, p.tiles, pairs, before, shift, first,
+    chain_carry<PACKED, W, kGroup, chain_mine(NARROW, V)>(chain, tile, p.tiles, pairs, before, shift, first,
                                                              [](int w) { return w; });
 #pragma unroll
     for (int v = 0; v < V; ++v) h[v] = before.entering[c * V + v];

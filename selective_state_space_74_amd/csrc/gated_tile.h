@@ -7,7 +7,7 @@
 // has to travel to the tiles after it.
 //
 // The carry.  Tiles are numbered along the scan (backwards in time for the
-// adjoint) and every kChainGroup of them form a group.  A tile publishes its
+// adjoint) and every chain_group() of them form a group.  A tile publishes its
 // (P, H) as soon as it has them, without waiting for anything.  It then takes
 // the state that left the group before, and folds the (P, H) of its
 // predecessors within the group into it; the last tile of a group
@@ -39,11 +39,19 @@ namespace ssm {
 
 constexpr int kWaveTokens = 16;   // tokens of a wavefront (the backward with two channels a lane: 8)
 constexpr int kMaxWaves = 8;
-constexpr int kChainGroup = 16;
-// Words of predecessors that a thread fetches at most: with 64 channels the
-// workgroup has 8 threads a channel; narrow calls have 16 or more.
-constexpr int kMine = (kChainGroup - 1 + kMaxWaves - 1) / kMaxWaves;
-constexpr int kMineNarrow = (kChainGroup - 1 + 2 * kMaxWaves - 1) / (2 * kMaxWaves);
+// Tiles of a group.  A call of few channels is one chain, which the way from
+// group to group bounds, so narrow calls have longer ones: 2,052,244 x 31 bf16
+// takes 249 us forward with 32 tiles and 355 with 16 (64: 225, but from 8 packed
+// sequences 265 as with 32, and the backward 431 against 388).  Elsewhere the
+// words to fetch count: 16 / 32 / 64 tiles 372 / 403 / 572 us at 4 x 4096 x 5120
+// bf16 training.
+constexpr int chain_group(bool narrow) { return narrow ? 32 : 16; }
+// Words of predecessors that a thread fetches at most: the workgroup has 8 / V
+// threads a channel, 16 or more in a narrow call.
+constexpr int chain_mine(bool narrow, int V) {
+  const int parts = narrow ? 2 * kMaxWaves : kMaxWaves / V;
+  return (chain_group(narrow) - 1 + parts - 1) / parts;
+}
 constexpr uint64_t kNoWord = ~uint64_t{0};
 
 __device__ __forceinline__ uint64_t chain_word(float p, float h) {
@@ -98,9 +106,9 @@ struct Chain {
 };
 
 // What a workgroup keeps of the tiles before it, and the state entering it.
-template <int W>
+template <int W, int GROUP>
 struct ChainShared {
-  float2 tiles[kChainGroup - 1][W];
+  float2 tiles[GROUP - 1][W];
   float entering[W];
 };
 
@@ -115,13 +123,13 @@ struct ChainShared {
 // are folded into one pair, and the tile's own wavefronts into another, before
 // the state that left the group before is asked for: from group to group the
 // carry costs one product, one read and one write.
-template <bool PACKED, int W, int MINE, typename Order>
+template <bool PACKED, int W, int GROUP, int MINE, typename Order>
 __device__ __forceinline__ void chain_carry(const Chain& c, int64_t k, int64_t ntiles, float2 (&pairs)[kMaxWaves][W],
-                                            ChainShared<W>& sh, int shift, float first, Order order) {
+                                            ChainShared<W, GROUP>& sh, int shift, float first, Order order) {
   const int parts = (64 * kMaxWaves) >> shift;
   const int ch = threadIdx.x & ((1 << shift) - 1), part = threadIdx.x >> shift;
-  const int in_group = static_cast<int>(k % kChainGroup);
-  const int64_t group = k / kChainGroup;
+  const int in_group = static_cast<int>(k % GROUP);
+  const int64_t group = k / GROUP;
   uint64_t* const mine = c.tiles + k * c.width + ch;
   float2 own = make_float2(1.0f, 0.0f);
   if (part == 0) {
@@ -130,7 +138,7 @@ __device__ __forceinline__ void chain_carry(const Chain& c, int64_t k, int64_t n
       const float2 q = pairs[order(w)][ch];
       own = make_float2(chain_product<PACKED>(own.x, q.x), chain_apply<PACKED>(q.x, q.y, own.y));
     }
-    if (in_group != kChainGroup - 1) chain_store(mine, chain_word(own.x, own.y));
+    if (in_group != GROUP - 1) chain_store(mine, chain_word(own.x, own.y));
   }
   uint64_t w[MINE];
 #pragma unroll
@@ -148,7 +156,7 @@ __device__ __forceinline__ void chain_carry(const Chain& c, int64_t k, int64_t n
   if (part == 0) {
     float2 q = make_float2(1.0f, 0.0f);   // of the group's tiles before this one
 #pragma unroll
-    for (int j = 0; j < kChainGroup - 1; ++j) {
+    for (int j = 0; j < GROUP - 1; ++j) {
       if (j < in_group) {
         const float2 t = sh.tiles[j][ch];
         q = make_float2(chain_product<PACKED>(q.x, t.x), chain_apply<PACKED>(t.x, t.y, q.y));
@@ -156,7 +164,7 @@ __device__ __forceinline__ void chain_carry(const Chain& c, int64_t k, int64_t n
     }
     uint64_t* const left = c.groups + (group - 1) * c.width + ch;
     const float h = chain_apply<PACKED>(q.x, q.y, group > 0 ? word_h(chain_wait(left, chain_load(left))) : first);
-    if (in_group == kChainGroup - 1 && k + 1 < ntiles)
+    if (in_group == GROUP - 1 && k + 1 < ntiles)
       chain_store(c.groups + group * c.width + ch, chain_word(0.0f, chain_apply<PACKED>(own.x, own.y, h)));
     sh.entering[ch] = h;
   }
@@ -301,7 +309,8 @@ inline GatedPlan gated_plan(int64_t batch, int64_t L, int64_t D, bool packed, in
   q.waves = static_cast<int>(wave_blocks < 1 ? 1 : wave_blocks < kMaxWaves ? wave_blocks : kMaxWaves);
   q.tiles = (wave_blocks + q.waves - 1) / q.waves;
   q.cols = (D + width - 1) / width;
-  q.words = q.tiles > 1 ? batch * q.cols * (q.tiles + (q.tiles + kChainGroup - 1) / kChainGroup) * width : 0;
+  const int64_t group = chain_group(shift != 0);
+  q.words = q.tiles > 1 ? batch * q.cols * (q.tiles + (q.tiles + group - 1) / group) * width : 0;
   q.marks_at = q.words ? 256 : 0;   // the ticket counter
   q.words_at = q.marks_at + (packed ? round256((L + kWaveTokens - 1) / kWaveTokens * kWaveTokens * 4) : 0);
   q.parts_at = q.words_at + round256(q.words * 8);
