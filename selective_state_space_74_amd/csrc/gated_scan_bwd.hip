@@ -8,8 +8,6 @@
 //   dgate_a = dv v (1 - sigma(gate_a))
 //   dlam    = c sigma(lam) sum_t dv sigma(gate_a)
 //   dh0     = a_first e_first
-#include <type_traits>
-
 #include "gated_tile.h"
 
 namespace ssm {
@@ -69,7 +67,8 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams 
   const int64_t d = live ? ch : p.D - V;   // per-channel values: lanes past the channels repeat the last ones
   // a lane's offset from the wavefront's row j of a tensor
   auto at = [&](int64_t stride) {
-    if constexpr (NARROW) return live ? static_cast<uint32_t>((c + sub * kTok * stride) * sizeof(T)) : kNowhere;
+    if constexpr (NARROW)
+      return live && n > 0 ? static_cast<uint32_t>((c + sub * kTok * stride) * sizeof(T)) : kNowhere;
     else return static_cast<uint32_t>(ch) * static_cast<uint32_t>(sizeof(T));
   };
 
@@ -82,65 +81,79 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams 
     P[v] = 1.0f;
     Q[v] = 0.0f;
   }
-  // Which tokens are a sequence's first or last, or in none (past the end of the
-  // row, or of every packed sequence): a bit each, in scalars, and a branch over
-  // what such a token asks for.  (With a path of its own for wavefronts that hold
-  // any, 30,011 x 1536 bf16 packed from 64 sequences took 190 us, and from one 161;
-  // now 151 and 151: its code came from memory, and registers were spilled.)  In
-  // a narrow call, whose stretches differ, wavefronts without such tokens do take
-  // a path of their own.
+  // Which of the lane's tokens are a sequence's first or last, or in none (past
+  // the end of the row, or of every packed sequence): a bit each.  A token that is
+  // so for any lane (the any_ bits, scalars) has a branch over what it asks for.
+  // With a path of its own for wavefronts that hold such tokens 30,011 x 1536
+  // bf16, packed from 64 sequences, took 190 us, and from one 161 (now 151 and
+  // 151): that path's code came from memory, and its registers were spilled.
   uint32_t firsts = 0, lasts = 0, outs = 0;
-  int32_t marks = 0, each[NARROW ? kTok : 1];
   auto mark_at = [&](int64_t t) {
     const int32_t m = p.marks[t];
     return m >> 2 < p.nseq ? m : kOutside;
   };
-  if constexpr (!NARROW && !PACKED) outs = ~0u << n;
-  if constexpr (!NARROW && PACKED) {
+  int32_t marks = 0;
+  if constexpr (!PACKED) {
+    outs = ~0u << n;
+  } else if constexpr (!NARROW) {
     marks = some ? mark_at(t0 + lane % kTok) : kOutside;
     firsts = static_cast<uint32_t>(__ballot(marks & 1));
     outs = static_cast<uint32_t>(__ballot(marks < 0));
     lasts = static_cast<uint32_t>(__ballot(marks & 2)) & ~outs;
+  } else {
+    // a stretch's lanes have a token's mark each, of 2^shift tokens at a time
+    const uint64_t own = (uint64_t{1} << width) - 1;
+    for (int i = 0; i < kTok; i += width) {
+      const int32_t m = c + i >= kTok ? 0 : c + i < n ? mark_at(t0 + c + i) : kOutside;
+      auto bits = [&](bool of) { return static_cast<uint32_t>(__ballot(of) >> (sub << shift) & own) << i; };
+      firsts |= bits(m & 1);
+      outs |= bits(m < 0);
+      lasts |= bits(m >= 0 && (m & 2));
+    }
+  }
+  uint32_t any_firsts = firsts, any_lasts = lasts, any_outs = outs;
+  if constexpr (NARROW) {
+    any_firsts = any_lasts = any_outs = 0;
+    for (int i = 0; i < 64; i += width) {
+      any_firsts |= __builtin_amdgcn_readlane(firsts, i);
+      any_lasts |= __builtin_amdgcn_readlane(lasts, i);
+      any_outs |= __builtin_amdgcn_readlane(outs, i);
+    }
   }
   auto bit = [](uint32_t of, int j) { return (of >> j & 1) != 0; };
-  if constexpr (PACKED && NARROW)
-    for (int i = c; i < n; i += width) marks |= mark_at(t0 + i);   // kOutside sets every bit
-  auto mark = [&](int j) { return NARROW ? each[NARROW ? j : 0] : __builtin_amdgcn_readlane(marks, j); };
+  // a packed token's row of h0, dlast or dh0; only of tokens in a sequence
+  auto seq_row = [&](int j) {
+    const int32_t m = NARROW ? mark_at(t0 + j) : __builtin_amdgcn_readlane(marks, j);
+    return static_cast<int64_t>(max(m, 0) >> 2) * p.D + d;
+  };
 
-  auto tokens = [&](auto every) {
-    constexpr bool PLAIN = decltype(every)::value;
-    constexpr bool MARKED = NARROW && PACKED && !PLAIN;
+  if (some) {
     uint32_t rx[kTok], ra[kTok], rg[kTok], rd[kTok];
-    const TokenRows tx = token_rows<T>(p.x, b * p.xb + wave_t0 * p.xs, p.xs, p.D, subs),
-                    ta = token_rows<T>(p.ga, b * p.gab + wave_t0 * p.gas, p.gas, p.D, subs),
-                    tg = token_rows<T>(p.gx, b * p.gxb + wave_t0 * p.gxs, p.gxs, p.D, subs),
-                    td = token_rows<T>(p.dout, b * p.dob + wave_t0 * p.dos, p.dos, p.D, subs);
+    const int64_t left = p.L - wave_t0;
+    const TokenRows tx = token_rows<T>(p.x, b * p.xb + wave_t0 * p.xs, p.xs, p.D, subs, left),
+                    ta = token_rows<T>(p.ga, b * p.gab + wave_t0 * p.gas, p.gas, p.D, subs, left),
+                    tg = token_rows<T>(p.gx, b * p.gxb + wave_t0 * p.gxs, p.gxs, p.D, subs, left),
+                    td = token_rows<T>(p.dout, b * p.dob + wave_t0 * p.dos, p.dos, p.D, subs, left);
     float h[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = p.ck[(b * p.nck + (NARROW ? min(t0 / kGatedCkpt, p.nck - 1) : t0 / kGatedCkpt)) * p.D + d + v];
+    for (int v = 0; v < V; ++v)
+      h[v] = p.ck[(b * p.nck + (NARROW ? min(t0 / kGatedCkpt, p.nck - 1) : t0 / kGatedCkpt)) * p.D + d + v];
 #pragma unroll
     for (int j = 0; j < kTok; ++j) {
-      const bool in = !NARROW || PLAIN || j < n, none = !NARROW && bit(outs, j);
-      ra[j] = ta.load<kBytes, CACHE>(j, in ? at(p.gas) : kNowhere, none);
-      rg[j] = tg.load<kBytes, CACHE>(j, in ? at(p.gxs) : kNowhere, none);
-      rx[j] = tx.load<kBytes, CACHE>(j, in ? at(p.xs) : kNowhere, none);
-      rd[j] = td.load<kBytes, CACHE>(j, in ? at(p.dos) : kNowhere, none);
+      ra[j] = ta.load_within<kBytes, CACHE>(j, at(p.gas));
+      rg[j] = tg.load_within<kBytes, CACHE>(j, at(p.gxs));
+      rx[j] = tx.load_within<kBytes, CACHE>(j, at(p.xs));
+      rd[j] = td.load_within<kBytes, CACHE>(j, at(p.dos));
     }
 #pragma unroll
     for (int j = 0; j < kTok; ++j) {
-      if constexpr (!NARROW && PACKED) {
-        if (bit(firsts, j)) [[unlikely]] {
+      if (PACKED && bit(any_firsts, j)) [[unlikely]] {
 #pragma unroll
-          for (int v = 0; v < V; ++v)
-            h[v] = !bit(outs, j) && p.h0 ? p.h0[static_cast<int64_t>(mark(j) >> 2) * p.D + d + v] : 0.0f;
-        }
+        for (int v = 0; v < V; ++v)
+          if (bit(firsts, j)) h[v] = !bit(outs, j) && p.h0 ? p.h0[seq_row(j) + v] : 0.0f;
       }
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        if constexpr (MARKED) {
-          if (mark(j) & 1)   // first token of its sequence, or in none
-            h[v] = mark(j) >= 0 && p.h0 ? p.h0[static_cast<int64_t>(mark(j) >> 2) * p.D + d + v] : 0.0f;
-        }
         const float x = widen<T, V>(rx[j], v), sa = sigmoid_f32(widen<T, V>(ra[j], v)),
                     g = sigmoid_f32(widen<T, V>(rg[j], v));
         const float aj = __builtin_amdgcn_exp2f(s[v].log2a * sa);
@@ -157,24 +170,15 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams 
         fl[j][v] = dv;
         fa[j][v] = dv * fmaf(-s[v].s, sa, s[v].s);
         dout[j][v] = widen<T, V>(rd[j], v);
-        if constexpr (MARKED) {
-          // dlast enters at a sequence's last token
-          if (mark(j) >= 0 && (mark(j) & 2) && p.dlast)
-            dout[j][v] += p.dlast[static_cast<int64_t>(mark(j) >> 2) * p.D + d + v];
-        }
-        if constexpr (!PLAIN) {
-          a[j][v] = j < n ? a[j][v] : 1.0f;
-          dout[j][v] = j < n ? dout[j][v] : 0.0f;
-        }
       }
-      if constexpr (!NARROW) {
-        if (bit(outs | lasts, j)) [[unlikely]] {
+      if (bit(any_outs | any_lasts, j)) [[unlikely]] {
 #pragma unroll
-          for (int v = 0; v < V; ++v) {
-            if (bit(outs, j)) {   // dout was read as 0
-              a[j][v] = PACKED ? 0.0f : 1.0f;
-              fx[j][v] = fg[j][v] = fl[j][v] = fa[j][v] = 0.0f;
-            } else if (p.dlast) dout[j][v] += p.dlast[static_cast<int64_t>(mark(j) >> 2) * p.D + d + v];
+        for (int v = 0; v < V; ++v) {
+          if (bit(outs, j)) {
+            a[j][v] = PACKED ? 0.0f : 1.0f;
+            fx[j][v] = fg[j][v] = fl[j][v] = fa[j][v] = dout[j][v] = 0.0f;
+          } else if (PACKED && p.dlast && bit(lasts, j)) {   // dlast enters at a sequence's last token
+            dout[j][v] += p.dlast[seq_row(j) + v];
           }
         }
       }
@@ -184,32 +188,14 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams 
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         P[v] *= a[j][v];
-        Q[v] = MARKED && (mark(j) & 1) && (PLAIN || j < n) ? 0.0f : a[j][v] * (dout[j][v] + Q[v]);
+        Q[v] = a[j][v] * (dout[j][v] + Q[v]);
       }
-      if constexpr (!NARROW && PACKED) {
-        if (bit(firsts, j)) [[unlikely]] {
+      if (PACKED && bit(any_firsts, j)) [[unlikely]] {
 #pragma unroll
-          for (int v = 0; v < V; ++v) Q[v] = 0.0f;
-        }
+        for (int v = 0; v < V; ++v) Q[v] = bit(firsts, j) ? 0.0f : Q[v];
       }
     }
-  };
-  const bool plain = NARROW ? __all(n == kTok) && !__any(marks < 0 || (marks & 3)) : some;
-  if (plain) tokens(std::true_type{});
-  if constexpr (NARROW) {
-    if (!plain && some) {
-      if constexpr (PACKED) {
-#pragma unroll
-        for (int j = 0; j < kTok; ++j) each[j] = j < n ? mark_at(t0 + j) : kOutside;
-        marks = 0;   // of the lane's own stretch now
-#pragma unroll
-        for (int j = 0; j < kTok; ++j) marks |= j < n ? each[j] : 0;
-      }
-      tokens(std::false_type{});
-    }
-  }
-  if constexpr (PACKED) {
-    if (NARROW ? !plain && (marks & 1) : some && firsts) {
+    if (PACKED && firsts) {
 #pragma unroll
       for (int v = 0; v < V; ++v) P[v] = kCut;
     }
@@ -251,49 +237,38 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(BwdParams 
         e[v] = chain_apply<PACKED>(q.x, q.y, e[v]);
       }
     if constexpr (NARROW) e[0] = chain_apply<PACKED>(P[0], Q[0], e[0]);   // the stretches behind this one
-    const TokenRows dx = token_rows<T>(p.dx, b * p.dxb + wave_t0 * p.dxs, p.dxs, p.D, subs),
-                    dga = token_rows<T>(p.dga, b * p.dgab + wave_t0 * p.dgas, p.dgas, p.D, subs),
-                    dgx = token_rows<T>(p.dgx, b * p.dgxb + wave_t0 * p.dgxs, p.dgxs, p.D, subs);
-    auto outputs = [&](auto every) {
-      constexpr bool PLAIN = decltype(every)::value;
-      constexpr bool MARKED = NARROW && PACKED && !PLAIN;
+    const int64_t left = p.L - wave_t0;
+    const TokenRows dx = token_rows<T>(p.dx, b * p.dxb + wave_t0 * p.dxs, p.dxs, p.D, subs, left),
+                    dga = token_rows<T>(p.dga, b * p.dgab + wave_t0 * p.dgas, p.dgas, p.D, subs, left),
+                    dgx = token_rows<T>(p.dgx, b * p.dgxb + wave_t0 * p.dgxs, p.dgxs, p.D, subs, left);
 #pragma unroll
-      for (int j = kTok - 1; j >= 0; --j) {
-        if (!NARROW && !PACKED && bit(outs, j)) continue;
-        float ox[V], oa[V], og[V];
+    for (int j = kTok - 1; j >= 0; --j) {
+      // past the end e passes unchanged, be it an infinity; outside packed
+      // sequences it is 0, and so are all the products
+      if (!PACKED && !NARROW && bit(outs, j)) continue;
+      float ox[V], oa[V], og[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float et = dout[j][v] + e[v];
+        ox[v] = et * fx[j][v];
+        og[v] = et * fg[j][v];
+        oa[v] = et * fa[j][v];
+        if (PACKED || !NARROW || !bit(any_outs, j)) acc[v] = fmaf(et, fl[j][v], acc[v]);
+        else acc[v] = bit(outs, j) ? acc[v] : fmaf(et, fl[j][v], acc[v]);
+        e[v] = a[j][v] * et;
+      }
+      if (PACKED && bit(any_firsts, j)) [[unlikely]] {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          const bool in = (!MARKED || mark(j) >= 0) && (PLAIN || j < n);
-          const float et = dout[j][v] + e[v];
-          ox[v] = in ? et * fx[j][v] : 0.0f;
-          og[v] = in ? et * fg[j][v] : 0.0f;
-          oa[v] = in ? et * fa[j][v] : 0.0f;
-          if (in) acc[v] = fmaf(et, fl[j][v], acc[v]);
-          e[v] = a[j][v] * et;
-          if constexpr (MARKED) {
-            if (mark(j) & 1) {
-              if (in && p.dh0 && live) p.dh0[static_cast<int64_t>(mark(j) >> 2) * p.D + d + v] = e[v];
-              e[v] = 0.0f;
-            }
-          }
+          if (!bit(firsts, j)) continue;
+          if (p.dh0 && live && !bit(outs, j)) p.dh0[seq_row(j) + v] = e[v];
+          e[v] = 0.0f;
         }
-        if constexpr (!NARROW && PACKED) {
-          if (bit(firsts, j)) [[unlikely]] {
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-              if (!bit(outs, j) && p.dh0 && live) p.dh0[static_cast<int64_t>(mark(j) >> 2) * p.D + d + v] = e[v];
-              e[v] = 0.0f;
-            }
-          }
-        }
-        const bool write = !NARROW || PLAIN || j < n, past = !NARROW && PACKED && j >= n;
-        dx.store<kBytes, CACHE>(j, write ? at(p.dxs) : kNowhere, narrow<T, V>(ox), past);
-        dga.store<kBytes, CACHE>(j, write ? at(p.dgas) : kNowhere, narrow<T, V>(oa), past);
-        dgx.store<kBytes, CACHE>(j, write ? at(p.dgxs) : kNowhere, narrow<T, V>(og), past);
       }
-    };
-    if (plain) outputs(std::true_type{});
-    else if constexpr (NARROW) outputs(std::false_type{});
+      dx.store_within<kBytes, CACHE>(j, at(p.dxs), narrow<T, V>(ox));
+      dga.store_within<kBytes, CACHE>(j, at(p.dgas), narrow<T, V>(oa));
+      dgx.store_within<kBytes, CACHE>(j, at(p.dgxs), narrow<T, V>(og));
+    }
     if constexpr (!PACKED) {
       if (p.dh0 && live && t0 == 0 && n > 0) {
 #pragma unroll

@@ -253,37 +253,60 @@ inline bool on_lines(const void* p, int64_t batch_stride, int64_t seq_stride, in
 // lane's offset the same for every row, and lanes past the channels read zeros
 // and write nothing.  `subs` rows of 16 tokens apart are reached through one
 // descriptor (narrow calls); a lane without a token there has offset kNowhere.
+// The _within forms also read zeros and write nothing past `left` tokens: their
+// descriptors end behind the last row, that is there.
 constexpr uint32_t kNowhere = ~0u;
 struct TokenRows {
   char* first;
   int64_t stride;     // bytes
-  uint32_t bytes;
+  uint32_t bytes, row_bytes;
+  int left;
   template <typename T>
-  __device__ __forceinline__ void set(const void* p, int64_t elements, int64_t row_stride, int64_t D, int subs, T) {
+  __device__ __forceinline__ void set(const void* p, int64_t elements, int64_t row_stride, int64_t D, int subs,
+                                      int64_t tokens, T) {
     first = static_cast<char*>(const_cast<void*>(p)) + elements * static_cast<int64_t>(sizeof(T));
     stride = row_stride * static_cast<int64_t>(sizeof(T));
-    bytes = static_cast<uint32_t>((subs - 1) * kWaveTokens * stride + D * static_cast<int64_t>(sizeof(T)));
+    row_bytes = static_cast<uint32_t>(D * static_cast<int64_t>(sizeof(T)));
+    bytes = static_cast<uint32_t>((subs - 1) * kWaveTokens * stride) + row_bytes;
+    left = static_cast<int>(min(tokens, static_cast<int64_t>(subs * kWaveTokens)));
   }
-  // none: a row of no bytes
-  __device__ __forceinline__ __amdgpu_buffer_rsrc_t row(int j, bool none) const {
-    return __builtin_amdgcn_make_buffer_rsrc(first + j * stride, 0, none ? 0 : static_cast<int>(bytes), kRsrcWord3);
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t row(int j, uint32_t n) const {
+    return __builtin_amdgcn_make_buffer_rsrc(first + j * stride, 0, static_cast<int>(n), kRsrcWord3);
+  }
+  // bytes of the rows j, j + 16, ... that are there
+  __device__ __forceinline__ uint32_t within(int j) const {
+    return left <= j ? 0u : static_cast<uint32_t>((left - j - 1) / kWaveTokens * kWaveTokens * stride) + row_bytes;
   }
   template <int BYTES, int CACHE>
-  __device__ __forceinline__ uint32_t load(int j, uint32_t at, bool none = false) const {
-    if constexpr (BYTES == 4) return __builtin_amdgcn_raw_buffer_load_b32(row(j, none), at, 0, CACHE);
-    else return __builtin_amdgcn_raw_buffer_load_b16(row(j, none), at, 0, CACHE);
+  static __device__ __forceinline__ uint32_t load(__amdgpu_buffer_rsrc_t r, uint32_t at) {
+    if constexpr (BYTES == 4) return __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, CACHE);
+    else return __builtin_amdgcn_raw_buffer_load_b16(r, at, 0, CACHE);
   }
   template <int BYTES, int CACHE>
-  __device__ __forceinline__ void store(int j, uint32_t at, uint32_t v, bool none = false) const {
-    if constexpr (BYTES == 4) __builtin_amdgcn_raw_buffer_store_b32(v, row(j, none), at, 0, CACHE);
-    else __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(v), row(j, none), at, 0, CACHE);
+  static __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, uint32_t at, uint32_t v) {
+    if constexpr (BYTES == 4) __builtin_amdgcn_raw_buffer_store_b32(v, r, at, 0, CACHE);
+    else __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(v), r, at, 0, CACHE);
+  }
+  template <int BYTES, int CACHE>
+  __device__ __forceinline__ uint32_t load(int j, uint32_t at) const { return load<BYTES, CACHE>(row(j, bytes), at); }
+  template <int BYTES, int CACHE>
+  __device__ __forceinline__ void store(int j, uint32_t at, uint32_t v) const {
+    store<BYTES, CACHE>(row(j, bytes), at, v);
+  }
+  template <int BYTES, int CACHE>
+  __device__ __forceinline__ uint32_t load_within(int j, uint32_t at) const {
+    return load<BYTES, CACHE>(row(j, within(j)), at);
+  }
+  template <int BYTES, int CACHE>
+  __device__ __forceinline__ void store_within(int j, uint32_t at, uint32_t v) const {
+    store<BYTES, CACHE>(row(j, within(j)), at, v);
   }
 };
 template <typename T>
 __device__ __forceinline__ TokenRows token_rows(const void* p, int64_t elements, int64_t row_stride, int64_t D,
-                                                int subs = 1) {
+                                                int subs = 1, int64_t left = 0) {
   TokenRows r;
-  r.set(p, elements, row_stride, D, subs, T{});
+  r.set(p, elements, row_stride, D, subs, left, T{});
   return r;
 }
 
