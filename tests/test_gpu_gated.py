@@ -213,6 +213,44 @@ def test_nan_of_one_sequence_spares_the_others_gradients(D):
     assert torch.isfinite(out[:300]).all() and torch.isfinite(out[317:]).all() and torch.isfinite(last[[0, 2]]).all()
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [12, 66, 512])
+def test_nan_outside_every_sequence_reaches_nothing(D, io):
+    """Rows before, between and behind the sequences' bounds, an odd tail too."""
+    cu = torch.tensor([37, 60, 60, 301], dtype=torch.int32, device=DEV)
+    t = make((333,), D, io, n=3, seed=25)
+    outside = torch.ones(333, dtype=torch.bool, device=DEV)
+    outside[37:301] = False
+    out, last, ck = forward(t, cu)
+    g = backward(t, ck, cu)
+    for k in ("x", "gate_a", "gate_x", "dout"):
+        t[k][outside] = float("nan")
+    out2, last2, ck2 = forward(t, cu)
+    g2 = backward(t, ck2, cu)
+    assert torch.equal(out, out2) and torch.equal(last, last2)
+    for k in g:
+        assert torch.equal(g[k], g2[k]), k
+    for v in (out2, g2["dx"], g2["dgate_a"], g2["dgate_x"]):
+        assert not v[outside].any()
+
+
+@pytest.mark.parametrize("D", [12, 66])
+def test_an_infinite_upstream_of_the_last_state_passes_the_rows_end(D):
+    """One token: every gradient of the channel is e = inf times a factor that is
+    not 0, and the places behind the row's end in its block add nothing."""
+    t = make((2, 1), D, "f32", seed=26)
+    t["dlast"][0, 5] = float("inf")
+    _, _, ck = forward(t)
+    g = backward(t, ck)
+    for k in ("dx", "dgate_a", "dgate_x"):
+        assert torch.isinf(g[k][0, 0, 5]), k
+    assert torch.isinf(g["dh0"][0, 5]) and torch.isinf(g["dlam"][5])
+    for k in ("dx", "dgate_a", "dgate_x", "dh0"):
+        bad = torch.zeros_like(g[k], dtype=torch.bool)
+        bad[0, ..., 5] = True
+        assert torch.isfinite(g[k][~bad]).all(), k
+
+
 def test_zero_sizes():
     for lead in ((0, 5), (3, 0)):
         t = make(lead, 8, "f32", n=lead[0], seed=15)
