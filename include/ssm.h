@@ -392,9 +392,9 @@ typedef struct ssm_ssd_args {
  *                holds where that token begins a sequence or is in none is
  *                unspecified).  NULL: none written.
  * Sizes: zero sizes are no-ops, but that empty sequences still set last_state;
- * seqlen below 2^31 - 64, dim at most 2^28, nseq below 2^29, and
- * batch * ceil(seqlen / 16) * ceil(dim / 64) below 2^31 (SSM_ERR_UNSUPPORTED
- * past that).
+ * dim at most 2^26, nseq below 2^29, and batch * ceil(seqlen / 16) *
+ * ceil(dim / 64) below 2^24, zeros counting as 1 (SSM_ERR_UNSUPPORTED past
+ * that).
  * Precision: fp32 arithmetic and state; bf16 inputs are widened exactly and
  * out is rounded once.
  * Aliasing: out, last_state, checkpoints and the workspace must not overlap

@@ -29,12 +29,15 @@ bool collide(const Tokens& t, int64_t batch, int64_t L, int64_t D) {
 
 constexpr int64_t kMaxGroups = int64_t{1} << 31;
 constexpr int64_t kGatedTokens = SSM_GATED_CHECKPOINT_TOKENS;
-constexpr int64_t kMaxDim = int64_t{1} << 28;
+constexpr int64_t kMaxDim = int64_t{1} << 26;
 constexpr int64_t kMaxPacked = int64_t{1} << 29;   // sequence numbers and two marks share 32 bits
-bool too_many_groups(int64_t batch, int64_t L, int64_t D) {
-  const int64_t tiles = (L + 15) / 16, cols = (D + 63) / 64;
-  if (tiles == 0 || cols == 0 || batch == 0) return batch >= kMaxGroups || cols >= kMaxGroups;
-  return batch >= kMaxGroups / tiles || cols >= kMaxGroups / (batch * tiles);
+// A launch has less than 2^32 threads.  Blocks of 16 tokens and 64 channels, a
+// wavefront each: workgroups of 8 wavefronts and the backward's blocks of 8
+// tokens make it up to 2.7 times as many wavefronts.
+constexpr int64_t kMaxBlocks = int64_t{1} << 24;
+bool too_many_blocks(int64_t batch, int64_t L, int64_t D) {
+  const int64_t blocks = max((L + 15) / 16, int64_t{1}) * max((D + 63) / 64, int64_t{1});
+  return batch > (kMaxBlocks - 1) / blocks;
 }
 
 // What the gated scan and its backward check alike.
@@ -46,7 +49,7 @@ int check_gated(const Args* a) {
   if (bad_dtype(a->io_dtype)) return SSM_ERR_DTYPE;
   if (a->seqlen > kMaxSeqlen) return SSM_ERR_UNSUPPORTED;
   // rows are addressed by 32-bit byte offsets
-  if (a->dim > kMaxDim || too_many_groups(a->batch, a->seqlen, a->dim)) return SSM_ERR_UNSUPPORTED;
+  if (a->dim > kMaxDim || too_many_blocks(a->batch, a->seqlen, a->dim)) return SSM_ERR_UNSUPPORTED;
   if (a->cu_seqlens && a->nseq >= kMaxPacked) return SSM_ERR_UNSUPPORTED;
   return SSM_OK;
 }

@@ -135,6 +135,8 @@ def test_gated_refusals(make, check):
     e(DTYPE, io_dtype=2)
     e(UNSUP, seqlen=(1 << 31) - 63)
     e(UNSUP, batch=1 << 20, seqlen=1 << 20)
+    e(UNSUP, batch=1 << 24, seqlen=1), e(UNSUP, batch=1, seqlen=1 << 28), e(UNSUP, dim=(1 << 26) + 1)
+    e(UNSUP, batch=1 << 24, seqlen=0)
     for k in ("x", "gate_a", "gate_x", "lam"):
         e(NULL, **{k: None})
     for k in ("x", "gate_a", "gate_x"):
