@@ -328,8 +328,8 @@ int shift_of(const ssm_gated_bwd_args& a) {
 // of 128 channels and more than one tile.  A tile is then 64 tokens and not 128:
 // with fewer groups the carry through the tiles, about 0.9 tokens a nanosecond
 // and group, would bound the call, and a second tile costs a launch.  Forward and
-// backward with two against one: 390 against 400 us at 4 x 4096 x 5120 bf16, 261
-// against 273 at 2 x 8587 x 2306; with one group, 282 against 203 at 250,095 x 40.
+// backward with two against one: 367 against 419 us at 4 x 4096 x 5120 bf16, 250
+// against 281 at 2 x 8587 x 2306; with one group, 280 against 200 at 250,095 x 40.
 constexpr int64_t kMinGroups = 4;
 int channels_per_lane(const ssm_gated_bwd_args& a) {
   auto ok = [&](const void* p, int64_t sb, int64_t ss) {

@@ -29,8 +29,8 @@
 // its low half would be one particular NaN, and NaNs are published as another.
 // Bound by memory traffic (8 bytes a value forward in bf16, 16 in fp32; 14 and
 // 28 backward) with the vector units about two thirds busy: 262,144 x 1536 bf16
-// forward 596 us, 5.4 TB/s; 4 x 4096 x 5120 bf16 forward 131 us and backward
-// 258 us, 5.1 and 4.6 TB/s.
+// forward 574 us, 5.6 TB/s; 4 x 4096 x 5120 bf16 forward 133 us and backward
+// 231 us, 5.4 and 5.3 TB/s.
 #pragma once
 
 #include "gated_math.h"
@@ -238,10 +238,10 @@ __device__ __forceinline__ uint32_t narrow(const float (&h)[V]) {
 
 // Cache policy of the token rows.  Where every row begins on a cache line each
 // byte passes once, and the nontemporal bit helps (2 x 8587 x 2304 bf16 forward
-// and backward: 204 us, and 213 us without).
+// and backward: 195 us, and 205 us without).
 // Otherwise two wavefronts share the lines at their border, which have to stay
-// until both have had them: 2 x 8587 x 2306 bf16 training takes 272 us with the
-// plain policy and 354 us with the nontemporal one.
+// until both have had them: 2 x 8587 x 2306 bf16 training takes 251 us with the
+// plain policy and 278 us with the nontemporal one.
 constexpr int kPlain = 0, kStream = 2;
 constexpr int64_t kLine = 128;
 inline bool on_lines(const void* p, int64_t batch_stride, int64_t seq_stride, int64_t esz) {
