@@ -151,6 +151,18 @@ def test_slices_of_wider_tensors(lead, D, io):
     run_and_check(s, io, f"sequence-major {lead} {D} {io}")
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("L,D", [(1, 12), (300, 12), (150, 66), (133, 512)])
+def test_inputs_that_are_one_row_for_all_tokens(L, D, io):
+    t = make((2, L), D, io, seed=27)
+    for k in ("gate_a", "x", "dout"):
+        t[k] = t[k][:, :1].expand(-1, L, -1)
+    run_and_check(t, io, f"one row {L} {D} {io}")
+    p = {k: (v[1] if v.dim() == 3 else v) for k, v in t.items()}
+    cu = torch.tensor([0, L // 2, L], dtype=torch.int32, device=DEV)
+    run_and_check(p, io, f"one row, packed {L} {D} {io}", cu)
+
+
 def test_out_as_a_slice_next_to_the_input():
     t = make((2, 70), 48, "f32", seed=12)
     both = torch.zeros(2, 70, 96, device=DEV)
