@@ -965,7 +965,7 @@ def gated_scan_fwd(x, gate_a, gate_x, lam, c=8.0, h0=None, cu_seqlens=None, retu
         if made:
             out = _empty(x, shape, io, dev)
         if return_last_state and last_state is None:
-            last_state = torch.empty((n, dim), dtype=torch.float32, device=dev)
+            last_state = _empty(x if h0 is None else h0, (n, dim), torch.float32, dev)
         a = GatedArgs(batch, L, dim, nseq, code, made, c, *inputs, lam_p, cu, h0_p,
                       _fp32("last_state", last_state, (n, dim), dev), *_tokens("out", out, shape, io, dev),
                       checkpoints if checkpoints is None else
@@ -996,9 +996,9 @@ def gated_scan_bwd(dout, x, gate_a, gate_x, lam, checkpoints, c=8.0, h0=None, cu
     c = _decay_constant(c)
     with _on(dev, stream) as s:
         dx, dga, dgx = (_empty(dout, shape, io, dev) for _ in range(3))
-        g = dict(dx=dx, dgate_a=dga, dgate_x=dgx, dlam=torch.empty(dim, dtype=torch.float32, device=dev))
+        g = dict(dx=dx, dgate_a=dga, dgate_x=dgx, dlam=torch.empty_like(lam))
         if h0 is not None:
-            g["dh0"] = torch.empty((n, dim), dtype=torch.float32, device=dev)
+            g["dh0"] = torch.empty_like(h0)
         # the three gradients have the same strides: a row of tokens after another
         rows = (L * dim, dim)
         a = GatedBwdArgs(batch, L, dim, nseq, code, c, *inputs, lam_p, cu, h0_p, ck_p, *upstream, dlast_p,
