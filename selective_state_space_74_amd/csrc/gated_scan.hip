@@ -36,6 +36,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_fwd_kernel(FwdParams p) 
   __shared__ float2 pairs[kMaxWaves][W];
   constexpr int kGroup = chain_group(NARROW);
   __shared__ ChainShared<CHAIN ? W : 1, kGroup> before;
+  __shared__ float initial[PACKED ? 1 : W];
   __shared__ uint32_t taken;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -162,6 +163,18 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_fwd_kernel(FwdParams p) 
 #pragma unroll
     for (int v = 0; v < V; ++v) pairs[wave][lane * V + v] = make_float2(P[v], H[v]);
   }
+  // last_state may be h0 itself: h0 has therefore been read, into LDS, before the
+  // tile's first barrier.  The state is stored behind that barrier or, by another
+  // tile, behind words that this one publishes there.  (A packed sequence's first
+  // token takes its h0 into the pair.)  Of a chain, the first group's tiles start
+  // from h0.  (Read here: a register that holds it through the tokens would be the
+  // 65th in fp32, and cost a workgroup a compute unit.)
+  if constexpr (!PACKED) {
+    if (wave == 0 && sub == 0 && (!CHAIN || tile < static_cast<uint32_t>(kGroup))) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) initial[c * V + v] = p.h0 ? p.h0[b * p.D + d + v] : 0.0f;
+    }
+  }
   __syncthreads();
   float h[V];
   if constexpr (CHAIN) {
@@ -170,15 +183,14 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_fwd_kernel(FwdParams p) 
     uint64_t* const base = p.words + (static_cast<int64_t>(row) * p.cols + col) * (p.tiles + ngroups) * width;
     const Chain chain{base, base + static_cast<int64_t>(p.tiles) * width, width};
     // thread i of the first 2^shift has channel i of the group
-    const int64_t di = min(static_cast<int64_t>(col) * W + (threadIdx.x & (width - 1)), p.D - 1);
-    const float first = !PACKED && p.h0 ? p.h0[b * p.D + di] : 0.0f;
+    const float first = PACKED ? 0.0f : initial[threadIdx.x & (width - 1)];   // of the first group's tiles
     chain_carry<PACKED, W, kGroup, chain_mine(NARROW, V)>(chain, tile, p.tiles, pairs, before, shift, first,
                                                              [](int w) { return w; });
 #pragma unroll
     for (int v = 0; v < V; ++v) h[v] = before.entering[c * V + v];
   } else {
 #pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = !PACKED && p.h0 ? p.h0[b * p.D + d + v] : 0.0f;
+    for (int v = 0; v < V; ++v) h[v] = PACKED ? 0.0f : initial[c * V + v];
   }
   if (!some) return;
   for (int w = 0; w < wave; ++w)

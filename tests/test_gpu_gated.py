@@ -284,6 +284,30 @@ def test_state_carried_in_place():
     assert torch.equal(h, last)
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [12, 66, 256])
+@pytest.mark.parametrize("L", [1, 40, 100, 128, 333, 1100])
+def test_state_in_place_gives_the_bits_of_two_tensors(L, D, io):
+    """last_state that is h0: one tile of several wavefronts, chains that end inside
+    their first group, narrow calls and packed rows; the outputs and checkpoints,
+    which a state read too late would change, too."""
+    t = make((24, L), D, io, seed=L + D)
+    want = forward(t)
+    h, ck = t["h0"].clone(), torch.empty_like(want[2])
+    out, last = ssm.gated_scan_fwd(t["x"], t["gate_a"], t["gate_x"], t["lam"], h0=h, last_state=h,
+                                   return_last_state=True, checkpoints=ck)
+    assert last is h and all(torch.equal(a, b) for a, b in zip((out, h, ck), want))
+    # the same rows packed, with an empty sequence between them
+    p = {k: (v.reshape(-1, D) if v.dim() == 3 else v) for k, v in t.items()}
+    bounds = [k * L for k in range(12)] + [k * L for k in range(11, 24)]
+    cu = torch.tensor(bounds, dtype=torch.int32, device=DEV)
+    want = forward(p, cu)
+    h = t["h0"].clone()
+    out, last = ssm.gated_scan_fwd(p["x"], p["gate_a"], p["gate_x"], p["lam"], h0=h, last_state=h, cu_seqlens=cu,
+                                   return_last_state=True)
+    assert torch.equal(out, want[0]) and torch.equal(h, want[1]) and torch.equal(h[11], t["h0"][11])
+
+
 def test_split_sequence_carries_the_state():
     t = make((2, 1000), 130, "f32", seed=18)
     val, bnd = expected(t)
