@@ -8,13 +8,16 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// Two chain words, stored at once: the workspace is 8-byte aligned, no more.
+struct alignas(8) WordPair { uint64_t w[2]; };
+
 __global__ __launch_bounds__(kThreads) void gated_prep_kernel(PrepParams p) {
   const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads;
   if (i0 == 0 && p.ticket) *p.ticket = 0;
-  // words in pairs: their number is even (64 channels a group)
-  uint4* const w = reinterpret_cast<uint4*>(p.words);
-  for (int64_t i = i0; i < p.nwords / 2; i += step) w[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
+  // words in pairs: their number is even (8 channels a group at least)
+  WordPair* const w = reinterpret_cast<WordPair*>(p.words);
+  for (int64_t i = i0; i < p.nwords / 2; i += step) w[i] = WordPair{{kNoWord, kNoWord}};
   if (p.marks) {
     // padded to whole wavefronts of tokens with tokens outside
     const int64_t n = (p.L + kWaveTokens - 1) / kWaveTokens * kWaveTokens;

@@ -408,6 +408,18 @@ def test_workspace_kept_across_calls_of_different_sizes():
         assert torch.equal(o, o2) and torch.equal(l, l2) and all(torch.equal(g[k], g2[k]) for k in g)
 
 
+@pytest.mark.parametrize("D", [12, 140])
+def test_workspace_aligned_to_8_bytes_and_no_more(D):
+    t = make((2, 3000), D, "f32", seed=D)
+    out, last, ck = forward(t)
+    g = backward(t, ck)
+    ws = torch.full((16 << 20,), 255, dtype=torch.uint8, device=DEV)[8:]
+    assert ws.data_ptr() % 16 == 8
+    out2, last2, ck2 = forward(t, workspace=ws)
+    g2 = backward(t, ck2, workspace=ws)
+    assert torch.equal(out, out2) and torch.equal(last, last2) and all(torch.equal(g[k], g2[k]) for k in g)
+
+
 def test_autograd():
     t = make((2, 90), 40, "f32", seed=25)
     leaves = {k: t[k].clone().requires_grad_() for k in ("x", "gate_a", "gate_x", "lam", "h0")}

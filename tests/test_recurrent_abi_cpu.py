@@ -175,6 +175,15 @@ def test_gated_workspace_is_required():
         assert ssm.validate_gated(a) == SCRATCH
 
 
+@pytest.mark.parametrize("make,check", [(lambda: good_gated(packed=True), ssm.validate_gated), (good_bwd, ssm.validate_gated_bwd)])
+def test_gated_workspace_alignment(make, check):
+    for off, status in ((8, OK), (4, ALIGN), (12, ALIGN)):
+        a = make()
+        assert a.workspace_bytes
+        a.workspace += off
+        assert check(a) == status, off
+
+
 def test_gated_backward_refusals():
     e = lambda status, **f: expect(good_bwd, ssm.validate_gated_bwd, status, **f)  # noqa: E731
     for k in ("checkpoints", "dout", "dx", "dgate_a", "dgate_x", "dlam"):
