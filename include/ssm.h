@@ -594,8 +594,10 @@ size_t ssm_ssd_workspace_size(const ssm_ssd_args* args);
 size_t ssm_scan_bwd_workspace_size(const ssm_scan_bwd_args* args);
 
 /* Workspace bytes the gated scan and its backward need for this argument
- * block (0: none).  Read only sizes and whether cu_seqlens is given; pure host
- * code. */
+ * block (0: none).  Read only sizes and whether cu_seqlens is given, as long as
+ * out_seq_stride (dx_seq_stride) is 0: the size then does for every io_dtype and
+ * all strides.  Where it is set, io_dtype and the sequence strides are read too,
+ * and the size is that of calls with these (at most as large).  Pure host code. */
 size_t ssm_gated_scan_workspace_size(const ssm_gated_args* args);
 size_t ssm_gated_scan_bwd_workspace_size(const ssm_gated_bwd_args* args);
 

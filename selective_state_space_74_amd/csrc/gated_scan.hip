@@ -353,11 +353,9 @@ void launch_fwd(const FwdParams& p, const GatedPlan& q, bool packed, hipStream_t
 
 }  // namespace
 
-// The size for whichever form runs: it depends on no address.
+// No output has rows 0 elements apart, but one of a single token.
 size_t gated_workspace_bytes(const ssm_gated_args& a) {
-  const int shift = shift_of(a);
-  const int64_t one = plan(a, 1, shift).bytes, two = shift ? 0 : plan(a, 2, 0).bytes;
-  return static_cast<size_t>(one > two ? one : two);
+  return gated_bytes(shift_of(a), a.out_seq_stride != 0, [&](int V, int shift) { return plan(a, V, shift); });
 }
 
 hipError_t launch_gated_fwd(const ssm_gated_args& a, hipStream_t stream) {

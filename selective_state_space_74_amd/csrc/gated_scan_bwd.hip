@@ -385,11 +385,9 @@ void launch_rows(const ssm_gated_bwd_args& a, const BwdParams& p, const GatedPla
 
 }  // namespace
 
-// The size for whichever form runs: it depends on no address.
+// No output has rows 0 elements apart, but one of a single token.
 size_t gated_bwd_workspace_bytes(const ssm_gated_bwd_args& a) {
-  const int shift = shift_of(a);
-  const int64_t one = plan(a, 1, shift).bytes, two = shift ? 0 : plan(a, 2, 0).bytes;
-  return static_cast<size_t>(one > two ? one : two);
+  return gated_bytes(shift_of(a), a.dx_seq_stride != 0, [&](int V, int shift) { return plan(a, V, shift); });
 }
 
 hipError_t launch_gated_bwd(const ssm_gated_bwd_args& a, hipStream_t stream) {

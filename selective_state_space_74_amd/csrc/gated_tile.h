@@ -352,4 +352,14 @@ inline bool narrow_fits(int64_t D, int64_t row_stride, int64_t esz) {
   return row_stride < (int64_t{1} << 31) / (subs * kWaveTokens * esz);
 }
 
+// Workspace for whichever form runs; it depends on no address.  Of a narrow call
+// (shift) whose strides are not known yet, for the wide forms too: it may turn out
+// not to fit.  plan_of(V, shift) is a form's plan.
+template <typename PlanOf>
+size_t gated_bytes(int shift, bool strides_known, PlanOf plan_of) {
+  int64_t bytes = shift ? plan_of(1, shift).bytes : 0;
+  if (!shift || !strides_known) bytes = max(bytes, max(plan_of(1, 0).bytes, plan_of(2, 0).bytes));
+  return static_cast<size_t>(bytes);
+}
+
 }  // namespace ssm

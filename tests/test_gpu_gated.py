@@ -349,6 +349,24 @@ def test_offsets_past_32_bits():
     assert all(torch.equal(a[k], b[k]) for k in a)
 
 
+@pytest.mark.parametrize("D", [3, 12, 30])
+def test_few_channels_with_rows_far_apart(D):
+    """Up to 32 channels, rows 2^25 elements apart: too far for several blocks of
+    tokens behind one descriptor."""
+    L = 200
+    big = torch.empty(L << 25, dtype=torch.bfloat16, device=DEV)
+    view = lambda at: big.as_strided((1, L, D), (L << 25, 1 << 25, 1), at)  # noqa: E731
+    t = make((1, L), D, "bf16", seed=D)
+    for i, k in enumerate(("x", "gate_a", "gate_x", "dout")):
+        far = view(i * 64)
+        far.copy_(t[k])
+        t[k] = far
+    out, _, _, _ = run_and_check(t, "bf16", f"far rows {D}")
+    given = view(1024)
+    ssm.gated_scan_fwd(t["x"], t["gate_a"], t["gate_x"], t["lam"], h0=t["h0"], out=given)
+    assert torch.equal(given, out)
+
+
 def test_another_stream_and_two_at_once():
     """The same call on two streams at once, each with its own workspace."""
     ts = [make((1, 6000), 300, "f32", seed=21 + i) for i in range(2)]

@@ -184,6 +184,33 @@ def test_gated_workspace_alignment(make, check):
         assert check(a) == status, off
 
 
+@pytest.mark.parametrize("make,check,size", [
+    (good_gated, ssm.validate_gated, ssm.gated_scan_workspace_size),
+    (good_bwd, ssm.validate_gated_bwd, ssm.gated_scan_bwd_workspace_size)])
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("D", [1, 3, 8, 13, 16, 20, 32, 33, 300])
+def test_gated_workspace_asked_for_by_sizes_alone(make, check, size, D, packed):
+    """What the size function says of the sizes does for every type and stride,
+    rows too far apart for the form with several blocks of tokens a wavefront
+    among them; asked again with the strides, it says no more."""
+    for L in (1, 100, 700, 5000, 200000):
+        full = make(L=L, D=D, packed=packed)
+        strides = [k for k, _ in full._fields_ if k.endswith("_seq_stride")]
+        bare = type(full)(batch=full.batch, seqlen=L, dim=D, nseq=full.nseq, c=8.0, cu_seqlens=full.cu_seqlens)
+        need = size(bare)
+        for io in (0, 1):
+            for stride in (D, 1 << 21, 1 << 23, 1 << 25):
+                for far in ([], strides[:1], strides):
+                    a = make(L=L, D=D, io=io, packed=packed)
+                    for i, k in enumerate(strides):
+                        setattr(a, k.replace("_seq_stride", ""), BASE + (i + 1 << 52))
+                        setattr(a, k, stride if k in far else D)
+                        setattr(a, k.replace("_seq", "_batch"), L * getattr(a, k))
+                    assert size(a) <= need
+                    a.workspace, a.workspace_bytes = (BASE + (14 << 52), need) if need else (None, 0)
+                    assert check(a) == OK, (L, io, stride)
+
+
 def test_gated_backward_refusals():
     e = lambda status, **f: expect(good_bwd, ssm.validate_gated_bwd, status, **f)  # noqa: E731
     for k in ("checkpoints", "dout", "dx", "dgate_a", "dgate_x", "dlam"):
