@@ -4,6 +4,8 @@
 
 #include <stdint.h>
 
+#include <numeric>
+
 #include "ssm.h"
 
 namespace ssm {
@@ -47,18 +49,20 @@ struct Rows {
 
 inline Rows rows3(const void* p, int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t n2,
                   int64_t esz) {
-  return Rows{span3(p, n0, s0, n1, s1, n2, esz), n0 > 1 ? s0 * esz : 0, s1 * esz, n2 * esz};
+  return Rows{span3(p, n0, s0, n1, s1, n2, esz), n0 > 1 ? s0 * esz : 0, n1 > 1 ? s1 * esz : 0, n2 * esz};
 }
 
 // Whether two such tensors share bytes.  Slices of one wider tensor (the same
-// strides, whole rows apart) interleave without sharing any.
+// strides, in either order) interleave without sharing any: every row of a tensor
+// begins at the same place of a period that both strides are multiples of.
 inline bool overlap(const Rows& a, const Rows& b) {
   if (!overlap(a.span, b.span)) return false;
-  if (a.s1 != b.s1 || a.s0 != b.s0 || a.s1 <= 0 || a.s0 % a.s1 != 0) return true;
+  const int64_t period = std::gcd(a.s0, a.s1);
+  if (a.s0 != b.s0 || a.s1 != b.s1 || period == 0) return true;
   const Rows& lo = a.span.lo <= b.span.lo ? a : b;
   const Rows& hi = a.span.lo <= b.span.lo ? b : a;
-  const int64_t off = static_cast<int64_t>((hi.span.lo - lo.span.lo) % static_cast<uintptr_t>(a.s1));
-  return off < lo.row || off + hi.row > a.s1;
+  const int64_t off = static_cast<int64_t>((hi.span.lo - lo.span.lo) % static_cast<uintptr_t>(period));
+  return off < lo.row || off + hi.row > period;
 }
 inline bool overlap(const Rows& a, const Span& b) { return overlap(a.span, b); }
 

@@ -173,6 +173,17 @@ def test_out_as_a_slice_next_to_the_input():
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("L", [1, 70])
+def test_out_next_to_the_input_in_a_sequence_major_tensor(L, io):
+    t = make((3, L), 48, io, seed=41)
+    both = torch.zeros(L, 3, 96, device=DEV, dtype=TYPES[io]).transpose(0, 1)
+    both[..., :48] = t["x"]
+    ref_out, _, _ = forward(t)
+    ssm.gated_scan_fwd(both[..., :48], t["gate_a"], t["gate_x"], t["lam"], h0=t["h0"], out=both[..., 48:])
+    assert torch.equal(both[..., 48:], ref_out) and torch.equal(both[..., :48], t["x"])
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
 def test_extreme_gates(io):
     """Gates at both ends: a of 0 and 1, an input scale of 0 with its root's
     derivative taken as 0, huge and tiny decay rates."""

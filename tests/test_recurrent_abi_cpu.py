@@ -158,6 +158,25 @@ def test_gated_forward_refusals():
     e(OK, out=addr(0) + 32 * 4, **half), e(ALIAS, out=addr(0) + 31 * 4, **half), e(ALIAS, out=addr(0) + 33 * 4, **half)
 
 
+@pytest.mark.parametrize("batch,L,ss,sb", [(2, 64, 128, 64), (3, 1, 7, 64), (1, 64, 64, 7), (2, 64, 64, 64 * 64 + 192),
+                                           (5, 9, 5 * 64, 64)])
+def test_slices_of_one_tensor_interleave_in_any_order(batch, L, ss, sb):
+    """out next to x in a (L, batch, 2 dim) or (batch, L, 2 dim) tensor, and two
+    gradients so, are no overlap; one element further either way is.  A stride of
+    an axis of one is of no account."""
+    for shift, status in ((32, OK), (31, ALIAS), (33, OK if batch == L == 1 else ALIAS)):
+        a = good_gated(batch=batch, L=L, D=32)
+        for k in ("x", "out"):
+            setattr(a, k + "_seq_stride", ss), setattr(a, k + "_batch_stride", sb)
+        a.out = a.x + 4 * shift
+        assert ssm.validate_gated(a) == status, shift
+        a = good_bwd(batch=batch, L=L, D=32)
+        for k in ("dgate_a", "dgate_x"):
+            setattr(a, k + "_seq_stride", ss), setattr(a, k + "_batch_stride", sb)
+        a.dgate_x = a.dgate_a + 4 * shift
+        assert ssm.validate_gated_bwd(a) == status, shift
+
+
 def test_gated_workspace_is_required():
     a = good_bwd()
     a.workspace_bytes -= 1
