@@ -1013,13 +1013,14 @@ def gated_scan(x, gate_a, gate_x, lam, c=8.0, h0=None, cu_seqlens=None, return_l
     """gated_scan_fwd as a differentiable torch op: gradients flow to x,
     gate_a, gate_x, lam and h0, from out and from the last state."""
     torch = _torch()
+    recording = torch.is_grad_enabled()   # asked here: within forward it never is
 
     class _GatedScan(torch.autograd.Function):
         @staticmethod
         def forward(ctx, x, gate_a, gate_x, lam, h0):
             ctx.set_materialize_grads(False)
             ck = None
-            if any(ctx.needs_input_grad):
+            if recording and any(ctx.needs_input_grad):
                 ck = torch.empty(gated_checkpoint_shape(x.shape), dtype=torch.float32, device=x.device)
             out, last = gated_scan_fwd(x, gate_a, gate_x, lam, c=c, h0=h0, cu_seqlens=cu_seqlens,
                                        return_last_state=True, checkpoints=ck)

@@ -304,3 +304,26 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
     with pytest.raises(ValueError):
         ssm.state_cache_write(codes, scales, torch.zeros(2, 4, 16))   # not on a GPU
     assert ssm.gated_checkpoint_shape((2, 33, 7)) == (2, 5, 7) and ssm.gated_checkpoint_shape((0, 7)) == (0, 7)
+
+
+def test_autograd_op_writes_checkpoints_only_for_a_backward(monkeypatch):
+    torch = pytest.importorskip("torch")
+    asked = []
+
+    def forward(x, gate_a, gate_x, lam, checkpoints=None, **kw):
+        asked.append(checkpoints is not None)
+        return x.clone(), torch.zeros(x.shape[0], x.shape[-1])
+
+    monkeypatch.setattr(ssm, "gated_scan_fwd", forward)
+    x, lam = torch.ones(2, 20, 4), torch.ones(4, requires_grad=True)
+    out = ssm.gated_scan(x, x, x, lam)
+    assert asked == [True] and out.requires_grad
+    for mode in (torch.no_grad, torch.inference_mode):
+        with mode():
+            out = ssm.gated_scan(x, x, x, lam)
+        assert asked.pop() is False and not out.requires_grad
+    ssm.gated_scan(x, x, x, lam.detach())
+    assert asked.pop() is False
+    with torch.no_grad(), torch.enable_grad():
+        ssm.gated_scan(x, x, x, lam)
+    assert asked == [True, True]
