@@ -201,6 +201,57 @@ def test_extreme_gates(io):
         assert torch.isfinite(g[k]).all(), k
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [20, 64])
+def test_extreme_gates_all_gradients(D, io):
+    """dgate_a and dlam too, against the 64-bit form.  Added to its bounds, with
+    |e| <= E, the sum of the upstreams' magnitudes: where 1 - a^2 is below 2^-126
+    (here: 2^-125) fp32 has 2^63 for 1 / beta, so dv sigma(gate_a) is off by
+    E |x| (1 / beta + 2^63) sigma(gate_a); and a decay below 2^-126 is 0, which is
+    E 2^-126 |h| there."""
+    t = make((2, 200), D, io, seed=43)
+    big = torch.tensor([float("-inf"), -1e4, -60.0, -20.0, 0.0, 20.0, 60.0, 1e4, float("inf")])
+    idx = torch.arange(200) % 9
+    t["gate_a"] = big[idx][None, :, None].expand(2, 200, D).to(TYPES[io]).to(DEV).contiguous()
+    t["gate_x"] = big[(idx + 4) % 9][None, :, None].expand(2, 200, D).to(TYPES[io]).to(DEV).contiguous()
+    t["lam"] = torch.linspace(-30, 30, D, device=DEV)
+    val, bnd = expected(t)
+    with np.errstate(all="ignore"):
+        sa = 1 / (1 + np.exp(-f64(t["gate_a"])))
+        s = 8 * (np.maximum(f64(t["lam"]), 0) + np.log1p(np.exp(-np.abs(f64(t["lam"])))))
+        q = -np.expm1(-2 * s * sa)
+        inv = np.where(q > 0, 1 / np.sqrt(q), 0) + 2.0 ** 63
+    E = np.abs(f64(t["dout"])).sum(1, keepdims=True) + np.abs(f64(t["dlast"]))[:, None]
+    size = max(np.abs(val["out"]).max(), np.abs(f64(t["h0"])).max())
+    off = E * (np.abs(f64(t["x"])) * np.where(q < 2.0 ** -125, inv, 0) + 2.0 ** -126 * size) * sa
+    bnd["dgate_a"] = bnd["dgate_a"] + off * s
+    bnd["dlam"] = bnd["dlam"] + 8 / (1 + np.exp(-f64(t["lam"]))) * off.sum((0, 1))
+    out, last, ck = forward(t)
+    check(backward(t, ck), val, bnd, io, f"extreme {D} {io}")
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("D,L", [(3, 70000), (13, 36000), (31, 20000)])
+def test_few_channels_over_several_groups_of_tiles(D, L, io):
+    """The carry from group to group where a group is 32,768 tokens (up to 8
+    channels), 16,384 (16) or 8192 (32); batched, and packed with sequences that
+    end in other groups than they begin in.  The same bits every time."""
+    t = make((1, L), D, io, seed=D)
+    t["lam"] = t["lam"] - 6      # decays close to 1: a state reaches over groups
+    first = run_and_check(t, io, f"groups {D} {io}")
+    p = {k: (v[0] if v.dim() == 3 else v) for k, v in t.items()}
+    cu = torch.tensor([0, 11, L // 2 + 5, L // 2 + 5, L - 3], dtype=torch.int32, device=DEV)
+    p["h0"], p["dlast"] = torch.randn(4, D, device=DEV), torch.randn(4, D, device=DEV)
+    packed = run_and_check(p, io, f"packed groups {D} {io}", cu)
+    for i in range(3):
+        again = forward(t)
+        assert all(torch.equal(a, b) for a, b in zip(again, first))
+        assert all(torch.equal(g, first[3][k]) for k, g in backward(t, again[2]).items())
+        again = forward(p, cu)
+        assert all(torch.equal(a, b) for a, b in zip(again[:2], packed))
+        assert all(torch.equal(g, packed[3][k]) for k, g in backward(p, again[2], cu).items())
+
+
 def test_nan_stays_in_its_channel_and_sequence():
     t = make((2, 300), 66, "f32", seed=14)
     clean, _, _ = forward(t)
@@ -285,6 +336,16 @@ def test_zero_sizes():
             assert torch.equal(g["dh0"], t["dlast"])
     t = make((2, 3), 0, "f32", seed=16)
     assert forward(t)[0].shape == (2, 3, 0)
+
+
+def test_packed_without_tokens():
+    """Sequences that are all empty, and no token outside either."""
+    cu = torch.zeros(4, dtype=torch.int32, device=DEV)
+    t = make((0,), 8, "f32", n=3, seed=16)
+    out, last, ck = forward(t, cu)
+    g = backward(t, ck, cu)
+    assert out.shape == (0, 8) and torch.equal(last, t["h0"])
+    assert torch.equal(g["dh0"], t["dlast"]) and not g["dlam"].any() and g["dx"].shape == (0, 8)
 
 
 def test_state_carried_in_place():
