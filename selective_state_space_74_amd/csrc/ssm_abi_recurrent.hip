@@ -40,18 +40,26 @@ bool too_many_blocks(int64_t batch, int64_t L, int64_t D) {
   return batch > (kMaxBlocks - 1) / blocks;
 }
 
-// What the gated scan and its backward check alike.
+// What the gated scan and its backward check alike: sizes, and the limits on them.
 template <typename Args>
-int check_gated(const Args* a) {
+int check_shape(const Args* a) {
   if (a->batch < 0 || a->dim < 0 || a->seqlen < 0 || a->nseq < 0) return SSM_ERR_SHAPE;
-  if (a->cu_seqlens && a->batch != 1) return SSM_ERR_SHAPE;
-  if (!(a->c > 0.0f) || !isfinite(a->c)) return SSM_ERR_SHAPE;
-  if (bad_dtype(a->io_dtype)) return SSM_ERR_DTYPE;
+  return a->cu_seqlens && a->batch != 1 ? SSM_ERR_SHAPE : SSM_OK;
+}
+template <typename Args>
+int check_limits(const Args* a) {
   if (a->seqlen > kMaxSeqlen) return SSM_ERR_UNSUPPORTED;
   // rows are addressed by 32-bit byte offsets
   if (a->dim > kMaxDim || too_many_blocks(a->batch, a->seqlen, a->dim)) return SSM_ERR_UNSUPPORTED;
   if (a->cu_seqlens && a->nseq >= kMaxPacked) return SSM_ERR_UNSUPPORTED;
   return SSM_OK;
+}
+template <typename Args>
+int check_gated(const Args* a) {
+  if (const int st = check_shape(a)) return st;
+  if (!(a->c > 0.0f) || !isfinite(a->c)) return SSM_ERR_SHAPE;
+  if (bad_dtype(a->io_dtype)) return SSM_ERR_DTYPE;
+  return check_limits(a);
 }
 
 int check_tokens(const Tokens* t, int n, int64_t esz) {
@@ -74,12 +82,12 @@ size_t ssm_state_cache_args_size(void) { return sizeof(ssm_state_cache_args); }
 size_t ssm_cached_update_args_size(void) { return sizeof(ssm_cached_update_args); }
 
 size_t ssm_gated_scan_workspace_size(const ssm_gated_args* a) {
-  if (!a || check_gated(a) != SSM_OK || a->batch == 0 || a->dim == 0) return 0;
+  if (!a || check_shape(a) != SSM_OK || check_limits(a) != SSM_OK || a->batch == 0 || a->dim == 0) return 0;
   return gated_workspace_bytes(*a);
 }
 
 size_t ssm_gated_scan_bwd_workspace_size(const ssm_gated_bwd_args* a) {
-  if (!a || check_gated(a) != SSM_OK || a->dim == 0) return 0;
+  if (!a || check_shape(a) != SSM_OK || check_limits(a) != SSM_OK || a->dim == 0) return 0;
   return gated_bwd_workspace_bytes(*a);
 }
 

@@ -158,6 +158,21 @@ def test_gated_forward_refusals():
     e(OK, out=addr(0) + 32 * 4, **half), e(ALIAS, out=addr(0) + 31 * 4, **half), e(ALIAS, out=addr(0) + 33 * 4, **half)
 
 
+@pytest.mark.parametrize("make,size", [(good_gated, ssm.gated_scan_workspace_size),
+                                       (good_bwd, ssm.gated_scan_bwd_workspace_size)])
+def test_gated_workspace_of_a_block_with_only_sizes(make, size):
+    """c and io_dtype are no sizes: unset or not yet right, they change nothing."""
+    a = make(L=3000, D=140)
+    bare = type(a)(batch=a.batch, seqlen=a.seqlen, dim=a.dim)
+    assert size(bare) >= size(a) > 0
+    bare.io_dtype, bare.c = 7, float("nan")
+    assert size(bare) >= size(a)
+    for field, value in (("batch", -1), ("dim", (1 << 26) + 1), ("seqlen", 1 << 31)):
+        b = type(a)(batch=a.batch, seqlen=a.seqlen, dim=a.dim)
+        setattr(b, field, value)
+        assert size(b) == 0
+
+
 @pytest.mark.parametrize("batch,L,ss,sb", [(2, 64, 128, 64), (3, 1, 7, 64), (1, 64, 64, 7), (2, 64, 64, 64 * 64 + 192),
                                            (5, 9, 5 * 64, 64)])
 def test_slices_of_one_tensor_interleave_in_any_order(batch, L, ss, sb):
