@@ -430,9 +430,10 @@ typedef struct ssm_gated_args {
  *   dx, dgate_a, dgate_x : like x, io_dtype, dim stride 1.
  *   dlam    : (dim) fp32, summed over all tokens.
  *   dh0     : like h0, fp32; NULL: not wanted.
- * Where a_t rounds to 1 and its input scale to 0, the derivative of the square
- * root is taken as 0.  All sums run in a fixed order: every output is the same
- * bits from run to run.
+ * Where 1 - a_t^2 is below 2^-126, 2^63 stands for the reciprocal of its root
+ * (infinite at gate_a = -inf, where dgate_a is 0 and dlam gets nothing, as
+ * sigma(gate_a) is 0).  All sums run in fp32 and in a fixed order: every output
+ * is the same bits from run to run.
  * Sizes, aliasing and workspace (ssm_gated_scan_bwd_workspace_size(), always
  * required) as for the forward. */
 typedef struct ssm_gated_bwd_args {

@@ -11,10 +11,12 @@
 // for them, measured 19.7 us with two and 21.5 with four against 20.0 at
 // 256 x 5120 x 16; A's rows come from L2 anyway.)
 //
-// 256 x 5120 x 16 states move 53 MB a step, 10 us of memory time, where the
-// fp32 update moves 178 MB; 327 vector instructions a wavefront, a fifth of them
+// 256 x 5120 x 16 states move 55 MB a step, 9.3 us of memory time, where the
+// fp32 update moves 179 MB; 327 vector instructions a wavefront, a fifth of them
 // the generator's, are 11 us of issue.  A wavefront loads, computes and stores
-// once, six of them a SIMD: 19.3 us.
+// once, seven of them a SIMD: 19.1 us, 17.4 rounded to nearest.  With 32 states 36.4
+// us (97 MB); with 64, four or two wavefronts a SIMD for a lane's 109 to 212
+// registers, 87.6 (184 MB).
 #include "slots.h"
 #include "state_cache.h"
 

@@ -28,9 +28,12 @@
 // are filled with kNoWord before the kernel, which no published pair equals:
 // its low half would be one particular NaN, and NaNs are published as another.
 // Bound by memory traffic (8 bytes a value forward in bf16, 16 in fp32; 14 and
-// 28 backward) with the vector units about two thirds busy: 262,144 x 1536 bf16
-// forward 574 us, 5.6 TB/s; 4 x 4096 x 5120 bf16 forward 133 us and backward
-// 231 us, 5.4 and 5.3 TB/s.
+// 28 backward) with the vector units about two thirds busy, where there are many
+// groups of channels and rows begin on cache lines: a call of 262,144 x 1536 bf16
+// takes 576 us forward (5.6 TB/s), one of 4 x 4096 x 5120 bf16 366 us forward and
+// backward (5.0 TB/s).  Few groups of channels are bound by the hops of the carry
+// (2,052,244 x 31 bf16 forward 241 us for 0.5 GB), rows off the lines by lines that
+// two workgroups share (9 x 1386 x 1796 bf16 forward and backward 153 us for 0.5 GB).
 #pragma once
 
 #include "gated_math.h"

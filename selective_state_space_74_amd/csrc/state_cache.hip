@@ -1,14 +1,15 @@
 // state_cache.hip -- writing recurrent states to a quantised cache and reading
 // them back, for gfx950.  Formats: state_cache.h.
 //
-// Both are bound by memory traffic: 4 bytes (fp32) against 1 or 1/2 a value,
-// and a scale byte a block.  A lane takes 4 consecutive values of a block, so
+// Both move 4 bytes (fp32) against 1 or 1/2 a value, and a scale byte a block.  A lane takes 4 consecutive values of a block, so
 // that the lanes of a block (8 for 32 values, fewer for shorter rows) read or
 // write 16 bytes each in one run, and the block's maximum is two or three DPP
 // steps.  Which row of the batch a workgroup has comes from the grid; only the
 // row's place in the cache waits for its slot.  64 x 5120 x 16 fp32 states to
-// int8: 7.9 us written and 6.7 us read (27 MB, 3.4 and 4.0 TB/s); 24 x 2048 x 128
-// to e2m1 8.7 and 7.6 us.
+// int8: 7.7 us written and 6.5 us read (27 MB, 3.4 and 4.1 TB/s); 24 x 2048 x 128
+// to e2m1 8.6 and 7.8 us.  About 2.6 us of each are the way from the slot to the
+// values, there with next to no data too; the rest is memory traffic: 256 x 5120 x
+// 16 to int8 take 22.9 and 17.3 us (106 MB, 4.6 and 6.1 TB/s).
 #include "state_cache.h"
 
 namespace ssm {
