@@ -823,6 +823,8 @@ class _Current:
 @contextlib.contextmanager
 def _switched(device, stream):
     torch = _torch()
+    if hasattr(stream, "device") and stream.device.index != device:
+        raise ValueError(f"stream is of {stream.device}, the tensors are on device {device}")
     with torch.cuda.device(device):
         if stream is None:
             yield torch.cuda.current_stream().cuda_stream
@@ -980,6 +982,8 @@ def gated_scan_bwd(dout, x, gate_a, gate_x, lam, checkpoints, c=8.0, h0=None, cu
     """Gradients of gated_scan_fwd for the upstream gradient dout on out (and
     dlast on last_state), from the checkpoints that forward wrote.  Returns a
     dict: dx, dgate_a, dgate_x (like x), dlam (fp32) and, with h0, dh0 (fp32).
+    The inputs are those that the forward read; h0 too, so not a tensor that it
+    has since carried in place.
     Rows of tokens outside every sequence are zero.  Every output is the same
     bits from run to run.  `workspace`: as for gated_scan_fwd."""
     torch = _torch()

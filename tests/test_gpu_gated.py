@@ -460,6 +460,19 @@ def test_another_stream_and_two_at_once():
         assert torch.equal(o, wo) and torch.equal(l, wl) and all(torch.equal(g[k], wg[k]) for k in g)
 
 
+def test_a_stream_by_its_handle():
+    t = make((2, 500), 70, "f32", seed=44)
+    want = forward(t)
+    g = backward(t, want[2])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = forward(t, stream=s.cuda_stream)
+    s.synchronize()   # the checkpoints were allocated on the current stream
+    got += (backward(t, got[2], stream=s.cuda_stream),)
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and all(torch.equal(got[3][k], g[k]) for k in g)
+
+
 def test_captured_and_replayed():
     t = make((1, 4000), 192, "bf16", seed=23)
     cu = torch.tensor([0, 5, 5, 2222, 4000], dtype=torch.int32, device=DEV)

@@ -321,6 +321,17 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
     assert ssm.gated_checkpoint_shape((2, 33, 7)) == (2, 5, 7) and ssm.gated_checkpoint_shape((0, 7)) == (0, 7)
 
 
+def test_binding_refuses_a_stream_of_another_device():
+    torch = pytest.importorskip("torch")
+
+    class Stream:
+        cuda_stream, device = 16, torch.device("cuda", 1)
+
+    with pytest.raises(ValueError, match="device"):
+        with ssm._on(0, Stream()):
+            pass
+
+
 def test_autograd_op_writes_checkpoints_only_for_a_backward(monkeypatch):
     torch = pytest.importorskip("torch")
     asked = []
