@@ -501,6 +501,39 @@ def test_captured_and_replayed():
         assert torch.equal(o, eo) and torch.equal(l, el) and all(torch.equal(g[k], eg[k]) for k in g)
 
 
+@pytest.mark.parametrize("D,L", [(12, 90), (130, 100), (130, 900)])
+def test_state_carried_in_place_through_two_captured_graphs(D, L):
+    """A layer's chunk and token, the state carried in place by both, captured
+    twice and replayed on two streams at once."""
+    def layer(t, h):
+        out = ssm.gated_scan_fwd(t["x"], t["gate_a"], t["gate_x"], t["lam"], h0=h, last_state=h)
+        return out, ssm.gated_state_update(h, *(t[k][:, 0] for k in ("x", "gate_a", "gate_x")), t["lam"])
+
+    ts = [make((3, L), D, "f32", seed=50 + i) for i in range(2)]
+    hs, streams = [t["h0"].clone() for t in ts], [torch.cuda.Stream() for _ in ts]
+    graphs, got = [], []
+    for t, h, s in zip(ts, hs, streams):
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            layer(t, h.clone())
+        torch.cuda.current_stream().wait_stream(s)
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            got.append(layer(t, h))
+    for h, t in zip(hs, ts):
+        h.copy_(t["h0"])
+    eager = [t["h0"].clone() for t in ts]
+    for _ in range(4):
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for t, h, e, (out, y) in zip(ts, hs, eager, got):
+            eout, ey = layer(t, e)
+            assert torch.equal(out, eout) and torch.equal(y, ey) and torch.equal(h, e)
+
+
 def test_workspace_kept_across_calls_of_different_sizes():
     ws = torch.full((64 << 20,), 255, dtype=torch.uint8, device=DEV)
     for L in (3000, 40, 5000, 3000):
