@@ -2,9 +2,11 @@
  * ssm.h -- C ABI of libssm.so, the gfx950 (MI355X) selective-scan library.
  *
  * Four operations from the Mamba pages (cited by page title and section), and
- * two families next to them: a gated linear recurrence (ssm_gated_*) and a
+ * three families next to them: a gated linear recurrence (ssm_gated_*), a
  * quantised cache of recurrent states (ssm_state_cache_*,
- * ssm_selective_state_update_cached), each described at its arguments.
+ * ssm_selective_state_update_cached), and what the Mamba-2 layer needs around
+ * its prefill (ssm_token_conv_*, ssm_ssd_state_update), each described at its
+ * arguments.
  *
  *   ssm_selective_scan_fwd  -- prefill.  For every batch row b, channel d and
  *     state index n, with Delta_t = softplus(delta_t + bias[d]) (Mamba paper
@@ -557,6 +559,138 @@ typedef struct ssm_cached_update_args {
   int64_t ngroups;    /* B/C groups; 0 or 1: one group */
 } ssm_cached_update_args;
 
+/* Arguments of the causal depthwise convolution over tokens: the layer's short
+ * convolution in the token-major layout of the SSD layer, whose x, B and C go
+ * through it side by side.  For every sequence and channel d
+ *     pre_t = bias[d] + sum_{k<d_conv} weight[d,k] x_{t-(d_conv-1)+k}
+ *     out_t = silu(pre_t)   (pre_t without conv_silu)
+ * the inputs before a sequence being those of state_in, or zero.
+ *   x, out     : (batch, seqlen, dim), dim stride 1; element (b, t, d) at
+ *                ptr[b * *_batch_stride + t * *_seq_stride + d].
+ *   weight     : (dim, d_conv) fp32, contiguous; 1 <= d_conv <= SSM_MAX_CONV.
+ *   bias       : (dim) fp32; NULL means 0.
+ *   cu_seqlens : NULL: every batch row is one sequence.  Otherwise batch must be
+ *                1 and the row holds nseq packed sequences, as in
+ *                ssm_gated_args: int32, device memory, nseq + 1 entries, not
+ *                decreasing.  Tokens of no sequence: their rows of out are left
+ *                as they are, or set to zero with zero_outside.  The values are
+ *                not checked on the host; values that break these rules give
+ *                unspecified results but no access outside the tensors.
+ *   state_in, state_out : (nseq, dim, d_conv), or (batch, dim, d_conv) without
+ *                cu_seqlens; fp32, contiguous.  state_in holds the inputs before
+ *                the sequence (element k = x_{k-d_conv}), NULL means zeros;
+ *                state_out receives the last d_conv inputs (from state_in where
+ *                the sequence is shorter), NULL: not wanted.  It is the state
+ *                that ssm_token_conv_update continues from.
+ * Sizes: zero sizes are no-ops, but that empty sequences still set state_out;
+ * seqlen below 2^31 - 64, dim at most 2^26, nseq below 2^29, and batch *
+ * ceil(seqlen / 16) * ceil(dim / 64) below 2^28 (SSM_ERR_UNSUPPORTED past
+ * that).
+ * Precision: fp32 arithmetic; out is rounded once.
+ * Aliasing: out and state_out must not overlap any input or each other. */
+typedef struct ssm_token_conv_args {
+  int64_t batch, seqlen, dim, nseq;
+  int32_t io_dtype;      /* ssm_dtype */
+  int32_t d_conv;
+  int32_t conv_silu;     /* bool */
+  int32_t zero_outside;  /* bool */
+  const void* x;       int64_t x_batch_stride, x_seq_stride;
+  const float* weight;
+  const float* bias;
+  const int32_t* cu_seqlens;
+  const float* state_in;
+  float* state_out;
+  void* out;           int64_t out_batch_stride, out_seq_stride;
+} ssm_token_conv_args;
+
+/* Arguments of its backward.  The forward inputs keep their meaning and must be
+ * the ones the forward ran with; the convolution is computed again from them.
+ *   dout       : like out.  dstate_out: like state_out, NULL means 0.
+ * Outputs, fully overwritten (tokens of no sequence get zeros):
+ *   dx         : like x, io_dtype, dim stride 1.
+ *   dweight    : (dim, d_conv) fp32, dbias : (dim) fp32 (NULL: not wanted),
+ *                summed over all tokens in fp32 and in a fixed order.
+ *   dstate_in  : like state_in, fp32; NULL: not wanted.
+ * Sizes and aliasing as for the forward; no output may overlap another.
+ * Workspace: device scratch owned by the caller, 4-byte aligned, of at least
+ * ssm_token_conv_bwd_workspace_size() bytes (required: SSM_ERR_SCRATCH
+ * otherwise), not overlapping any tensor and not in use by another call that
+ * may run at the same time. */
+typedef struct ssm_token_conv_bwd_args {
+  int64_t batch, seqlen, dim, nseq;
+  int32_t io_dtype;    /* ssm_dtype */
+  int32_t d_conv;
+  int32_t conv_silu;   /* bool */
+  const void* x;       int64_t x_batch_stride, x_seq_stride;
+  const float* weight;
+  const float* bias;
+  const int32_t* cu_seqlens;
+  const float* state_in;
+  const void* dout;    int64_t dout_batch_stride, dout_seq_stride;
+  const float* dstate_out;
+  void* dx;            int64_t dx_batch_stride, dx_seq_stride;
+  float* dweight;
+  float* dbias;
+  float* dstate_in;
+  void* workspace;     size_t workspace_bytes;
+} ssm_token_conv_bwd_args;
+
+/* Arguments of its single-token step on a pool of states.
+ *   state  : (nslots, dim, d_conv) fp32, contiguous within a slot, shifted IN
+ *            PLACE by one token (oldest dropped, x appended).
+ *   x, out : (batch, dim), dim stride 1.
+ *   slots  : int32 (batch) in device memory: row b's state is state[slots[b]].
+ *            NULL: row b's state is state[b] (batch must not exceed nslots).
+ * A row whose slot is outside [0, nslots) (a padded batch) touches no state and
+ * gets a zero row of out.  Rows that name the same slot are taken in the order
+ * of the rows.  Sizes: batch at most 65535, dim at most 2^26.
+ * Aliasing: out and state must not overlap any input or each other. */
+typedef struct ssm_token_conv_update_args {
+  int64_t batch, nslots, dim;
+  int32_t io_dtype;    /* ssm_dtype */
+  int32_t d_conv;
+  int32_t conv_silu;   /* bool */
+  float* state;        int64_t state_slot_stride;
+  const void* x;       int64_t x_batch_stride;
+  const float* weight;
+  const float* bias;
+  const int32_t* slots;
+  void* out;           int64_t out_batch_stride;
+} ssm_token_conv_update_args;
+
+/* Largest state size of the SSD layer's single-token step. */
+#define SSM_MAX_SSD_STEP_DSTATE 256
+
+/* Arguments of the single-token step of the Mamba-2 SSM (see ssm_ssd_args for
+ * the recurrence) on a pool of states.
+ *   state  : (nslots, nheads, headdim, dstate) fp32, contiguous within a slot,
+ *            updated IN PLACE.
+ *   x, z, out : (batch, nheads, headdim), headdim stride 1; z NULL: no gate.
+ *   dt     : (batch, nheads), head stride 1, io_dtype.
+ *   B, C   : (batch, ngroups, dstate), state stride 1; head h reads group
+ *            h / (nheads / ngroups); ngroups 0 or 1 is one group.
+ *   A, D, dt_bias : (nheads) fp32; D and dt_bias NULL mean 0.
+ *   slots  : as in ssm_token_conv_update_args.
+ * Sizes: batch at most 65535, nheads * headdim * dstate below 2^31;
+ * 1 <= dstate <= SSM_MAX_SSD_STEP_DSTATE.
+ * Aliasing: out and state must not overlap any input or each other. */
+typedef struct ssm_ssd_update_args {
+  int64_t batch, nslots, nheads, headdim, ngroups, dstate;
+  int32_t io_dtype;    /* ssm_dtype */
+  int32_t dt_softplus; /* bool */
+  float* state;        int64_t state_slot_stride;
+  const void* x;       int64_t x_batch_stride, x_head_stride;
+  const void* dt;      int64_t dt_batch_stride;
+  const void* z;       int64_t z_batch_stride, z_head_stride;
+  const void* B;       int64_t B_batch_stride, B_group_stride;
+  const void* C;       int64_t C_batch_stride, C_group_stride;
+  const float* A;
+  const float* D;
+  const float* dt_bias;
+  const int32_t* slots;
+  void* out;           int64_t out_batch_stride, out_head_stride;
+} ssm_ssd_update_args;
+
 /* ABI version of the loaded library (SSM_ABI_VERSION at build time). */
 int ssm_abi_version(void);
 
@@ -570,6 +704,10 @@ size_t ssm_gated_bwd_args_size(void);
 size_t ssm_gated_update_args_size(void);
 size_t ssm_state_cache_args_size(void);
 size_t ssm_cached_update_args_size(void);
+size_t ssm_token_conv_args_size(void);
+size_t ssm_token_conv_bwd_args_size(void);
+size_t ssm_token_conv_update_args_size(void);
+size_t ssm_ssd_update_args_size(void);
 
 /* Workspace bytes the scan can use for this argument block (0 when it would
  * run single-segment anyway): for G segments, with BD = batch * dim and
@@ -602,6 +740,11 @@ size_t ssm_scan_bwd_workspace_size(const ssm_scan_bwd_args* args);
 size_t ssm_gated_scan_workspace_size(const ssm_gated_args* args);
 size_t ssm_gated_scan_bwd_workspace_size(const ssm_gated_bwd_args* args);
 
+/* Workspace bytes the backward of the token convolution needs: partial sums of
+ * dweight and dbias, (d_conv + 1) * dim fp32 values for each run of tokens.
+ * Reads only sizes; pure host code. */
+size_t ssm_token_conv_bwd_workspace_size(const ssm_token_conv_bwd_args* args);
+
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char* ssm_status_string(int status);
 
@@ -617,6 +760,10 @@ int ssm_validate_gated_update(const ssm_gated_update_args* args);
 int ssm_validate_state_cache_write(const ssm_state_cache_args* args);
 int ssm_validate_state_cache_read(const ssm_state_cache_args* args);
 int ssm_validate_cached_update(const ssm_cached_update_args* args);
+int ssm_validate_token_conv(const ssm_token_conv_args* args);
+int ssm_validate_token_conv_bwd(const ssm_token_conv_bwd_args* args);
+int ssm_validate_token_conv_update(const ssm_token_conv_update_args* args);
+int ssm_validate_ssd_update(const ssm_ssd_update_args* args);
 
 /* Prefill scan (see ssm_scan_args).  Validates, then launches on `stream`. */
 int ssm_selective_scan_fwd(const ssm_scan_args* args, void* stream);
@@ -661,6 +808,15 @@ int ssm_gated_state_update(const ssm_gated_update_args* args, void* stream);
 int ssm_state_cache_write(const ssm_state_cache_args* args, void* stream);
 int ssm_state_cache_read(const ssm_state_cache_args* args, void* stream);
 int ssm_selective_state_update_cached(const ssm_cached_update_args* args, void* stream);
+
+/* Causal convolution over tokens, its backward and its single-token step (see
+ * ssm_token_conv_args, ssm_token_conv_bwd_args, ssm_token_conv_update_args). */
+int ssm_token_conv_fwd(const ssm_token_conv_args* args, void* stream);
+int ssm_token_conv_bwd(const ssm_token_conv_bwd_args* args, void* stream);
+int ssm_token_conv_update(const ssm_token_conv_update_args* args, void* stream);
+
+/* Single-token step of the Mamba-2 SSM (see ssm_ssd_update_args). */
+int ssm_ssd_state_update(const ssm_ssd_update_args* args, void* stream);
 
 #ifdef __cplusplus
 }

@@ -28,6 +28,16 @@ CPU fallback, and importing a missing library raises.
     gated_state_update(state, x, gate_a, gate_x, lam, c=8.0, slots=None) -> out
         (a gated linear recurrence with one state per channel, token-major,
         batched or packed: prefill, gradients, and its single-token step)
+    token_conv_fwd(x, weight, bias=None, silu=True, state_in=None, cu_seqlens=None,
+                   return_state=False) -> out, or (out, state)
+    token_conv_bwd(dout, x, weight, ...) -> dict of gradients
+    token_conv(x, weight, ...)  (the two as a differentiable torch op)
+    token_conv_update(state, x, weight, bias=None, silu=True, slots=None) -> out
+        (the causal depthwise convolution, token-major, batched or packed:
+        prefill, gradients, and its single-token step)
+    ssd_state_update(state, x, dt, A, B, C, D=None, z=None, dt_bias=None,
+                     dt_softplus=True, slots=None) -> out
+        (the Mamba-2 SSM's single-token step on a pool of states)
 
 Shapes (N = dstate, 1..64): u, delta, z (batch, dim, L) with time stride 1;
 B, C (batch, N, L), or (batch, G, N, L) for G groups of dim // G channels,
@@ -204,6 +214,58 @@ class CachedUpdateArgs(ctypes.Structure):
                 ("slots", _P), ("seed", _P), ("ngroups", _I64)]
 
 
+class TokenConvArgs(ctypes.Structure):
+    """Mirror of ssm_token_conv_args."""
+    _fields_ = [("batch", _I64), ("seqlen", _I64), ("dim", _I64), ("nseq", _I64),
+                ("io_dtype", _I32), ("d_conv", _I32), ("conv_silu", _I32), ("zero_outside", _I32),
+                ("x", _P), ("x_batch_stride", _I64), ("x_seq_stride", _I64),
+                ("weight", _P), ("bias", _P), ("cu_seqlens", _P), ("state_in", _P), ("state_out", _P),
+                ("out", _P), ("out_batch_stride", _I64), ("out_seq_stride", _I64)]
+
+
+class TokenConvBwdArgs(ctypes.Structure):
+    """Mirror of ssm_token_conv_bwd_args."""
+    _fields_ = [("batch", _I64), ("seqlen", _I64), ("dim", _I64), ("nseq", _I64),
+                ("io_dtype", _I32), ("d_conv", _I32), ("conv_silu", _I32),
+                ("x", _P), ("x_batch_stride", _I64), ("x_seq_stride", _I64),
+                ("weight", _P), ("bias", _P), ("cu_seqlens", _P), ("state_in", _P),
+                ("dout", _P), ("dout_batch_stride", _I64), ("dout_seq_stride", _I64), ("dstate_out", _P),
+                ("dx", _P), ("dx_batch_stride", _I64), ("dx_seq_stride", _I64),
+                ("dweight", _P), ("dbias", _P), ("dstate_in", _P),
+                ("workspace", _P), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class TokenConvUpdateArgs(ctypes.Structure):
+    """Mirror of ssm_token_conv_update_args."""
+    _fields_ = [("batch", _I64), ("nslots", _I64), ("dim", _I64),
+                ("io_dtype", _I32), ("d_conv", _I32), ("conv_silu", _I32),
+                ("state", _P), ("state_slot_stride", _I64), ("x", _P), ("x_batch_stride", _I64),
+                ("weight", _P), ("bias", _P), ("slots", _P), ("out", _P), ("out_batch_stride", _I64)]
+
+
+class SsdUpdateArgs(ctypes.Structure):
+    """Mirror of ssm_ssd_update_args."""
+    _fields_ = [("batch", _I64), ("nslots", _I64), ("nheads", _I64), ("headdim", _I64),
+                ("ngroups", _I64), ("dstate", _I64), ("io_dtype", _I32), ("dt_softplus", _I32),
+                ("state", _P), ("state_slot_stride", _I64),
+                ("x", _P), ("x_batch_stride", _I64), ("x_head_stride", _I64),
+                ("dt", _P), ("dt_batch_stride", _I64),
+                ("z", _P), ("z_batch_stride", _I64), ("z_head_stride", _I64),
+                ("B", _P), ("B_batch_stride", _I64), ("B_group_stride", _I64),
+                ("C", _P), ("C_batch_stride", _I64), ("C_group_stride", _I64),
+                ("A", _P), ("D", _P), ("dt_bias", _P), ("slots", _P),
+                ("out", _P), ("out_batch_stride", _I64), ("out_head_stride", _I64)]
+
+
+# Entry points by argument block: (block, launching functions, validating ones,
+# workspace size functions, without their prefixes), for the families after the
+# scans.
+_MAMBA2 = ((TokenConvArgs, "token_conv_fwd", "token_conv", None),
+           (TokenConvBwdArgs, "token_conv_bwd", "token_conv_bwd", "token_conv_bwd"),
+           (TokenConvUpdateArgs, "token_conv_update", "token_conv_update", None),
+           (SsdUpdateArgs, "ssd_state_update", "ssd_update", None))
+
+
 class SSMError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -263,6 +325,14 @@ def lib():
         for name, T in (("gated_scan", GatedArgs), ("gated_scan_bwd", GatedBwdArgs)):
             f = getattr(L, "ssm_%s_workspace_size" % name)
             f.restype, f.argtypes = ctypes.c_size_t, [ctypes.POINTER(T)]
+        for T, entry, check, size in _MAMBA2:
+            f = getattr(L, "ssm_" + entry)
+            f.restype, f.argtypes = ctypes.c_int, [ctypes.POINTER(T), _P]
+            f = getattr(L, "ssm_validate_" + check)
+            f.restype, f.argtypes = ctypes.c_int, [ctypes.POINTER(T)]
+            if size:
+                f = getattr(L, "ssm_%s_workspace_size" % size)
+                f.restype, f.argtypes = ctypes.c_size_t, [ctypes.POINTER(T)]
         if L.ssm_abi_version() != SSM_ABI_VERSION:
             raise ImportError(f"libssm.so ABI {L.ssm_abi_version()} != {SSM_ABI_VERSION}")
         if (L.ssm_scan_args_size() != ctypes.sizeof(ScanArgs)
@@ -271,7 +341,8 @@ def lib():
                 or L.ssm_ssd_args_size() != ctypes.sizeof(SsdArgs)):
             raise ImportError("libssm.so argument struct layout differs from the binding")
         for name, T in (("gated", GatedArgs), ("gated_bwd", GatedBwdArgs), ("gated_update", GatedUpdateArgs),
-                        ("state_cache", StateCacheArgs), ("cached_update", CachedUpdateArgs)):
+                        ("state_cache", StateCacheArgs), ("cached_update", CachedUpdateArgs),
+                        *((check, T) for T, _, check, _ in _MAMBA2)):
             f = getattr(L, "ssm_%s_args_size" % name)
             f.restype = ctypes.c_size_t
             if f() != ctypes.sizeof(T):
@@ -1220,4 +1291,204 @@ def selective_state_update_cached(codes, scales, x, dt, A, B, C, D=None, z=None,
                              C.data_ptr(), C.stride(0), C.stride(1) if G else 0, A.data_ptr(), A.stride(0), D_p, bias_p,
                              *_row_tokens("out", out, shape, io, dev), _ptr(slots), _ptr(seed), G)
         _launch("ssm_selective_state_update_cached", a, s)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# the Mamba-2 layer's convolution and single-token steps
+
+def validate_token_conv(args: TokenConvArgs) -> int:
+    return lib().ssm_validate_token_conv(ctypes.byref(args))
+
+
+def validate_token_conv_bwd(args: TokenConvBwdArgs) -> int:
+    return lib().ssm_validate_token_conv_bwd(ctypes.byref(args))
+
+
+def validate_token_conv_update(args: TokenConvUpdateArgs) -> int:
+    return lib().ssm_validate_token_conv_update(ctypes.byref(args))
+
+
+def validate_ssd_update(args: SsdUpdateArgs) -> int:
+    return lib().ssm_validate_ssd_update(ctypes.byref(args))
+
+
+def token_conv_bwd_workspace_size(args: TokenConvBwdArgs) -> int:
+    return lib().ssm_token_conv_bwd_workspace_size(ctypes.byref(args))
+
+
+def _conv_width(weight, dim):
+    if weight.dim() != 2 or weight.shape[0] != dim or not 1 <= weight.shape[1] <= MAX_CONV:
+        raise ValueError(f"weight must be (dim, d_conv) with d_conv 1 to {MAX_CONV}")
+    return weight.shape[1]
+
+
+def token_conv_fwd(x, weight, bias=None, silu=True, state_in=None, cu_seqlens=None, return_state=False,
+                   out=None, state_out=None, stream=None):
+    """Causal depthwise convolution over whole sequences on the GPU:
+        out_t = silu(bias + sum_k weight[:, k] x_{t-(K-1)+k})     (no SiLU with silu=False)
+
+    x: (batch, L, dim), or (tokens, dim) with cu_seqlens, the int32 device
+    tensor of nseq + 1 sequence bounds; dim stride 1, any token stride, float32
+    or bfloat16.  weight (dim, K) fp32, K from 1 to 8; bias (dim,) fp32.
+    state_in (batch or nseq, dim, K) fp32: the inputs before each sequence,
+    element k being x_{k-K}; None: zeros.  Returns out, or (out, state): the
+    state each sequence leaves, its last K inputs (an empty sequence's is its
+    state_in), from which token_conv_update goes on.  Tokens outside every
+    sequence: zero rows in an `out` made here, left as they were in one that is
+    given."""
+    torch = _torch()
+    code = _io_code(x)
+    shape, dev, io = x.shape, _gpu("x", x), x.dtype
+    batch, L, n, nseq, cu = _gated_sizes(x, cu_seqlens)
+    dim = shape[-1]
+    K = _conv_width(weight, dim)
+    inputs = _tokens("x", x, shape, io, dev)
+    params = (_fp32("weight", weight, (dim, K), dev), _fp32("bias", bias, (dim,), dev), cu,
+              _fp32("state_in", state_in, (n, dim, K), dev))
+    with _on(dev, stream) as s:
+        made = out is None
+        if made:
+            out = _empty(x, shape, io, dev)
+        if return_state and state_out is None:
+            state_out = torch.empty((n, dim, K), dtype=torch.float32, device=dev)
+        a = TokenConvArgs(batch, L, dim, nseq, code, K, bool(silu), made, *inputs, *params,
+                          _fp32("state_out", state_out, (n, dim, K), dev), *_tokens("out", out, shape, io, dev))
+        _launch("ssm_token_conv_fwd", a, s)
+    return (out, state_out) if return_state else out
+
+
+def token_conv_bwd(dout, x, weight, bias=None, silu=True, state_in=None, cu_seqlens=None, dstate=None,
+                   stream=None, workspace=None):
+    """Gradients of token_conv_fwd for the upstream gradient dout on out (and
+    dstate on the state that it returns).  Returns a dict: dx (like x), dweight,
+    dbias (fp32; with or without a bias) and, with state_in, dstate_in (fp32).
+    Rows of tokens outside every sequence are zero.  Every output is the same
+    bits from run to run.  `workspace`: a device tensor reused across calls, by
+    one call at a time; None allocates one."""
+    torch = _torch()
+    code = _io_code(x)
+    shape, dev, io = x.shape, _gpu("x", x), x.dtype
+    batch, L, n, nseq, cu = _gated_sizes(x, cu_seqlens)
+    dim = shape[-1]
+    K = _conv_width(weight, dim)
+    inputs = _tokens("x", x, shape, io, dev)
+    params = (_fp32("weight", weight, (dim, K), dev), _fp32("bias", bias, (dim,), dev), cu,
+              _fp32("state_in", state_in, (n, dim, K), dev))
+    upstream = _tokens("dout", dout, shape, io, dev)
+    dstate_p = _fp32("dstate", dstate, (n, dim, K), dev)
+    with _on(dev, stream) as s:
+        dx = _empty(dout, shape, io, dev)
+        g = dict(dx=dx, dweight=torch.empty_like(weight), dbias=torch.empty((dim,), dtype=torch.float32, device=dev))
+        if state_in is not None:
+            g["dstate_in"] = torch.empty_like(state_in)
+        a = TokenConvBwdArgs(batch, L, dim, nseq, code, K, bool(silu), *inputs, *params, *upstream, dstate_p,
+                             dx.data_ptr(), L * dim, dim, g["dweight"].data_ptr(), g["dbias"].data_ptr(),
+                             _ptr(g.get("dstate_in")))
+        workspace = _set_workspace(a, token_conv_bwd_workspace_size(a), workspace, dev)
+        _launch("ssm_token_conv_bwd", a, s)
+    return g
+
+
+def token_conv(x, weight, bias=None, silu=True, state_in=None, cu_seqlens=None, return_state=False):
+    """token_conv_fwd as a differentiable torch op: gradients flow to x, weight,
+    bias and state_in, from out and from the returned state."""
+    torch = _torch()
+
+    class _TokenConv(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, weight, bias, state_in):
+            ctx.set_materialize_grads(False)
+            out, state = token_conv_fwd(x, weight, bias, silu=silu, state_in=state_in, cu_seqlens=cu_seqlens,
+                                        return_state=True)
+            ctx.save_for_backward(x, weight, bias, state_in, cu_seqlens)
+            return out, state
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, dout, dstate):
+            x, weight, bias, state_in, cu = ctx.saved_tensors
+            dout = torch.zeros_like(x, memory_format=torch.contiguous_format) if dout is None else dout.contiguous()
+            g = token_conv_bwd(dout, x, weight, bias, silu=silu, state_in=state_in, cu_seqlens=cu,
+                               dstate=None if dstate is None else dstate.contiguous())
+            return g["dx"], g["dweight"], None if bias is None else g["dbias"], g.get("dstate_in")
+
+    out, state = _TokenConv.apply(x, weight, bias, state_in)
+    return (out, state) if return_state else out
+
+
+def token_conv_update(state, x, weight, bias=None, silu=True, slots=None, out=None, stream=None):
+    """Single-token step of the convolution; `state` (nslots, dim, K) fp32,
+    contiguous within a slot, is shifted in place.  x: (batch, dim).  slots:
+    int32 (batch,), the pool row of each batch row (None: row b on state b); a
+    slot outside the pool marks a padding row (no state touched, zero out), and
+    rows naming the same slot are taken in order."""
+    torch = _torch()
+    if state.dim() != 3 or x.dim() != 2:
+        raise ValueError("state must be (nslots, dim, d_conv) and x (batch, dim)")
+    code = _io_code(x)
+    (nslots, dim, K), dev, io = state.shape, _gpu("state", state), x.dtype
+    if _conv_width(weight, dim) != K:
+        raise ValueError("state and weight must have the same d_conv")
+    shape = (x.shape[0], dim)
+    _placed("state", state, torch.float32, dev)
+    if not state.is_contiguous() and not _inner_contiguous(state):
+        raise ValueError("state must be contiguous within a slot")
+    inputs = _row_tokens("x", x, shape, io, dev)
+    params = _fp32("weight", weight, (dim, K), dev), _fp32("bias", bias, (dim,), dev)
+    _check_slots(slots, shape[0], nslots, dev)
+    with _on(dev, stream) as s:
+        if out is None:
+            out = _empty(x, shape, io, dev)
+        a = TokenConvUpdateArgs(shape[0], nslots, dim, code, K, bool(silu), state.data_ptr(), state.stride(0), *inputs,
+                                *params, _ptr(slots), *_row_tokens("out", out, shape, io, dev))
+        _launch("ssm_token_conv_update", a, s)
+    return out
+
+
+def _inner_rows(name, t, shape, dtype, device):
+    """Pointer and the first two strides of a 3-D tensor with last stride 1,
+    (None, 0, 0) for None."""
+    if t is None:
+        return None, 0, 0
+    _placed(name, t, dtype, device)
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    st = t.stride()
+    if st[2] != 1 and shape[2] > 1:
+        raise ValueError(f"{name} must have a unit innermost stride")
+    return t.data_ptr(), st[0], st[1]
+
+
+def ssd_state_update(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=True, slots=None, out=None,
+                     stream=None):
+    """Single-token step of the Mamba-2 SSM (ssd_scan_fwd for one token a row);
+    `state` (nslots, nheads, headdim, dstate) fp32, contiguous within a slot, is
+    updated in place.  x, z: (batch, nheads, headdim); dt: (batch, nheads); B, C:
+    (batch, ngroups, dstate), dstate up to 256; A, D, dt_bias: (nheads,) fp32.
+    slots: as for token_conv_update."""
+    torch = _torch()
+    if state.dim() != 4 or x.dim() != 3 or B.dim() != 3:
+        raise ValueError("state must be (nslots, nheads, headdim, dstate), x (batch, nheads, headdim) and "
+                         "B (batch, ngroups, dstate)")
+    code = _io_code(x)
+    (nslots, H, P, N), dev, io = state.shape, _gpu("state", state), x.dtype
+    batch, G = x.shape[0], B.shape[1]
+    _placed("state", state, torch.float32, dev)
+    if not state.is_contiguous() and not _inner_contiguous(state):
+        raise ValueError("state must be contiguous within a slot")
+    shape = (batch, H, P)
+    if G < 1:
+        raise ValueError("B must have at least one group")
+    inputs = _inner_rows("x", x, shape, io, dev) + _row_tokens("dt", dt, (batch, H), io, dev) + \
+        _inner_rows("z", z, shape, io, dev) + _inner_rows("B", B, (batch, G, N), io, dev) + \
+        _inner_rows("C", C, (batch, G, N), io, dev)
+    params = _fp32("A", A, (H,), dev), _fp32("D", D, (H,), dev), _fp32("dt_bias", dt_bias, (H,), dev)
+    _check_slots(slots, batch, nslots, dev)
+    with _on(dev, stream) as s:
+        if out is None:
+            out = _empty(x, shape, io, dev)
+        a = SsdUpdateArgs(batch, nslots, H, P, G, N, code, bool(dt_softplus), state.data_ptr(), state.stride(0), *inputs,
+                          *params, _ptr(slots), *_inner_rows("out", out, shape, io, dev))
+        _launch("ssm_ssd_state_update", a, s)
     return out

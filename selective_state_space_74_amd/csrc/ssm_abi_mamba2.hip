@@ -1,0 +1,218 @@
+// ssm_abi_mamba2.hip -- the extern "C" surface of the token convolution and of
+// the Mamba-2 SSM's step: host-side validation (pure host code, no HIP call)
+// and dispatch.
+#include <stdint.h>
+
+#include "abi_checks.h"
+#include "ssm_internal.h"
+
+using namespace ssm;
+
+namespace {
+
+bool bad_dtype(int32_t dt) { return dt != SSM_F32 && dt != SSM_BF16; }
+
+constexpr int64_t kMaxDim = int64_t{1} << 26;
+constexpr int64_t kMaxPacked = int64_t{1} << 29;
+
+// A (batch, L, dim) tensor with its strides.
+struct Tokens {
+  const void* p;
+  int64_t sb, ss;
+};
+
+int check_tokens(const Tokens& t, int64_t esz) {
+  if (!t.p) return SSM_ERR_NULL;
+  if (t.sb < 0 || t.ss < 0) return SSM_ERR_STRIDE;
+  return misaligned(t.p, esz) ? SSM_ERR_ALIGN : SSM_OK;
+}
+
+// Whether rows of one output can share bytes; batch rows may interleave along
+// the sequence (a (L, batch, dim) layout).
+bool collide(const Tokens& t, int64_t batch, int64_t L, int64_t D) {
+  if (batch > 1 && L > 1 && t.ss >= batch * t.sb) return t.sb < D;
+  return rows_collide(batch, t.sb, L, t.ss, D);
+}
+
+// What the convolution and its backward check alike: sizes, and the limits on them.
+template <typename Args>
+int check_conv(const Args* a) {
+  if (a->batch < 0 || a->dim < 0 || a->seqlen < 0 || a->nseq < 0) return SSM_ERR_SHAPE;
+  if (a->cu_seqlens && a->batch != 1) return SSM_ERR_SHAPE;
+  if (a->d_conv < 1) return SSM_ERR_SHAPE;
+  if (bad_dtype(a->io_dtype)) return SSM_ERR_DTYPE;
+  if (a->d_conv > SSM_MAX_CONV || a->seqlen > kMaxSeqlen || a->dim > kMaxDim) return SSM_ERR_UNSUPPORTED;
+  if (a->cu_seqlens && a->nseq >= kMaxPacked) return SSM_ERR_UNSUPPORTED;
+  // a launch has less than 2^32 threads
+  const int64_t blocks = max((a->seqlen + 15) / 16, int64_t{1}) * max((a->dim + 63) / 64, int64_t{1});
+  return a->batch > ((int64_t{1} << 28) - 1) / blocks ? SSM_ERR_UNSUPPORTED : SSM_OK;
+}
+
+// No output may share bytes with an input or with another output.
+template <size_t NI, size_t NO>
+int check_apart(const Rows (&inputs)[NI], const Rows (&outputs)[NO]) {
+  for (const Rows& o : outputs) {
+    for (const Rows& i : inputs)
+      if (overlap(o, i)) return SSM_ERR_ALIAS;
+    for (const Rows& o2 : outputs)
+      if (&o2 != &o && overlap(o, o2)) return SSM_ERR_ALIAS;
+  }
+  return SSM_OK;
+}
+
+Rows flat(const void* p, int64_t n, int64_t esz) { return Rows{span1(p, n, esz)}; }
+
+}  // namespace
+
+extern "C" {
+
+size_t ssm_token_conv_args_size(void) { return sizeof(ssm_token_conv_args); }
+size_t ssm_token_conv_bwd_args_size(void) { return sizeof(ssm_token_conv_bwd_args); }
+size_t ssm_token_conv_update_args_size(void) { return sizeof(ssm_token_conv_update_args); }
+size_t ssm_ssd_update_args_size(void) { return sizeof(ssm_ssd_update_args); }
+
+size_t ssm_token_conv_bwd_workspace_size(const ssm_token_conv_bwd_args* a) {
+  if (!a) return 0;
+  ssm_token_conv_bwd_args s = *a;   // the size is that of either type
+  if (bad_dtype(s.io_dtype)) s.io_dtype = SSM_F32;
+  if (check_conv(&s) != SSM_OK || s.dim == 0) return 0;
+  return token_conv_bwd_workspace_bytes(s);
+}
+
+int ssm_validate_token_conv(const ssm_token_conv_args* a) {
+  if (!a) return SSM_ERR_NULL;
+  if (const int st = check_conv(a)) return st;
+  if (a->batch == 0 || a->dim == 0) return SSM_OK;
+  const int64_t B = a->batch, L = a->seqlen, D = a->dim, S = a->cu_seqlens ? a->nseq : B, K = a->d_conv;
+  const int64_t esz = io_size(a->io_dtype);
+  const Tokens x{a->x, a->x_batch_stride, a->x_seq_stride}, out{a->out, a->out_batch_stride, a->out_seq_stride};
+  if (L > 0) {
+    if (!a->weight) return SSM_ERR_NULL;
+    if (const int st = check_tokens(x, esz)) return st;
+    if (const int st = check_tokens(out, esz)) return st;
+    if (collide(out, B, L, D)) return SSM_ERR_ALIAS;
+  }
+  if (misaligned(a->weight, 4) || misaligned(a->bias, 4) || misaligned(a->cu_seqlens, 4) || misaligned(a->state_in, 4) ||
+      misaligned(a->state_out, 4))
+    return SSM_ERR_ALIGN;
+  auto rows = [&](const Tokens& t) { return rows3(L > 0 ? t.p : nullptr, B, t.sb, L, t.ss, D, esz); };
+  const Rows inputs[] = {rows(x), flat(a->weight, D * K, 4), flat(a->bias, D, 4), flat(a->cu_seqlens, S + 1, 4),
+                         flat(a->state_in, S * D * K, 4)};
+  const Rows outputs[] = {rows(out), flat(a->state_out, S * D * K, 4)};
+  return check_apart(inputs, outputs);
+}
+
+int ssm_validate_token_conv_bwd(const ssm_token_conv_bwd_args* a) {
+  if (!a) return SSM_ERR_NULL;
+  if (const int st = check_conv(a)) return st;
+  if (a->dim == 0) return SSM_OK;
+  if (!a->weight || !a->dweight) return SSM_ERR_NULL;   // dweight is set (to zero) without any token too
+  const int64_t B = a->batch, L = a->seqlen, D = a->dim, S = a->cu_seqlens ? a->nseq : B, K = a->d_conv;
+  const int64_t esz = io_size(a->io_dtype);
+  const Tokens x{a->x, a->x_batch_stride, a->x_seq_stride}, dout{a->dout, a->dout_batch_stride, a->dout_seq_stride},
+      dx{a->dx, a->dx_batch_stride, a->dx_seq_stride};
+  if (L > 0 && B > 0) {
+    for (const Tokens& t : {x, dout, dx})
+      if (const int st = check_tokens(t, esz)) return st;
+    if (collide(dx, B, L, D)) return SSM_ERR_ALIAS;
+  }
+  if (misaligned(a->weight, 4) || misaligned(a->bias, 4) || misaligned(a->cu_seqlens, 4) || misaligned(a->state_in, 4) ||
+      misaligned(a->dstate_out, 4) || misaligned(a->dweight, 4) || misaligned(a->dbias, 4) ||
+      misaligned(a->dstate_in, 4) || misaligned(a->workspace, 4))
+    return SSM_ERR_ALIGN;
+  const size_t need = token_conv_bwd_workspace_bytes(*a);
+  if (need && (!a->workspace || a->workspace_bytes < need)) return SSM_ERR_SCRATCH;
+  auto rows = [&](const Tokens& t) { return rows3(L > 0 ? t.p : nullptr, B, t.sb, L, t.ss, D, esz); };
+  const Rows inputs[] = {rows(x), rows(dout), flat(a->weight, D * K, 4), flat(a->bias, D, 4),
+                         flat(a->cu_seqlens, S + 1, 4), flat(a->state_in, S * D * K, 4), flat(a->dstate_out, S * D * K, 4)};
+  const Rows outputs[] = {rows(dx), flat(a->dweight, D * K, 4), flat(a->dbias, D, 4), flat(a->dstate_in, S * D * K, 4),
+                          flat(a->workspace, static_cast<int64_t>(a->workspace_bytes), 1)};
+  return check_apart(inputs, outputs);
+}
+
+int ssm_validate_token_conv_update(const ssm_token_conv_update_args* a) {
+  if (!a) return SSM_ERR_NULL;
+  if (a->batch < 0 || a->dim < 0 || a->nslots < 0 || a->d_conv < 1 || (!a->slots && a->batch > a->nslots))
+    return SSM_ERR_SHAPE;
+  if (bad_dtype(a->io_dtype)) return SSM_ERR_DTYPE;
+  if (a->d_conv > SSM_MAX_CONV || a->batch > 65535 || a->dim > kMaxDim) return SSM_ERR_UNSUPPORTED;
+  if (a->batch == 0 || a->dim == 0) return SSM_OK;
+  if ((!a->state && a->nslots > 0) || !a->weight) return SSM_ERR_NULL;
+  const int64_t esz = io_size(a->io_dtype), B = a->batch, D = a->dim, S = a->nslots, K = a->d_conv;
+  const Tokens x{a->x, 0, a->x_batch_stride}, out{a->out, 0, a->out_batch_stride};
+  if (const int st = check_tokens(x, esz)) return st;
+  if (const int st = check_tokens(out, esz)) return st;
+  if (a->state_slot_stride < 0) return SSM_ERR_STRIDE;
+  if (misaligned(a->state, 4) || misaligned(a->weight, 4) || misaligned(a->bias, 4) || misaligned(a->slots, 4))
+    return SSM_ERR_ALIGN;
+  if (rows_collide(1, 0, B, a->out_batch_stride, D) || rows_collide(1, 0, S, a->state_slot_stride, D * K))
+    return SSM_ERR_ALIAS;
+  auto rows = [&](const Tokens& t) { return rows3(t.p, 1, 0, B, t.ss, D, esz); };
+  const Rows inputs[] = {rows(x), flat(a->weight, D * K, 4), flat(a->bias, D, 4), flat(a->slots, B, 4)};
+  const Rows outputs[] = {rows(out), rows3(a->state, 1, 0, S, a->state_slot_stride, D * K, 4)};
+  return check_apart(inputs, outputs);
+}
+
+int ssm_validate_ssd_update(const ssm_ssd_update_args* a) {
+  if (!a) return SSM_ERR_NULL;
+  if (a->batch < 0 || a->nslots < 0 || a->nheads < 1 || a->headdim < 1 || a->dstate < 1 ||
+      (!a->slots && a->batch > a->nslots) || bad_groups(a->ngroups, a->nheads))
+    return SSM_ERR_SHAPE;
+  if (bad_dtype(a->io_dtype)) return SSM_ERR_DTYPE;
+  const int64_t most = (int64_t{1} << 31) - 1;
+  if (a->dstate > SSM_MAX_SSD_STEP_DSTATE || a->batch > 65535 || a->nheads > most / a->headdim ||
+      a->nheads * a->headdim > most / a->dstate)
+    return SSM_ERR_UNSUPPORTED;
+  if (a->batch == 0) return SSM_OK;
+  const int64_t esz = io_size(a->io_dtype), Bt = a->batch, H = a->nheads, P = a->headdim, N = a->dstate, S = a->nslots;
+  const int64_t G = groups_of(a->ngroups);
+  if ((!a->state && S > 0) || !a->x || !a->dt || !a->B || !a->C || !a->A || !a->out) return SSM_ERR_NULL;
+  const int64_t strides[] = {a->state_slot_stride, a->x_batch_stride, a->x_head_stride, a->dt_batch_stride,
+                             a->z ? a->z_batch_stride : 0, a->z ? a->z_head_stride : 0, a->B_batch_stride,
+                             a->C_batch_stride, G > 1 ? a->B_group_stride : 0, G > 1 ? a->C_group_stride : 0,
+                             a->out_batch_stride, a->out_head_stride};
+  for (int64_t s : strides)
+    if (s < 0) return SSM_ERR_STRIDE;
+  if (misaligned(a->x, esz) || misaligned(a->dt, esz) || misaligned(a->z, esz) || misaligned(a->B, esz) ||
+      misaligned(a->C, esz) || misaligned(a->out, esz) || misaligned(a->state, 4) || misaligned(a->A, 4) ||
+      misaligned(a->D, 4) || misaligned(a->dt_bias, 4) || misaligned(a->slots, 4))
+    return SSM_ERR_ALIGN;
+  if (rows_collide(Bt, a->out_batch_stride, H, a->out_head_stride, P) ||
+      rows_collide(1, 0, S, a->state_slot_stride, H * P * N))
+    return SSM_ERR_ALIAS;
+  const Rows inputs[] = {rows3(a->x, Bt, a->x_batch_stride, H, a->x_head_stride, P, esz),
+                         rows3(a->dt, 1, 0, Bt, a->dt_batch_stride, H, esz),
+                         rows3(a->z, Bt, a->z_batch_stride, H, a->z_head_stride, P, esz),
+                         rows3(a->B, Bt, a->B_batch_stride, G, a->B_group_stride, N, esz),
+                         rows3(a->C, Bt, a->C_batch_stride, G, a->C_group_stride, N, esz),
+                         flat(a->A, H, 4), flat(a->D, H, 4), flat(a->dt_bias, H, 4), flat(a->slots, Bt, 4)};
+  const Rows outputs[] = {rows3(a->out, Bt, a->out_batch_stride, H, a->out_head_stride, P, esz),
+                          rows3(a->state, 1, 0, S, a->state_slot_stride, H * P * N, 4)};
+  return check_apart(inputs, outputs);
+}
+
+int ssm_token_conv_fwd(const ssm_token_conv_args* a, void* stream) {
+  if (const int st = ssm_validate_token_conv(a)) return st;
+  if (a->batch == 0 || a->dim == 0) return SSM_OK;
+  return launch_token_conv_fwd(*a, static_cast<hipStream_t>(stream)) == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+}
+
+int ssm_token_conv_bwd(const ssm_token_conv_bwd_args* a, void* stream) {
+  if (const int st = ssm_validate_token_conv_bwd(a)) return st;
+  if (a->dim == 0) return SSM_OK;
+  return launch_token_conv_bwd(*a, static_cast<hipStream_t>(stream)) == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+}
+
+int ssm_token_conv_update(const ssm_token_conv_update_args* a, void* stream) {
+  if (const int st = ssm_validate_token_conv_update(a)) return st;
+  if (a->batch == 0 || a->dim == 0) return SSM_OK;
+  return launch_token_conv_update(*a, static_cast<hipStream_t>(stream)) == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+}
+
+int ssm_ssd_state_update(const ssm_ssd_update_args* a, void* stream) {
+  if (const int st = ssm_validate_ssd_update(a)) return st;
+  if (a->batch == 0) return SSM_OK;
+  return launch_ssd_step(*a, static_cast<hipStream_t>(stream)) == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+}
+
+}  // extern "C"

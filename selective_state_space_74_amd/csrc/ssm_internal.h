@@ -30,6 +30,11 @@ hipError_t launch_gated_step(const ssm_gated_update_args& a, hipStream_t stream)
 hipError_t launch_cache_write(const ssm_state_cache_args& a, hipStream_t stream);
 hipError_t launch_cache_read(const ssm_state_cache_args& a, hipStream_t stream);
 hipError_t launch_cached_update(const ssm_cached_update_args& a, hipStream_t stream);
+hipError_t launch_token_conv_fwd(const ssm_token_conv_args& a, hipStream_t stream);
+hipError_t launch_token_conv_bwd(const ssm_token_conv_bwd_args& a, hipStream_t stream);
+size_t token_conv_bwd_workspace_bytes(const ssm_token_conv_bwd_args& a);
+hipError_t launch_token_conv_update(const ssm_token_conv_update_args& a, hipStream_t stream);
+hipError_t launch_ssd_step(const ssm_ssd_update_args& a, hipStream_t stream);
 
 // ---------------------------------------------------------------------------
 // Device helpers.

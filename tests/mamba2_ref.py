@@ -1,0 +1,158 @@
+"""Plain 64-bit forms of the Mamba-2 layer's convolution and single-token step
+(numpy), each with a bound on how far fp32 arithmetic may be from it.
+
+The bounds are running error analyses in units of U = 2^-24 (half a step of
+fp32, relative).  A sum of n products, whatever its order, is off by at most
+(n + 1) U of the sum of their magnitudes.  The hardware's exp2, log2 and
+reciprocal are within one step (2 U): a sigmoid of a z that is off by e is off
+by at most e/4 + (2 |z| + 6) U sigma, silu by 1.1 e + (2 |z| + 8) U |silu|, and
+silu' (whose derivative is at most 1/2) by e/2 + (2 |z| + 10) (1 + |z|) U sigma."""
+import numpy as np
+
+U = 2.0 ** -24
+HALF_STEP = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8}
+TINY = 2.0 ** -126
+
+
+def sigmoid(z):
+    with np.errstate(over="ignore"):
+        return 1.0 / (1.0 + np.exp(-z))
+
+
+def softplus(z):
+    return np.maximum(z, 0) + np.log1p(np.exp(-np.abs(z)))
+
+
+def bounds_of(shape, cu):
+    """(batch row, first token, token after the last, which sequence)."""
+    if cu is None:
+        return [(b, 0, shape[1], b) for b in range(shape[0])]
+    return [(0, int(cu[k]), int(cu[k + 1]), k) for k in range(len(cu) - 1)]
+
+
+def token_conv(x, w, b, silu=True, state=None, cu=None, dout=None, dstate=None):
+    """({name: value}, {name: bound}): out and the state left, and with dout (or
+    dstate) the gradients.  Arrays are (batch, L, D), or (tokens, D) with cu."""
+    packed = cu is not None
+    lift = lambda t: np.asarray(t, np.float64)[None] if packed else np.asarray(t, np.float64)  # noqa: E731
+    x, w, (D, K) = lift(x), np.asarray(w, np.float64), np.shape(w)
+    b = np.zeros(D) if b is None else np.asarray(b, np.float64)
+    seqs = bounds_of(x.shape, cu)
+    n = len(seqs)
+    grad = dout is not None or dstate is not None
+    val = dict(out=np.zeros_like(x), state=np.zeros((n, D, K)))
+    bnd = dict(out=np.zeros_like(x), state=np.zeros((n, D, K)))
+    if grad:
+        dout = np.zeros_like(x) if dout is None else lift(dout)
+        for d in (val, bnd):
+            d.update(dx=np.zeros_like(x), dweight=np.zeros((D, K)), dbias=np.zeros(D), dstate_in=np.zeros((n, D, K)))
+        mag_w, mag_b = np.zeros((D, K)), np.zeros(D)
+    for r, lo, hi, k in seqs:
+        L = hi - lo
+        held = np.zeros((K, D)) if state is None else np.asarray(state, np.float64)[k].T
+        row = np.concatenate((held, x[r, lo:hi]))
+        val["state"][k] = row[L:].T
+        taps = np.stack([row[1 + j:1 + j + L] for j in range(K)], -1)   # (L, D, K)
+        pre = b + (taps * w).sum(-1)
+        mag = np.abs(b) + np.abs(taps * w).sum(-1)
+        ep = (K + 2) * U * mag
+        s = sigmoid(pre)
+        val["out"][r, lo:hi] = pre * s if silu else pre
+        bnd["out"][r, lo:hi] = 1.1 * ep + (2 * np.abs(pre) + 8) * U * np.abs(pre * s) if silu else ep
+        if not grad:
+            continue
+        d = dout[r, lo:hi]
+        f = s * (1 + pre * (1 - s)) if silu else np.ones_like(pre)
+        ef = ep / 2 + (2 * np.abs(pre) + 10) * (1 + np.abs(pre)) * U * s if silu else np.zeros_like(pre)
+        e, ee = d * f, np.abs(d) * ef + U * np.abs(d * f)
+        back, eback, mback = (np.zeros_like(row) for _ in range(3))
+        for j in range(K):
+            back[1 + j:1 + j + L] += e * w[:, j]
+            eback[1 + j:1 + j + L] += ee * np.abs(w[:, j])
+            mback[1 + j:1 + j + L] += np.abs(e * w[:, j])
+        if dstate is not None:
+            up = np.asarray(dstate, np.float64)[k].T
+            back[L:] += up
+            mback[L:] += np.abs(up)
+        eback += (K + 2) * U * mback
+        val["dx"][r, lo:hi], bnd["dx"][r, lo:hi] = back[K:], eback[K:]
+        val["dstate_in"][k], bnd["dstate_in"][k] = back[:K].T, eback[:K].T
+        val["dweight"] += (e[..., None] * taps).sum(0)
+        val["dbias"] += e.sum(0)
+        bnd["dweight"] += (ee[..., None] * np.abs(taps)).sum(0)
+        bnd["dbias"] += ee.sum(0)
+        mag_w += np.abs(e[..., None] * taps).sum(0)
+        mag_b += np.abs(e).sum(0)
+    if grad:
+        # runs of up to 32 tokens in order, 16 runs in a tree, groups of 512 tokens in 4 strands
+        terms = 32 + 8 + x.shape[0] * (x.shape[1] // 128 + 1) / 4 + 4
+        bnd["dweight"] += terms * U * mag_w
+        bnd["dbias"] += terms * U * mag_b
+    if packed:
+        for d in (val, bnd):
+            for key in ("out", "dx"):
+                if key in d:
+                    d[key] = d[key][0]
+    return val, bnd
+
+
+def conv_step(state, x, w, b, silu=True, slots=None):
+    """(out, its bound, the pool afterwards); rows of the batch one after the other."""
+    state, x, w = np.array(state, np.float64), np.asarray(x, np.float64), np.asarray(w, np.float64)
+    out, bnd = np.zeros_like(x), np.zeros_like(x)
+    K = w.shape[1]
+    for r in range(x.shape[0]):
+        k = r if slots is None else int(slots[r])
+        if not 0 <= k < state.shape[0]:
+            continue
+        state[k] = np.concatenate((state[k][:, 1:], x[r][:, None]), 1)
+        pre = (state[k] * w).sum(-1) + (0 if b is None else b)
+        ep = (K + 2) * U * (np.abs(state[k] * w).sum(-1) + (0 if b is None else np.abs(b)))
+        s = sigmoid(pre)
+        out[r] = pre * s if silu else pre
+        bnd[r] = 1.1 * ep + (2 * np.abs(pre) + 8) * U * np.abs(pre * s) if silu else ep
+    return out, bnd, state
+
+
+def step_parts(dt, bias, A, softplus_on=True):
+    """Step size, decay, and their relative errors, softplus being within 3 U of
+    its value where its argument is exact."""
+    pre = dt + (0 if bias is None else bias)
+    delta = softplus(pre) if softplus_on else pre
+    slope = sigmoid(pre) if softplus_on else np.ones_like(pre)
+    with np.errstate(divide="ignore", invalid="ignore"):
+        ed = np.where(delta != 0, slope * U * np.abs(pre) / np.abs(delta), 0) + (3 * U if softplus_on else 0)
+    z = delta * A
+    return delta, np.exp(z), ed, np.abs(z) * (ed + 3 * U) + 2 * U
+
+
+def ssd_step(state, x, dt, A, B, C, D=None, z=None, bias=None, softplus_on=True, slots=None):
+    """(out, its bound, the pool afterwards, its bound): (batch, H, P) inputs,
+    (batch, G, N) B and C, one row after the other."""
+    state, x, dt, A, B, C = (np.array(t, np.float64) for t in (state, x, dt, A, B, C))
+    es = np.zeros_like(state)
+    H, G, N = x.shape[1], B.shape[1], B.shape[2]
+    B, C = np.repeat(B, H // G, 1), np.repeat(C, H // G, 1)
+    out, bnd = np.zeros_like(x), np.zeros_like(x)
+    for r in range(x.shape[0]):
+        k = r if slots is None else int(slots[r])
+        if not 0 <= k < state.shape[0]:
+            continue
+        delta, a, ed, ea = step_parts(dt[r], bias, A, softplus_on)
+        col = lambda t: t[:, None, None]  # noqa: E731
+        old = col(a) * state[k]
+        new = col(delta) * x[r][..., None] * B[r][:, None]
+        es[k] = col(a) * es[k] + np.abs(old) * (col(ea) + U) + np.abs(new) * (col(ed) + 3 * U)
+        state[k] = old + new
+        es[k] += U * np.abs(state[k]) + TINY
+        y = (state[k] * C[r][:, None]).sum(-1)
+        ey = (es[k] * np.abs(C[r][:, None])).sum(-1) + (N + 2) * U * np.abs(state[k] * C[r][:, None]).sum(-1)
+        if D is not None:
+            y = y + D[:, None] * x[r]
+            ey = ey + 2 * U * (np.abs(D[:, None] * x[r]) + np.abs(y))
+        if z is not None:
+            g = z[r] * sigmoid(z[r])
+            ey = ey * np.abs(g) + np.abs(y * g) * (2 * np.abs(z[r]) + 9) * U
+            y = y * g
+        out[r], bnd[r] = y, ey
+    return out, bnd, state, es
