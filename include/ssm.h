@@ -5,8 +5,8 @@
  * three families next to them: a gated linear recurrence (ssm_gated_*), a
  * quantised cache of recurrent states (ssm_state_cache_*,
  * ssm_selective_state_update_cached), and what the Mamba-2 layer needs around
- * its prefill (ssm_token_conv_*, ssm_ssd_state_update), each described at its
- * arguments.
+ * its prefill (ssm_token_conv_*, ssm_ssd_packed_fwd, ssm_ssd_scan_bwd,
+ * ssm_ssd_state_update), each described at its arguments.
  *
  *   ssm_selective_scan_fwd  -- prefill.  For every batch row b, channel d and
  *     state index n, with Delta_t = softplus(delta_t + bias[d]) (Mamba paper
@@ -691,6 +691,108 @@ typedef struct ssm_ssd_update_args {
   void* out;           int64_t out_batch_stride, out_head_stride;
 } ssm_ssd_update_args;
 
+/* Arguments of the Mamba-2 SSM prefill over packed sequences: the recurrence of
+ * ssm_ssd_args, with the tensors' batch axis gone.
+ *   x, z, out   : (seqlen, nheads, headdim), headdim stride 1.
+ *   dt          : (seqlen, nheads), head stride 1, io_dtype.
+ *   B, C        : (seqlen, ngroups, dstate), state stride 1.
+ *   A, D, dt_bias : (nheads) fp32; D and dt_bias NULL mean 0; z NULL: no gate.
+ *   cu_seqlens  : as in ssm_gated_args, nseq + 1 entries (required).  Tokens of no
+ *                 sequence: their rows of out are left as they are, or set to
+ *                 zero with zero_outside.
+ *   h0, last_state : (nseq, nheads, headdim, dstate) fp32, contiguous; NULL: a
+ *                 zero state, and not wanted.  An empty sequence's last state is
+ *                 its h0 (or zero).
+ * Sizes: seqlen >= 0 and below 2^31 - 64; nheads, headdim, dstate >= 1; ngroups 0
+ * or 1 (one group) or a divisor of nheads; dstate at most 128 for bf16 IO and 64
+ * for fp32 IO; nseq below 2^29; nheads * headdim * dstate below 2^31 and
+ * (seqlen / 64 + min(nseq, seqlen)) * nheads below 2^24; (63 * seq_stride + inner
+ * size) * element size below 2^31 for x, z, B, C and out, as in ssm_ssd_args
+ * (SSM_ERR_UNSUPPORTED past that).
+ * A NaN or an infinity in a token's inputs stays within its sequence, but may
+ * reach earlier tokens of its chunk (64 tokens from the sequence's first on).
+ * Precision: fp32 accumulation, states and decays.  With bf16 IO the products run
+ * on bf16 operands: the masked chunk scores are rounded to bf16, while the states
+ * and what is summed into them enter as a bf16 value plus its bf16 remainder (16
+ * bits; last_state is good to about 2^-17); with fp32 IO every product is fp32.
+ * Aliasing: out, last_state and the workspace must not overlap any input or each
+ * other, except that last_state may be exactly h0.
+ * Workspace: device scratch owned by the caller, 16-byte aligned, of at least
+ * ssm_ssd_packed_workspace_size() bytes (required: SSM_ERR_SCRATCH otherwise), not
+ * overlapping any tensor and not in use by another call that may run at the same
+ * time.  It holds the state that enters each chunk of 64 tokens. */
+typedef struct ssm_ssd_packed_args {
+  int64_t seqlen, nheads, headdim, ngroups, dstate, nseq;
+  int32_t io_dtype;      /* ssm_dtype */
+  int32_t dt_softplus;   /* bool */
+  int32_t zero_outside;  /* bool */
+  const void* x;   int64_t x_seq_stride, x_head_stride;
+  const void* dt;  int64_t dt_seq_stride;
+  const void* z;   int64_t z_seq_stride, z_head_stride;
+  const void* B;   int64_t B_seq_stride, B_group_stride;
+  const void* C;   int64_t C_seq_stride, C_group_stride;
+  const float* A;
+  const float* D;
+  const float* dt_bias;
+  const int32_t* cu_seqlens;
+  const float* h0;
+  float* last_state;
+  void* out;       int64_t out_seq_stride, out_head_stride;
+  void* workspace; size_t workspace_bytes;
+} ssm_ssd_packed_args;
+
+/* Arguments of the gradients of the Mamba-2 SSM prefill, batched
+ * (ssm_ssd_args) or packed (ssm_ssd_packed_args).  The forward inputs keep their
+ * meaning and must be the ones the forward ran with; the states are computed
+ * again from them.
+ *   cu_seqlens  : NULL: every batch row is one sequence.  Otherwise batch must be
+ *                 1 and the row holds nseq packed sequences.
+ *   dout        : like out, headdim stride 1.
+ *   dlast       : like last_state, fp32, contiguous; NULL means 0.
+ * Outputs, contiguous, fully overwritten (tokens of no sequence get zeros):
+ *   dx, dz      : (batch, seqlen, nheads, headdim), io_dtype; dz is required when
+ *                 z is given, else ignored.
+ *   ddt         : (batch, seqlen, nheads), io_dtype (of dt before its bias).
+ *   dB, dC      : (batch, seqlen, ngroups, dstate), io_dtype, each summed over
+ *                 the heads of its group in fp32 and rounded once.
+ *   dA          : (nheads) fp32; dD, ddt_bias: the same, NULL: not wanted.
+ *   dh0         : like h0, fp32; NULL: not wanted.
+ * Every output is the same bits from run to run.
+ * Sizes as in ssm_ssd_packed_args, with batch * ceil(seqlen / 64) in place of its
+ * count of chunks without cu_seqlens.  As in ssm_ssd_args, 64 tokens of a tensor's
+ * rows are reached through 31-bit byte windows.
+ * Precision: as there; the gradients of dt, A, dt_bias and D come from products
+ * whose operands carry 16 bits at least.
+ * Aliasing: no output may overlap an input, another output or the workspace.
+ * Workspace: as in ssm_ssd_packed_args, of ssm_ssd_bwd_workspace_size() bytes. */
+typedef struct ssm_ssd_bwd_args {
+  int64_t batch, seqlen, nheads, headdim, ngroups, dstate, nseq;
+  int32_t io_dtype;      /* ssm_dtype */
+  int32_t dt_softplus;   /* bool */
+  const void* x;   int64_t x_batch_stride, x_seq_stride, x_head_stride;
+  const void* dt;  int64_t dt_batch_stride, dt_seq_stride;
+  const void* z;   int64_t z_batch_stride, z_seq_stride, z_head_stride;
+  const void* B;   int64_t B_batch_stride, B_seq_stride, B_group_stride;
+  const void* C;   int64_t C_batch_stride, C_seq_stride, C_group_stride;
+  const float* A;
+  const float* D;
+  const float* dt_bias;
+  const int32_t* cu_seqlens;
+  const float* h0;
+  const void* dout; int64_t dout_batch_stride, dout_seq_stride, dout_head_stride;
+  const float* dlast;
+  void* dx;
+  void* ddt;
+  void* dz;
+  void* dB;
+  void* dC;
+  float* dA;
+  float* dD;
+  float* ddt_bias;
+  float* dh0;
+  void* workspace; size_t workspace_bytes;
+} ssm_ssd_bwd_args;
+
 /* ABI version of the loaded library (SSM_ABI_VERSION at build time). */
 int ssm_abi_version(void);
 
@@ -708,6 +810,8 @@ size_t ssm_token_conv_args_size(void);
 size_t ssm_token_conv_bwd_args_size(void);
 size_t ssm_token_conv_update_args_size(void);
 size_t ssm_ssd_update_args_size(void);
+size_t ssm_ssd_packed_args_size(void);
+size_t ssm_ssd_bwd_args_size(void);
 
 /* Workspace bytes the scan can use for this argument block (0 when it would
  * run single-segment anyway): for G segments, with BD = batch * dim and
@@ -745,6 +849,14 @@ size_t ssm_gated_scan_bwd_workspace_size(const ssm_gated_bwd_args* args);
  * Reads only sizes; pure host code. */
 size_t ssm_token_conv_bwd_workspace_size(const ssm_token_conv_bwd_args* args);
 
+/* Workspace bytes the packed SSD prefill and the SSD gradients need: for each
+ * chunk of 64 tokens and head a state of headdim * dstate fp32 values (the
+ * gradients: two, and partial sums of dB and dC where several workgroups share a
+ * group's heads).  Read only sizes and whether cu_seqlens is given; pure host
+ * code. */
+size_t ssm_ssd_packed_workspace_size(const ssm_ssd_packed_args* args);
+size_t ssm_ssd_bwd_workspace_size(const ssm_ssd_bwd_args* args);
+
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char* ssm_status_string(int status);
 
@@ -764,6 +876,8 @@ int ssm_validate_token_conv(const ssm_token_conv_args* args);
 int ssm_validate_token_conv_bwd(const ssm_token_conv_bwd_args* args);
 int ssm_validate_token_conv_update(const ssm_token_conv_update_args* args);
 int ssm_validate_ssd_update(const ssm_ssd_update_args* args);
+int ssm_validate_ssd_packed(const ssm_ssd_packed_args* args);
+int ssm_validate_ssd_bwd(const ssm_ssd_bwd_args* args);
 
 /* Prefill scan (see ssm_scan_args).  Validates, then launches on `stream`. */
 int ssm_selective_scan_fwd(const ssm_scan_args* args, void* stream);
@@ -815,7 +929,10 @@ int ssm_token_conv_fwd(const ssm_token_conv_args* args, void* stream);
 int ssm_token_conv_bwd(const ssm_token_conv_bwd_args* args, void* stream);
 int ssm_token_conv_update(const ssm_token_conv_update_args* args, void* stream);
 
-/* Single-token step of the Mamba-2 SSM (see ssm_ssd_update_args). */
+/* Packed prefill, gradients and single-token step of the Mamba-2 SSM (see
+ * ssm_ssd_packed_args, ssm_ssd_bwd_args, ssm_ssd_update_args). */
+int ssm_ssd_packed_fwd(const ssm_ssd_packed_args* args, void* stream);
+int ssm_ssd_scan_bwd(const ssm_ssd_bwd_args* args, void* stream);
 int ssm_ssd_state_update(const ssm_ssd_update_args* args, void* stream);
 
 #ifdef __cplusplus

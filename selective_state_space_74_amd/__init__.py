@@ -35,9 +35,15 @@ CPU fallback, and importing a missing library raises.
     token_conv_update(state, x, weight, bias=None, silu=True, slots=None) -> out
         (the causal depthwise convolution, token-major, batched or packed:
         prefill, gradients, and its single-token step)
+    ssd_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=True, h0=None,
+                 return_last_state=False, cu_seqlens=None) -> out, or (out, last_state)
+    ssd_scan_bwd(dout, x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=True,
+                 h0=None, dlast=None, cu_seqlens=None) -> dict of gradients
+    ssd_scan(x, dt, A, B, C, ...)  (the two as a differentiable torch op)
     ssd_state_update(state, x, dt, A, B, C, D=None, z=None, dt_bias=None,
                      dt_softplus=True, slots=None) -> out
-        (the Mamba-2 SSM's single-token step on a pool of states)
+        (the Mamba-2 SSM, batched or packed: prefill, gradients, and its
+        single-token step on a pool of states)
 
 Shapes (N = dstate, 1..64): u, delta, z (batch, dim, L) with time stride 1;
 B, C (batch, N, L), or (batch, G, N, L) for G groups of dim // G channels,
@@ -257,12 +263,43 @@ class SsdUpdateArgs(ctypes.Structure):
                 ("out", _P), ("out_batch_stride", _I64), ("out_head_stride", _I64)]
 
 
+class SsdPackedArgs(ctypes.Structure):
+    """Mirror of ssm_ssd_packed_args."""
+    _fields_ = [("seqlen", _I64), ("nheads", _I64), ("headdim", _I64), ("ngroups", _I64), ("dstate", _I64), ("nseq", _I64),
+                ("io_dtype", _I32), ("dt_softplus", _I32), ("zero_outside", _I32),
+                ("x", _P), ("x_seq_stride", _I64), ("x_head_stride", _I64),
+                ("dt", _P), ("dt_seq_stride", _I64),
+                ("z", _P), ("z_seq_stride", _I64), ("z_head_stride", _I64),
+                ("B", _P), ("B_seq_stride", _I64), ("B_group_stride", _I64),
+                ("C", _P), ("C_seq_stride", _I64), ("C_group_stride", _I64),
+                ("A", _P), ("D", _P), ("dt_bias", _P), ("cu_seqlens", _P), ("h0", _P), ("last_state", _P),
+                ("out", _P), ("out_seq_stride", _I64), ("out_head_stride", _I64),
+                ("workspace", _P), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class SsdBwdArgs(ctypes.Structure):
+    """Mirror of ssm_ssd_bwd_args."""
+    _fields_ = [("batch", _I64), ("seqlen", _I64), ("nheads", _I64), ("headdim", _I64), ("ngroups", _I64), ("dstate", _I64),
+                ("nseq", _I64), ("io_dtype", _I32), ("dt_softplus", _I32),
+                ("x", _P), ("x_batch_stride", _I64), ("x_seq_stride", _I64), ("x_head_stride", _I64),
+                ("dt", _P), ("dt_batch_stride", _I64), ("dt_seq_stride", _I64),
+                ("z", _P), ("z_batch_stride", _I64), ("z_seq_stride", _I64), ("z_head_stride", _I64),
+                ("B", _P), ("B_batch_stride", _I64), ("B_seq_stride", _I64), ("B_group_stride", _I64),
+                ("C", _P), ("C_batch_stride", _I64), ("C_seq_stride", _I64), ("C_group_stride", _I64),
+                ("A", _P), ("D", _P), ("dt_bias", _P), ("cu_seqlens", _P), ("h0", _P),
+                ("dout", _P), ("dout_batch_stride", _I64), ("dout_seq_stride", _I64), ("dout_head_stride", _I64),
+                ("dlast", _P), ("dx", _P), ("ddt", _P), ("dz", _P), ("dB", _P), ("dC", _P), ("dA", _P), ("dD", _P),
+                ("ddt_bias", _P), ("dh0", _P), ("workspace", _P), ("workspace_bytes", ctypes.c_size_t)]
+
+
 # Entry points by argument block: (block, launching functions, validating ones,
 # workspace size functions, without their prefixes), for the families after the
 # scans.
 _MAMBA2 = ((TokenConvArgs, "token_conv_fwd", "token_conv", None),
            (TokenConvBwdArgs, "token_conv_bwd", "token_conv_bwd", "token_conv_bwd"),
            (TokenConvUpdateArgs, "token_conv_update", "token_conv_update", None),
+           (SsdPackedArgs, "ssd_packed_fwd", "ssd_packed", "ssd_packed"),
+           (SsdBwdArgs, "ssd_scan_bwd", "ssd_bwd", "ssd_bwd"),
            (SsdUpdateArgs, "ssd_state_update", "ssd_update", None))
 
 
@@ -748,7 +785,8 @@ def selective_scan_bwd(dout, u, delta, A, B, C, checkpoints, D=None, z=None, del
 
 
 def ssd_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=True, h0=None,
-                 return_last_state=False, out=None, last_state=None, stream=None, workspace=None):
+                 return_last_state=False, out=None, last_state=None, stream=None, workspace=None,
+                 cu_seqlens=None):
     """Mamba-2 SSM (SSD layer) prefill on the GPU.
 
     x, z: (batch, L, nheads, headdim) with headdim stride 1; dt: (batch, L,
@@ -756,8 +794,17 @@ def ssd_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=True,
     with state stride 1; A, D, dt_bias: (nheads,) fp32; h0: (batch, nheads,
     headdim, dstate) fp32.  Returns out (like x) or (out, last_state).
     `workspace`: as for selective_scan_fwd (None allocates what the library
-    asks for, False passes none: each sequence then runs as one segment)."""
+    asks for, False passes none: each sequence then runs as one segment).
+    With cu_seqlens, the int32 device tensor of nseq + 1 sequence bounds, the
+    sequences are packed: all tensors without their batch axis, h0 and
+    last_state (nseq, nheads, headdim, dstate); an empty sequence's last state
+    is its h0, and last_state may be h0 itself.  Tokens outside every sequence:
+    zero rows in an `out` made here, left as they were in one that is given.
+    The workspace is then needed (not False), by one call at a time."""
     torch = _torch()
+    if cu_seqlens is not None:
+        return _ssd_packed_fwd(x, dt, A, B, C, D, z, dt_bias, dt_softplus, h0, return_last_state, out, last_state, stream,
+                               workspace, cu_seqlens)
     if x.dim() != 4:
         raise ValueError("x must be (batch, L, nheads, headdim)")
     batch, L, H, P = x.shape
@@ -1492,3 +1539,149 @@ def ssd_state_update(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_sof
                           *params, _ptr(slots), *_inner_rows("out", out, shape, io, dev))
         _launch("ssm_ssd_state_update", a, s)
     return out
+
+
+def validate_ssd_packed(args: SsdPackedArgs) -> int:
+    return lib().ssm_validate_ssd_packed(ctypes.byref(args))
+
+
+def validate_ssd_bwd(args: SsdBwdArgs) -> int:
+    return lib().ssm_validate_ssd_bwd(ctypes.byref(args))
+
+
+def ssd_packed_workspace_size(args: SsdPackedArgs) -> int:
+    return lib().ssm_ssd_packed_workspace_size(ctypes.byref(args))
+
+
+def ssd_bwd_workspace_size(args: SsdBwdArgs) -> int:
+    return lib().ssm_ssd_bwd_workspace_size(ctypes.byref(args))
+
+
+def _by_heads(name, t, shape, dtype, device):
+    """Pointer and strides (but the last) of a tensor of this shape, None and
+    zeros for None."""
+    if t is None:
+        return (None,) + (0,) * (len(shape) - 1)
+    _placed(name, t, dtype, device)
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"{name} must have a unit innermost stride")
+    return (t.data_ptr(),) + st[:-1]
+
+
+def _ssd_sizes(x, B, cu_seqlens):
+    """(lead axes, heads, headdim, groups, dstate, number of sequences, nseq field, bounds' pointer)."""
+    torch = _torch()
+    packed = cu_seqlens is not None
+    axes = 3 if packed else 4
+    if x.dim() != axes or B.dim() != axes:
+        raise ValueError("with cu_seqlens x must be (tokens, nheads, headdim) and B, C (tokens, ngroups, dstate)" if packed
+                         else "x must be (batch, L, nheads, headdim) and B, C (batch, L, ngroups, dstate)")
+    if B.shape[-2] < 1:
+        raise ValueError("B must have at least one group")
+    lead, (H, P), (G, N) = tuple(x.shape[:-2]), x.shape[-2:], B.shape[-2:]
+    if not packed:
+        return lead, H, P, G, N, lead[0], 0, None
+    _placed("cu_seqlens", cu_seqlens, torch.int32, x.get_device())
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1 or not cu_seqlens.is_contiguous():
+        raise ValueError("cu_seqlens must be a contiguous int32 vector of nseq + 1 entries")
+    n = cu_seqlens.numel() - 1
+    return lead, H, P, G, N, n, n, cu_seqlens.data_ptr()
+
+
+def _ssd_packed_fwd(x, dt, A, B, C, D, z, dt_bias, dt_softplus, h0, return_last_state, out, last_state, stream, workspace,
+                    cu_seqlens):
+    torch = _torch()
+    code, dev, io = _io_code(x), _gpu("x", x), x.dtype
+    lead, H, P, G, N, n, nseq, cu = _ssd_sizes(x, B, cu_seqlens)
+    shape, states = lead + (H, P), (n, H, P, N)
+    if workspace is False:
+        raise ValueError("packed sequences need a workspace")
+    inputs = _by_heads("x", x, shape, io, dev) + _by_heads("dt", dt, lead + (H,), io, dev) + _by_heads("z", z, shape, io, dev) + \
+        _by_heads("B", B, lead + (G, N), io, dev) + _by_heads("C", C, lead + (G, N), io, dev)
+    params = _fp32("A", A, (H,), dev), _fp32("D", D, (H,), dev), _fp32("dt_bias", dt_bias, (H,), dev), cu, \
+        _fp32("h0", h0, states, dev)
+    with _on(dev, stream) as s:
+        made = out is None
+        if made:
+            out = _empty(x, shape, io, dev)
+        if return_last_state and last_state is None:
+            last_state = torch.empty(states, dtype=torch.float32, device=dev)
+        a = SsdPackedArgs(lead[0], H, P, G, N, nseq, code, bool(dt_softplus), made, *inputs, *params,
+                          _fp32("last_state", last_state, states, dev), *_by_heads("out", out, shape, io, dev))
+        workspace = _set_workspace(a, ssd_packed_workspace_size(a), workspace, dev)
+        _launch("ssm_ssd_packed_fwd", a, s)
+    return (out, last_state) if return_last_state else out
+
+
+def ssd_scan_bwd(dout, x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=True, h0=None, dlast=None,
+                 cu_seqlens=None, stream=None, workspace=None):
+    """Gradients of ssd_scan_fwd, batched or packed, for the upstream gradient
+    dout on out (and dlast on last_state); the states are computed again, nothing
+    of the forward is needed but its inputs.  Returns a dict: dx, ddt, dB, dC (IO
+    dtype, shaped like their inputs; dB and dC summed over the heads of their
+    group in fp32 and rounded once), dA (fp32) and, for the inputs that were
+    given, dz (IO dtype), dD, ddt_bias, dh0 (fp32).  Rows of tokens outside every
+    sequence are zero.  Every output is the same bits from run to run.
+    `workspace`: a device tensor reused across calls, by one call at a time;
+    None allocates one (it holds two fp32 states for each 64 tokens and head)."""
+    torch = _torch()
+    code, dev, io = _io_code(x), _gpu("x", x), x.dtype
+    lead, H, P, G, N, n, nseq, cu = _ssd_sizes(x, B, cu_seqlens)
+    shape, states = lead + (H, P), (n, H, P, N)
+
+    def of(name, t, want):   # a packed tensor's batch stride is 0
+        f = _by_heads(name, t, want, io, dev)
+        return f if cu is None else f[:1] + (0,) + f[1:]
+    inputs = of("x", x, shape) + of("dt", dt, lead + (H,)) + of("z", z, shape) + of("B", B, lead + (G, N)) + \
+        of("C", C, lead + (G, N))
+    params = _fp32("A", A, (H,), dev), _fp32("D", D, (H,), dev), _fp32("dt_bias", dt_bias, (H,), dev), cu, \
+        _fp32("h0", h0, states, dev)
+    upstream = of("dout", dout, shape) + (_fp32("dlast", dlast, states, dev),)
+    with _on(dev, stream) as s:
+        new = lambda *size, dtype=io: torch.empty(size, dtype=dtype, device=dev)  # noqa: E731
+        g = dict(dx=new(*shape), ddt=new(*lead, H), dB=new(*lead, G, N), dC=new(*lead, G, N), dA=torch.empty_like(A))
+        if z is not None:
+            g["dz"] = new(*shape)
+        if D is not None:
+            g["dD"] = torch.empty_like(D)
+        if dt_bias is not None:
+            g["ddt_bias"] = torch.empty_like(dt_bias)
+        if h0 is not None:
+            g["dh0"] = torch.empty_like(h0)
+        a = SsdBwdArgs(lead[0] if cu is None else 1, lead[-1], H, P, G, N, nseq, code, bool(dt_softplus), *inputs, *params,
+                       *upstream, *(_ptr(g.get(k)) for k in ("dx", "ddt", "dz", "dB", "dC", "dA", "dD", "ddt_bias", "dh0")))
+        workspace = _set_workspace(a, ssd_bwd_workspace_size(a), workspace, dev)
+        _launch("ssm_ssd_scan_bwd", a, s)
+    return g
+
+
+def ssd_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=True, h0=None, cu_seqlens=None,
+             return_last_state=False):
+    """ssd_scan_fwd, batched or packed, as a differentiable torch op: gradients
+    flow to x, dt, A, B, C and, where given, D, z, dt_bias and h0, from out and
+    from the last state."""
+    torch = _torch()
+
+    class _SsdScan(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, dt, A, B, C, D, z, dt_bias, h0):
+            ctx.set_materialize_grads(False)
+            out, last = ssd_scan_fwd(x, dt, A, B, C, D=D, z=z, dt_bias=dt_bias, dt_softplus=dt_softplus, h0=h0,
+                                     return_last_state=True, cu_seqlens=cu_seqlens)
+            ctx.save_for_backward(x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens)
+            return out, last
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, dout, dlast):
+            x, dt, A, B, C, D, z, dt_bias, h0, cu = ctx.saved_tensors
+            dout = torch.zeros_like(x, memory_format=torch.contiguous_format) if dout is None else dout.contiguous()
+            g = ssd_scan_bwd(dout, x, dt, A, B, C, D=D, z=z, dt_bias=dt_bias, dt_softplus=dt_softplus, h0=h0,
+                             dlast=None if dlast is None else dlast.contiguous(), cu_seqlens=cu)
+            return tuple(g.get(k) for k in ("dx", "ddt", "dA", "dB", "dC", "dD", "dz", "ddt_bias", "dh0"))
+
+    out, last = _SsdScan.apply(x, dt, A, B, C, D, z, dt_bias, h0)
+    return (out, last) if return_last_state else out

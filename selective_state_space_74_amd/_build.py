@@ -25,11 +25,12 @@ HIPCC_FLAGS = ["-O3", "-std=c++17", f"--offload-arch={ARCH}", "-fPIC", "-Wall",
                "-I", INCLUDE, "-I", CSRC]
 
 
-# Per-source extra flags.  The SSD kernel keeps its matrix-product
+# Per-source extra flags.  The SSD kernels keep their matrix-product
 # accumulators in the ordinary VGPR file (the VGPR form of the MFMA
 # instructions) instead of the accumulation registers, which saves the
 # copies between the two files.
-SOURCE_FLAGS = {"ssd_fwd.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+_MFMA_IN_VGPRS = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
+SOURCE_FLAGS = {src: _MFMA_IN_VGPRS for src in ("ssd_fwd.hip", "ssd_chunk.hip", "ssd_bwd.hip")}
 
 
 def flags_for(src: str) -> list:

@@ -1,0 +1,669 @@
+// ssd_bwd.hip -- gradients of the Mamba-2 SSM prefill on gfx950, chunk by chunk on
+// the matrix cores (see ssd_chunk.h for S_in and dS_out, which two kernels there
+// leave for every chunk and head).
+//
+// Within a chunk, with dy_t = dout_t silu(z_t), L[t,s] = e^{a_t - a_s} for s <= t (else
+// 0), G = C B^T (one for all heads of a group) and M = dy x^T:
+//   dx_s  = Delta_s (sum_t (G L)[t,s] dy_t + e^{a_end - a_s} dS_out B_s) + D dy_s
+//   dC_t  = sum_h sum_s (M L)[t,s] Delta_s B_s + e^{a_t} S_in^T dy_t
+//   dB_s  = sum_h sum_t (M L)[t,s] Delta_s C_t + e^{a_end - a_s} Delta_s dS_out^T x_s
+// The gradients of the steps need no further product.  With K = G L M (elementwise;
+// what of the output at t comes from the input at s, times dy_t, over Delta_s), and
+//   r_t = e^{a_t} C_t . (S_in^T dy_t),   c_s = e^{a_end - a_s} B_s . (dS_out^T x_s)
+// the gradient that flows through the decay of step s is everything from before s
+// to s or after:
+//   g_s = sum_{t >= s} sum_{u < s} K[t,u] Delta_u + sum_{t >= s} r_t + sum_{u < s} c_u Delta_u
+//         + e^{a_end} <S_in, dS_out>
+// whose differences are sums of K's columns and rows without its diagonal:
+//   g_{s+1} - g_s = Delta_s (sum_{t > s} K[t,s] + c_s) - sum_{u < s} K[s,u] Delta_u - r_s
+//   dDelta_s = sum_{t >= s} K[t,s] + c_s + A g_s,   dA = sum Delta_s g_s,
+//   ddt = dDelta softplus'(dt + bias),   dD = sum_t M[t,t]
+// For bf16 IO K comes from products of the inputs as they are (dy, where it is gated,
+// as a bf16 value and its remainder, as are S_in and dS_out), so these sums carry 16
+// bits; G L and M L are rounded to bf16 where they enter the products for dx, dB and
+// dC, which are rounded to bf16 themselves.
+//
+// A workgroup takes a chunk and up to 8 heads of a group; a wavefront owns 16 of the
+// chunk's tokens, as s for dx and dB and as t for dC.  G, the sum over the heads of M
+// L Delta, and dB and dC stay in registers from head to head, so dB and dC cost one
+// product with C and B for all heads.
+#include <algorithm>
+
+#include "abi_checks.h"
+#include "ssd_chunk.h"
+
+namespace ssm {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+constexpr int QB = kQ / 16;
+
+// Keeps the loads of one tile's operands from being moved ahead of the tiles before
+// it: unrolled as they are, all of them at once would not fit the registers.
+__device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0); }
+
+struct GradParams {
+  void* dx;          // contiguous (row, token, H, P)
+  void* ddt;         // contiguous (row, token, H)
+  void* dB;          // contiguous (row, token, G, N), where a group has one workgroup
+  void* dC;
+  float* parts;      // [3][H][nc] sums of dA, ddt_bias and dD
+  float* dBparts;    // [block][row, token][G][N], where it has several
+  float* dCparts;
+  int64_t tokens;    // of all rows
+};
+
+template <typename T, int NMAX, bool kGate, bool kVec>
+__global__ __launch_bounds__(kThreads, 2) void ssd_grad_kernel(ChunkParams p, GradParams q, int grid) {
+  using E = typename Lds<T>::E;
+  using F = typename Frag<T>::V;
+  constexpr bool kBF = sizeof(T) == 2;
+  constexpr int kPad = 16 / sizeof(E), NP = NMAX + kPad, XP = kPB + kPad, GP = kQ + kPad, NT = NMAX / 16;
+  // heads: x, dy (and its remainder), a state (and its remainder); before and after
+  // them: B and C, and the sum over the heads
+  constexpr int kX = 0, kDy = kQ * XP, kDyl = 2 * kQ * XP, kS = (kGate && kBF ? 3 : 2) * kQ * XP, kSl = kS + kPB * NP;
+  constexpr int kHead = kS + (kBF ? 2 : 1) * kPB * NP, kEnds = 2 * kQ * NP + kQ * GP;
+  __shared__ __align__(16) E lds[kHead > kEnds ? kHead : kEnds];
+  __shared__ __align__(16) float sDl[kMostHeads][kQ];
+  __shared__ __align__(16) float sLa[kMostHeads][kQ];
+  __shared__ float sSlope[kMostHeads][kQ];
+  __shared__ float sRow[kWaves][kQ], sCol[kQ], sDiag[kQ], sC0[kQ], sR[kQ], sM0[kQ], sE[kWaves];
+  const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lq = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int id = static_cast<int>(xcd_order(blockIdx.x, grid));
+  const int c = id / (p.G * p.blocks), g = id / p.blocks % p.G, block = id % p.blocks, h0 = g * p.per_group + block * p.hb;
+  const int heads = min(p.hb, (g + 1) * p.per_group - h0);
+  const Chunk k = chunk_of(p, c);
+  if (k.len == 0) {   // not a chunk: nothing to the sums
+    for (int i = tid; i < 3 * heads; i += kThreads) q.parts[(static_cast<int64_t>(i % 3) * p.H + h0 + i / 3) * p.nc + c] = 0.0f;
+    return;
+  }
+  for (int i = wave; i < heads; i += kWaves) {
+    const Steps s = steps_of<T>(p, k, h0 + i, lane);
+    sDl[i][lane] = s.delta;
+    sLa[i][lane] = s.la;
+    sSlope[i][lane] = s.slope;
+  }
+  E* const sB = lds;
+  E* const sC = lds + kQ * NP;
+  auto stage_bc = [&]() {
+    stage_rows<T, NMAX, kThreads, kVec>(sB, NP, rows_of<T>(p.B, k, g, 0, p.N), tid);
+    stage_rows<T, NMAX, kThreads, kVec>(sC, NP, rows_of<T>(p.C, k, g, 0, p.N), tid);
+  };
+  stage_bc();
+  __syncthreads();
+
+  // lane's token, as s and as t; its B and C, states 16 n + 4 lq ..
+  const int own = 16 * wave + lr;
+  F bf[NT], cf[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    bf[n] = frag_along<T>(sB, NP, 16 * wave, 16 * n, lr, lq);
+    cf[n] = frag_along<T>(sC, NP, 16 * wave, 16 * n, lr, lq);
+  }
+  // tiles of G and of the sum over the heads: lane holds t = 16 tb + 4 lq + i, s = own
+  v4f G[QB], sum[QB], dB[NT], dC[NT];
+#pragma unroll
+  for (int tb = 0; tb < QB; ++tb) {
+    G[tb] = sum[tb] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    if (tb < wave) continue;
+    if constexpr (kBF) {
+#pragma unroll
+      for (int n = 0; n < NT; n += 2)
+        G[tb] = mma32(frag_along<T>(sC, NP, 16 * tb, 16 * n, lr, lq), frag_along<T>(sC, NP, 16 * tb, 16 * n + 16, lr, lq), bf[n],
+                      bf[n + 1], G[tb]);
+    } else {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) G[tb] = mma16<T>(frag_along<T>(sC, NP, 16 * tb, 16 * n, lr, lq), bf[n], G[tb]);
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n) dB[n] = dC[n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  __syncthreads();
+
+  E* const sX = lds + kX;
+  E* const sY = lds + kDy;
+  [[maybe_unused]] E* const sYl = lds + kDyl;
+  E* const sS = lds + kS;
+  [[maybe_unused]] E* const sSl = lds + kSl;
+  const int nt = (p.N + 15) / 16;
+  constexpr int kPer = NMAX / 4, kN = kPB * kPer / kThreads;   // pieces of a state row, of a thread
+  auto put_state = [&](int at, int j, const v4u& v) {
+    const int r = at / kPer + j * (kThreads / kPer), n = at % kPer * 4;
+    if constexpr (kBF) {
+      *reinterpret_cast<v2u*>(sS + r * NP + n) = v2u{highs(v[0], v[1]), highs(v[2], v[3])};
+      *reinterpret_cast<v2u*>(sSl + r * NP + n) = v2u{lows(v[0], v[1]), lows(v[2], v[3])};
+    } else {
+      *reinterpret_cast<v4u*>(sS + r * NP + n) = v;
+    }
+  };
+  auto held = [&](uint32_t v) { return kBF ? joined_bf16(v) : __uint_as_float(v); };
+  // a 16 x 16 tile of the state (rows n, k = channel) times x or dy of `own`; the
+  // remainders' products in the k = 32 form too: sums whose chain of products mixed
+  // it with the k = 16 form came out wrong
+  auto state_tile = [&](int n, int kbs, const F (&f)[kPB / 16], [[maybe_unused]] const F (&fl)[kPB / 16], auto with_rest) {
+    v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    if constexpr (kBF) {
+#pragma unroll
+      for (int kb = 0; kb < kPB / 16; kb += 2) {
+        if (kb >= kbs) continue;
+        const F s0 = frag_down<T>(sS, NP, 16 * kb, 16 * n, lr, lq), s1 = frag_down<T>(sS, NP, 16 * kb + 16, 16 * n, lr, lq);
+        acc = mma32(s0, frag_down<T>(sSl, NP, 16 * kb, 16 * n, lr, lq), f[kb], f[kb], acc);
+        acc = mma32(s1, frag_down<T>(sSl, NP, 16 * kb + 16, 16 * n, lr, lq), f[kb + 1], f[kb + 1], acc);
+        if constexpr (decltype(with_rest)::value) acc = mma32(s0, s1, fl[kb], fl[kb + 1], acc);
+      }
+    } else {
+#pragma unroll
+      for (int kb = 0; kb < kPB / 16; ++kb)
+        if (kb < kbs) acc = mma16<T>(frag_down<T>(sS, NP, 16 * kb, 16 * n, lr, lq), f[kb], acc);
+    }
+    return acc;
+  };
+
+  for (int i = 0; i < heads; ++i) {
+    const int h = h0 + i;
+    // offsets of staged pieces are computed anew for each head: kept across the loop,
+    // all of them would take half the registers
+    int at = tid;
+    asm volatile("" : "+v"(at));
+    const float la_s = sLa[i][own], dl_s = sDl[i][own];
+    const float ew = __builtin_amdgcn_exp2f(sLa[i][kQ - 1] - la_s), ea = __builtin_amdgcn_exp2f(la_s);
+    const float Dh = p.D ? p.D[h] : 0.0f;
+    v4f M[QB];
+#pragma unroll
+    for (int tb = 0; tb < QB; ++tb) M[tb] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    float r_t = 0.0f, c_s = 0.0f, pairs = 0.0f;
+    const int64_t state_at = (static_cast<int64_t>(c) * p.H + h) * p.P * p.N;
+    // x and dy of channels p0 .. of the head
+    auto stage_tokens = [&](int p0, bool with_x) {
+      if (with_x) stage_rows<T, kPB, kThreads, kVec>(sX, XP, rows_of<T>(p.x, k, h, p0, p.P), at);
+      const Rows64 er = rows_of<T>(p.dout, k, h, p0, p.P);
+      if constexpr (!kGate) {
+        stage_rows<T, kPB, kThreads, kVec>(sY, XP, er, at);
+      } else {
+        const Rows64 zr = rows_of<T>(p.z, k, h, p0, p.P);
+        constexpr int kPerX = kPB / kPiece<T>, kStep = kThreads / kPerX, kNX = kQ / kStep;
+        const int r0 = at / kPerX, col = at % kPerX * kPiece<T>;
+        v4u va[kNX], za[kNX];
+#pragma unroll
+        for (int j = 0; j < kNX; ++j) {
+          va[j] = load_piece<T, kVec>(er, r0 + j * kStep, col);
+          za[j] = load_piece<T, kVec>(zr, r0 + j * kStep, col);
+        }
+#pragma unroll
+        for (int j = 0; j < kNX; ++j) {
+          const int r = r0 + j * kStep;
+          const v4u v = va[j], z = za[j];
+          uint32_t s[kPiece<T>];
+#pragma unroll
+          for (int e = 0; e < kPiece<T>; ++e) {
+            const float f = piece_f32<T>(v, e) * silu_f32(piece_f32<T>(z, e));
+            s[e] = kBF ? split_bf16(f) : __float_as_uint(f);
+          }
+          if constexpr (kBF) {
+            *reinterpret_cast<v4u*>(sY + r * XP + col) = v4u{highs(s[0], s[1]), highs(s[2], s[3]), highs(s[4], s[5]), highs(s[6], s[7])};
+            *reinterpret_cast<v4u*>(sYl + r * XP + col) = v4u{lows(s[0], s[1]), lows(s[2], s[3]), lows(s[4], s[5]), lows(s[6], s[7])};
+          } else {
+            *reinterpret_cast<v4u*>(sY + r * XP + col) = v4u{s[0], s[1], s[2], s[3]};
+          }
+        }
+      }
+    };
+    F xf[kPB / 16], yf[kPB / 16], yl[kPB / 16];
+    for (int p0 = 0; p0 < p.P; p0 += kPB) {
+      const int cols = p.P - p0, kbs = (min(kPB, cols) + 15) / 16;
+      if (p0 > 0) __syncthreads();
+      stage_tokens(p0, true);
+      const StateRows in = state_rows(p.state, state_at + static_cast<int64_t>(p0) * p.N, min(kPB, cols), p.N);
+#pragma unroll
+      for (int j = 0; j < kN; ++j) put_state(at, j, load_states<kVec>(in, at / kPer + j * (kThreads / kPer), at % kPer * 4));
+      __syncthreads();
+#pragma unroll
+      for (int kb = 0; kb < kPB / 16; ++kb) {
+        xf[kb] = frag_along<T>(sX, XP, 16 * wave, 16 * kb, lr, lq);
+        yf[kb] = frag_along<T>(sY, XP, 16 * wave, 16 * kb, lr, lq);
+        if constexpr (kGate && kBF) yl[kb] = frag_along<T>(sYl, XP, 16 * wave, 16 * kb, lr, lq);
+        else yl[kb] = yf[kb];
+      }
+      // M[t][s] += dy_t . x_s
+#pragma unroll
+      for (int tb = 0; tb < QB; ++tb) {
+        if (tb < wave) continue;
+#pragma unroll
+        for (int kb = 0; kb < kPB / 16; kb += kBF ? 2 : 1) {
+          if (kb >= kbs) continue;
+          const F y0 = frag_along<T>(sY, XP, 16 * tb, 16 * kb, lr, lq);
+          if constexpr (kBF) {
+            M[tb] = mma32(y0, frag_along<T>(sY, XP, 16 * tb, 16 * kb + 16, lr, lq), xf[kb], xf[kb + 1], M[tb]);
+            if constexpr (kGate)
+              M[tb] = mma32(frag_along<T>(sYl, XP, 16 * tb, 16 * kb, lr, lq), frag_along<T>(sYl, XP, 16 * tb, 16 * kb + 16, lr, lq),
+                            xf[kb], xf[kb + 1], M[tb]);
+          } else {
+            M[tb] = mma16<T>(y0, xf[kb], M[tb]);
+          }
+        }
+        keep_order();
+      }
+      // S_in^T dy_t: lane holds states 16 n + 4 lq + e
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        if (n >= nt) continue;
+        const v4f v = state_tile(n, kbs, yf, yl, std::integral_constant<bool, kGate>{});
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r_t = fmaf(elem<T>(cf[n], e), v[e], r_t);
+        dC[n] += v * ea;
+        keep_order();
+      }
+      __syncthreads();
+      // dS_out in the place of S_in, which it meets on the way
+      const StateRows leaving = state_rows(p.dstate, state_at + static_cast<int64_t>(p0) * p.N, min(kPB, cols), p.N);
+#pragma unroll
+      for (int j = 0; j < kN; ++j) {
+        const int r = at / kPer + j * (kThreads / kPer), n = at % kPer * 4;
+        const v4u v = load_states<kVec>(leaving, r, n);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float s = Lds<T>::f(sS[r * NP + n + e]);
+          if constexpr (kBF) s += Lds<T>::f(sSl[r * NP + n + e]);
+          pairs = fmaf(s, held(v[e]), pairs);
+        }
+        put_state(at, j, v);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        if (n >= nt) continue;
+        const v4f v = state_tile(n, kbs, xf, xf, std::false_type{});
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c_s = fmaf(elem<T>(bf[n], e), v[e], c_s);
+        dB[n] += v * (ew * dl_s);
+        keep_order();
+      }
+    }
+    // K, its sums, and the operands of dx
+    F gl[QB];
+    float col = 0.0f, diag = 0.0f, m0 = 0.0f;
+#pragma unroll
+    for (int tb = 0; tb < QB; ++tb) {
+      if (tb < wave) {
+        gl[tb] = tofrag<T>(0.0f, 0.0f, 0.0f, 0.0f);
+        continue;
+      }
+      const v4f la_t = *reinterpret_cast<const v4f*>(&sLa[i][16 * tb + 4 * lq]);
+      v4f w, rows;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int t = 16 * tb + 4 * lq + e;
+        const float L = t >= own ? __builtin_amdgcn_exp2f(la_t[e] - la_s) : 0.0f;
+        w[e] = t >= own ? G[tb][e] * L : 0.0f;
+        const float m = t >= own ? M[tb][e] : 0.0f;
+        sum[tb][e] = fmaf(m * L, dl_s, sum[tb][e]);
+        const float K = w[e] * m;
+        const bool strict = t > own;
+        rows[e] = strict ? K * dl_s : 0.0f;
+        col += strict ? K : 0.0f;
+        diag += t == own ? K : 0.0f;
+        m0 += t == own ? m : 0.0f;
+      }
+      gl[tb] = tofrag<T>(w[0], w[1], w[2], w[3]);
+      const float s = row_sums(rows, lane);
+      if (lr < 4) sRow[wave][16 * tb + 4 * lq + lr] = s;
+      keep_order();
+    }
+    col = quarter_sum(col);
+    diag = quarter_sum(diag);
+    m0 = quarter_sum(m0);
+    r_t = quarter_sum(r_t) * ea;
+    c_s = quarter_sum(c_s) * ew;
+    pairs = wave_sum(pairs);
+    if (lq == 0) {
+      sCol[own] = col;
+      sDiag[own] = diag;
+      sM0[own] = m0;
+      sR[own] = r_t;
+      sC0[own] = c_s;
+    }
+    if (lane == 0) sE[wave] = pairs * __builtin_amdgcn_exp2f(sLa[i][kQ - 1]);
+    // dx
+    for (int p0 = 0; p0 < p.P; p0 += kPB) {
+      const int cols = p.P - p0, pts = (min(kPB, cols) + 15) / 16;
+      if (p.P > kPB) {   // what is in LDS is the last pass's
+        __syncthreads();
+        stage_tokens(p0, false);
+        const StateRows leaving = state_rows(p.dstate, state_at + static_cast<int64_t>(p0) * p.N, min(kPB, cols), p.N);
+#pragma unroll
+        for (int j = 0; j < kN; ++j) put_state(at, j, load_states<kVec>(leaving, at / kPer + j * (kThreads / kPer), at % kPer * 4));
+        __syncthreads();
+      }
+#pragma unroll
+      for (int pt = 0; pt < kPB / 16; ++pt) {
+        if (pt >= pts) continue;
+        v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int n = 0; n < NT; n += kBF ? 2 : 1) {
+          if (n >= nt) continue;
+          const F s0 = frag_along<T>(sS, NP, 16 * pt, 16 * n, lr, lq);
+          if constexpr (kBF) acc = mma32(s0, frag_along<T>(sS, NP, 16 * pt, 16 * n + 16, lr, lq), bf[n], bf[n + 1], acc);
+          else acc = mma16<T>(s0, bf[n], acc);
+        }
+        acc *= ew;
+#pragma unroll
+        for (int tb = 0; tb < QB; tb += kBF ? 2 : 1) {
+          if (tb + (kBF ? 1 : 0) < wave) continue;
+          const F y0 = frag_down<T>(sY, XP, 16 * tb, 16 * pt, lr, lq);
+          if constexpr (kBF) acc = mma32(y0, frag_down<T>(sY, XP, 16 * tb + 16, 16 * pt, lr, lq), gl[tb], gl[tb + 1], acc);
+          else acc = mma16<T>(y0, gl[tb], acc);
+        }
+        keep_order();
+        const int c0 = 16 * pt + 4 * lq;
+        if (own >= k.len || c0 >= cols) continue;
+        float d[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) d[e] = fmaf(dl_s, acc[e], Dh * Lds<T>::f(sY[own * XP + c0 + e]));
+        T* const to = static_cast<T*>(q.dx) + ((k.b * p.L + k.t0 + own) * p.H + h) * p.P + p0 + c0;
+        if constexpr (kVec) {
+          if constexpr (kBF) *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3]));
+          else *reinterpret_cast<float4*>(to) = make_float4(d[0], d[1], d[2], d[3]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (c0 + e < cols) io<T>::store(to + e, d[e]);
+        }
+      }
+    }
+    __syncthreads();   // the sums are there, and LDS is free
+    if (wave == i % kWaves) {   // the steps' gradients; written over after the next barrier
+      float row = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w)
+        if (w <= lane / 16) row += sRow[w][lane];
+      const float dl = sDl[i][lane], cs = sC0[lane], cl = sCol[lane], r = sR[lane];
+      const float step = dl * (cl + cs) - row - r;
+      float g0 = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) g0 += sE[w];
+      const float flow = wave_sum(r) + g0 + (wave_prefix_sum(step) - step);
+      float d = cl + sDiag[lane] + cs + p.A[h] * flow;
+      d = lane < k.len ? d * sSlope[i][lane] : 0.0f;
+      if (lane < k.len) io<T>::store(static_cast<T*>(q.ddt) + (k.b * p.L + k.t0 + lane) * p.H + h, d);
+      const float da = wave_sum(dl * flow), db = wave_sum(d), dd = wave_sum(sM0[lane]);
+      if (lane < 3) q.parts[(static_cast<int64_t>(lane) * p.H + h) * p.nc + c] = lane == 0 ? da : lane == 1 ? db : dd;
+    }
+  }
+
+  // dB and dC of the chunk: the products with C and B, over the sum of the heads
+  E* const sG = lds + 2 * kQ * NP;   // [t][s]
+  stage_bc();
+  F sf[QB];
+#pragma unroll
+  for (int tb = 0; tb < QB; ++tb) {
+    sf[tb] = tofrag<T>(sum[tb][0], sum[tb][1], sum[tb][2], sum[tb][3]);
+    if (tb < wave) continue;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sG[(16 * tb + 4 * lq + e) * GP + own] = Lds<T>::from(sum[tb][e]);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int tb = 0; tb < QB; ++tb) {
+    if (tb >= wave) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        if (n < nt) dB[n] = mma16<T>(frag_down<T>(sC, NP, 16 * tb, 16 * n, lr, lq), sf[tb], dB[n]);
+    }
+    if (tb <= wave) {
+      const F gf = frag_along<T>(sG, GP, 16 * wave, 16 * tb, lr, lq);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        if (n < nt) dC[n] = mma16<T>(frag_down<T>(sB, NP, 16 * tb, 16 * n, lr, lq), gf, dC[n]);
+    }
+  }
+  if (own >= k.len) return;
+  const int64_t token = k.b * p.L + k.t0 + own, at = (token * p.G + g) * p.N;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int s0 = 16 * n + 4 * lq;
+    if (s0 >= p.N) continue;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      const v4f v = which ? dC[n] : dB[n];
+      if (p.blocks > 1) {
+        float* const to = (which ? q.dCparts : q.dBparts) + block * q.tokens * p.G * p.N + at + s0;
+        if constexpr (kVec) {
+          *reinterpret_cast<v4f*>(to) = v;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (s0 + e < p.N) to[e] = v[e];
+        }
+      } else {
+        T* const to = static_cast<T*>(which ? q.dC : q.dB) + at + s0;
+        if constexpr (kVec) {
+          if constexpr (kBF) *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+          else *reinterpret_cast<v4f*>(to) = v;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (s0 + e < p.N) io<T>::store(to + e, v[e]);
+        }
+      }
+    }
+  }
+}
+
+// dB and dC from the workgroups' parts, in their order; packed: only for tokens of
+// a sequence (the others' rows are cleared elsewhere).
+template <typename T>
+__global__ __launch_bounds__(kThreads) void ssd_sum_parts_kernel(const float* parts, int blocks, int64_t n, int64_t row,
+                                                                 const int32_t* cu, int64_t nseq, int64_t L, T* dB, T* dC) {
+  int64_t lo = 0, hi = n;
+  if (cu) {
+    lo = min(max(int64_t{cu[0]}, int64_t{0}), L) * row;
+    hi = min(max(int64_t{cu[nseq]}, int64_t{0}), L) * row;
+  }
+  const float* const from = parts + blockIdx.y * blocks * n;
+  T* const to = blockIdx.y ? dC : dB;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * kThreads) {
+    if (i < lo || i >= hi) continue;
+    float s = 0.0f;
+    for (int b = 0; b < blocks; ++b) s += from[b * n + i];
+    io<T>::store(to + i, s);
+  }
+}
+
+// dA, ddt_bias and dD of a head: its chunks' sums, in a fixed order.
+__global__ __launch_bounds__(kThreads) void ssd_sum_heads_kernel(const float* parts, int nc, int H, float* dA, float* dbias, float* dD) {
+  __shared__ float sums[kWaves];
+  const int h = blockIdx.x, which = blockIdx.y;
+  float s = 0.0f;
+  for (int c = threadIdx.x; c < nc; c += kThreads) s += parts[(static_cast<int64_t>(which) * H + h) * nc + c];
+  s = wave_sum(s);
+  if (threadIdx.x % 64 == 0) sums[threadIdx.x / 64] = s;
+  __syncthreads();
+  float* const to = which == 0 ? dA : which == 1 ? dbias : dD;
+  if (threadIdx.x == 0 && to) to[h] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+}
+
+size_t align_up(size_t n) { return (n + 255) / 256 * 256; }
+
+// Where the parts of a workspace lie (bytes).
+struct Layout {
+  size_t table, seq_chunk, lam, state, dstate, parts, bc, size;
+};
+Layout layout_of(const ChunkPlan& q, bool packed, bool backward, int64_t nseq, int64_t H, int64_t P, int64_t N, int64_t G, int64_t tokens) {
+  Layout l;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += align_up(bytes);
+    return here;
+  };
+  const size_t states = static_cast<size_t>(q.nc) * H * P * N * 4;
+  l.table = take(packed ? static_cast<size_t>(q.nc) * sizeof(ChunkEntry) : 0);
+  l.seq_chunk = take(packed ? static_cast<size_t>(nseq + 1) * 4 : 0);
+  l.lam = take(static_cast<size_t>(q.nc) * H * 4);
+  l.state = take(states);
+  l.dstate = take(backward ? states : 0);
+  l.parts = take(backward ? static_cast<size_t>(3) * H * q.nc * 4 : 0);
+  l.bc = take(backward && q.blocks > 1 ? static_cast<size_t>(2) * q.blocks * tokens * G * N * 4 : 0);
+  l.size = at;
+  return l;
+}
+
+TokenTensor tensor(const void* ptr, int64_t sb, int64_t ss, int64_t sh, int64_t inner, bool bf16) {
+  const int64_t piece = bf16 ? 8 : 4;
+  const bool vec = inner % piece == 0 && reinterpret_cast<uintptr_t>(ptr) % 16 == 0 && sb % piece == 0 && ss % piece == 0 &&
+                   sh % piece == 0;
+  return TokenTensor{ptr, sb, ss, sh, vec};
+}
+
+template <typename T, int NMAX>
+void launch_grad(const ChunkParams& p, const GradParams& q, hipStream_t stream) {
+  const int grid = p.nc * p.G * p.blocks;
+  auto go = [&](auto gate, auto vec) {
+    ssd_grad_kernel<T, NMAX, gate.value, vec.value><<<grid, kThreads, 0, stream>>>(p, q, grid);
+  };
+  if (p.z.p && p.vec) go(std::true_type{}, std::true_type{});
+  else if (p.z.p) go(std::true_type{}, std::false_type{});
+  else if (p.vec) go(std::false_type{}, std::true_type{});
+  else go(std::false_type{}, std::false_type{});
+}
+
+// The parameters that both calls have.
+template <typename Args>
+ChunkParams params_of(const Args& a, const ChunkPlan& q, const Layout& l, bool packed) {
+  char* const ws = static_cast<char*>(a.workspace);
+  ChunkParams p{};
+  p.A = a.A;
+  p.D = a.D;
+  p.bias = a.dt_bias;
+  p.L = static_cast<int>(a.seqlen);
+  p.H = static_cast<int>(a.nheads);
+  p.P = static_cast<int>(a.headdim);
+  p.G = static_cast<int>(groups_of(a.ngroups));
+  p.N = static_cast<int>(a.dstate);
+  p.per_group = p.H / p.G;
+  p.softplus = a.dt_softplus != 0;
+  p.nc = static_cast<int>(q.nc);
+  p.per_row = static_cast<int>(q.per_row);
+  p.hb = static_cast<int>(q.hb);
+  p.blocks = static_cast<int>(q.blocks);
+  p.table = packed ? reinterpret_cast<const ChunkEntry*>(ws + l.table) : nullptr;
+  p.seq_chunk = packed ? reinterpret_cast<const int32_t*>(ws + l.seq_chunk) : nullptr;
+  p.lam = reinterpret_cast<float*>(ws + l.lam);
+  p.state = reinterpret_cast<uint32_t*>(ws + l.state);
+  p.dstate = reinterpret_cast<uint32_t*>(ws + l.dstate);
+  p.dt = a.dt;
+  p.dts = a.dt_seq_stride;
+  return p;
+}
+
+ChunkPlan plan_of(const ssm_ssd_packed_args& a) {
+  return chunk_plan(1, a.seqlen, a.nseq, true, a.nheads, groups_of(a.ngroups));
+}
+ChunkPlan plan_of(const ssm_ssd_bwd_args& a) {
+  return chunk_plan(a.batch, a.seqlen, a.nseq, a.cu_seqlens != nullptr, a.nheads, groups_of(a.ngroups));
+}
+Layout layout(const ssm_ssd_packed_args& a, const ChunkPlan& q) {
+  return layout_of(q, true, false, a.nseq, a.nheads, a.headdim, a.dstate, groups_of(a.ngroups), a.seqlen);
+}
+Layout layout(const ssm_ssd_bwd_args& a, const ChunkPlan& q) {
+  return layout_of(q, a.cu_seqlens != nullptr, true, a.nseq, a.nheads, a.headdim, a.dstate, groups_of(a.ngroups),
+                   a.batch * a.seqlen);
+}
+
+}  // namespace
+
+size_t ssd_packed_workspace_bytes(const ssm_ssd_packed_args& a) { return layout(a, plan_of(a)).size; }
+size_t ssd_bwd_workspace_bytes(const ssm_ssd_bwd_args& a) { return layout(a, plan_of(a)).size; }
+
+hipError_t launch_ssd_packed_fwd(const ssm_ssd_packed_args& a, hipStream_t stream) {
+  const ChunkPlan q = plan_of(a);
+  const Layout l = layout(a, q);
+  const bool bf16 = a.io_dtype == SSM_BF16;
+  const int64_t es = bf16 ? 2 : 4;
+  ChunkParams p = params_of(a, q, l, true);
+  const int64_t Bg = p.G > 1 ? a.B_group_stride : 0, Cg = p.G > 1 ? a.C_group_stride : 0;
+  p.x = tensor(a.x, 0, a.x_seq_stride, a.x_head_stride, p.P, bf16);
+  p.z = tensor(a.z, 0, a.z_seq_stride, a.z_head_stride, p.P, bf16);
+  p.B = tensor(a.B, 0, a.B_seq_stride, Bg, p.N, bf16);
+  p.C = tensor(a.C, 0, a.C_seq_stride, Cg, p.N, bf16);
+  OutsideRows rows;
+  if (a.zero_outside && a.seqlen > 0) {
+    const bool whole = a.out_head_stride == a.headdim;   // the heads side by side
+    rows.add(a.out, (whole ? a.nheads : 1) * a.headdim * es, a.out_seq_stride * es, whole ? 1 : a.nheads, a.out_head_stride * es);
+  }
+  hipError_t e = launch_chunk_table(a.cu_seqlens, a.seqlen, a.nseq, q.nc, reinterpret_cast<ChunkEntry*>(static_cast<char*>(a.workspace) + l.table),
+                                    reinterpret_cast<int32_t*>(static_cast<char*>(a.workspace) + l.seq_chunk), rows, stream);
+  if (e != hipSuccess) return e;
+  e = launch_chunk_states(p, bf16, false, a.nseq, a.h0, a.last_state, nullptr, nullptr, stream);
+  if (e != hipSuccess) return e;
+  p.vec = p.x.vec && p.B.vec && p.C.vec && tensor(a.out, 0, a.out_seq_stride, a.out_head_stride, p.P, bf16).vec && (!a.z || p.z.vec);
+  const ChunkOut o{a.out, 0, a.out_seq_stride, a.out_head_stride, nullptr};
+  return launch_chunk_outputs(p, o, bf16, stream);
+}
+
+hipError_t launch_ssd_bwd(const ssm_ssd_bwd_args& a, hipStream_t stream) {
+  const ChunkPlan q = plan_of(a);
+  const Layout l = layout(a, q);
+  const bool bf16 = a.io_dtype == SSM_BF16, packed = a.cu_seqlens != nullptr;
+  const int64_t es = bf16 ? 2 : 4;
+  char* const ws = static_cast<char*>(a.workspace);
+  ChunkParams p = params_of(a, q, l, packed);
+  const int64_t Bg = p.G > 1 ? a.B_group_stride : 0, Cg = p.G > 1 ? a.C_group_stride : 0;
+  p.dtb = a.dt_batch_stride;
+  p.x = tensor(a.x, a.x_batch_stride, a.x_seq_stride, a.x_head_stride, p.P, bf16);
+  p.z = tensor(a.z, a.z_batch_stride, a.z_seq_stride, a.z_head_stride, p.P, bf16);
+  p.B = tensor(a.B, a.B_batch_stride, a.B_seq_stride, Bg, p.N, bf16);
+  p.C = tensor(a.C, a.C_batch_stride, a.C_seq_stride, Cg, p.N, bf16);
+  p.dout = tensor(a.dout, a.dout_batch_stride, a.dout_seq_stride, a.dout_head_stride, p.P, bf16);
+  auto aligned = [](const void* ptr) { return reinterpret_cast<uintptr_t>(ptr) % 16 == 0; };
+  p.vec = p.x.vec && p.B.vec && p.C.vec && p.dout.vec && aligned(a.dx) && aligned(a.dB) && aligned(a.dC) &&
+          (!a.z || (p.z.vec && aligned(a.dz)));
+  const int64_t HP = a.nheads * a.headdim, GN = static_cast<int64_t>(p.G) * p.N;
+  hipError_t e = hipSuccess;
+  if (packed) {
+    OutsideRows rows;
+    if (a.seqlen > 0) {
+      rows.add(a.dx, HP * es, HP * es);
+      rows.add(a.ddt, a.nheads * es, a.nheads * es);
+      rows.add(a.dB, GN * es, GN * es);
+      rows.add(a.dC, GN * es, GN * es);
+      if (a.z) rows.add(a.dz, HP * es, HP * es);
+    }
+    e = launch_chunk_table(a.cu_seqlens, a.seqlen, a.nseq, q.nc, reinterpret_cast<ChunkEntry*>(ws + l.table),
+                           reinterpret_cast<int32_t*>(ws + l.seq_chunk), rows, stream);
+    if (e != hipSuccess) return e;
+  }
+  e = launch_chunk_states(p, bf16, true, packed ? a.nseq : a.batch, a.h0, nullptr, a.dlast, a.dh0, stream);
+  if (e != hipSuccess) return e;
+  if (q.nc > 0) {
+    if (a.z) {
+      const ChunkOut o{nullptr, a.seqlen * HP, HP, a.headdim, a.dz};
+      e = launch_chunk_outputs(p, o, bf16, stream);
+      if (e != hipSuccess) return e;
+    }
+    GradParams g{a.dx, a.ddt, a.dB, a.dC, reinterpret_cast<float*>(ws + l.parts), reinterpret_cast<float*>(ws + l.bc), nullptr,
+                 a.batch * a.seqlen};
+    g.dCparts = g.dBparts + q.blocks * g.tokens * GN;
+    if (!bf16) launch_grad<float, 64>(p, g, stream);
+    else if (p.N > 64) launch_grad<uint16_t, 128>(p, g, stream);
+    else launch_grad<uint16_t, 64>(p, g, stream);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (q.blocks > 1) {
+      const int64_t n = g.tokens * GN;
+      const dim3 grid(static_cast<unsigned>(std::min<int64_t>((n + kThreads - 1) / kThreads, 4096)), 2);
+      if (bf16)
+        ssd_sum_parts_kernel<uint16_t><<<grid, kThreads, 0, stream>>>(g.dBparts, p.blocks, n, GN, a.cu_seqlens, a.nseq, a.seqlen,
+                                                                      static_cast<uint16_t*>(a.dB), static_cast<uint16_t*>(a.dC));
+      else
+        ssd_sum_parts_kernel<float><<<grid, kThreads, 0, stream>>>(g.dBparts, p.blocks, n, GN, a.cu_seqlens, a.nseq, a.seqlen,
+                                                                   static_cast<float*>(a.dB), static_cast<float*>(a.dC));
+    }
+  }
+  ssd_sum_heads_kernel<<<dim3(p.H, 3), kThreads, 0, stream>>>(reinterpret_cast<float*>(ws + l.parts), p.nc, p.H, a.dA, a.ddt_bias, a.dD);
+  return hipGetLastError();
+}
+
+}  // namespace ssm

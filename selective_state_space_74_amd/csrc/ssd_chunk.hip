@@ -1,0 +1,487 @@
+// ssd_chunk.hip -- the states of chunks, and the outputs from them: the
+// chunk-parallel SSD prefill over packed sequences, gfx950 (see ssd_chunk.h).
+#include <algorithm>
+
+#include "ssd_chunk.h"
+
+namespace ssm {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+
+// ---- the chunks of packed sequences --------------------------------------------
+
+// Workgroup 0: each sequence's count of chunks, their sums, and the chunks.  The
+// bounds are held to the row and the chunks to nc, whatever the bounds say.  The
+// other workgroups clear rows of tokens outside every sequence.
+constexpr int kTableThreads = 1024;
+__global__ __launch_bounds__(kTableThreads) void chunk_table_kernel(const int32_t* cu, int64_t L, int64_t nseq, int nc,
+                                                                    ChunkEntry* table, int32_t* seq_chunk, OutsideRows rows) {
+  const int tid = threadIdx.x;
+  auto bound = [&](int64_t i) { return min(max(int64_t{cu[i]}, int64_t{0}), L); };
+  if (blockIdx.x > 0) {
+    const int64_t lo = bound(0), hi = max(bound(nseq), lo), n = lo + (L - hi);
+    for (int64_t i = blockIdx.x - 1; i < n; i += gridDim.x - 1) {
+      const int64_t t = i < lo ? i : hi + (i - lo);
+      for (int k = 0; k < rows.n; ++k) {
+        const OutsideRows::Tensor& r = rows.t[k];
+        for (int64_t h = 0; h < r.heads; ++h) {
+          uint16_t* const q = reinterpret_cast<uint16_t*>(static_cast<char*>(r.p) + t * r.stride + h * r.head_stride);
+          for (int64_t j = tid; j < r.bytes / 2; j += kTableThreads) q[j] = 0;
+        }
+      }
+    }
+    return;
+  }
+  __shared__ int32_t part[kTableThreads / 64];
+  int64_t before = 0;   // chunks of the sequences done
+  for (int64_t base = 0; base < nseq; base += kTableThreads) {
+    const int64_t k = base + tid;
+    int count = 0;
+    if (k < nseq) {
+      const int64_t lo = bound(k), hi = max(bound(k + 1), lo);
+      count = static_cast<int>((hi - lo + kQ - 1) / kQ);
+    }
+    int sum = count;   // inclusive, over the wavefront and then the workgroup
+    for (int d = 1; d < 64; d <<= 1) {
+      const int v = __shfl_up(sum, d, 64);
+      if (tid % 64 >= d) sum += v;
+    }
+    if (tid % 64 == 63) part[tid / 64] = sum;
+    __syncthreads();
+    int64_t at = before + sum - count;
+    int64_t all = 0;
+    for (int w = 0; w < kTableThreads / 64; ++w) {
+      if (w < tid / 64) at += part[w];
+      all += part[w];
+    }
+    if (k < nseq) seq_chunk[k] = static_cast<int32_t>(min(at, int64_t{nc}));
+    before += all;
+    __syncthreads();
+  }
+  before = min(before, int64_t{nc});
+  if (tid == 0) seq_chunk[nseq] = static_cast<int32_t>(before);
+  __syncthreads();   // this workgroup's own stores to seq_chunk are read below
+  for (int c = tid; c < nc; c += kTableThreads) {
+    ChunkEntry e{0, 0};
+    if (c < before) {
+      int64_t a = 0, b = nseq;   // the last sequence that begins at or before chunk c
+      while (b - a > 1) {
+        const int64_t m = (a + b) / 2;
+        if (seq_chunk[m] <= c) a = m; else b = m;
+      }
+      const int64_t lo = bound(a), hi = max(bound(a + 1), lo);
+      const int64_t t0 = lo + int64_t{c - seq_chunk[a]} * kQ;
+      e.t0 = static_cast<int32_t>(min(t0, L));
+      e.len = static_cast<int32_t>(max(min(hi - t0, int64_t{kQ}), int64_t{0}));
+    }
+    table[c] = e;
+  }
+}
+
+// ---- what a chunk adds to the state ------------------------------------------------
+
+// Workgroup: (chunk, heads of one group, direction).  B (C backward) of the chunk
+// is staged once; then for each head the rows x_s (dy_t) times their weight, split
+// in two for bf16 so that the sums carry 16 bits.  A wavefront owns 16 channels of
+// the state (fewer channels: a share of its columns).  Bound by memory: the states
+// written are 4 N bytes for 2 x (64 tokens) bytes of x read.
+template <typename T, int NMAX, bool kVec>
+__global__ __launch_bounds__(kThreads) void ssd_states_kernel(ChunkParams p, int grid) {
+  using E = typename Lds<T>::E;
+  constexpr bool kBF = sizeof(T) == 2;
+  constexpr int kPad = 16 / sizeof(E), NP = NMAX + kPad, XP = kPB + kPad, NT = NMAX / 16;
+  __shared__ __align__(16) E sM[kQ * NP];
+  __shared__ __align__(16) E sX[kQ * XP];
+  __shared__ __align__(16) E sXL[kBF ? kQ * XP : 1];
+  __shared__ float sW[kMostHeads][kQ];
+  const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lq = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const bool back = blockIdx.y != 0;
+  const int id = static_cast<int>(xcd_order(blockIdx.x, grid));
+  const int c = id / (p.G * p.blocks), g = id / p.blocks % p.G, h0 = g * p.per_group + id % p.blocks * p.hb;
+  const int heads = min(p.hb, (g + 1) * p.per_group - h0);
+  const Chunk k = chunk_of(p, c);
+  if (k.len == 0) return;
+
+  for (int i = wave; i < heads; i += kWaves) {
+    const Steps s = steps_of<T>(p, k, h0 + i, lane);
+    const float end = lane_value(s.la, 63);
+    sW[i][lane] = back ? __builtin_amdgcn_exp2f(s.la) : __builtin_amdgcn_exp2f(end - s.la) * s.delta;
+    if (!back && lane == 0) p.lam[static_cast<int64_t>(c) * p.H + h0 + i] = __builtin_amdgcn_exp2f(end);
+  }
+  const TokenTensor& m = back ? p.C : p.B;
+  stage_rows<T, NMAX, kThreads, kVec>(sM, NP, rows_of<T>(m, k, g, 0, p.N), tid);
+  __syncthreads();
+
+  const TokenTensor& x = back ? p.dout : p.x;
+  const bool gate = back && p.z.p;
+  const int nt = (p.N + 15) / 16, kb = (k.len + 15) / 16;
+  for (int i = 0; i < heads; ++i) {
+    for (int p0 = 0; p0 < p.P; p0 += kPB) {
+      const Rows64 xr = rows_of<T>(x, k, h0 + i, p0, p.P);
+      Rows64 zr = xr;
+      if (gate) zr = rows_of<T>(p.z, k, h0 + i, p0, p.P);
+      const int cols = p.P - p0;
+      constexpr int kPer = kPB / kPiece<T>, kStep = kThreads / kPer, kN = kQ / kStep;
+      const int r0 = tid / kPer, col = tid % kPer * kPiece<T>;
+      v4u v[kN], zv[kN];
+#pragma unroll
+      for (int j = 0; j < kN; ++j) {
+        v[j] = load_piece<T, kVec>(xr, r0 + j * kStep, col);
+        if (gate) zv[j] = load_piece<T, kVec>(zr, r0 + j * kStep, col);
+      }
+#pragma unroll
+      for (int j = 0; j < kN; ++j) {
+        const int r = r0 + j * kStep;
+        const float w = sW[i][r];
+        uint32_t s[kPiece<T>];
+#pragma unroll
+        for (int e = 0; e < kPiece<T>; ++e) {
+          float f = piece_f32<T>(v[j], e) * w;
+          if (gate) f *= silu_f32(piece_f32<T>(zv[j], e));
+          s[e] = kBF ? split_bf16(f) : __float_as_uint(f);
+        }
+        if constexpr (kBF) {
+          *reinterpret_cast<v4u*>(sX + r * XP + col) = v4u{highs(s[0], s[1]), highs(s[2], s[3]), highs(s[4], s[5]), highs(s[6], s[7])};
+          *reinterpret_cast<v4u*>(sXL + r * XP + col) = v4u{lows(s[0], s[1]), lows(s[2], s[3]), lows(s[4], s[5]), lows(s[6], s[7])};
+        } else {
+          *reinterpret_cast<v4u*>(sX + r * XP + col) = v4u{s[0], s[1], s[2], s[3]};
+        }
+      }
+      __syncthreads();
+      // channels' tiles of this pass (1, 2 or 4) and the wavefronts that share one
+      const int pts = min(kPB, cols) > 32 ? 4 : min(kPB, cols) > 16 ? 2 : 1;
+      const int pt = wave % pts, first = wave / pts, step = kWaves / pts;
+      v4f acc[NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) acc[n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int q = 0; q < kb; ++q) {
+        const auto xf = frag_down<T>(sX, XP, 16 * q, 16 * pt, lr, lq);
+        [[maybe_unused]] auto xl = xf;
+        if constexpr (kBF) xl = frag_down<T>(sXL, XP, 16 * q, 16 * pt, lr, lq);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if (n % step != first || n >= nt) continue;
+          const auto mf = frag_down<T>(sM, NP, 16 * q, 16 * n, lr, lq);
+          if constexpr (kBF) acc[n] = mma32(mf, mf, xf, xl, acc[n]);
+          else acc[n] = mma16<T>(mf, xf, acc[n]);
+        }
+      }
+      // lane: channel 16 pt + lr, states 16 n + 4 lq ..
+      const int pp = p0 + 16 * pt + lr;
+      if (pp < p.P) {
+        float* const to = reinterpret_cast<float*>(back ? p.dstate : p.state) +
+                          ((static_cast<int64_t>(c) * p.H + h0 + i) * p.P + pp) * p.N;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if (n % step != first) continue;
+          const int s0 = 16 * n + 4 * lq;
+          if constexpr (kVec) {
+            if (s0 < p.N) *reinterpret_cast<v4f*>(to + s0) = acc[n];
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (s0 + e < p.N) to[s0 + e] = acc[n][e];
+          }
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// ---- the carry from chunk to chunk -----------------------------------------------
+
+struct CarryParams {
+  const int32_t* seq_chunk;
+  const float* lam;
+  uint32_t* state[2];
+  const float* from[2];
+  float* to[2];
+  int64_t nseq, elems;
+  int per_row, H, head_elems;
+};
+
+// A lane has V values of a sequence's state and goes along its chunks (blockIdx.z
+// = 1: from the end), kAhead chunks' loads in flight; in place of what a chunk adds
+// it leaves the state that enters it, for bf16 IO as two bf16 halves.
+template <bool kBF, int V>
+__global__ __launch_bounds__(kThreads) void ssd_carry_kernel(CarryParams p) {
+  constexpr int kAhead = 8;
+  struct alignas(4 * V) Pack { uint32_t e[V]; };
+  const int64_t e0 = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) * V;
+  if (e0 >= p.elems) return;
+  const int dir = blockIdx.z;
+  const int head = static_cast<int>(e0 / p.head_elems);   // V values are of one head
+  for (int64_t s = blockIdx.y; s < p.nseq; s += gridDim.y) {
+    const int lo = p.seq_chunk ? p.seq_chunk[s] : static_cast<int>(s) * p.per_row;
+    const int hi = p.seq_chunk ? p.seq_chunk[s + 1] : lo + p.per_row;
+    float h[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) h[v] = p.from[dir] ? p.from[dir][s * p.elems + e0 + v] : 0.0f;
+    uint32_t* const base = p.state[dir] + e0;
+    for (int c = 0; c < hi - lo; c += kAhead) {
+      Pack add[kAhead];
+      float lam[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (c + i >= hi - lo) break;
+        const int at = dir ? hi - 1 - c - i : lo + c + i;
+        add[i] = *reinterpret_cast<const Pack*>(base + at * p.elems);
+        lam[i] = p.lam[static_cast<int64_t>(at) * p.H + head];
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (c + i >= hi - lo) break;
+        const int at = dir ? hi - 1 - c - i : lo + c + i;
+        Pack in;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          in.e[v] = kBF ? split_bf16(h[v]) : __float_as_uint(h[v]);
+          h[v] = fmaf(lam[i], h[v], __uint_as_float(add[i].e[v]));
+        }
+        *reinterpret_cast<Pack*>(base + at * p.elems) = in;
+      }
+    }
+    if (p.to[dir]) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) p.to[dir][s * p.elems + e0 + v] = h[v];
+    }
+  }
+}
+
+// ---- outputs ------------------------------------------------------------------------
+
+// Workgroup: (chunk, heads of one group), a wavefront 16 of its tokens.  The scores
+// C_t . B_s of the chunk are computed once and stay in registers for all heads.
+// Tiles lie so that a lane has four channels of one token.
+// kDz: the gate's gradient dout y silu'(z) in place of the output.
+template <typename T, int NMAX, bool kDz, bool kVec>
+__global__ __launch_bounds__(kThreads) void ssd_outputs_kernel(ChunkParams p, ChunkOut o, int grid) {
+  using E = typename Lds<T>::E;
+  constexpr bool kBF = sizeof(T) == 2;
+  constexpr int kPad = 16 / sizeof(E), NP = NMAX + kPad, XP = kPB + kPad, NT = NMAX / 16, QB = kQ / 16;
+  constexpr int kScores = 2 * kQ * NP, kHead = kQ * XP + (kBF ? 2 : 1) * kPB * NP;
+  __shared__ __align__(16) E lds[kScores > kHead ? kScores : kHead];
+  __shared__ __align__(16) float sDl[kMostHeads][kQ];
+  __shared__ __align__(16) float sLa[kMostHeads][kQ];
+  const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lq = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int id = static_cast<int>(xcd_order(blockIdx.x, grid));
+  const int c = id / (p.G * p.blocks), g = id / p.blocks % p.G, h0 = g * p.per_group + id % p.blocks * p.hb;
+  const int heads = min(p.hb, (g + 1) * p.per_group - h0);
+  const Chunk k = chunk_of(p, c);
+  if (k.len == 0) return;
+
+  for (int i = wave; i < heads; i += kWaves) {
+    const Steps s = steps_of<T>(p, k, h0 + i, lane);
+    sDl[i][lane] = s.delta;
+    sLa[i][lane] = s.la;
+  }
+  E* const sB = lds;
+  E* const sC = lds + kQ * NP;
+  stage_rows<T, NMAX, kThreads, kVec>(sB, NP, rows_of<T>(p.B, k, g, 0, p.N), tid);
+  stage_rows<T, NMAX, kThreads, kVec>(sC, NP, rows_of<T>(p.C, k, g, 0, p.N), tid);
+  __syncthreads();
+  // scores[sb]: lane holds s = 16 sb + 4 lq + i, t = 16 wave + lr
+  const int own = 16 * wave + lr;
+  v4f scores[QB];
+  typename Frag<T>::V cf[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) cf[n] = frag_along<T>(sC, NP, 16 * wave, 16 * n, lr, lq);
+#pragma unroll
+  for (int sb = 0; sb < QB; ++sb) {
+    scores[sb] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    if (sb > wave) continue;
+    if constexpr (kBF) {
+#pragma unroll
+      for (int n = 0; n < NT; n += 2)
+        scores[sb] = mma32(frag_along<T>(sB, NP, 16 * sb, 16 * n, lr, lq), frag_along<T>(sB, NP, 16 * sb, 16 * n + 16, lr, lq),
+                           cf[n], cf[n + 1], scores[sb]);
+    } else {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) scores[sb] = mma16<T>(frag_along<T>(sB, NP, 16 * sb, 16 * n, lr, lq), cf[n], scores[sb]);
+    }
+  }
+  __syncthreads();   // the scores' operands make room for the heads'
+
+  E* const sX = lds;
+  E* const sH = lds + kQ * XP;
+  [[maybe_unused]] E* const sHL = sH + kPB * NP;
+  const int nt = (p.N + 15) / 16;
+  for (int i = 0; i < heads; ++i) {
+    const int h = h0 + i;
+    // masked and weighted scores of the head, as operands
+    typename Frag<T>::V mf[QB];
+    const float la_t = sLa[i][own];
+#pragma unroll
+    for (int sb = 0; sb < QB; ++sb) {
+      if (sb > wave) {
+        mf[sb] = tofrag<T>(0.0f, 0.0f, 0.0f, 0.0f);
+        continue;
+      }
+      const v4f la_s = *reinterpret_cast<const v4f*>(&sLa[i][16 * sb + 4 * lq]);
+      const v4f dl_s = *reinterpret_cast<const v4f*>(&sDl[i][16 * sb + 4 * lq]);
+      float m[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        m[e] = 16 * sb + 4 * lq + e <= own ? scores[sb][e] * __builtin_amdgcn_exp2f(la_t - la_s[e]) * dl_s[e] : 0.0f;
+      mf[sb] = tofrag<T>(m[0], m[1], m[2], m[3]);
+    }
+    const float ea = __builtin_amdgcn_exp2f(la_t), Dh = p.D ? p.D[h] : 0.0f;
+    for (int p0 = 0; p0 < p.P; p0 += kPB) {
+      const int cols = p.P - p0;
+      stage_rows<T, kPB, kThreads, kVec>(sX, XP, rows_of<T>(p.x, k, h, p0, p.P), tid);
+      // S_in: kPB rows of N states
+      const StateRows from = state_rows(p.state, ((static_cast<int64_t>(c) * p.H + h) * p.P + p0) * p.N, min(kPB, cols), p.N);
+      constexpr int kPer = NMAX / 4, kN = kPB * kPer / kThreads;
+#pragma unroll
+      for (int j = 0; j < kN; ++j) {
+        const int r = tid / kPer + j * (kThreads / kPer), n = tid % kPer * 4;
+        const v4u v = load_states<kVec>(from, r, n);
+        if constexpr (kBF) {
+          *reinterpret_cast<v2u*>(sH + r * NP + n) = v2u{highs(v[0], v[1]), highs(v[2], v[3])};
+          *reinterpret_cast<v2u*>(sHL + r * NP + n) = v2u{lows(v[0], v[1]), lows(v[2], v[3])};
+        } else {
+          *reinterpret_cast<v4u*>(sH + r * NP + n) = v;
+        }
+      }
+      __syncthreads();
+      const bool live = own < k.len;
+      const int pts = (min(kPB, cols) + 15) / 16;
+#pragma unroll
+      for (int pt = 0; pt < kPB / 16; ++pt) {
+        if (pt >= pts) continue;
+        v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if (n >= nt) continue;
+          const auto hf = frag_along<T>(sH, NP, 16 * pt, 16 * n, lr, lq);
+          if constexpr (kBF) acc = mma32(hf, frag_along<T>(sHL, NP, 16 * pt, 16 * n, lr, lq), cf[n], cf[n], acc);
+          else acc = mma16<T>(hf, cf[n], acc);
+        }
+        acc *= ea;
+        if constexpr (kBF) {
+#pragma unroll
+          for (int sb = 0; sb < QB; sb += 2)
+            if (sb <= wave)
+              acc = mma32(frag_down<T>(sX, XP, 16 * sb, 16 * pt, lr, lq), frag_down<T>(sX, XP, 16 * sb + 16, 16 * pt, lr, lq), mf[sb],
+                          mf[sb + 1], acc);
+        } else {
+#pragma unroll
+          for (int sb = 0; sb < QB; ++sb)
+            if (sb <= wave) acc = mma16<T>(frag_down<T>(sX, XP, 16 * sb, 16 * pt, lr, lq), mf[sb], acc);
+        }
+        // token own, channels 16 pt + 4 lq ..
+        const int c0 = 16 * pt + 4 * lq;
+        if (!live || c0 >= cols) continue;
+        const T* const z = p.z.p ? static_cast<const T*>(p.z.p) + k.b * p.z.sb + (k.t0 + own) * p.z.ss + h * p.z.sh + p0 + c0 : nullptr;
+        const T* const e = kDz ? static_cast<const T*>(p.dout.p) + k.b * p.dout.sb + (k.t0 + own) * p.dout.ss + h * p.dout.sh + p0 + c0
+                               : nullptr;
+        T* const to = static_cast<T*>(kDz ? o.dz : o.out) + k.b * o.sb + (k.t0 + own) * o.ss + h * o.sh + p0 + c0;
+        const int left = cols - c0;
+        float y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          y[j] = fmaf(Dh, Lds<T>::f(sX[own * XP + c0 + j]), acc[j]);
+          if (z && j < left) {
+            const float zv = io<T>::load(z + j);
+            if constexpr (kDz) {
+              const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-zv * kLog2e));
+              y[j] *= io<T>::load(e + j) * (s * fmaf(zv, 1.0f - s, 1.0f));
+            } else {
+              y[j] *= silu_f32(zv);
+            }
+          }
+        }
+        if constexpr (kVec) {
+          if constexpr (kBF) *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+          else *reinterpret_cast<float4*>(to) = make_float4(y[0], y[1], y[2], y[3]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (j < left) io<T>::store(to + j, y[j]);
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
+
+template <typename T, int NMAX>
+void launch_states(const ChunkParams& p, bool backward, hipStream_t stream) {
+  const int grid = p.nc * p.G * p.blocks;
+  if (p.vec) ssd_states_kernel<T, NMAX, true><<<dim3(grid, backward ? 2 : 1), kThreads, 0, stream>>>(p, grid);
+  else ssd_states_kernel<T, NMAX, false><<<dim3(grid, backward ? 2 : 1), kThreads, 0, stream>>>(p, grid);
+}
+
+template <typename T, int NMAX>
+void launch_outputs(const ChunkParams& p, const ChunkOut& o, hipStream_t stream) {
+  const int grid = p.nc * p.G * p.blocks;
+  auto go = [&](auto dz, auto vec) {
+    ssd_outputs_kernel<T, NMAX, dz.value, vec.value><<<grid, kThreads, 0, stream>>>(p, o, grid);
+  };
+  if (o.dz && p.vec) go(std::true_type{}, std::true_type{});
+  else if (o.dz) go(std::true_type{}, std::false_type{});
+  else if (p.vec) go(std::false_type{}, std::true_type{});
+  else go(std::false_type{}, std::false_type{});
+}
+
+}  // namespace
+
+// Heads of a workgroup: as many as share the chunk's B and C (up to 8) while
+// three workgroups a compute unit remain.
+ChunkPlan chunk_plan(int64_t batch, int64_t L, int64_t nseq, bool packed, int64_t H, int64_t G) {
+  ChunkPlan q;
+  q.per_row = (L + kQ - 1) / kQ;
+  q.nc = packed ? (L ? L / kQ + std::min(nseq, L) : 0) : batch * q.per_row;
+  const int64_t per_group = H / G;
+  q.hb = std::min<int64_t>(kMostHeads, per_group);
+  while (q.hb > 1 && q.nc * G * ((per_group + q.hb - 1) / q.hb) < 768) q.hb = (q.hb + 1) / 2;
+  q.blocks = (per_group + q.hb - 1) / q.hb;
+  return q;
+}
+
+hipError_t launch_chunk_table(const int32_t* cu, int64_t L, int64_t nseq, int64_t nc, ChunkEntry* table, int32_t* seq_chunk,
+                              const OutsideRows& rows, hipStream_t stream) {
+  chunk_table_kernel<<<rows.n ? 64 : 1, kTableThreads, 0, stream>>>(cu, L, nseq, static_cast<int>(nc), table, seq_chunk, rows);
+  return hipGetLastError();
+}
+
+hipError_t launch_chunk_states(const ChunkParams& p, bool bf16, bool backward, int64_t nseq, const float* h0, float* last,
+                               const float* dlast, float* dh0, hipStream_t stream) {
+  if (p.nc > 0) {
+    if (!bf16) launch_states<float, 64>(p, backward, stream);
+    else if (p.N > 64) launch_states<uint16_t, 128>(p, backward, stream);
+    else launch_states<uint16_t, 64>(p, backward, stream);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (nseq == 0) return hipSuccess;
+  CarryParams q{p.seq_chunk, p.lam, {p.state, p.dstate}, {h0, dlast}, {last, dh0}, nseq,
+                static_cast<int64_t>(p.H) * p.P * p.N, p.per_row, p.H, p.P * p.N};
+  const bool four = p.P * p.N % 4 == 0;
+  const int64_t lanes = four ? q.elems / 4 : q.elems;
+  const dim3 grid(static_cast<unsigned>((lanes + kThreads - 1) / kThreads), static_cast<unsigned>(std::min<int64_t>(nseq, 4096)),
+                  backward ? 2 : 1);
+  if (bf16) {
+    if (four) ssd_carry_kernel<true, 4><<<grid, kThreads, 0, stream>>>(q);
+    else ssd_carry_kernel<true, 1><<<grid, kThreads, 0, stream>>>(q);
+  } else {
+    if (four) ssd_carry_kernel<false, 4><<<grid, kThreads, 0, stream>>>(q);
+    else ssd_carry_kernel<false, 1><<<grid, kThreads, 0, stream>>>(q);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_chunk_outputs(const ChunkParams& p, const ChunkOut& o, bool bf16, hipStream_t stream) {
+  if (p.nc == 0) return hipSuccess;
+  if (!bf16) launch_outputs<float, 64>(p, o, stream);
+  else if (p.N > 64) launch_outputs<uint16_t, 128>(p, o, stream);
+  else launch_outputs<uint16_t, 64>(p, o, stream);
+  return hipGetLastError();
+}
+
+}  // namespace ssm

@@ -1,6 +1,6 @@
 // ssm_abi_mamba2.hip -- the extern "C" surface of the token convolution and of
-// the Mamba-2 SSM's step: host-side validation (pure host code, no HIP call)
-// and dispatch.
+// the Mamba-2 SSM's packed prefill, gradients and step: host-side validation
+// (pure host code, no HIP call) and dispatch.
 #include <stdint.h>
 
 #include "abi_checks.h"
@@ -62,6 +62,53 @@ int check_apart(const Rows (&inputs)[NI], const Rows (&outputs)[NO]) {
 
 Rows flat(const void* p, int64_t n, int64_t esz) { return Rows{span1(p, n, esz)}; }
 
+// ---- the SSD scans -------------------------------------------------------------------
+
+// A (batch, token, head or group, inner) tensor.
+struct Heads {
+  const void* p;
+  int64_t sb, ss, sh, heads, inner;
+};
+Rows rows_of(const Heads& t, int64_t batch, int64_t L, int64_t esz) {
+  return Rows{span4(t.p, batch, t.sb, L, t.ss, t.heads, t.sh, t.inner, esz)};
+}
+int check_heads(const Heads& t, int64_t batch, int64_t esz) {
+  if (!t.p) return SSM_ERR_NULL;
+  if ((batch > 1 && t.sb < 0) || t.ss < 0 || (t.heads > 1 && t.sh < 0)) return SSM_ERR_STRIDE;
+  if (misaligned(t.p, esz)) return SSM_ERR_ALIGN;
+  // a chunk of 64 tokens is reached through a 31-bit byte window
+  return t.ss >= (int64_t{1} << 31) || (63 * t.ss + t.inner) * esz >= (int64_t{1} << 31) ? SSM_ERR_UNSUPPORTED : SSM_OK;
+}
+
+// Sizes of the packed scan and of the gradients, and the limits on them.
+int check_ssd(int64_t batch, int64_t L, int64_t H, int64_t P, int64_t ngroups, int64_t N, int64_t nseq, bool packed,
+              int32_t dtype) {
+  if (batch < 0 || L < 0 || nseq < 0 || H < 1 || P < 1 || N < 1 || bad_groups(ngroups, H) || (packed && batch != 1))
+    return SSM_ERR_SHAPE;
+  if (bad_dtype(dtype)) return SSM_ERR_DTYPE;
+  const int64_t most = (int64_t{1} << 31) - 1, chunks = (int64_t{1} << 24) - 1;
+  if (N > (dtype == SSM_BF16 ? 128 : 64) || L > kMaxSeqlen || H > most / P || H * P > most / N) return SSM_ERR_UNSUPPORTED;
+  if (packed && nseq >= kMaxPacked) return SSM_ERR_UNSUPPORTED;
+  const int64_t of_row = packed ? L / 64 + min(nseq, L) : (L + 63) / 64;
+  if (H > chunks || batch > most || (of_row > 0 && (of_row > chunks / H || batch > chunks / H / of_row)))
+    return SSM_ERR_UNSUPPORTED;
+  return SSM_OK;
+}
+int check_ssd(const ssm_ssd_packed_args* a) {
+  return check_ssd(1, a->seqlen, a->nheads, a->headdim, a->ngroups, a->dstate, a->nseq, true, a->io_dtype);
+}
+int check_ssd(const ssm_ssd_bwd_args* a) {
+  return check_ssd(a->batch, a->seqlen, a->nheads, a->headdim, a->ngroups, a->dstate, a->nseq, a->cu_seqlens != nullptr,
+                   a->io_dtype);
+}
+// The size functions read sizes alone; those of fp32 pass the limits of bf16.
+template <typename Args>
+bool sizes_pass(const Args* a) {
+  Args s = *a;
+  s.io_dtype = SSM_BF16;
+  return check_ssd(&s) == SSM_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -77,6 +124,112 @@ size_t ssm_token_conv_bwd_workspace_size(const ssm_token_conv_bwd_args* a) {
   if (bad_dtype(s.io_dtype)) s.io_dtype = SSM_F32;
   if (check_conv(&s) != SSM_OK || s.dim == 0) return 0;
   return token_conv_bwd_workspace_bytes(s);
+}
+
+size_t ssm_ssd_packed_args_size(void) { return sizeof(ssm_ssd_packed_args); }
+size_t ssm_ssd_bwd_args_size(void) { return sizeof(ssm_ssd_bwd_args); }
+
+size_t ssm_ssd_packed_workspace_size(const ssm_ssd_packed_args* a) {
+  return a && sizes_pass(a) ? ssd_packed_workspace_bytes(*a) : 0;
+}
+size_t ssm_ssd_bwd_workspace_size(const ssm_ssd_bwd_args* a) {
+  return a && sizes_pass(a) ? ssd_bwd_workspace_bytes(*a) : 0;
+}
+
+int ssm_validate_ssd_packed(const ssm_ssd_packed_args* a) {
+  if (!a) return SSM_ERR_NULL;
+  if (const int st = check_ssd(a)) return st;
+  const int64_t L = a->seqlen, H = a->nheads, P = a->headdim, N = a->dstate, G = groups_of(a->ngroups), S = a->nseq;
+  const int64_t esz = io_size(a->io_dtype);
+  if (!a->cu_seqlens || !a->A) return SSM_ERR_NULL;
+  const Heads x{a->x, 0, a->x_seq_stride, a->x_head_stride, H, P}, z{a->z, 0, a->z_seq_stride, a->z_head_stride, H, P},
+      B{a->B, 0, a->B_seq_stride, a->B_group_stride, G, N}, C{a->C, 0, a->C_seq_stride, a->C_group_stride, G, N},
+      out{a->out, 0, a->out_seq_stride, a->out_head_stride, H, P};
+  if (L > 0) {
+    for (const Heads& t : {x, B, C, out})
+      if (const int st = check_heads(t, 1, esz)) return st;
+    if (a->z)
+      if (const int st = check_heads(z, 1, esz)) return st;
+    if (!a->dt) return SSM_ERR_NULL;
+    if (a->dt_seq_stride < 0) return SSM_ERR_STRIDE;
+    if (misaligned(a->dt, esz)) return SSM_ERR_ALIGN;
+    // rows of out in either order of tokens and heads
+    if (rows_collide(L, out.ss, H, out.sh, P) && rows_collide(H, out.sh, L, out.ss, P)) return SSM_ERR_ALIAS;
+  }
+  if (misaligned(a->A, 4) || misaligned(a->D, 4) || misaligned(a->dt_bias, 4) || misaligned(a->cu_seqlens, 4) ||
+      misaligned(a->h0, 4) || misaligned(a->last_state, 4) || misaligned(a->workspace, 16))
+    return SSM_ERR_ALIGN;
+  const size_t need = ssd_packed_workspace_bytes(*a);
+  if (need && (!a->workspace || a->workspace_bytes < need)) return SSM_ERR_SCRATCH;
+  const int64_t states = S * H * P * N;
+  const Rows inputs[] = {rows_of(x, 1, L, esz), rows3(a->dt, 1, 0, L, a->dt_seq_stride, H, esz), rows_of(z, 1, L, esz),
+                         rows_of(B, 1, L, esz), rows_of(C, 1, L, esz), flat(a->A, H, 4), flat(a->D, H, 4),
+                         flat(a->dt_bias, H, 4), flat(a->cu_seqlens, S + 1, 4), flat(a->h0, states, 4)};
+  const Rows outputs[] = {rows_of(out, 1, L, esz), flat(a->last_state, states, 4),
+                          flat(a->workspace, static_cast<int64_t>(a->workspace_bytes), 1)};
+  for (const Rows& o : outputs) {
+    for (const Rows& i : inputs) {
+      // last_state may be exactly h0 (the state carried in place)
+      if (&o == &outputs[1] && &i == &inputs[9] && a->last_state == a->h0) continue;
+      if (overlap(o, i)) return SSM_ERR_ALIAS;
+    }
+    for (const Rows& o2 : outputs)
+      if (&o2 != &o && overlap(o, o2)) return SSM_ERR_ALIAS;
+  }
+  return SSM_OK;
+}
+
+int ssm_validate_ssd_bwd(const ssm_ssd_bwd_args* a) {
+  if (!a) return SSM_ERR_NULL;
+  if (const int st = check_ssd(a)) return st;
+  const int64_t Bt = a->batch, L = a->seqlen, H = a->nheads, P = a->headdim, N = a->dstate, G = groups_of(a->ngroups);
+  const int64_t S = a->cu_seqlens ? a->nseq : Bt, esz = io_size(a->io_dtype);
+  if (!a->A || !a->dA) return SSM_ERR_NULL;   // dA is set (to zero) without any token too
+  const Heads x{a->x, a->x_batch_stride, a->x_seq_stride, a->x_head_stride, H, P},
+      z{a->z, a->z_batch_stride, a->z_seq_stride, a->z_head_stride, H, P},
+      B{a->B, a->B_batch_stride, a->B_seq_stride, a->B_group_stride, G, N},
+      C{a->C, a->C_batch_stride, a->C_seq_stride, a->C_group_stride, G, N},
+      dout{a->dout, a->dout_batch_stride, a->dout_seq_stride, a->dout_head_stride, H, P};
+  const int64_t T = Bt * L;
+  if (T > 0) {
+    for (const Heads& t : {x, B, C, dout})
+      if (const int st = check_heads(t, Bt, esz)) return st;
+    if (a->z) {
+      if (const int st = check_heads(z, Bt, esz)) return st;
+      if (!a->dz) return SSM_ERR_NULL;
+    }
+    if (!a->dt || !a->dx || !a->ddt || !a->dB || !a->dC) return SSM_ERR_NULL;
+    if (a->dt_seq_stride < 0 || (Bt > 1 && a->dt_batch_stride < 0)) return SSM_ERR_STRIDE;
+    for (const void* p : {a->dt, static_cast<const void*>(a->dx), static_cast<const void*>(a->ddt),
+                          static_cast<const void*>(a->dz), static_cast<const void*>(a->dB), static_cast<const void*>(a->dC)})
+      if (misaligned(p, esz)) return SSM_ERR_ALIGN;
+  }
+  if (misaligned(a->A, 4) || misaligned(a->D, 4) || misaligned(a->dt_bias, 4) || misaligned(a->cu_seqlens, 4) ||
+      misaligned(a->h0, 4) || misaligned(a->dlast, 4) || misaligned(a->dA, 4) || misaligned(a->dD, 4) ||
+      misaligned(a->ddt_bias, 4) || misaligned(a->dh0, 4) || misaligned(a->workspace, 16))
+    return SSM_ERR_ALIGN;
+  const size_t need = ssd_bwd_workspace_bytes(*a);
+  if (need && (!a->workspace || a->workspace_bytes < need)) return SSM_ERR_SCRATCH;
+  const int64_t states = S * H * P * N;
+  const Rows inputs[] = {rows_of(x, Bt, L, esz), rows3(a->dt, Bt, a->dt_batch_stride, L, a->dt_seq_stride, H, esz),
+                         rows_of(z, Bt, L, esz), rows_of(B, Bt, L, esz), rows_of(C, Bt, L, esz), rows_of(dout, Bt, L, esz),
+                         flat(a->A, H, 4), flat(a->D, H, 4), flat(a->dt_bias, H, 4),
+                         flat(a->cu_seqlens, S + 1, 4), flat(a->h0, states, 4), flat(a->dlast, states, 4)};
+  const Rows outputs[] = {flat(a->dx, T * H * P, esz), flat(a->ddt, T * H, esz), flat(a->z ? a->dz : nullptr, T * H * P, esz),
+                          flat(a->dB, T * G * N, esz), flat(a->dC, T * G * N, esz), flat(a->dA, H, 4), flat(a->dD, H, 4),
+                          flat(a->ddt_bias, H, 4), flat(a->dh0, states, 4),
+                          flat(a->workspace, static_cast<int64_t>(a->workspace_bytes), 1)};
+  return check_apart(inputs, outputs);
+}
+
+int ssm_ssd_packed_fwd(const ssm_ssd_packed_args* a, void* stream) {
+  if (const int st = ssm_validate_ssd_packed(a)) return st;
+  return launch_ssd_packed_fwd(*a, static_cast<hipStream_t>(stream)) == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+}
+
+int ssm_ssd_scan_bwd(const ssm_ssd_bwd_args* a, void* stream) {
+  if (const int st = ssm_validate_ssd_bwd(a)) return st;
+  return launch_ssd_bwd(*a, static_cast<hipStream_t>(stream)) == hipSuccess ? SSM_OK : SSM_ERR_HIP;
 }
 
 int ssm_validate_token_conv(const ssm_token_conv_args* a) {

@@ -34,6 +34,10 @@ hipError_t launch_token_conv_fwd(const ssm_token_conv_args& a, hipStream_t strea
 hipError_t launch_token_conv_bwd(const ssm_token_conv_bwd_args& a, hipStream_t stream);
 size_t token_conv_bwd_workspace_bytes(const ssm_token_conv_bwd_args& a);
 hipError_t launch_token_conv_update(const ssm_token_conv_update_args& a, hipStream_t stream);
+hipError_t launch_ssd_packed_fwd(const ssm_ssd_packed_args& a, hipStream_t stream);
+size_t ssd_packed_workspace_bytes(const ssm_ssd_packed_args& a);
+hipError_t launch_ssd_bwd(const ssm_ssd_bwd_args& a, hipStream_t stream);
+size_t ssd_bwd_workspace_bytes(const ssm_ssd_bwd_args& a);
 hipError_t launch_ssd_step(const ssm_ssd_update_args& a, hipStream_t stream);
 
 // ---------------------------------------------------------------------------

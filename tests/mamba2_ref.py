@@ -156,3 +156,123 @@ def ssd_step(state, x, dt, A, B, C, D=None, z=None, bias=None, softplus_on=True,
             y = y * g
         out[r], bnd[r] = y, ey
     return out, bnd, state, es
+
+
+CHUNK = 64   # tokens of the kernels' chunks, from each sequence's first on
+
+
+def ssd_scan(x, dt, A, B, C, D=None, z=None, bias=None, softplus_on=True, h0=None, cu=None, dout=None, dlast=None, io="f32"):
+    """({name: value}, {name: bound}) of the Mamba-2 SSM over whole sequences and,
+    with dout, of its gradients, token by token.  Arrays are (batch, L, H, P) and
+    so on, or without the batch axis with cu.
+
+    The bounds are multiples of the same sums taken over magnitudes (names that
+    end in m).  With a the sums of A Delta in a chunk, at most a_max in size: a
+    decay e^(a_t - a_s) is off by (20 a_max + 6) U (a prefix sum of 64 steps in six
+    levels, its product with A log2 e, the difference, exp2); products of N, P
+    and 64 terms, and a carry over the chunks with two roundings each, add
+    (N + P + 64 + 4 chunks + 60) U: together e.  For bf16 IO an operand in two
+    halves is off by 2^-16 of its size, two of them in a row by 2^-15; a rounded
+    operand by 2^-8: the weighted scores (out, dx, dB, dC), the state in dx, and a
+    gated dout in dx, dB and dC.  The flow through a step's decay is a difference
+    of prefix sums over its chunk: 20 U of all that they sum."""
+    packed = cu is not None
+    lift = lambda t: None if t is None else (np.asarray(t, np.float64)[None] if packed else np.asarray(t, np.float64))  # noqa: E731
+    x, dt, B, C, z, dout = (lift(t) for t in (x, dt, B, C, z, dout))
+    A = np.asarray(A, np.float64)
+    seqs = bounds_of(x.shape, cu)
+    n, (H, P), (G, N) = len(seqs), x.shape[2:], B.shape[2:]
+    each = H // G
+    zero = lambda *s: np.zeros(s)  # noqa: E731
+    names = dict(out=x.shape, last=(n, H, P, N))
+    if dout is not None:
+        names.update(dx=x.shape, ddt=dt.shape, dB=B.shape, dC=C.shape, dA=(H,), ddt_bias=(H,), dD=(H,), dh0=(n, H, P, N), dz=x.shape)
+    val, bnd = ({k: zero(*s) for k, s in names.items()} for _ in range(2))
+    half = 2.0 ** -8 if io == "bf16" else 0.0
+    split = 2.0 ** -15 if io == "bf16" else 0.0
+    Dh = np.zeros(H) if D is None else np.asarray(D, np.float64)
+    col = lambda t: t[:, None]  # noqa: E731
+    tokens = x.shape[0] * x.shape[1]
+    for r, lo, hi, k in seqs:
+        L = hi - lo
+        h = zero(H, P, N) if h0 is None else np.asarray(h0, np.float64)[k]
+        hm = np.abs(h)
+        delta, alpha, ed, _ = step_parts(dt[r, lo:hi], bias, A, softplus_on)
+        amax = max((np.abs(A * delta[c:c + CHUNK].sum(0)).max() for c in range(0, L, CHUNK)), default=0)
+        e = (20 * amax + 6 + N + P + 64 + 4 * (L // CHUNK + 1) + 60) * U + (ed.max() if L else 0)
+        Br, Cr = (np.repeat(t[r, lo:hi], each, 1)[:, :, None] for t in (B, C))      # (L, H, 1, N)
+        xr = x[r, lo:hi][..., None]                                                # (L, H, P, 1)
+        hs, hms, y, ym = [h], [hm], zero(L, H, P), zero(L, H, P)
+        for t in range(L):
+            add = delta[t][:, None, None] * xr[t] * Br[t]
+            h = alpha[t][:, None, None] * h + add
+            hm = alpha[t][:, None, None] * hm + np.abs(add)
+            hs.append(h)
+            hms.append(hm)
+            y[t], ym[t] = (h * Cr[t]).sum(-1), (hm * np.abs(Cr[t])).sum(-1)
+        val["last"][k], bnd["last"][k] = h, (e + split) * hm
+        full = y + col(Dh) * x[r, lo:hi]
+        efull = (e + split + half) * ym + 3 * U * (np.abs(col(Dh) * x[r, lo:hi]) + ym)
+        s = None if z is None else sigmoid(z[r, lo:hi])
+        gate = 1.0 if z is None else z[r, lo:hi] * s
+        eg = 0.0 if z is None else (2 * np.abs(z[r, lo:hi]) + 9) * U
+        val["out"][r, lo:hi] = full * gate
+        bnd["out"][r, lo:hi] = efull * np.abs(gate) + np.abs(full * gate) * eg
+        if dout is None:
+            continue
+        d = dout[r, lo:hi]
+        if z is not None:
+            f = s * (1 + z[r, lo:hi] * (1 - s))
+            ef = (2 * np.abs(z[r, lo:hi]) + 11) * (1 + np.abs(z[r, lo:hi])) * U * s
+            val["dz"][r, lo:hi] = d * full * f
+            bnd["dz"][r, lo:hi] = np.abs(d) * (efull * np.abs(f) + np.abs(full) * ef) + 2 * U * np.abs(d * full * f)
+        gated = half if z is not None else 0.0
+        es = e + (np.max(eg) if np.size(eg) else 0) + (2 * split if z is not None else split)   # of sums that carry 16 bits
+        dy = d * gate
+        dh = zero(H, P, N) if dlast is None else np.asarray(dlast, np.float64)[k]
+        dhm = np.abs(dh)
+        flow, flowm, tox, toxm, terms = (zero(L, H) for _ in range(5))
+        ends = {}
+        for t in range(L - 1, -1, -1):
+            if t == L - 1 or (t + 1) % CHUNK == 0:
+                ends[t // CHUNK] = (dhm * hms[t + 1]).sum((-1, -2))
+            m = np.abs(dy[t])
+            dC = (dy[t][..., None] * hs[t + 1]).sum(1)
+            dCm = (m[..., None] * hms[t + 1]).sum(1)
+            dh = dh + dy[t][..., None] * Cr[t]
+            dhm = dhm + m[..., None] * np.abs(Cr[t])
+            to_x, to_xm = (dh * Br[t]).sum(-1), (dhm * np.abs(Br[t])).sum(-1)
+            dB = col(delta[t]) * (dh * xr[t]).sum(1)
+            dBm = col(delta[t]) * (dhm * np.abs(xr[t])).sum(1)
+            flow[t] = (dh * hs[t]).sum((-1, -2)) * alpha[t]
+            flowm[t] = (dhm * hms[t]).sum((-1, -2)) * alpha[t]
+            tox[t], toxm[t] = (to_x * x[r, lo + t]).sum(-1), (to_xm * np.abs(x[r, lo + t])).sum(-1)
+            terms[t] = delta[t] * toxm[t] + (m * ym[t]).sum(-1)
+            val["dx"][r, lo + t] = col(delta[t]) * to_x + col(Dh) * dy[t]
+            bnd["dx"][r, lo + t] = (es + 2 * half + gated) * col(delta[t]) * to_xm + (gated + es) * np.abs(col(Dh) * dy[t])
+            for which, v, vm in (("dB", dB, dBm), ("dC", dC, dCm)):
+                val[which][r, lo + t] = v.reshape(G, each, N).sum(1)
+                bnd[which][r, lo + t] = ((es + half + gated + each * U) * vm).reshape(G, each, N).sum(1)
+            dh, dhm = alpha[t][:, None, None] * dh, alpha[t][:, None, None] * dhm
+        total = np.stack([terms[c:c + CHUNK].sum(0) + ends[c // CHUNK] for c in range(0, L, CHUNK)]) if L else zero(0, H)
+        eflow = es * flowm + 20 * U * np.repeat(total, CHUNK, 0)[:L]
+        slope = sigmoid(dt[r, lo:hi] + (0 if bias is None else bias)) if softplus_on else np.ones((L, H))
+        dd = tox + A * flow
+        edd = es * toxm + np.abs(A) * eflow + 3 * U * (toxm + np.abs(A) * flowm)
+        val["ddt"][r, lo:hi] = dd * slope
+        pre = np.abs(dt[r, lo:hi] + (0 if bias is None else bias))
+        pre = np.where(slope > 0, pre, 0)   # no step at all: nothing to be off
+        bnd["ddt"][r, lo:hi] = edd * slope + np.abs(dd) * slope * (2 * pre + 8) * U
+        val["dh0"][k], bnd["dh0"][k] = dh, es * dhm
+        val["dA"] += (delta * flow).sum(0)
+        bnd["dA"] += (delta * (eflow + (ed + U * (tokens / 64 + 70)) * flowm)).sum(0)
+        val["ddt_bias"] += (dd * slope).sum(0)
+        bnd["ddt_bias"] += (bnd["ddt"][r, lo:hi] + U * (tokens / 64 + 70) * np.abs(dd * slope)).sum(0)
+        val["dD"] += (dy * x[r, lo:hi]).sum((0, 2))
+        bnd["dD"] += ((es + U * (P + tokens / 64 + 70)) * np.abs(dy * x[r, lo:hi])).sum((0, 2))
+    if packed:
+        for q in (val, bnd):
+            for key in ("out", "dx", "ddt", "dB", "dC", "dz"):
+                if key in q:
+                    q[key] = q[key][0]
+    return val, bnd

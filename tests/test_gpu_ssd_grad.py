@@ -1,0 +1,328 @@
+"""The packed prefill and the gradients of the Mamba-2 SSM on the GPU against
+their 64-bit form, within the error bounds that form computes (mamba2_ref) plus
+the rounding of the IO type."""
+import numpy as np
+import pytest
+
+import mamba2_ref as ref
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # collected on CPU machines only to be skipped
+    pytest.skip("no GPU", allow_module_level=True)
+
+import selective_state_space_74_amd as ssm  # noqa: E402
+
+DEV = "cuda"
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+IO_TYPED = ("out", "dx", "ddt", "dB", "dC", "dz")
+
+
+def f64(t):
+    return None if t is None else t.detach().to(torch.float64).cpu().numpy()
+
+
+def make(lead, H, P, G, N, io="f32", n=None, seed=0, gate=True, h0=True, full=True, pad=0, decay=16.0):
+    """Inputs on the device: x, B and C the parts of one tensor (rows longer by
+    pad), steps of 0.001 to 0.1 and decay rates of 1 to `decay`."""
+    g = torch.Generator().manual_seed(seed)
+    dt = TYPES[io]
+    r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    u = lambda *s: torch.rand(*s, generator=g)  # noqa: E731
+    n = lead[0] if n is None else n
+    xbc = r(*lead, H * P + 2 * G * N + pad).to(dt).to(DEV)
+    t = dict(x=xbc[..., :H * P].unflatten(-1, (H, P)), B=xbc[..., H * P:H * P + G * N].unflatten(-1, (G, N)),
+             C=xbc[..., H * P + G * N:H * P + 2 * G * N].unflatten(-1, (G, N)))
+    step = torch.exp(np.log(1e-3) + u(H) * np.log(1e2))
+    t.update(dt=(0.1 * r(*lead, H)).to(dt).to(DEV), A=-torch.exp(np.log(decay) * u(H)).to(DEV),
+             D=r(H).to(DEV) if full else None, z=r(*lead, H, P).to(dt).to(DEV) if gate else None,
+             dt_bias=(step + torch.log(-torch.expm1(-step))).to(DEV) if full else None,
+             h0=r(n, H, P, N).to(DEV) if h0 else None, dout=r(*lead, H, P).to(dt).to(DEV), dlast=r(n, H, P, N).to(DEV))
+    return t
+
+
+def call(t, fn, *first, softplus=True, cu=None, **kw):
+    return fn(*first, t["x"], t["dt"], t["A"], t["B"], t["C"], D=t["D"], z=t["z"], dt_bias=t["dt_bias"], dt_softplus=softplus,
+              h0=t["h0"], cu_seqlens=cu, **kw)
+
+
+def expected(t, io, cu=None, softplus=True, dlast=True):
+    return ref.ssd_scan(*(f64(t[k]) for k in ("x", "dt", "A", "B", "C", "D", "z", "dt_bias")), softplus_on=softplus, h0=f64(t["h0"]),
+                        cu=None if cu is None else cu.tolist(), dout=f64(t["dout"]), dlast=f64(t["dlast"]) if dlast else None, io=io)
+
+
+# the framework's parity bars, here of the error's norm against the result's: a
+# worst-case bound of a long sum is wide, and a term that is wrong shows here
+BARS = {"f32": 1e-4, "bf16": 2e-2}
+
+
+def check(got, val, bnd, io, what, weak=()):
+    """weak: results that are next to nothing against what they are sums of."""
+    for k, g in got.items():
+        half = ref.HALF_STEP[io] if k in IO_TYPED else ref.U
+        y = f64(g)
+        room = bnd[k] + half * (np.abs(val[k]) + bnd[k]) + ref.TINY
+        assert np.all(np.isfinite(y)), (what, k)
+        off = np.abs(y - val[k])
+        worst = np.max(off / room, initial=0)
+        size = np.sqrt(np.mean(val[k] ** 2)) if val[k].size else 0
+        print(f"[{what}] {k}: {worst:.3f} of the bound, rms {np.sqrt(np.mean(off ** 2)) / size if size else 0:.2e} of its size", flush=True)
+        assert worst <= 1, (what, k)
+        if k not in weak:
+            assert np.linalg.norm(off) <= BARS[io if k in IO_TYPED else "f32"] * np.linalg.norm(val[k]), (what, k)
+
+
+def run_and_check(t, io, what, cu=None, softplus=True, dlast=True, weak=()):
+    val, bnd = expected(t, io, cu, softplus, dlast)
+    if cu is not None:
+        out, last = call(t, ssm.ssd_scan_fwd, softplus=softplus, cu=cu, return_last_state=True)
+        check(dict(out=out, last=last), val, bnd, io, what, weak)
+    g = call(t, ssm.ssd_scan_bwd, t["dout"], softplus=softplus, cu=cu, dlast=t["dlast"] if dlast else None)
+    want = {"dx", "ddt", "dB", "dC", "dA"} | {d for k, d in (("z", "dz"), ("D", "dD"), ("dt_bias", "ddt_bias"), ("h0", "dh0"))
+                                              if t[k] is not None}
+    assert set(g) == want
+    check(g, val, bnd, io, what, weak)
+    return g
+
+
+SHAPES = [(1, 1, 1, 1, 1, 1), (2, 3, 2, 5, 1, 7), (1, 63, 4, 16, 2, 16), (2, 64, 3, 64, 1, 64), (1, 65, 2, 33, 2, 20), (3, 130, 4, 20, 2, 33),
+          (1, 300, 9, 64, 1, 64), (2, 129, 2, 65, 1, 64), (1, 70, 2, 128, 1, 16), (1, 80, 1, 130, 1, 8), (40, 2, 2, 8, 1, 4),
+          (1, 200, 20, 8, 4, 24), (2, 100, 24, 32, 1, 32)]
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
+def test_batched(shape, io):
+    b, L, H, P, G, N = shape
+    t = make((b, L), H, P, G, N, io, seed=sum(shape), gate=H % 2 == 0, h0=L % 2 == 1, full=P != 33)
+    run_and_check(t, io, f"{shape} {io}", dlast=b % 2 == 1)
+
+
+@pytest.mark.parametrize("shape", [(1, 65, 2, 64, 1, 128), (2, 100, 3, 20, 1, 100), (1, 70, 4, 33, 2, 65), (1, 66, 2, 128, 2, 128),
+                                   (1, 80, 10, 64, 1, 128)], ids=lambda s: "x".join(map(str, s)))
+def test_many_states(shape):
+    b, L, H, P, G, N = shape
+    for gate in (False, True):
+        t = make((b, L), H, P, G, N, "bf16", seed=sum(shape), gate=gate, h0=True)
+        run_and_check(t, "bf16", f"{shape} gate {gate}")
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("offset", [1, 8])
+def test_rows_off_their_alignment(offset, io):
+    t = make((2, 70), 4, 16, 2, 16, io, seed=offset, pad=offset)
+    run_and_check(t, io, f"pad {offset} {io}")
+    # head-major storage, one step size and one dout for all tokens
+    for k in ("x", "z"):
+        t[k] = t[k].transpose(1, 2).contiguous().transpose(1, 2)
+    t["dout"] = t["dout"][:, :1].expand(-1, 70, -1, -1)
+    t["dt"] = t["dt"][:1].expand(2, -1, -1)
+    run_and_check(t, io, f"layouts {offset} {io}")
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_steps_as_they_are_and_strong_decay(io):
+    t = make((2, 150), 4, 16, 1, 16, io, seed=3)
+    t["dt"], t["dt_bias"] = t["dt"].abs(), None   # the bias is softplus's: with it the steps are negative and e^(A Delta) overflows 64 bits
+    run_and_check(t, io, f"no softplus {io}", softplus=False)
+    t = make((1, 150), 4, 16, 1, 16, io, seed=4)
+    t["dt"] = 30 * t["dt"]   # steps up to about 10: decays down to e^-160 a token
+    run_and_check(t, io, f"strong decay {io}", weak=("dA", "dh0"))
+    t["dt"][:, 70:] = float("-inf")   # no step at all
+    t["dt"][:, 130:] = -200.0
+    run_and_check(t, io, f"steps of 0 {io}", weak=("dA", "dh0"))
+
+
+PACKED = {
+    "one": [0, 40],
+    "on_chunks": [0, 64, 128, 192],
+    "empty_and_single": [0, 0, 1, 2, 2, 2, 19, 20, 150, 150],
+    "outside": [5, 9, 140, 260],
+    "all_empty": [7, 7, 7],
+    "none": [0],
+    "many": list(range(0, 400, 3)),
+    "long": [0, 3, 150, 151, 500],
+}
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("name", PACKED)
+@pytest.mark.parametrize("H,P,G,N,gate", [(2, 16, 1, 16, True), (4, 33, 2, 20, False), (3, 64, 1, 64, False)])
+def test_packed(name, H, P, G, N, gate, io):
+    cu = torch.tensor(PACKED[name], dtype=torch.int32, device=DEV)
+    T = PACKED[name][-1] + (13 if name in ("outside", "all_empty", "none") else 0)
+    t = make((T,), H, P, G, N, io, n=cu.numel() - 1, seed=T + H, gate=gate, h0=P != 64)
+    g = run_and_check(t, io, f"packed {name} {H} {P} {N} {io}", cu)
+    # rows in no sequence: zeros in what is made here, untouched in what is given
+    out = call(t, ssm.ssd_scan_fwd, cu=cu)
+    given = torch.full((H, T, P), 7.0, device=DEV, dtype=TYPES[io]).transpose(0, 1)
+    call(t, ssm.ssd_scan_fwd, cu=cu, out=given)
+    lo, hi = PACKED[name][0], PACKED[name][-1]
+    assert torch.equal(given[lo:hi], out[lo:hi])
+    for part in (slice(0, lo), slice(hi, T)):
+        assert not out[part].any() and torch.all(given[part] == 7.0)
+        assert not any(g[k][part].any() for k in ("dx", "ddt", "dB", "dC", "dz") if k in g)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_packed_and_batched_agree_bit_for_bit(io):
+    """A sequence's gradients do not depend on where it lies."""
+    t = make((3, 77), 4, 64, 1, 32, io, seed=5)
+    cu = torch.arange(0, 3 * 77 + 1, 77, dtype=torch.int32, device=DEV)
+    a = call(t, ssm.ssd_scan_bwd, t["dout"], dlast=t["dlast"])
+    flat = {k: v.flatten(0, 1) if k in ("x", "dt", "B", "C", "z", "dout") else v for k, v in t.items()}
+    b = call(flat, ssm.ssd_scan_bwd, flat["dout"], cu=cu, dlast=t["dlast"])
+    for k in a:
+        if k in ("dx", "ddt", "dz", "dh0"):
+            assert torch.equal(a[k].flatten(), b[k].flatten()), k
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_packed_next_to_the_batched_prefill(io):
+    t = make((3, 150), 4, 32, 2, 32, io, seed=6)
+    cu = torch.arange(0, 3 * 150 + 1, 150, dtype=torch.int32, device=DEV)
+    a = call(t, ssm.ssd_scan_fwd, return_last_state=True)
+    flat = {k: v.flatten(0, 1) if k in ("x", "dt", "B", "C", "z", "dout") else v for k, v in t.items()}
+    b = call(flat, ssm.ssd_scan_fwd, cu=cu, return_last_state=True)
+    val, bnd = expected(t, io)
+    for out, last in (a, (b[0].unflatten(0, (3, 150)), b[1])):
+        check(dict(out=out), val, bnd, io, f"prefill {io}")
+    assert torch.allclose(a[1], b[1], rtol=0, atol=float(np.max(bnd["last"] + 2.0 ** -8 * np.abs(val["last"]).max())))
+
+
+def test_state_in_place_and_given_outputs():
+    t = make((90,), 3, 16, 1, 16, n=3, seed=7)
+    cu = torch.tensor([0, 30, 30, 90], dtype=torch.int32, device=DEV)
+    out, last = call(t, ssm.ssd_scan_fwd, cu=cu, return_last_state=True)
+    state, o2 = t["h0"].clone(), torch.empty_like(out)
+    t2 = {**t, "h0": state}
+    ws = torch.empty(8 << 20, dtype=torch.uint8, device=DEV)
+    got = call(t2, ssm.ssd_scan_fwd, cu=cu, return_last_state=True, last_state=state, out=o2, workspace=ws)
+    assert got[0] is o2 and got[1] is state and torch.equal(o2, out) and torch.equal(state, last)
+    assert torch.equal(last[1], t["h0"][1])
+    # the second part of a sequence goes on from the first one's state
+    one = {k: v[:60] if k in ("x", "dt", "B", "C", "z") else v for k, v in t.items()}
+    cut = torch.tensor([0, 30, 30, 60], dtype=torch.int32, device=DEV)
+    _, st = call(one, ssm.ssd_scan_fwd, cu=cut, return_last_state=True)
+    two = {k: v[60:] if k in ("x", "dt", "B", "C", "z") else v for k, v in t.items()}
+    two["h0"] = st
+    b, st = call(two, ssm.ssd_scan_fwd, cu=torch.tensor([0, 0, 0, 30], dtype=torch.int32, device=DEV), return_last_state=True)
+    assert torch.allclose(b, out[60:], rtol=1e-4, atol=1e-4) and torch.allclose(st, last, rtol=1e-4, atol=1e-5)
+
+
+def test_nan_stays_with_its_sequence():
+    cu = torch.tensor([3, 70, 140, 200], dtype=torch.int32, device=DEV)
+    t = make((205,), 2, 16, 1, 16, n=3, seed=8)
+    clean, last0 = call(t, ssm.ssd_scan_fwd, cu=cu, return_last_state=True)
+    g0 = call(t, ssm.ssd_scan_bwd, t["dout"], cu=cu, dlast=t["dlast"])
+    for k in ("x", "B", "dt", "dout", "z", "C"):
+        t[k] = t[k].clone()
+        t[k][:3] = float("nan")
+        t[k][203:] = float("inf")
+        if k != "dt":
+            t[k][100] = float("nan")
+    out, last = call(t, ssm.ssd_scan_fwd, cu=cu, return_last_state=True)
+    g = call(t, ssm.ssd_scan_bwd, t["dout"], cu=cu, dlast=t["dlast"])
+    for part in (slice(0, 70), slice(140, 205)):
+        assert torch.equal(out[part], clean[part])
+        for k in ("dx", "ddt", "dB", "dC", "dz"):
+            assert torch.equal(g[k][part], g0[k][part]), k
+    for k in (0, 2):
+        assert torch.equal(last[k], last0[k]) and torch.equal(g["dh0"][k], g0["dh0"][k])
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_no_tokens(packed):
+    lead, n = ((0,), 2) if packed else ((2, 0), 2)
+    cu = torch.zeros(3, dtype=torch.int32, device=DEV) if packed else None
+    t = make(lead, 3, 8, 1, 8, n=n, seed=9)
+    g = call(t, ssm.ssd_scan_bwd, t["dout"], cu=cu, dlast=t["dlast"])
+    assert torch.equal(g["dh0"], t["dlast"]) and not any(g[k].any() for k in ("dA", "dD", "ddt_bias"))
+    if packed:
+        out, last = call(t, ssm.ssd_scan_fwd, cu=cu, return_last_state=True)
+        assert out.shape == t["x"].shape and torch.equal(last, t["h0"])
+
+
+def test_same_bits_every_run():
+    t = make((2, 500), 16, 64, 1, 64, "bf16", seed=10)
+    runs = [call(t, ssm.ssd_scan_bwd, t["dout"], dlast=t["dlast"]) for _ in range(3)]
+    for k in runs[0]:
+        assert all(torch.equal(runs[0][k], r[k]) for r in runs[1:]), k
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("packed", [False, True])
+def test_autograd(packed, io):
+    cu = torch.tensor([0, 9, 9, 50, 80], dtype=torch.int32, device=DEV) if packed else None
+    t = make((80,) if packed else (2, 40), 4, 16, 2, 16, io, n=4 if packed else 2, seed=11)
+    leaves = {k: t[k].detach().clone().requires_grad_() for k in ("x", "dt", "A", "B", "C", "D", "z", "dt_bias", "h0")}
+    out, last = ssm.ssd_scan(**leaves, cu_seqlens=cu, return_last_state=True)
+    g = torch.autograd.grad([out, last], list(leaves.values()), [t["dout"], t["dlast"]])
+    want = call(t, ssm.ssd_scan_bwd, t["dout"], cu=cu, dlast=t["dlast"])
+    for a, k in zip(g, ("dx", "ddt", "dA", "dB", "dC", "dD", "dz", "ddt_bias", "dh0")):
+        assert torch.equal(a, want[k]), k
+    # nothing optional, only the state's gradient
+    x = t["x"].detach().clone().requires_grad_()
+    _, last = ssm.ssd_scan(x, t["dt"], t["A"], t["B"], t["C"], cu_seqlens=cu, return_last_state=True)
+    (a,) = torch.autograd.grad(last, x, t["dlast"])
+    b = ssm.ssd_scan_bwd(torch.zeros_like(t["dout"]), t["x"], t["dt"], t["A"], t["B"], t["C"], dlast=t["dlast"], cu_seqlens=cu)
+    assert torch.equal(a, b["dx"])
+
+
+def test_two_captured_graphs_at_once():
+    ts = [make((2, 150), 4, 32, 1, 32, "bf16", seed=20 + k) for k in range(2)]
+    cu = torch.tensor([0, 100, 300], dtype=torch.int32, device=DEV)
+    flats = [{k: v.flatten(0, 1) if k in ("x", "dt", "B", "C", "z", "dout") else v for k, v in t.items()} for t in ts]
+
+    def run(t, f, **kw):
+        return call(f, ssm.ssd_scan_fwd, cu=cu, return_last_state=True, **kw), call(t, ssm.ssd_scan_bwd, t["dout"], dlast=t["dlast"], **kw)
+    want = [run(t, f) for t, f in zip(ts, flats)]
+    graphs, streams = [], [torch.cuda.Stream() for _ in ts]
+    for t, f, s in zip(ts, flats, streams):
+        ws = torch.empty(16 << 20, dtype=torch.uint8, device=DEV)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            got = run(t, f, workspace=ws)
+        graphs.append((g, got, ws))
+    for _ in range(4):
+        for _, ((o, last), g), _ in graphs:
+            for v in (o, last, *g.values()):
+                v.zero_()
+        torch.cuda.synchronize()
+        for (g, _, _), s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for (_, ((o, last), g), _), ((wo, wl), wg) in zip(graphs, want):
+            assert torch.equal(o, wo) and torch.equal(last, wl)
+            for k in wg:
+                assert torch.equal(g[k], wg[k]), k
+
+
+def test_refusals():
+    t = make((2, 70), 4, 16, 2, 16, seed=12)
+    args = dict(dout=t["dout"], x=t["x"], dt=t["dt"], A=t["A"], B=t["B"], C=t["C"])
+    cu = torch.tensor([0, 70], dtype=torch.int32, device=DEV)
+    for bad in (dict(dout=t["dout"][:, :60]), dict(dt=t["dt"][:, :, :3]), dict(C=t["C"][..., :8]), dict(A=t["A"][:2]), dict(cu_seqlens=cu),
+                dict(h0=t["h0"][:1]), dict(dlast=t["h0"][:1]), dict(x=t["x"].cpu()), dict(z=t["z"].transpose(2, 3).contiguous().transpose(2, 3))):
+        with pytest.raises(ValueError):
+            ssm.ssd_scan_bwd(**{**args, **bad})
+    for bad in (dict(dout=t["dout"].bfloat16()), dict(dt=t["dt"].half()), dict(A=t["A"].double()), dict(x=t["x"].half())):
+        with pytest.raises(TypeError):
+            ssm.ssd_scan_bwd(**{**args, **bad})
+    wide = torch.zeros(2, 70, 2, 65, device=DEV)   # more states than fp32 IO takes; groups that do not divide the heads
+    three = torch.zeros(2, 70, 3, 16, device=DEV)
+    for bad in (dict(B=wide, C=wide), dict(B=three, C=three)):
+        with pytest.raises(ssm.SSMError):
+            ssm.ssd_scan_bwd(**{**args, **bad})
+    p = dict(x=t["x"][0], dt=t["dt"][0], A=t["A"], B=t["B"][0], C=t["C"][0], cu_seqlens=cu)
+    ssm.ssd_scan_fwd(**p)
+    for bad in (dict(workspace=False), dict(x=t["x"]), dict(h0=t["h0"]), dict(out=torch.zeros(70, 4, 15, device=DEV)), dict(dt=t["dt"][0, :60])):
+        with pytest.raises(ValueError):
+            ssm.ssd_scan_fwd(**{**p, **bad})
+    with pytest.raises(TypeError):
+        ssm.ssd_scan_fwd(**{**p, "cu_seqlens": cu.long()})
+    with pytest.raises(ssm.SSMError):
+        ssm.ssd_scan_fwd(**{**p, "out": t["x"][0]})

@@ -66,3 +66,45 @@ def test_ssd_step_is_the_recurrence():
         h = np.exp(step * A) * h + step * B * x
         assert np.isclose(state[0, 0, 0, 0], h, rtol=1e-12)
         assert np.isclose(out[0, 0, 0], (C * h + D * x) * z / (1 + np.exp(-z)), rtol=1e-12)
+
+
+def _scan_inputs(rng, lead, n, H=2, P=2, G=1, N=2):
+    return dict(x=rng.standard_normal(lead + (H, P)), dt=rng.standard_normal(lead + (H,)), A=-np.exp(rng.standard_normal(H)),
+                B=rng.standard_normal(lead + (G, N)), C=rng.standard_normal(lead + (G, N)), D=rng.standard_normal(H),
+                z=rng.standard_normal(lead + (H, P)), bias=rng.standard_normal(H), h0=rng.standard_normal((n, H, P, N)))
+
+
+def test_ssd_steps_are_the_scan():
+    rng = np.random.default_rng(5)
+    t = _scan_inputs(rng, (2, 6), 2, H=4, P=3, G=2, N=5)
+    v, _ = ref.ssd_scan(**t)
+    state = t["h0"]
+    for k in range(6):
+        out, _, state, _ = ref.ssd_step(state, t["x"][:, k], t["dt"][:, k], t["A"], t["B"][:, k], t["C"][:, k], D=t["D"],
+                                        z=t["z"][:, k], bias=t["bias"])
+        assert np.allclose(out, v["out"][:, k], rtol=1e-12, atol=1e-12)
+    assert np.allclose(state, v["last"], rtol=1e-12)
+
+
+@pytest.mark.parametrize("cu", [None, [1, 1, 2, 5, 5, 8]])
+def test_ssd_gradients_are_the_differences(cu):
+    rng = np.random.default_rng(6)
+    lead, n = ((2, 4), 2) if cu is None else ((9,), len(cu) - 1)
+    args = _scan_inputs(rng, lead, n)
+    dout, dlast = rng.standard_normal(lead + (2, 2)), rng.standard_normal((n, 2, 2, 2))
+
+    def loss(**kw):
+        v, _ = ref.ssd_scan(cu=cu, **kw)
+        return (v["out"] * dout).sum() + (v["last"] * dlast).sum()
+
+    g, _ = ref.ssd_scan(cu=cu, dout=dout, dlast=dlast, **args)
+    for name, key in (("x", "dx"), ("dt", "ddt"), ("A", "dA"), ("B", "dB"), ("C", "dC"), ("D", "dD"), ("z", "dz"),
+                      ("bias", "ddt_bias"), ("h0", "dh0")):
+        for idx in np.ndindex(args[name].shape):
+            step = 1e-5
+            up, dn = ({k: t.copy() for k, t in args.items()} for _ in range(2))
+            up[name][idx] += step
+            dn[name][idx] -= step
+            d = (loss(**up) - loss(**dn)) / (2 * step)
+            # central differences: step^2 of the third derivative, and 2^-53 |loss| / step
+            assert abs(d - g[key][idx]) <= 1e-6 * (1 + abs(d)), (key, idx)
