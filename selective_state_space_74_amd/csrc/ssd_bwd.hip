@@ -23,10 +23,12 @@
 // bits; G L and M L are rounded to bf16 where they enter the products for dx, dB and
 // dC, which are rounded to bf16 themselves.
 //
-// A workgroup takes a chunk and up to 8 heads of a group; a wavefront owns 16 of the
-// chunk's tokens, as s for dx and dB and as t for dC.  G, the sum over the heads of M
-// L Delta, and dB and dC stay in registers from head to head, so dB and dC cost one
-// product with C and B for all heads.
+// A workgroup takes a chunk and up to 8 heads of a group.  Two of its 8 wavefronts
+// share 16 of the chunk's tokens, as s for dx and dB and as t for dC: each has every
+// other tile of G and M, half of the states for dB and dC and half of the channels
+// for dx.  G, the sum over the heads of M L Delta, and dB and dC stay in registers
+// from head to head, so dB and dC cost one product with C and B for all heads; the
+// next head's loads are under way while one is computed.
 #include <algorithm>
 
 #include "abi_checks.h"
@@ -37,11 +39,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-constexpr int QB = kQ / 16;
-
-// Keeps the loads of one tile's operands from being moved ahead of the tiles before
-// it: unrolled as they are, all of them at once would not fit the registers.
-__device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0); }
+constexpr int kGradThreads = 512;
+constexpr int QB = kQ / 16;        // blocks of 16 tokens
+constexpr int kTiles = QB / 2;     // tiles of a wavefront, of its tokens as s
 
 struct GradParams {
   void* dx;          // contiguous (row, token, H, P)
@@ -54,72 +54,103 @@ struct GradParams {
   int64_t tokens;    // of all rows
 };
 
-template <typename T, int NMAX, bool kGate, bool kVec>
-__global__ __launch_bounds__(kThreads, 2) void ssd_grad_kernel(ChunkParams p, GradParams q, int grid) {
+// kOne: a head's channels are one pass.
+template <typename T, int NMAX, bool kGate, bool kVec, bool kOne>
+__global__ __launch_bounds__(kGradThreads, sizeof(T) == 2 && NMAX == 64 ? 4 : 2) void ssd_grad_kernel(ChunkParams p, GradParams q, int grid) {
   using E = typename Lds<T>::E;
   using F = typename Frag<T>::V;
   constexpr bool kBF = sizeof(T) == 2;
-  constexpr int kPad = 16 / sizeof(E), NP = NMAX + kPad, XP = kPB + kPad, GP = kQ + kPad, NT = NMAX / 16;
-  // heads: x, dy (and its remainder), a state (and its remainder); before and after
-  // them: B and C, and the sum over the heads
+  constexpr int kPad = 16 / sizeof(E), NP = NMAX + kPad, XP = kPB + kPad, GP = kQ + kPad, NT = NMAX / 16, NH = NT / 2;
+  // heads: x, dy (and its remainder), a state (and its remainder), (G L)^T; before and
+  // after them: B and C, and the sum over the heads
   constexpr int kX = 0, kDy = kQ * XP, kDyl = 2 * kQ * XP, kS = (kGate && kBF ? 3 : 2) * kQ * XP, kSl = kS + kPB * NP;
-  constexpr int kHead = kS + (kBF ? 2 : 1) * kPB * NP, kEnds = 2 * kQ * NP + kQ * GP;
-  __shared__ __align__(16) E lds[kHead > kEnds ? kHead : kEnds];
-  __shared__ __align__(16) float sDl[kMostHeads][kQ];
-  __shared__ __align__(16) float sLa[kMostHeads][kQ];
-  __shared__ float sSlope[kMostHeads][kQ];
-  __shared__ float sRow[kWaves][kQ], sCol[kQ], sDiag[kQ], sC0[kQ], sR[kQ], sM0[kQ], sE[kWaves];
+  constexpr int kGl = kS + (kBF ? 2 : 1) * kPB * NP, kHead = kGl + kQ * GP, kEnds = 2 * kQ * NP + kQ * GP;
+  // kKeep: B and C stay in LDS, next to the heads' operands; their fragments are read
+  // again and again, which leaves the registers for two workgroups a compute unit
+  // (128 of them).  Else they make room, and their fragments stay in registers.
+  constexpr bool kKeep = kBF && NMAX == 64;
+  constexpr int kB = kKeep ? kHead : 0, kC = kB + kQ * NP, kG = kKeep ? 0 : 2 * kQ * NP;
+  // the small arrays first: their addresses are then offsets in the instruction
+  struct Shared {
+    float dl[kMostHeads][kQ], la[kMostHeads][kQ];
+    float row[QB][kQ], col[2][kQ], c[2][kQ], r[2][kQ], diag[kQ], m[kQ], pairs[kGradThreads / 64];
+    alignas(16) E tiles[kKeep ? kHead + 2 * kQ * NP : kHead > kEnds ? kHead : kEnds];
+  };
+  __shared__ __align__(16) Shared sh;
+  E* const lds = sh.tiles;
   const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lq = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), tok = wave % QB, half = wave / QB;
   const int id = static_cast<int>(xcd_order(blockIdx.x, grid));
   const int c = id / (p.G * p.blocks), g = id / p.blocks % p.G, block = id % p.blocks, h0 = g * p.per_group + block * p.hb;
   const int heads = min(p.hb, (g + 1) * p.per_group - h0);
   const Chunk k = chunk_of(p, c);
   if (k.len == 0) {   // not a chunk: nothing to the sums
-    for (int i = tid; i < 3 * heads; i += kThreads) q.parts[(static_cast<int64_t>(i % 3) * p.H + h0 + i / 3) * p.nc + c] = 0.0f;
+    for (int i = tid; i < 3 * heads; i += kGradThreads)
+      q.parts[(static_cast<int64_t>(i % 3) * p.H + h0 + i / 3) * p.nc + c] = 0.0f;
     return;
   }
-  for (int i = wave; i < heads; i += kWaves) {
+  for (int i = wave; i < heads; i += kGradThreads / 64) {
     const Steps s = steps_of<T>(p, k, h0 + i, lane);
-    sDl[i][lane] = s.delta;
-    sLa[i][lane] = s.la;
-    sSlope[i][lane] = s.slope;
+    sh.dl[i][lane] = s.delta;
+    sh.la[i][lane] = s.la;
   }
-  E* const sB = lds;
-  E* const sC = lds + kQ * NP;
+  E* const sB = lds + kB;
+  E* const sC = lds + kC;
   auto stage_bc = [&]() {
-    stage_rows<T, NMAX, kThreads, kVec>(sB, NP, rows_of<T>(p.B, k, g, 0, p.N), tid);
-    stage_rows<T, NMAX, kThreads, kVec>(sC, NP, rows_of<T>(p.C, k, g, 0, p.N), tid);
+    stage_rows<T, NMAX, kGradThreads, kVec>(sB, NP, rows_of<T>(p.B, k, g, 0, p.N), tid);
+    stage_rows<T, NMAX, kGradThreads, kVec>(sC, NP, rows_of<T>(p.C, k, g, 0, p.N), tid);
   };
   stage_bc();
   __syncthreads();
 
-  // lane's token, as s and as t; its B and C, states 16 n + 4 lq ..
-  const int own = 16 * wave + lr;
-  F bf[NT], cf[NT];
+  // the lane's token, as s and as t; its B, and of B and C the states of the
+  // wavefront's half: tiles n0 .. n0 + NH - 1, lane: states 16 n + 4 lq ..
+  const int own = 16 * tok + lr, n0 = half * NH, nt = (p.N + 15) / 16;
+  F bf[kKeep ? 1 : NT], bh[kKeep ? 1 : NH], cf[kKeep ? 1 : NH];
+  auto frag_b = [&](int n) { return frag_along<T>(sB, NP, 16 * tok, 16 * n, lr, lq); };
+  auto frag_c = [&](int n) { return frag_along<T>(sC, NP, 16 * tok, 16 * n, lr, lq); };
+  if constexpr (!kKeep) {
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    bf[n] = frag_along<T>(sB, NP, 16 * wave, 16 * n, lr, lq);
-    cf[n] = frag_along<T>(sC, NP, 16 * wave, 16 * n, lr, lq);
+    for (int n = 0; n < NT; ++n) bf[n] = frag_b(n);
+#pragma unroll
+    for (int n = 0; n < NH; ++n) {
+      bh[n] = frag_b(n0 + n);
+      cf[n] = frag_c(n0 + n);
+    }
   }
-  // tiles of G and of the sum over the heads: lane holds t = 16 tb + 4 lq + i, s = own
-  v4f G[QB], sum[QB], dB[NT], dC[NT];
+  auto own_b = [&](int n) {
+    if constexpr (kKeep) return frag_b(n);
+    else return bf[n];
+  };
+  auto half_b = [&](int n) {
+    if constexpr (kKeep) return frag_b(n0 + n);
+    else return anew_words(bh[n]);
+  };
+  auto half_c = [&](int n) {
+    if constexpr (kKeep) return frag_c(n0 + n);
+    else return anew_words(cf[n]);
+  };
+  // tiles of G and of the sum over the heads: t block tok + half + 2 j, lane holds
+  // t = 16 tb + 4 lq + e, s = own
+  auto block_of = [&](int j) { return tok + half + 2 * j; };
+  v4f G[kTiles], sum[kTiles], dB[NH], dC[NH];
 #pragma unroll
-  for (int tb = 0; tb < QB; ++tb) {
-    G[tb] = sum[tb] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    if (tb < wave) continue;
+  for (int j = 0; j < kTiles; ++j) {
+    G[j] = sum[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    const int tb = block_of(j);
+    if (tb >= QB) continue;
     if constexpr (kBF) {
 #pragma unroll
       for (int n = 0; n < NT; n += 2)
-        G[tb] = mma32(frag_along<T>(sC, NP, 16 * tb, 16 * n, lr, lq), frag_along<T>(sC, NP, 16 * tb, 16 * n + 16, lr, lq), bf[n],
-                      bf[n + 1], G[tb]);
+        G[j] = mma32(frag_along<T>(sC, NP, 16 * tb, 16 * n, lr, lq), frag_along<T>(sC, NP, 16 * tb, 16 * n + 16, lr, lq), own_b(n),
+                     own_b(n + 1), G[j]);
     } else {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) G[tb] = mma16<T>(frag_along<T>(sC, NP, 16 * tb, 16 * n, lr, lq), bf[n], G[tb]);
+      for (int n = 0; n < NT; ++n) G[j] = mma16<T>(frag_along<T>(sC, NP, 16 * tb, 16 * n, lr, lq), own_b(n), G[j]);
     }
   }
 #pragma unroll
-  for (int n = 0; n < NT; ++n) dB[n] = dC[n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int n = 0; n < NH; ++n) dB[n] = dC[n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
   __syncthreads();
 
   E* const sX = lds + kX;
@@ -127,302 +158,321 @@ __global__ __launch_bounds__(kThreads, 2) void ssd_grad_kernel(ChunkParams p, Gr
   [[maybe_unused]] E* const sYl = lds + kDyl;
   E* const sS = lds + kS;
   [[maybe_unused]] E* const sSl = lds + kSl;
-  const int nt = (p.N + 15) / 16;
-  constexpr int kPer = NMAX / 4, kN = kPB * kPer / kThreads;   // pieces of a state row, of a thread
-  auto put_state = [&](int at, int j, const v4u& v) {
-    const int r = at / kPer + j * (kThreads / kPer), n = at % kPer * 4;
-    if constexpr (kBF) {
-      *reinterpret_cast<v2u*>(sS + r * NP + n) = v2u{highs(v[0], v[1]), highs(v[2], v[3])};
-      *reinterpret_cast<v2u*>(sSl + r * NP + n) = v2u{lows(v[0], v[1]), lows(v[2], v[3])};
+  E* const sGl = lds + kGl;   // [s][t]
+  using Tokens = Pieces<T, kPB, kGradThreads>;
+  using States = StatePieces<T, NMAX, kGradThreads>;
+  Tokens xv, yv, zv;
+  States sv;
+  auto load_y = [&](int h, int p0) {
+    yv.template load<kVec>(rows_of<T>(p.dout, k, h, p0, p.P), tid);
+    if constexpr (kGate) zv.template load<kVec>(rows_of<T>(p.z, k, h, p0, p.P), tid);
+  };
+  auto load_state = [&](const uint32_t* state, int h, int p0) {
+    sv.template load<kVec>(state_rows(state, ((static_cast<int64_t>(c) * p.H + h) * p.P + p0) * p.N, min(kPB, p.P - p0), p.N), tid);
+  };
+  auto load_head = [&](int h, int p0) {
+    xv.template load<kVec>(rows_of<T>(p.x, k, h, p0, p.P), tid);
+    load_y(h, p0);
+    load_state(p.state, h, p0);
+  };
+  // dy = dout, or dout silu(z), bf16 then in two parts
+  auto put_y = [&]() {
+    if constexpr (!kGate) {
+      yv.put(sY, XP, tid);
     } else {
-      *reinterpret_cast<v4u*>(sS + r * NP + n) = v;
+#pragma unroll
+      for (int j = 0; j < Tokens::kN; ++j) {
+        const int at = (tid / Tokens::kPer + j * Tokens::kStep) * XP + tid % Tokens::kPer * kPiece<T>;
+        uint32_t s[kPiece<T>];
+#pragma unroll
+        for (int e = 0; e < kPiece<T>; ++e) {
+          const float f = piece_f32<T>(yv.v[j], e) * silu_f32(piece_f32<T>(zv.v[j], e));
+          s[e] = kBF ? split_bf16(f) : __float_as_uint(f);
+        }
+        if constexpr (kBF) {
+          *reinterpret_cast<v4u*>(sY + at) = v4u{highs(s[0], s[1]), highs(s[2], s[3]), highs(s[4], s[5]), highs(s[6], s[7])};
+          *reinterpret_cast<v4u*>(sYl + at) = v4u{lows(s[0], s[1]), lows(s[2], s[3]), lows(s[4], s[5]), lows(s[6], s[7])};
+        } else {
+          *reinterpret_cast<v4u*>(sY + at) = v4u{s[0], s[1], s[2], s[3]};
+        }
+      }
     }
   };
+  auto put_state = [&]() { sv.put(sS, kBF ? sSl : sS, NP, tid); };
   auto held = [&](uint32_t v) { return kBF ? joined_bf16(v) : __uint_as_float(v); };
-  // a 16 x 16 tile of the state (rows n, k = channel) times x or dy of `own`; the
-  // remainders' products in the k = 32 form too: sums whose chain of products mixed
-  // it with the k = 16 form came out wrong
-  auto state_tile = [&](int n, int kbs, const F (&f)[kPB / 16], [[maybe_unused]] const F (&fl)[kPB / 16], auto with_rest) {
+  // a 16 x 16 tile of the state (rows n, k = channel) times x or dy of `own`, whose
+  // rows are in X (remainders in Xl); the remainders' products in the k = 32 form
+  // too: sums whose chain of products mixed it with the k = 16 form came out wrong
+  auto state_tile = [&](int n, int kbs, const E* X, [[maybe_unused]] const E* Xl, auto with_rest) {
     v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
     if constexpr (kBF) {
 #pragma unroll
       for (int kb = 0; kb < kPB / 16; kb += 2) {
         if (kb >= kbs) continue;
         const F s0 = frag_down<T>(sS, NP, 16 * kb, 16 * n, lr, lq), s1 = frag_down<T>(sS, NP, 16 * kb + 16, 16 * n, lr, lq);
-        acc = mma32(s0, frag_down<T>(sSl, NP, 16 * kb, 16 * n, lr, lq), f[kb], f[kb], acc);
-        acc = mma32(s1, frag_down<T>(sSl, NP, 16 * kb + 16, 16 * n, lr, lq), f[kb + 1], f[kb + 1], acc);
-        if constexpr (decltype(with_rest)::value) acc = mma32(s0, s1, fl[kb], fl[kb + 1], acc);
+        const F f0 = frag_along<T>(X, XP, 16 * tok, 16 * kb, lr, lq), f1 = frag_along<T>(X, XP, 16 * tok, 16 * kb + 16, lr, lq);
+        acc = mma32(s0, frag_down<T>(sSl, NP, 16 * kb, 16 * n, lr, lq), f0, f0, acc);
+        acc = mma32(s1, frag_down<T>(sSl, NP, 16 * kb + 16, 16 * n, lr, lq), f1, f1, acc);
+        if constexpr (decltype(with_rest)::value)
+          acc = mma32(s0, s1, frag_along<T>(Xl, XP, 16 * tok, 16 * kb, lr, lq), frag_along<T>(Xl, XP, 16 * tok, 16 * kb + 16, lr, lq),
+                      acc);
       }
     } else {
 #pragma unroll
       for (int kb = 0; kb < kPB / 16; ++kb)
-        if (kb < kbs) acc = mma16<T>(frag_down<T>(sS, NP, 16 * kb, 16 * n, lr, lq), f[kb], acc);
+        if (kb < kbs)
+          acc = mma16<T>(frag_down<T>(sS, NP, 16 * kb, 16 * n, lr, lq), frag_along<T>(X, XP, 16 * tok, 16 * kb, lr, lq), acc);
     }
     return acc;
   };
 
+  load_head(h0, 0);
   for (int i = 0; i < heads; ++i) {
     const int h = h0 + i;
-    // offsets of staged pieces are computed anew for each head: kept across the loop,
-    // all of them would take half the registers
-    int at = tid;
-    asm volatile("" : "+v"(at));
-    const float la_s = sLa[i][own], dl_s = sDl[i][own];
-    const float ew = __builtin_amdgcn_exp2f(sLa[i][kQ - 1] - la_s), ea = __builtin_amdgcn_exp2f(la_s);
+    const float la_s = sh.la[i][own], dl_s = sh.dl[i][own];
+    const float ew = __builtin_amdgcn_exp2f(sh.la[i][kQ - 1] - la_s), ea = __builtin_amdgcn_exp2f(la_s);
     const float Dh = p.D ? p.D[h] : 0.0f;
-    v4f M[QB];
+    v4f M[kTiles];
 #pragma unroll
-    for (int tb = 0; tb < QB; ++tb) M[tb] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < kTiles; ++j) M[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     float r_t = 0.0f, c_s = 0.0f, pairs = 0.0f;
-    const int64_t state_at = (static_cast<int64_t>(c) * p.H + h) * p.P * p.N;
-    // x and dy of channels p0 .. of the head
-    auto stage_tokens = [&](int p0, bool with_x) {
-      if (with_x) stage_rows<T, kPB, kThreads, kVec>(sX, XP, rows_of<T>(p.x, k, h, p0, p.P), at);
-      const Rows64 er = rows_of<T>(p.dout, k, h, p0, p.P);
-      if constexpr (!kGate) {
-        stage_rows<T, kPB, kThreads, kVec>(sY, XP, er, at);
-      } else {
-        const Rows64 zr = rows_of<T>(p.z, k, h, p0, p.P);
-        constexpr int kPerX = kPB / kPiece<T>, kStep = kThreads / kPerX, kNX = kQ / kStep;
-        const int r0 = at / kPerX, col = at % kPerX * kPiece<T>;
-        v4u va[kNX], za[kNX];
-#pragma unroll
-        for (int j = 0; j < kNX; ++j) {
-          va[j] = load_piece<T, kVec>(er, r0 + j * kStep, col);
-          za[j] = load_piece<T, kVec>(zr, r0 + j * kStep, col);
-        }
-#pragma unroll
-        for (int j = 0; j < kNX; ++j) {
-          const int r = r0 + j * kStep;
-          const v4u v = va[j], z = za[j];
-          uint32_t s[kPiece<T>];
-#pragma unroll
-          for (int e = 0; e < kPiece<T>; ++e) {
-            const float f = piece_f32<T>(v, e) * silu_f32(piece_f32<T>(z, e));
-            s[e] = kBF ? split_bf16(f) : __float_as_uint(f);
-          }
-          if constexpr (kBF) {
-            *reinterpret_cast<v4u*>(sY + r * XP + col) = v4u{highs(s[0], s[1]), highs(s[2], s[3]), highs(s[4], s[5]), highs(s[6], s[7])};
-            *reinterpret_cast<v4u*>(sYl + r * XP + col) = v4u{lows(s[0], s[1]), lows(s[2], s[3]), lows(s[4], s[5]), lows(s[6], s[7])};
-          } else {
-            *reinterpret_cast<v4u*>(sY + r * XP + col) = v4u{s[0], s[1], s[2], s[3]};
-          }
-        }
-      }
-    };
-    F xf[kPB / 16], yf[kPB / 16], yl[kPB / 16];
-    for (int p0 = 0; p0 < p.P; p0 += kPB) {
+    for (int p0 = 0; p0 < (kOne ? 1 : p.P); p0 += kPB) {
       const int cols = p.P - p0, kbs = (min(kPB, cols) + 15) / 16;
-      if (p0 > 0) __syncthreads();
-      stage_tokens(p0, true);
-      const StateRows in = state_rows(p.state, state_at + static_cast<int64_t>(p0) * p.N, min(kPB, cols), p.N);
-#pragma unroll
-      for (int j = 0; j < kN; ++j) put_state(at, j, load_states<kVec>(in, at / kPer + j * (kThreads / kPer), at % kPer * 4));
-      __syncthreads();
-#pragma unroll
-      for (int kb = 0; kb < kPB / 16; ++kb) {
-        xf[kb] = frag_along<T>(sX, XP, 16 * wave, 16 * kb, lr, lq);
-        yf[kb] = frag_along<T>(sY, XP, 16 * wave, 16 * kb, lr, lq);
-        if constexpr (kGate && kBF) yl[kb] = frag_along<T>(sYl, XP, 16 * wave, 16 * kb, lr, lq);
-        else yl[kb] = yf[kb];
+      if (!kOne && p0 > 0) {   // the loads of a head's first pass are under way since the head before
+        __syncthreads();
+        load_head(h, p0);
       }
+      xv.put(sX, XP, tid);
+      put_y();
+      put_state();
+      __syncthreads();
+      load_state(p.dstate, h, p0);
       // M[t][s] += dy_t . x_s
 #pragma unroll
-      for (int tb = 0; tb < QB; ++tb) {
-        if (tb < wave) continue;
+      for (int kb = 0; kb < kPB / 16; kb += kBF ? 2 : 1) {
+        if (kb >= kbs) continue;
+        const F x0 = frag_along<T>(sX, XP, 16 * tok, 16 * kb, lr, lq);
+        [[maybe_unused]] const F x1 = kBF ? frag_along<T>(sX, XP, 16 * tok, 16 * kb + 16, lr, lq) : x0;
 #pragma unroll
-        for (int kb = 0; kb < kPB / 16; kb += kBF ? 2 : 1) {
-          if (kb >= kbs) continue;
+        for (int j = 0; j < kTiles; ++j) {
+          const int tb = block_of(j);
+          if (tb >= QB) continue;
           const F y0 = frag_along<T>(sY, XP, 16 * tb, 16 * kb, lr, lq);
           if constexpr (kBF) {
-            M[tb] = mma32(y0, frag_along<T>(sY, XP, 16 * tb, 16 * kb + 16, lr, lq), xf[kb], xf[kb + 1], M[tb]);
+            M[j] = mma32(y0, frag_along<T>(sY, XP, 16 * tb, 16 * kb + 16, lr, lq), x0, x1, M[j]);
             if constexpr (kGate)
-              M[tb] = mma32(frag_along<T>(sYl, XP, 16 * tb, 16 * kb, lr, lq), frag_along<T>(sYl, XP, 16 * tb, 16 * kb + 16, lr, lq),
-                            xf[kb], xf[kb + 1], M[tb]);
+              M[j] = mma32(frag_along<T>(sYl, XP, 16 * tb, 16 * kb, lr, lq), frag_along<T>(sYl, XP, 16 * tb, 16 * kb + 16, lr, lq), x0,
+                           x1, M[j]);
           } else {
-            M[tb] = mma16<T>(y0, xf[kb], M[tb]);
+            M[j] = mma16<T>(y0, x0, M[j]);
           }
         }
-        keep_order();
+      }
+      if (kOne || p0 + kPB >= p.P) {
+        // M is complete: K, its sums, and the operands of dx; only the diagonal's tile
+        // (half 0, its first) has elements above it
+        float col = 0.0f;
+        auto tile = [&](int j, auto on_diagonal) {
+          constexpr bool kDiag = decltype(on_diagonal)::value;
+          const int tb = block_of(j);
+          const v4f la_t = *reinterpret_cast<const v4f*>(&sh.la[i][16 * tb + 4 * lq]);
+          float w[4], diag = 0.0f, m0 = 0.0f;
+          v4f rows;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int over = 4 * lq + e - lr;   // t - s on the diagonal's tile
+            float L = __builtin_amdgcn_exp2f(la_t[e] - la_s), m = M[j][e];
+            if constexpr (kDiag) {
+              L = over >= 0 ? L : 0.0f;
+              m = over >= 0 ? m : 0.0f;
+            }
+            w[e] = G[j][e] * L;
+            if constexpr (kDiag) w[e] = over >= 0 ? w[e] : 0.0f;
+            sum[j][e] = fmaf(m * L, dl_s, sum[j][e]);
+            float K = w[e] * m;
+            if constexpr (kDiag) {
+              diag += over == 0 ? K : 0.0f;
+              m0 += over == 0 ? m : 0.0f;
+              K = over > 0 ? K : 0.0f;
+            }
+            rows[e] = K * dl_s;
+            col += K;
+          }
+          *reinterpret_cast<F*>(sGl + own * GP + 16 * tb + 4 * lq) = tofrag<T>(w[0], w[1], w[2], w[3]);
+          const float s = row_sums(rows, lane);
+          if (lr < 4) sh.row[tok][16 * tb + 4 * lq + lr] = s;
+          if constexpr (kDiag) {
+            diag = quarter_sum(diag);
+            m0 = quarter_sum(m0);
+            if (lq == 0) {
+              sh.diag[own] = diag;
+              sh.m[own] = m0;
+            }
+          }
+        };
+        if (half == 0) tile(0, std::true_type{});
+        else if (block_of(0) < QB) tile(0, std::false_type{});
+#pragma unroll
+        for (int j = 1; j < kTiles; ++j)
+          if (block_of(j) < QB) tile(j, std::false_type{});
+        col = quarter_sum(col);
+        if (lq == 0) sh.col[half][own] = col;
       }
       // S_in^T dy_t: lane holds states 16 n + 4 lq + e
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        if (n >= nt) continue;
-        const v4f v = state_tile(n, kbs, yf, yl, std::integral_constant<bool, kGate>{});
+      for (int n = 0; n < NH; ++n) {
+        if (n0 + n >= nt) continue;
+        const F f = half_c(n);
+        const v4f v = state_tile(n0 + n, kbs, sY, sYl, std::integral_constant<bool, kGate>{});
 #pragma unroll
-        for (int e = 0; e < 4; ++e) r_t = fmaf(elem<T>(cf[n], e), v[e], r_t);
+        for (int e = 0; e < 4; ++e) r_t = fmaf(elem<T>(f, e), v[e], r_t);
         dC[n] += v * ea;
-        keep_order();
       }
       __syncthreads();
       // dS_out in the place of S_in, which it meets on the way
-      const StateRows leaving = state_rows(p.dstate, state_at + static_cast<int64_t>(p0) * p.N, min(kPB, cols), p.N);
 #pragma unroll
-      for (int j = 0; j < kN; ++j) {
-        const int r = at / kPer + j * (kThreads / kPer), n = at % kPer * 4;
-        const v4u v = load_states<kVec>(leaving, r, n);
+      for (int j = 0; j < States::kN; ++j) {
+        const int at = (tid / States::kPer + j * States::kStep) * NP + tid % States::kPer * 4;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float s = Lds<T>::f(sS[r * NP + n + e]);
-          if constexpr (kBF) s += Lds<T>::f(sSl[r * NP + n + e]);
-          pairs = fmaf(s, held(v[e]), pairs);
+          float s = Lds<T>::f(sS[at + e]);
+          if constexpr (kBF) s += Lds<T>::f(sSl[at + e]);
+          pairs = fmaf(s, held(sv.v[j][e]), pairs);
         }
-        put_state(at, j, v);
       }
+      put_state();
       __syncthreads();
+      if (kOne && i + 1 < heads) load_head(h + 1, 0);
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        if (n >= nt) continue;
-        const v4f v = state_tile(n, kbs, xf, xf, std::false_type{});
+      for (int n = 0; n < NH; ++n) {
+        if (n0 + n >= nt) continue;
+        const F f = half_b(n);
+        const v4f v = state_tile(n0 + n, kbs, sX, sX, std::false_type{});
 #pragma unroll
-        for (int e = 0; e < 4; ++e) c_s = fmaf(elem<T>(bf[n], e), v[e], c_s);
+        for (int e = 0; e < 4; ++e) c_s = fmaf(elem<T>(f, e), v[e], c_s);
         dB[n] += v * (ew * dl_s);
-        keep_order();
       }
     }
-    // K, its sums, and the operands of dx
-    F gl[QB];
-    float col = 0.0f, diag = 0.0f, m0 = 0.0f;
-#pragma unroll
-    for (int tb = 0; tb < QB; ++tb) {
-      if (tb < wave) {
-        gl[tb] = tofrag<T>(0.0f, 0.0f, 0.0f, 0.0f);
-        continue;
-      }
-      const v4f la_t = *reinterpret_cast<const v4f*>(&sLa[i][16 * tb + 4 * lq]);
-      v4f w, rows;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int t = 16 * tb + 4 * lq + e;
-        const float L = t >= own ? __builtin_amdgcn_exp2f(la_t[e] - la_s) : 0.0f;
-        w[e] = t >= own ? G[tb][e] * L : 0.0f;
-        const float m = t >= own ? M[tb][e] : 0.0f;
-        sum[tb][e] = fmaf(m * L, dl_s, sum[tb][e]);
-        const float K = w[e] * m;
-        const bool strict = t > own;
-        rows[e] = strict ? K * dl_s : 0.0f;
-        col += strict ? K : 0.0f;
-        diag += t == own ? K : 0.0f;
-        m0 += t == own ? m : 0.0f;
-      }
-      gl[tb] = tofrag<T>(w[0], w[1], w[2], w[3]);
-      const float s = row_sums(rows, lane);
-      if (lr < 4) sRow[wave][16 * tb + 4 * lq + lr] = s;
-      keep_order();
-    }
-    col = quarter_sum(col);
-    diag = quarter_sum(diag);
-    m0 = quarter_sum(m0);
     r_t = quarter_sum(r_t) * ea;
     c_s = quarter_sum(c_s) * ew;
     pairs = wave_sum(pairs);
     if (lq == 0) {
-      sCol[own] = col;
-      sDiag[own] = diag;
-      sM0[own] = m0;
-      sR[own] = r_t;
-      sC0[own] = c_s;
+      sh.r[half][own] = r_t;
+      sh.c[half][own] = c_s;
     }
-    if (lane == 0) sE[wave] = pairs * __builtin_amdgcn_exp2f(sLa[i][kQ - 1]);
-    // dx
-    for (int p0 = 0; p0 < p.P; p0 += kPB) {
-      const int cols = p.P - p0, pts = (min(kPB, cols) + 15) / 16;
-      if (p.P > kPB) {   // what is in LDS is the last pass's
+    if (lane == 0) sh.pairs[wave] = pairs * __builtin_amdgcn_exp2f(sh.la[i][kQ - 1]);
+    // dx, every other 16 channels
+    for (int p0 = 0; p0 < (kOne ? 1 : p.P); p0 += kPB) {
+      const int cols = p.P - p0;
+      if (!kOne) {   // what is in LDS is the last pass's
         __syncthreads();
-        stage_tokens(p0, false);
-        const StateRows leaving = state_rows(p.dstate, state_at + static_cast<int64_t>(p0) * p.N, min(kPB, cols), p.N);
-#pragma unroll
-        for (int j = 0; j < kN; ++j) put_state(at, j, load_states<kVec>(leaving, at / kPer + j * (kThreads / kPer), at % kPer * 4));
+        load_y(h, p0);
+        load_state(p.dstate, h, p0);
+        put_y();
+        put_state();
         __syncthreads();
+        if (p0 + kPB >= p.P && i + 1 < heads) load_head(h + 1, 0);
       }
+      // the chunk's rows of dx, from the head's channel p0 on
+      const __amdgpu_buffer_rsrc_t dx = __builtin_amdgcn_make_buffer_rsrc(
+          static_cast<T*>(q.dx) + ((k.b * p.L + k.t0) * p.H + h) * p.P + p0, 0,
+          static_cast<int>(((k.len - 1) * p.H * p.P + cols) * sizeof(T)), kRsrcWord3);
 #pragma unroll
-      for (int pt = 0; pt < kPB / 16; ++pt) {
-        if (pt >= pts) continue;
+      for (int j = 0; j < kPB / 32; ++j) {
+        const int pt = 2 * j + half, c0 = 16 * pt + 4 * lq;
+        if (16 * pt >= cols) continue;
         v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int n = 0; n < NT; n += kBF ? 2 : 1) {
           if (n >= nt) continue;
           const F s0 = frag_along<T>(sS, NP, 16 * pt, 16 * n, lr, lq);
-          if constexpr (kBF) acc = mma32(s0, frag_along<T>(sS, NP, 16 * pt, 16 * n + 16, lr, lq), bf[n], bf[n + 1], acc);
-          else acc = mma16<T>(s0, bf[n], acc);
+          if constexpr (kBF) acc = mma32(s0, frag_along<T>(sS, NP, 16 * pt, 16 * n + 16, lr, lq), own_b(n), own_b(n + 1), acc);
+          else acc = mma16<T>(s0, own_b(n), acc);
         }
         acc *= ew;
+        // (G L)^T rows: blocks of t before the wavefront's own are not written, nor read
 #pragma unroll
         for (int tb = 0; tb < QB; tb += kBF ? 2 : 1) {
-          if (tb + (kBF ? 1 : 0) < wave) continue;
+          if (tb + (kBF ? 1 : 0) < tok) continue;
           const F y0 = frag_down<T>(sY, XP, 16 * tb, 16 * pt, lr, lq);
-          if constexpr (kBF) acc = mma32(y0, frag_down<T>(sY, XP, 16 * tb + 16, 16 * pt, lr, lq), gl[tb], gl[tb + 1], acc);
-          else acc = mma16<T>(y0, gl[tb], acc);
+          const F w0 = tb >= tok ? frag_along<T>(sGl, GP, 16 * tok, 16 * tb, lr, lq) : tofrag<T>(0.0f, 0.0f, 0.0f, 0.0f);
+          if constexpr (kBF)
+            acc = mma32(y0, frag_down<T>(sY, XP, 16 * tb + 16, 16 * pt, lr, lq), w0,
+                        frag_along<T>(sGl, GP, 16 * tok, 16 * tb + 16, lr, lq), acc);
+          else acc = mma16<T>(y0, w0, acc);
         }
-        keep_order();
-        const int c0 = 16 * pt + 4 * lq;
         if (own >= k.len || c0 >= cols) continue;
         float d[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) d[e] = fmaf(dl_s, acc[e], Dh * Lds<T>::f(sY[own * XP + c0 + e]));
-        T* const to = static_cast<T*>(q.dx) + ((k.b * p.L + k.t0 + own) * p.H + h) * p.P + p0 + c0;
-        if constexpr (kVec) {
-          if constexpr (kBF) *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3]));
-          else *reinterpret_cast<float4*>(to) = make_float4(d[0], d[1], d[2], d[3]);
+        const uint32_t off = (own * p.H * p.P + c0) * static_cast<uint32_t>(sizeof(T));
+        if constexpr (kVec && kBF) {
+          __builtin_amdgcn_raw_buffer_store_b64(v2u{pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3])}, dx, off, 0, 0);
+        } else if constexpr (kVec) {
+          __builtin_amdgcn_raw_buffer_store_b128(v4u{__float_as_uint(d[0]), __float_as_uint(d[1]), __float_as_uint(d[2]), __float_as_uint(d[3])},
+                                                 dx, off, 0, 0);
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (c0 + e < cols) io<T>::store(to + e, d[e]);
+            if (c0 + e < cols) Elem<T>::store(dx, off + e * static_cast<uint32_t>(sizeof(T)), d[e]);
         }
       }
     }
     __syncthreads();   // the sums are there, and LDS is free
-    if (wave == i % kWaves) {   // the steps' gradients; written over after the next barrier
+    if (wave == i) {   // the steps' gradients; written over after the next barrier
       float row = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w)
-        if (w <= lane / 16) row += sRow[w][lane];
-      const float dl = sDl[i][lane], cs = sC0[lane], cl = sCol[lane], r = sR[lane];
+      for (int w = 0; w < QB; ++w)
+        if (w <= lane / 16) row += sh.row[w][lane];
+      const Steps st = steps_of<T>(p, k, h, lane);
+      const float dl = st.delta, cs = sh.c[0][lane] + sh.c[1][lane], cl = sh.col[0][lane] + sh.col[1][lane], r = sh.r[0][lane] + sh.r[1][lane];
       const float step = dl * (cl + cs) - row - r;
       float g0 = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) g0 += sE[w];
+      for (int w = 0; w < kGradThreads / 64; ++w) g0 += sh.pairs[w];
       const float flow = wave_sum(r) + g0 + (wave_prefix_sum(step) - step);
-      float d = cl + sDiag[lane] + cs + p.A[h] * flow;
-      d = lane < k.len ? d * sSlope[i][lane] : 0.0f;
+      float d = cl + sh.diag[lane] + cs + p.A[h] * flow;
+      d = lane < k.len ? d * st.slope : 0.0f;
       if (lane < k.len) io<T>::store(static_cast<T*>(q.ddt) + (k.b * p.L + k.t0 + lane) * p.H + h, d);
-      const float da = wave_sum(dl * flow), db = wave_sum(d), dd = wave_sum(sM0[lane]);
+      const float da = wave_sum(dl * flow), db = wave_sum(d), dd = wave_sum(sh.m[lane]);
       if (lane < 3) q.parts[(static_cast<int64_t>(lane) * p.H + h) * p.nc + c] = lane == 0 ? da : lane == 1 ? db : dd;
     }
   }
 
   // dB and dC of the chunk: the products with C and B, over the sum of the heads
-  E* const sG = lds + 2 * kQ * NP;   // [t][s]
-  stage_bc();
-  F sf[QB];
+  E* const sG = lds + kG;   // [t][s]
+  E* const sGt = sGl;       // [s][t]
+  static_assert(kKeep ? kGl >= kQ * GP : kGl >= kEnds, "the two lie apart, and past B and C");
+  if constexpr (!kKeep) stage_bc();
 #pragma unroll
-  for (int tb = 0; tb < QB; ++tb) {
-    sf[tb] = tofrag<T>(sum[tb][0], sum[tb][1], sum[tb][2], sum[tb][3]);
-    if (tb < wave) continue;
+  for (int j = 0; j < kTiles; ++j) {
+    const int tb = block_of(j);
+    if (tb >= QB) continue;
+    *reinterpret_cast<F*>(sGt + own * GP + 16 * tb + 4 * lq) = tofrag<T>(sum[j][0], sum[j][1], sum[j][2], sum[j][3]);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sG[(16 * tb + 4 * lq + e) * GP + own] = Lds<T>::from(sum[tb][e]);
+    for (int e = 0; e < 4; ++e) sG[(16 * tb + 4 * lq + e) * GP + own] = Lds<T>::from(sum[j][e]);
   }
   __syncthreads();
 #pragma unroll
   for (int tb = 0; tb < QB; ++tb) {
-    if (tb >= wave) {
+    if (tb >= tok) {
+      const F gf = frag_along<T>(sGt, GP, 16 * tok, 16 * tb, lr, lq);
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-        if (n < nt) dB[n] = mma16<T>(frag_down<T>(sC, NP, 16 * tb, 16 * n, lr, lq), sf[tb], dB[n]);
+      for (int n = 0; n < NH; ++n)
+        if (n0 + n < nt) dB[n] = mma16<T>(frag_down<T>(sC, NP, 16 * tb, 16 * (n0 + n), lr, lq), gf, dB[n]);
     }
-    if (tb <= wave) {
-      const F gf = frag_along<T>(sG, GP, 16 * wave, 16 * tb, lr, lq);
+    if (tb <= tok) {
+      const F gf = frag_along<T>(sG, GP, 16 * tok, 16 * tb, lr, lq);
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-        if (n < nt) dC[n] = mma16<T>(frag_down<T>(sB, NP, 16 * tb, 16 * n, lr, lq), gf, dC[n]);
+      for (int n = 0; n < NH; ++n)
+        if (n0 + n < nt) dC[n] = mma16<T>(frag_down<T>(sB, NP, 16 * tb, 16 * (n0 + n), lr, lq), gf, dC[n]);
     }
   }
   if (own >= k.len) return;
   const int64_t token = k.b * p.L + k.t0 + own, at = (token * p.G + g) * p.N;
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int s0 = 16 * n + 4 * lq;
+  for (int n = 0; n < NH; ++n) {
+    const int s0 = 16 * (n0 + n) + 4 * lq;
     if (s0 >= p.N) continue;
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
@@ -521,7 +571,8 @@ template <typename T, int NMAX>
 void launch_grad(const ChunkParams& p, const GradParams& q, hipStream_t stream) {
   const int grid = p.nc * p.G * p.blocks;
   auto go = [&](auto gate, auto vec) {
-    ssd_grad_kernel<T, NMAX, gate.value, vec.value><<<grid, kThreads, 0, stream>>>(p, q, grid);
+    if (p.P <= kPB) ssd_grad_kernel<T, NMAX, gate.value, vec.value, true><<<grid, kGradThreads, 0, stream>>>(p, q, grid);
+    else ssd_grad_kernel<T, NMAX, gate.value, vec.value, false><<<grid, kGradThreads, 0, stream>>>(p, q, grid);
   };
   if (p.z.p && p.vec) go(std::true_type{}, std::true_type{});
   else if (p.z.p) go(std::true_type{}, std::false_type{});
@@ -588,6 +639,8 @@ hipError_t launch_ssd_packed_fwd(const ssm_ssd_packed_args& a, hipStream_t strea
   p.z = tensor(a.z, 0, a.z_seq_stride, a.z_head_stride, p.P, bf16);
   p.B = tensor(a.B, 0, a.B_seq_stride, Bg, p.N, bf16);
   p.C = tensor(a.C, 0, a.C_seq_stride, Cg, p.N, bf16);
+  p.vec = p.x.vec && p.B.vec && p.C.vec && tensor(a.out, 0, a.out_seq_stride, a.out_head_stride, p.P, bf16).vec &&
+          (!a.z || p.z.vec);
   OutsideRows rows;
   if (a.zero_outside && a.seqlen > 0) {
     const bool whole = a.out_head_stride == a.headdim;   // the heads side by side
@@ -598,7 +651,6 @@ hipError_t launch_ssd_packed_fwd(const ssm_ssd_packed_args& a, hipStream_t strea
   if (e != hipSuccess) return e;
   e = launch_chunk_states(p, bf16, false, a.nseq, a.h0, a.last_state, nullptr, nullptr, stream);
   if (e != hipSuccess) return e;
-  p.vec = p.x.vec && p.B.vec && p.C.vec && tensor(a.out, 0, a.out_seq_stride, a.out_head_stride, p.P, bf16).vec && (!a.z || p.z.vec);
   const ChunkOut o{a.out, 0, a.out_seq_stride, a.out_head_stride, nullptr};
   return launch_chunk_outputs(p, o, bf16, stream);
 }

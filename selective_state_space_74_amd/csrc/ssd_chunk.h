@@ -119,6 +119,24 @@ __device__ __forceinline__ float wave_sum(float v) { return lane_value(wave_pref
 
 // ---- tiles in LDS ---------------------------------------------------------------
 
+// A thread's number that the compiler takes for a new one: offsets made from it are
+// computed where they are used, and not kept in registers around a loop.
+__device__ __forceinline__ int anew(int tid) {
+  asm volatile("" : "+v"(tid));
+  return tid;
+}
+
+template <typename V>
+__device__ __forceinline__ V anew_words(V v) {
+  if constexpr (sizeof(V) == 8) {
+    v2u w = __builtin_bit_cast(v2u, v);
+    asm volatile("" : "+v"(w));
+    return __builtin_bit_cast(V, w);
+  } else {
+    return v;
+  }
+}
+
 // 16 bytes of a row as registers hold them.
 template <typename T> constexpr int kPiece = 16 / sizeof(T);
 
@@ -144,18 +162,29 @@ __device__ __forceinline__ float piece_f32(const v4u& v, int i) {
   else return __uint_as_float(i % 2 ? v[i / 2] & 0xffff0000u : v[i / 2] << 16);
 }
 
-// Rows of a chunk into LDS (kQ rows of W columns, `pitch` apart), zeros past the
-// chunk's tokens and past the real columns.
+// Rows of a chunk (kQ rows of W columns) in a workgroup's registers, on their way to
+// LDS; zeros past the chunk's tokens and past the real columns.
+template <typename T, int W, int kThreads>
+struct Pieces {
+  static constexpr int kPer = W / kPiece<T>, kStep = kThreads / kPer, kN = kQ / kStep;
+  static_assert(kThreads % kPer == 0 && kQ % kStep == 0, "whole rows a step");
+  v4u v[kN];
+  template <bool kVec>
+  __device__ __forceinline__ void load(const Rows64& w, int tid) {
+    tid = anew(tid);
+#pragma unroll
+    for (int i = 0; i < kN; ++i) v[i] = load_piece<T, kVec>(w, tid / kPer + i * kStep, tid % kPer * kPiece<T>);
+  }
+  __device__ __forceinline__ void put(typename Lds<T>::E* dst, int pitch, int tid) const {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) *reinterpret_cast<v4u*>(dst + (tid / kPer + i * kStep) * pitch + tid % kPer * kPiece<T>) = v[i];
+  }
+};
 template <typename T, int W, int kThreads, bool kVec>
 __device__ __forceinline__ void stage_rows(typename Lds<T>::E* dst, int pitch, const Rows64& w, int tid) {
-  constexpr int kPer = W / kPiece<T>, kStep = kThreads / kPer, kN = kQ / kStep;
-  static_assert(kThreads % kPer == 0 && kQ % kStep == 0, "whole rows a step");
-  const int r0 = tid / kPer, col = tid % kPer * kPiece<T>;
-  v4u v[kN];
-#pragma unroll
-  for (int i = 0; i < kN; ++i) v[i] = load_piece<T, kVec>(w, r0 + i * kStep, col);
-#pragma unroll
-  for (int i = 0; i < kN; ++i) *reinterpret_cast<v4u*>(dst + (r0 + i * kStep) * pitch + col) = v[i];
+  Pieces<T, W, kThreads> q;
+  q.template load<kVec>(w, tid);
+  q.put(dst, pitch, tid);
 }
 
 // Four states n .. n + 3 of row r of a chunk's state: the words that the carry left.
@@ -177,6 +206,36 @@ __device__ __forceinline__ v4u load_states(const StateRows& w, int r, int n) {
   return v;
 }
 
+// The high (low) halves of two words, the first one's low.
+__device__ __forceinline__ uint32_t highs(uint32_t a, uint32_t b) { return a >> 16 | (b & 0xffff0000u); }
+__device__ __forceinline__ uint32_t lows(uint32_t a, uint32_t b) { return (a & 0xffffu) | b << 16; }
+
+// kPB rows of a state, likewise; bf16: the values to one array of LDS, the remainders
+// to another.
+template <typename T, int NMAX, int kThreads>
+struct StatePieces {
+  static constexpr int kPer = NMAX / 4, kStep = kThreads / kPer, kN = kPB / kStep;
+  v4u v[kN];
+  template <bool kVec>
+  __device__ __forceinline__ void load(const StateRows& w, int tid) {
+    tid = anew(tid);
+#pragma unroll
+    for (int i = 0; i < kN; ++i) v[i] = load_states<kVec>(w, tid / kPer + i * kStep, tid % kPer * 4);
+  }
+  __device__ __forceinline__ void put(typename Lds<T>::E* dst, typename Lds<T>::E* rest, int pitch, int tid) const {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int at = (tid / kPer + i * kStep) * pitch + tid % kPer * 4;
+      if constexpr (sizeof(T) == 2) {
+        *reinterpret_cast<v2u*>(dst + at) = v2u{highs(v[i][0], v[i][1]), highs(v[i][2], v[i][3])};
+        *reinterpret_cast<v2u*>(rest + at) = v2u{lows(v[i][0], v[i][1]), lows(v[i][2], v[i][3])};
+      } else {
+        *reinterpret_cast<v4u*>(dst + at) = v[i];
+      }
+    }
+  }
+};
+
 // A value as bf16 and the remainder's bf16, 16 bits together: the value in the
 // high half of a word, as it is widened, the remainder in the low one.
 __device__ __forceinline__ uint32_t split_bf16(float v) {
@@ -186,10 +245,6 @@ __device__ __forceinline__ uint32_t split_bf16(float v) {
 __device__ __forceinline__ float joined_bf16(uint32_t v) {
   return __uint_as_float(v & 0xffff0000u) + __uint_as_float(v << 16);
 }
-// The high (low) halves of two words, the first one's low.
-__device__ __forceinline__ uint32_t highs(uint32_t a, uint32_t b) { return a >> 16 | (b & 0xffff0000u); }
-__device__ __forceinline__ uint32_t lows(uint32_t a, uint32_t b) { return (a & 0xffffu) | b << 16; }
-
 // A 16-wide tile's fragment down the rows of LDS: X[k0 + 4 lq + i][c0 + lr].
 template <typename T>
 __device__ __forceinline__ typename Frag<T>::V frag_down(const typename Lds<T>::E* X, int pitch, int k0, int c0, int lr, int lq) {

@@ -118,29 +118,26 @@ __global__ __launch_bounds__(kThreads) void ssd_states_kernel(ChunkParams p, int
   const TokenTensor& x = back ? p.dout : p.x;
   const bool gate = back && p.z.p;
   const int nt = (p.N + 15) / 16, kb = (k.len + 15) / 16;
+  using Tokens = Pieces<T, kPB, kThreads>;
+  Tokens xv, zv;
+  auto load = [&](int i, int p0) {
+    xv.template load<kVec>(rows_of<T>(x, k, h0 + i, p0, p.P), tid);
+    if (gate) zv.template load<kVec>(rows_of<T>(p.z, k, h0 + i, p0, p.P), tid);
+  };
+  load(0, 0);
   for (int i = 0; i < heads; ++i) {
     for (int p0 = 0; p0 < p.P; p0 += kPB) {
-      const Rows64 xr = rows_of<T>(x, k, h0 + i, p0, p.P);
-      Rows64 zr = xr;
-      if (gate) zr = rows_of<T>(p.z, k, h0 + i, p0, p.P);
-      const int cols = p.P - p0;
-      constexpr int kPer = kPB / kPiece<T>, kStep = kThreads / kPer, kN = kQ / kStep;
-      const int r0 = tid / kPer, col = tid % kPer * kPiece<T>;
-      v4u v[kN], zv[kN];
+      const int cols = p.P - p0, col = tid % Tokens::kPer * kPiece<T>;
 #pragma unroll
-      for (int j = 0; j < kN; ++j) {
-        v[j] = load_piece<T, kVec>(xr, r0 + j * kStep, col);
-        if (gate) zv[j] = load_piece<T, kVec>(zr, r0 + j * kStep, col);
-      }
-#pragma unroll
-      for (int j = 0; j < kN; ++j) {
-        const int r = r0 + j * kStep;
+      for (int j = 0; j < Tokens::kN; ++j) {
+        const int r = tid / Tokens::kPer + j * Tokens::kStep;
+        const v4u v = xv.v[j];
         const float w = sW[i][r];
         uint32_t s[kPiece<T>];
 #pragma unroll
         for (int e = 0; e < kPiece<T>; ++e) {
-          float f = piece_f32<T>(v[j], e) * w;
-          if (gate) f *= silu_f32(piece_f32<T>(zv[j], e));
+          float f = piece_f32<T>(v, e) * w;
+          if (gate) f *= silu_f32(piece_f32<T>(zv.v[j], e));
           s[e] = kBF ? split_bf16(f) : __float_as_uint(f);
         }
         if constexpr (kBF) {
@@ -151,6 +148,9 @@ __global__ __launch_bounds__(kThreads) void ssd_states_kernel(ChunkParams p, int
         }
       }
       __syncthreads();
+      // the next pass's loads are under way while this one is computed
+      if (p0 + kPB < p.P) load(i, p0 + kPB);
+      else if (i + 1 < heads) load(i + 1, 0);
       // channels' tiles of this pass (1, 2 or 4) and the wavefronts that share one
       const int pts = min(kPB, cols) > 32 ? 4 : min(kPB, cols) > 16 ? 2 : 1;
       const int pt = wave % pts, first = wave / pts, step = kWaves / pts;
@@ -254,47 +254,75 @@ __global__ __launch_bounds__(kThreads) void ssd_carry_kernel(CarryParams p) {
 
 // ---- outputs ------------------------------------------------------------------------
 
-// Workgroup: (chunk, heads of one group), a wavefront 16 of its tokens.  The scores
-// C_t . B_s of the chunk are computed once and stay in registers for all heads.
-// Tiles lie so that a lane has four channels of one token.
+// Workgroup: (chunk, heads of one group); two of its 8 wavefronts share 16 of the
+// tokens, each with every other 16 channels of a head.  The scores C_t . B_s of the
+// chunk are computed once and stay in registers for all heads; the next head's loads
+// are under way while one is computed.  Tiles lie so that a lane has four channels
+// of one token.
 // kDz: the gate's gradient dout y silu'(z) in place of the output.
+constexpr int kOutThreads = 512;
+
+// Four values of a row from column c on (of `cols`), as they lie.
+template <typename T, bool kVec>
+__device__ __forceinline__ void load4(const Rows64& w, int r, int c, float (&v)[4]) {
+  const uint32_t off = r * w.stride + c * static_cast<uint32_t>(sizeof(T));
+  if constexpr (kVec) {
+    const uint32_t at = r < w.len && c < w.cols ? off : kNowhere;
+    if constexpr (sizeof(T) == 4) {
+      const v4u q = __builtin_amdgcn_raw_buffer_load_b128(w.r, at, 0, 0);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(q[e]);
+    } else {
+      const v2u q = __builtin_amdgcn_raw_buffer_load_b64(w.r, at, 0, 0);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(e % 2 ? q[e / 2] & 0xffff0000u : q[e / 2] << 16);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      v[e] = Elem<T>::f32(Elem<T>::load(w.r, r < w.len && c + e < w.cols ? off + e * static_cast<uint32_t>(sizeof(T)) : kNowhere));
+  }
+}
+
 template <typename T, int NMAX, bool kDz, bool kVec>
-__global__ __launch_bounds__(kThreads) void ssd_outputs_kernel(ChunkParams p, ChunkOut o, int grid) {
+__global__ __launch_bounds__(kOutThreads, 4) void ssd_outputs_kernel(ChunkParams p, ChunkOut o, int grid) {
   using E = typename Lds<T>::E;
   constexpr bool kBF = sizeof(T) == 2;
   constexpr int kPad = 16 / sizeof(E), NP = NMAX + kPad, XP = kPB + kPad, NT = NMAX / 16, QB = kQ / 16;
   constexpr int kScores = 2 * kQ * NP, kHead = kQ * XP + (kBF ? 2 : 1) * kPB * NP;
-  __shared__ __align__(16) E lds[kScores > kHead ? kScores : kHead];
-  __shared__ __align__(16) float sDl[kMostHeads][kQ];
-  __shared__ __align__(16) float sLa[kMostHeads][kQ];
+  struct Shared {
+    float dl[kMostHeads][kQ], la[kMostHeads][kQ];
+    alignas(16) E tiles[kScores > kHead ? kScores : kHead];
+  };
+  __shared__ __align__(16) Shared sh;
   const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lq = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), tok = wave % QB, half = wave / QB;
   const int id = static_cast<int>(xcd_order(blockIdx.x, grid));
   const int c = id / (p.G * p.blocks), g = id / p.blocks % p.G, h0 = g * p.per_group + id % p.blocks * p.hb;
   const int heads = min(p.hb, (g + 1) * p.per_group - h0);
   const Chunk k = chunk_of(p, c);
   if (k.len == 0) return;
 
-  for (int i = wave; i < heads; i += kWaves) {
+  for (int i = wave; i < heads; i += kOutThreads / 64) {
     const Steps s = steps_of<T>(p, k, h0 + i, lane);
-    sDl[i][lane] = s.delta;
-    sLa[i][lane] = s.la;
+    sh.dl[i][lane] = s.delta;
+    sh.la[i][lane] = s.la;
   }
-  E* const sB = lds;
-  E* const sC = lds + kQ * NP;
-  stage_rows<T, NMAX, kThreads, kVec>(sB, NP, rows_of<T>(p.B, k, g, 0, p.N), tid);
-  stage_rows<T, NMAX, kThreads, kVec>(sC, NP, rows_of<T>(p.C, k, g, 0, p.N), tid);
+  E* const sB = sh.tiles;
+  E* const sC = sh.tiles + kQ * NP;
+  stage_rows<T, NMAX, kOutThreads, kVec>(sB, NP, rows_of<T>(p.B, k, g, 0, p.N), tid);
+  stage_rows<T, NMAX, kOutThreads, kVec>(sC, NP, rows_of<T>(p.C, k, g, 0, p.N), tid);
   __syncthreads();
-  // scores[sb]: lane holds s = 16 sb + 4 lq + i, t = 16 wave + lr
-  const int own = 16 * wave + lr;
+  // scores[sb]: lane holds s = 16 sb + 4 lq + e, t = own
+  const int own = 16 * tok + lr;
   v4f scores[QB];
   typename Frag<T>::V cf[NT];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) cf[n] = frag_along<T>(sC, NP, 16 * wave, 16 * n, lr, lq);
+  for (int n = 0; n < NT; ++n) cf[n] = frag_along<T>(sC, NP, 16 * tok, 16 * n, lr, lq);
 #pragma unroll
   for (int sb = 0; sb < QB; ++sb) {
     scores[sb] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    if (sb > wave) continue;
+    if (sb > tok) continue;
     if constexpr (kBF) {
 #pragma unroll
       for (int n = 0; n < NT; n += 2)
@@ -307,53 +335,61 @@ __global__ __launch_bounds__(kThreads) void ssd_outputs_kernel(ChunkParams p, Ch
   }
   __syncthreads();   // the scores' operands make room for the heads'
 
-  E* const sX = lds;
-  E* const sH = lds + kQ * XP;
+  E* const sX = sh.tiles;
+  E* const sH = sh.tiles + kQ * XP;
   [[maybe_unused]] E* const sHL = sH + kPB * NP;
   const int nt = (p.N + 15) / 16;
+  Pieces<T, kPB, kOutThreads> xv;
+  StatePieces<T, NMAX, kOutThreads> sv;
+  auto load = [&](int h, int p0) {
+    xv.template load<kVec>(rows_of<T>(p.x, k, h, p0, p.P), tid);
+    sv.template load<kVec>(state_rows(p.state, ((static_cast<int64_t>(c) * p.H + h) * p.P + p0) * p.N, min(kPB, p.P - p0), p.N), tid);
+  };
+  load(h0, 0);
   for (int i = 0; i < heads; ++i) {
     const int h = h0 + i;
-    // masked and weighted scores of the head, as operands
+    // weighted scores of the head, as operands; those above the diagonal are zero
     typename Frag<T>::V mf[QB];
-    const float la_t = sLa[i][own];
+    const float la_t = sh.la[i][own];
 #pragma unroll
     for (int sb = 0; sb < QB; ++sb) {
-      if (sb > wave) {
-        mf[sb] = tofrag<T>(0.0f, 0.0f, 0.0f, 0.0f);
-        continue;
-      }
-      const v4f la_s = *reinterpret_cast<const v4f*>(&sLa[i][16 * sb + 4 * lq]);
-      const v4f dl_s = *reinterpret_cast<const v4f*>(&sDl[i][16 * sb + 4 * lq]);
+      mf[sb] = tofrag<T>(0.0f, 0.0f, 0.0f, 0.0f);
+      if (sb > tok) continue;
+      const v4f la_s = *reinterpret_cast<const v4f*>(&sh.la[i][16 * sb + 4 * lq]);
+      const v4f dl_s = *reinterpret_cast<const v4f*>(&sh.dl[i][16 * sb + 4 * lq]);
       float m[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        m[e] = 16 * sb + 4 * lq + e <= own ? scores[sb][e] * __builtin_amdgcn_exp2f(la_t - la_s[e]) * dl_s[e] : 0.0f;
+      for (int e = 0; e < 4; ++e) m[e] = scores[sb][e] * __builtin_amdgcn_exp2f(la_t - la_s[e]) * dl_s[e];
+      if (sb == tok) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m[e] = 4 * lq + e <= lr ? m[e] : 0.0f;
+      }
       mf[sb] = tofrag<T>(m[0], m[1], m[2], m[3]);
     }
     const float ea = __builtin_amdgcn_exp2f(la_t), Dh = p.D ? p.D[h] : 0.0f;
     for (int p0 = 0; p0 < p.P; p0 += kPB) {
       const int cols = p.P - p0;
-      stage_rows<T, kPB, kThreads, kVec>(sX, XP, rows_of<T>(p.x, k, h, p0, p.P), tid);
-      // S_in: kPB rows of N states
-      const StateRows from = state_rows(p.state, ((static_cast<int64_t>(c) * p.H + h) * p.P + p0) * p.N, min(kPB, cols), p.N);
-      constexpr int kPer = NMAX / 4, kN = kPB * kPer / kThreads;
-#pragma unroll
-      for (int j = 0; j < kN; ++j) {
-        const int r = tid / kPer + j * (kThreads / kPer), n = tid % kPer * 4;
-        const v4u v = load_states<kVec>(from, r, n);
-        if constexpr (kBF) {
-          *reinterpret_cast<v2u*>(sH + r * NP + n) = v2u{highs(v[0], v[1]), highs(v[2], v[3])};
-          *reinterpret_cast<v2u*>(sHL + r * NP + n) = v2u{lows(v[0], v[1]), lows(v[2], v[3])};
-        } else {
-          *reinterpret_cast<v4u*>(sH + r * NP + n) = v;
-        }
-      }
+      xv.put(sX, XP, tid);
+      sv.put(sH, kBF ? sHL : sH, NP, tid);
       __syncthreads();
-      const bool live = own < k.len;
-      const int pts = (min(kPB, cols) + 15) / 16;
+      // what the end of this pass needs, and the next one
+      float z[kPB / 32][4], up[kPB / 32][4];
+      if (p.z.p) {
+        const Rows64 zr = rows_of<T>(p.z, k, h, p0, p.P);
 #pragma unroll
-      for (int pt = 0; pt < kPB / 16; ++pt) {
-        if (pt >= pts) continue;
+        for (int j = 0; j < kPB / 32; ++j) load4<T, kVec>(zr, own, 16 * (2 * j + half) + 4 * lq, z[j]);
+      }
+      if constexpr (kDz) {
+        const Rows64 er = rows_of<T>(p.dout, k, h, p0, p.P);
+#pragma unroll
+        for (int j = 0; j < kPB / 32; ++j) load4<T, kVec>(er, own, 16 * (2 * j + half) + 4 * lq, up[j]);
+      }
+      if (p0 + kPB < p.P) load(h, p0 + kPB);
+      else if (i + 1 < heads) load(h + 1, 0);
+#pragma unroll
+      for (int j = 0; j < kPB / 32; ++j) {
+        const int pt = 2 * j + half, c0 = 16 * pt + 4 * lq;
+        if (16 * pt >= cols) continue;
         v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -366,43 +402,35 @@ __global__ __launch_bounds__(kThreads) void ssd_outputs_kernel(ChunkParams p, Ch
         if constexpr (kBF) {
 #pragma unroll
           for (int sb = 0; sb < QB; sb += 2)
-            if (sb <= wave)
+            if (sb <= tok)
               acc = mma32(frag_down<T>(sX, XP, 16 * sb, 16 * pt, lr, lq), frag_down<T>(sX, XP, 16 * sb + 16, 16 * pt, lr, lq), mf[sb],
                           mf[sb + 1], acc);
         } else {
 #pragma unroll
           for (int sb = 0; sb < QB; ++sb)
-            if (sb <= wave) acc = mma16<T>(frag_down<T>(sX, XP, 16 * sb, 16 * pt, lr, lq), mf[sb], acc);
+            if (sb <= tok) acc = mma16<T>(frag_down<T>(sX, XP, 16 * sb, 16 * pt, lr, lq), mf[sb], acc);
         }
-        // token own, channels 16 pt + 4 lq ..
-        const int c0 = 16 * pt + 4 * lq;
-        if (!live || c0 >= cols) continue;
-        const T* const z = p.z.p ? static_cast<const T*>(p.z.p) + k.b * p.z.sb + (k.t0 + own) * p.z.ss + h * p.z.sh + p0 + c0 : nullptr;
-        const T* const e = kDz ? static_cast<const T*>(p.dout.p) + k.b * p.dout.sb + (k.t0 + own) * p.dout.ss + h * p.dout.sh + p0 + c0
-                               : nullptr;
-        T* const to = static_cast<T*>(kDz ? o.dz : o.out) + k.b * o.sb + (k.t0 + own) * o.ss + h * o.sh + p0 + c0;
-        const int left = cols - c0;
+        // token own, channels c0 ..
+        if (own >= k.len || c0 >= cols) continue;
         float y[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          y[j] = fmaf(Dh, Lds<T>::f(sX[own * XP + c0 + j]), acc[j]);
-          if (z && j < left) {
-            const float zv = io<T>::load(z + j);
-            if constexpr (kDz) {
-              const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-zv * kLog2e));
-              y[j] *= io<T>::load(e + j) * (s * fmaf(zv, 1.0f - s, 1.0f));
-            } else {
-              y[j] *= silu_f32(zv);
-            }
+        for (int e = 0; e < 4; ++e) {
+          y[e] = fmaf(Dh, Lds<T>::f(sX[own * XP + c0 + e]), acc[e]);
+          if constexpr (kDz) {
+            const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-z[j][e] * kLog2e));
+            y[e] *= up[j][e] * (s * fmaf(z[j][e], 1.0f - s, 1.0f));
+          } else if (p.z.p) {
+            y[e] *= silu_f32(z[j][e]);
           }
         }
+        T* const to = static_cast<T*>(kDz ? o.dz : o.out) + k.b * o.sb + (k.t0 + own) * o.ss + h * o.sh + p0 + c0;
         if constexpr (kVec) {
           if constexpr (kBF) *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
           else *reinterpret_cast<float4*>(to) = make_float4(y[0], y[1], y[2], y[3]);
         } else {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (j < left) io<T>::store(to + j, y[j]);
+          for (int e = 0; e < 4; ++e)
+            if (c0 + e < cols) io<T>::store(to + e, y[e]);
         }
       }
       __syncthreads();
@@ -421,7 +449,7 @@ template <typename T, int NMAX>
 void launch_outputs(const ChunkParams& p, const ChunkOut& o, hipStream_t stream) {
   const int grid = p.nc * p.G * p.blocks;
   auto go = [&](auto dz, auto vec) {
-    ssd_outputs_kernel<T, NMAX, dz.value, vec.value><<<grid, kThreads, 0, stream>>>(p, o, grid);
+    ssd_outputs_kernel<T, NMAX, dz.value, vec.value><<<grid, kOutThreads, 0, stream>>>(p, o, grid);
   };
   if (o.dz && p.vec) go(std::true_type{}, std::true_type{});
   else if (o.dz) go(std::true_type{}, std::false_type{});

@@ -192,6 +192,8 @@ int ssm_validate_ssd_bwd(const ssm_ssd_bwd_args* a) {
       dout{a->dout, a->dout_batch_stride, a->dout_seq_stride, a->dout_head_stride, H, P};
   const int64_t T = Bt * L;
   if (T > 0) {
+    // dx, contiguous, is written through such windows too
+    if (H * P * esz >= (int64_t{1} << 25)) return SSM_ERR_UNSUPPORTED;
     for (const Heads& t : {x, B, C, dout})
       if (const int st = check_heads(t, Bt, esz)) return st;
     if (a->z) {
