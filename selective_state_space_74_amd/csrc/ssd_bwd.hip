@@ -72,7 +72,7 @@ __global__ __launch_bounds__(kGradThreads, sizeof(T) == 2 && NMAX == 64 ? 4 : 2)
   constexpr int kB = kKeep ? kHead : 0, kC = kB + kQ * NP, kG = kKeep ? 0 : 2 * kQ * NP;
   // the small arrays first: their addresses are then offsets in the instruction
   struct Shared {
-    float dl[kMostHeads][kQ], la[kMostHeads][kQ];
+    float dl[kMostHeads][kQ], la[kMostHeads][kQ], A[kMostHeads], D[kMostHeads];
     float row[QB][kQ], col[2][kQ], c[2][kQ], r[2][kQ], diag[kQ], m[kQ], pairs[kGradThreads / 64];
     alignas(16) E tiles[kKeep ? kHead + 2 * kQ * NP : kHead > kEnds ? kHead : kEnds];
   };
@@ -93,6 +93,10 @@ __global__ __launch_bounds__(kGradThreads, sizeof(T) == 2 && NMAX == 64 ? 4 : 2)
     const Steps s = steps_of<T>(p, k, h0 + i, lane);
     sh.dl[i][lane] = s.delta;
     sh.la[i][lane] = s.la;
+    if (lane == 0) {
+      sh.A[i] = p.A[h0 + i];
+      sh.D[i] = p.D ? p.D[h0 + i] : 0.0f;
+    }
   }
   E* const sB = lds + kB;
   E* const sC = lds + kC;
@@ -231,7 +235,7 @@ __global__ __launch_bounds__(kGradThreads, sizeof(T) == 2 && NMAX == 64 ? 4 : 2)
     const int h = h0 + i;
     const float la_s = sh.la[i][own], dl_s = sh.dl[i][own];
     const float ew = __builtin_amdgcn_exp2f(sh.la[i][kQ - 1] - la_s), ea = __builtin_amdgcn_exp2f(la_s);
-    const float Dh = p.D ? p.D[h] : 0.0f;
+    const float Dh = sh.D[i];
     v4f M[kTiles];
 #pragma unroll
     for (int j = 0; j < kTiles; ++j) M[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
@@ -424,15 +428,14 @@ __global__ __launch_bounds__(kGradThreads, sizeof(T) == 2 && NMAX == 64 ? 4 : 2)
 #pragma unroll
       for (int w = 0; w < QB; ++w)
         if (w <= lane / 16) row += sh.row[w][lane];
-      const Steps st = steps_of<T>(p, k, h, lane);
-      const float dl = st.delta, cs = sh.c[0][lane] + sh.c[1][lane], cl = sh.col[0][lane] + sh.col[1][lane], r = sh.r[0][lane] + sh.r[1][lane];
+      const float dl = sh.dl[i][lane], cs = sh.c[0][lane] + sh.c[1][lane], cl = sh.col[0][lane] + sh.col[1][lane], r = sh.r[0][lane] + sh.r[1][lane];
       const float step = dl * (cl + cs) - row - r;
       float g0 = 0.0f;
 #pragma unroll
       for (int w = 0; w < kGradThreads / 64; ++w) g0 += sh.pairs[w];
       const float flow = wave_sum(r) + g0 + (wave_prefix_sum(step) - step);
-      float d = cl + sh.diag[lane] + cs + p.A[h] * flow;
-      d = lane < k.len ? d * st.slope : 0.0f;
+      float d = cl + sh.diag[lane] + cs + sh.A[i] * flow;
+      d = lane < k.len ? d * (p.softplus ? slope_of(dl) : 1.0f) : 0.0f;
       if (lane < k.len) io<T>::store(static_cast<T*>(q.ddt) + (k.b * p.L + k.t0 + lane) * p.H + h, d);
       const float da = wave_sum(dl * flow), db = wave_sum(d), dd = wave_sum(sh.m[lane]);
       if (lane < 3) q.parts[(static_cast<int64_t>(lane) * p.H + h) * p.nc + c] = lane == 0 ? da : lane == 1 ? db : dd;

@@ -90,27 +90,44 @@ __device__ __forceinline__ Rows64 rows_of(const TokenTensor& t, const Chunk& k, 
   return w;
 }
 
-// Step sizes of a chunk, one token a lane: Delta (0 past the end), the sums of
-// A Delta up to each token in units of log 2, and the derivative of Delta.
+// Step sizes of a chunk, one token a lane: Delta (0 past the end), and the sums of
+// A Delta up to each token in units of log 2.
 struct Steps {
-  float delta, la, slope;
+  float delta, la;
 };
+// What they take of a head, read once: a load within a loop would wait for those
+// ahead of it.
+struct StepHead {
+  float a2, bias;
+  int softplus;
+};
+__device__ __forceinline__ StepHead step_head(const ChunkParams& p, int h) {
+  return StepHead{p.A[h] * kLog2e, p.bias ? p.bias[h] : 0.0f, p.softplus};
+}
+// v: the lane's step before its bias.
+__device__ __forceinline__ Steps steps_from(const StepHead& q, float v, int len, int lane) {
+  Steps s;
+  v += q.bias;
+  s.delta = lane < len ? (q.softplus ? softplus_close_f32(v) : v) : 0.0f;
+  s.la = wave_prefix_sum(s.delta) * q.a2;
+  return s;
+}
 template <typename T>
 __device__ __forceinline__ Steps steps_of(const ChunkParams& p, const Chunk& k, int h, int lane) {
-  Steps s;
-  const bool in = lane < k.len;
   float v = 0.0f;
-  if (in) v = io<T>::load(static_cast<const T*>(p.dt) + k.b * p.dtb + (k.t0 + lane) * p.dts + h);
-  if (p.bias) v += p.bias[h];
-  float d = v;
-  s.slope = 1.0f;
-  if (p.softplus) {
-    d = softplus_close_f32(v);
-    s.slope = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-v * kLog2e));
-  }
-  s.delta = in ? d : 0.0f;
-  s.la = wave_prefix_sum(s.delta) * (p.A[h] * kLog2e);
-  return s;
+  if (lane < k.len) v = io<T>::load(static_cast<const T*>(p.dt) + k.b * p.dtb + (k.t0 + lane) * p.dts + h);
+  return steps_from(step_head(p, h), v, k.len, lane);
+}
+// softplus'(v) from Delta = softplus(v): sigmoid(v) = 1 - e^-Delta, by its series where
+// the difference would cancel (Delta < 1/4: the first term left out is below 2^-26 of it).
+__device__ __forceinline__ float slope_of(float delta) {
+  float s = fmaf(delta, -1.0f / 5040, 1.0f / 720);
+  s = fmaf(-delta, s, 1.0f / 120);
+  s = fmaf(-delta, s, 1.0f / 24);
+  s = fmaf(-delta, s, 1.0f / 6);
+  s = fmaf(-delta, s, 0.5f);
+  s = delta * fmaf(-delta, s, 1.0f);
+  return delta < 0.25f ? s : 1.0f - __builtin_amdgcn_exp2f(-delta * kLog2e);
 }
 __device__ __forceinline__ float lane_value(float v, int lane) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));

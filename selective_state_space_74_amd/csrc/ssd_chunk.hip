@@ -82,6 +82,53 @@ __global__ __launch_bounds__(kTableThreads) void chunk_table_kernel(const int32_
 
 // ---- what a chunk adds to the state ------------------------------------------------
 
+// Rows of x (or of dout, gated) times their weights into LDS, for bf16 in two parts
+// so that the sums carry 16 bits.
+template <typename T, bool kGate, int kN, typename W>
+__device__ __forceinline__ void put_weighted(typename Lds<T>::E* sX, typename Lds<T>::E* sXL, int pitch,
+                                             const Pieces<T, kPB, kN>& x, [[maybe_unused]] const Pieces<T, kPB, kN>& z, W&& weight,
+                                             int tid) {
+  using Tokens = Pieces<T, kPB, kN>;
+#pragma unroll
+  for (int j = 0; j < Tokens::kN; ++j) {
+    const int r = tid / Tokens::kPer + j * Tokens::kStep, at = r * pitch + tid % Tokens::kPer * kPiece<T>;
+    const float w = weight(r);
+    uint32_t s[kPiece<T>];
+#pragma unroll
+    for (int e = 0; e < kPiece<T>; ++e) {
+      float f = piece_f32<T>(x.v[j], e) * w;
+      if constexpr (kGate) f *= silu_f32(piece_f32<T>(z.v[j], e));
+      s[e] = sizeof(T) == 2 ? split_bf16(f) : __float_as_uint(f);
+    }
+    if constexpr (sizeof(T) == 2) {
+      *reinterpret_cast<v4u*>(sX + at) = v4u{highs(s[0], s[1]), highs(s[2], s[3]), highs(s[4], s[5]), highs(s[6], s[7])};
+      *reinterpret_cast<v4u*>(sXL + at) = v4u{lows(s[0], s[1]), lows(s[2], s[3]), lows(s[4], s[5]), lows(s[6], s[7])};
+    } else {
+      *reinterpret_cast<v4u*>(sX + at) = v4u{s[0], s[1], s[2], s[3]};
+    }
+  }
+}
+
+// acc[n] += the sums over a chunk's tokens (kb blocks of 16) for the states' tiles n =
+// first, first + step .. and the channels' tile pt; lane: channel lr, states 4 lq ..
+template <typename T, int NT>
+__device__ __forceinline__ void add_tiles(v4f (&acc)[NT], const typename Lds<T>::E* sX, const typename Lds<T>::E* sXL, int XP,
+                                          const typename Lds<T>::E* sM, int NP, int kb, int pt, int first, int step, int nt,
+                                          int lr, int lq) {
+  for (int q = 0; q < kb; ++q) {
+    const auto xf = frag_down<T>(sX, XP, 16 * q, 16 * pt, lr, lq);
+    [[maybe_unused]] auto xl = xf;
+    if constexpr (sizeof(T) == 2) xl = frag_down<T>(sXL, XP, 16 * q, 16 * pt, lr, lq);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      if (n % step != first || n >= nt) continue;
+      const auto mf = frag_down<T>(sM, NP, 16 * q, 16 * n, lr, lq);
+      if constexpr (sizeof(T) == 2) acc[n] = mma32(mf, mf, xf, xl, acc[n]);
+      else acc[n] = mma16<T>(mf, xf, acc[n]);
+    }
+  }
+}
+
 // Workgroup: (chunk, heads of one group, direction).  B (C backward) of the chunk
 // is staged once; then for each head the rows x_s (dy_t) times their weight, split
 // in two for bf16 so that the sums carry 16 bits.  A wavefront owns 16 channels of
@@ -127,26 +174,10 @@ __global__ __launch_bounds__(kThreads) void ssd_states_kernel(ChunkParams p, int
   load(0, 0);
   for (int i = 0; i < heads; ++i) {
     for (int p0 = 0; p0 < p.P; p0 += kPB) {
-      const int cols = p.P - p0, col = tid % Tokens::kPer * kPiece<T>;
-#pragma unroll
-      for (int j = 0; j < Tokens::kN; ++j) {
-        const int r = tid / Tokens::kPer + j * Tokens::kStep;
-        const v4u v = xv.v[j];
-        const float w = sW[i][r];
-        uint32_t s[kPiece<T>];
-#pragma unroll
-        for (int e = 0; e < kPiece<T>; ++e) {
-          float f = piece_f32<T>(v, e) * w;
-          if (gate) f *= silu_f32(piece_f32<T>(zv.v[j], e));
-          s[e] = kBF ? split_bf16(f) : __float_as_uint(f);
-        }
-        if constexpr (kBF) {
-          *reinterpret_cast<v4u*>(sX + r * XP + col) = v4u{highs(s[0], s[1]), highs(s[2], s[3]), highs(s[4], s[5]), highs(s[6], s[7])};
-          *reinterpret_cast<v4u*>(sXL + r * XP + col) = v4u{lows(s[0], s[1]), lows(s[2], s[3]), lows(s[4], s[5]), lows(s[6], s[7])};
-        } else {
-          *reinterpret_cast<v4u*>(sX + r * XP + col) = v4u{s[0], s[1], s[2], s[3]};
-        }
-      }
+      const int cols = p.P - p0;
+      auto weight = [&](int r) { return sW[i][r]; };
+      if (gate) put_weighted<T, true>(sX, sXL, XP, xv, zv, weight, tid);
+      else put_weighted<T, false>(sX, sXL, XP, xv, zv, weight, tid);
       __syncthreads();
       // the next pass's loads are under way while this one is computed
       if (p0 + kPB < p.P) load(i, p0 + kPB);
@@ -157,18 +188,7 @@ __global__ __launch_bounds__(kThreads) void ssd_states_kernel(ChunkParams p, int
       v4f acc[NT];
 #pragma unroll
       for (int n = 0; n < NT; ++n) acc[n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-      for (int q = 0; q < kb; ++q) {
-        const auto xf = frag_down<T>(sX, XP, 16 * q, 16 * pt, lr, lq);
-        [[maybe_unused]] auto xl = xf;
-        if constexpr (kBF) xl = frag_down<T>(sXL, XP, 16 * q, 16 * pt, lr, lq);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          if (n % step != first || n >= nt) continue;
-          const auto mf = frag_down<T>(sM, NP, 16 * q, 16 * n, lr, lq);
-          if constexpr (kBF) acc[n] = mma32(mf, mf, xf, xl, acc[n]);
-          else acc[n] = mma16<T>(mf, xf, acc[n]);
-        }
-      }
+      add_tiles<T, NT>(acc, sX, sXL, XP, sM, NP, kb, pt, first, step, nt, lr, lq);
       // lane: channel 16 pt + lr, states 16 n + 4 lq ..
       const int pp = p0 + 16 * pt + lr;
       if (pp < p.P) {
@@ -252,6 +272,149 @@ __global__ __launch_bounds__(kThreads) void ssd_carry_kernel(CarryParams p) {
   }
 }
 
+// ---- both at once, where whole sequences keep the machine busy -------------------------
+
+constexpr int kWalkThreads = 512;
+
+struct WalkParams {
+  const float* from[2];
+  float* to[2];
+  int split, cols;   // workgroups of a head, channels of one
+};
+
+// Workgroup: (batch row, head, some of its channels, direction).  It goes along the
+// row's chunks with the state in registers, so that the states are written once and
+// not read and written again by the carry: loads are two chunks ahead, LDS in two
+// halves makes do with one barrier a chunk.
+template <typename T, int NMAX, bool kVec>
+__global__ __launch_bounds__(kWalkThreads) void ssd_walk_kernel(ChunkParams p, WalkParams q) {
+  using E = typename Lds<T>::E;
+  constexpr bool kBF = sizeof(T) == 2;
+  constexpr int kPad = 16 / sizeof(E), NP = NMAX + kPad, XP = kPB + kPad, NT = NMAX / 16;
+  constexpr int kHalf = kQ * NP + (kBF ? 2 : 1) * kQ * XP;
+  __shared__ __align__(16) E lds[2 * kHalf];
+  const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lq = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int dir = blockIdx.y, h = static_cast<int>(blockIdx.x / q.split) % p.H;
+  const int b = static_cast<int>(blockIdx.x / q.split) / p.H, p0 = static_cast<int>(blockIdx.x % q.split) * q.cols;
+  const int last = min(p.P, p0 + q.cols);   // channels p0 .. last - 1
+  const bool gate = dir && p.z.p;
+  const TokenTensor& x = dir ? p.dout : p.x;
+  const TokenTensor& m = dir ? p.C : p.B;
+  uint32_t* const state = dir ? p.dstate : p.state;
+  const int g = h / p.per_group, nt = (p.N + 15) / 16;
+  const StepHead steps = step_head(p, h);
+  // channels' tiles (1, 2 or 4) and the wavefronts that share one, at least two: tiles
+  // of states first, first + step ..; lane: channel 16 pt + lr, states 16 n + 4 lq ..
+  const int pts = last - p0 > 32 ? 4 : last - p0 > 16 ? 2 : 1;
+  const int pt = wave % pts, first = wave / pts, step = kWalkThreads / 64 / pts;
+  constexpr int kMost = NT / 2;
+  const int pp = p0 + 16 * pt + lr;
+  // the lane's place in a head's state, or none
+  auto place = [&](int j, int e) {
+    const int s = 16 * (first + step * j) + 4 * lq + e;
+    return pp < last && s < p.N ? (pp * p.N + s) * 4u : kNowhere;
+  };
+  auto head_of = [&](const float* t) {   // h0 and the like
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(t + (static_cast<int64_t>(b) * p.H + h) * p.P * p.N), 0, p.P * p.N * 4,
+                                             kRsrcWord3);
+  };
+
+  v4f acc[kMost];
+#pragma unroll
+  for (int j = 0; j < kMost; ++j) {
+    acc[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    if (q.from[dir]) {
+      const __amdgpu_buffer_rsrc_t from = head_of(q.from[dir]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[j][e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(from, place(j, e), 0, 0));
+    }
+  }
+  // what a chunk needs, loaded two chunks ahead; past the row its last chunk again.
+  // Loads and stores are issued whether or not a lane has any (their offsets then
+  // lie nowhere): a wait can then count them and leave the latest in flight.
+  struct Ahead {
+    Pieces<T, kPB, kWalkThreads> x, z;
+    Pieces<T, NMAX, kWalkThreads> m;
+    uint32_t raw;   // the lane's step, before its bias
+    int len;
+  } ahead[2];
+  auto load = [&](int i, Ahead& a) {
+    i = min(i, p.per_row - 1);
+    const int t0 = (dir ? p.per_row - 1 - i : i) * kQ;
+    const Chunk k{b, t0, min(kQ, p.L - t0)};
+    a.len = k.len;
+    const T* const dt = static_cast<const T*>(p.dt) + k.b * p.dtb + k.t0 * p.dts + h;
+    a.raw = Elem<T>::load(__builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(dt), 0, 0x7fffffff, kRsrcWord3),
+                          lane < k.len ? lane * static_cast<uint32_t>(p.dts) * static_cast<uint32_t>(sizeof(T)) : kNowhere);
+    a.x.template load<kVec>(rows_of<T>(x, k, h, p0, last), tid);
+    if (gate) a.z.template load<kVec>(rows_of<T>(p.z, k, h, p0, last), tid);
+    a.m.template load<kVec>(rows_of<T>(m, k, g, 0, p.N), tid);
+  };
+  auto chunk = [&](int i, Ahead& a) {
+    E* const sM = lds + (i % 2) * kHalf;
+    E* const sX = sM + kQ * NP;
+    [[maybe_unused]] E* const sXL = sX + kQ * XP;
+    const int len = a.len;
+    const Steps s = steps_from(steps, Elem<T>::f32(a.raw), len, lane);
+    const float end = lane_value(s.la, 63);
+    const float w = dir ? __builtin_amdgcn_exp2f(s.la) : __builtin_amdgcn_exp2f(end - s.la) * s.delta;
+    a.m.put(sM, NP, tid);
+    auto weight = [&](int r) { return __shfl(w, r, 64); };
+    if (gate) put_weighted<T, true>(sX, sXL, XP, a.x, a.z, weight, tid);
+    else put_weighted<T, false>(sX, sXL, XP, a.x, a.z, weight, tid);
+    __syncthreads();
+    load(i + 2, a);
+    // the state that enters the chunk
+    const int64_t c = static_cast<int64_t>(b) * p.per_row + (dir ? p.per_row - 1 - i : i);
+    const __amdgpu_buffer_rsrc_t to =
+        __builtin_amdgcn_make_buffer_rsrc(state + (c * p.H + h) * p.P * p.N, 0, p.P * p.N * 4, kRsrcWord3);
+    const float through = __builtin_amdgcn_exp2f(end);
+#pragma unroll
+    for (int j = 0; j < kMost; ++j) {
+      v4u v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = kBF ? split_bf16(acc[j][e]) : __float_as_uint(acc[j][e]);
+      if constexpr (kVec) {
+        __builtin_amdgcn_raw_buffer_store_b128(v, to, place(j, 0), 0, 0);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) __builtin_amdgcn_raw_buffer_store_b32(v[e], to, place(j, e), 0, 0);
+      }
+      acc[j] *= through;
+    }
+    const int kb = (len + 15) / 16;
+#pragma unroll
+    for (int t = 0; t < kQ / 16; ++t) {
+      if (t >= kb) continue;
+      const auto xf = frag_down<T>(sX, XP, 16 * t, 16 * pt, lr, lq);
+      [[maybe_unused]] auto xl = xf;
+      if constexpr (kBF) xl = frag_down<T>(sXL, XP, 16 * t, 16 * pt, lr, lq);
+#pragma unroll
+      for (int j = 0; j < kMost; ++j) {
+        const int n = first + step * j;
+        if (n >= nt) continue;
+        const auto mf = frag_down<T>(sM, NP, 16 * t, 16 * n, lr, lq);
+        if constexpr (kBF) acc[j] = mma32(mf, mf, xf, xl, acc[j]);
+        else acc[j] = mma16<T>(mf, xf, acc[j]);
+      }
+    }
+  };
+  load(0, ahead[0]);
+  load(1, ahead[1]);
+  for (int i = 0; i < p.per_row; i += 2) {
+    chunk(i, ahead[0]);
+    if (i + 1 < p.per_row) chunk(i + 1, ahead[1]);
+  }
+  if (q.to[dir]) {
+    const __amdgpu_buffer_rsrc_t to = head_of(q.to[dir]);
+#pragma unroll
+    for (int j = 0; j < kMost; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(acc[j][e]), to, place(j, e), 0, 0);
+  }
+}
+
 // ---- outputs ------------------------------------------------------------------------
 
 // Workgroup: (chunk, heads of one group); two of its 8 wavefronts share 16 of the
@@ -291,7 +454,7 @@ __global__ __launch_bounds__(kOutThreads, 4) void ssd_outputs_kernel(ChunkParams
   constexpr int kPad = 16 / sizeof(E), NP = NMAX + kPad, XP = kPB + kPad, NT = NMAX / 16, QB = kQ / 16;
   constexpr int kScores = 2 * kQ * NP, kHead = kQ * XP + (kBF ? 2 : 1) * kPB * NP;
   struct Shared {
-    float dl[kMostHeads][kQ], la[kMostHeads][kQ];
+    float dl[kMostHeads][kQ], la[kMostHeads][kQ], D[kMostHeads];
     alignas(16) E tiles[kScores > kHead ? kScores : kHead];
   };
   __shared__ __align__(16) Shared sh;
@@ -307,6 +470,7 @@ __global__ __launch_bounds__(kOutThreads, 4) void ssd_outputs_kernel(ChunkParams
     const Steps s = steps_of<T>(p, k, h0 + i, lane);
     sh.dl[i][lane] = s.delta;
     sh.la[i][lane] = s.la;
+    if (lane == 0) sh.D[i] = p.D ? p.D[h0 + i] : 0.0f;
   }
   E* const sB = sh.tiles;
   E* const sC = sh.tiles + kQ * NP;
@@ -366,7 +530,7 @@ __global__ __launch_bounds__(kOutThreads, 4) void ssd_outputs_kernel(ChunkParams
       }
       mf[sb] = tofrag<T>(m[0], m[1], m[2], m[3]);
     }
-    const float ea = __builtin_amdgcn_exp2f(la_t), Dh = p.D ? p.D[h] : 0.0f;
+    const float ea = __builtin_amdgcn_exp2f(la_t), Dh = sh.D[i];
     for (int p0 = 0; p0 < p.P; p0 += kPB) {
       const int cols = p.P - p0;
       xv.put(sX, XP, tid);
@@ -478,8 +642,35 @@ hipError_t launch_chunk_table(const int32_t* cu, int64_t L, int64_t nseq, int64_
   return hipGetLastError();
 }
 
+namespace {
+
+template <typename T, int NMAX>
+void launch_walk(const ChunkParams& p, const WalkParams& q, bool backward, int64_t rows, hipStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(rows * p.H * q.split), backward ? 2 : 1);
+  if (p.vec) ssd_walk_kernel<T, NMAX, true><<<grid, kWalkThreads, 0, stream>>>(p, q);
+  else ssd_walk_kernel<T, NMAX, false><<<grid, kWalkThreads, 0, stream>>>(p, q);
+}
+
+}  // namespace
+
 hipError_t launch_chunk_states(const ChunkParams& p, bool bf16, bool backward, int64_t nseq, const float* h0, float* last,
                                const float* dlast, float* dh0, hipStream_t stream) {
+  // batch rows of equal length: a workgroup goes along a whole row where two
+  // workgroups a compute unit remain, a head's channels in up to 4 parts.  Measured
+  // on gradients, 8 x 2048 x 32 x 64 x 64 bf16: 118 us, and 88 + 84 chunk by chunk; with
+  // the channels in two parts (1024 workgroups) 194.
+  if (!p.table && p.nc > 0) {
+    WalkParams q{{h0, dlast}, {last, dh0}, 0, 0};
+    const int64_t heads = nseq * p.H * (backward ? 2 : 1);
+    for (q.cols = kPB; q.cols > 16 && heads * ((p.P + q.cols - 1) / q.cols) < 512;) q.cols /= 2;
+    q.split = (p.P + q.cols - 1) / q.cols;
+    if (heads * q.split >= 512) {
+      if (!bf16) launch_walk<float, 64>(p, q, backward, nseq, stream);
+      else if (p.N > 64) launch_walk<uint16_t, 128>(p, q, backward, nseq, stream);
+      else launch_walk<uint16_t, 64>(p, q, backward, nseq, stream);
+      return hipGetLastError();
+    }
+  }
   if (p.nc > 0) {
     if (!bf16) launch_states<float, 64>(p, backward, stream);
     else if (p.N > 64) launch_states<uint16_t, 128>(p, backward, stream);

@@ -10,29 +10,36 @@ constexpr int kConvThreads = 256;
 constexpr int kConvLanes = 16;                              // runs of channels side by side in a workgroup
 constexpr int kConvRuns = kConvThreads / kConvLanes;        // runs of tokens in a workgroup
 constexpr int kConvBounds = 1024;                           // sequence bounds held in LDS
+constexpr int kConvV = 4;                                   // channels of a lane: 8 bytes of bf16, 16 of fp32
 
-// V consecutive channels of a token as fp32.  kVec: the row allows one access of
-// V elements; else element by element, nv of them real.
+// V consecutive channels of a token.  kVec: the row allows one access of V elements;
+// else element by element, nv of them real.
+template <typename T, int V>
+struct alignas(sizeof(T) * V) Channels {
+  T e[V];
+  __device__ __forceinline__ void widen(float (&v)[V]) const {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = io<T>::load(&e[i]);
+  }
+};
 template <typename T, int V, bool kVec>
-__device__ __forceinline__ void load_channels(const T* p, int nv, float (&v)[V]) {
+__device__ __forceinline__ Channels<T, V> load_channels(const T* p, int nv) {
   if constexpr (kVec) {
-    struct alignas(sizeof(T) * V) Pack { T e[V]; };
-    const Pack q = *reinterpret_cast<const Pack*>(p);
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = io<T>::load(&q.e[i]);
+    return *reinterpret_cast<const Channels<T, V>*>(p);
   } else {
+    Channels<T, V> q;
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = i < nv ? io<T>::load(p + i) : 0.0f;
+    for (int i = 0; i < V; ++i) q.e[i] = i < nv ? p[i] : T{0};
+    return q;
   }
 }
 template <typename T, int V, bool kVec>
 __device__ __forceinline__ void store_channels(T* p, int nv, const float (&v)[V]) {
   if constexpr (kVec) {
-    struct alignas(sizeof(T) * V) Pack { T e[V]; };
-    Pack q;
+    Channels<T, V> q;
 #pragma unroll
     for (int i = 0; i < V; ++i) io<T>::store(&q.e[i], v[i]);
-    *reinterpret_cast<Pack*>(p) = q;
+    *reinterpret_cast<Channels<T, V>*>(p) = q;
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i)
