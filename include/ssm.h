@@ -706,15 +706,16 @@ typedef struct ssm_ssd_update_args {
  * Sizes: seqlen >= 0 and below 2^31 - 64; nheads, headdim, dstate >= 1; ngroups 0
  * or 1 (one group) or a divisor of nheads; dstate at most 128 for bf16 IO and 64
  * for fp32 IO; nseq below 2^29; nheads * headdim * dstate below 2^31 and
- * (seqlen / 64 + min(nseq, seqlen)) * nheads below 2^24; (63 * seq_stride + inner
+ * (seqlen / 64 + min(nseq, seqlen)) * nheads below 2^23; (63 * seq_stride + inner
  * size) * element size below 2^31 for x, z, B, C and out, as in ssm_ssd_args
  * (SSM_ERR_UNSUPPORTED past that).
  * A NaN or an infinity in a token's inputs stays within its sequence, but may
  * reach earlier tokens of its chunk (64 tokens from the sequence's first on).
  * Precision: fp32 accumulation, states and decays.  With bf16 IO the products run
  * on bf16 operands: the masked chunk scores are rounded to bf16, while the states
- * and what is summed into them enter as a bf16 value plus its bf16 remainder (16
- * bits; last_state is good to about 2^-17); with fp32 IO every product is fp32.
+ * enter as a bf16 value plus its bf16 remainder (16 bits), and what is summed into
+ * them as three bf16 parts (24 bits: last_state is as good as fp32 sums are); with
+ * fp32 IO every product is fp32.
  * Aliasing: out, last_state and the workspace must not overlap any input or each
  * other, except that last_state may be exactly h0.
  * Workspace: device scratch owned by the caller, 16-byte aligned, of at least
@@ -759,8 +760,9 @@ typedef struct ssm_ssd_packed_args {
  *   dh0         : like h0, fp32; NULL: not wanted.
  * Every output is the same bits from run to run.
  * Sizes as in ssm_ssd_packed_args, with batch * ceil(seqlen / 64) in place of its
- * count of chunks without cu_seqlens.  As in ssm_ssd_args, 64 tokens of a tensor's
- * rows are reached through 31-bit byte windows.
+ * count of chunks without cu_seqlens.  64 tokens of a tensor's rows are reached
+ * through 31-bit byte windows: the limit on strides holds for x, z, B, C and dout,
+ * and nheads * headdim * element size is below 2^25 (rows of dx).
  * Precision: as there; the gradients of dt, A, dt_bias and D come from products
  * whose operands carry 16 bits at least.
  * Aliasing: no output may overlap an input, another output or the workspace.

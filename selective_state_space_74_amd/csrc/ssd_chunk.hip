@@ -82,11 +82,12 @@ __global__ __launch_bounds__(kTableThreads) void chunk_table_kernel(const int32_
 
 // ---- what a chunk adds to the state ------------------------------------------------
 
-// Rows of x (or of dout, gated) times their weights into LDS, for bf16 in two parts
-// so that the sums carry 16 bits.
+// Rows of x (or of dout, gated) times their weights into LDS, for bf16 in three parts
+// (kParts arrays, one behind the other): the products are then of all 24 bits, and the last
+// state and dh0 as exact as fp32 sums are.  With two parts, 16 bits, they were 2e-6 off.
+template <typename T> constexpr int kParts = sizeof(T) == 2 ? 3 : 1;
 template <typename T, bool kGate, int kN, typename W>
-__device__ __forceinline__ void put_weighted(typename Lds<T>::E* sX, typename Lds<T>::E* sXL, int pitch,
-                                             const Pieces<T, kPB, kN>& x, [[maybe_unused]] const Pieces<T, kPB, kN>& z, W&& weight,
+__device__ __forceinline__ void put_weighted(typename Lds<T>::E* sX, int pitch, const Pieces<T, kPB, kN>& x, [[maybe_unused]] const Pieces<T, kPB, kN>& z, W&& weight,
                                              int tid) {
   using Tokens = Pieces<T, kPB, kN>;
 #pragma unroll
@@ -94,54 +95,55 @@ __device__ __forceinline__ void put_weighted(typename Lds<T>::E* sX, typename Ld
     const int r = tid / Tokens::kPer + j * Tokens::kStep, at = r * pitch + tid % Tokens::kPer * kPiece<T>;
     const float w = weight(r);
     uint32_t s[kPiece<T>];
+    [[maybe_unused]] uint32_t mid[kPiece<T>], rest[kPiece<T>];
 #pragma unroll
     for (int e = 0; e < kPiece<T>; ++e) {
       float f = piece_f32<T>(x.v[j], e) * w;
       if constexpr (kGate) f *= silu_f32(piece_f32<T>(z.v[j], e));
-      s[e] = sizeof(T) == 2 ? split_bf16(f) : __float_as_uint(f);
+      s[e] = __float_as_uint(f);
+      if constexpr (sizeof(T) == 2) {   // 8 bits of the significand each, cut off and not rounded: every difference is exact
+        f -= __uint_as_float(s[e] & 0xffff0000u);
+        mid[e] = __float_as_uint(f);
+        rest[e] = __float_as_uint(f - __uint_as_float(mid[e] & 0xffff0000u));
+      }
     }
     if constexpr (sizeof(T) == 2) {
-      *reinterpret_cast<v4u*>(sX + at) = v4u{highs(s[0], s[1]), highs(s[2], s[3]), highs(s[4], s[5]), highs(s[6], s[7])};
-      *reinterpret_cast<v4u*>(sXL + at) = v4u{lows(s[0], s[1]), lows(s[2], s[3]), lows(s[4], s[5]), lows(s[6], s[7])};
+      auto put = [&](int part, const uint32_t (&v)[kPiece<T>]) {
+        *reinterpret_cast<v4u*>(sX + part * kQ * pitch + at) = v4u{highs(v[0], v[1]), highs(v[2], v[3]), highs(v[4], v[5]), highs(v[6], v[7])};
+      };
+      put(0, s);
+      put(1, mid);
+      put(2, rest);
     } else {
       *reinterpret_cast<v4u*>(sX + at) = v4u{s[0], s[1], s[2], s[3]};
     }
   }
 }
 
-// acc[n] += the sums over a chunk's tokens (kb blocks of 16) for the states' tiles n =
-// first, first + step .. and the channels' tile pt; lane: channel lr, states 4 lq ..
-template <typename T, int NT>
-__device__ __forceinline__ void add_tiles(v4f (&acc)[NT], const typename Lds<T>::E* sX, const typename Lds<T>::E* sXL, int XP,
-                                          const typename Lds<T>::E* sM, int NP, int kb, int pt, int first, int step, int nt,
-                                          int lr, int lq) {
-  for (int q = 0; q < kb; ++q) {
-    const auto xf = frag_down<T>(sX, XP, 16 * q, 16 * pt, lr, lq);
-    [[maybe_unused]] auto xl = xf;
-    if constexpr (sizeof(T) == 2) xl = frag_down<T>(sXL, XP, 16 * q, 16 * pt, lr, lq);
+// A tile of those rows, 16 tokens by 16 channels, and its product with B's (C's).
+template <typename T>
+struct WeightedFrag {
+  typename Frag<T>::V v[kParts<T>];
+  __device__ __forceinline__ WeightedFrag(const typename Lds<T>::E* sX, int pitch, int k0, int c0, int lr, int lq) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      if (n % step != first || n >= nt) continue;
-      const auto mf = frag_down<T>(sM, NP, 16 * q, 16 * n, lr, lq);
-      if constexpr (sizeof(T) == 2) acc[n] = mma32(mf, mf, xf, xl, acc[n]);
-      else acc[n] = mma16<T>(mf, xf, acc[n]);
-    }
+    for (int i = 0; i < kParts<T>; ++i) v[i] = frag_down<T>(sX + i * kQ * pitch, pitch, k0, c0, lr, lq);
   }
-}
+  __device__ __forceinline__ v4f times(const typename Frag<T>::V& mf, v4f acc) const {
+    if constexpr (sizeof(T) == 2) return mma32(mf, mf, v[0], v[1], mma32(mf, mf, v[2], typename Frag<T>::V{}, acc));
+    else return mma16<T>(mf, v[0], acc);
+  }
+};
 
 // Workgroup: (chunk, heads of one group, direction).  B (C backward) of the chunk
-// is staged once; then for each head the rows x_s (dy_t) times their weight, split
-// in two for bf16 so that the sums carry 16 bits.  A wavefront owns 16 channels of
+// is staged once; then for each head the rows x_s (dy_t) times their weight.  A wavefront owns 16 channels of
 // the state (fewer channels: a share of its columns).  Bound by memory: the states
 // written are 4 N bytes for 2 x (64 tokens) bytes of x read.
 template <typename T, int NMAX, bool kVec>
 __global__ __launch_bounds__(kThreads) void ssd_states_kernel(ChunkParams p, int grid) {
   using E = typename Lds<T>::E;
-  constexpr bool kBF = sizeof(T) == 2;
   constexpr int kPad = 16 / sizeof(E), NP = NMAX + kPad, XP = kPB + kPad, NT = NMAX / 16;
   __shared__ __align__(16) E sM[kQ * NP];
-  __shared__ __align__(16) E sX[kQ * XP];
-  __shared__ __align__(16) E sXL[kBF ? kQ * XP : 1];
+  __shared__ __align__(16) E sX[kParts<T> * kQ * XP];
   __shared__ float sW[kMostHeads][kQ];
   const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lq = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -176,8 +178,8 @@ __global__ __launch_bounds__(kThreads) void ssd_states_kernel(ChunkParams p, int
     for (int p0 = 0; p0 < p.P; p0 += kPB) {
       const int cols = p.P - p0;
       auto weight = [&](int r) { return sW[i][r]; };
-      if (gate) put_weighted<T, true>(sX, sXL, XP, xv, zv, weight, tid);
-      else put_weighted<T, false>(sX, sXL, XP, xv, zv, weight, tid);
+      if (gate) put_weighted<T, true>(sX, XP, xv, zv, weight, tid);
+      else put_weighted<T, false>(sX, XP, xv, zv, weight, tid);
       __syncthreads();
       // the next pass's loads are under way while this one is computed
       if (p0 + kPB < p.P) load(i, p0 + kPB);
@@ -188,7 +190,14 @@ __global__ __launch_bounds__(kThreads) void ssd_states_kernel(ChunkParams p, int
       v4f acc[NT];
 #pragma unroll
       for (int n = 0; n < NT; ++n) acc[n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-      add_tiles<T, NT>(acc, sX, sXL, XP, sM, NP, kb, pt, first, step, nt, lr, lq);
+      for (int q = 0; q < kb; ++q) {
+        const WeightedFrag<T> xf(sX, XP, 16 * q, 16 * pt, lr, lq);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if (n % step != first || n >= nt) continue;
+          acc[n] = xf.times(frag_down<T>(sM, NP, 16 * q, 16 * n, lr, lq), acc[n]);
+        }
+      }
       // lane: channel 16 pt + lr, states 16 n + 4 lq ..
       const int pp = p0 + 16 * pt + lr;
       if (pp < p.P) {
@@ -291,7 +300,7 @@ __global__ __launch_bounds__(kWalkThreads) void ssd_walk_kernel(ChunkParams p, W
   using E = typename Lds<T>::E;
   constexpr bool kBF = sizeof(T) == 2;
   constexpr int kPad = 16 / sizeof(E), NP = NMAX + kPad, XP = kPB + kPad, NT = NMAX / 16;
-  constexpr int kHalf = kQ * NP + (kBF ? 2 : 1) * kQ * XP;
+  constexpr int kHalf = kQ * NP + kParts<T> * kQ * XP;
   __shared__ __align__(16) E lds[2 * kHalf];
   const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lq = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -354,15 +363,14 @@ __global__ __launch_bounds__(kWalkThreads) void ssd_walk_kernel(ChunkParams p, W
   auto chunk = [&](int i, Ahead& a) {
     E* const sM = lds + (i % 2) * kHalf;
     E* const sX = sM + kQ * NP;
-    [[maybe_unused]] E* const sXL = sX + kQ * XP;
     const int len = a.len;
     const Steps s = steps_from(steps, Elem<T>::f32(a.raw), len, lane);
     const float end = lane_value(s.la, 63);
     const float w = dir ? __builtin_amdgcn_exp2f(s.la) : __builtin_amdgcn_exp2f(end - s.la) * s.delta;
     a.m.put(sM, NP, tid);
     auto weight = [&](int r) { return __shfl(w, r, 64); };
-    if (gate) put_weighted<T, true>(sX, sXL, XP, a.x, a.z, weight, tid);
-    else put_weighted<T, false>(sX, sXL, XP, a.x, a.z, weight, tid);
+    if (gate) put_weighted<T, true>(sX, XP, a.x, a.z, weight, tid);
+    else put_weighted<T, false>(sX, XP, a.x, a.z, weight, tid);
     __syncthreads();
     load(i + 2, a);
     // the state that enters the chunk
@@ -387,16 +395,12 @@ __global__ __launch_bounds__(kWalkThreads) void ssd_walk_kernel(ChunkParams p, W
 #pragma unroll
     for (int t = 0; t < kQ / 16; ++t) {
       if (t >= kb) continue;
-      const auto xf = frag_down<T>(sX, XP, 16 * t, 16 * pt, lr, lq);
-      [[maybe_unused]] auto xl = xf;
-      if constexpr (kBF) xl = frag_down<T>(sXL, XP, 16 * t, 16 * pt, lr, lq);
+      const WeightedFrag<T> xf(sX, XP, 16 * t, 16 * pt, lr, lq);
 #pragma unroll
       for (int j = 0; j < kMost; ++j) {
         const int n = first + step * j;
         if (n >= nt) continue;
-        const auto mf = frag_down<T>(sM, NP, 16 * t, 16 * n, lr, lq);
-        if constexpr (kBF) acc[j] = mma32(mf, mf, xf, xl, acc[j]);
-        else acc[j] = mma16<T>(mf, xf, acc[j]);
+        acc[j] = xf.times(frag_down<T>(sM, NP, 16 * t, 16 * n, lr, lq), acc[j]);
       }
     }
   };
@@ -657,14 +661,15 @@ hipError_t launch_chunk_states(const ChunkParams& p, bool bf16, bool backward, i
                                const float* dlast, float* dh0, hipStream_t stream) {
   // batch rows of equal length: a workgroup goes along a whole row where two
   // workgroups a compute unit remain, a head's channels in up to 4 parts.  Measured
-  // on gradients, 8 x 2048 x 32 x 64 x 64 bf16: 118 us, and 88 + 84 chunk by chunk; with
+  // on gradients, 8 x 2048 x 32 x 64 x 64 bf16: 122 us, and 95 + 84 chunk by chunk; with
   // the channels in two parts (1024 workgroups) 194.
   if (!p.table && p.nc > 0) {
     WalkParams q{{h0, dlast}, {last, dh0}, 0, 0};
     const int64_t heads = nseq * p.H * (backward ? 2 : 1);
     for (q.cols = kPB; q.cols > 16 && heads * ((p.P + q.cols - 1) / q.cols) < 512;) q.cols /= 2;
     q.split = (p.P + q.cols - 1) / q.cols;
-    if (heads * q.split >= 512) {
+    // (its windows hold a head's state, its grid 2^32 threads)
+    if (heads * q.split >= 512 && heads * q.split < (int64_t{1} << 23) && static_cast<int64_t>(p.P) * p.N < (int64_t{1} << 29)) {
       if (!bf16) launch_walk<float, 64>(p, q, backward, nseq, stream);
       else if (p.N > 64) launch_walk<uint16_t, 128>(p, q, backward, nseq, stream);
       else launch_walk<uint16_t, 64>(p, q, backward, nseq, stream);

@@ -86,7 +86,8 @@ int check_ssd(int64_t batch, int64_t L, int64_t H, int64_t P, int64_t ngroups, i
   if (batch < 0 || L < 0 || nseq < 0 || H < 1 || P < 1 || N < 1 || bad_groups(ngroups, H) || (packed && batch != 1))
     return SSM_ERR_SHAPE;
   if (bad_dtype(dtype)) return SSM_ERR_DTYPE;
-  const int64_t most = (int64_t{1} << 31) - 1, chunks = (int64_t{1} << 24) - 1;
+  // a grid has 2^32 threads, 512 to a chunk's head
+  const int64_t most = (int64_t{1} << 31) - 1, chunks = (int64_t{1} << 23) - 1;
   if (N > (dtype == SSM_BF16 ? 128 : 64) || L > kMaxSeqlen || H > most / P || H * P > most / N) return SSM_ERR_UNSUPPORTED;
   if (packed && nseq >= kMaxPacked) return SSM_ERR_UNSUPPORTED;
   const int64_t of_row = packed ? L / 64 + min(nseq, L) : (L + 63) / 64;

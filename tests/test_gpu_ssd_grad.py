@@ -134,6 +134,47 @@ def test_steps_as_they_are_and_strong_decay(io):
     run_and_check(t, io, f"steps of 0 {io}", weak=("dA", "dh0"))
 
 
+# batches with enough heads for a row's states to be made in one walk
+ROWS = [(16, 70, 16, 64, 1, 64), (33, 1, 8, 5, 2, 7), (16, 64, 16, 20, 4, 33), (20, 129, 16, 16, 1, 24), (16, 65, 4, 64, 1, 16),
+        (8, 200, 32, 33, 1, 20), (4, 130, 16, 130, 2, 16), (64, 66, 4, 16, 1, 128), (16, 66, 8, 64, 2, 128), (32, 63, 8, 17, 1, 65)]
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", ROWS, ids=lambda s: "x".join(map(str, s)))
+def test_many_rows(shape, io):
+    b, L, H, P, G, N = shape
+    if io == "f32" and N > 64:
+        N //= 2
+    t = make((b, L), H, P, G, N, io, seed=sum(shape), gate=H % 8 == 0, h0=L % 2 == 0, full=P != 33, pad=8 if P == 20 else 0)
+    g = run_and_check(t, io, f"{shape} {io}", dlast=L != 129)
+    again = call(t, ssm.ssd_scan_bwd, t["dout"], dlast=t["dlast"] if L != 129 else None)
+    assert all(torch.equal(g[k], again[k]) for k in g)
+
+
+def test_a_row_next_to_many():
+    """A row's gradients, chunk by chunk and in a walk: sums in another order."""
+    t = make((16, 200), 16, 64, 1, 32, "bf16", seed=13)
+    many = call(t, ssm.ssd_scan_bwd, t["dout"], dlast=t["dlast"])
+    one = {k: v[5:6] if k in ("x", "dt", "B", "C", "z", "dout", "h0", "dlast") else v for k, v in t.items()}
+    g = call(one, ssm.ssd_scan_bwd, one["dout"], dlast=one["dlast"])
+    val, bnd = expected(one, "bf16")
+    check({k: v for k, v in g.items()}, val, bnd, "bf16", "a row alone")
+    check({k: many[k][5:6] for k in ("dx", "ddt", "dB", "dC", "dz", "dh0")}, val, bnd, "bf16", "a row of many")
+
+
+def test_many_rows_nan_stays_with_its_row():
+    t = make((16, 130), 16, 16, 1, 16, seed=14)
+    g0 = call(t, ssm.ssd_scan_bwd, t["dout"], dlast=t["dlast"])
+    for k in ("x", "B", "C", "dout", "z"):
+        t[k] = t[k].clone()
+        t[k][7, 100] = float("nan")
+    t["dt"][9] = float("nan")
+    g = call(t, ssm.ssd_scan_bwd, t["dout"], dlast=t["dlast"])
+    keep = [r for r in range(16) if r not in (7, 9)]
+    for k in ("dx", "ddt", "dB", "dC", "dz", "dh0"):
+        assert torch.equal(g[k][keep], g0[k][keep]), k
+
+
 PACKED = {
     "one": [0, 40],
     "on_chunks": [0, 64, 128, 192],
@@ -299,6 +340,22 @@ def test_two_captured_graphs_at_once():
             assert torch.equal(o, wo) and torch.equal(last, wl)
             for k in wg:
                 assert torch.equal(g[k], wg[k]), k
+
+
+def test_many_rows_captured():
+    t = make((16, 150), 16, 16, 1, 16, "bf16", seed=15)
+    want = call(t, ssm.ssd_scan_bwd, t["dout"], dlast=t["dlast"])
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = call(t, ssm.ssd_scan_bwd, t["dout"], dlast=t["dlast"])
+    for _ in range(3):
+        for v in got.values():
+            v.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for k in want:
+            assert torch.equal(got[k], want[k]), k
 
 
 def test_refusals():

@@ -75,7 +75,8 @@ def expect(make, status, **fields):
     a = make()
     for k, v in fields.items():
         setattr(a, k, v)
-    assert CHECKS[make](a) == status, (make.__name__, fields, CHECKS[make](a))
+    got = {**CHECKS, **SCANS}[make](a)
+    assert got == status, (make.__name__, fields, got)
 
 
 def test_struct_sizes():
@@ -215,3 +216,165 @@ def test_zero_sizes_need_nothing():
     expect(conv_bwd, OK, seqlen=0, x=None, dout=None, dx=None, workspace=None, workspace_bytes=0)
     expect(conv_step, OK, batch=0, state=None)
     expect(ssd_step, OK, batch=0, state=None)
+
+
+# ---- the packed prefill and the gradients ----------------------------------------
+
+
+def ssd_tensors(a, names, T, H, P, G, N, batch=None):
+    """Contiguous x, B, C and the like."""
+    for i, k in enumerate(names):
+        heads, inner, which = (G, N, "group") if k in "BC" else (H, P, "head")
+        setattr(a, k, addr(30 + i))
+        if batch is not None:
+            setattr(a, k + "_batch_stride", T * heads * inner)
+        setattr(a, k + "_seq_stride", heads * inner)
+        setattr(a, f"{k}_{which}_stride", inner)
+
+
+def ssd_packed(T=300, H=8, P=16, G=2, N=32, nseq=5, io=1):
+    a = ssm.SsdPackedArgs()
+    a.seqlen, a.nheads, a.headdim, a.ngroups, a.dstate, a.nseq, a.io_dtype, a.dt_softplus = T, H, P, G, N, nseq, io, 1
+    ssd_tensors(a, ("x", "z", "B", "C", "out"), T, H, P, G, N)
+    a.dt, a.dt_seq_stride = addr(40), H
+    for i, k in enumerate(("A", "D", "dt_bias", "cu_seqlens", "h0", "last_state", "workspace")):
+        setattr(a, k, addr(41 + i))
+    a.workspace_bytes = ssm.ssd_packed_workspace_size(a)
+    return a
+
+
+def ssd_bwd(batch=2, T=300, H=8, P=16, G=2, N=32, nseq=0, io=1):
+    a = ssm.SsdBwdArgs()
+    a.batch, a.seqlen, a.nheads, a.headdim, a.ngroups, a.dstate, a.nseq, a.io_dtype, a.dt_softplus = batch, T, H, P, G, N, nseq, io, 1
+    ssd_tensors(a, ("x", "z", "B", "C", "dout"), T, H, P, G, N, batch)
+    a.dt, a.dt_batch_stride, a.dt_seq_stride = addr(40), T * H, H
+    for i, k in enumerate(("A", "D", "dt_bias", "h0", "dlast", "dx", "ddt", "dz", "dB", "dC", "dA", "dD", "ddt_bias", "dh0", "workspace")):
+        setattr(a, k, addr(41 + i))
+    if nseq:
+        a.cu_seqlens = addr(60)
+    a.workspace_bytes = ssm.ssd_bwd_workspace_size(a)
+    return a
+
+
+SCANS = {ssd_packed: ssm.validate_ssd_packed, ssd_bwd: ssm.validate_ssd_bwd}
+
+def test_scan_struct_sizes_and_null_blocks():
+    for name, T in (("ssd_packed", ssm.SsdPackedArgs), ("ssd_bwd", ssm.SsdBwdArgs)):
+        assert getattr(ssm.lib(), f"ssm_{name}_args_size")() == ctypes.sizeof(T)
+        assert getattr(ssm.lib(), "ssm_validate_" + name)(None) == NULL
+        assert getattr(ssm.lib(), f"ssm_{name}_workspace_size")(None) == 0
+
+
+@pytest.mark.parametrize("io,most", [(0, 64), (1, 128)])
+def test_good_scans_pass(io, most):
+    for N in (1, 20, 64, most):
+        assert ssm.validate_ssd_packed(ssd_packed(N=N, io=io)) == OK
+        assert ssm.validate_ssd_bwd(ssd_bwd(N=N, io=io)) == OK
+        assert ssm.validate_ssd_bwd(ssd_bwd(batch=1, nseq=4, N=N, io=io)) == OK
+    for make in SCANS:
+        a = make(N=most, io=io)
+        a.dstate = most + 1
+        assert SCANS[make](a) == UNSUP
+
+
+@pytest.mark.parametrize("make,fields", [
+    (ssd_packed, ("x", "dt", "B", "C", "A", "out", "cu_seqlens")),
+    (ssd_bwd, ("x", "dt", "B", "C", "A", "dout", "dx", "ddt", "dz", "dB", "dC", "dA"))])
+def test_missing_pointers_of_scans(make, fields):
+    for f in fields:
+        expect(make, NULL, **{f: None})
+
+
+def test_optional_pointers_of_scans():
+    for f in ("z", "D", "dt_bias", "h0", "last_state"):
+        expect(ssd_packed, OK, **{f: None})
+    for f in ("z", "D", "dt_bias", "h0", "dlast", "dD", "ddt_bias", "dh0"):
+        expect(ssd_bwd, OK, **{f: None})
+    expect(ssd_bwd, OK, z=None, dz=None)
+
+
+@pytest.mark.parametrize("make", SCANS)
+def test_sizes_and_types_of_scans(make):
+    expect(make, SHAPE, seqlen=-1)
+    for f in ("nheads", "headdim", "dstate"):
+        expect(make, SHAPE, **{f: 0})
+    expect(make, SHAPE, ngroups=3)
+    expect(make, SHAPE, nseq=-1)
+    expect(make, DTYPE, io_dtype=2)
+    expect(make, UNSUP, seqlen=(1 << 31) - 64)
+    expect(make, UNSUP, headdim=1 << 26)
+    expect(make, UNSUP, nheads=1 << 24, ngroups=1)
+    if make is ssd_packed:
+        expect(make, UNSUP, nseq=1 << 29)
+        expect(make, UNSUP, seqlen=1 << 20, nseq=1 << 20)   # a chunk each, of 8 heads
+    else:
+        expect(make, SHAPE, batch=-1)
+        expect(make, SHAPE, cu_seqlens=addr(60))   # packed rows are one row
+        expect(make, UNSUP, batch=1 << 20)         # chunks x heads past a grid's threads
+        expect(make, UNSUP, batch=1 << 62)
+        expect(make, UNSUP, headdim=1 << 21)       # 64 rows of dx past a window
+
+
+@pytest.mark.parametrize("make,fields", [
+    (ssd_packed, ("x_seq_stride", "z_head_stride", "dt_seq_stride", "B_group_stride", "C_seq_stride", "out_head_stride")),
+    (ssd_bwd, ("x_batch_stride", "z_seq_stride", "dt_batch_stride", "dt_seq_stride", "B_seq_stride", "C_group_stride", "dout_head_stride"))])
+def test_negative_and_wide_strides_of_scans(make, fields):
+    for f in fields:
+        expect(make, STRIDE, **{f: -8})
+    for k in ("x", "z", "B", "C", "out" if make is ssd_packed else "dout"):
+        expect(make, OK, **{k + "_seq_stride": 1 << 20})
+        expect(make, UNSUP, **{k + "_seq_stride": 1 << 25})
+        expect(make, UNSUP, **{k + "_seq_stride": 1 << 61})
+
+
+@pytest.mark.parametrize("make,fields", [
+    (ssd_packed, ("x", "dt", "z", "B", "C", "A", "D", "dt_bias", "cu_seqlens", "h0", "last_state", "out", "workspace")),
+    (ssd_bwd, ("x", "dt", "z", "B", "C", "A", "D", "dt_bias", "h0", "dout", "dlast", "dx", "ddt", "dz", "dB", "dC", "dA", "dD", "ddt_bias",
+               "dh0", "workspace"))])
+def test_misaligned_scans(make, fields):
+    for f in fields:
+        expect(make, ALIGN, **{f: getattr(make(), f) + 1})
+
+
+def test_overlaps_of_scans():
+    for f in ("x", "dt", "z", "B", "C", "A", "cu_seqlens", "h0", "last_state", "workspace"):
+        expect(ssd_packed, ALIAS, out=getattr(ssd_packed(), f))
+    expect(ssd_packed, ALIAS, out_seq_stride=100)
+    expect(ssd_packed, ALIAS, out_seq_stride=0)
+    expect(ssd_packed, ALIAS, out_head_stride=15)
+    a = ssd_packed()
+    expect(ssd_packed, OK, last_state=a.h0)            # the state carried in place
+    expect(ssd_packed, ALIAS, last_state=a.h0 + 4)
+    # heads first in memory
+    expect(ssd_packed, OK, out_seq_stride=16, out_head_stride=16 * 300)
+    ins = ("x", "dt", "z", "B", "C", "A", "D", "dt_bias", "h0", "dout", "dlast")
+    outs = ("dx", "ddt", "dz", "dB", "dC", "dA", "dD", "ddt_bias", "dh0", "workspace")
+    a = ssd_bwd()
+    for o in outs:
+        expect(ssd_bwd, ALIAS, **{o: getattr(a, ins[outs.index(o)])})
+        expect(ssd_bwd, ALIAS, **{o: getattr(a, outs[outs.index(o) - 1])})
+
+
+@pytest.mark.parametrize("make", SCANS)
+def test_workspace_of_scans(make):
+    size = {ssd_packed: ssm.ssd_packed_workspace_size, ssd_bwd: ssm.ssd_bwd_workspace_size}[make]
+    a = make()
+    need = size(a)
+    assert need > 0 and size(make(io=0)) == need       # asked for by sizes alone
+    expect(make, SCRATCH, workspace=None)
+    expect(make, SCRATCH, workspace_bytes=need - 1)
+    states = (9 if make is ssd_packed else 2 * 10) * 8 * 16 * 32 * 4
+    assert need >= states
+    a.x = a.B = a.cu_seqlens = None
+    assert size(a) == need
+    a.seqlen = -1
+    assert size(a) == 0
+
+
+def test_scans_without_tokens():
+    none = dict(x=None, dt=None, z=None, B=None, C=None)
+    expect(ssd_packed, OK, seqlen=0, out=None, **none)
+    expect(ssd_packed, OK, nseq=0)
+    expect(ssd_bwd, OK, seqlen=0, dout=None, dx=None, ddt=None, dz=None, dB=None, dC=None, **none)
+    expect(ssd_bwd, OK, batch=0, dout=None, dx=None, ddt=None, dz=None, dB=None, dC=None, **none)
+    expect(ssd_bwd, NULL, seqlen=0, dA=None)
