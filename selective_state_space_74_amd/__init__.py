@@ -977,11 +977,10 @@ def _placed(name, t, dtype, device):
 
 
 def _empty(like, shape, dtype, device):
-    """A new tensor of this shape, by the shorter way where `like` has it."""
-    torch = _torch()
-    if like.shape == shape and like.dtype == dtype and like.is_contiguous():
-        return torch.empty_like(like)
-    return torch.empty(shape, dtype=dtype, device=device)
+    """A new tensor of this shape, by the shorter way where `like` has its type."""
+    if like.dtype == dtype:
+        return like.new_empty(shape)
+    return _torch().empty(shape, dtype=dtype, device=device)
 
 
 def _launch(name, args, stream):
@@ -1641,10 +1640,10 @@ def ssd_scan_bwd(dout, x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus
         _fp32("h0", h0, states, dev)
     upstream = of("dout", dout, shape) + (_fp32("dlast", dlast, states, dev),)
     with _on(dev, stream) as s:
-        new = lambda *size, dtype=io: torch.empty(size, dtype=dtype, device=dev)  # noqa: E731
-        g = dict(dx=new(*shape), ddt=new(*lead, H), dB=new(*lead, G, N), dC=new(*lead, G, N), dA=torch.empty_like(A))
+        g = dict(dx=x.new_empty(shape), ddt=x.new_empty(lead + (H,)), dB=x.new_empty(lead + (G, N)), dC=x.new_empty(lead + (G, N)),
+                 dA=torch.empty_like(A))
         if z is not None:
-            g["dz"] = new(*shape)
+            g["dz"] = x.new_empty(shape)
         if D is not None:
             g["dD"] = torch.empty_like(D)
         if dt_bias is not None:
@@ -1669,8 +1668,9 @@ def ssd_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=True, h0=
         @staticmethod
         def forward(ctx, x, dt, A, B, C, D, z, dt_bias, h0):
             ctx.set_materialize_grads(False)
-            out, last = ssd_scan_fwd(x, dt, A, B, C, D=D, z=z, dt_bias=dt_bias, dt_softplus=dt_softplus, h0=h0,
-                                     return_last_state=True, cu_seqlens=cu_seqlens)
+            with _on(_gpu("x", x), None):
+                out, last = ssd_scan_fwd(x, dt, A, B, C, D=D, z=z, dt_bias=dt_bias, dt_softplus=dt_softplus, h0=h0,
+                                         return_last_state=True, cu_seqlens=cu_seqlens)
             ctx.save_for_backward(x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens)
             return out, last
 

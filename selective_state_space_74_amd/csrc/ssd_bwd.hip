@@ -28,7 +28,9 @@
 // other tile of G and M, half of the states for dB and dC and half of the channels
 // for dx.  G, the sum over the heads of M L Delta, and dB and dC stay in registers
 // from head to head, so dB and dC cost one product with C and B for all heads; the
-// next head's loads are under way while one is computed.
+// next head's loads are under way while one is computed.  Bound by memory and the
+// latency of a head's five stages between barriers: 8 x 2048 x 32 x 64 x 64 bf16 in
+// 144 us, 3.3 TB/s of x, dout, both states and dx; one wavefront a token block: 203.
 #include <algorithm>
 
 #include "abi_checks.h"
@@ -504,37 +506,49 @@ __global__ __launch_bounds__(kGradThreads, sizeof(T) == 2 && NMAX == 64 ? 4 : 2)
   }
 }
 
-// dB and dC from the workgroups' parts, in their order; packed: only for tokens of
-// a sequence (the others' rows are cleared elsewhere).
+// What the workgroups left in parts, each sum in a fixed order.  Workgroups 0 .. 3 H - 1:
+// dA, ddt_bias and dD of a head, over its chunks; the others, where a group's heads
+// were several workgroups': dB and dC (packed: only for tokens of a sequence; the
+// others' rows are cleared elsewhere).  One launch for both: each would take 4 us
+// however little it does.
+struct SumParams {
+  const float* parts;      // [3][H][nc]
+  const float* bc;         // [2][blocks][n]
+  const int32_t* cu;
+  int64_t nseq, L, n, row; // elements of dB (and of dC), and of a token of theirs
+  int nc, H, blocks;
+  float *dA, *dbias, *dD;
+  void *dB, *dC;
+};
 template <typename T>
-__global__ __launch_bounds__(kThreads) void ssd_sum_parts_kernel(const float* parts, int blocks, int64_t n, int64_t row,
-                                                                 const int32_t* cu, int64_t nseq, int64_t L, T* dB, T* dC) {
-  int64_t lo = 0, hi = n;
-  if (cu) {
-    lo = min(max(int64_t{cu[0]}, int64_t{0}), L) * row;
-    hi = min(max(int64_t{cu[nseq]}, int64_t{0}), L) * row;
+__global__ __launch_bounds__(kThreads) void ssd_sum_parts_kernel(SumParams p) {
+  if (blockIdx.x < 3u * p.H) {
+    __shared__ float sums[kWaves];
+    const int h = blockIdx.x / 3, which = blockIdx.x % 3;
+    const float* const from = p.parts + (static_cast<int64_t>(which) * p.H + h) * p.nc;
+    float s = 0.0f;
+    for (int c = threadIdx.x; c < p.nc; c += kThreads) s += from[c];
+    s = wave_sum(s);
+    if (threadIdx.x % 64 == 0) sums[threadIdx.x / 64] = s;
+    __syncthreads();
+    float* const to = which == 0 ? p.dA : which == 1 ? p.dbias : p.dD;
+    if (threadIdx.x == 0 && to) to[h] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+    return;
   }
-  const float* const from = parts + blockIdx.y * blocks * n;
-  T* const to = blockIdx.y ? dC : dB;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * kThreads) {
+  int64_t lo = 0, hi = p.n;
+  if (p.cu) {
+    lo = min(max(int64_t{p.cu[0]}, int64_t{0}), p.L) * p.row;
+    hi = min(max(int64_t{p.cu[p.nseq]}, int64_t{0}), p.L) * p.row;
+  }
+  const int id = blockIdx.x - 3 * p.H, step = (gridDim.x - 3 * p.H) / 2;
+  const float* const from = p.bc + (id & 1) * p.blocks * p.n;
+  T* const to = static_cast<T*>(id & 1 ? p.dC : p.dB);
+  for (int64_t i = static_cast<int64_t>(id >> 1) * kThreads + threadIdx.x; i < p.n; i += static_cast<int64_t>(step) * kThreads) {
     if (i < lo || i >= hi) continue;
     float s = 0.0f;
-    for (int b = 0; b < blocks; ++b) s += from[b * n + i];
+    for (int b = 0; b < p.blocks; ++b) s += from[b * p.n + i];
     io<T>::store(to + i, s);
   }
-}
-
-// dA, ddt_bias and dD of a head: its chunks' sums, in a fixed order.
-__global__ __launch_bounds__(kThreads) void ssd_sum_heads_kernel(const float* parts, int nc, int H, float* dA, float* dbias, float* dD) {
-  __shared__ float sums[kWaves];
-  const int h = blockIdx.x, which = blockIdx.y;
-  float s = 0.0f;
-  for (int c = threadIdx.x; c < nc; c += kThreads) s += parts[(static_cast<int64_t>(which) * H + h) * nc + c];
-  s = wave_sum(s);
-  if (threadIdx.x % 64 == 0) sums[threadIdx.x / 64] = s;
-  __syncthreads();
-  float* const to = which == 0 ? dA : which == 1 ? dbias : dD;
-  if (threadIdx.x == 0 && to) to[h] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
 }
 
 size_t align_up(size_t n) { return (n + 255) / 256 * 256; }
@@ -706,18 +720,13 @@ hipError_t launch_ssd_bwd(const ssm_ssd_bwd_args& a, hipStream_t stream) {
     else launch_grad<uint16_t, 64>(p, g, stream);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    if (q.blocks > 1) {
-      const int64_t n = g.tokens * GN;
-      const dim3 grid(static_cast<unsigned>(std::min<int64_t>((n + kThreads - 1) / kThreads, 4096)), 2);
-      if (bf16)
-        ssd_sum_parts_kernel<uint16_t><<<grid, kThreads, 0, stream>>>(g.dBparts, p.blocks, n, GN, a.cu_seqlens, a.nseq, a.seqlen,
-                                                                      static_cast<uint16_t*>(a.dB), static_cast<uint16_t*>(a.dC));
-      else
-        ssd_sum_parts_kernel<float><<<grid, kThreads, 0, stream>>>(g.dBparts, p.blocks, n, GN, a.cu_seqlens, a.nseq, a.seqlen,
-                                                                   static_cast<float*>(a.dB), static_cast<float*>(a.dC));
-    }
   }
-  ssd_sum_heads_kernel<<<dim3(p.H, 3), kThreads, 0, stream>>>(reinterpret_cast<float*>(ws + l.parts), p.nc, p.H, a.dA, a.ddt_bias, a.dD);
+  SumParams m{reinterpret_cast<float*>(ws + l.parts), reinterpret_cast<float*>(ws + l.bc), a.cu_seqlens, a.nseq, a.seqlen,
+              a.batch * a.seqlen * GN, GN, p.nc, p.H, p.blocks, a.dA, a.ddt_bias, a.dD, a.dB, a.dC};
+  const int64_t more = q.nc > 0 && q.blocks > 1 ? 2 * std::min<int64_t>((m.n + kThreads - 1) / kThreads, 4096) : 0;
+  const unsigned grid = static_cast<unsigned>(3 * a.nheads + more);
+  if (bf16) ssd_sum_parts_kernel<uint16_t><<<grid, kThreads, 0, stream>>>(m);
+  else ssd_sum_parts_kernel<float><<<grid, kThreads, 0, stream>>>(m);
   return hipGetLastError();
 }
 

@@ -78,15 +78,16 @@ struct Rows64 {
 };
 constexpr uint32_t kNowhere = 0x80000000u;
 
+// any = false: a window of nothing.
 template <typename T>
-__device__ __forceinline__ Rows64 rows_of(const TokenTensor& t, const Chunk& k, int head, int first, int inner) {
+__device__ __forceinline__ Rows64 rows_of(const TokenTensor& t, const Chunk& k, int head, int first, int inner, bool any = true) {
   const T* const base = static_cast<const T*>(t.p) + k.b * t.sb + k.t0 * t.ss + head * t.sh + first;
   Rows64 w;
   w.stride = static_cast<uint32_t>(t.ss) * sizeof(T);
   w.len = k.len;
   w.cols = inner - first;
-  w.r = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(base), 0, static_cast<int>((k.len - 1) * w.stride + w.cols * sizeof(T)),
-                                          kRsrcWord3);
+  w.r = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(base), 0,
+                                          any ? static_cast<int>((k.len - 1) * w.stride + w.cols * sizeof(T)) : 0, kRsrcWord3);
   return w;
 }
 

@@ -135,9 +135,10 @@ struct WeightedFrag {
 };
 
 // Workgroup: (chunk, heads of one group, direction).  B (C backward) of the chunk
-// is staged once; then for each head the rows x_s (dy_t) times their weight.  A wavefront owns 16 channels of
-// the state (fewer channels: a share of its columns).  Bound by memory: the states
-// written are 4 N bytes for 2 x (64 tokens) bytes of x read.
+// is staged once; then for each head the rows x_s (dy_t) times their weight.  A
+// wavefront owns 16 channels of the state (fewer channels: a share of its columns).
+// Bound by memory: the states written are 4 N bytes for 2 x (64 tokens) bytes of x
+// read; 16,411 packed x 32 x 64 x 64 bf16, 5 sequences: 56 us, 3.7 TB/s.
 template <typename T, int NMAX, bool kVec>
 __global__ __launch_bounds__(kThreads) void ssd_states_kernel(ChunkParams p, int grid) {
   using E = typename Lds<T>::E;
@@ -235,7 +236,8 @@ struct CarryParams {
 
 // A lane has V values of a sequence's state and goes along its chunks (blockIdx.z
 // = 1: from the end), kAhead chunks' loads in flight; in place of what a chunk adds
-// it leaves the state that enters it, for bf16 IO as two bf16 halves.
+// it leaves the state that enters it, for bf16 IO as two bf16 halves.  Bound by
+// memory, as fast as a copy: 283 MB of the same case in 52 us, 5.4 TB/s.
 template <bool kBF, int V>
 __global__ __launch_bounds__(kThreads) void ssd_carry_kernel(CarryParams p) {
   constexpr int kAhead = 8;
@@ -294,7 +296,8 @@ struct WalkParams {
 // Workgroup: (batch row, head, some of its channels, direction).  It goes along the
 // row's chunks with the state in registers, so that the states are written once and
 // not read and written again by the carry: loads are two chunks ahead, LDS in two
-// halves makes do with one barrier a chunk.
+// halves makes do with one barrier a chunk.  Bound by the chain of chunks, 3.8 us
+// each: 8 x 2048 x 32 x 64 x 64 bf16, both directions, 122 us, 3.4 TB/s.
 template <typename T, int NMAX, bool kVec>
 __global__ __launch_bounds__(kWalkThreads) void ssd_walk_kernel(ChunkParams p, WalkParams q) {
   using E = typename Lds<T>::E;
@@ -423,33 +426,60 @@ __global__ __launch_bounds__(kWalkThreads) void ssd_walk_kernel(ChunkParams p, W
 
 // Workgroup: (chunk, heads of one group); two of its 8 wavefronts share 16 of the
 // tokens, each with every other 16 channels of a head.  The scores C_t . B_s of the
-// chunk are computed once and stay in registers for all heads; the next head's loads
+// chunk are computed once and stay in registers for all heads; the next heads' loads
 // are under way while one is computed.  Tiles lie so that a lane has four channels
-// of one token.
+// of one token.  Bound by the latency of a pass (stage, barrier, products, barrier;
+// 69% of a wavefront's cycles are waits) with 16 wavefronts a compute unit: the case
+// above in 102 us, 2.7 TB/s.  Loads one pass ahead and not two: 111 us; four
+// wavefronts, each with all channels of 16 tokens: 169.
 // kDz: the gate's gradient dout y silu'(z) in place of the output.
 constexpr int kOutThreads = 512;
 
 // Four values of a row from column c on (of `cols`), as they lie.
 template <typename T, bool kVec>
-__device__ __forceinline__ void load4(const Rows64& w, int r, int c, float (&v)[4]) {
-  const uint32_t off = r * w.stride + c * static_cast<uint32_t>(sizeof(T));
-  if constexpr (kVec) {
-    const uint32_t at = r < w.len && c < w.cols ? off : kNowhere;
-    if constexpr (sizeof(T) == 4) {
-      const v4u q = __builtin_amdgcn_raw_buffer_load_b128(w.r, at, 0, 0);
+struct Four {
+  uint32_t w[sizeof(T)];
+  __device__ __forceinline__ void load(const Rows64& r, int row, int c) {
+    const uint32_t off = row * r.stride + c * static_cast<uint32_t>(sizeof(T));
+    if constexpr (!kVec) {
+      uint32_t v[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(q[e]);
+      for (int e = 0; e < 4; ++e)
+        v[e] = Elem<T>::load(r.r, row < r.len && c + e < r.cols ? off + e * static_cast<uint32_t>(sizeof(T)) : kNowhere);
+#pragma unroll
+      for (int e = 0; e < static_cast<int>(sizeof(T)); ++e) w[e] = sizeof(T) == 4 ? v[e] : v[2 * e % 4] | v[(2 * e + 1) % 4] << 16;
     } else {
-      const v2u q = __builtin_amdgcn_raw_buffer_load_b64(w.r, at, 0, 0);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(e % 2 ? q[e / 2] & 0xffff0000u : q[e / 2] << 16);
+      const uint32_t at = ((row < r.len) & (c < r.cols)) ? off : kNowhere;
+      if constexpr (sizeof(T) == 4) __builtin_memcpy(w, &static_cast<const v4u&>(__builtin_amdgcn_raw_buffer_load_b128(r.r, at, 0, 0)), 16);
+      else __builtin_memcpy(w, &static_cast<const v2u&>(__builtin_amdgcn_raw_buffer_load_b64(r.r, at, 0, 0)), 8);
     }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      v[e] = Elem<T>::f32(Elem<T>::load(w.r, r < w.len && c + e < w.cols ? off + e * static_cast<uint32_t>(sizeof(T)) : kNowhere));
   }
-}
+  __device__ __forceinline__ void store(const Rows64& r, int row, int c) const {
+    const uint32_t off = row * r.stride + c * static_cast<uint32_t>(sizeof(T));
+    if constexpr (!kVec) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        Elem<T>::store(r.r, row < r.len && c + e < r.cols ? off + e * static_cast<uint32_t>(sizeof(T)) : kNowhere, (*this)[e]);
+    } else {
+      const uint32_t at = ((row < r.len) & (c < r.cols)) ? off : kNowhere;
+      if constexpr (sizeof(T) == 4) __builtin_amdgcn_raw_buffer_store_b128(v4u{w[0], w[1], w[2], w[3]}, r.r, at, 0, 0);
+      else __builtin_amdgcn_raw_buffer_store_b64(v2u{w[0], w[1]}, r.r, at, 0, 0);
+    }
+  }
+  __device__ __forceinline__ float operator[](int e) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[e]);
+    else return __uint_as_float(e % 2 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+  }
+  __device__ __forceinline__ void set(const float (&v)[4]) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(v[e]);
+    } else {
+      w[0] = pack_bf16x2(v[0], v[1]);
+      w[1] = pack_bf16x2(v[2], v[3]);
+    }
+  }
+};
 
 template <typename T, int NMAX, bool kDz, bool kVec>
 __global__ __launch_bounds__(kOutThreads, 4) void ssd_outputs_kernel(ChunkParams p, ChunkOut o, int grid) {
@@ -507,57 +537,85 @@ __global__ __launch_bounds__(kOutThreads, 4) void ssd_outputs_kernel(ChunkParams
   E* const sH = sh.tiles + kQ * XP;
   [[maybe_unused]] E* const sHL = sH + kPB * NP;
   const int nt = (p.N + 15) / 16;
-  Pieces<T, kPB, kOutThreads> xv;
-  StatePieces<T, NMAX, kOutThreads> sv;
-  auto load = [&](int h, int p0) {
-    xv.template load<kVec>(rows_of<T>(p.x, k, h, p0, p.P), tid);
-    sv.template load<kVec>(state_rows(p.state, ((static_cast<int64_t>(c) * p.H + h) * p.P + p0) * p.N, min(kPB, p.P - p0), p.N), tid);
-  };
-  load(h0, 0);
-  for (int i = 0; i < heads; ++i) {
-    const int h = h0 + i;
-    // weighted scores of the head, as operands; those above the diagonal are zero
-    typename Frag<T>::V mf[QB];
-    const float la_t = sh.la[i][own];
+  // what a pass (64 channels of a head) needs, loaded kDepth passes ahead.  Loads and
+  // stores are issued whether or not there is anything to take or leave (their offsets
+  // then lie nowhere), so that a wait can count them and leave the later ones in flight.
+  constexpr int kDepth = kBF && NMAX == 64 && !kDz ? 2 : 1;
+  constexpr int kTiles = kPB / 32;
+  const int of_head = (p.P + kPB - 1) / kPB, passes = heads * of_head;
+  struct Ahead {
+    Pieces<T, kPB, kOutThreads> x;
+    StatePieces<T, NMAX, kOutThreads> s;
+    Four<T, kVec> z[kTiles], up[kDz ? kTiles : 1];
+  } ahead[kDepth];
+  const bool gated = p.z.p != nullptr;
+  const TokenTensor zt = gated ? p.z : p.x;
+  auto load = [&](int s, Ahead& a) {
+    const bool any = s < passes;
+    s = any ? s : 0;
+    const int h = h0 + s / of_head, p0 = s % of_head * kPB;
+    const Rows64 x = rows_of<T>(p.x, k, h, p0, p.P, any), z = rows_of<T>(zt, k, h, p0, p.P, any && gated);
+    const StateRows st = state_rows(p.state, ((static_cast<int64_t>(c) * p.H + h) * p.P + p0) * p.N, any ? min(kPB, p.P - p0) : 0, p.N);
+    a.x.template load<kVec>(x, tid);
+    a.s.template load<kVec>(st, tid);
 #pragma unroll
-    for (int sb = 0; sb < QB; ++sb) {
-      mf[sb] = tofrag<T>(0.0f, 0.0f, 0.0f, 0.0f);
-      if (sb > tok) continue;
-      const v4f la_s = *reinterpret_cast<const v4f*>(&sh.la[i][16 * sb + 4 * lq]);
-      const v4f dl_s = *reinterpret_cast<const v4f*>(&sh.dl[i][16 * sb + 4 * lq]);
-      float m[4];
+    for (int j = 0; j < kTiles; ++j) a.z[j].load(z, own, 16 * (2 * j + half) + 4 * lq);
+    if constexpr (kDz) {
+      const Rows64 up = rows_of<T>(p.dout, k, h, p0, p.P, any);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) m[e] = scores[sb][e] * __builtin_amdgcn_exp2f(la_t - la_s[e]) * dl_s[e];
-      if (sb == tok) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) m[e] = 4 * lq + e <= lr ? m[e] : 0.0f;
-      }
-      mf[sb] = tofrag<T>(m[0], m[1], m[2], m[3]);
+      for (int j = 0; j < kTiles; ++j) a.up[j].load(up, own, 16 * (2 * j + half) + 4 * lq);
     }
-    const float ea = __builtin_amdgcn_exp2f(la_t), Dh = sh.D[i];
-    for (int p0 = 0; p0 < p.P; p0 += kPB) {
-      const int cols = p.P - p0;
-      xv.put(sX, XP, tid);
-      sv.put(sH, kBF ? sHL : sH, NP, tid);
-      __syncthreads();
-      // what the end of this pass needs, and the next one
-      float z[kPB / 32][4], up[kPB / 32][4];
-      if (p.z.p) {
-        const Rows64 zr = rows_of<T>(p.z, k, h, p0, p.P);
+  };
+  typename Frag<T>::V mf[QB];
+  float ea = 0.0f, Dh = 0.0f;
+  auto pass = [&](int s, Ahead& a) {
+    const int i = s / of_head, h = h0 + i, p0 = s % of_head * kPB, cols = s < passes ? p.P - p0 : 0;
+    if (p0 == 0 && cols > 0) {
+      // weighted scores of the head, as operands; those above the diagonal are zero
+      const float la_t = sh.la[i][own];
 #pragma unroll
-        for (int j = 0; j < kPB / 32; ++j) load4<T, kVec>(zr, own, 16 * (2 * j + half) + 4 * lq, z[j]);
+      for (int sb = 0; sb < QB; ++sb) {
+        mf[sb] = tofrag<T>(0.0f, 0.0f, 0.0f, 0.0f);
+        if (sb > tok) continue;
+        const v4f la_s = *reinterpret_cast<const v4f*>(&sh.la[i][16 * sb + 4 * lq]);
+        const v4f dl_s = *reinterpret_cast<const v4f*>(&sh.dl[i][16 * sb + 4 * lq]);
+        float m[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m[e] = scores[sb][e] * __builtin_amdgcn_exp2f(la_t - la_s[e]) * dl_s[e];
+        if (sb == tok) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) m[e] = 4 * lq + e <= lr ? m[e] : 0.0f;
+        }
+        mf[sb] = tofrag<T>(m[0], m[1], m[2], m[3]);
       }
-      if constexpr (kDz) {
-        const Rows64 er = rows_of<T>(p.dout, k, h, p0, p.P);
+      ea = __builtin_amdgcn_exp2f(la_t);
+      Dh = sh.D[i];
+    }
+    a.x.put(sX, XP, tid);
+    a.s.put(sH, kBF ? sHL : sH, NP, tid);
+    float by[kTiles][4];   // what the sums are multiplied by
 #pragma unroll
-        for (int j = 0; j < kPB / 32; ++j) load4<T, kVec>(er, own, 16 * (2 * j + half) + 4 * lq, up[j]);
+    for (int j = 0; j < kTiles; ++j) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float z = a.z[j][e];
+        if constexpr (kDz) {
+          const float g = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-z * kLog2e));
+          by[j][e] = a.up[j][e] * (g * fmaf(z, 1.0f - g, 1.0f));
+        } else {
+          by[j][e] = gated ? silu_f32(z) : 1.0f;
+        }
+        asm volatile("" : "+v"(by[j][e]));   // here, and not behind the next loads: a copy of z would wait for them
       }
-      if (p0 + kPB < p.P) load(h, p0 + kPB);
-      else if (i + 1 < heads) load(h + 1, 0);
+    }
+    __syncthreads();
+    load(s + kDepth, a);
+    const Rows64 to = rows_of<T>(TokenTensor{kDz ? o.dz : o.out, o.sb, o.ss, o.sh, kVec}, k, h, p0, p.P, cols > 0);
 #pragma unroll
-      for (int j = 0; j < kPB / 32; ++j) {
-        const int pt = 2 * j + half, c0 = 16 * pt + 4 * lq;
-        if (16 * pt >= cols) continue;
+    for (int j = 0; j < kTiles; ++j) {
+      const int pt = 2 * j + half, c0 = 16 * pt + 4 * lq;
+      Four<T, kVec> out{};
+      if (16 * pt < cols) {
         v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -579,35 +637,39 @@ __global__ __launch_bounds__(kOutThreads, 4) void ssd_outputs_kernel(ChunkParams
             if (sb <= tok) acc = mma16<T>(frag_down<T>(sX, XP, 16 * sb, 16 * pt, lr, lq), mf[sb], acc);
         }
         // token own, channels c0 ..
-        if (own >= k.len || c0 >= cols) continue;
         float y[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          y[e] = fmaf(Dh, Lds<T>::f(sX[own * XP + c0 + e]), acc[e]);
-          if constexpr (kDz) {
-            const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-z[j][e] * kLog2e));
-            y[e] *= up[j][e] * (s * fmaf(z[j][e], 1.0f - s, 1.0f));
-          } else if (p.z.p) {
-            y[e] *= silu_f32(z[j][e]);
-          }
-        }
-        T* const to = static_cast<T*>(kDz ? o.dz : o.out) + k.b * o.sb + (k.t0 + own) * o.ss + h * o.sh + p0 + c0;
-        if constexpr (kVec) {
-          if constexpr (kBF) *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
-          else *reinterpret_cast<float4*>(to) = make_float4(y[0], y[1], y[2], y[3]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (c0 + e < cols) io<T>::store(to + e, y[e]);
-        }
+        for (int e = 0; e < 4; ++e) y[e] = fmaf(Dh, Lds<T>::f(sX[own * XP + c0 + e]), acc[e]) * by[j][e];
+        out.set(y);
       }
-      __syncthreads();
+      out.store(to, own, c0);
+    }
+    __syncthreads();
+  };
+  if constexpr (kDepth == 1) {
+    load(0, ahead[0]);
+    for (int s = 0; s < passes; ++s) pass(s, ahead[0]);
+  } else {
+    load(0, ahead[0]);
+    load(1, ahead[1]);
+    // always two: with an exit between them the waits could not count on both
+    for (int s = 0; s < passes; s += 2) {
+      pass(s, ahead[0]);
+      pass(s + 1, ahead[1]);
     }
   }
 }
 
 template <typename T, int NMAX>
-void launch_states(const ChunkParams& p, bool backward, hipStream_t stream) {
+void launch_states(ChunkParams p, bool backward, hipStream_t stream) {
+  // half of more than 4 heads a workgroup where the grid is less than one and a half
+  // times what the machine holds at once (1024 workgroups), so that its end leaves
+  // less of it idle: 16,411 packed x 32 x 64 x 64 bf16, 8 heads 62 us and 4 heads 56
+  // (the outputs 102 with either); from 4 to 2 B is staged too often
+  if (p.hb > 4 && static_cast<int64_t>(p.nc) * p.G * p.blocks < 1536) {
+    p.hb = (p.hb + 1) / 2;
+    p.blocks = (p.per_group + p.hb - 1) / p.hb;
+  }
   const int grid = p.nc * p.G * p.blocks;
   if (p.vec) ssd_states_kernel<T, NMAX, true><<<dim3(grid, backward ? 2 : 1), kThreads, 0, stream>>>(p, grid);
   else ssd_states_kernel<T, NMAX, false><<<dim3(grid, backward ? 2 : 1), kThreads, 0, stream>>>(p, grid);
