@@ -402,15 +402,23 @@ __global__ __launch_bounds__(kGradThreads, sizeof(T) == 2 && NMAX == 64 ? 4 : 2)
           if (tb + (kBF ? 1 : 0) < tok) continue;
           const F y0 = frag_down<T>(sY, XP, 16 * tb, 16 * pt, lr, lq);
           const F w0 = tb >= tok ? frag_along<T>(sGl, GP, 16 * tok, 16 * tb, lr, lq) : tofrag<T>(0.0f, 0.0f, 0.0f, 0.0f);
-          if constexpr (kBF)
-            acc = mma32(y0, frag_down<T>(sY, XP, 16 * tb + 16, 16 * pt, lr, lq), w0,
-                        frag_along<T>(sGl, GP, 16 * tok, 16 * tb + 16, lr, lq), acc);
-          else acc = mma16<T>(y0, w0, acc);
+          if constexpr (kBF) {
+            const F w1 = frag_along<T>(sGl, GP, 16 * tok, 16 * tb + 16, lr, lq);
+            acc = mma32(y0, frag_down<T>(sY, XP, 16 * tb + 16, 16 * pt, lr, lq), w0, w1, acc);
+            if constexpr (kGate)
+              acc = mma32(frag_down<T>(sYl, XP, 16 * tb, 16 * pt, lr, lq), frag_down<T>(sYl, XP, 16 * tb + 16, 16 * pt, lr, lq), w0, w1, acc);
+          } else {
+            acc = mma16<T>(y0, w0, acc);
+          }
         }
         if (own >= k.len || c0 >= cols) continue;
         float d[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) d[e] = fmaf(dl_s, acc[e], Dh * Lds<T>::f(sY[own * XP + c0 + e]));
+        for (int e = 0; e < 4; ++e) {
+          float dy = Lds<T>::f(sY[own * XP + c0 + e]);
+          if constexpr (kGate && kBF) dy += Lds<T>::f(sYl[own * XP + c0 + e]);
+          d[e] = fmaf(dl_s, acc[e], Dh * dy);
+        }
         const uint32_t off = (own * p.H * p.P + c0) * static_cast<uint32_t>(sizeof(T));
         if constexpr (kVec && kBF) {
           __builtin_amdgcn_raw_buffer_store_b64(v2u{pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3])}, dx, off, 0, 0);
