@@ -103,8 +103,8 @@ __global__ __launch_bounds__(kGradThreads, sizeof(T) == 2 && NMAX == 64 ? 4 : 2)
   E* const sB = lds + kB;
   E* const sC = lds + kC;
   auto stage_bc = [&]() {
-    stage_rows<T, NMAX, kGradThreads, kVec>(sB, NP, rows_of<T>(p.B, k, g, 0, p.N), tid);
-    stage_rows<T, NMAX, kGradThreads, kVec>(sC, NP, rows_of<T>(p.C, k, g, 0, p.N), tid);
+    stage_rows<T, NMAX, kGradThreads, kVec>(sB, NP, rows_of<T>(p.B, k, g, 0, p.N), tid, p.bc_vec);
+    stage_rows<T, NMAX, kGradThreads, kVec>(sC, NP, rows_of<T>(p.C, k, g, 0, p.N), tid, p.bc_vec);
   };
   stage_bc();
   __syncthreads();
@@ -664,7 +664,8 @@ hipError_t launch_ssd_packed_fwd(const ssm_ssd_packed_args& a, hipStream_t strea
   p.z = tensor(a.z, 0, a.z_seq_stride, a.z_head_stride, p.P, bf16);
   p.B = tensor(a.B, 0, a.B_seq_stride, Bg, p.N, bf16);
   p.C = tensor(a.C, 0, a.C_seq_stride, Cg, p.N, bf16);
-  p.vec = p.x.vec && p.B.vec && p.C.vec && tensor(a.out, 0, a.out_seq_stride, a.out_head_stride, p.P, bf16).vec &&
+  p.bc_vec = p.B.vec && p.C.vec;
+  p.vec = p.x.vec && p.N % 4 == 0 && tensor(a.out, 0, a.out_seq_stride, a.out_head_stride, p.P, bf16).vec &&
           (!a.z || p.z.vec);
   OutsideRows rows;
   if (a.zero_outside && a.seqlen > 0) {
@@ -693,9 +694,10 @@ hipError_t launch_ssd_bwd(const ssm_ssd_bwd_args& a, hipStream_t stream) {
   p.z = tensor(a.z, a.z_batch_stride, a.z_seq_stride, a.z_head_stride, p.P, bf16);
   p.B = tensor(a.B, a.B_batch_stride, a.B_seq_stride, Bg, p.N, bf16);
   p.C = tensor(a.C, a.C_batch_stride, a.C_seq_stride, Cg, p.N, bf16);
+  p.bc_vec = p.B.vec && p.C.vec;
   p.dout = tensor(a.dout, a.dout_batch_stride, a.dout_seq_stride, a.dout_head_stride, p.P, bf16);
   auto aligned = [](const void* ptr) { return reinterpret_cast<uintptr_t>(ptr) % 16 == 0; };
-  p.vec = p.x.vec && p.B.vec && p.C.vec && p.dout.vec && aligned(a.dx) && aligned(a.dB) && aligned(a.dC) &&
+  p.vec = p.x.vec && p.N % 4 == 0 && p.dout.vec && aligned(a.dx) && aligned(a.dB) && aligned(a.dC) &&
           (!a.z || (p.z.vec && aligned(a.dz)));
   const int64_t HP = a.nheads * a.headdim, GN = static_cast<int64_t>(p.G) * p.N;
   hipError_t e = hipSuccess;

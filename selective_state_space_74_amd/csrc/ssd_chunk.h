@@ -43,7 +43,8 @@ struct ChunkParams {
   int L, H, P, G, N, per_group, softplus;
   int nc, per_row;             // chunks; of a row
   int hb, blocks;              // heads of a workgroup, workgroups of a group
-  bool vec;                    // rows of all tensors are made of 16-byte pieces
+  bool vec;                    // rows of the heads' tensors and of states are made of 16-byte pieces
+  bool bc_vec;                 // rows of B and C are
   float* lam;                  // [nc][H] decay over a chunk
   uint32_t* state;             // [nc][H][P][N] what a chunk adds; then S_in
   uint32_t* dstate;            // the same backward; then dS_out
@@ -159,7 +160,7 @@ __device__ __forceinline__ V anew_words(V v) {
 template <typename T> constexpr int kPiece = 16 / sizeof(T);
 
 // A thread's piece of a row: columns col .. of row r; zeros past the real ones.
-// kVec: rows are made of whole 16-byte pieces (of all tensors of a call); else
+// kVec: rows are made of whole 16-byte pieces (of all tensors of a kind); else
 // element by element.
 template <typename T, bool kVec>
 __device__ __forceinline__ v4u load_piece(const Rows64& w, int r, int col) {
@@ -198,10 +199,13 @@ struct Pieces {
     for (int i = 0; i < kN; ++i) *reinterpret_cast<v4u*>(dst + (tid / kPer + i * kStep) * pitch + tid % kPer * kPiece<T>) = v[i];
   }
 };
+// vec: as kVec, found out here (a chunk's B and C are staged once for several heads,
+// and 100 states a row do not make 16-byte pieces of bf16).
 template <typename T, int W, int kThreads, bool kVec>
-__device__ __forceinline__ void stage_rows(typename Lds<T>::E* dst, int pitch, const Rows64& w, int tid) {
+__device__ __forceinline__ void stage_rows(typename Lds<T>::E* dst, int pitch, const Rows64& w, int tid, bool vec) {
   Pieces<T, W, kThreads> q;
-  q.template load<kVec>(w, tid);
+  if (kVec && vec) q.template load<true>(w, tid);
+  else q.template load<false>(w, tid);
   q.put(dst, pitch, tid);
 }
 

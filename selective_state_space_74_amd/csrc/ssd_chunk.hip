@@ -138,7 +138,7 @@ struct WeightedFrag {
 // is staged once; then for each head the rows x_s (dy_t) times their weight.  A
 // wavefront owns 16 channels of the state (fewer channels: a share of its columns).
 // Bound by memory: the states written are 4 N bytes for 2 x (64 tokens) bytes of x
-// read; 16,411 packed x 32 x 64 x 64 bf16, 5 sequences: 56 us, 3.7 TB/s.
+// read; 16,411 packed x 32 x 64 x 64 bf16, 23 sequences: 56 us, 3.7 TB/s.
 template <typename T, int NMAX, bool kVec>
 __global__ __launch_bounds__(kThreads) void ssd_states_kernel(ChunkParams p, int grid) {
   using E = typename Lds<T>::E;
@@ -162,7 +162,7 @@ __global__ __launch_bounds__(kThreads) void ssd_states_kernel(ChunkParams p, int
     if (!back && lane == 0) p.lam[static_cast<int64_t>(c) * p.H + h0 + i] = __builtin_amdgcn_exp2f(end);
   }
   const TokenTensor& m = back ? p.C : p.B;
-  stage_rows<T, NMAX, kThreads, kVec>(sM, NP, rows_of<T>(m, k, g, 0, p.N), tid);
+  stage_rows<T, NMAX, kThreads, kVec>(sM, NP, rows_of<T>(m, k, g, 0, p.N), tid, p.bc_vec);
   __syncthreads();
 
   const TokenTensor& x = back ? p.dout : p.x;
@@ -298,7 +298,7 @@ struct WalkParams {
 // not read and written again by the carry: loads are two chunks ahead, LDS in two
 // halves makes do with one barrier a chunk.  Bound by the chain of chunks, 3.8 us
 // each: 8 x 2048 x 32 x 64 x 64 bf16, both directions, 122 us, 3.4 TB/s.
-template <typename T, int NMAX, bool kVec>
+template <typename T, int NMAX>
 __global__ __launch_bounds__(kWalkThreads) void ssd_walk_kernel(ChunkParams p, WalkParams q) {
   using E = typename Lds<T>::E;
   constexpr bool kBF = sizeof(T) == 2;
@@ -359,9 +359,9 @@ __global__ __launch_bounds__(kWalkThreads) void ssd_walk_kernel(ChunkParams p, W
     const T* const dt = static_cast<const T*>(p.dt) + k.b * p.dtb + k.t0 * p.dts + h;
     a.raw = Elem<T>::load(__builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(dt), 0, 0x7fffffff, kRsrcWord3),
                           lane < k.len ? lane * static_cast<uint32_t>(p.dts) * static_cast<uint32_t>(sizeof(T)) : kNowhere);
-    a.x.template load<kVec>(rows_of<T>(x, k, h, p0, last), tid);
-    if (gate) a.z.template load<kVec>(rows_of<T>(p.z, k, h, p0, last), tid);
-    a.m.template load<kVec>(rows_of<T>(m, k, g, 0, p.N), tid);
+    a.x.template load<true>(rows_of<T>(x, k, h, p0, last), tid);
+    if (gate) a.z.template load<true>(rows_of<T>(p.z, k, h, p0, last), tid);
+    a.m.template load<true>(rows_of<T>(m, k, g, 0, p.N), tid);
   };
   auto chunk = [&](int i, Ahead& a) {
     E* const sM = lds + (i % 2) * kHalf;
@@ -386,12 +386,7 @@ __global__ __launch_bounds__(kWalkThreads) void ssd_walk_kernel(ChunkParams p, W
       v4u v;
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = kBF ? split_bf16(acc[j][e]) : __float_as_uint(acc[j][e]);
-      if constexpr (kVec) {
-        __builtin_amdgcn_raw_buffer_store_b128(v, to, place(j, 0), 0, 0);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) __builtin_amdgcn_raw_buffer_store_b32(v[e], to, place(j, e), 0, 0);
-      }
+      __builtin_amdgcn_raw_buffer_store_b128(v, to, place(j, 0), 0, 0);
       acc[j] *= through;
     }
     const int kb = (len + 15) / 16;
@@ -430,7 +425,7 @@ __global__ __launch_bounds__(kWalkThreads) void ssd_walk_kernel(ChunkParams p, W
 // are under way while one is computed.  Tiles lie so that a lane has four channels
 // of one token.  Bound by the latency of a pass (stage, barrier, products, barrier;
 // 69% of a wavefront's cycles are waits) with 16 wavefronts a compute unit: the case
-// above in 102 us, 2.7 TB/s.  Loads one pass ahead and not two: 111 us; four
+// above, gated, in 102 us, 3.4 TB/s.  Loads one pass ahead and not two: 111 us; four
 // wavefronts, each with all channels of 16 tokens: 169.
 // kDz: the gate's gradient dout y silu'(z) in place of the output.
 constexpr int kOutThreads = 512;
@@ -508,8 +503,8 @@ __global__ __launch_bounds__(kOutThreads, 4) void ssd_outputs_kernel(ChunkParams
   }
   E* const sB = sh.tiles;
   E* const sC = sh.tiles + kQ * NP;
-  stage_rows<T, NMAX, kOutThreads, kVec>(sB, NP, rows_of<T>(p.B, k, g, 0, p.N), tid);
-  stage_rows<T, NMAX, kOutThreads, kVec>(sC, NP, rows_of<T>(p.C, k, g, 0, p.N), tid);
+  stage_rows<T, NMAX, kOutThreads, kVec>(sB, NP, rows_of<T>(p.B, k, g, 0, p.N), tid, p.bc_vec);
+  stage_rows<T, NMAX, kOutThreads, kVec>(sC, NP, rows_of<T>(p.C, k, g, 0, p.N), tid, p.bc_vec);
   __syncthreads();
   // scores[sb]: lane holds s = 16 sb + 4 lq + e, t = own
   const int own = 16 * tok + lr;
@@ -713,8 +708,7 @@ namespace {
 template <typename T, int NMAX>
 void launch_walk(const ChunkParams& p, const WalkParams& q, bool backward, int64_t rows, hipStream_t stream) {
   const dim3 grid(static_cast<unsigned>(rows * p.H * q.split), backward ? 2 : 1);
-  if (p.vec) ssd_walk_kernel<T, NMAX, true><<<grid, kWalkThreads, 0, stream>>>(p, q);
-  else ssd_walk_kernel<T, NMAX, false><<<grid, kWalkThreads, 0, stream>>>(p, q);
+  ssd_walk_kernel<T, NMAX><<<grid, kWalkThreads, 0, stream>>>(p, q);
 }
 
 }  // namespace
@@ -724,8 +718,9 @@ hipError_t launch_chunk_states(const ChunkParams& p, bool bf16, bool backward, i
   // batch rows of equal length: a workgroup goes along a whole row where two
   // workgroups a compute unit remain, a head's channels in up to 4 parts.  Measured
   // on gradients, 8 x 2048 x 32 x 64 x 64 bf16: 122 us, and 95 + 84 chunk by chunk; with
-  // the channels in two parts (1024 workgroups) 194.
-  if (!p.table && p.nc > 0) {
+  // the channels in two parts (1024 workgroups) 194.  Rows of 16-byte pieces only: by
+  // elements the walk waits for its loads, 4 x 1000 x 16 x 64 x 100 bf16 168 us for 51.
+  if (!p.table && p.nc > 0 && p.vec && p.bc_vec) {
     WalkParams q{{h0, dlast}, {last, dh0}, 0, 0};
     const int64_t heads = nseq * p.H * (backward ? 2 : 1);
     for (q.cols = kPB; q.cols > 16 && heads * ((p.P + q.cols - 1) / q.cols) < 512;) q.cols /= 2;
