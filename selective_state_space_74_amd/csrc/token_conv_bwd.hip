@@ -9,9 +9,14 @@
 // the last K - 1 inputs and the K - 1 gradients that are not complete yet in
 // registers; it goes on for K - 1 tokens into the next run (their x and dout
 // come from L2).  Bound by memory, two reads and one write, and by the 160 registers
-// that leave 12 wavefronts a compute unit: 8 x 2048 x 2176 bf16 in 62 us, 3.5 TB/s.  dweight and dbias:
-// sums of a run in registers, of a workgroup's 16 runs by shuffles and LDS, and
-// of all workgroups by a second kernel, in a fixed order.
+// that leave 12 wavefronts a compute unit: 8 x 2048 x 2176 bf16 in 62 us, 3.5 TB/s.
+// dweight and dbias: sums of a run in registers, of a workgroup's 16 runs by shuffles
+// and LDS, and of all workgroups by a second kernel, in a fixed order.
+//
+// Registers grow with K, 26 a tap; with 8 they are held to 256, so that two wavefronts
+// a SIMD remain (4 x 2000 x 2176 bf16 forward and backward, K 4, 5, 6, 7 and 8: 58, 75,
+// 85, 113 and 110 us; K 8 without the bound 149).  The lambdas are always inline: called,
+// they kept a lane's arrays in memory (K 5: 240 us).
 #include "token_conv.h"
 
 namespace ssm {
@@ -34,7 +39,7 @@ struct ConvBwdParams {
 };
 
 template <typename T, int K, bool kVec>
-__global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(ConvBwdParams p) {
+__global__ __launch_bounds__(kConvThreads, K > 7 ? 2 : 1) void conv_bwd_kernel(ConvBwdParams p) {
   constexpr int V = kConvV;
   __shared__ int32_t held[kConvBounds];
   __shared__ float sums[kConvThreads / 64][kConvLanes][(K + 1) * V];
@@ -92,13 +97,13 @@ __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(ConvBwdParams p)
 #pragma unroll
       for (int v = 0; v < V; ++v) h[j][v] = pend[j][v] = 0.0f;
     auto state_at = [&](int back) { return (walk.k * p.D + c) * K + K + back; };
-    auto from_state = [&](int back, float (&v)[V]) {
+    auto from_state = [&](int back, float (&v)[V]) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < V; ++i) v[i] = p.state_in && i < nv ? p.state_in[state_at(back) + i * K] : 0.0f;
     };
     // the gradient of the input at token q of the walk's sequence (before its
     // first token: of the state) is complete
-    auto emit = [&](int q, float (&g)[V]) {
+    auto emit = [&](int q, float (&g)[V]) __attribute__((always_inline)) {
       if (!walk.inside()) return;
       const bool token = q >= walk.lo;
       if (token ? q < t0 || q >= t1 : !p.dstate_in || walk.lo < t0 || walk.lo >= t1) return;
@@ -117,11 +122,11 @@ __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(ConvBwdParams p)
       }
     };
     // the walk's sequence ends before token u: so are all its gradients
-    auto flush = [&](int u) {
+    auto flush = [&](int u) __attribute__((always_inline)) {
 #pragma unroll
       for (int j = 0; j < K - 1; ++j) emit(u - (K - 1) + j, pend[j]);
     };
-    auto begin = [&]() {   // a sequence's first token
+    auto begin = [&]() __attribute__((always_inline)) {   // a sequence's first token
 #pragma unroll
       for (int j = 0; j < K - 1; ++j) {
         if (walk.inside()) from_state(j - (K - 1), h[j + 1]);
@@ -136,7 +141,7 @@ __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(ConvBwdParams p)
     };
     // token u, its input and upstream gradient; own: one of the run's.  Leaves in
     // `done` the gradient of the input at u - (K - 1), now complete.
-    auto add = [&](const float (&xu)[V], const float (&eu)[V], bool own, float (&done)[V]) {
+    auto add = [&](const float (&xu)[V], const float (&eu)[V], bool own, float (&done)[V]) __attribute__((always_inline)) {
 #pragma unroll
       for (int j = 0; j < K - 1; ++j)
 #pragma unroll
@@ -166,7 +171,7 @@ __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(ConvBwdParams p)
 #pragma unroll
         for (int v = 0; v < V; ++v) pend[j][v] = pend[j + 1][v];
     };
-    auto token = [&](int u, const float (&xu)[V], const float (&eu)[V], bool own) {
+    auto token = [&](int u, const float (&xu)[V], const float (&eu)[V], bool own) __attribute__((always_inline)) {
       float done[V];
       add(xu, eu, own, done);
       emit(u - (K - 1), done);
@@ -188,7 +193,7 @@ __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(ConvBwdParams p)
     const T* xt = x + t0 * p.xs;
     const T* et = dout + t0 * p.es;
     T* dt = dx + (t0 - (K - 1)) * p.gs;   // where the gradient that token t completes goes
-    auto load = [&](int left) {
+    auto load = [&](int left) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {   // past the run: its last token again, not used
         const int at = left >= kAhead ? i : min(i, left - 1);
