@@ -424,7 +424,7 @@ __global__ __launch_bounds__(kWalkThreads) void ssd_walk_kernel(ChunkParams p, W
 // chunk are computed once and stay in registers for all heads; the next heads' loads
 // are under way while one is computed.  Tiles lie so that a lane has four channels
 // of one token.  Bound by the latency of a pass (stage, barrier, products, barrier;
-// 69% of a wavefront's cycles are waits) with 16 wavefronts a compute unit: the case
+// 47% of a wavefront's cycles are waits) with 16 wavefronts a compute unit: the case
 // above, gated, in 102 us, 3.4 TB/s.  Loads one pass ahead and not two: 111 us; four
 // wavefronts, each with all channels of 16 tokens: 169.
 // kDz: the gate's gradient dout y silu'(z) in place of the output.
