@@ -725,8 +725,9 @@ hipError_t launch_chunk_states(const ChunkParams& p, bool bf16, bool backward, i
     const int64_t heads = nseq * p.H * (backward ? 2 : 1);
     for (q.cols = kPB; q.cols > 16 && heads * ((p.P + q.cols - 1) / q.cols) < 512;) q.cols /= 2;
     q.split = (p.P + q.cols - 1) / q.cols;
-    // (its windows hold a head's state, its grid 2^32 threads)
-    if (heads * q.split >= 512 && heads * q.split < (int64_t{1} << 23) && static_cast<int64_t>(p.P) * p.N < (int64_t{1} << 29)) {
+    // (its windows hold a head's state and a chunk of dt, its grid 2^32 threads)
+    if (heads * q.split >= 512 && heads * q.split < (int64_t{1} << 23) && static_cast<int64_t>(p.P) * p.N < (int64_t{1} << 29) &&
+        p.dts < (int64_t{1} << 23)) {
       if (!bf16) launch_walk<float, 64>(p, q, backward, nseq, stream);
       else if (p.N > 64) launch_walk<uint16_t, 128>(p, q, backward, nseq, stream);
       else launch_walk<uint16_t, 64>(p, q, backward, nseq, stream);

@@ -97,3 +97,19 @@ def test_steps_on_pools():
     y = ssm.token_conv_update(pool, x, w, slots=at)
     assert torch.equal(y, ssm.token_conv_update(start, x, w)) and torch.equal(pool[at.long()], start)
     assert not pool[:3].any() and not pool[slots - 2].any()
+
+
+def test_steps_far_apart():
+    """dt a view whose tokens lie 2^25 values apart, where many rows are made in a
+    walk: next to the same values side by side, to the bar of a scan in fp32."""
+    b, L, H, P, N, apart = 16, 64, 16, 16, 16, 2 ** 25
+    dt = randn(1, L, H, seed=1, dtype=torch.float32)
+    wide = torch.empty((L - 1) * apart + H, device=DEV).as_strided((1, L, H), (0, apart, 1))
+    wide.copy_(dt)
+    f32 = dict(dtype=torch.float32)
+    args = dict(x=randn(b, L, H, P, seed=2, **f32), A=-torch.rand(H, device=DEV) - 0.5, B=randn(b, L, 1, N, seed=3, **f32),
+                C=randn(b, L, 1, N, seed=4, **f32))
+    dout = randn(b, L, H, P, seed=5, **f32)
+    a, w = (ssm.ssd_scan_bwd(dout, dt=v.expand(b, -1, -1), **args) for v in (dt, wide))
+    for k in a:
+        assert (a[k].double() - w[k].double()).norm() <= 1e-4 * a[k].double().norm(), k
