@@ -75,7 +75,7 @@ __global__ __launch_bounds__(kGradThreads, sizeof(T) == 2 && NMAX == 64 ? 4 : 2)
   // the small arrays first: their addresses are then offsets in the instruction
   struct Shared {
     float dl[kMostHeads][kQ], la[kMostHeads][kQ], A[kMostHeads], D[kMostHeads];
-    float row[QB][kQ], col[2][kQ], c[2][kQ], r[2][kQ], diag[kQ], m[kQ], pairs[kGradThreads / 64];
+    float row[QB][kQ], col[2][kQ], c[2][kQ], r[2][kQ], diag[kQ], m[kQ], pairs[kGradThreads / 64], dd[kGradThreads / 64];
     alignas(16) E tiles[kKeep ? kHead + 2 * kQ * NP : kHead > kEnds ? kHead : kEnds];
   };
   __shared__ __align__(16) Shared sh;
@@ -181,8 +181,11 @@ __global__ __launch_bounds__(kGradThreads, sizeof(T) == 2 && NMAX == 64 ? 4 : 2)
     load_y(h, p0);
     load_state(p.state, h, p0);
   };
-  // dy = dout, or dout silu(z), bf16 then in two parts
-  auto put_y = [&]() {
+  // dy = dout, or dout silu(z), bf16 then in two parts; and what it gives dD: of a bf16
+  // gate here, as M's diagonal would have 16 bits of dy
+  constexpr bool kOwnD = kGate && kBF;
+  [[maybe_unused]] float dd_own = 0.0f;
+  auto put_y = [&](auto first) {
     if constexpr (!kGate) {
       yv.put(sY, XP, tid);
     } else {
@@ -194,6 +197,7 @@ __global__ __launch_bounds__(kGradThreads, sizeof(T) == 2 && NMAX == 64 ? 4 : 2)
         for (int e = 0; e < kPiece<T>; ++e) {
           const float f = piece_f32<T>(yv.v[j], e) * silu_f32(piece_f32<T>(zv.v[j], e));
           s[e] = kBF ? split_bf16(f) : __float_as_uint(f);
+          if constexpr (kOwnD && decltype(first)::value) dd_own = fmaf(f, piece_f32<T>(xv.v[j], e), dd_own);
         }
         if constexpr (kBF) {
           *reinterpret_cast<v4u*>(sY + at) = v4u{highs(s[0], s[1]), highs(s[2], s[3]), highs(s[4], s[5]), highs(s[6], s[7])};
@@ -249,7 +253,7 @@ __global__ __launch_bounds__(kGradThreads, sizeof(T) == 2 && NMAX == 64 ? 4 : 2)
         load_head(h, p0);
       }
       xv.put(sX, XP, tid);
-      put_y();
+      put_y(std::true_type{});
       put_state();
       __syncthreads();
       load_state(p.dstate, h, p0);
@@ -367,6 +371,11 @@ __global__ __launch_bounds__(kGradThreads, sizeof(T) == 2 && NMAX == 64 ? 4 : 2)
       sh.c[half][own] = c_s;
     }
     if (lane == 0) sh.pairs[wave] = pairs * __builtin_amdgcn_exp2f(sh.la[i][kQ - 1]);
+    if constexpr (kOwnD) {
+      const float s = wave_sum(dd_own);
+      dd_own = 0.0f;
+      if (lane == 0) sh.dd[wave] = s;
+    }
     // dx, every other 16 channels
     for (int p0 = 0; p0 < (kOne ? 1 : p.P); p0 += kPB) {
       const int cols = p.P - p0;
@@ -374,7 +383,7 @@ __global__ __launch_bounds__(kGradThreads, sizeof(T) == 2 && NMAX == 64 ? 4 : 2)
         __syncthreads();
         load_y(h, p0);
         load_state(p.dstate, h, p0);
-        put_y();
+        put_y(std::false_type{});
         put_state();
         __syncthreads();
         if (p0 + kPB >= p.P && i + 1 < heads) load_head(h + 1, 0);
@@ -434,20 +443,29 @@ __global__ __launch_bounds__(kGradThreads, sizeof(T) == 2 && NMAX == 64 ? 4 : 2)
     }
     __syncthreads();   // the sums are there, and LDS is free
     if (wave == i) {   // the steps' gradients; written over after the next barrier
-      float row = 0.0f;
+      double row = 0.0;
 #pragma unroll
       for (int w = 0; w < QB; ++w)
         if (w <= lane / 16) row += sh.row[w][lane];
-      const float dl = sh.dl[i][lane], cs = sh.c[0][lane] + sh.c[1][lane], cl = sh.col[0][lane] + sh.col[1][lane], r = sh.r[0][lane] + sh.r[1][lane];
-      const float step = dl * (cl + cs) - row - r;
-      float g0 = 0.0f;
+      // the flow is a difference of sums over the chunk: these in 64 bits
+      const float dl = sh.dl[i][lane];
+      const double cs = static_cast<double>(sh.c[0][lane]) + sh.c[1][lane], cl = static_cast<double>(sh.col[0][lane]) + sh.col[1][lane],
+                   r = static_cast<double>(sh.r[0][lane]) + sh.r[1][lane], step = dl * (cl + cs) - row - r;
+      double g0 = 0.0;
 #pragma unroll
       for (int w = 0; w < kGradThreads / 64; ++w) g0 += sh.pairs[w];
-      const float flow = wave_sum(r) + g0 + (wave_prefix_sum(step) - step);
-      float d = cl + sh.diag[lane] + cs + sh.A[i] * flow;
+      const double flow = wave_sum64(r) + g0 + (wave_prefix_sum64(step) - step);
+      float d = static_cast<float>(cl + sh.diag[lane] + cs + sh.A[i] * flow);
       d = lane < k.len ? d * (p.softplus ? slope_of(dl) : 1.0f) : 0.0f;
       if (lane < k.len) io<T>::store(static_cast<T*>(q.ddt) + (k.b * p.L + k.t0 + lane) * p.H + h, d);
-      const float da = wave_sum(dl * flow), db = wave_sum(d), dd = wave_sum(sh.m[lane]);
+      const float da = static_cast<float>(wave_sum64(dl * flow)), db = wave_sum(d);
+      float dd = 0.0f;
+      if constexpr (kOwnD) {
+#pragma unroll
+        for (int w = 0; w < kGradThreads / 64; ++w) dd += sh.dd[w];
+      } else {
+        dd = wave_sum(sh.m[lane]);
+      }
       if (lane < 3) q.parts[(static_cast<int64_t>(lane) * p.H + h) * p.nc + c] = lane == 0 ? da : lane == 1 ? db : dd;
     }
   }
