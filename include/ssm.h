@@ -763,8 +763,8 @@ typedef struct ssm_ssd_packed_args {
  * count of chunks without cu_seqlens.  64 tokens of a tensor's rows are reached
  * through 31-bit byte windows: the limit on strides holds for x, z, B, C and dout,
  * and nheads * headdim * element size is below 2^25 (rows of dx).
- * Non-finite values stay within their sequence, as there, but may reach all tokens
- * of their chunk.
+ * A NaN or an infinity stays within its sequence (and the sums over all tokens), as
+ * there, but may reach every token of its chunk.
  * Precision: as there; the gradients of dt, A and dt_bias come from products whose
  * operands carry 16 bits at least, that of D from fp32.
  * Aliasing: no output may overlap an input, another output or the workspace.

@@ -546,8 +546,11 @@ struct SumParams {
   float *dA, *dbias, *dD;
   void *dB, *dC;
 };
-template <typename T>
+// kV: values of a lane, 4 where rows allow it.
+template <typename T, int kV>
 __global__ __launch_bounds__(kThreads) void ssd_sum_parts_kernel(SumParams p) {
+  struct alignas(kV * 4) Part { float e[kV]; };
+  struct alignas(kV * sizeof(T)) Out { T e[kV]; };
   if (blockIdx.x < 3u * p.H) {
     __shared__ float sums[kWaves];
     const int h = blockIdx.x / 3, which = blockIdx.x % 3;
@@ -569,11 +572,18 @@ __global__ __launch_bounds__(kThreads) void ssd_sum_parts_kernel(SumParams p) {
   const int id = blockIdx.x - 3 * p.H, step = (gridDim.x - 3 * p.H) / 2;
   const float* const from = p.bc + (id & 1) * p.blocks * p.n;
   T* const to = static_cast<T*>(id & 1 ? p.dC : p.dB);
-  for (int64_t i = static_cast<int64_t>(id >> 1) * kThreads + threadIdx.x; i < p.n; i += static_cast<int64_t>(step) * kThreads) {
+  for (int64_t i = (static_cast<int64_t>(id >> 1) * kThreads + threadIdx.x) * kV; i < p.n; i += static_cast<int64_t>(step) * kThreads * kV) {
     if (i < lo || i >= hi) continue;
-    float s = 0.0f;
-    for (int b = 0; b < p.blocks; ++b) s += from[b * p.n + i];
-    io<T>::store(to + i, s);
+    float s[kV] = {};
+    for (int b = 0; b < p.blocks; ++b) {
+      const Part v = *reinterpret_cast<const Part*>(from + b * p.n + i);
+#pragma unroll
+      for (int e = 0; e < kV; ++e) s[e] += v.e[e];
+    }
+    Out o;
+#pragma unroll
+    for (int e = 0; e < kV; ++e) io<T>::store(&o.e[e], s[e]);
+    *reinterpret_cast<Out*>(to + i) = o;
   }
 }
 
@@ -751,10 +761,14 @@ hipError_t launch_ssd_bwd(const ssm_ssd_bwd_args& a, hipStream_t stream) {
   }
   SumParams m{reinterpret_cast<float*>(ws + l.parts), reinterpret_cast<float*>(ws + l.bc), a.cu_seqlens, a.nseq, a.seqlen,
               a.batch * a.seqlen * GN, GN, p.nc, p.H, p.blocks, a.dA, a.ddt_bias, a.dD, a.dB, a.dC};
-  const int64_t more = q.nc > 0 && q.blocks > 1 ? 2 * std::min<int64_t>((m.n + kThreads - 1) / kThreads, 4096) : 0;
+  const bool four = GN % 4 == 0 && aligned(a.dB) && aligned(a.dC);
+  const int64_t per = kThreads * (four ? 4 : 1);
+  const int64_t more = q.nc > 0 && q.blocks > 1 ? 2 * std::min<int64_t>((m.n + per - 1) / per, 4096) : 0;
   const unsigned grid = static_cast<unsigned>(3 * a.nheads + more);
-  if (bf16) ssd_sum_parts_kernel<uint16_t><<<grid, kThreads, 0, stream>>>(m);
-  else ssd_sum_parts_kernel<float><<<grid, kThreads, 0, stream>>>(m);
+  if (bf16 && four) ssd_sum_parts_kernel<uint16_t, 4><<<grid, kThreads, 0, stream>>>(m);
+  else if (bf16) ssd_sum_parts_kernel<uint16_t, 1><<<grid, kThreads, 0, stream>>>(m);
+  else if (four) ssd_sum_parts_kernel<float, 4><<<grid, kThreads, 0, stream>>>(m);
+  else ssd_sum_parts_kernel<float, 1><<<grid, kThreads, 0, stream>>>(m);
   return hipGetLastError();
 }
 
