@@ -535,7 +535,10 @@ __global__ __launch_bounds__(kOutThreads, 4) void ssd_outputs_kernel(ChunkParams
   // what a pass (64 channels of a head) needs, loaded kDepth passes ahead.  Loads and
   // stores are issued whether or not there is anything to take or leave (their offsets
   // then lie nowhere), so that a wait can count them and leave the later ones in flight.
-  constexpr int kDepth = kBF && NMAX == 64 && !kDz ? 2 : 1;
+  // Two ahead where 128 registers hold them: not for rows by elements (5000 packed x 16
+  // x 33 x 64 bf16: whole call 111 us for 77) nor with dout besides (104 and 108 us at
+  // 8 x 2048 x 32 x 64 x 64).
+  constexpr int kDepth = kBF && NMAX == 64 && kVec && !kDz ? 2 : 1;
   constexpr int kTiles = kPB / 32;
   const int of_head = (p.P + kPB - 1) / kPB, passes = heads * of_head;
   struct Ahead {
