@@ -74,7 +74,8 @@ __global__ __launch_bounds__(kGradThreads, sizeof(T) == 2 && NMAX == 64 ? 4 : 2)
   constexpr int kB = kKeep ? kHead : 0, kC = kB + kQ * NP, kG = kKeep ? 0 : 2 * kQ * NP;
   // the small arrays first: their addresses are then offsets in the instruction
   struct Shared {
-    float dl[kMostHeads][kQ], la[kMostHeads][kQ], A[kMostHeads], D[kMostHeads];
+    double la[kMostHeads][kQ];
+    float dl[kMostHeads][kQ], A[kMostHeads], D[kMostHeads];
     float row[QB][kQ], col[2][kQ], c[2][kQ], r[2][kQ], diag[kQ], m[kQ], pairs[kGradThreads / 64], dd[kGradThreads / 64];
     alignas(16) E tiles[kKeep ? kHead + 2 * kQ * NP : kHead > kEnds ? kHead : kEnds];
   };
@@ -239,8 +240,9 @@ __global__ __launch_bounds__(kGradThreads, sizeof(T) == 2 && NMAX == 64 ? 4 : 2)
   load_head(h0, 0);
   for (int i = 0; i < heads; ++i) {
     const int h = h0 + i;
-    const float la_s = sh.la[i][own], dl_s = sh.dl[i][own];
-    const float ew = __builtin_amdgcn_exp2f(sh.la[i][kQ - 1] - la_s), ea = __builtin_amdgcn_exp2f(la_s);
+    const double la_s = sh.la[i][own];
+    const float dl_s = sh.dl[i][own];
+    const float ew = decay_of(sh.la[i][kQ - 1] - la_s), ea = decay_of(la_s);
     const float Dh = sh.D[i];
     v4f M[kTiles];
 #pragma unroll
@@ -285,13 +287,13 @@ __global__ __launch_bounds__(kGradThreads, sizeof(T) == 2 && NMAX == 64 ? 4 : 2)
         auto tile = [&](int j, auto on_diagonal) {
           constexpr bool kDiag = decltype(on_diagonal)::value;
           const int tb = block_of(j);
-          const v4f la_t = *reinterpret_cast<const v4f*>(&sh.la[i][16 * tb + 4 * lq]);
+          const v4d la_t = *reinterpret_cast<const v4d*>(&sh.la[i][16 * tb + 4 * lq]);
           float w[4], diag = 0.0f, m0 = 0.0f;
           v4f rows;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int over = 4 * lq + e - lr;   // t - s on the diagonal's tile
-            float L = __builtin_amdgcn_exp2f(la_t[e] - la_s), m = M[j][e];
+            float L = decay_of(la_t[e] - la_s), m = M[j][e];
             if constexpr (kDiag) {
               L = over >= 0 ? L : 0.0f;
               m = over >= 0 ? m : 0.0f;
@@ -370,7 +372,7 @@ __global__ __launch_bounds__(kGradThreads, sizeof(T) == 2 && NMAX == 64 ? 4 : 2)
       sh.r[half][own] = r_t;
       sh.c[half][own] = c_s;
     }
-    if (lane == 0) sh.pairs[wave] = pairs * __builtin_amdgcn_exp2f(sh.la[i][kQ - 1]);
+    if (lane == 0) sh.pairs[wave] = pairs * decay_of(sh.la[i][kQ - 1]);
     if constexpr (kOwnD) {
       const float s = wave_sum(dd_own);
       dd_own = 0.0f;

@@ -92,26 +92,56 @@ __device__ __forceinline__ Rows64 rows_of(const TokenTensor& t, const Chunk& k, 
   return w;
 }
 
+// Sums over the lanes up to each, in 64 bits.
+template <int kCtrl, int kRows = 0xf>
+__device__ __forceinline__ double dpp0(double v) {
+  const v2u w = __builtin_bit_cast(v2u, v);
+  return __builtin_bit_cast(double, v2u{static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(w[0]), kCtrl, kRows, 0xf, false)),
+                                        static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(w[1]), kCtrl, kRows, 0xf, false))});
+}
+__device__ __forceinline__ double wave_prefix_sum64(double v) {
+  v += dpp0<0x111>(v);
+  v += dpp0<0x112>(v);
+  v += dpp0<0x114>(v);
+  v += dpp0<0x118>(v);
+  v += dpp0<0x142, 0xa>(v);
+  v += dpp0<0x143, 0xc>(v);
+  return v;
+}
+__device__ __forceinline__ double lane_value(double v, int lane) {
+  const v2u w = __builtin_bit_cast(v2u, v);
+  return __builtin_bit_cast(double, v2u{static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(w[0]), lane)),
+                                        static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(w[1]), lane))});
+}
+__device__ __forceinline__ double wave_sum64(double v) { return lane_value(wave_prefix_sum64(v), 63); }
+
 // Step sizes of a chunk, one token a lane: Delta (0 past the end), and the sums of
-// A Delta up to each token in units of log 2.
+// A Delta up to each token in units of log 2.  These are of 64 bits: a decay is a
+// difference of two, and one large step (a model that drops its state) would take the
+// low bits of every later sum of the chunk in 32 (after a step of 1000 at A = -16
+// outputs 1.4e-4 off, and 2.4e-7 now).
 struct Steps {
-  float delta, la;
+  float delta;
+  double la;
 };
+// The decay between two sums.
+__device__ __forceinline__ float decay_of(double difference) { return __builtin_amdgcn_exp2f(static_cast<float>(difference)); }
 // What they take of a head, read once: a load within a loop would wait for those
 // ahead of it.
 struct StepHead {
-  float a2, bias;
+  double a2;
+  float bias;
   int softplus;
 };
 __device__ __forceinline__ StepHead step_head(const ChunkParams& p, int h) {
-  return StepHead{p.A[h] * kLog2e, p.bias ? p.bias[h] : 0.0f, p.softplus};
+  return StepHead{p.A[h] * 1.4426950408889634, p.bias ? p.bias[h] : 0.0f, p.softplus};
 }
 // v: the lane's step before its bias.
 __device__ __forceinline__ Steps steps_from(const StepHead& q, float v, int len, int lane) {
   Steps s;
   v += q.bias;
   s.delta = lane < len ? (q.softplus ? softplus_close_f32(v) : v) : 0.0f;
-  s.la = wave_prefix_sum(s.delta) * q.a2;
+  s.la = wave_prefix_sum64(s.delta) * q.a2;
   return s;
 }
 template <typename T>
@@ -135,28 +165,6 @@ __device__ __forceinline__ float lane_value(float v, int lane) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
 }
 __device__ __forceinline__ float wave_sum(float v) { return lane_value(wave_prefix_sum(v), 63); }
-
-// Sums over the lanes up to each, in 64 bits.
-template <int kCtrl, int kRows = 0xf>
-__device__ __forceinline__ double dpp0(double v) {
-  const v2u w = __builtin_bit_cast(v2u, v);
-  return __builtin_bit_cast(double, v2u{static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(w[0]), kCtrl, kRows, 0xf, false)),
-                                        static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(w[1]), kCtrl, kRows, 0xf, false))});
-}
-__device__ __forceinline__ double wave_prefix_sum64(double v) {
-  v += dpp0<0x111>(v);
-  v += dpp0<0x112>(v);
-  v += dpp0<0x114>(v);
-  v += dpp0<0x118>(v);
-  v += dpp0<0x142, 0xa>(v);
-  v += dpp0<0x143, 0xc>(v);
-  return v;
-}
-__device__ __forceinline__ double wave_sum64(double v) {
-  const v2u w = __builtin_bit_cast(v2u, wave_prefix_sum64(v));
-  return __builtin_bit_cast(double, v2u{static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(w[0]), 63)),
-                                        static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(w[1]), 63))});
-}
 
 // ---- tiles in LDS ---------------------------------------------------------------
 

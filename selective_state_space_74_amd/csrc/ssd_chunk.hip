@@ -157,9 +157,9 @@ __global__ __launch_bounds__(kThreads) void ssd_states_kernel(ChunkParams p, int
 
   for (int i = wave; i < heads; i += kWaves) {
     const Steps s = steps_of<T>(p, k, h0 + i, lane);
-    const float end = lane_value(s.la, 63);
-    sW[i][lane] = back ? __builtin_amdgcn_exp2f(s.la) : __builtin_amdgcn_exp2f(end - s.la) * s.delta;
-    if (!back && lane == 0) p.lam[static_cast<int64_t>(c) * p.H + h0 + i] = __builtin_amdgcn_exp2f(end);
+    const double end = lane_value(s.la, 63);
+    sW[i][lane] = back ? decay_of(s.la) : decay_of(end - s.la) * s.delta;
+    if (!back && lane == 0) p.lam[static_cast<int64_t>(c) * p.H + h0 + i] = decay_of(end);
   }
   const TokenTensor& m = back ? p.C : p.B;
   stage_rows<T, NMAX, kThreads, kVec>(sM, NP, rows_of<T>(m, k, g, 0, p.N), tid, p.bc_vec);
@@ -368,8 +368,8 @@ __global__ __launch_bounds__(kWalkThreads) void ssd_walk_kernel(ChunkParams p, W
     E* const sX = sM + kQ * NP;
     const int len = a.len;
     const Steps s = steps_from(steps, Elem<T>::f32(a.raw), len, lane);
-    const float end = lane_value(s.la, 63);
-    const float w = dir ? __builtin_amdgcn_exp2f(s.la) : __builtin_amdgcn_exp2f(end - s.la) * s.delta;
+    const double end = lane_value(s.la, 63);
+    const float w = dir ? decay_of(s.la) : decay_of(end - s.la) * s.delta;
     a.m.put(sM, NP, tid);
     auto weight = [&](int r) { return __shfl(w, r, 64); };
     if (gate) put_weighted<T, true>(sX, XP, a.x, a.z, weight, tid);
@@ -380,7 +380,7 @@ __global__ __launch_bounds__(kWalkThreads) void ssd_walk_kernel(ChunkParams p, W
     const int64_t c = static_cast<int64_t>(b) * p.per_row + (dir ? p.per_row - 1 - i : i);
     const __amdgpu_buffer_rsrc_t to =
         __builtin_amdgcn_make_buffer_rsrc(state + (c * p.H + h) * p.P * p.N, 0, p.P * p.N * 4, kRsrcWord3);
-    const float through = __builtin_amdgcn_exp2f(end);
+    const float through = decay_of(end);
 #pragma unroll
     for (int j = 0; j < kMost; ++j) {
       v4u v;
@@ -483,7 +483,8 @@ __global__ __launch_bounds__(kOutThreads, 4) void ssd_outputs_kernel(ChunkParams
   constexpr int kPad = 16 / sizeof(E), NP = NMAX + kPad, XP = kPB + kPad, NT = NMAX / 16, QB = kQ / 16;
   constexpr int kScores = 2 * kQ * NP, kHead = kQ * XP + (kBF ? 2 : 1) * kPB * NP;
   struct Shared {
-    float dl[kMostHeads][kQ], la[kMostHeads][kQ], D[kMostHeads];
+    double la[kMostHeads][kQ];
+    float dl[kMostHeads][kQ], D[kMostHeads];
     alignas(16) E tiles[kScores > kHead ? kScores : kHead];
   };
   __shared__ __align__(16) Shared sh;
@@ -570,23 +571,23 @@ __global__ __launch_bounds__(kOutThreads, 4) void ssd_outputs_kernel(ChunkParams
     const int i = s / of_head, h = h0 + i, p0 = s % of_head * kPB, cols = s < passes ? p.P - p0 : 0;
     if (p0 == 0 && cols > 0) {
       // weighted scores of the head, as operands; those above the diagonal are zero
-      const float la_t = sh.la[i][own];
+      const double la_t = sh.la[i][own];
 #pragma unroll
       for (int sb = 0; sb < QB; ++sb) {
         mf[sb] = tofrag<T>(0.0f, 0.0f, 0.0f, 0.0f);
         if (sb > tok) continue;
-        const v4f la_s = *reinterpret_cast<const v4f*>(&sh.la[i][16 * sb + 4 * lq]);
+        const v4d la_s = *reinterpret_cast<const v4d*>(&sh.la[i][16 * sb + 4 * lq]);
         const v4f dl_s = *reinterpret_cast<const v4f*>(&sh.dl[i][16 * sb + 4 * lq]);
         float m[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) m[e] = scores[sb][e] * __builtin_amdgcn_exp2f(la_t - la_s[e]) * dl_s[e];
+        for (int e = 0; e < 4; ++e) m[e] = scores[sb][e] * decay_of(la_t - la_s[e]) * dl_s[e];
         if (sb == tok) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) m[e] = 4 * lq + e <= lr ? m[e] : 0.0f;
         }
         mf[sb] = tofrag<T>(m[0], m[1], m[2], m[3]);
       }
-      ea = __builtin_amdgcn_exp2f(la_t);
+      ea = decay_of(la_t);
       Dh = sh.D[i];
     }
     a.x.put(sX, XP, tid);

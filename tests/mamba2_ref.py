@@ -161,7 +161,8 @@ def ssd_step(state, x, dt, A, B, C, D=None, z=None, bias=None, softplus_on=True,
 CHUNK = 64   # tokens of the kernels' chunks, from each sequence's first on
 
 
-def ssd_scan(x, dt, A, B, C, D=None, z=None, bias=None, softplus_on=True, h0=None, cu=None, dout=None, dlast=None, io="f32"):
+def ssd_scan(x, dt, A, B, C, D=None, z=None, bias=None, softplus_on=True, h0=None, cu=None, dout=None, dlast=None, io="f32",
+             sharp=False):
     """({name: value}, {name: bound}) of the Mamba-2 SSM over whole sequences and,
     with dout, of its gradients, token by token.  Arrays are (batch, L, H, P) and
     so on, or without the batch axis with cu.
@@ -175,7 +176,13 @@ def ssd_scan(x, dt, A, B, C, D=None, z=None, bias=None, softplus_on=True, h0=Non
     halves is off by 2^-16 of its size, two of them in a row by 2^-15; a rounded
     operand by 2^-8: the weighted scores (out, dx, dB, dC), the state in dx, and a
     gated dout in dx, dB and dC.  The flow through a step's decay is a difference
-    of prefix sums over its chunk: 20 U of all that they sum."""
+    of prefix sums over its chunk: 20 U of all that they sum.
+
+    sharp: bounds that large steps elsewhere in a chunk leave as they are.  A term
+    whose decay is e^-E is off by E (2 U + the steps' own relative error) of itself,
+    whatever the other steps of the chunk: its exponent is rounded once, and again
+    where a chunk ends (sums that carry E along end in x below).  The flow through a
+    step is then a sum of terms which cross that step, and off by e of those alone."""
     packed = cu is not None
     lift = lambda t: None if t is None else (np.asarray(t, np.float64)[None] if packed else np.asarray(t, np.float64))  # noqa: E731
     x, dt, B, C, z, dout = (lift(t) for t in (x, dt, B, C, z, dout))
@@ -197,22 +204,28 @@ def ssd_scan(x, dt, A, B, C, D=None, z=None, bias=None, softplus_on=True, h0=Non
         L = hi - lo
         h = zero(H, P, N) if h0 is None else np.asarray(h0, np.float64)[k]
         hm = np.abs(h)
+        hx = np.zeros_like(h)
         delta, alpha, ed, _ = step_parts(dt[r, lo:hi], bias, A, softplus_on)
         amax = max((np.abs(A * delta[c:c + CHUNK].sum(0)).max() for c in range(0, L, CHUNK)), default=0)
-        e = (20 * amax + 6 + N + P + 64 + 4 * (L // CHUNK + 1) + 60) * U + (ed.max() if L else 0)
+        e = ((0 if sharp else 20 * amax) + 6 + N + P + 64 + 4 * (L // CHUNK + 1) + 60) * U + (ed.max() if L else 0)
+        ex = 2 * U + ed.max() if sharp and L else 0.0
+        rate = (np.abs(A * delta) if sharp else zero(L, H))[..., None, None]       # (L, H, 1, 1)
         Br, Cr = (np.repeat(t[r, lo:hi], each, 1)[:, :, None] for t in (B, C))      # (L, H, 1, N)
         xr = x[r, lo:hi][..., None]                                                # (L, H, P, 1)
-        hs, hms, y, ym = [h], [hm], zero(L, H, P), zero(L, H, P)
+        hs, hms, hxs, y, ym, yx = [h], [hm], [hx], zero(L, H, P), zero(L, H, P), zero(L, H, P)
         for t in range(L):
             add = delta[t][:, None, None] * xr[t] * Br[t]
             h = alpha[t][:, None, None] * h + add
+            hx = alpha[t][:, None, None] * (hx + rate[t] * hm)
             hm = alpha[t][:, None, None] * hm + np.abs(add)
             hs.append(h)
             hms.append(hm)
+            hxs.append(hx)
+            yx[t] = (hx * np.abs(Cr[t])).sum(-1)
             y[t], ym[t] = (h * Cr[t]).sum(-1), (hm * np.abs(Cr[t])).sum(-1)
-        val["last"][k], bnd["last"][k] = h, (e + split) * hm
+        val["last"][k], bnd["last"][k] = h, (e + split) * hm + ex * hx
         full = y + col(Dh) * x[r, lo:hi]
-        efull = (e + split + half) * ym + 3 * U * (np.abs(col(Dh) * x[r, lo:hi]) + ym)
+        efull = (e + split + half) * ym + ex * yx + 3 * U * (np.abs(col(Dh) * x[r, lo:hi]) + ym)
         s = None if z is None else sigmoid(z[r, lo:hi])
         gate = 1.0 if z is None else z[r, lo:hi] * s
         eg = 0.0 if z is None else (2 * np.abs(z[r, lo:hi]) + 9) * U
@@ -231,6 +244,7 @@ def ssd_scan(x, dt, A, B, C, D=None, z=None, bias=None, softplus_on=True, h0=Non
         dy = d * gate
         dh = zero(H, P, N) if dlast is None else np.asarray(dlast, np.float64)[k]
         dhm = np.abs(dh)
+        dhx, flowx, toxx = np.zeros_like(dh), zero(L, H), zero(L, H)
         flow, flowm, tox, toxm, terms = (zero(L, H) for _ in range(5))
         ends = {}
         for t in range(L - 1, -1, -1):
@@ -241,29 +255,35 @@ def ssd_scan(x, dt, A, B, C, D=None, z=None, bias=None, softplus_on=True, h0=Non
             dCm = (m[..., None] * hms[t + 1]).sum(1)
             dh = dh + dy[t][..., None] * Cr[t]
             dhm = dhm + m[..., None] * np.abs(Cr[t])
-            to_x, to_xm = (dh * Br[t]).sum(-1), (dhm * np.abs(Br[t])).sum(-1)
+            dCx = (m[..., None] * hxs[t + 1]).sum(1)
+            to_x, to_xm, to_xx = (dh * Br[t]).sum(-1), (dhm * np.abs(Br[t])).sum(-1), (dhx * np.abs(Br[t])).sum(-1)
+            dBx = col(delta[t]) * (dhx * np.abs(xr[t])).sum(1)
             dB = col(delta[t]) * (dh * xr[t]).sum(1)
             dBm = col(delta[t]) * (dhm * np.abs(xr[t])).sum(1)
             flow[t] = (dh * hs[t]).sum((-1, -2)) * alpha[t]
             flowm[t] = (dhm * hms[t]).sum((-1, -2)) * alpha[t]
+            flowx[t] = (dhx * hms[t] + dhm * hxs[t] + rate[t] * dhm * hms[t]).sum((-1, -2)) * alpha[t]
+            toxx[t] = (to_xx * np.abs(x[r, lo + t])).sum(-1)
             tox[t], toxm[t] = (to_x * x[r, lo + t]).sum(-1), (to_xm * np.abs(x[r, lo + t])).sum(-1)
             terms[t] = delta[t] * toxm[t] + (m * ym[t]).sum(-1)
             val["dx"][r, lo + t] = col(delta[t]) * to_x + col(Dh) * dy[t]
-            bnd["dx"][r, lo + t] = (es + 2 * half + gated) * col(delta[t]) * to_xm + (gated + es) * np.abs(col(Dh) * dy[t])
-            for which, v, vm in (("dB", dB, dBm), ("dC", dC, dCm)):
+            bnd["dx"][r, lo + t] = (es + 2 * half + gated) * col(delta[t]) * to_xm + (gated + es) * np.abs(col(Dh) * dy[t]) + \
+                ex * col(delta[t]) * to_xx
+            for which, v, vm, vx in (("dB", dB, dBm, dBx), ("dC", dC, dCm, dCx)):
                 val[which][r, lo + t] = v.reshape(G, each, N).sum(1)
-                bnd[which][r, lo + t] = ((es + half + gated + each * U) * vm).reshape(G, each, N).sum(1)
+                bnd[which][r, lo + t] = ((es + half + gated + each * U) * vm + ex * vx).reshape(G, each, N).sum(1)
+            dhx = alpha[t][:, None, None] * (dhx + rate[t] * dhm)
             dh, dhm = alpha[t][:, None, None] * dh, alpha[t][:, None, None] * dhm
         total = np.stack([terms[c:c + CHUNK].sum(0) + ends[c // CHUNK] for c in range(0, L, CHUNK)]) if L else zero(0, H)
-        eflow = es * flowm + 20 * U * np.repeat(total, CHUNK, 0)[:L]
+        eflow = es * flowm + (ex * flowx if sharp else 20 * U * np.repeat(total, CHUNK, 0)[:L])
         slope = sigmoid(dt[r, lo:hi] + (0 if bias is None else bias)) if softplus_on else np.ones((L, H))
         dd = tox + A * flow
-        edd = es * toxm + np.abs(A) * eflow + 3 * U * (toxm + np.abs(A) * flowm)
+        edd = es * toxm + ex * toxx + np.abs(A) * eflow + 3 * U * (toxm + np.abs(A) * flowm)
         val["ddt"][r, lo:hi] = dd * slope
         pre = np.abs(dt[r, lo:hi] + (0 if bias is None else bias))
         pre = np.where(slope > 0, pre, 0)   # no step at all: nothing to be off
         bnd["ddt"][r, lo:hi] = edd * slope + np.abs(dd) * slope * (2 * pre + 8) * U
-        val["dh0"][k], bnd["dh0"][k] = dh, es * dhm
+        val["dh0"][k], bnd["dh0"][k] = dh, es * dhm + ex * dhx
         val["dA"] += (delta * flow).sum(0)
         bnd["dA"] += (delta * (eflow + (ed + U * (tokens / 64 + 70)) * flowm)).sum(0)
         val["ddt_bias"] += (dd * slope).sum(0)
