@@ -127,15 +127,27 @@ __device__ __forceinline__ float dpp0(float v) {
   return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), kCtrl, kRowMask, 0xf, true));
 }
 
-// Inclusive prefix sum over the 64 lanes of a wavefront in registers: row
-// shifts by 1, 2, 4 and 8 sum each 16-lane row, then row_bcast:15 adds row
-// 0's total to row 1 and row 2's to row 3, and row_bcast:31 adds lane 31's
-// (rows 0 and 1) to rows 2 and 3.
-__device__ __forceinline__ float wave_prefix_sum(float v) {
+// Inclusive prefix sums over each 16 lanes: row shifts by 1, 2, 4 and 8.
+__device__ __forceinline__ float row_prefix_sum(float v) {
   v += dpp0<0x111>(v);         // row_shr:1
   v += dpp0<0x112>(v);         // row_shr:2
   v += dpp0<0x114>(v);         // row_shr:4
-  v += dpp0<0x118>(v);         // row_shr:8
+  return v + dpp0<0x118>(v);   // row_shr:8
+}
+
+// The same from each 16 lanes' end: row shifts the other way.
+__device__ __forceinline__ float row_suffix_sum(float v) {
+  v += dpp0<0x101>(v);         // row_shl:1
+  v += dpp0<0x102>(v);         // row_shl:2
+  v += dpp0<0x104>(v);         // row_shl:4
+  return v + dpp0<0x108>(v);   // row_shl:8
+}
+
+// Inclusive prefix sum over the 64 lanes of a wavefront in registers: each
+// 16-lane row, then row_bcast:15 adds row 0's total to row 1 and row 2's to
+// row 3, and row_bcast:31 adds lane 31's (rows 0 and 1) to rows 2 and 3.
+__device__ __forceinline__ float wave_prefix_sum(float v) {
+  v = row_prefix_sum(v);
   v += dpp0<0x142, 0xa>(v);    // row_bcast:15 into rows 1 and 3
   v += dpp0<0x143, 0xc>(v);    // row_bcast:31 into rows 2 and 3
   return v;

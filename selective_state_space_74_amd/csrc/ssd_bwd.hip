@@ -14,9 +14,14 @@
 // to s or after:
 //   g_s = sum_{t >= s} sum_{u < s} K[t,u] Delta_u + sum_{t >= s} r_t + sum_{u < s} c_u Delta_u
 //         + e^{a_end} <S_in, dS_out>
-// whose differences are sums of K's columns and rows without its diagonal:
-//   g_{s+1} - g_s = Delta_s (sum_{t > s} K[t,s] + c_s) - sum_{u < s} K[s,u] Delta_u - r_s
 //   dDelta_s = sum_{t >= s} K[t,s] + c_s + A g_s,   dA = sum Delta_s g_s,
+// Every term of g_s has the decay of step s in it.  All 64 could be had as running sums
+// of row and column sums of K, but a step that drops the state would then leave the
+// rounding of the whole chunk where next to nothing flows (with every 8th step 100 at
+// A = -16, dA 4e-4 off).  So nothing is subtracted: the rectangle t >= s, u < s of K
+// Delta is made of row sums over the 16 u of a block, added over t >= s (blocks of u
+// before s's), column sums over the blocks of t after s's, added over u < s, and of the
+// tile on the diagonal, where sums down its columns are added along its rows.
 //   ddt = dDelta softplus'(dt + bias),   dD = sum_t M[t,t]
 // For bf16 IO K comes from products of the inputs as they are (dy, where it is gated,
 // as a bf16 value and its remainder, as are S_in and dS_out), so these sums carry 16
@@ -76,7 +81,9 @@ __global__ __launch_bounds__(kGradThreads, sizeof(T) == 2 && NMAX == 64 ? 4 : 2)
   struct Shared {
     double la[kMostHeads][kQ];
     float dl[kMostHeads][kQ], A[kMostHeads], D[kMostHeads];
-    float row[QB][kQ], col[2][kQ], c[2][kQ], r[2][kQ], diag[kQ], m[kQ], pairs[kGradThreads / 64], dd[kGradThreads / 64];
+    // of a token: K Delta of its block's rectangle; sums over K's column in its block, and
+    // below (by the wavefronts' halves); M's diagonal, where that gives dD
+    float in_block[kQ], col[kQ], below[2][kQ], m[kGate && kBF ? 1 : kQ], pairs[kGradThreads / 64], dd[kGradThreads / 64];
     alignas(16) E tiles[kKeep ? kHead + 2 * kQ * NP : kHead > kEnds ? kHead : kEnds];
   };
   __shared__ __align__(16) Shared sh;
@@ -166,6 +173,11 @@ __global__ __launch_bounds__(kGradThreads, sizeof(T) == 2 && NMAX == 64 ? 4 : 2)
   E* const sS = lds + kS;
   [[maybe_unused]] E* const sSl = lds + kSl;
   E* const sGl = lds + kGl;   // [s][t]
+  // four more sums a token lie behind its rows (two workgroups then fit a compute unit):
+  // r and c of both halves behind x, K Delta's row over each block before it behind dy
+  auto sums_rc = [&](int t) { return reinterpret_cast<float*>(sX + t * XP + kPB); };
+  auto sums_row = [&](int t) { return reinterpret_cast<float*>(sY + t * XP + kPB); };
+  static_assert(kPad * sizeof(E) == 4 * sizeof(float), "four floats behind a row");
   using Tokens = Pieces<T, kPB, kGradThreads>;
   using States = StatePieces<T, NMAX, kGradThreads>;
   Tokens xv, yv, zv;
@@ -283,12 +295,12 @@ __global__ __launch_bounds__(kGradThreads, sizeof(T) == 2 && NMAX == 64 ? 4 : 2)
       if (kOne || p0 + kPB >= p.P) {
         // M is complete: K, its sums, and the operands of dx; only the diagonal's tile
         // (half 0, its first) has elements above it
-        float col = 0.0f;
+        float below = 0.0f;
         auto tile = [&](int j, auto on_diagonal) {
           constexpr bool kDiag = decltype(on_diagonal)::value;
           const int tb = block_of(j);
           const v4d la_t = *reinterpret_cast<const v4d*>(&sh.la[i][16 * tb + 4 * lq]);
-          float w[4], diag = 0.0f, m0 = 0.0f;
+          float w[4], in_col = 0.0f, m0 = 0.0f;
           v4f rows;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -302,23 +314,32 @@ __global__ __launch_bounds__(kGradThreads, sizeof(T) == 2 && NMAX == 64 ? 4 : 2)
             if constexpr (kDiag) w[e] = over >= 0 ? w[e] : 0.0f;
             sum[j][e] = fmaf(m * L, dl_s, sum[j][e]);
             float K = w[e] * m;
+            (kDiag ? in_col : below) += K;
             if constexpr (kDiag) {
-              diag += over == 0 ? K : 0.0f;
               m0 += over == 0 ? m : 0.0f;
               K = over > 0 ? K : 0.0f;
             }
             rows[e] = K * dl_s;
-            col += K;
           }
           *reinterpret_cast<F*>(sGl + own * GP + 16 * tb + 4 * lq) = tofrag<T>(w[0], w[1], w[2], w[3]);
+          if constexpr (kDiag) {   // down the column from t on, then along the row up to t
+#pragma unroll
+            for (int e = 2; e >= 0; --e) rows[e] += rows[e + 1];
+            const RowPair near = row_pair<16>(rows[0]);
+            const float pair = row_pair<32>(near.first + near.second).second;
+            const float under = (lq & 1 ? 0.0f : near.second) + (lq & 2 ? 0.0f : pair);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) rows[e] = lr < 4 * lq + e ? rows[e] + under : 0.0f;
+          }
           const float s = row_sums(rows, lane);
-          if (lr < 4) sh.row[tok][16 * tb + 4 * lq + lr] = s;
+          const int t = 16 * tb + anew(4 * lq + lr);
+          if (lr < 4) (kDiag ? sh.in_block[t] : sums_row(t)[tok]) = s;
           if constexpr (kDiag) {
-            diag = quarter_sum(diag);
-            m0 = quarter_sum(m0);
-            if (lq == 0) {
-              sh.diag[own] = diag;
-              sh.m[own] = m0;
+            in_col = quarter_sum(in_col);
+            if (lq == 0) sh.col[own] = in_col;
+            if constexpr (!(kGate && kBF)) {
+              m0 = quarter_sum(m0);
+              if (lq == 0) sh.m[own] = m0;
             }
           }
         };
@@ -327,8 +348,8 @@ __global__ __launch_bounds__(kGradThreads, sizeof(T) == 2 && NMAX == 64 ? 4 : 2)
 #pragma unroll
         for (int j = 1; j < kTiles; ++j)
           if (block_of(j) < QB) tile(j, std::false_type{});
-        col = quarter_sum(col);
-        if (lq == 0) sh.col[half][own] = col;
+        below = quarter_sum(below);
+        if (lq == 0) sh.below[half][own] = below;
       }
       // S_in^T dy_t: lane holds states 16 n + 4 lq + e
 #pragma unroll
@@ -369,8 +390,9 @@ __global__ __launch_bounds__(kGradThreads, sizeof(T) == 2 && NMAX == 64 ? 4 : 2)
     c_s = quarter_sum(c_s) * ew;
     pairs = wave_sum(pairs);
     if (lq == 0) {
-      sh.r[half][own] = r_t;
-      sh.c[half][own] = c_s;
+      float* const to = sums_rc(anew(own)) + half;
+      to[0] = r_t;
+      to[2] = c_s;
     }
     if (lane == 0) sh.pairs[wave] = pairs * decay_of(sh.la[i][kQ - 1]);
     if constexpr (kOwnD) {
@@ -445,32 +467,46 @@ __global__ __launch_bounds__(kGradThreads, sizeof(T) == 2 && NMAX == 64 ? 4 : 2)
     }
     __syncthreads();   // the sums are there, and LDS is free
     if (wave == i) {   // the steps' gradients; written over after the next barrier
-      double row = 0.0;
-#pragma unroll
-      for (int w = 0; w < QB; ++w)
-        if (w <= lane / 16) row += sh.row[w][lane];
-      // the flow is a difference of sums over the chunk: these in 64 bits
-      const float dl = sh.dl[i][lane];
-      const double cs = static_cast<double>(sh.c[0][lane]) + sh.c[1][lane], cl = static_cast<double>(sh.col[0][lane]) + sh.col[1][lane],
-                   r = static_cast<double>(sh.r[0][lane]) + sh.r[1][lane], step = dl * (cl + cs) - row - r;
-      double g0 = 0.0;
+      const int me = anew(lane);
+      const float dl = sh.dl[i][me];
+      float g0 = 0.0f;
 #pragma unroll
       for (int w = 0; w < kGradThreads / 64; ++w) g0 += sh.pairs[w];
-      const double flow = wave_sum64(r) + g0 + (wave_prefix_sum64(step) - step);
-      float d = static_cast<float>(cl + sh.diag[lane] + cs + sh.A[i] * flow);
-      d = lane < k.len ? d * (p.softplus ? slope_of(dl) : 1.0f) : 0.0f;
-      if (lane < k.len) io<T>::store(static_cast<T*>(q.ddt) + (k.b * p.L + k.t0 + lane) * p.H + h, d);
-      const float da = static_cast<float>(wave_sum64(dl * flow)), db = wave_sum(d);
+      // from the lane's token on: sums over its block, and the totals of later blocks
+      const int block = me / 16;
+      const float* const of_block = sums_row(me);
+      const float r = row_suffix_sum(sums_rc(me)[0] + sums_rc(me)[1]);
+      const float u0 = row_suffix_sum(block > 0 ? of_block[0] : 0.0f), u1 = row_suffix_sum(block > 1 ? of_block[1] : 0.0f),
+                  u2 = row_suffix_sum(block > 2 ? of_block[2] : 0.0f);
+      const float r3 = lane_value(r, 48), r23 = lane_value(r, 32) + r3, u03 = lane_value(u0, 48);
+      const float later = block == 0   ? lane_value(r, 16) + r23
+                          : block == 1 ? r23 + (lane_value(u0, 32) + u03)
+                          : block == 2 ? r3 + (u03 + lane_value(u1, 48))
+                                       : 0.0f;
+      const float after = (r + u0) + (u1 + u2) + sh.in_block[me] + later;
+      // and of the tokens before the lane's
+      auto c_of = [&](int u) { return sums_rc(u)[2] + sums_rc(u)[3]; };
+      auto below_of = [&](int u) { return sh.below[0][u] + sh.below[1][u]; };
+      const int u = max(me - 1, 0);
+      const float dl_u = me ? sh.dl[i][u] : 0.0f;
+      const float flow = after + wave_prefix_sum(me ? c_of(u) * dl_u : 0.0f) +
+                         row_prefix_sum(me % 16 ? below_of(u) * dl_u : 0.0f) + g0;
+      float d = sh.col[me] + below_of(me) + c_of(me) + sh.A[i] * flow;
+      d = me < k.len ? d * (p.softplus ? slope_of(dl) : 1.0f) : 0.0f;
+      if (me < k.len) io<T>::store(static_cast<T*>(q.ddt) + (k.b * p.L + k.t0 + me) * p.H + h, d);
+      const float da = wave_sum(dl * flow), db = wave_sum(d);
       float dd = 0.0f;
       if constexpr (kOwnD) {
 #pragma unroll
         for (int w = 0; w < kGradThreads / 64; ++w) dd += sh.dd[w];
       } else {
-        dd = wave_sum(sh.m[lane]);
+        dd = wave_sum(sh.m[me]);
       }
-      if (lane < 3) q.parts[(static_cast<int64_t>(lane) * p.H + h) * p.nc + c] = lane == 0 ? da : lane == 1 ? db : dd;
+      if (me < 3) q.parts[(static_cast<int64_t>(me) * p.H + h) * p.nc + c] = me == 0 ? da : me == 1 ? db : dd;
     }
   }
+
+  __syncthreads();   // the last head's sums lie in the tiles' rows
 
   // dB and dC of the chunk: the products with C and B, over the sum of the heads
   E* const sG = lds + kG;   // [t][s]

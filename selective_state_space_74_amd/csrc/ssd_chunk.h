@@ -113,7 +113,6 @@ __device__ __forceinline__ double lane_value(double v, int lane) {
   return __builtin_bit_cast(double, v2u{static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(w[0]), lane)),
                                         static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(w[1]), lane))});
 }
-__device__ __forceinline__ double wave_sum64(double v) { return lane_value(wave_prefix_sum64(v), 63); }
 
 // Step sizes of a chunk, one token a lane: Delta (0 past the end), and the sums of
 // A Delta up to each token in units of log 2.  These are of 64 bits: a decay is a
@@ -320,10 +319,26 @@ __device__ __forceinline__ float elem(const typename Frag<T>::V& v, int e) {
   else return v[e];
 }
 
+// Rows of 16 lanes, two at a time: the first and the second of each pair, in both
+// (kOver 16: rows 0 and 1, 2 and 3; 32: rows 0 and 2, 1 and 3).
+struct RowPair {
+  float first, second;
+};
+template <int kOver>
+__device__ __forceinline__ RowPair row_pair(float v) {
+  const uint32_t w = __float_as_uint(v);
+  if constexpr (kOver == 16) {
+    const auto q = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+    return RowPair{__uint_as_float(q[0]), __uint_as_float(q[1])};
+  } else {
+    const auto q = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+    return RowPair{__uint_as_float(q[0]), __uint_as_float(q[1])};
+  }
+}
 // Sum over the four lanes that hold a tile's column (or row), 16 lanes apart.
 __device__ __forceinline__ float quarter_sum(float v) {
-  v += __shfl_xor(v, 16, 64);
-  return v + __shfl_xor(v, 32, 64);
+  const RowPair near = row_pair<16>(v), far = row_pair<32>(near.first + near.second);
+  return far.first + far.second;
 }
 
 // Four values a lane, summed over each 16-lane row: lane lr gets value lr % 4.
