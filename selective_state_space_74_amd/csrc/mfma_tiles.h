@@ -2,6 +2,8 @@
 // 16-wide tiles, products, and sums over a wavefront.
 #pragma once
 
+#include <type_traits>
+
 #include "ssm_internal.h"
 
 namespace ssm {
@@ -37,13 +39,37 @@ template <typename T> struct Frag;
 template <> struct Frag<uint16_t> { using V = v4s; };
 template <> struct Frag<float> { using V = v4f; };
 
+// Sums of the bf16 k = 16 form, a type of their own: they must not go on from the
+// k = 32 form's directly.  The compiler puts no wait between the two where the second
+// reads the first's result as its sum, and the shorter one then takes part of it too
+// early: with small integers 128 of 256 values were wrong right behind each other, none
+// with 16 wait states between, nor the other way round or within one form, whichever
+// registers hold the sums.
+struct Sum16 {
+  v4f v;
+};
+template <typename T> struct SumOf { using V = v4f; };
+template <> struct SumOf<uint16_t> { using V = Sum16; };
+__device__ __forceinline__ float value_of(const v4f& c, int i) { return c[i]; }
+__device__ __forceinline__ float value_of(const Sum16& c, int i) { return c.v[i]; }
+
 template <typename T>
-__device__ __forceinline__ v4f mma16(typename Frag<T>::V a, typename Frag<T>::V b, v4f c) {
+__device__ __forceinline__ typename SumOf<T>::V mma16(typename Frag<T>::V a, typename Frag<T>::V b, typename SumOf<T>::V c) {
   if constexpr (sizeof(T) == 2) {
-    return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(a, b, c, 0, 0, 0);
+    return Sum16{__builtin_amdgcn_mfma_f32_16x16x16bf16_1k(a, b, c.v, 0, 0, 0)};
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], b[i], c, 0, 0, 0);
+    return c;
+  }
+}
+// Sums made some other way, to go on with in mma16.
+template <typename T>
+__device__ __forceinline__ typename SumOf<T>::V go_on_16(v4f c) {
+  if constexpr (sizeof(T) == 2) {
+    asm volatile("s_nop 15" : "+v"(c));
+    return Sum16{c};
+  } else {
     return c;
   }
 }
@@ -64,6 +90,9 @@ __device__ __forceinline__ v4f mma32(v4s a0, v4s a1, v4s b0, v4s b1, v4f c) {
   return mma32(__builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7),
                __builtin_shufflevector(b0, b1, 0, 1, 2, 3, 4, 5, 6, 7), c);
 }
+
+// One form's sums are not the other's argument.
+static_assert(!std::is_convertible_v<v4f, Sum16> && !std::is_convertible_v<Sum16, v4f>);
 
 // Four consecutive LDS elements (8 or 16 bytes, aligned) as a fragment.
 template <typename T>

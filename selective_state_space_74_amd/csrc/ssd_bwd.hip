@@ -224,8 +224,7 @@ __global__ __launch_bounds__(kGradThreads, sizeof(T) == 2 && NMAX == 64 ? 4 : 2)
   auto put_state = [&]() { sv.put(sS, kBF ? sSl : sS, NP, tid); };
   auto held = [&](uint32_t v) { return kBF ? joined_bf16(v) : __uint_as_float(v); };
   // a 16 x 16 tile of the state (rows n, k = channel) times x or dy of `own`, whose
-  // rows are in X (remainders in Xl); the remainders' products in the k = 32 form
-  // too: sums whose chain of products mixed it with the k = 16 form came out wrong
+  // rows are in X (remainders in Xl); the remainders' products in the k = 32 form too
   auto state_tile = [&](int n, int kbs, const E* X, [[maybe_unused]] const E* Xl, auto with_rest) {
     v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
     if constexpr (kBF) {
@@ -522,19 +521,25 @@ __global__ __launch_bounds__(kGradThreads, sizeof(T) == 2 && NMAX == 64 ? 4 : 2)
     for (int e = 0; e < 4; ++e) sG[(16 * tb + 4 * lq + e) * GP + own] = Lds<T>::from(sum[j][e]);
   }
   __syncthreads();
+  typename SumOf<T>::V to_b[NH], to_c[NH];
+#pragma unroll
+  for (int n = 0; n < NH; ++n) {
+    to_b[n] = go_on_16<T>(dB[n]);
+    to_c[n] = go_on_16<T>(dC[n]);
+  }
 #pragma unroll
   for (int tb = 0; tb < QB; ++tb) {
     if (tb >= tok) {
       const F gf = frag_along<T>(sGt, GP, 16 * tok, 16 * tb, lr, lq);
 #pragma unroll
       for (int n = 0; n < NH; ++n)
-        if (n0 + n < nt) dB[n] = mma16<T>(frag_down<T>(sC, NP, 16 * tb, 16 * (n0 + n), lr, lq), gf, dB[n]);
+        if (n0 + n < nt) to_b[n] = mma16<T>(frag_down<T>(sC, NP, 16 * tb, 16 * (n0 + n), lr, lq), gf, to_b[n]);
     }
     if (tb <= tok) {
       const F gf = frag_along<T>(sG, GP, 16 * tok, 16 * tb, lr, lq);
 #pragma unroll
       for (int n = 0; n < NH; ++n)
-        if (n0 + n < nt) dC[n] = mma16<T>(frag_down<T>(sB, NP, 16 * tb, 16 * (n0 + n), lr, lq), gf, dC[n]);
+        if (n0 + n < nt) to_c[n] = mma16<T>(frag_down<T>(sB, NP, 16 * tb, 16 * (n0 + n), lr, lq), gf, to_c[n]);
     }
   }
   if (own >= k.len) return;
@@ -545,7 +550,9 @@ __global__ __launch_bounds__(kGradThreads, sizeof(T) == 2 && NMAX == 64 ? 4 : 2)
     if (s0 >= p.N) continue;
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
-      const v4f v = which ? dC[n] : dB[n];
+      v4f v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = value_of(which ? to_c[n] : to_b[n], e);
       if (p.blocks > 1) {
         float* const to = (which ? q.dCparts : q.dBparts) + block * q.tokens * p.G * p.N + at + s0;
         if constexpr (kVec) {

@@ -509,9 +509,9 @@ void ssd_fwd_kernel(SsdParams p) {
     {
       const int tb = 16 * wave;
       const float la_t = sLa[tb + lr];
-      v4f y1[PB];
+      typename SumOf<T>::V y1[PB];
 #pragma unroll
-      for (int q = 0; q < PB; ++q) y1[q] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int q = 0; q < PB; ++q) y1[q] = {};
       for (int sbk = 0; sbk <= wave; ++sbk) {
         // scores G[s][t] for s in block sbk, t in block wave: A = B (row s,
         // k = n), B operand = C^T (k = n, column t)
@@ -583,7 +583,7 @@ void ssd_fwd_kernel(SsdParams p) {
           float xval;
           if constexpr (kBF) xval = L::f(static_cast<uint16_t>(xq[i]));
           else xval = L::f(sXT[pl][tl]);
-          float y = fmaf(ea[i], y2[q][i], y1[q][i]);
+          float y = fmaf(ea[i], y2[q][i], value_of(y1[q], i));
           y = fmaf(Dh, xval, y);
           const float gz = silu_f32(Elem<T>::f32(zr[q][i]));
           y *= zg ? gz : 1.0f;
