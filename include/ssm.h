@@ -671,7 +671,8 @@ typedef struct ssm_token_conv_update_args {
  *            h / (nheads / ngroups); ngroups 0 or 1 is one group.
  *   A, D, dt_bias : (nheads) fp32; D and dt_bias NULL mean 0.
  *   slots  : as in ssm_token_conv_update_args.
- * Sizes: batch at most 65535, nheads * headdim * dstate below 2^31;
+ * Sizes: batch at most 65535, nheads * headdim * dstate below 2^31, nheads *
+ * ceil(headdim / 64) at most 2^26 - 4 (SSM_ERR_UNSUPPORTED past that);
  * 1 <= dstate <= SSM_MAX_SSD_STEP_DSTATE.
  * Aliasing: out and state must not overlap any input or each other. */
 typedef struct ssm_ssd_update_args {

@@ -319,6 +319,8 @@ int ssm_validate_ssd_update(const ssm_ssd_update_args* a) {
   if (a->dstate > SSM_MAX_SSD_STEP_DSTATE || a->batch > 65535 || a->nheads > most / a->headdim ||
       a->nheads * a->headdim > most / a->dstate)
     return SSM_ERR_UNSUPPORTED;
+  // a launch has less than 2^32 threads, a wavefront for up to 64 channels of a head
+  if (a->nheads * ((a->headdim + 63) / 64) > (int64_t{1} << 26) - 4) return SSM_ERR_UNSUPPORTED;
   if (a->batch == 0) return SSM_OK;
   const int64_t esz = io_size(a->io_dtype), Bt = a->batch, H = a->nheads, P = a->headdim, N = a->dstate, S = a->nslots;
   const int64_t G = groups_of(a->ngroups);

@@ -1,0 +1,15 @@
+"""Sizes at the edge of what the Mamba-2 layer's launches can run: what passes the
+host-side checks fits a grid (less than 2^32 threads) and the kernels' index types,
+what does not is refused.  No GPU is touched."""
+import selective_state_space_74_amd as ssm
+from test_mamba2_abi_cpu import OK, UNSUP, ssd_step
+
+
+def test_step_heads_fill_a_grid():
+    """Four wavefronts a workgroup of 256: 2^24 - 1 workgroups hold 2^26 - 4 heads of up to 64 channels."""
+    most = (1 << 26) - 4
+    for P in (1, 8):
+        assert ssm.validate_ssd_update(ssd_step(H=most, P=P, G=1, N=1)) == OK
+        assert ssm.validate_ssd_update(ssd_step(H=most + 1, P=P, G=1, N=1)) == UNSUP
+    assert ssm.validate_ssd_update(ssd_step(H=1 << 24, P=100, G=1, N=1)) == OK
+    assert ssm.validate_ssd_update(ssd_step(H=(1 << 31) - 1, P=1, G=1, N=1)) == UNSUP
