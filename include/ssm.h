@@ -672,8 +672,8 @@ typedef struct ssm_token_conv_update_args {
  *   A, D, dt_bias : (nheads) fp32; D and dt_bias NULL mean 0.
  *   slots  : as in ssm_token_conv_update_args.
  * Sizes: batch at most 65535, nheads * headdim * dstate below 2^31, nheads *
- * ceil(headdim / 64) at most 2^26 - 4 (SSM_ERR_UNSUPPORTED past that);
- * 1 <= dstate <= SSM_MAX_SSD_STEP_DSTATE.
+ * ceil(headdim / 64) at most 2^26 - 4, headdim at most 2^30
+ * (SSM_ERR_UNSUPPORTED past that); 1 <= dstate <= SSM_MAX_SSD_STEP_DSTATE.
  * Aliasing: out and state must not overlap any input or each other. */
 typedef struct ssm_ssd_update_args {
   int64_t batch, nslots, nheads, headdim, ngroups, dstate;

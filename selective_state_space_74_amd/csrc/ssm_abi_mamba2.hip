@@ -316,7 +316,8 @@ int ssm_validate_ssd_update(const ssm_ssd_update_args* a) {
     return SSM_ERR_SHAPE;
   if (bad_dtype(a->io_dtype)) return SSM_ERR_DTYPE;
   const int64_t most = (int64_t{1} << 31) - 1;
-  if (a->dstate > SSM_MAX_SSD_STEP_DSTATE || a->batch > 65535 || a->nheads > most / a->headdim ||
+  // headdim: the kernel counts rows in 32 bits, up to a wavefront's share past the last
+  if (a->dstate > SSM_MAX_SSD_STEP_DSTATE || a->batch > 65535 || a->headdim > int64_t{1} << 30 || a->nheads > most / a->headdim ||
       a->nheads * a->headdim > most / a->dstate)
     return SSM_ERR_UNSUPPORTED;
   // a launch has less than 2^32 threads, a wavefront for up to 64 channels of a head

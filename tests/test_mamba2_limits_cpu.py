@@ -13,3 +13,12 @@ def test_step_heads_fill_a_grid():
         assert ssm.validate_ssd_update(ssd_step(H=most + 1, P=P, G=1, N=1)) == UNSUP
     assert ssm.validate_ssd_update(ssd_step(H=1 << 24, P=100, G=1, N=1)) == OK
     assert ssm.validate_ssd_update(ssd_step(H=(1 << 31) - 1, P=1, G=1, N=1)) == UNSUP
+
+
+def test_step_rows_stay_within_ints():
+    """Rows are counted in 32 bits up to a wavefront's share, 128 at most, past the last one."""
+    for N in (1, 2):
+        assert ssm.validate_ssd_update(ssd_step(batch=1, H=1, P=1 << 29, G=1, N=N)) == OK
+    assert ssm.validate_ssd_update(ssd_step(batch=1, H=1, P=1 << 30, G=1, N=1)) == OK
+    assert ssm.validate_ssd_update(ssd_step(batch=1, H=1, P=(1 << 30) + 1, G=1, N=1)) == UNSUP
+    assert ssm.validate_ssd_update(ssd_step(batch=1, H=1, P=(1 << 31) - 1, G=1, N=1)) == UNSUP
