@@ -577,7 +577,7 @@ __global__ __launch_bounds__(kGradThreads, sizeof(T) == 2 && NMAX == 64 ? 4 : 2)
   }
 }
 
-// What the workgroups left in parts, each sum in a fixed order.  Workgroups 0 .. 3 H - 1:
+// What the workgroups left in parts, each sum in a fixed order.  The first workgroups:
 // dA, ddt_bias and dD of a head, over its chunks; the others, where a group's heads
 // were several workgroups': dB and dC (packed: only for tokens of a sequence; the
 // others' rows are cleared elsewhere).  One launch for both: each would take 4 us
@@ -588,6 +588,7 @@ struct SumParams {
   const int32_t* cu;
   int64_t nseq, L, n, row; // elements of dB (and of dC), and of a token of theirs
   int nc, H, blocks;
+  int of_heads;            // workgroups for the 3 H sums over chunks
   float *dA, *dbias, *dD;
   void *dB, *dC;
 };
@@ -596,17 +597,20 @@ template <typename T, int kV>
 __global__ __launch_bounds__(kThreads) void ssd_sum_parts_kernel(SumParams p) {
   struct alignas(kV * 4) Part { float e[kV]; };
   struct alignas(kV * sizeof(T)) Out { T e[kV]; };
-  if (blockIdx.x < 3u * p.H) {
+  if (static_cast<int>(blockIdx.x) < p.of_heads) {
     __shared__ float sums[kWaves];
-    const int h = blockIdx.x / 3, which = blockIdx.x % 3;
-    const float* const from = p.parts + (static_cast<int64_t>(which) * p.H + h) * p.nc;
-    float s = 0.0f;
-    for (int c = threadIdx.x; c < p.nc; c += kThreads) s += from[c];
-    s = wave_sum(s);
-    if (threadIdx.x % 64 == 0) sums[threadIdx.x / 64] = s;
-    __syncthreads();
-    float* const to = which == 0 ? p.dA : which == 1 ? p.dbias : p.dD;
-    if (threadIdx.x == 0 && to) to[h] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+    for (int i = blockIdx.x; i < 3 * p.H; i += p.of_heads) {
+      const int h = i / 3, which = i % 3;
+      const float* const from = p.parts + (static_cast<int64_t>(which) * p.H + h) * p.nc;
+      float s = 0.0f;
+      for (int c = threadIdx.x; c < p.nc; c += kThreads) s += from[c];
+      s = wave_sum(s);
+      if (threadIdx.x % 64 == 0) sums[threadIdx.x / 64] = s;
+      __syncthreads();
+      float* const to = which == 0 ? p.dA : which == 1 ? p.dbias : p.dD;
+      if (threadIdx.x == 0 && to) to[h] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+      __syncthreads();
+    }
     return;
   }
   int64_t lo = 0, hi = p.n;
@@ -614,7 +618,7 @@ __global__ __launch_bounds__(kThreads) void ssd_sum_parts_kernel(SumParams p) {
     lo = min(max(int64_t{p.cu[0]}, int64_t{0}), p.L) * p.row;
     hi = min(max(int64_t{p.cu[p.nseq]}, int64_t{0}), p.L) * p.row;
   }
-  const int id = blockIdx.x - 3 * p.H, step = (gridDim.x - 3 * p.H) / 2;
+  const int id = blockIdx.x - p.of_heads, step = (gridDim.x - p.of_heads) / 2;
   const float* const from = p.bc + (id & 1) * p.blocks * p.n;
   T* const to = static_cast<T*>(id & 1 ? p.dC : p.dB);
   for (int64_t i = (static_cast<int64_t>(id >> 1) * kThreads + threadIdx.x) * kV; i < p.n; i += static_cast<int64_t>(step) * kThreads * kV) {
@@ -805,11 +809,11 @@ hipError_t launch_ssd_bwd(const ssm_ssd_bwd_args& a, hipStream_t stream) {
     if (e != hipSuccess) return e;
   }
   SumParams m{reinterpret_cast<float*>(ws + l.parts), reinterpret_cast<float*>(ws + l.bc), a.cu_seqlens, a.nseq, a.seqlen,
-              a.batch * a.seqlen * GN, GN, p.nc, p.H, p.blocks, a.dA, a.ddt_bias, a.dD, a.dB, a.dC};
+              a.batch * a.seqlen * GN, GN, p.nc, p.H, p.blocks, std::min(3 * p.H, 1 << 20), a.dA, a.ddt_bias, a.dD, a.dB, a.dC};
   const bool four = GN % 4 == 0 && aligned(a.dB) && aligned(a.dC);
   const int64_t per = kThreads * (four ? 4 : 1);
   const int64_t more = q.nc > 0 && q.blocks > 1 ? 2 * std::min<int64_t>((m.n + per - 1) / per, 4096) : 0;
-  const unsigned grid = static_cast<unsigned>(3 * a.nheads + more);
+  const unsigned grid = static_cast<unsigned>(m.of_heads + more);
   if (bf16 && four) ssd_sum_parts_kernel<uint16_t, 4><<<grid, kThreads, 0, stream>>>(m);
   else if (bf16) ssd_sum_parts_kernel<uint16_t, 1><<<grid, kThreads, 0, stream>>>(m);
   else if (four) ssd_sum_parts_kernel<float, 4><<<grid, kThreads, 0, stream>>>(m);
