@@ -583,9 +583,9 @@ typedef struct ssm_cached_update_args {
  *                the sequence is shorter), NULL: not wanted.  It is the state
  *                that ssm_token_conv_update continues from.
  * Sizes: zero sizes are no-ops, but that empty sequences still set state_out;
- * seqlen below 2^31 - 64, dim at most 2^26, nseq below 2^29, and batch *
- * ceil(seqlen / 16) * ceil(dim / 64) below 2^28 (SSM_ERR_UNSUPPORTED past
- * that).
+ * seqlen below 2^31 - 64, dim at most 2^26, nseq below 2^29, and
+ * ceil(batch * ceil(seqlen / 16) / 16) * ceil(dim / 64) at most 2^24 - 257
+ * (SSM_ERR_UNSUPPORTED past that).
  * Precision: fp32 arithmetic; out is rounded once.
  * Aliasing: out and state_out must not overlap any input or each other. */
 typedef struct ssm_token_conv_args {

@@ -43,9 +43,12 @@ int check_conv(const Args* a) {
   if (bad_dtype(a->io_dtype)) return SSM_ERR_DTYPE;
   if (a->d_conv > SSM_MAX_CONV || a->seqlen > kMaxSeqlen || a->dim > kMaxDim) return SSM_ERR_UNSUPPORTED;
   if (a->cu_seqlens && a->nseq >= kMaxPacked) return SSM_ERR_UNSUPPORTED;
-  // a launch has less than 2^32 threads
-  const int64_t blocks = max((a->seqlen + 15) / 16, int64_t{1}) * max((a->dim + 63) / 64, int64_t{1});
-  return a->batch > ((int64_t{1} << 28) - 1) / blocks ? SSM_ERR_UNSUPPORTED : SSM_OK;
+  // a launch has less than 2^32 threads: 2^24 - 1 workgroups, 256 of them for sequences
+  // without tokens at most, the others of 16 runs (of 16 tokens or more where there are
+  // many) by 64 channels
+  const int64_t per_row = max((a->seqlen + 15) / 16, int64_t{1}), cols = max((a->dim + 63) / 64, int64_t{1});
+  if (a->batch > (int64_t{1} << 28) / per_row) return SSM_ERR_UNSUPPORTED;
+  return (a->batch * per_row + 15) / 16 > ((int64_t{1} << 24) - 257) / cols ? SSM_ERR_UNSUPPORTED : SSM_OK;
 }
 
 // No output may share bytes with an input or with another output.
