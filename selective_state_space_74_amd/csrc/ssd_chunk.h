@@ -92,28 +92,6 @@ __device__ __forceinline__ Rows64 rows_of(const TokenTensor& t, const Chunk& k, 
   return w;
 }
 
-// Sums over the lanes up to each, in 64 bits.
-template <int kCtrl, int kRows = 0xf>
-__device__ __forceinline__ double dpp0(double v) {
-  const v2u w = __builtin_bit_cast(v2u, v);
-  return __builtin_bit_cast(double, v2u{static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(w[0]), kCtrl, kRows, 0xf, false)),
-                                        static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(w[1]), kCtrl, kRows, 0xf, false))});
-}
-__device__ __forceinline__ double wave_prefix_sum64(double v) {
-  v += dpp0<0x111>(v);
-  v += dpp0<0x112>(v);
-  v += dpp0<0x114>(v);
-  v += dpp0<0x118>(v);
-  v += dpp0<0x142, 0xa>(v);
-  v += dpp0<0x143, 0xc>(v);
-  return v;
-}
-__device__ __forceinline__ double lane_value(double v, int lane) {
-  const v2u w = __builtin_bit_cast(v2u, v);
-  return __builtin_bit_cast(double, v2u{static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(w[0]), lane)),
-                                        static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(w[1]), lane))});
-}
-
 // Step sizes of a chunk, one token a lane: Delta (0 past the end), and the sums of
 // A Delta up to each token in units of log 2.  These are of 64 bits: a decay is a
 // difference of two, and one large step (a model that drops its state) would take the
@@ -123,8 +101,6 @@ struct Steps {
   float delta;
   double la;
 };
-// The decay between two sums.
-__device__ __forceinline__ float decay_of(double difference) { return __builtin_amdgcn_exp2f(static_cast<float>(difference)); }
 // What they take of a head, read once: a load within a loop would wait for those
 // ahead of it.
 struct StepHead {

@@ -138,7 +138,7 @@ void ssd_fwd_kernel(SsdParams p) {
   // carries the fp32 state to about 16 bits (two bf16 products)
   __shared__ __align__(16) E sHL[kBP][kBF ? NMAX : 1][kPB];
   __shared__ __align__(16) float sDl[kQ];      // Delta_s (0 past the end)
-  __shared__ __align__(16) float sLa[kQ];      // a_t * log2(e)
+  __shared__ __align__(16) double sLa[kQ];     // a_t * log2(e)
   // segmented passes (kept in LDS, not in registers across the chunk loop):
   __shared__ float sRed[kWaves];               // per-wavefront state maxima (pass 2 check)
   __shared__ float sHin[kWaves];               // per-wavefront maxima of |h_in| (pass 2)
@@ -451,16 +451,19 @@ void ssd_fwd_kernel(SsdParams p) {
       const float x = Elem<T>::f32(st.dt) + bias;
       float dl = kSoftplus ? softplus_f32(x) : x;
       dl = tv ? dl : 0.0f;
-      const float cum = wave_prefix_sum(dl);
-      const float la = cum * a2;
-      const float last = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(la), 63));
+      // 64 bits: a decay is a difference of two sums, and one large step would take
+      // the low bits of every later sum of the chunk in 32 (after a step of 1000 at
+      // A = -16 outputs 1.3e-4 off)
+      const double cum = wave_prefix_sum64(dl);
+      const double la = cum * a2;
+      const double last = lane_value(la, 63);
       if constexpr (kSegd) {
         // segmented: read at the next chunk's top and after the loop, past
         // this chunk's barriers
-        const float csum = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(cum), 63));
-        if (tid == 0) sSum += static_cast<double>(csum);
+        const double csum = lane_value(cum, 63);
+        if (tid == 0) sSum += csum;
       }
-      const float w = __builtin_amdgcn_exp2f(last - la) * dl;   // exp(a_{Q-1} - a_s) Delta_s
+      const float w = decay_of(last - la) * dl;   // exp(a_{Q-1} - a_s) Delta_s
       w_row = __shfl(w, srow, 64);
       if (wave == 0) {
         sDl[lane] = dl;
@@ -508,7 +511,7 @@ void ssd_fwd_kernel(SsdParams p) {
     // ---- outputs of tokens 16 w .. 16 w + 15 ----
     {
       const int tb = 16 * wave;
-      const float la_t = sLa[tb + lr];
+      const double la_t = sLa[tb + lr];
       typename SumOf<T>::V y1[PB];
 #pragma unroll
       for (int q = 0; q < PB; ++q) y1[q] = {};
@@ -529,13 +532,13 @@ void ssd_fwd_kernel(SsdParams p) {
         }
         // mask and scale: lane holds s = 16 sbk + 4 lq + i, t = tb + lr
         const int s0 = 16 * sbk + 4 * lq;
-        const float4 la_s = *reinterpret_cast<const float4*>(&sLa[s0]);
+        const v4d la_s = *reinterpret_cast<const v4d*>(&sLa[s0]);
         const float4 dl_s = *reinterpret_cast<const float4*>(&sDl[s0]);
         const int t = tb + lr;
-        const float m0 = s0 + 0 <= t ? sc[0] * __builtin_amdgcn_exp2f(la_t - la_s.x) * dl_s.x : 0.0f;
-        const float m1 = s0 + 1 <= t ? sc[1] * __builtin_amdgcn_exp2f(la_t - la_s.y) * dl_s.y : 0.0f;
-        const float m2 = s0 + 2 <= t ? sc[2] * __builtin_amdgcn_exp2f(la_t - la_s.z) * dl_s.z : 0.0f;
-        const float m3 = s0 + 3 <= t ? sc[3] * __builtin_amdgcn_exp2f(la_t - la_s.w) * dl_s.w : 0.0f;
+        const float m0 = s0 + 0 <= t ? sc[0] * decay_of(la_t - la_s[0]) * dl_s.x : 0.0f;
+        const float m1 = s0 + 1 <= t ? sc[1] * decay_of(la_t - la_s[1]) * dl_s.y : 0.0f;
+        const float m2 = s0 + 2 <= t ? sc[2] * decay_of(la_t - la_s[2]) * dl_s.z : 0.0f;
+        const float m3 = s0 + 3 <= t ? sc[3] * decay_of(la_t - la_s[3]) * dl_s.w : 0.0f;
         // intra: A = M (row t, k = s), B operand = x (k = s, column p) of
         // every channel block
         const auto mf = tofrag<T>(m0, m1, m2, m3);
@@ -568,9 +571,8 @@ void ssd_fwd_kernel(SsdParams p) {
       const __amdgpu_buffer_rsrc_t ro = window(og, p.osl, p.P - p0, t0);
       const uint32_t oend = static_cast<uint32_t>(std::min(p.L - 1 - t0, kQ - 1)) * p.osl +
                             (p.P - p0) * ES;
-      const float4 la_o = *reinterpret_cast<const float4*>(&sLa[tb + 4 * lq]);
-      const float ea[4] = {__builtin_amdgcn_exp2f(la_o.x), __builtin_amdgcn_exp2f(la_o.y),
-                           __builtin_amdgcn_exp2f(la_o.z), __builtin_amdgcn_exp2f(la_o.w)};
+      const v4d la_o = *reinterpret_cast<const v4d*>(&sLa[tb + 4 * lq]);
+      const float ea[4] = {decay_of(la_o[0]), decay_of(la_o[1]), decay_of(la_o[2]), decay_of(la_o[3])};
 #pragma unroll
       for (int q = 0; q < PB; ++q) {
         const int pl = kPB * q + lr;
@@ -596,7 +598,7 @@ void ssd_fwd_kernel(SsdParams p) {
 
     // ---- state update: H_out^T = exp(a_last) H_in^T + (w x)^T B ----
     {
-      const float decay = __builtin_amdgcn_exp2f(sLa[kQ - 1]);
+      const float decay = decay_of(sLa[kQ - 1]);
 #pragma unroll
       for (int j = 0; j < NBW; ++j) {
         const int m = wave + kWaves * j;

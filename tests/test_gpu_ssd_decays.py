@@ -88,3 +88,16 @@ def test_after_a_large_step_as_before_it(big):
     off["dA"] = np.linalg.norm(f64(got["dA"]) - val["dA"]) / np.linalg.norm(val["dA"])
     print(f"[{big}] {off}", flush=True)
     assert max(off.values()) <= 1e-5, off
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("where,big", PATTERNS, ids=lambda v: str(v))
+def test_batched(where, big, io):
+    """The batched prefill, along a row."""
+    t = scan((2, 150), 4, 64, 2, 64, where, big, io, gate=io == "f32", seed=int(big) + 1)
+    val, bnd = expected(t, io)
+    out, last = call(t, ssm.ssd_scan_fwd, softplus=False, return_last_state=True)
+    got = dict(out=out)
+    if io == "f32":   # in bf16 what enters the state is rounded to bf16, which the bounds do not know
+        got["last"] = last
+    check(got, val, bnd, io, f"batched {where} {big} {io}")
