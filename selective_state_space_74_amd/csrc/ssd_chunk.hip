@@ -290,10 +290,10 @@ constexpr int kWalkThreads = 512;
 struct WalkParams {
   const float* from[2];
   float* to[2];
-  int split, cols;   // workgroups of a head, channels of one
+  int split;   // workgroups of a head, up to 64 channels each
 };
 
-// Workgroup: (batch row, head, some of its channels, direction).  It goes along the
+// Workgroup: (batch row, head, 64 of its channels, direction).  It goes along the
 // row's chunks with the state in registers, so that the states are written once and
 // not read and written again by the carry: loads are two chunks ahead, LDS in two
 // halves makes do with one barrier a chunk.  Bound by the chain of chunks, 3.8 us
@@ -308,8 +308,8 @@ __global__ __launch_bounds__(kWalkThreads) void ssd_walk_kernel(ChunkParams p, W
   const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lq = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int dir = blockIdx.y, h = static_cast<int>(blockIdx.x / q.split) % p.H;
-  const int b = static_cast<int>(blockIdx.x / q.split) / p.H, p0 = static_cast<int>(blockIdx.x % q.split) * q.cols;
-  const int last = min(p.P, p0 + q.cols);   // channels p0 .. last - 1
+  const int b = static_cast<int>(blockIdx.x / q.split) / p.H, p0 = static_cast<int>(blockIdx.x % q.split) * kPB;
+  const int last = min(p.P, p0 + kPB);   // channels p0 .. last - 1
   const bool gate = dir && p.z.p;
   const TokenTensor& x = dir ? p.dout : p.x;
   const TokenTensor& m = dir ? p.C : p.B;
@@ -719,19 +719,23 @@ void launch_walk(const ChunkParams& p, const WalkParams& q, bool backward, int64
 
 hipError_t launch_chunk_states(const ChunkParams& p, bool bf16, bool backward, int64_t nseq, const float* h0, float* last,
                                const float* dlast, float* dh0, hipStream_t stream) {
-  // batch rows of equal length: a workgroup goes along a whole row where two
-  // workgroups a compute unit remain, a head's channels in up to 4 parts.  Measured
-  // on gradients, 8 x 2048 x 32 x 64 x 64 bf16: 122 us, and 95 + 84 chunk by chunk; with
-  // the channels in two parts (1024 workgroups) 194.  Rows of 16-byte pieces only: by
-  // elements the walk waits for its loads, 4 x 1000 x 16 x 64 x 100 bf16 168 us for 51.
-  if (!p.table && p.nc > 0 && p.vec && p.bc_vec) {
-    WalkParams q{{h0, dlast}, {last, dh0}, 0, 0};
-    const int64_t heads = nseq * p.H * (backward ? 2 : 1);
-    for (q.cols = kPB; q.cols > 16 && heads * ((p.P + q.cols - 1) / q.cols) < 512;) q.cols /= 2;
-    q.split = (p.P + q.cols - 1) / q.cols;
+  // batch rows of equal length: a workgroup goes along a whole row where that gives at
+  // least three of four compute units one.  Gradients of rows x 32 heads of 64 channels, L 2048,
+  // us chunk by chunk and by the walk:
+  //   rows         1 (64)     2 (128)     3 (192)     4 (256)     8 (512)    16 (1024 workgroups)
+  //   N 64 bf16    71, 96     97, 106    129, 121    166, 148    319, 256    639, 487
+  //   N 128 bf16  126, 163   191, 203    247, 226    331, 278    625, 499   1234, 985
+  //   N 64 fp32   117, 157   174, 196    229, 231    300, 283    549, 493   1102, 969
+  // and alike with L 8192 and 64 heads.  Cutting a head's 64 channels over more
+  // workgroups stages B and C again and never won (8 rows, N 64: 298 in halves).  Heads
+  // of 16 channels leave too little to a wavefront (4 x 64, N 128: 330, 354).  Rows of
+  // 16-byte pieces only: by elements the walk waits for its loads, 4 x 1000 x 16 x 64 x
+  // 100 bf16 51 us, 168.
+  if (!p.table && p.nc > 0 && p.vec && p.bc_vec && p.P > 16) {
+    WalkParams q{{h0, dlast}, {last, dh0}, (p.P + kPB - 1) / kPB};
+    const int64_t groups = nseq * p.H * q.split, all = groups * (backward ? 2 : 1);
     // (its windows hold a head's state and a chunk of dt, its grid 2^32 threads)
-    if (heads * q.split >= 512 && heads * q.split < (int64_t{1} << 23) && static_cast<int64_t>(p.P) * p.N < (int64_t{1} << 29) &&
-        p.dts < (int64_t{1} << 23)) {
+    if (all >= 192 && groups < (int64_t{1} << 23) && static_cast<int64_t>(p.P) * p.N < (int64_t{1} << 29) && p.dts < (int64_t{1} << 23)) {
       if (!bf16) launch_walk<float, 64>(p, q, backward, nseq, stream);
       else if (p.N > 64) launch_walk<uint16_t, 128>(p, q, backward, nseq, stream);
       else launch_walk<uint16_t, 64>(p, q, backward, nseq, stream);
