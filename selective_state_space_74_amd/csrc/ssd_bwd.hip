@@ -61,9 +61,19 @@ struct GradParams {
   int64_t tokens;    // of all rows
 };
 
+// Wavefronts a SIMD: four (two workgroups a compute unit, 128 registers) for up to 64
+// states in bf16, though only the ungated form of 16-byte rows and one pass fits them;
+// the others keep 11 to 36 registers in scratch, which costs less than half the
+// wavefronts, but for gated rows by elements or of several passes (59 and 64 registers).
+// Gradients with four and, without scratch, two, us: 8 x 2048 x 32 x 64 x 64 gated 414,
+// 453; 4 x 2048 x 16 x 128 183, 186, gated 271, 267; 4 x 2048 x 32 x 36 by elements
+// 243, 249, gated 433, 420; 4 x 2048 x 16 x 132 408, 416, gated 715, 678.
+template <typename T, int NMAX, bool kGate, bool kVec, bool kOne>
+constexpr int kGradWaves = sizeof(T) == 2 && NMAX == 64 && (!kGate || (kVec && kOne)) ? 4 : 2;
+
 // kOne: a head's channels are one pass.
 template <typename T, int NMAX, bool kGate, bool kVec, bool kOne>
-__global__ __launch_bounds__(kGradThreads, sizeof(T) == 2 && NMAX == 64 ? 4 : 2) void ssd_grad_kernel(ChunkParams p, GradParams q, int grid) {
+__global__ __launch_bounds__(kGradThreads, (kGradWaves<T, NMAX, kGate, kVec, kOne>)) void ssd_grad_kernel(ChunkParams p, GradParams q, int grid) {
   using E = typename Lds<T>::E;
   using F = typename Frag<T>::V;
   constexpr bool kBF = sizeof(T) == 2;
