@@ -428,6 +428,10 @@ __global__ __launch_bounds__(kWalkThreads) void ssd_walk_kernel(ChunkParams p, W
 // above, gated, in 102 us, 3.4 TB/s.  Loads one pass ahead and not two: 111 us; four
 // wavefronts, each with all channels of 16 tokens: 169.
 // kDz: the gate's gradient dout y silu'(z) in place of the output.
+// Two workgroups a compute unit (128 registers); rows by elements then keep up to 37
+// registers in scratch, which costs less than one workgroup without any (5000 packed x 32
+// x 33 x 128 bf16 171 us, 174; x 64 fp32 118, 135), but for the gate's gradient with 128
+// states (79 registers: gradients of 4 x 1000 x 32 x 33 x 128 bf16 369, 347).
 constexpr int kOutThreads = 512;
 
 // Four values of a row from column c on (of `cols`), as they lie.
@@ -477,7 +481,7 @@ struct Four {
 };
 
 template <typename T, int NMAX, bool kDz, bool kVec>
-__global__ __launch_bounds__(kOutThreads, 4) void ssd_outputs_kernel(ChunkParams p, ChunkOut o, int grid) {
+__global__ __launch_bounds__(kOutThreads, kDz && !kVec && NMAX == 128 ? 2 : 4) void ssd_outputs_kernel(ChunkParams p, ChunkOut o, int grid) {
   using E = typename Lds<T>::E;
   constexpr bool kBF = sizeof(T) == 2;
   constexpr int kPad = 16 / sizeof(E), NP = NMAX + kPad, XP = kPB + kPad, NT = NMAX / 16, QB = kQ / 16;
