@@ -711,7 +711,9 @@ typedef struct ssm_ssd_update_args {
  * size) * element size below 2^31 for x, z, B, C and out, as in ssm_ssd_args
  * (SSM_ERR_UNSUPPORTED past that).
  * A NaN or an infinity in a token's inputs stays within its sequence, but may
- * reach earlier tokens of its chunk (64 tokens from the sequence's first on).
+ * reach earlier tokens of its chunk (64 tokens from the sequence's first on), and
+ * an infinity may become a NaN (where its decay over a chunk rounds to zero, and
+ * in the parts that bf16 products take).
  * Precision: fp32 accumulation, states and decays.  With bf16 IO the products run
  * on bf16 operands: the masked chunk scores are rounded to bf16, while the states
  * enter as a bf16 value plus its bf16 remainder (16 bits), and what is summed into
