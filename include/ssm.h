@@ -768,8 +768,8 @@ typedef struct ssm_ssd_packed_args {
  * and nheads * headdim * element size is below 2^25 (rows of dx).
  * A NaN or an infinity stays within its sequence (and the sums over all tokens), as
  * there, but may reach every token of its chunk.
- * Precision: as there; the gradients of dt, A and dt_bias come from products whose
- * operands carry 16 bits at least, that of D from fp32.
+ * Precision: as there; the gradients of dt, A, D, dt_bias and h0 come from products
+ * whose operands carry 24 bits.
  * Aliasing: no output may overlap an input, another output or the workspace.
  * Workspace: as in ssm_ssd_packed_args, of ssm_ssd_bwd_workspace_size() bytes. */
 typedef struct ssm_ssd_bwd_args {

@@ -23,10 +23,12 @@
 // before s's), column sums over the blocks of t after s's, added over u < s, and of the
 // tile on the diagonal, where sums down its columns are added along its rows.
 //   ddt = dDelta softplus'(dt + bias),   dD = sum_t M[t,t]
-// For bf16 IO K comes from products of the inputs as they are (dy, where it is gated,
-// as a bf16 value and its remainder, as are S_in and dS_out), so these sums carry 16
-// bits; G L and M L are rounded to bf16 where they enter the products for dx, dB and
-// dC, which are rounded to bf16 themselves.
+// For bf16 IO K comes from products of the inputs as they are, and dy, where it is gated,
+// and the states S_in and dS_out enter as three bf16 parts, 24 bits (with two, 16 bits, dA
+// and the bias's gradient were 2 to 5e-6 off, and 8 x 2048 x 32 x 64 x 64 took 252 us for
+// 266, gated 414 for 483); so these sums are as good as fp32's.  Rounded to bf16 are, where
+// they enter the products for dx, dB and dC, which are rounded to bf16 themselves, G L and
+// M L, and dS_out where it enters dx; a gated dy enters dx in two parts.
 //
 // A workgroup takes a chunk and up to 8 heads of a group.  Two of its 8 wavefronts
 // share 16 of the chunk's tokens, as s for dx and dB and as t for dC: each has every
@@ -62,26 +64,29 @@ struct GradParams {
 };
 
 // Wavefronts a SIMD: four (two workgroups a compute unit, 128 registers) for up to 64
-// states in bf16, though only the ungated form of 16-byte rows and one pass fits them;
-// the others keep 11 to 36 registers in scratch, which costs less than half the
-// wavefronts, but for gated rows by elements or of several passes (59 and 64 registers).
-// Gradients with four and, without scratch, two, us: 8 x 2048 x 32 x 64 x 64 gated 414,
-// 453; 4 x 2048 x 16 x 128 183, 186, gated 271, 267; 4 x 2048 x 32 x 36 by elements
-// 243, 249, gated 433, 420; 4 x 2048 x 16 x 132 408, 416, gated 715, 678.
-template <typename T, int NMAX, bool kGate, bool kVec, bool kOne>
-constexpr int kGradWaves = sizeof(T) == 2 && NMAX == 64 && (!kGate || (kVec && kOne)) ? 4 : 2;
+// states in bf16 without a gate, though only the form of 16-byte rows and one pass fits
+// them; the others keep 11 to 26 registers in scratch, which costs less than half the
+// wavefronts.  Gradients with four and, without scratch, two, us: 8 x 2048 x 32 x 64 x 64
+// 266, 325; 4 x 2048 x 16 x 128 180, 196; 4 x 2048 x 32 x 36 by elements 238, 259; 4 x
+// 2048 x 16 x 132 391, 427.  A gate's dy in three parts leaves LDS for one workgroup; with
+// B and C in registers instead there was room for two and 32 to 60 registers in scratch
+// (8 x 2048 x 32 x 64 x 64 485 -> 517, 4 x 2048 x 32 x 36 434 -> 482).
+template <typename T, int NMAX, bool kGate>
+constexpr int kGradWaves = sizeof(T) == 2 && NMAX == 64 && !kGate ? 4 : 2;
 
 // kOne: a head's channels are one pass.
 template <typename T, int NMAX, bool kGate, bool kVec, bool kOne>
-__global__ __launch_bounds__(kGradThreads, (kGradWaves<T, NMAX, kGate, kVec, kOne>)) void ssd_grad_kernel(ChunkParams p, GradParams q, int grid) {
+__global__ __launch_bounds__(kGradThreads, (kGradWaves<T, NMAX, kGate>)) void ssd_grad_kernel(ChunkParams p, GradParams q, int grid) {
   using E = typename Lds<T>::E;
   using F = typename Frag<T>::V;
   constexpr bool kBF = sizeof(T) == 2;
   constexpr int kPad = 16 / sizeof(E), NP = NMAX + kPad, XP = kPB + kPad, GP = kQ + kPad, NT = NMAX / 16, NH = NT / 2;
-  // heads: x, dy (and its remainder), a state (and its remainder), (G L)^T; before and
-  // after them: B and C, and the sum over the heads
-  constexpr int kX = 0, kDy = kQ * XP, kDyl = 2 * kQ * XP, kS = (kGate && kBF ? 3 : 2) * kQ * XP, kSl = kS + kPB * NP;
-  constexpr int kGl = kS + (kBF ? 2 : 1) * kPB * NP, kHead = kGl + kQ * GP, kEnds = 2 * kQ * NP + kQ * GP;
+  // bf16: a state in three parts, a gated dout too, 24 bits together
+  constexpr int kSP = kBF ? 3 : 1, kYP = kBF && kGate ? 3 : 1, kPartS = kPB * NP, kPartY = kQ * XP;
+  // heads: x, dy, a state, (G L)^T; before and after them: B and C, and the sum over
+  // the heads
+  constexpr int kX = 0, kDy = kQ * XP, kS = kDy + kYP * kPartY;
+  constexpr int kGl = kS + kSP * kPartS, kHead = kGl + kQ * GP, kEnds = 2 * kQ * NP + kQ * GP;
   // kKeep: B and C stay in LDS, next to the heads' operands; their fragments are read
   // again and again, which leaves the registers for two workgroups a compute unit
   // (128 of them).  Else they make room, and their fragments stay in registers.
@@ -179,9 +184,7 @@ __global__ __launch_bounds__(kGradThreads, (kGradWaves<T, NMAX, kGate, kVec, kOn
 
   E* const sX = lds + kX;
   E* const sY = lds + kDy;
-  [[maybe_unused]] E* const sYl = lds + kDyl;
   E* const sS = lds + kS;
-  [[maybe_unused]] E* const sSl = lds + kSl;
   E* const sGl = lds + kGl;   // [s][t]
   // four more sums a token lie behind its rows (two workgroups then fit a compute unit):
   // r and c of both halves behind x, K Delta's row over each block before it behind dy
@@ -196,7 +199,7 @@ __global__ __launch_bounds__(kGradThreads, (kGradWaves<T, NMAX, kGate, kVec, kOn
     yv.template load<kVec>(rows_of<T>(p.dout, k, h, p0, p.P), tid);
     if constexpr (kGate) zv.template load<kVec>(rows_of<T>(p.z, k, h, p0, p.P), tid);
   };
-  auto load_state = [&](const uint32_t* state, int h, int p0) {
+  auto load_state = [&](const float* state, int h, int p0) {
     sv.template load<kVec>(state_rows(state, ((static_cast<int64_t>(c) * p.H + h) * p.P + p0) * p.N, min(kPB, p.P - p0), p.N), tid);
   };
   auto load_head = [&](int h, int p0) {
@@ -204,8 +207,7 @@ __global__ __launch_bounds__(kGradThreads, (kGradWaves<T, NMAX, kGate, kVec, kOn
     load_y(h, p0);
     load_state(p.state, h, p0);
   };
-  // dy = dout, or dout silu(z), bf16 then in two parts; and what it gives dD: of a bf16
-  // gate here, as M's diagonal would have 16 bits of dy
+  // dy = dout, or dout silu(z), bf16 then in parts; and what it gives dD, of a bf16 gate
   constexpr bool kOwnD = kGate && kBF;
   [[maybe_unused]] float dd_own = 0.0f;
   auto put_y = [&](auto first) {
@@ -215,39 +217,47 @@ __global__ __launch_bounds__(kGradThreads, (kGradWaves<T, NMAX, kGate, kVec, kOn
 #pragma unroll
       for (int j = 0; j < Tokens::kN; ++j) {
         const int at = (tid / Tokens::kPer + j * Tokens::kStep) * XP + tid % Tokens::kPer * kPiece<T>;
-        uint32_t s[kPiece<T>];
+        float f[kPiece<T>];
 #pragma unroll
         for (int e = 0; e < kPiece<T>; ++e) {
-          const float f = piece_f32<T>(yv.v[j], e) * silu_f32(piece_f32<T>(zv.v[j], e));
-          s[e] = kBF ? split_bf16(f) : __float_as_uint(f);
-          if constexpr (kOwnD && decltype(first)::value) dd_own = fmaf(f, piece_f32<T>(xv.v[j], e), dd_own);
+          f[e] = piece_f32<T>(yv.v[j], e) * silu_f32(piece_f32<T>(zv.v[j], e));
+          if constexpr (kOwnD && decltype(first)::value) dd_own = fmaf(f[e], piece_f32<T>(xv.v[j], e), dd_own);
         }
         if constexpr (kBF) {
-          *reinterpret_cast<v4u*>(sY + at) = v4u{highs(s[0], s[1]), highs(s[2], s[3]), highs(s[4], s[5]), highs(s[6], s[7])};
-          *reinterpret_cast<v4u*>(sYl + at) = v4u{lows(s[0], s[1]), lows(s[2], s[3]), lows(s[4], s[5]), lows(s[6], s[7])};
+          uint32_t w[kPiece<T> / 2][kYP];
+#pragma unroll
+          for (int e = 0; e < kPiece<T> / 2; ++e) split_bf16(f[2 * e], f[2 * e + 1], w[e]);
+#pragma unroll
+          for (int k = 0; k < kYP; ++k) *reinterpret_cast<v4u*>(sY + k * kPartY + at) = v4u{w[0][k], w[1][k], w[2][k], w[3][k]};
         } else {
-          *reinterpret_cast<v4u*>(sY + at) = v4u{s[0], s[1], s[2], s[3]};
+          *reinterpret_cast<v4u*>(sY + at) =
+              v4u{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
         }
       }
     }
   };
-  auto put_state = [&]() { sv.put(sS, kBF ? sSl : sS, NP, tid); };
-  auto held = [&](uint32_t v) { return kBF ? joined_bf16(v) : __uint_as_float(v); };
+  auto put_state = [&]() { sv.template put<kSP>(sS, kPartS, NP, tid); };
   // a 16 x 16 tile of the state (rows n, k = channel) times x or dy of `own`, whose
-  // rows are in X (remainders in Xl); the remainders' products in the k = 32 form too
-  auto state_tile = [&](int n, int kbs, const E* X, [[maybe_unused]] const E* Xl, auto with_rest) {
+  // rows are in X, in as many parts; of parts' products those of 2^-16 and more
+  auto state_tile = [&](int n, int kbs, const E* X, auto parts) {
     v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
     if constexpr (kBF) {
 #pragma unroll
       for (int kb = 0; kb < kPB / 16; kb += 2) {
         if (kb >= kbs) continue;
-        const F s0 = frag_down<T>(sS, NP, 16 * kb, 16 * n, lr, lq), s1 = frag_down<T>(sS, NP, 16 * kb + 16, 16 * n, lr, lq);
-        const F f0 = frag_along<T>(X, XP, 16 * tok, 16 * kb, lr, lq), f1 = frag_along<T>(X, XP, 16 * tok, 16 * kb + 16, lr, lq);
-        acc = mma32(s0, frag_down<T>(sSl, NP, 16 * kb, 16 * n, lr, lq), f0, f0, acc);
-        acc = mma32(s1, frag_down<T>(sSl, NP, 16 * kb + 16, 16 * n, lr, lq), f1, f1, acc);
-        if constexpr (decltype(with_rest)::value)
-          acc = mma32(s0, s1, frag_along<T>(Xl, XP, 16 * tok, 16 * kb, lr, lq), frag_along<T>(Xl, XP, 16 * tok, 16 * kb + 16, lr, lq),
-                      acc);
+        F s0[kSP], s1[kSP];
+#pragma unroll
+        for (int i = 0; i < kSP; ++i) {
+          s0[i] = frag_down<T>(sS + i * kPartS, NP, 16 * kb, 16 * n, lr, lq);
+          s1[i] = frag_down<T>(sS + i * kPartS, NP, 16 * kb + 16, 16 * n, lr, lq);
+        }
+#pragma unroll
+        for (int j = 0; j < decltype(parts)::value; ++j) {
+          const F f0 = frag_along<T>(X + j * kPartY, XP, 16 * tok, 16 * kb, lr, lq),
+                  f1 = frag_along<T>(X + j * kPartY, XP, 16 * tok, 16 * kb + 16, lr, lq);
+#pragma unroll
+          for (int i = 0; i + j < kSP; ++i) acc = mma32(s0[i], s1[i], f0, f1, acc);
+        }
       }
     } else {
 #pragma unroll
@@ -290,14 +300,13 @@ __global__ __launch_bounds__(kGradThreads, (kGradWaves<T, NMAX, kGate, kVec, kOn
         for (int j = 0; j < kTiles; ++j) {
           const int tb = block_of(j);
           if (tb >= QB) continue;
-          const F y0 = frag_along<T>(sY, XP, 16 * tb, 16 * kb, lr, lq);
           if constexpr (kBF) {
-            M[j] = mma32(y0, frag_along<T>(sY, XP, 16 * tb, 16 * kb + 16, lr, lq), x0, x1, M[j]);
-            if constexpr (kGate)
-              M[j] = mma32(frag_along<T>(sYl, XP, 16 * tb, 16 * kb, lr, lq), frag_along<T>(sYl, XP, 16 * tb, 16 * kb + 16, lr, lq), x0,
-                           x1, M[j]);
+#pragma unroll
+            for (int i = 0; i < kYP; ++i)
+              M[j] = mma32(frag_along<T>(sY + i * kPartY, XP, 16 * tb, 16 * kb, lr, lq),
+                           frag_along<T>(sY + i * kPartY, XP, 16 * tb, 16 * kb + 16, lr, lq), x0, x1, M[j]);
           } else {
-            M[j] = mma16<T>(y0, x0, M[j]);
+            M[j] = mma16<T>(frag_along<T>(sY, XP, 16 * tb, 16 * kb, lr, lq), x0, M[j]);
           }
         }
       }
@@ -365,7 +374,7 @@ __global__ __launch_bounds__(kGradThreads, (kGradWaves<T, NMAX, kGate, kVec, kOn
       for (int n = 0; n < NH; ++n) {
         if (n0 + n >= nt) continue;
         const F f = half_c(n);
-        const v4f v = state_tile(n0 + n, kbs, sY, sYl, std::integral_constant<bool, kGate>{});
+        const v4f v = state_tile(n0 + n, kbs, sY, std::integral_constant<int, kYP>{});
 #pragma unroll
         for (int e = 0; e < 4; ++e) r_t = fmaf(elem<T>(f, e), v[e], r_t);
         dC[n] += v * ea;
@@ -377,9 +386,10 @@ __global__ __launch_bounds__(kGradThreads, (kGradWaves<T, NMAX, kGate, kVec, kOn
         const int at = (tid / States::kPer + j * States::kStep) * NP + tid % States::kPer * 4;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float s = Lds<T>::f(sS[at + e]);
-          if constexpr (kBF) s += Lds<T>::f(sSl[at + e]);
-          pairs = fmaf(s, held(sv.v[j][e]), pairs);
+          float s = 0.0f;   // the parts' sum is exact
+#pragma unroll
+          for (int i = kSP - 1; i >= 0; --i) s += Lds<T>::f(sS[i * kPartS + at + e]);
+          pairs = fmaf(s, __uint_as_float(sv.v[j][e]), pairs);
         }
       }
       put_state();
@@ -389,7 +399,7 @@ __global__ __launch_bounds__(kGradThreads, (kGradWaves<T, NMAX, kGate, kVec, kOn
       for (int n = 0; n < NH; ++n) {
         if (n0 + n >= nt) continue;
         const F f = half_b(n);
-        const v4f v = state_tile(n0 + n, kbs, sX, sX, std::false_type{});
+        const v4f v = state_tile(n0 + n, kbs, sX, std::integral_constant<int, 1>{});
 #pragma unroll
         for (int e = 0; e < 4; ++e) c_s = fmaf(elem<T>(f, e), v[e], c_s);
         dB[n] += v * (ew * dl_s);
@@ -448,7 +458,8 @@ __global__ __launch_bounds__(kGradThreads, (kGradWaves<T, NMAX, kGate, kVec, kOn
             const F w1 = frag_along<T>(sGl, GP, 16 * tok, 16 * tb + 16, lr, lq);
             acc = mma32(y0, frag_down<T>(sY, XP, 16 * tb + 16, 16 * pt, lr, lq), w0, w1, acc);
             if constexpr (kGate)
-              acc = mma32(frag_down<T>(sYl, XP, 16 * tb, 16 * pt, lr, lq), frag_down<T>(sYl, XP, 16 * tb + 16, 16 * pt, lr, lq), w0, w1, acc);
+              acc = mma32(frag_down<T>(sY + kPartY, XP, 16 * tb, 16 * pt, lr, lq), frag_down<T>(sY + kPartY, XP, 16 * tb + 16, 16 * pt, lr, lq),
+                          w0, w1, acc);
           } else {
             acc = mma16<T>(y0, w0, acc);
           }
@@ -458,7 +469,7 @@ __global__ __launch_bounds__(kGradThreads, (kGradWaves<T, NMAX, kGate, kVec, kOn
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           float dy = Lds<T>::f(sY[own * XP + c0 + e]);
-          if constexpr (kGate && kBF) dy += Lds<T>::f(sYl[own * XP + c0 + e]);
+          if constexpr (kYP > 1) dy += Lds<T>::f(sY[kPartY + own * XP + c0 + e]);
           d[e] = fmaf(dl_s, acc[e], Dh * dy);
         }
         const uint32_t off = (own * p.H * p.P + c0) * static_cast<uint32_t>(sizeof(T));
@@ -714,8 +725,8 @@ ChunkParams params_of(const Args& a, const ChunkPlan& q, const Layout& l, bool p
   p.table = packed ? reinterpret_cast<const ChunkEntry*>(ws + l.table) : nullptr;
   p.seq_chunk = packed ? reinterpret_cast<const int32_t*>(ws + l.seq_chunk) : nullptr;
   p.lam = reinterpret_cast<float*>(ws + l.lam);
-  p.state = reinterpret_cast<uint32_t*>(ws + l.state);
-  p.dstate = reinterpret_cast<uint32_t*>(ws + l.dstate);
+  p.state = reinterpret_cast<float*>(ws + l.state);
+  p.dstate = reinterpret_cast<float*>(ws + l.dstate);
   p.dt = a.dt;
   p.dts = a.dt_seq_stride;
   return p;

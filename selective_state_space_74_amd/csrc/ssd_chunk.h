@@ -46,8 +46,8 @@ struct ChunkParams {
   bool vec;                    // rows of the heads' tensors and of states are made of 16-byte pieces
   bool bc_vec;                 // rows of B and C are
   float* lam;                  // [nc][H] decay over a chunk
-  uint32_t* state;             // [nc][H][P][N] what a chunk adds; then S_in
-  uint32_t* dstate;            // the same backward; then dS_out
+  float* state;                // [nc][H][P][N] what a chunk adds; then S_in
+  float* dstate;               // the same backward; then dS_out
 };
 
 struct Chunk {
@@ -214,14 +214,14 @@ __device__ __forceinline__ void stage_rows(typename Lds<T>::E* dst, int pitch, c
   q.put(dst, pitch, tid);
 }
 
-// Four states n .. n + 3 of row r of a chunk's state: the words that the carry left.
+// Four states n .. n + 3 of row r of a chunk's state.
 // rows of the window: the head's channels from a pass's first on.
 struct StateRows {
   __amdgpu_buffer_rsrc_t r;
   int N;
 };
-__device__ __forceinline__ StateRows state_rows(const uint32_t* state, int64_t at, int rows, int N) {
-  return StateRows{__builtin_amdgcn_make_buffer_rsrc(const_cast<uint32_t*>(state + at), 0, rows * N * 4, kRsrcWord3), N};
+__device__ __forceinline__ StateRows state_rows(const float* state, int64_t at, int rows, int N) {
+  return StateRows{__builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(state + at), 0, rows * N * 4, kRsrcWord3), N};
 }
 template <bool kVec>
 __device__ __forceinline__ v4u load_states(const StateRows& w, int r, int n) {
@@ -233,12 +233,24 @@ __device__ __forceinline__ v4u load_states(const StateRows& w, int r, int n) {
   return v;
 }
 
-// The high (low) halves of two words, the first one's low.
+// The high halves of two words, the first one's low.
 __device__ __forceinline__ uint32_t highs(uint32_t a, uint32_t b) { return a >> 16 | (b & 0xffff0000u); }
-__device__ __forceinline__ uint32_t lows(uint32_t a, uint32_t b) { return (a & 0xffffu) | b << 16; }
 
-// kPB rows of a state, likewise; bf16: the values to one array of LDS, the remainders
-// to another.
+// Two fp32 values as kParts bf16 parts, each the nearest to what the ones before it
+// leave: 8 bits more a part, the second value in the high halves.
+template <int kParts>
+__device__ __forceinline__ void split_bf16(float a, float b, uint32_t (&w)[kParts]) {
+#pragma unroll
+  for (int i = 0; i < kParts; ++i) {
+    w[i] = pack_bf16x2(a, b);
+    if (i + 1 == kParts) break;
+    a -= __uint_as_float(w[i] << 16);
+    b -= __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+// kPB rows of a state, likewise; bf16: as kParts parts in as many arrays of LDS, `part`
+// elements apart.
 template <typename T, int NMAX, int kThreads>
 struct StatePieces {
   static constexpr int kPer = NMAX / 4, kStep = kThreads / kPer, kN = kPB / kStep;
@@ -249,13 +261,17 @@ struct StatePieces {
 #pragma unroll
     for (int i = 0; i < kN; ++i) v[i] = load_states<kVec>(w, tid / kPer + i * kStep, tid % kPer * 4);
   }
-  __device__ __forceinline__ void put(typename Lds<T>::E* dst, typename Lds<T>::E* rest, int pitch, int tid) const {
+  template <int kParts>
+  __device__ __forceinline__ void put(typename Lds<T>::E* dst, [[maybe_unused]] int part, int pitch, int tid) const {
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
       const int at = (tid / kPer + i * kStep) * pitch + tid % kPer * 4;
       if constexpr (sizeof(T) == 2) {
-        *reinterpret_cast<v2u*>(dst + at) = v2u{highs(v[i][0], v[i][1]), highs(v[i][2], v[i][3])};
-        *reinterpret_cast<v2u*>(rest + at) = v2u{lows(v[i][0], v[i][1]), lows(v[i][2], v[i][3])};
+        uint32_t a[kParts], b[kParts];
+        split_bf16(__uint_as_float(v[i][0]), __uint_as_float(v[i][1]), a);
+        split_bf16(__uint_as_float(v[i][2]), __uint_as_float(v[i][3]), b);
+#pragma unroll
+        for (int k = 0; k < kParts; ++k) *reinterpret_cast<v2u*>(dst + k * part + at) = v2u{a[k], b[k]};
       } else {
         *reinterpret_cast<v4u*>(dst + at) = v[i];
       }
@@ -263,15 +279,6 @@ struct StatePieces {
   }
 };
 
-// A value as bf16 and the remainder's bf16, 16 bits together: the value in the
-// high half of a word, as it is widened, the remainder in the low one.
-__device__ __forceinline__ uint32_t split_bf16(float v) {
-  const uint32_t hi = f32_to_bf16(v);
-  return hi << 16 | f32_to_bf16(v - __uint_as_float(hi << 16));
-}
-__device__ __forceinline__ float joined_bf16(uint32_t v) {
-  return __uint_as_float(v & 0xffff0000u) + __uint_as_float(v << 16);
-}
 // A 16-wide tile's fragment down the rows of LDS: X[k0 + 4 lq + i][c0 + lr].
 template <typename T>
 __device__ __forceinline__ typename Frag<T>::V frag_down(const typename Lds<T>::E* X, int pitch, int k0, int c0, int lr, int lq) {

@@ -202,7 +202,7 @@ __global__ __launch_bounds__(kThreads) void ssd_states_kernel(ChunkParams p, int
       // lane: channel 16 pt + lr, states 16 n + 4 lq ..
       const int pp = p0 + 16 * pt + lr;
       if (pp < p.P) {
-        float* const to = reinterpret_cast<float*>(back ? p.dstate : p.state) +
+        float* const to = (back ? p.dstate : p.state) +
                           ((static_cast<int64_t>(c) * p.H + h0 + i) * p.P + pp) * p.N;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -227,7 +227,7 @@ __global__ __launch_bounds__(kThreads) void ssd_states_kernel(ChunkParams p, int
 struct CarryParams {
   const int32_t* seq_chunk;
   const float* lam;
-  uint32_t* state[2];
+  float* state[2];
   const float* from[2];
   float* to[2];
   int64_t nseq, elems;
@@ -236,12 +236,11 @@ struct CarryParams {
 
 // A lane has V values of a sequence's state and goes along its chunks (blockIdx.z
 // = 1: from the end), kAhead chunks' loads in flight; in place of what a chunk adds
-// it leaves the state that enters it, for bf16 IO as two bf16 halves.  Bound by
-// memory, as fast as a copy: 283 MB of the same case in 52 us, 5.4 TB/s.
-template <bool kBF, int V>
+// it leaves the state that enters it.  Bound by memory, as fast as a copy: 283 MB of the same case in 52 us, 5.4 TB/s.
+template <int V>
 __global__ __launch_bounds__(kThreads) void ssd_carry_kernel(CarryParams p) {
   constexpr int kAhead = 8;
-  struct alignas(4 * V) Pack { uint32_t e[V]; };
+  struct alignas(4 * V) Pack { float e[V]; };
   const int64_t e0 = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) * V;
   if (e0 >= p.elems) return;
   const int dir = blockIdx.z;
@@ -252,7 +251,7 @@ __global__ __launch_bounds__(kThreads) void ssd_carry_kernel(CarryParams p) {
     float h[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) h[v] = p.from[dir] ? p.from[dir][s * p.elems + e0 + v] : 0.0f;
-    uint32_t* const base = p.state[dir] + e0;
+    float* const base = p.state[dir] + e0;
     for (int c = 0; c < hi - lo; c += kAhead) {
       Pack add[kAhead];
       float lam[kAhead];
@@ -270,8 +269,8 @@ __global__ __launch_bounds__(kThreads) void ssd_carry_kernel(CarryParams p) {
         Pack in;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          in.e[v] = kBF ? split_bf16(h[v]) : __float_as_uint(h[v]);
-          h[v] = fmaf(lam[i], h[v], __uint_as_float(add[i].e[v]));
+          in.e[v] = h[v];
+          h[v] = fmaf(lam[i], h[v], add[i].e[v]);
         }
         *reinterpret_cast<Pack*>(base + at * p.elems) = in;
       }
@@ -301,7 +300,6 @@ struct WalkParams {
 template <typename T, int NMAX>
 __global__ __launch_bounds__(kWalkThreads) void ssd_walk_kernel(ChunkParams p, WalkParams q) {
   using E = typename Lds<T>::E;
-  constexpr bool kBF = sizeof(T) == 2;
   constexpr int kPad = 16 / sizeof(E), NP = NMAX + kPad, XP = kPB + kPad, NT = NMAX / 16;
   constexpr int kHalf = kQ * NP + kParts<T> * kQ * XP;
   __shared__ __align__(16) E lds[2 * kHalf];
@@ -313,7 +311,7 @@ __global__ __launch_bounds__(kWalkThreads) void ssd_walk_kernel(ChunkParams p, W
   const bool gate = dir && p.z.p;
   const TokenTensor& x = dir ? p.dout : p.x;
   const TokenTensor& m = dir ? p.C : p.B;
-  uint32_t* const state = dir ? p.dstate : p.state;
+  float* const state = dir ? p.dstate : p.state;
   const int g = h / p.per_group, nt = (p.N + 15) / 16;
   const StepHead steps = step_head(p, h);
   // channels' tiles (1, 2 or 4) and the wavefronts that share one, at least two: tiles
@@ -385,7 +383,7 @@ __global__ __launch_bounds__(kWalkThreads) void ssd_walk_kernel(ChunkParams p, W
     for (int j = 0; j < kMost; ++j) {
       v4u v;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = kBF ? split_bf16(acc[j][e]) : __float_as_uint(acc[j][e]);
+      for (int e = 0; e < 4; ++e) v[e] = __float_as_uint(acc[j][e]);
       __builtin_amdgcn_raw_buffer_store_b128(v, to, place(j, 0), 0, 0);
       acc[j] *= through;
     }
@@ -595,7 +593,7 @@ __global__ __launch_bounds__(kOutThreads, kDz && !kVec && NMAX == 128 ? 2 : 4) v
       Dh = sh.D[i];
     }
     a.x.put(sX, XP, tid);
-    a.s.put(sH, kBF ? sHL : sH, NP, tid);
+    a.s.template put<kBF ? 2 : 1>(sH, kPB * NP, NP, tid);
     float by[kTiles][4];   // what the sums are multiplied by
 #pragma unroll
     for (int j = 0; j < kTiles; ++j) {
@@ -760,13 +758,8 @@ hipError_t launch_chunk_states(const ChunkParams& p, bool bf16, bool backward, i
   const int64_t lanes = four ? q.elems / 4 : q.elems;
   const dim3 grid(static_cast<unsigned>((lanes + kThreads - 1) / kThreads), static_cast<unsigned>(std::min<int64_t>(nseq, 4096)),
                   backward ? 2 : 1);
-  if (bf16) {
-    if (four) ssd_carry_kernel<true, 4><<<grid, kThreads, 0, stream>>>(q);
-    else ssd_carry_kernel<true, 1><<<grid, kThreads, 0, stream>>>(q);
-  } else {
-    if (four) ssd_carry_kernel<false, 4><<<grid, kThreads, 0, stream>>>(q);
-    else ssd_carry_kernel<false, 1><<<grid, kThreads, 0, stream>>>(q);
-  }
+  if (four) ssd_carry_kernel<4><<<grid, kThreads, 0, stream>>>(q);
+  else ssd_carry_kernel<1><<<grid, kThreads, 0, stream>>>(q);
   return hipGetLastError();
 }
 
