@@ -186,8 +186,8 @@ __device__ __forceinline__ float wave_prefix_sum(float v) {
 template <int kCtrl, int kRows = 0xf>
 __device__ __forceinline__ double dpp0(double v) {
   const v2u w = __builtin_bit_cast(v2u, v);
-  return __builtin_bit_cast(double, v2u{static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(w[0]), kCtrl, kRows, 0xf, false)),
-                                        static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(w[1]), kCtrl, kRows, 0xf, false))});
+  return __builtin_bit_cast(double, v2u{static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(w[0]), kCtrl, kRows, 0xf, true)),
+                                        static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(w[1]), kCtrl, kRows, 0xf, true))});
 }
 __device__ __forceinline__ double wave_prefix_sum64(double v) {
   v += dpp0<0x111>(v);

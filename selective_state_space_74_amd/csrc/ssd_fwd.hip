@@ -98,8 +98,13 @@ struct SsdParams {
 // The one-block bf16 kernel with 64 states and vector staging fits four
 // wavefronts per SIMD (128 registers) without spilling; asking for that keeps
 // a grid of 4 x 256 workgroups in one wave of residency.
-template <typename T, int NMAX, bool kVec, int PB>
-constexpr bool kFourWaves() { return sizeof(T) == 2 && NMAX == 64 && kVec && PB == 1; }
+// With two blocks it fits three, segmented only if asked to (1M tokens of 32 heads
+// otherwise take 7.7 ms for 6.8).
+template <typename T, int NMAX, bool kVec, int PB, bool kSegd>
+constexpr int kWavesPerSimd() {
+  if (sizeof(T) != 2 || NMAX != 64 || !kVec) return 1;
+  return PB == 1 ? 4 : PB == 2 && kSegd ? 3 : 1;
+}
 
 // kVec: B/C rows, x rows and their strides are 16-byte (x: 8-byte for bf16)
 // aligned and dstate is a multiple of NMAX / 4, so staging uses vector loads
@@ -109,7 +114,7 @@ constexpr bool kFourWaves() { return sizeof(T) == 2 && NMAX == 64 && kVec && PB 
 // sequence (p.mode 1 or 2); without it, one segment and none of their code.
 template <typename T, int NMAX, bool kSoftplus, bool kVec, int PB, bool kSegd>
 __global__ __launch_bounds__(kThreads)
-__attribute__((amdgpu_waves_per_eu(kFourWaves<T, NMAX, kVec, PB>() ? 4 : 1)))
+__attribute__((amdgpu_waves_per_eu(kWavesPerSimd<T, NMAX, kVec, PB, kSegd>())))
 void ssd_fwd_kernel(SsdParams p) {
   using L = Lds<T>;
   using E = typename L::E;
@@ -138,7 +143,8 @@ void ssd_fwd_kernel(SsdParams p) {
   // carries the fp32 state to about 16 bits (two bf16 products)
   __shared__ __align__(16) E sHL[kBP][kBF ? NMAX : 1][kPB];
   __shared__ __align__(16) float sDl[kQ];      // Delta_s (0 past the end)
-  __shared__ __align__(16) double sLa[kQ];     // a_t * log2(e)
+  __shared__ __align__(16) float sLa[kQ];      // a_t * log2(e), rounded
+  __shared__ __align__(16) float sLr[kQ];      // and what that leaves
   // segmented passes (kept in LDS, not in registers across the chunk loop):
   __shared__ float sRed[kWaves];               // per-wavefront state maxima (pass 2 check)
   __shared__ float sHin[kWaves];               // per-wavefront maxima of |h_in| (pass 2)
@@ -467,7 +473,8 @@ void ssd_fwd_kernel(SsdParams p) {
       w_row = __shfl(w, srow, 64);
       if (wave == 0) {
         sDl[lane] = dl;
-        sLa[lane] = la;
+        sLa[lane] = static_cast<float>(la);
+        sLr[lane] = static_cast<float>(la - static_cast<float>(la));
       }
     }
     // ---- decay-weighted x^T (needs the step sizes) ----
@@ -511,7 +518,7 @@ void ssd_fwd_kernel(SsdParams p) {
     // ---- outputs of tokens 16 w .. 16 w + 15 ----
     {
       const int tb = 16 * wave;
-      const double la_t = sLa[tb + lr];
+      const float la_t = sLa[tb + lr], lr_t = sLr[tb + lr];
       typename SumOf<T>::V y1[PB];
 #pragma unroll
       for (int q = 0; q < PB; ++q) y1[q] = {};
@@ -532,13 +539,13 @@ void ssd_fwd_kernel(SsdParams p) {
         }
         // mask and scale: lane holds s = 16 sbk + 4 lq + i, t = tb + lr
         const int s0 = 16 * sbk + 4 * lq;
-        const v4d la_s = *reinterpret_cast<const v4d*>(&sLa[s0]);
+        const v4f la_s = *reinterpret_cast<const v4f*>(&sLa[s0]), lr_s = *reinterpret_cast<const v4f*>(&sLr[s0]);
         const float4 dl_s = *reinterpret_cast<const float4*>(&sDl[s0]);
         const int t = tb + lr;
-        const float m0 = s0 + 0 <= t ? sc[0] * decay_of(la_t - la_s[0]) * dl_s.x : 0.0f;
-        const float m1 = s0 + 1 <= t ? sc[1] * decay_of(la_t - la_s[1]) * dl_s.y : 0.0f;
-        const float m2 = s0 + 2 <= t ? sc[2] * decay_of(la_t - la_s[2]) * dl_s.z : 0.0f;
-        const float m3 = s0 + 3 <= t ? sc[3] * decay_of(la_t - la_s[3]) * dl_s.w : 0.0f;
+        const float m0 = s0 + 0 <= t ? sc[0] * __builtin_amdgcn_exp2f((la_t - la_s[0]) + (lr_t - lr_s[0])) * dl_s.x : 0.0f;
+        const float m1 = s0 + 1 <= t ? sc[1] * __builtin_amdgcn_exp2f((la_t - la_s[1]) + (lr_t - lr_s[1])) * dl_s.y : 0.0f;
+        const float m2 = s0 + 2 <= t ? sc[2] * __builtin_amdgcn_exp2f((la_t - la_s[2]) + (lr_t - lr_s[2])) * dl_s.z : 0.0f;
+        const float m3 = s0 + 3 <= t ? sc[3] * __builtin_amdgcn_exp2f((la_t - la_s[3]) + (lr_t - lr_s[3])) * dl_s.w : 0.0f;
         // intra: A = M (row t, k = s), B operand = x (k = s, column p) of
         // every channel block
         const auto mf = tofrag<T>(m0, m1, m2, m3);
@@ -571,8 +578,9 @@ void ssd_fwd_kernel(SsdParams p) {
       const __amdgpu_buffer_rsrc_t ro = window(og, p.osl, p.P - p0, t0);
       const uint32_t oend = static_cast<uint32_t>(std::min(p.L - 1 - t0, kQ - 1)) * p.osl +
                             (p.P - p0) * ES;
-      const v4d la_o = *reinterpret_cast<const v4d*>(&sLa[tb + 4 * lq]);
-      const float ea[4] = {decay_of(la_o[0]), decay_of(la_o[1]), decay_of(la_o[2]), decay_of(la_o[3])};
+      const float4 la_o = *reinterpret_cast<const float4*>(&sLa[tb + 4 * lq]);
+      const float ea[4] = {__builtin_amdgcn_exp2f(la_o.x), __builtin_amdgcn_exp2f(la_o.y),
+                           __builtin_amdgcn_exp2f(la_o.z), __builtin_amdgcn_exp2f(la_o.w)};
 #pragma unroll
       for (int q = 0; q < PB; ++q) {
         const int pl = kPB * q + lr;
@@ -598,7 +606,7 @@ void ssd_fwd_kernel(SsdParams p) {
 
     // ---- state update: H_out^T = exp(a_last) H_in^T + (w x)^T B ----
     {
-      const float decay = decay_of(sLa[kQ - 1]);
+      const float decay = __builtin_amdgcn_exp2f(sLa[kQ - 1]);
 #pragma unroll
       for (int j = 0; j < NBW; ++j) {
         const int m = wave + kWaves * j;
