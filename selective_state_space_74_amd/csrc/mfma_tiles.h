@@ -9,7 +9,6 @@
 namespace ssm {
 
 typedef float v4f __attribute__((ext_vector_type(4)));
-typedef double v4d __attribute__((ext_vector_type(4), aligned(16)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef short v8s __attribute__((ext_vector_type(8)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
@@ -202,6 +201,19 @@ __device__ __forceinline__ double lane_value(double v, int lane) {
   const v2u w = __builtin_bit_cast(v2u, v);
   return __builtin_bit_cast(double, v2u{static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(w[0]), lane)),
                                         static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(w[1]), lane))});
+}
+
+// A sum of steps as it is kept in LDS, a float and what its rounding leaves: the
+// difference of two is then rounded once, and the sums' own sizes do not matter.
+struct TwoFloats {
+  float v, rest;
+};
+__device__ __forceinline__ TwoFloats two_floats(double v) {
+  const float f = static_cast<float>(v);
+  return TwoFloats{f, static_cast<float>(v - f)};
+}
+__device__ __forceinline__ float decay_between(float to, float to_rest, const TwoFloats& from) {
+  return __builtin_amdgcn_exp2f((to - from.v) + (to_rest - from.rest));
 }
 
 // The decay between two sums of steps times their rate, in units of log 2.

@@ -94,8 +94,7 @@ __global__ __launch_bounds__(kGradThreads, (kGradWaves<T, NMAX, kGate>)) void ss
   constexpr int kB = kKeep ? kHead : 0, kC = kB + kQ * NP, kG = kKeep ? 0 : 2 * kQ * NP;
   // the small arrays first: their addresses are then offsets in the instruction
   struct Shared {
-    double la[kMostHeads][kQ];
-    float dl[kMostHeads][kQ], A[kMostHeads], D[kMostHeads];
+    float la[kMostHeads][kQ], lr[kMostHeads][kQ], dl[kMostHeads][kQ], A[kMostHeads], D[kMostHeads];
     // of a token: K Delta of its block's rectangle; sums over K's column in its block, and
     // below (by the wavefronts' halves); M's diagonal, where that gives dD
     float in_block[kQ], col[kQ], below[2][kQ], m[kGate && kBF ? 1 : kQ], pairs[kGradThreads / 64], dd[kGradThreads / 64];
@@ -117,7 +116,9 @@ __global__ __launch_bounds__(kGradThreads, (kGradWaves<T, NMAX, kGate>)) void ss
   for (int i = wave; i < heads; i += kGradThreads / 64) {
     const Steps s = steps_of<T>(p, k, h0 + i, lane);
     sh.dl[i][lane] = s.delta;
-    sh.la[i][lane] = s.la;
+    const TwoFloats la = two_floats(s.la);
+    sh.la[i][lane] = la.v;
+    sh.lr[i][lane] = la.rest;
     if (lane == 0) {
       sh.A[i] = p.A[h0 + i];
       sh.D[i] = p.D ? p.D[h0 + i] : 0.0f;
@@ -271,9 +272,9 @@ __global__ __launch_bounds__(kGradThreads, (kGradWaves<T, NMAX, kGate>)) void ss
   load_head(h0, 0);
   for (int i = 0; i < heads; ++i) {
     const int h = h0 + i;
-    const double la_s = sh.la[i][own];
+    const TwoFloats la_s{sh.la[i][own], sh.lr[i][own]};
     const float dl_s = sh.dl[i][own];
-    const float ew = decay_of(sh.la[i][kQ - 1] - la_s), ea = decay_of(la_s);
+    const float ew = decay_between(sh.la[i][kQ - 1], sh.lr[i][kQ - 1], la_s), ea = __builtin_amdgcn_exp2f(la_s.v);
     const float Dh = sh.D[i];
     v4f M[kTiles];
 #pragma unroll
@@ -317,13 +318,13 @@ __global__ __launch_bounds__(kGradThreads, (kGradWaves<T, NMAX, kGate>)) void ss
         auto tile = [&](int j, auto on_diagonal) {
           constexpr bool kDiag = decltype(on_diagonal)::value;
           const int tb = block_of(j);
-          const v4d la_t = *reinterpret_cast<const v4d*>(&sh.la[i][16 * tb + 4 * lq]);
+          const v4f la_t = *reinterpret_cast<const v4f*>(&sh.la[i][16 * tb + 4 * lq]), lr_t = *reinterpret_cast<const v4f*>(&sh.lr[i][16 * tb + 4 * lq]);
           float w[4], in_col = 0.0f, m0 = 0.0f;
           v4f rows;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int over = 4 * lq + e - lr;   // t - s on the diagonal's tile
-            float L = decay_of(la_t[e] - la_s), m = M[j][e];
+            float L = decay_between(la_t[e], lr_t[e], la_s), m = M[j][e];
             if constexpr (kDiag) {
               L = over >= 0 ? L : 0.0f;
               m = over >= 0 ? m : 0.0f;
@@ -413,7 +414,7 @@ __global__ __launch_bounds__(kGradThreads, (kGradWaves<T, NMAX, kGate>)) void ss
       to[0] = r_t;
       to[2] = c_s;
     }
-    if (lane == 0) sh.pairs[wave] = pairs * decay_of(sh.la[i][kQ - 1]);
+    if (lane == 0) sh.pairs[wave] = pairs * __builtin_amdgcn_exp2f(sh.la[i][kQ - 1]);
     if constexpr (kOwnD) {
       const float s = wave_sum(dd_own);
       dd_own = 0.0f;

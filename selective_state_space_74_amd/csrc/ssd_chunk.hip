@@ -485,8 +485,7 @@ __global__ __launch_bounds__(kOutThreads, kDz && !kVec && NMAX == 128 ? 2 : 4) v
   constexpr int kPad = 16 / sizeof(E), NP = NMAX + kPad, XP = kPB + kPad, NT = NMAX / 16, QB = kQ / 16;
   constexpr int kScores = 2 * kQ * NP, kHead = kQ * XP + (kBF ? 2 : 1) * kPB * NP;
   struct Shared {
-    double la[kMostHeads][kQ];
-    float dl[kMostHeads][kQ], D[kMostHeads];
+    float la[kMostHeads][kQ], lr[kMostHeads][kQ], dl[kMostHeads][kQ], D[kMostHeads];
     alignas(16) E tiles[kScores > kHead ? kScores : kHead];
   };
   __shared__ __align__(16) Shared sh;
@@ -501,7 +500,9 @@ __global__ __launch_bounds__(kOutThreads, kDz && !kVec && NMAX == 128 ? 2 : 4) v
   for (int i = wave; i < heads; i += kOutThreads / 64) {
     const Steps s = steps_of<T>(p, k, h0 + i, lane);
     sh.dl[i][lane] = s.delta;
-    sh.la[i][lane] = s.la;
+    const TwoFloats la = two_floats(s.la);
+    sh.la[i][lane] = la.v;
+    sh.lr[i][lane] = la.rest;
     if (lane == 0) sh.D[i] = p.D ? p.D[h0 + i] : 0.0f;
   }
   E* const sB = sh.tiles;
@@ -573,23 +574,24 @@ __global__ __launch_bounds__(kOutThreads, kDz && !kVec && NMAX == 128 ? 2 : 4) v
     const int i = s / of_head, h = h0 + i, p0 = s % of_head * kPB, cols = s < passes ? p.P - p0 : 0;
     if (p0 == 0 && cols > 0) {
       // weighted scores of the head, as operands; those above the diagonal are zero
-      const double la_t = sh.la[i][own];
+      const float la_t = sh.la[i][own], lr_t = sh.lr[i][own];
 #pragma unroll
       for (int sb = 0; sb < QB; ++sb) {
         mf[sb] = tofrag<T>(0.0f, 0.0f, 0.0f, 0.0f);
         if (sb > tok) continue;
-        const v4d la_s = *reinterpret_cast<const v4d*>(&sh.la[i][16 * sb + 4 * lq]);
+        const v4f la_s = *reinterpret_cast<const v4f*>(&sh.la[i][16 * sb + 4 * lq]);
+        const v4f lr_s = *reinterpret_cast<const v4f*>(&sh.lr[i][16 * sb + 4 * lq]);
         const v4f dl_s = *reinterpret_cast<const v4f*>(&sh.dl[i][16 * sb + 4 * lq]);
         float m[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) m[e] = scores[sb][e] * decay_of(la_t - la_s[e]) * dl_s[e];
+        for (int e = 0; e < 4; ++e) m[e] = scores[sb][e] * decay_between(la_t, lr_t, TwoFloats{la_s[e], lr_s[e]}) * dl_s[e];
         if (sb == tok) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) m[e] = 4 * lq + e <= lr ? m[e] : 0.0f;
         }
         mf[sb] = tofrag<T>(m[0], m[1], m[2], m[3]);
       }
-      ea = decay_of(la_t);
+      ea = __builtin_amdgcn_exp2f(la_t);
       Dh = sh.D[i];
     }
     a.x.put(sX, XP, tid);

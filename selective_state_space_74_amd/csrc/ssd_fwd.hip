@@ -473,8 +473,9 @@ void ssd_fwd_kernel(SsdParams p) {
       w_row = __shfl(w, srow, 64);
       if (wave == 0) {
         sDl[lane] = dl;
-        sLa[lane] = static_cast<float>(la);
-        sLr[lane] = static_cast<float>(la - static_cast<float>(la));
+        const TwoFloats sum = two_floats(la);
+        sLa[lane] = sum.v;
+        sLr[lane] = sum.rest;
       }
     }
     // ---- decay-weighted x^T (needs the step sizes) ----
@@ -542,10 +543,10 @@ void ssd_fwd_kernel(SsdParams p) {
         const v4f la_s = *reinterpret_cast<const v4f*>(&sLa[s0]), lr_s = *reinterpret_cast<const v4f*>(&sLr[s0]);
         const float4 dl_s = *reinterpret_cast<const float4*>(&sDl[s0]);
         const int t = tb + lr;
-        const float m0 = s0 + 0 <= t ? sc[0] * __builtin_amdgcn_exp2f((la_t - la_s[0]) + (lr_t - lr_s[0])) * dl_s.x : 0.0f;
-        const float m1 = s0 + 1 <= t ? sc[1] * __builtin_amdgcn_exp2f((la_t - la_s[1]) + (lr_t - lr_s[1])) * dl_s.y : 0.0f;
-        const float m2 = s0 + 2 <= t ? sc[2] * __builtin_amdgcn_exp2f((la_t - la_s[2]) + (lr_t - lr_s[2])) * dl_s.z : 0.0f;
-        const float m3 = s0 + 3 <= t ? sc[3] * __builtin_amdgcn_exp2f((la_t - la_s[3]) + (lr_t - lr_s[3])) * dl_s.w : 0.0f;
+        const float m0 = s0 + 0 <= t ? sc[0] * decay_between(la_t, lr_t, TwoFloats{la_s[0], lr_s[0]}) * dl_s.x : 0.0f;
+        const float m1 = s0 + 1 <= t ? sc[1] * decay_between(la_t, lr_t, TwoFloats{la_s[1], lr_s[1]}) * dl_s.y : 0.0f;
+        const float m2 = s0 + 2 <= t ? sc[2] * decay_between(la_t, lr_t, TwoFloats{la_s[2], lr_s[2]}) * dl_s.z : 0.0f;
+        const float m3 = s0 + 3 <= t ? sc[3] * decay_between(la_t, lr_t, TwoFloats{la_s[3], lr_s[3]}) * dl_s.w : 0.0f;
         // intra: A = M (row t, k = s), B operand = x (k = s, column p) of
         // every channel block
         const auto mf = tofrag<T>(m0, m1, m2, m3);
