@@ -36,8 +36,9 @@
 // for dx.  G, the sum over the heads of M L Delta, and dB and dC stay in registers
 // from head to head, so dB and dC cost one product with C and B for all heads; the
 // next head's loads are under way while one is computed.  Bound by memory and the
-// latency of a head's five stages between barriers: 8 x 2048 x 32 x 64 x 64 bf16 in
-// 144 us, 3.3 TB/s of x, dout, both states and dx; one wavefront a token block: 203.
+// latency of a head's five stages between barriers (55% of a wavefront's cycles are
+// waits): 8 x 2048 x 32 x 64 x 64 bf16 in 152 us, 3.1 TB/s of x, dout, both states and
+// dx; one wavefront a token block was 39 us slower.
 #include <algorithm>
 
 #include "abi_checks.h"
@@ -65,7 +66,7 @@ struct GradParams {
 
 // Wavefronts a SIMD: four (two workgroups a compute unit, 128 registers) for up to 64
 // states in bf16 without a gate, though only the form of 16-byte rows and one pass fits
-// them; the others keep 11 to 26 registers in scratch, which costs less than half the
+// them; the others keep 8 to 26 registers in scratch, which costs less than half the
 // wavefronts.  Gradients with four and, without scratch, two, us: 8 x 2048 x 32 x 64 x 64
 // 266, 325; 4 x 2048 x 16 x 128 180, 196; 4 x 2048 x 32 x 36 by elements 238, 259; 4 x
 // 2048 x 16 x 132 391, 427.  A gate's dy in three parts leaves LDS for one workgroup; with

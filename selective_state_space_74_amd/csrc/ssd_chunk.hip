@@ -138,7 +138,7 @@ struct WeightedFrag {
 // is staged once; then for each head the rows x_s (dy_t) times their weight.  A
 // wavefront owns 16 channels of the state (fewer channels: a share of its columns).
 // Bound by memory: the states written are 4 N bytes for 2 x (64 tokens) bytes of x
-// read; 16,411 packed x 32 x 64 x 64 bf16, 23 sequences: 56 us, 3.7 TB/s.
+// read; 16,411 packed x 32 x 64 x 64 bf16, 23 sequences: 57 us, 3.7 TB/s.
 template <typename T, int NMAX, bool kVec>
 __global__ __launch_bounds__(kThreads) void ssd_states_kernel(ChunkParams p, int grid) {
   using E = typename Lds<T>::E;
@@ -422,13 +422,14 @@ __global__ __launch_bounds__(kWalkThreads) void ssd_walk_kernel(ChunkParams p, W
 // chunk are computed once and stay in registers for all heads; the next heads' loads
 // are under way while one is computed.  Tiles lie so that a lane has four channels
 // of one token.  Bound by the latency of a pass (stage, barrier, products, barrier;
-// 47% of a wavefront's cycles are waits) with 16 wavefronts a compute unit: the case
-// above, gated, in 102 us, 3.4 TB/s.  Loads one pass ahead and not two: 111 us; four
-// wavefronts, each with all channels of 16 tokens: 169.
+// 46% of a wavefront's cycles are waits) with 16 wavefronts a compute unit: the case
+// above, gated, in 106 us, 3.3 TB/s (102 while the carry left the states split, which
+// held them to 16 bits for the gradients too).  Loads one pass ahead and not two were 9 us
+// slower, four wavefronts, each with all channels of 16 tokens, 67.
 // kDz: the gate's gradient dout y silu'(z) in place of the output.
-// Two workgroups a compute unit (128 registers); rows by elements then keep up to 37
+// Two workgroups a compute unit (128 registers); rows by elements then keep up to 24
 // registers in scratch, which costs less than one workgroup without any (5000 packed x 32
-// x 33 x 128 bf16 171 us, 174; x 64 fp32 118, 135), but for the gate's gradient with 128
+// x 33 x 128 bf16 167 us, 174; x 64 fp32 118, 135), but for the gate's gradient with 128
 // states (79 registers: gradients of 4 x 1000 x 32 x 33 x 128 bf16 369, 347).
 constexpr int kOutThreads = 512;
 
